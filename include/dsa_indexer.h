@@ -326,6 +326,43 @@ DSA_API dsa_status_t dsa_sparse_mla_decode(const void *q, const void *kv_cache, 
                                            void *stream);
 
 
+/* ---- Residual addition and RMS norm -----------------------------------------
+ *
+ * The hidden rows that the projections read (the bf16 rows of
+ * dsa_indexer_qw_proj, 8-bit rows for an 8-bit product), or index keys in the
+ * fp8 cache's format.  Per row of d elements, in fp32:
+ *     h = x + residual (x where residual_opt is NULL)
+ *     y = h / sqrt(mean(h^2) + eps) * weight
+ *     residual_out = h,  out = y                       (bf16, one rounding each)
+ *     scale_G = max_G |y| / 448,  code = y / scale_G    (e4m3, one rounding)
+ * with one scale per group of 64 or 128 consecutive elements (the last group of
+ * a row may be short) or per row (group 0).  A group whose maximum is 0 (or so
+ * small that the scale is) has scale 1.  For finite rows every scale is positive and finite.
+ *
+ *   x            bf16 [rows, d], rows x_stride >= 0 elements apart (a view of
+ *                wider rows, or 0: the same row every time)
+ *   residual_opt bf16 [rows, d];  weight bf16 or fp32 [d] (weight_fp32 0 or 1)
+ *   residual_out bf16 [rows, d], given exactly when residual_opt is
+ *   out          bf16 [rows, d] (dsa_rmsnorm_fp8: may be NULL)
+ *   codes        uint8 [rows, d];  scales fp32 [rows, ceil(d / group)] or [rows]
+ * No alignment beyond the element's is asked for; 16-byte aligned rows (and a
+ * d that is a multiple of 8) are faster.  out and residual_out may be x or
+ * residual themselves (x only with x_stride == d); otherwise outputs overlap
+ * neither inputs nor each other.  rows = 0 launches nothing.  1 <= d <= 32768
+ * (above: DSA_ERR_UNSUPPORTED), rows < 2^31, eps finite and >= 0.  The result of
+ * a row depends on that row alone.  No workspace; capture-safe.
+ */
+#define DSA_NORM_MAX_DIM 32768
+
+DSA_API dsa_status_t dsa_rmsnorm(const void *x, int64_t x_stride, const void *residual_opt, const void *weight,
+                                 int32_t weight_fp32, int64_t rows, int32_t d, float eps, void *residual_out,
+                                 void *out, void *stream);
+
+/* The same with 8-bit rows out: group 64, 128, or 0 for one scale per row. */
+DSA_API dsa_status_t dsa_rmsnorm_fp8(const void *x, int64_t x_stride, const void *residual_opt, const void *weight,
+                                     int32_t weight_fp32, int64_t rows, int32_t d, float eps, int32_t group,
+                                     void *residual_out, void *out_opt, void *codes, float *scales, void *stream);
+
 /*
  * Read the sticky device error word into *code (host pointer).  Synchronises
  * `stream` (not capture-safe).  clear != 0 zeroes the word afterwards.

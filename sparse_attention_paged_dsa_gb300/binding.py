@@ -76,6 +76,10 @@ def load():
     lib.dsa_sparse_mla_workspace_size.restype = sz
     lib.dsa_sparse_mla_decode.argtypes = [p, p, i64, p, p, i32, i64, p, i32, ctypes.c_float, p, p, p, sz, p]
     lib.dsa_sparse_mla_decode.restype = st
+    lib.dsa_rmsnorm.argtypes = [p, i64, p, p, i32, i64, i32, ctypes.c_float, p, p, p]
+    lib.dsa_rmsnorm.restype = st
+    lib.dsa_rmsnorm_fp8.argtypes = [p, i64, p, p, i32, i64, i32, ctypes.c_float, i32, p, p, p, p, p]
+    lib.dsa_rmsnorm_fp8.restype = st
     lib.dsa_indexer_get_error.argtypes = [p, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int, p]
     lib.dsa_indexer_get_error.restype = st
     lib.dsa_status_string.argtypes = [st]
@@ -388,6 +392,89 @@ def dsa_sparse_mla_decode(q, kv_cache, page_table, seq_lens, max_context: int, t
                                       _stream(q.device))
     _check(st, "dsa_sparse_mla_decode")
     return out, lse
+
+
+def _run(name: str, device, *args):
+    """Call the C entry point ``name`` with ``args`` and the current stream of ``device``, on that device."""
+    fn = getattr(load(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if st != DSA_OK:
+        raise DsaError(st, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _norm_args(x, weight, residual, out, residual_out):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a [rows, d] tensor")
+    rows, d = x.shape
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.dtype not in _BF16:
+        raise TypeError(f"x has dtype {x.dtype}, expected one of {_BF16}")
+    if d > 1 and x.stride(1) != 1:
+        raise ValueError("the elements of a row of x must be contiguous")
+    _need(weight, "weight", _BF16 + (torch.float32,), (d,))
+    if residual is not None:
+        _need(residual, "residual", _BF16, (rows, d))
+        if residual_out is None:
+            residual_out = torch.empty((rows, d), dtype=torch.bfloat16, device=x.device)
+        _need(residual_out, "residual_out", _BF16, (rows, d))
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if out is not None:
+        _need(out, "out", _BF16, (rows, d))
+    _same_device(x.device, weight=weight, residual=residual, out=out, residual_out=residual_out)
+    return rows, d, int(weight.dtype == torch.float32), residual_out
+
+
+def dsa_rmsnorm(x, weight, eps: float, residual=None, out=None, residual_out=None):
+    """(out, residual_out): RMS norm of x + residual, and that sum (None without a residual).
+
+    x [rows, d] bf16 (rows may be strided, as a view of wider rows is), weight [d] bf16 or fp32.
+    ``out`` and ``residual_out`` may be ``x`` and ``residual`` themselves."""
+    rows, d, w32, residual_out = _norm_args(x, weight, residual, out, residual_out)
+    if out is None:
+        out = torch.empty((rows, d), dtype=torch.bfloat16, device=x.device)
+    _run("dsa_rmsnorm", x.device, x.data_ptr(), x.stride(0), _addr(residual), weight.data_ptr(), w32, rows, d, eps,
+         _addr(residual_out), out.data_ptr())
+    return out, residual_out
+
+
+def dsa_rmsnorm_fp8(x, weight, eps: float, group: int, residual=None, with_bf16: bool = False, out=None,
+                    residual_out=None, codes=None, scales=None):
+    """(codes, scales, out, residual_out): as ``dsa_rmsnorm`` with e4m3 rows and fp32 scales.
+
+    ``group`` 64 or 128 elements per scale, or 0 for one scale per row; ``out`` (bf16) is written
+    when given or with ``with_bf16``.  Rows of 64 with group 64 are the fp8 index-key cache's format."""
+    rows, d, w32, residual_out = _norm_args(x, weight, residual, out, residual_out)
+    if group not in (0, 64, 128):
+        raise ValueError(f"group must be 0, 64 or 128, got {group}")
+    if out is None and with_bf16:
+        out = torch.empty((rows, d), dtype=torch.bfloat16, device=x.device)
+    if codes is None:
+        codes = torch.empty((rows, d), dtype=torch.float8_e4m3fn, device=x.device)
+    _need(codes, "codes", _FP8, (rows, d))
+    groups = -(-d // group) if group else 1
+    if scales is None:
+        scales = torch.empty((rows, groups), dtype=torch.float32, device=x.device)
+    _need(scales, "scales", (torch.float32,), (rows, groups))
+    _same_device(x.device, codes=codes, scales=scales)
+    _run("dsa_rmsnorm_fp8", x.device, x.data_ptr(), x.stride(0), _addr(residual), weight.data_ptr(), w32, rows, d,
+         eps, group, _addr(residual_out), _addr(out), codes.data_ptr(), scales.data_ptr())
+    return codes, scales, out, residual_out
 
 
 def get_error(workspace, clear: bool = True) -> int:

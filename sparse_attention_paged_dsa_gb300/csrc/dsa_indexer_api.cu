@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -273,6 +274,61 @@ int mla_splits(int32_t batch, int32_t k) {
 }
 size_t mla_partial_floats(int32_t batch, int splits) {
     return splits > 1 ? size_t(batch) * size_t(splits) * dsa::kMlaHeads * (dsa::kMlaDv + 1) : 0;
+}
+
+// SMs of the current device (cached per device: the query is on every launch's path).
+cudaError_t sm_count(int* sms) {
+    static std::atomic<int> known[dsa::kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= dsa::kMaxDevices) return cudaErrorInvalidDevice;
+    *sms = known[dev].load(std::memory_order_relaxed);
+    if (*sms > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) known[dev].store(*sms, std::memory_order_relaxed);
+    return e;
+}
+
+dsa_status_t run_rmsnorm(dsa::RmsNormParams p, void* stream) {
+    if (p.rows < 0 || p.rows > INT32_MAX || p.d < 1 || p.x_stride < 0 || !std::isfinite(p.eps) || p.eps < 0.f ||
+        (p.weight_fp32 != 0 && p.weight_fp32 != 1))
+        return DSA_ERR_INVALID_ARG;
+    if (p.d > DSA_NORM_MAX_DIM) return DSA_ERR_UNSUPPORTED;
+    if (p.rows == 0) return DSA_OK;
+    if (p.rows == 1) p.x_stride = p.d;  // no second row: the stride means nothing
+    if (!p.x || !p.weight || (p.residual == nullptr) != (p.residual_out == nullptr) || (!p.out && !p.codes))
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned(p.x, 2) || !aligned(p.residual, 2) || !aligned(p.residual_out, 2) || !aligned(p.out, 2) ||
+        !aligned(p.weight, p.weight_fp32 ? 4 : 2) || !aligned(p.scales, 4))
+        return DSA_ERR_INVALID_ARG;
+    if (p.out && p.out == p.residual_out) return DSA_ERR_INVALID_ARG;
+    if ((p.out == p.x || p.residual_out == p.x) && p.x_stride != p.d) return DSA_ERR_INVALID_ARG;
+    const bool wide = p.d % 8 == 0 && p.x_stride % 8 == 0 && aligned(p.x, 16) && aligned(p.residual, 16) &&
+                      aligned(p.weight, 16) && aligned(p.residual_out, 16) && aligned(p.out, 16) &&
+                      aligned(p.codes, 8);
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    e = dsa::launch_rmsnorm(p, wide, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DSA_OK : cuda_fail(e, "RMS norm launch");
+}
+
+dsa::RmsNormParams norm_params(const void* x, int64_t x_stride, const void* residual, const void* weight,
+                               int32_t weight_fp32, int64_t rows, int32_t d, float eps, void* residual_out,
+                               void* out) {
+    dsa::RmsNormParams p{};
+    p.x = x;
+    p.residual = residual;
+    p.weight = weight;
+    p.residual_out = residual_out;
+    p.out = out;
+    p.x_stride = x_stride;
+    p.rows = rows;
+    p.d = d;
+    p.weight_fp32 = weight_fp32;
+    p.eps = eps;
+    return p;
 }
 
 }  // namespace
@@ -571,4 +627,25 @@ dsa_status_t dsa_sparse_mla_decode(const void* q, const void* kv_cache, int64_t 
     const cudaError_t e = dsa::launch_mla(q_map, kv_map, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "sparse MLA decode launch");
 }
+
+dsa_status_t dsa_rmsnorm(const void* x, int64_t x_stride, const void* residual_opt, const void* weight,
+                         int32_t weight_fp32, int64_t rows, int32_t d, float eps, void* residual_out, void* out,
+                         void* stream) {
+    return run_rmsnorm(norm_params(x, x_stride, residual_opt, weight, weight_fp32, rows, d, eps, residual_out, out),
+                       stream);
+}
+
+dsa_status_t dsa_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residual_opt, const void* weight,
+                             int32_t weight_fp32, int64_t rows, int32_t d, float eps, int32_t group,
+                             void* residual_out, void* out_opt, void* codes, float* scales, void* stream) {
+    dsa::RmsNormParams p =
+        norm_params(x, x_stride, residual_opt, weight, weight_fp32, rows, d, eps, residual_out, out_opt);
+    if (group != 0 && group != 64 && group != 128) return DSA_ERR_INVALID_ARG;
+    if (rows > 0 && (!codes || !scales)) return DSA_ERR_INVALID_ARG;
+    p.group = group;
+    p.codes = static_cast<uint8_t*>(codes);
+    p.scales = scales;
+    return run_rmsnorm(p, stream);
+}
+
 }  // extern "C"

@@ -137,4 +137,24 @@ size_t mla_smem_bytes();
 // one row x 64 (the row gathers' map).
 cudaError_t launch_mla(const CUtensorMap& q_map, const CUtensorMap& kv_map, const MlaParams& p, cudaStream_t stream);
 
+// Residual addition + RMS norm of bf16 rows.
+struct RmsNormParams {
+    const void* x;            // bf16, rows x_stride elements apart
+    const void* residual;     // bf16 [rows, d] or null
+    const void* weight;       // bf16 or fp32 [d]
+    void* residual_out;       // bf16 [rows, d], null without a residual
+    void* out;                // bf16 [rows, d] or null
+    uint8_t* codes;           // e4m3 [rows, d] or null
+    float* scales;            // [rows, groups of a row]
+    int64_t x_stride;
+    int64_t rows;
+    int32_t d;
+    int32_t group;            // 64, 128 or 0 (one scale per row)
+    int32_t weight_fp32;
+    int32_t row_threads;      // threads that share a row (set by the launch)
+    float eps;
+};
+// wide: 16-byte vectors of every array are aligned and d is a multiple of 8.
+cudaError_t launch_rmsnorm(RmsNormParams p, bool wide, int sms, cudaStream_t stream);
+
 }  // namespace dsa
