@@ -326,6 +326,39 @@ DSA_API dsa_status_t dsa_sparse_mla_decode(const void *q, const void *kv_cache, 
                                            void *stream);
 
 
+/* ---- Latent attention decode over every live entry ---------------------------
+ *
+ * The absorbed form without a top-k row: each of next_n query tokens per request
+ * attends to every entry it sees, by the rule of the multi-token indexer (token
+ * j of the request sees L_j = seq_len - (next_n - 1 - j) tokens, i.e. n_bj =
+ * ceil(max(L_j, 0) / 4) entries):
+ *     s_t = sm_scale * q[b, j, h, :] . kv_t[:]                     (576 dims)
+ *     out[b, j, h] = sum_t softmax_t(s) * kv_t[0:512]              (t < n_bj)
+ *     lse[b, j, h] = log sum_t exp(s_t)
+ * A token that sees no entry gets out = 0 and lse = -inf.  Layouts (C-contiguous):
+ *   q          [batch, next_n, 64, 576] bf16, 16-byte aligned
+ *   kv_cache   [num_pages, 64, 576] bf16, 16-byte aligned; page_table, seq_lens as above
+ *   out        [batch, next_n, 64, 512] bf16, lse [batch, next_n, 64] fp32, 16-byte aligned
+ *   workspace  >= dsa_mla_decode_workspace_size(batch, next_n) bytes, 256-byte
+ *              aligned, header zeroed once; holds the error word, the plan of the
+ *              split and the partial outputs (sized for the current device).
+ * The requests' entries are split over the whole device by length and joined by
+ * log-sum-exp; the launch depends on (batch, next_n, device) only.  Softmax
+ * weights are rounded to bf16 for the second product, sums are fp32.  Entries
+ * past n_bj are never used, whatever they hold; the entries a token sees, and
+ * q, must be finite.  An entry on a live page id outside [0, num_pages) is
+ * left out, and DSA_DEVERR_BAD_PAGE is set.  The order of a request's sums
+ * depends on the batch's lengths; for the same arguments results are the same
+ * bits.  1 <= next_n <= 4, finite sm_scale; num_pages above 2^25 - 1 returns
+ * DSA_ERR_UNSUPPORTED.  Asynchronous on `stream`, allocates nothing, capture-safe.
+ */
+DSA_API size_t dsa_mla_decode_workspace_size(int32_t batch, int32_t next_n);
+
+DSA_API dsa_status_t dsa_mla_decode(const void *q, const void *kv_cache, int64_t num_pages,
+                                    const int32_t *page_table, const int32_t *seq_lens, int32_t batch,
+                                    int32_t next_n, int64_t max_context, float sm_scale, void *out, float *lse,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- Residual addition and RMS norm -----------------------------------------
  *
  * The hidden rows that the projections read (the bf16 rows of

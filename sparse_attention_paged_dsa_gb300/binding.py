@@ -76,6 +76,10 @@ def load():
     lib.dsa_sparse_mla_workspace_size.restype = sz
     lib.dsa_sparse_mla_decode.argtypes = [p, p, i64, p, p, i32, i64, p, i32, ctypes.c_float, p, p, p, sz, p]
     lib.dsa_sparse_mla_decode.restype = st
+    lib.dsa_mla_decode_workspace_size.argtypes = [i32, i32]
+    lib.dsa_mla_decode_workspace_size.restype = sz
+    lib.dsa_mla_decode.argtypes = [p, p, i64, p, p, i32, i32, i64, ctypes.c_float, p, p, p, sz, p]
+    lib.dsa_mla_decode.restype = st
     lib.dsa_rmsnorm.argtypes = [p, i64, p, p, i32, i64, i32, ctypes.c_float, p, p, p]
     lib.dsa_rmsnorm.restype = st
     lib.dsa_rmsnorm_fp8.argtypes = [p, i64, p, p, i32, i64, i32, ctypes.c_float, i32, p, p, p, p, p]
@@ -414,6 +418,53 @@ def _same_device(device, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != device:
             raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def mla_decode_workspace_size(batch: int, next_n: int = 1) -> int:
+    """Workspace bytes of ``dsa_mla_decode`` on the current device (0 for an invalid shape)."""
+    return int(load().dsa_mla_decode_workspace_size(batch, next_n))
+
+
+def new_mla_workspace(batch: int, next_n: int = 1, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for ``dsa_mla_decode`` calls of this shape (and for ``dsa_mla_prefill``)."""
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        n = mla_decode_workspace_size(batch, next_n)
+        if n == 0:
+            raise ValueError("invalid shape for a workspace")
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def dsa_mla_decode(q, kv_cache, page_table, seq_lens, max_context: int, sm_scale: float, out=None, lse=None,
+                   workspace=None):
+    """(out, lse): attention of q over every live entry of the paged latent cache.
+
+    q [B, 64, 576] bf16, or [B, next_n, 64, 576] for next_n query tokens per request (token j sees
+    seq_len - (next_n - 1 - j) tokens); kv_cache [P, 64, 576] bf16; out bf16 [..., 64, 512]; lse fp32."""
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be [batch, 64, 576] or [batch, next_n, 64, 576]")
+    lead = q.shape[:-2]
+    B, Q = lead[0], (lead[1] if q.dim() == 4 else 1)
+    _need(q, "q", _BF16, (*lead, MLA_HEADS, MLA_DIM))
+    _need(kv_cache, "kv_cache", _BF16)
+    if kv_cache.dim() != 3 or tuple(kv_cache.shape[1:]) != (PAGE_ENTRIES, MLA_DIM):
+        raise ValueError(f"kv_cache must be [num_pages, 64, 576], got {tuple(kv_cache.shape)}")
+    _need(page_table, "page_table", (torch.int32,), (B, max_context // PAGE_TOKENS))
+    _need(seq_lens, "seq_lens", (torch.int32,), (B,))
+    if out is None:
+        out = torch.empty((*lead, MLA_HEADS, MLA_DV), dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", _BF16, (*lead, MLA_HEADS, MLA_DV))
+    if lse is None:
+        lse = torch.empty((*lead, MLA_HEADS), dtype=torch.float32, device=q.device)
+    _need(lse, "lse", (torch.float32,), (*lead, MLA_HEADS))
+    if workspace is None:
+        workspace = new_mla_workspace(B, Q, q.device)
+    _same_device(q.device, kv_cache=kv_cache, page_table=page_table, seq_lens=seq_lens, out=out, lse=lse,
+                 workspace=workspace)
+    _run("dsa_mla_decode", q.device, q.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0], page_table.data_ptr(),
+         seq_lens.data_ptr(), B, Q, max_context, sm_scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+         workspace.numel() * workspace.element_size())
+    return out, lse
 
 
 def _norm_args(x, weight, residual, out, residual_out):

@@ -290,6 +290,18 @@ cudaError_t sm_count(int* sms) {
     return e;
 }
 
+// Dense latent decode: one range of work per group of next_n CTAs, one CTA per SM.
+int dense_groups(int sms, int32_t next_n) {
+    const int g = sms / next_n;
+    return g < 1 ? 1 : (g > dsa::kMlaMaxGroups ? dsa::kMlaMaxGroups : g);
+}
+constexpr size_t kDensePlanBytes = size_t(DSA_MAX_BATCH) * sizeof(int2);
+size_t dense_parts(int groups, int32_t next_n) { return size_t(groups) * size_t(next_n) * 2; }
+size_t dense_workspace_bytes(int groups, int32_t next_n) {
+    return dsa::kWorkspaceHeaderBytes + kDensePlanBytes +
+           dense_parts(groups, next_n) * dsa::kMlaHeads * (dsa::kMlaDv + 1) * sizeof(float);
+}
+
 dsa_status_t run_rmsnorm(dsa::RmsNormParams p, void* stream) {
     if (p.rows < 0 || p.rows > INT32_MAX || p.d < 1 || p.x_stride < 0 || !std::isfinite(p.eps) || p.eps < 0.f ||
         (p.weight_fp32 != 0 && p.weight_fp32 != 1))
@@ -646,6 +658,61 @@ dsa_status_t dsa_rmsnorm_fp8(const void* x, int64_t x_stride, const void* residu
     p.codes = static_cast<uint8_t*>(codes);
     p.scales = scales;
     return run_rmsnorm(p, stream);
+}
+
+size_t dsa_mla_decode_workspace_size(int32_t batch, int32_t next_n) {
+    int sms = 0;
+    if (batch < 1 || batch > DSA_MAX_BATCH || next_n < 1 || next_n > DSA_MAX_NEXT_N) return 0;
+    if (sm_count(&sms) != cudaSuccess) sms = 160;  // no device: what a large part needs
+    return dense_workspace_bytes(dense_groups(sms, next_n), next_n);
+}
+
+dsa_status_t dsa_mla_decode(const void* q, const void* kv_cache, int64_t num_pages, const int32_t* page_table,
+                            const int32_t* seq_lens, int32_t batch, int32_t next_n, int64_t max_context,
+                            float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    dsa_status_t st = check_shape(batch, max_context);
+    if (st != DSA_OK) return st;
+    if (next_n < 1 || next_n > DSA_MAX_NEXT_N) return DSA_ERR_INVALID_ARG;
+    if (!q || !kv_cache || !page_table || !seq_lens || !out || !lse) return DSA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
+        !aligned(out, 16) || !aligned(lse, 16))
+        return DSA_ERR_INVALID_ARG;
+    if (num_pages < 1 || num_pages > kMaxPages || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+    // The tile loads address cache rows with 32-bit coordinates.
+    if (num_pages > (int64_t(1) << 31) / dsa::kPageEntries - 1) return DSA_ERR_UNSUPPORTED;
+    st = check_workspace(workspace, workspace_bytes, dsa::kWorkspaceHeaderBytes);
+    if (st != DSA_OK) return st;
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    const int groups = dense_groups(sms, next_n);
+    st = check_workspace(workspace, workspace_bytes, dense_workspace_bytes(groups, next_n));
+    if (st != DSA_OK) return st;
+    CUtensorMap q_map, kv_map;
+    st = make_rows_map(&q_map, q, int64_t(batch) * next_n * DSA_MLA_HEADS, DSA_MLA_DIM, 64, "mla q");
+    if (st != DSA_OK) return st;
+    st = make_rows_map(&kv_map, kv_cache, num_pages * dsa::kPageEntries, DSA_MLA_DIM, 64, "mla kv");
+    if (st != DSA_OK) return st;
+    dsa::MlaDenseParams p{};
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.page_table = page_table;
+    p.seq_lens = seq_lens;
+    p.out = static_cast<__nv_bfloat16_raw*>(out);
+    p.lse = lse;
+    p.plan = reinterpret_cast<int2*>(ws + dsa::kWorkspaceHeaderBytes);
+    p.o_part = reinterpret_cast<float*>(ws + dsa::kWorkspaceHeaderBytes + kDensePlanBytes);
+    p.lse_part = p.o_part + dense_parts(groups, next_n) * dsa::kMlaHeads * dsa::kMlaDv;
+    p.err = static_cast<uint32_t*>(workspace);
+    p.num_pages = num_pages;
+    p.max_context = max_context;
+    p.table_width = int32_t(max_context / DSA_PAGE_TOKENS);
+    p.batch = batch;
+    p.tokens = next_n;
+    p.groups = groups;
+    p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+    e = dsa::launch_mla_dense(q_map, kv_map, p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA decode launch");
 }
 
 }  // extern "C"

@@ -137,6 +137,32 @@ size_t mla_smem_bytes();
 // one row x 64 (the row gathers' map).
 cudaError_t launch_mla(const CUtensorMap& q_map, const CUtensorMap& kv_map, const MlaParams& p, cudaStream_t stream);
 
+// Latent attention decode over every live entry, 1-4 tokens per request.
+constexpr int kMlaMaxGroups = 256;
+constexpr int kMlaSegUnits = 2;  // a request's fixed cost in a range (q, output), in blocks
+constexpr int kMlaMinUnits = 3;  // least units worth a range of its own
+struct MlaDenseParams {
+    const int32_t* page_table; // [batch, table_width]
+    const int32_t* seq_lens;   // [batch] tokens
+    __nv_bfloat16_raw* out;    // [batch, tokens, 64, 512]
+    float* lse;                // [batch, tokens, 64]
+    int2* plan;                // [batch] first and last range of each request
+    float* o_part;             // [groups * tokens * 2, 64, 512] partial outputs
+    float* lse_part;           // [groups * tokens * 2, 64]
+    uint32_t* err;             // device error word
+    int64_t num_pages;
+    int64_t max_context;
+    int32_t table_width;
+    int32_t batch;
+    int32_t tokens;            // query tokens per request
+    int32_t groups;            // ranges: SMs / tokens
+    float sm_scale_log2;       // sm_scale * log2(e)
+};
+// q_map: q [batch * tokens * 64, 576] bf16; kv_map: the cache as [num_pages * 64, 576] bf16
+// rows; both 128-byte-swizzled boxes of 64 x 64.
+cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const MlaDenseParams& p,
+                             cudaStream_t stream);
+
 // Residual addition + RMS norm of bf16 rows.
 struct RmsNormParams {
     const void* x;            // bf16, rows x_stride elements apart

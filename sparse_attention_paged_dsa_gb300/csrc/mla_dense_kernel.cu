@@ -1,0 +1,769 @@
+// mla_dense_kernel.cu -- latent attention decode over every live entry of the
+// paged cache (absorbed form), one to four query tokens per request, sm_103a.
+//
+//     s[h, t] = sm_scale * q[b, j, h] . kv_t                 (576-wide entries)
+//     o[b, j, h] = sum_t softmax_t(s[h, :]) kv_t[:512],  lse = log sum_t exp(s[h, t])
+//
+// over t < ceil((seq_len - (next_n - 1 - j)) / 4).
+//
+// Work split.  A block is one page: 64 entries, 73,728 contiguous bytes.  The
+// requests' blocks, laid end to end with kSegUnits units of fixed cost before
+// each request, are cut into equal ranges, one per group of next_n CTAs (one CTA
+// per SM; token j of a group's requests belongs to its CTA j, so the tokens read
+// a page at about the same time and all but the first from L2).  Every CTA finds
+// its range from seq_lens alone.  A request inside one range is written straight
+// to the output; one that crosses ranges leaves an fp32 partial per range, and
+// the merge kernel joins them by log-sum-exp.
+//
+// Roles of a CTA (384 threads):
+//   * warp 0: TMA.  Each page into nine 64 x 64 slabs of 128-byte-swizzled rows
+//     (a ring of 8 slab pairs for the 512 value dims, 2 slabs for the last 64:
+//     two blocks), and each request's q.
+//   * warp 1: S[head, entry] = Q . K^T, M = 64, N = 64, K = 576, as slabs land;
+//     two S accumulators.
+//   * warp 2: O^T[dim, head] += V^T . P^T, M = 128 dims x 4, N = 64 heads, K = 64
+//     entries, V read in place as an MN-major operand.
+//   * warps 4-11: softmax.  Warp w reads the 16 heads of TMEM quadrant w % 4 and
+//     half of the block's entries with 16-lane loads that spread them over all 32
+//     lanes: 2 heads x 8 entries per thread.  The running maximum is raised only
+//     when a block passes it by more than 2^8; then the accumulators are rescaled
+//     in TMEM.  At a request's end the warps normalise O^T and store it.
+// Row sums add the unrounded fp32 weights; the weights are rounded to bf16 only
+// as the second product's operand.
+//
+// Entries past the live length, or on a page outside the cache, have weight 0
+// and their value rows are left out of the product (whole 16-entry steps) or
+// zeroed in shared memory, so that nothing stored there, NaN included, matters.
+//
+// What bounds it: bytes in flight.  A block's slots turn over after its landing
+// (loaded latency plus 73.7 KB at an SM's share of HBM) and the chain MMA1 tail,
+// softmax, MMA2; the ring holds two blocks, all the shared memory beside q.
+// Every wait is bounded (about 1 s); a timeout sets an error bit, the roles
+// drain, and TMEM is freed.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "indexer_kernels.h"
+#include "mla_common.cuh"
+#include "sm103_ptx.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kBlk = kPageEntries;             // entries per block: one page
+constexpr int kSlabBytes = kBlk * 128;         // 64 rows x 64 bf16 dims, 8 KiB
+constexpr int kPairBytes = 2 * kSlabBytes;     // value dims [128 j, 128 j + 128)
+constexpr int kVRing = 8;                      // slab pairs (two blocks' values)
+constexpr int kRRing = 2;                      // slabs of the last 64 dims
+constexpr int kQSlabs = kMlaDim / 64;          // 9
+constexpr int kOffQ = 0;
+constexpr int kOffP = kOffQ + kQSlabs * kSlabBytes;  // P [64 heads x 64 entries] bf16 (follows q's last
+                                                     // slab, whose rows 64..127 an M = 64 MMA may touch)
+constexpr int kOffV = kOffP + kSlabBytes;
+constexpr int kOffR = kOffV + kVRing * kPairBytes;
+constexpr int kOffCtl = kOffR + kRRing * kSlabBytes;
+constexpr int kThreadsD = 384;
+constexpr int kWarpsD = kThreadsD / 32;
+constexpr int kSoftWarp0 = 4;
+constexpr int kSoftThreads = 256;
+constexpr uint32_t kTmemColsD = 512;
+constexpr uint32_t kColS = 0;    // S: 2 x 64 columns
+constexpr uint32_t kColO = 128;  // O^T: 4 x 64 columns
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct __align__(8) DenseCtl {
+    uint64_t v_full[kVRing], v_empty[kVRing];
+    uint64_t r_full[kRRing], r_empty[kRRing];
+    uint64_t s_full[2], s_empty[2];
+    uint64_t q_full, q_empty, p_full, pv_done, o_empty, all_done;
+    uint32_t tmem_base;
+    int abort;
+    int first_req, first_unit;  // request of the range's first unit, and that unit within the request
+    int lo, hi;                 // the range, in units
+    int warp_units[kWarpsD];
+    float row_max[2][kMlaHeads];  // per half of the entries; the row sums at a request's end
+    float alpha[kMlaHeads];
+};
+constexpr int kSmemD = 1024 + kOffCtl + int(sizeof(DenseCtl));
+static_assert(kSmemD <= 232448, "fits one CTA per SM");
+
+// Named barrier over the 256 softmax threads returning the OR of `v`.
+__device__ __forceinline__ bool soft_bar_or(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred pi, po;\n\t"
+        "setp.ne.u32 pi, %1, 0;\n\t"
+        "bar.red.or.pred po, 1, 256, pi;\n\t"
+        "selp.u32 %0, 1, 0, po;\n\t}"
+        : "=r"(r)
+        : "r"(v ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void soft_bar_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// 16 TMEM lanes x 32 consecutive 32-bit columns over the warp's 32 threads: thread t gets rows
+// t / 4 and t / 4 + 8; r[4 k], r[4 k + 1] are row t / 4, columns 8 k + 2 (t % 4) and the next,
+// r[4 k + 2], r[4 k + 3] the same columns of row t / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Bounded wait for a phase of `bar`, whatever the other roles do.
+__device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
+    const uint32_t a = smem_u32(bar);
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(a, parity) && global_timer_ns() - t0 < kWaitLimitNs) {
+    }
+}
+
+// Tokens of a request, held to [0, max_context].
+__device__ __forceinline__ int seq_tokens(const MlaDenseParams& p, int b) {
+    const int seq = __ldg(p.seq_lens + b);
+    return seq < 0 ? 0 : (int64_t(seq) > p.max_context ? int(p.max_context) : seq);
+}
+__device__ __forceinline__ int blocks_of(int seq) { return (((seq + 3) >> 2) + kBlk - 1) / kBlk; }
+__device__ __forceinline__ int units_of(int blocks) { return blocks ? blocks + kMlaSegUnits : 0; }
+
+// The CTA's walk over its range: one step per request that has blocks in it.
+struct Walk {
+    int b, u0, lo, hi, batch;  // request b starts at unit u0; range [lo, hi)
+    int seq, nb, blo, bhi;     // current request: tokens, blocks, and this range's blocks [blo, bhi)
+    __device__ __forceinline__ Walk(const DenseCtl& ctl, const MlaDenseParams& p)
+        : b(ctl.first_req), u0(ctl.lo - ctl.first_unit), lo(ctl.lo), hi(ctl.hi), batch(p.batch) {}
+    __device__ __forceinline__ bool next(const MlaDenseParams& p) {
+        while (b < batch && u0 < hi) {
+            seq = seq_tokens(p, b);
+            nb = blocks_of(seq);
+            const int base = u0 + kMlaSegUnits, end = u0 + units_of(nb);
+            blo = max(lo, base) - base;
+            bhi = min(hi, end) - base;
+            ++b;
+            u0 = end;
+            if (nb > 0 && bhi > blo) return true;
+        }
+        return false;
+    }
+    __device__ __forceinline__ int req() const { return b - 1; }
+    // Entries of block `blk` that token `back` from the end sees.
+    __device__ __forceinline__ int valid(int blk, int back) const {
+        const int n = (max(seq - back, 0) + 3) >> 2;
+        return min(max(n - blk * kBlk, 0), kBlk);
+    }
+};
+
+// The pages of blocks [blk0, blk0 + 32) of the current request: lane's page id, -1 when outside
+// the cache or past the range.
+__device__ __forceinline__ int page_of_lane(const MlaDenseParams& p, const Walk& w, int blk0, int lane) {
+    const int blk = blk0 + lane;
+    if (blk >= w.bhi) return -1;
+    const int page = __ldg(p.page_table + int64_t(w.req()) * p.table_width + blk);
+    return (page >= 0 && int64_t(page) < p.num_pages) ? page : -1;
+}
+
+__global__ void __launch_bounds__(kThreadsD, 1)
+    mla_dense_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
+                     const MlaDenseParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    DenseCtl& ctl = *reinterpret_cast<DenseCtl*>(tiles + kOffCtl);
+    const uint32_t s_base = smem_u32(tiles);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int token = blockIdx.x;  // of the group
+    const int group = blockIdx.y;
+    const int back = p.tokens - 1 - token;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kVRing; ++i) {
+            mbar_init(&ctl.v_full[i], 1);
+            mbar_init(&ctl.v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.r_full[i], 1);
+            mbar_init(&ctl.r_empty[i], 1);
+            mbar_init(&ctl.s_full[i], 1);
+            mbar_init(&ctl.s_empty[i], kSoftThreads / 32);
+        }
+        mbar_init(&ctl.q_full, 1);
+        mbar_init(&ctl.q_empty, 1);
+        mbar_init(&ctl.p_full, kSoftThreads / 32);
+        mbar_init(&ctl.pv_done, 1);
+        mbar_init(&ctl.o_empty, kSoftThreads / 32);
+        mbar_init(&ctl.all_done, 2);
+        ctl.abort = 0;
+        ctl.first_req = p.batch;
+        ctl.first_unit = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&q_map);
+        tma_prefetch_map(&kv_map);
+    }
+    if (warp == 1) {
+        tmem_alloc(&ctl.tmem_base, kTmemColsD);
+        tmem_relinquish();
+    }
+    pdl_wait_prior_grid();
+    pdl_allow_next_grid();
+
+    // The range of this group, from the prefix sums of the requests' units.
+    const int per = (p.batch + kThreadsD - 1) / kThreadsD;
+    const int r0 = min(int(threadIdx.x) * per, p.batch), r1 = min(r0 + per, p.batch);
+    int mine = 0;
+    for (int b = r0; b < r1; ++b) {
+        const int seq = __ldg(p.seq_lens + b);
+        if ((seq < 0 || int64_t(seq) > p.max_context) && group == 0 && token == 0) atomicOr(p.err, kErrSeqLenClamped);
+        mine += units_of(blocks_of(seq_tokens(p, b)));
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) ctl.warp_units[warp] = incl;
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    int before = 0, total = 0;
+    for (int w = 0; w < kWarpsD; ++w) {
+        if (w < warp) before += ctl.warp_units[w];
+        total += ctl.warp_units[w];
+    }
+    int ngroups = min(p.groups, (total + kMlaMinUnits - 1) / kMlaMinUnits);
+    ngroups = ngroups < 1 ? 1 : ngroups;
+    const int lo = group < ngroups ? int(int64_t(total) * group / ngroups) : total;
+    const int hi = group < ngroups ? int(int64_t(total) * (group + 1) / ngroups) : total;
+    {
+        int u = before + incl - mine;
+        for (int b = r0; b < r1; ++b) {
+            const int nb = blocks_of(seq_tokens(p, b)), n = units_of(nb);
+            if (lo < hi && lo >= u && lo < u + n) {
+                ctl.first_req = b;
+                ctl.first_unit = lo - u;
+            }
+            if (group == 0 && token == 0) {  // which groups hold the request, for the merge
+                int2 g = make_int2(0, -1);   // no entry
+                if (nb > 0) {
+                    g.x = int((int64_t(u + kMlaSegUnits + 1) * ngroups - 1) / total);
+                    g.y = int((int64_t(u + n) * ngroups - 1) / total);
+                }
+                p.plan[b] = g;
+            }
+            u += n;
+        }
+    }
+    if (threadIdx.x == 0) {
+        ctl.lo = lo;
+        ctl.hi = hi;
+    }
+    __syncthreads();
+    const uint32_t tmem_base = ctl.tmem_base;
+
+    if (warp == 0) {
+        // ================= TMA =================
+        Walk w(ctl, p);
+        bool stop = false;
+        int n = 0, seg = 0;  // blocks and requests so far
+        int last_v = -1, last_r = -1, last_q = -1;  // the last fills issued
+        const uint64_t pol_q = l2_policy_evict_first();
+        // Tokens of a group share a page through L2; a single token reads it once.
+        const uint64_t pol_kv = p.tokens > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+        while (!stop && w.next(p)) {
+            if (lane == 0) {
+                if (mbar_wait(&ctl.q_empty, uint32_t(seg & 1) ^ 1u, &ctl.abort)) {
+                    mbar_arrive_expect_tx(&ctl.q_full, uint32_t(kQSlabs * kSlabBytes));
+                    for (int s = 0; s < kQSlabs; ++s)
+                        tma_load_2d(tiles + kOffQ + s * kSlabBytes, &q_map, &ctl.q_full, s * 64,
+                                    (w.req() * p.tokens + token) * kMlaHeads, pol_q);
+                    last_q = seg;
+                } else {
+                    stop = true;
+                }
+            }
+            stop = __any_sync(0xffffffffu, stop);
+            if (!stop) ++seg;
+            int page_l = -1;
+            for (int blk = w.blo; blk < w.bhi && !stop; ++blk, ++n) {
+                if (((blk - w.blo) & 31) == 0) {
+                    page_l = page_of_lane(p, w, blk, lane);
+                    if (blk + lane < w.bhi && page_l < 0) atomicOr(p.err, kErrBadPage);
+                }
+                // a page outside the cache: page 0 stands in, its entries are not used
+                const int page = max(__shfl_sync(0xffffffffu, page_l, (blk - w.blo) & 31), 0);
+                if (lane == 0) {
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        const int pos = 4 * n + j, slot = pos & (kVRing - 1), use = pos / kVRing;
+                        if (!mbar_wait(&ctl.v_empty[slot], uint32_t(use & 1) ^ 1u, &ctl.abort)) {
+                            stop = true;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&ctl.v_full[slot], uint32_t(kPairBytes));
+                        uint8_t* dst = tiles + kOffV + slot * kPairBytes;
+                        tma_load_2d(dst, &kv_map, &ctl.v_full[slot], 128 * j, page * kBlk, pol_kv);
+                        tma_load_2d(dst + kSlabBytes, &kv_map, &ctl.v_full[slot], 128 * j + 64, page * kBlk, pol_kv);
+                        last_v = pos;
+                    }
+                    const int slot = n & (kRRing - 1), use = n / kRRing;
+                    if (!stop && !mbar_wait(&ctl.r_empty[slot], uint32_t(use & 1) ^ 1u, &ctl.abort)) stop = true;
+                    if (!stop) {
+                        mbar_arrive_expect_tx(&ctl.r_full[slot], uint32_t(kSlabBytes));
+                        tma_load_2d(tiles + kOffR + slot * kSlabBytes, &kv_map, &ctl.r_full[slot], kMlaDv, page * kBlk,
+                                    pol_kv);
+                        last_r = n;
+                    }
+                }
+                stop = __any_sync(0xffffffffu, stop);
+            }
+        }
+        if (stop && lane == 0) {
+            atomicOr(p.err, kErrWaitTimeout);
+            ctl.abort = 1;
+        }
+        if (lane == 0) {  // no copy outlives the CTA (bounded waits; they have landed unless a role gave up)
+            for (int pos = last_v; pos >= 0 && pos > last_v - kVRing; --pos)
+                wait_landed(&ctl.v_full[pos & (kVRing - 1)], uint32_t(pos / kVRing) & 1u);
+            for (int i = last_r; i >= 0 && i > last_r - kRRing; --i)
+                wait_landed(&ctl.r_full[i & (kRRing - 1)], uint32_t(i / kRRing) & 1u);
+            if (last_q >= 0) wait_landed(&ctl.q_full, uint32_t(last_q) & 1u);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================= MMA1: S = Q . K^T =================
+        if (lane == 0) {
+            constexpr uint32_t kIdesc1 = idesc_bf16_f32(64, 64);
+            Walk w(ctl, p);
+            bool stop = false;
+            int n = 0, seg = 0;
+            while (!stop && w.next(p)) {
+                if (!mbar_wait(&ctl.q_full, uint32_t(seg & 1), &ctl.abort)) {
+                    stop = true;
+                    break;
+                }
+                ++seg;
+#pragma unroll 1
+                for (int blk = w.blo; blk < w.bhi && !stop; ++blk, ++n) {
+                    const int buf = n & 1;
+                    if (!mbar_wait(&ctl.s_empty[buf], uint32_t((n >> 1) & 1) ^ 1u, &ctl.abort)) {
+                        stop = true;
+                        break;
+                    }
+                    const uint32_t s_col = tmem_base + kColS + 64u * buf;
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        const int pos = 4 * n + j, slot = pos & (kVRing - 1), use = pos / kVRing;
+                        if (!mbar_wait(&ctl.v_full[slot], uint32_t(use & 1), &ctl.abort)) {
+                            stop = true;
+                            break;
+                        }
+                        tc_fence_after_sync();
+#pragma unroll
+                        for (int hs = 0; hs < 2; ++hs) {
+                            const int s = 2 * j + hs;
+                            const uint64_t a = smem_desc_kmajor_sw128(s_base + kOffQ + s * kSlabBytes);
+                            const uint64_t bd =
+                                smem_desc_kmajor_sw128(s_base + kOffV + slot * kPairBytes + hs * kSlabBytes);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_bf16_ss(s_col, a + 2u * kk, bd + 2u * kk, kIdesc1, (s | kk) != 0 ? 1u : 0u);
+                        }
+                    }
+                    if (stop) break;
+                    const int slot = n & (kRRing - 1), use = n / kRRing;
+                    if (!mbar_wait(&ctl.r_full[slot], uint32_t(use & 1), &ctl.abort)) {
+                        stop = true;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint64_t a = smem_desc_kmajor_sw128(s_base + kOffQ + 8 * kSlabBytes);
+                    const uint64_t bd = smem_desc_kmajor_sw128(s_base + kOffR + slot * kSlabBytes);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) umma_bf16_ss(s_col, a + 2u * kk, bd + 2u * kk, kIdesc1, 1u);
+                    umma_commit(&ctl.r_empty[slot]);
+                    umma_commit(&ctl.s_full[buf]);
+                }
+                if (!stop) umma_commit(&ctl.q_empty);
+            }
+            if (stop) {
+                atomicOr(p.err, kErrWaitTimeout);
+                ctl.abort = 1;
+            }
+            umma_commit(&ctl.all_done);  // every MMA this thread issued has completed when this arrives
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ================= MMA2: O^T += V^T . P^T =================
+        constexpr uint32_t kIdesc2 = idesc_bf16_f32(128, 64) | (1u << 15);  // A (V^T) MN-major
+        const uint64_t bp = smem_desc_kmajor_sw128(s_base + kOffP);
+        Walk w(ctl, p);
+        bool stop = false;
+        int n = 0, seg = 0;
+        while (!stop && w.next(p)) {
+            bool fresh = true;  // no product of this request yet
+            uint32_t bad = 0;
+#pragma unroll 1
+            for (int blk = w.blo; blk < w.bhi; ++blk, ++n) {
+                if (((blk - w.blo) & 31) == 0)
+                    bad = __ballot_sync(0xffffffffu, page_of_lane(p, w, blk, lane) < 0);
+                const int valid = ((bad >> ((blk - w.blo) & 31)) & 1u) ? 0 : w.valid(blk, back);
+                bool ok = mbar_wait(&ctl.p_full, uint32_t(n & 1), &ctl.abort);
+                if (ok && blk == w.blo) ok = mbar_wait(&ctl.o_empty, uint32_t(seg & 1) ^ 1u, &ctl.abort);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    stop = true;
+                    break;
+                }
+                tc_fence_after_sync();
+                const int steps = (valid + 15) >> 4;
+                if (valid & 15) {  // zero the value rows behind the live ones in the last step
+                    const int rows = 16 * steps - valid;
+                    for (int j = 0; j < 4; ++j) {  // landed long ago: orders these stores behind the copies
+                        const int pos = 4 * n + j;
+                        wait_landed(&ctl.v_full[pos & (kVRing - 1)], uint32_t(pos / kVRing) & 1u);
+                    }
+                    for (int i = lane; i < rows * 64; i += 32) {  // 8 slabs x 8 chunks of 16 bytes per row
+                        const int row = valid + (i >> 6), slab = (i >> 3) & 7, ch = i & 7;
+                        const int slot = (4 * n + (slab >> 1)) & (kVRing - 1);
+                        *reinterpret_cast<uint4*>(tiles + kOffV + slot * kPairBytes + (slab & 1) * kSlabBytes +
+                                                  row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+#pragma unroll 1
+                    for (int kk = 0; kk < steps; ++kk) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int slot = (4 * n + j) & (kVRing - 1);
+                            umma_bf16_ss(tmem_base + kColO + 64u * j,
+                                         desc_mn_sw128(s_base + kOffV + slot * kPairBytes + kk * 2048, kSlabBytes),
+                                         bp + 2u * kk, kIdesc2, (fresh && kk == 0) ? 0u : 1u);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) umma_commit(&ctl.v_empty[(4 * n + j) & (kVRing - 1)]);
+                    umma_commit(&ctl.pv_done);
+                }
+                __syncwarp();
+                if (steps > 0) fresh = false;
+            }
+            ++seg;
+        }
+        if (lane == 0) {
+            if (stop) {
+                atomicOr(p.err, kErrWaitTimeout);
+                ctl.abort = 1;
+            }
+            umma_commit(&ctl.all_done);
+        }
+        __syncwarp();
+    } else if (warp >= kSoftWarp0) {
+        // ================= softmax and output =================
+        const int quad = warp & 3;
+        const int half = (warp - kSoftWarp0) >> 2;        // entries [32 half, 32 half + 32)
+        const int h0 = quad * 16 + (lane >> 2);           // this thread's heads: h0 and h0 + 8
+        const uint32_t lane_addr = tmem_base + (uint32_t(quad * 32) << 16);
+        const float c2 = p.sm_scale_log2;
+        uint8_t* const pbuf = tiles + kOffP;
+        Walk w(ctl, p);
+        bool failed = false;
+        int n = 0;
+        while (!failed && w.next(p)) {
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            bool fresh = true;  // no product of this request yet: O^T holds nothing of it
+            uint32_t bad = 0;
+#pragma unroll 1
+            for (int blk = w.blo; blk < w.bhi; ++blk, ++n) {
+                if (((blk - w.blo) & 31) == 0)
+                    bad = __ballot_sync(0xffffffffu, page_of_lane(p, w, blk, lane) < 0);
+                const int valid = ((bad >> ((blk - w.blo) & 31)) & 1u) ? 0 : w.valid(blk, back);
+                const int buf = n & 1;
+                bool ok = mbar_wait(&ctl.s_full[buf], uint32_t((n >> 1) & 1), &ctl.abort);
+                ok = __all_sync(0xffffffffu, ok);
+                float x[16];
+                {
+                    uint32_t r[16];
+                    tc_fence_after_sync();
+                    tmem_ld_16x256b_x4(lane_addr + kColS + 64u * buf + 32u * half, r);
+                    tmem_ld_wait16(r);
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.s_empty[buf]);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]) * c2;
+                }
+                if (valid < kBlk) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int col = 32 * half + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
+                        if (col >= valid) x[i] = -INFINITY;
+                    }
+                }
+                float mx[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float a = fmaxf(x[2 * r], x[2 * r + 1]);
+#pragma unroll
+                    for (int k = 1; k < 4; ++k) a = fmaxf(a, fmaxf(x[4 * k + 2 * r], x[4 * k + 2 * r + 1]));
+                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                    mx[r] = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                }
+                const bool need = mx[0] > m[0] + kRescaleLog2 || mx[1] > m[1] + kRescaleLog2;
+                if (soft_bar_or(need || !ok)) {  // raise the running maximum (rare), or give up
+                    if (lane % 4 == 0) {
+                        ctl.row_max[half][h0] = ok ? mx[0] : NAN;
+                        ctl.row_max[half][h0 + 8] = mx[1];
+                    }
+                    if (soft_bar_or(!ok)) {
+                        failed = true;
+                        break;
+                    }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int h = h0 + 8 * r;
+                        const float top = fmaxf(ctl.row_max[0][h], ctl.row_max[1][h]);
+                        float alpha = 1.f;
+                        if (top > m[r] + kRescaleLog2) {
+                            alpha = exp2f(m[r] - top);
+                            m[r] = top;
+                            l[r] *= alpha;
+                        }
+                        if (half == 0 && lane % 4 == 0) ctl.alpha[h] = alpha;
+                    }
+                    if (!fresh) ok = mbar_wait(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort);
+                    if (soft_bar_or(!ok)) {
+                        failed = true;
+                        break;
+                    }
+                    if (!fresh) {
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t r[32];
+                            const uint32_t col = kColO + 64u * (2 * half + (j >> 1)) + 32u * (j & 1);
+                            tmem_ld_32x32b_x32(lane_addr + col, r);
+                            tmem_ld_wait(r);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                r[i] = __float_as_uint(__uint_as_float(r[i]) * ctl.alpha[(j & 1) * 32 + i]);
+                            tmem_st_x32(lane_addr + col, r);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                    }
+                }
+                uint32_t packed[8];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float mr = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float p0 = ex2_approx(x[4 * k + 2 * r] - mr);
+                        const float p1 = ex2_approx(x[4 * k + 2 * r + 1] - mr);
+                        l[r] += p0 + p1;
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
+                        packed[4 * r + k] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                }
+                // The P buffer is free once the previous block's product has read it.
+                if (n > 0) ok = mbar_wait(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0) ctl.abort = 1;  // the other warps see it at their next wait
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int h = h0 + 8 * r;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint32_t*>(pbuf + h * 128 + (((4 * half + k) ^ (h & 7)) << 4) +
+                                                     4 * (lane & 3)) = packed[4 * r + k];
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.p_full);
+                if (valid > 0) fresh = false;
+            }
+            if (failed) break;
+            // ---- the request's output (or partial)
+            bool ok = mbar_wait(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            }
+            if (lane % 4 == 0) {
+                ctl.row_max[half][h0] = l[0];
+                ctl.row_max[half][h0 + 8] = l[1];
+            }
+            if (soft_bar_or(!ok)) {
+                failed = true;
+                break;
+            }
+            tc_fence_after_sync();
+            const int64_t row = int64_t(w.req()) * p.tokens + token;
+            const bool whole = w.blo == 0 && w.bhi == w.nb;
+            const int64_t part = int64_t(group * p.tokens + token) * 2 + (w.blo == 0 ? 1 : 0);
+            if (half == 0 && lane % 4 == 0) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int h = h0 + 8 * r;
+                    const float sum = ctl.row_max[0][h] + ctl.row_max[1][h];
+                    ctl.alpha[h] = sum > 0.f ? 1.f / sum : 0.f;
+                    const float lse = sum > 0.f ? (m[r] + log2f(sum)) * kLn2 : -INFINITY;
+                    if (whole)
+                        p.lse[row * kMlaHeads + h] = lse;
+                    else
+                        p.lse_part[part * kMlaHeads + h] = lse;
+                }
+            }
+            soft_bar_sync();
+            // This warp: dims 128 j + 32 quad + lane of j = 2 half, 2 half + 1; all heads.
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                uint32_t r[32];
+                const int d = 128 * (2 * half + (j >> 1)) + 32 * quad + lane;
+                const int hb = 32 * (j & 1);
+                if (fresh) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = 0u;
+                } else {
+                    tmem_ld_32x32b_x32(lane_addr + kColO + 64u * (2 * half + (j >> 1)) + hb, r);
+                    tmem_ld_wait(r);
+                }
+                if (whole) {
+                    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + (row * kMlaHeads + hb) * kMlaDv + d;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i * kMlaDv] = __float2bfloat16_rn(__uint_as_float(r[i]) * ctl.alpha[hb + i]);
+                } else {
+                    float* o = p.o_part + (part * kMlaHeads + hb) * kMlaDv + d;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i * kMlaDv] = __uint_as_float(r[i]) * ctl.alpha[hb + i];
+                }
+            }
+            tc_fence_before_sync();
+            soft_bar_sync();  // alpha and row_max are free again
+            if (lane == 0) mbar_arrive(&ctl.o_empty);
+        }
+        if (failed && threadIdx.x == kSoftWarp0 * 32) {
+            atomicOr(p.err, kErrWaitTimeout);
+            ctl.abort = 1;
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        const uint32_t addr = smem_u32(&ctl.all_done);
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(addr, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+        }
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, kTmemColsD);
+    }
+}
+
+// o[r] = sum_i exp(lse_i - lse) o_i over the partials of a split request, lse = log sum_i exp(lse_i).
+// Grid (64 heads, rows); 128 threads per 512 dims, blockDim / 128 partials at a time.
+__global__ void __launch_bounds__(512) mla_dense_merge_kernel(const MlaDenseParams p) {
+    __shared__ float wgt[kMlaMaxGroups];
+    __shared__ float4 acc_s[3][128];
+    pdl_wait_prior_grid();
+    pdl_allow_next_grid();
+    const int h = blockIdx.x;
+    const int64_t row = blockIdx.y;
+    const int b = int(row / p.tokens), token = int(row % p.tokens);
+    const int2 g = p.plan[b];
+    if (g.x == g.y) return;  // one range: written by the decode kernel
+    const int quarter = threadIdx.x >> 7, d4 = threadIdx.x & 127;
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + (row * kMlaHeads + h) * kMlaDv + 4 * d4;
+    if (g.y < g.x) {  // no entry
+        if (quarter == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
+        if (threadIdx.x == 0) p.lse[row * kMlaHeads + h] = -INFINITY;
+        return;
+    }
+    const int S = g.y - g.x + 1;
+    // partial i: range g.x + i; the first one ends in the next range, the others began earlier
+    const auto part = [&](int i) { return (int64_t(g.x + i) * p.tokens + token) * 2 + (i == 0 ? 1 : 0); };
+    if (threadIdx.x < 32) {
+        float mx = -INFINITY;
+        for (int i = threadIdx.x; i < S; i += 32) {
+            wgt[i] = p.lse_part[part(i) * kMlaHeads + h];
+            mx = fmaxf(mx, wgt[i]);
+        }
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        float sum = 0.f;
+        for (int i = threadIdx.x; i < S; i += 32) {
+            const float e = mx == -INFINITY ? 0.f : expf(wgt[i] - mx);
+            wgt[i] = e;
+            sum += e;
+        }
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        for (int i = threadIdx.x; i < S; i += 32) wgt[i] *= inv;
+        if (threadIdx.x == 0) p.lse[row * kMlaHeads + h] = mx == -INFINITY ? -INFINITY : mx + logf(sum);
+    }
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int step = blockDim.x >> 7;
+#pragma unroll 8
+    for (int i = quarter; i < S; i += step) {
+        const float4 v = *reinterpret_cast<const float4*>(p.o_part + (part(i) * kMlaHeads + h) * kMlaDv + 4 * d4);
+        const float wt = wgt[i];
+        acc.x = fmaf(wt, v.x, acc.x), acc.y = fmaf(wt, v.y, acc.y);
+        acc.z = fmaf(wt, v.z, acc.z), acc.w = fmaf(wt, v.w, acc.w);
+    }
+    if (quarter > 0) acc_s[quarter - 1][d4] = acc;
+    __syncthreads();
+    if (quarter > 0) return;
+    for (int q = 1; q < step; ++q) {
+        const float4 v = acc_s[q - 1][d4];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+}  // namespace
+
+cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const MlaDenseParams& p,
+                             cudaStream_t stream) {
+    static SmemLimitOnce smem_limit;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = smem_limit.apply(dev, mla_dense_kernel, kSmemD);
+    if (e != cudaSuccess) return e;
+    if (p.groups < 1 || p.groups > kMlaMaxGroups || p.tokens < 1) return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(p.tokens), unsigned(p.groups));
+    cfg.blockDim = dim3(kThreadsD);
+    cfg.dynamicSmemBytes = size_t(kSmemD);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, mla_dense_kernel, q_map, kv_map, p);
+    if (e != cudaSuccess) return e;
+    // Few rows are split many ways: more threads per row read more partials at a time.
+    const int rows = p.batch * p.tokens;
+    cfg.gridDim = dim3(kMlaHeads, unsigned(rows));
+    cfg.blockDim = dim3(rows <= 16 ? 512 : 256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, mla_dense_merge_kernel, p);
+}
+
+}  // namespace dsa
