@@ -93,6 +93,8 @@ typedef enum {
 #define DSA_DEVERR_SEQ_LEN_CLAMPED 0x1u /* a seq_len was < 0 or > max_context */
 #define DSA_DEVERR_BAD_PAGE        0x2u /* a live page id was outside [0, num_pages) */
 #define DSA_DEVERR_WAIT_TIMEOUT    0x4u /* an in-kernel pipeline wait gave up (about 1 s) */
+#define DSA_DEVERR_BAD_RANGE       0x8u /* prefill: a request's rows or entries are out of order or out of the
+                                           tensor, or fewer entries than its seq_len needs */
 
 #define DSA_HEADS 32
 #define DSA_HEAD_DIM 64
@@ -358,6 +360,55 @@ DSA_API dsa_status_t dsa_mla_decode(const void *q, const void *kv_cache, int64_t
                                     const int32_t *page_table, const int32_t *seq_lens, int32_t batch,
                                     int32_t next_n, int64_t max_context, float sm_scale, void *out, float *lse,
                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Latent attention over prompts and prompt chunks ---------------------------
+ *
+ * The expanded form: per-head keys and values made from the latent entries by the
+ * caller's up-projection, for a ragged batch of new rows per request.  Request b
+ * has rows cu_q[b] .. cu_q[b + 1] of q and entries cu_kv[b] .. cu_kv[b + 1] of the
+ * keys and values; seq_lens[b] counts its tokens, its new rows included.  Row i
+ * of its n rows sees the entries of its causal prefix, by the same rule as the
+ * multi-token indexer and decode: L = seq_len - (n - 1 - i) tokens, the first
+ * ceil(max(L, 0) / entry_tokens) entries.
+ *     s_t = sm_scale * (q[i, h, 0:128] . k_nope[t, h] + q[i, h, 128:192] . k_rope[t])
+ *     out[i, h] = sum_t softmax_t(s) * v[t, h],   lse[i, h] = log sum_t exp(s_t)
+ * A row that sees nothing gets out = 0 and lse = -inf.  Rows of q outside
+ * [cu_q[0], cu_q[batch]) are neither used nor written.
+ *
+ *   q       bf16 [q_rows, heads, 192], rows q_row_stride and heads q_head_stride
+ *           elements apart; likewise k_nope [kv_rows, heads, 128] and v
+ *           [kv_rows, heads, 128] (e.g. the two halves of one [kv_rows, heads, 256]
+ *           product); k_rope bf16 [kv_rows, 64], rows k_rope_stride apart (e.g. the
+ *           last dims of the 576-wide entries).  16-byte aligned; strides are positive
+ *           multiples of 8 below 2^39 elements.
+ *   cu_q, cu_kv int32 [batch + 1], non-decreasing; seq_lens int32 [batch]
+ *   out     bf16 [q_rows, heads, 128] 16-byte aligned, lse fp32 [q_rows, heads], both contiguous
+ *   workspace >= DSA_PREFILL_WORKSPACE_BYTES, 256-byte aligned, zeroed once: the error word
+ *
+ * 1 <= batch <= 1024, 1 <= heads <= 128, 1 <= entry_tokens <= 64, sm_scale finite
+ * and >= 0, q_rows and kv_rows below 2^31 (0 rows: nothing is launched; 0 entries: every
+ * row sees nothing).  Softmax weights are rounded to bf16 for the second product,
+ * sums are fp32.  Entries that no row of their request sees are never used,
+ * whatever they hold; q and the entries that some row of a request sees must be
+ * finite.  Device data out of contract (DSA_DEVERR_BAD_RANGE, DSA_DEVERR_SEQ_LEN_CLAMPED)
+ * is never dereferenced: such rows are left out, or see the entries that there are.
+ * A row's result depends on its request alone.  The launch depends on (q_rows,
+ * batch, heads).  Asynchronous on `stream`, allocates nothing, capture-safe.
+ */
+#define DSA_PREFILL_QK_DIM 192
+#define DSA_PREFILL_NOPE_DIM 128
+#define DSA_PREFILL_ROPE_DIM 64
+#define DSA_PREFILL_V_DIM 128
+#define DSA_PREFILL_MAX_HEADS 128
+#define DSA_PREFILL_WORKSPACE_BYTES 256
+
+DSA_API dsa_status_t dsa_mla_prefill(const void *q, int64_t q_row_stride, int64_t q_head_stride, const void *k_nope,
+                                     int64_t k_row_stride, int64_t k_head_stride, const void *k_rope,
+                                     int64_t k_rope_stride, const void *v, int64_t v_row_stride,
+                                     int64_t v_head_stride, const int32_t *cu_q, const int32_t *cu_kv,
+                                     const int32_t *seq_lens, int32_t batch, int32_t heads, int64_t q_rows,
+                                     int64_t kv_rows, int32_t entry_tokens, float sm_scale, void *out, float *lse,
+                                     void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---- Residual addition and RMS norm -----------------------------------------
  *

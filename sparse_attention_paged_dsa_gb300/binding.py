@@ -21,6 +21,7 @@ WORKSPACE_HEADER_BYTES = 256
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE, DSA_ERR_CUDA = range(5)
 DEVERR_SEQ_LEN_CLAMPED, DEVERR_BAD_PAGE, DEVERR_WAIT_TIMEOUT = 0x1, 0x2, 0x4
+DEVERR_BAD_RANGE = 0x8
 
 _lib = None
 
@@ -80,6 +81,9 @@ def load():
     lib.dsa_mla_decode_workspace_size.restype = sz
     lib.dsa_mla_decode.argtypes = [p, p, i64, p, p, i32, i32, i64, ctypes.c_float, p, p, p, sz, p]
     lib.dsa_mla_decode.restype = st
+    lib.dsa_mla_prefill.argtypes = [p, i64, i64, p, i64, i64, p, i64, p, i64, i64, p, p, p, i32, i32, i64, i64, i32,
+                                    ctypes.c_float, p, p, p, sz, p]
+    lib.dsa_mla_prefill.restype = st
     lib.dsa_rmsnorm.argtypes = [p, i64, p, p, i32, i64, i32, ctypes.c_float, p, p, p]
     lib.dsa_rmsnorm.restype = st
     lib.dsa_rmsnorm_fp8.argtypes = [p, i64, p, p, i32, i64, i32, ctypes.c_float, i32, p, p, p, p, p]
@@ -464,6 +468,62 @@ def dsa_mla_decode(q, kv_cache, page_table, seq_lens, max_context: int, sm_scale
     _run("dsa_mla_decode", q.device, q.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0], page_table.data_ptr(),
          seq_lens.data_ptr(), B, Q, max_context, sm_scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
          workspace.numel() * workspace.element_size())
+    return out, lse
+
+
+PREFILL_QK, PREFILL_NOPE, PREFILL_ROPE, PREFILL_DV = 192, 128, 64, 128
+
+
+def _strided(t, name, shape):
+    """A bf16 CUDA tensor of ``shape`` whose last dimension is contiguous (other strides are free)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _BF16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_BF16}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def dsa_mla_prefill(q, k_nope, k_rope, v, cu_q, cu_kv, seq_lens, sm_scale: float, entry_tokens: int = 4, out=None,
+                    lse=None, workspace=None):
+    """(out, lse): causal attention of a ragged batch of prompt rows, expanded latent form.
+
+    q [Tq, H, 192] bf16, k_nope [Tk, H, 128], k_rope [Tk, 64], v [Tk, H, 128] (strided views are
+    fine); cu_q, cu_kv int32 [B + 1]; seq_lens int32 [B] tokens per request, the new rows included;
+    ``entry_tokens`` tokens per key entry (1: an entry per token).  out [Tq, H, 128] bf16 and lse
+    [Tq, H] fp32; rows outside [cu_q[0], cu_q[B]) are left as they are."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [rows, heads, 192]")
+    if not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("v must be [entries, heads, 128]")
+    Tq, H, Tk = q.shape[0], q.shape[1], v.shape[0]
+    _strided(q, "q", (Tq, H, PREFILL_QK))
+    _strided(k_nope, "k_nope", (Tk, H, PREFILL_NOPE))
+    _strided(k_rope, "k_rope", (Tk, PREFILL_ROPE))
+    _strided(v, "v", (Tk, H, PREFILL_DV))
+    _need(seq_lens, "seq_lens", (torch.int32,))
+    B = seq_lens.numel()
+    _need(seq_lens, "seq_lens", (torch.int32,), (B,))
+    _need(cu_q, "cu_q", (torch.int32,), (B + 1,))
+    _need(cu_kv, "cu_kv", (torch.int32,), (B + 1,))
+    if out is None:
+        out = torch.empty((Tq, H, PREFILL_DV), dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", _BF16, (Tq, H, PREFILL_DV))
+    if lse is None:
+        lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
+    _need(lse, "lse", (torch.float32,), (Tq, H))
+    if workspace is None:
+        workspace = torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=q.device)
+    _same_device(q.device, k_nope=k_nope, k_rope=k_rope, v=v, cu_q=cu_q, cu_kv=cu_kv, seq_lens=seq_lens, out=out,
+                 lse=lse, workspace=workspace)
+    _run("dsa_mla_prefill", q.device, q.data_ptr(), q.stride(0), q.stride(1), k_nope.data_ptr(), k_nope.stride(0),
+         k_nope.stride(1), k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), v.stride(0), v.stride(1),
+         cu_q.data_ptr(), cu_kv.data_ptr(), seq_lens.data_ptr(), B, H, Tq, Tk, entry_tokens, sm_scale,
+         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, lse
 
 

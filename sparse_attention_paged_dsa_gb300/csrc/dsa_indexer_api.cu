@@ -139,16 +139,37 @@ dsa_status_t make_plain_q_w_maps(CUtensorMap* q_map, CUtensorMap* w_map, const v
     return DSA_OK;
 }
 
-// bf16 2-D tensor [rows, cols] (cols contiguous) with a 128-byte-swizzled box of box_rows x 64.
+// bf16 2-D tensor [rows, cols] (cols contiguous, rows `row_stride` elements apart, by default cols) with a 128-byte-swizzled box of box_rows x 64.
 dsa_status_t make_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols, uint32_t box_rows,
-                           const char* what) {
+                           const char* what, int64_t row_stride = 0) {
     auto enc = encode_tiled();
     if (!enc) return cuda_fail(cudaErrorNotSupported, "cuTensorMapEncodeTiled lookup");
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(cols) * 2};
+    const cuuint64_t strides[1] = {cuuint64_t(row_stride ? row_stride : cols) * 2};
     const cuuint32_t box[2] = {64, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
+                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        std::snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "cuTensorMapEncodeTiled(%s): CUresult %d", what,
+                      int(r));
+        return DSA_ERR_CUDA;
+    }
+    return DSA_OK;
+}
+
+// bf16 [rows, heads, dim] with element strides (dim contiguous) as (dim, head, row): boxes of
+// 64 dims x 1 head x 128 rows, 128-byte swizzle.
+dsa_status_t make_heads_map(CUtensorMap* map, const void* ptr, int64_t rows, int32_t heads, int32_t dim,
+                            int64_t row_stride, int64_t head_stride, const char* what) {
+    auto enc = encode_tiled();
+    if (!enc) return cuda_fail(cudaErrorNotSupported, "cuTensorMapEncodeTiled lookup");
+    const cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(rows)};
+    const cuuint64_t strides[2] = {cuuint64_t(head_stride) * 2, cuuint64_t(row_stride) * 2};
+    const cuuint32_t box[3] = {64, 1, 128};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
                            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
@@ -713,6 +734,68 @@ dsa_status_t dsa_mla_decode(const void* q, const void* kv_cache, int64_t num_pag
     p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
     e = dsa::launch_mla_dense(q_map, kv_map, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA decode launch");
+}
+
+dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_nope,
+                             int64_t k_row_stride, int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride,
+                             const void* v, int64_t v_row_stride, int64_t v_head_stride, const int32_t* cu_q,
+                             const int32_t* cu_kv, const int32_t* seq_lens, int32_t batch, int32_t heads,
+                             int64_t q_rows, int64_t kv_rows, int32_t entry_tokens, float sm_scale, void* out,
+                             float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    if (batch < 1 || heads < 1 || q_rows < 0 || kv_rows < 0 || entry_tokens < 1) return DSA_ERR_INVALID_ARG;
+    if (batch > DSA_MAX_BATCH || heads > DSA_PREFILL_MAX_HEADS || entry_tokens > 64 || q_rows > INT32_MAX ||
+        kv_rows > INT32_MAX)
+        return DSA_ERR_UNSUPPORTED;
+    if (!std::isfinite(sm_scale) || sm_scale < 0.f) return DSA_ERR_INVALID_ARG;
+    const int64_t slots = q_rows / 256 + batch;
+    if (slots * heads > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+    if (!cu_q || !cu_kv || !seq_lens || !aligned(cu_q, 4) || !aligned(cu_kv, 4) || !aligned(seq_lens, 4))
+        return DSA_ERR_INVALID_ARG;
+    if (q_rows > 0 && (!q || !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)))
+        return DSA_ERR_INVALID_ARG;
+    if (kv_rows > 0 && (!k_nope || !k_rope || !v || !aligned(k_nope, 16) || !aligned(k_rope, 16) || !aligned(v, 16)))
+        return DSA_ERR_INVALID_ARG;
+    // A dimension of size 1 has no stride to speak of.
+    if (heads == 1) q_head_stride = k_head_stride = v_head_stride = DSA_PREFILL_QK_DIM;
+    if (q_rows <= 1) q_row_stride = DSA_PREFILL_QK_DIM;
+    if (kv_rows <= 1) k_row_stride = k_rope_stride = v_row_stride = DSA_PREFILL_QK_DIM;
+    for (int64_t s : {q_row_stride, q_head_stride, k_row_stride, k_head_stride, k_rope_stride, v_row_stride,
+                      v_head_stride})
+        if (s < 1 || s % 8 != 0 || s >= (int64_t(1) << 39)) return DSA_ERR_INVALID_ARG;
+    dsa_status_t st = check_workspace(workspace, workspace_bytes, DSA_PREFILL_WORKSPACE_BYTES);
+    if (st != DSA_OK) return st;
+    if (q_rows == 0) return DSA_OK;
+    CUtensorMap q_map, kn_map, kr_map, v_map;
+    st = make_heads_map(&q_map, q, q_rows, heads, DSA_PREFILL_QK_DIM, q_row_stride, q_head_stride, "prefill q");
+    if (st != DSA_OK) return st;
+    if (kv_rows > 0) {
+        st = make_heads_map(&kn_map, k_nope, kv_rows, heads, DSA_PREFILL_NOPE_DIM, k_row_stride, k_head_stride,
+                            "prefill k_nope");
+        if (st != DSA_OK) return st;
+        st = make_heads_map(&v_map, v, kv_rows, heads, DSA_PREFILL_V_DIM, v_row_stride, v_head_stride, "prefill v");
+        if (st != DSA_OK) return st;
+        st = make_rows_map(&kr_map, k_rope, kv_rows, DSA_PREFILL_ROPE_DIM, 128, "prefill k_rope", k_rope_stride);
+        if (st != DSA_OK) return st;
+    } else {
+        kn_map = kr_map = v_map = q_map;  // no entry: the kernel loads none
+    }
+    dsa::PrefillParams p{};
+    p.cu_q = cu_q;
+    p.cu_kv = cu_kv;
+    p.seq_lens = seq_lens;
+    p.out = static_cast<__nv_bfloat16_raw*>(out);
+    p.lse = lse;
+    p.err = static_cast<uint32_t*>(workspace);
+    p.q_rows = int32_t(q_rows);
+    p.kv_rows = int32_t(kv_rows);
+    p.batch = batch;
+    p.heads = heads;
+    p.entry_tokens = entry_tokens;
+    p.slots = int32_t(slots);
+    // A scale of 0 becomes one whose products vanish next to 1: hidden scores stay -inf times it.
+    p.sm_scale_log2 = std::fmax(sm_scale * 1.4426950408889634f, 1e-30f);
+    const cudaError_t e = dsa::launch_mla_prefill(q_map, kn_map, kr_map, v_map, p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA prefill launch");
 }
 
 }  // extern "C"

@@ -46,6 +46,7 @@ constexpr size_t kWorkspaceHeaderBytes = 256;
 constexpr uint32_t kErrSeqLenClamped = 0x1u;
 constexpr uint32_t kErrBadPage = 0x2u;
 constexpr uint32_t kErrWaitTimeout = 0x4u;
+constexpr uint32_t kErrBadRange = 0x8u;
 
 struct ScoresParams {
     const int32_t* page_table;  // [batch, table_width]
@@ -162,6 +163,28 @@ struct MlaDenseParams {
 // rows; both 128-byte-swizzled boxes of 64 x 64.
 cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const MlaDenseParams& p,
                              cudaStream_t stream);
+
+// Latent attention over ragged prompts, expanded form: per-head 128 + 64 shared key dims, 128 value dims.
+constexpr int kPrefillQk = 192;
+constexpr int kPrefillDv = 128;
+struct PrefillParams {
+    const int32_t* cu_q;       // [batch + 1] first row of each request
+    const int32_t* cu_kv;      // [batch + 1] first entry of each request
+    const int32_t* seq_lens;   // [batch] tokens, the request's rows included
+    __nv_bfloat16_raw* out;    // [q_rows, heads, 128]
+    float* lse;                // [q_rows, heads]
+    uint32_t* err;             // device error word
+    int32_t q_rows;
+    int32_t kv_rows;
+    int32_t batch;
+    int32_t heads;
+    int32_t entry_tokens;      // tokens per entry
+    int32_t slots;             // q_rows / 256 + batch blocks of up to 256 rows
+    float sm_scale_log2;       // sm_scale * log2(e), above 0
+};
+// Maps of 128-byte-swizzled boxes of 128 rows x 64 dims: q, k_nope and v as (dim, head, row), k_rope as (dim, row).
+cudaError_t launch_mla_prefill(const CUtensorMap& q_map, const CUtensorMap& kn_map, const CUtensorMap& kr_map,
+                               const CUtensorMap& v_map, const PrefillParams& p, cudaStream_t stream);
 
 // Residual addition + RMS norm of bf16 rows.
 struct RmsNormParams {
