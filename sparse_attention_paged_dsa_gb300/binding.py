@@ -402,26 +402,53 @@ def dsa_sparse_mla_decode(q, kv_cache, page_table, seq_lens, max_context: int, t
     return out, lse
 
 
-def _run(name: str, device, *args):
-    """Call the C entry point ``name`` with ``args`` and the current stream of ``device``, on that device."""
-    fn = getattr(load(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+def _run(fn, device: int, *args):
+    """Call the C entry point ``fn`` with ``args`` and the current stream of ``device``, on that device."""
+    if device == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
     if st != DSA_OK:
-        raise DsaError(st, name)
+        raise DsaError(st, fn.__name__)
+
+
+def _on(t, name, dtypes, shape, device: int):
+    """``_need`` for a tensor that must also be on ``device`` (one test on the path of a good call)."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
+        return
+    _need(t, name, dtypes, shape)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+
+
+def _device_of(t, name, dtypes, dims) -> int:
+    """The device index of the call's leading tensor, after its own checks but for the layout."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() not in dims:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}")
+    return t.get_device()
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _space(workspace, device: int):
+    """Address and bytes of a workspace on ``device``."""
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{device}")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+_F32, _I32 = (torch.float32,), (torch.int32,)
 
 
 def mla_decode_workspace_size(batch: int, next_n: int = 1) -> int:
@@ -445,47 +472,44 @@ def dsa_mla_decode(q, kv_cache, page_table, seq_lens, max_context: int, sm_scale
 
     q [B, 64, 576] bf16, or [B, next_n, 64, 576] for next_n query tokens per request (token j sees
     seq_len - (next_n - 1 - j) tokens); kv_cache [P, 64, 576] bf16; out bf16 [..., 64, 512]; lse fp32."""
-    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
-        raise ValueError("q must be [batch, 64, 576] or [batch, next_n, 64, 576]")
+    dev = _device_of(q, "q", _BF16, (3, 4))
     lead = q.shape[:-2]
-    B, Q = lead[0], (lead[1] if q.dim() == 4 else 1)
-    _need(q, "q", _BF16, (*lead, MLA_HEADS, MLA_DIM))
-    _need(kv_cache, "kv_cache", _BF16)
-    if kv_cache.dim() != 3 or tuple(kv_cache.shape[1:]) != (PAGE_ENTRIES, MLA_DIM):
-        raise ValueError(f"kv_cache must be [num_pages, 64, 576], got {tuple(kv_cache.shape)}")
-    _need(page_table, "page_table", (torch.int32,), (B, max_context // PAGE_TOKENS))
-    _need(seq_lens, "seq_lens", (torch.int32,), (B,))
+    B, Q = lead[0], (lead[1] if len(lead) == 2 else 1)
+    _on(q, "q", _BF16, (*lead, MLA_HEADS, MLA_DIM), dev)
+    pages = kv_cache.shape[0] if isinstance(kv_cache, torch.Tensor) and kv_cache.dim() else 0
+    _on(kv_cache, "kv_cache", _BF16, (pages, PAGE_ENTRIES, MLA_DIM), dev)
+    _on(page_table, "page_table", _I32, (B, max_context // PAGE_TOKENS), dev)
+    _on(seq_lens, "seq_lens", _I32, (B,), dev)
     if out is None:
         out = torch.empty((*lead, MLA_HEADS, MLA_DV), dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", _BF16, (*lead, MLA_HEADS, MLA_DV))
+    else:
+        _on(out, "out", _BF16, (*lead, MLA_HEADS, MLA_DV), dev)
     if lse is None:
         lse = torch.empty((*lead, MLA_HEADS), dtype=torch.float32, device=q.device)
-    _need(lse, "lse", (torch.float32,), (*lead, MLA_HEADS))
+    else:
+        _on(lse, "lse", _F32, (*lead, MLA_HEADS), dev)
     if workspace is None:
         workspace = new_mla_workspace(B, Q, q.device)
-    _same_device(q.device, kv_cache=kv_cache, page_table=page_table, seq_lens=seq_lens, out=out, lse=lse,
-                 workspace=workspace)
-    _run("dsa_mla_decode", q.device, q.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0], page_table.data_ptr(),
-         seq_lens.data_ptr(), B, Q, max_context, sm_scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-         workspace.numel() * workspace.element_size())
+    _run(load().dsa_mla_decode, dev, q.data_ptr(), kv_cache.data_ptr(), pages, page_table.data_ptr(),
+         seq_lens.data_ptr(), B, Q, max_context, sm_scale, out.data_ptr(), lse.data_ptr(),
+         *_space(workspace, dev))
     return out, lse
 
 
 PREFILL_QK, PREFILL_NOPE, PREFILL_ROPE, PREFILL_DV = 192, 128, 64, 128
 
 
-def _strided(t, name, shape):
-    """A bf16 CUDA tensor of ``shape`` whose last dimension is contiguous (other strides are free)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _BF16:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {_BF16}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
+def _strided(t, name, shape, device: int):
+    """A bf16 tensor of ``shape`` on ``device`` whose last dimension is contiguous (other strides are free)."""
+    if (isinstance(t, torch.Tensor) and t.dtype in _BF16 and t.shape == shape and t.get_device() == device
+            and t.stride(-1) == 1):
+        return
+    _device_of(t, name, _BF16, (len(shape),))
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
 def dsa_mla_prefill(q, k_nope, k_rope, v, cu_q, cu_kv, seq_lens, sm_scale: float, entry_tokens: int = 4, out=None,
@@ -496,59 +520,53 @@ def dsa_mla_prefill(q, k_nope, k_rope, v, cu_q, cu_kv, seq_lens, sm_scale: float
     fine); cu_q, cu_kv int32 [B + 1]; seq_lens int32 [B] tokens per request, the new rows included;
     ``entry_tokens`` tokens per key entry (1: an entry per token).  out [Tq, H, 128] bf16 and lse
     [Tq, H] fp32; rows outside [cu_q[0], cu_q[B]) are left as they are."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be [rows, heads, 192]")
-    if not isinstance(v, torch.Tensor) or v.dim() != 3:
-        raise ValueError("v must be [entries, heads, 128]")
+    dev = _device_of(q, "q", _BF16, (3,))
+    _device_of(v, "v", _BF16, (3,))
     Tq, H, Tk = q.shape[0], q.shape[1], v.shape[0]
-    _strided(q, "q", (Tq, H, PREFILL_QK))
-    _strided(k_nope, "k_nope", (Tk, H, PREFILL_NOPE))
-    _strided(k_rope, "k_rope", (Tk, PREFILL_ROPE))
-    _strided(v, "v", (Tk, H, PREFILL_DV))
-    _need(seq_lens, "seq_lens", (torch.int32,))
-    B = seq_lens.numel()
-    _need(seq_lens, "seq_lens", (torch.int32,), (B,))
-    _need(cu_q, "cu_q", (torch.int32,), (B + 1,))
-    _need(cu_kv, "cu_kv", (torch.int32,), (B + 1,))
+    _strided(q, "q", (Tq, H, PREFILL_QK), dev)
+    _strided(k_nope, "k_nope", (Tk, H, PREFILL_NOPE), dev)
+    _strided(k_rope, "k_rope", (Tk, PREFILL_ROPE), dev)
+    _strided(v, "v", (Tk, H, PREFILL_DV), dev)
+    B = seq_lens.numel() if isinstance(seq_lens, torch.Tensor) else 0
+    _on(seq_lens, "seq_lens", _I32, (B,), dev)
+    _on(cu_q, "cu_q", _I32, (B + 1,), dev)
+    _on(cu_kv, "cu_kv", _I32, (B + 1,), dev)
     if out is None:
         out = torch.empty((Tq, H, PREFILL_DV), dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", _BF16, (Tq, H, PREFILL_DV))
+    else:
+        _on(out, "out", _BF16, (Tq, H, PREFILL_DV), dev)
     if lse is None:
         lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
-    _need(lse, "lse", (torch.float32,), (Tq, H))
+    else:
+        _on(lse, "lse", _F32, (Tq, H), dev)
     if workspace is None:
         workspace = torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=q.device)
-    _same_device(q.device, k_nope=k_nope, k_rope=k_rope, v=v, cu_q=cu_q, cu_kv=cu_kv, seq_lens=seq_lens, out=out,
-                 lse=lse, workspace=workspace)
-    _run("dsa_mla_prefill", q.device, q.data_ptr(), q.stride(0), q.stride(1), k_nope.data_ptr(), k_nope.stride(0),
+    _run(load().dsa_mla_prefill, dev, q.data_ptr(), q.stride(0), q.stride(1), k_nope.data_ptr(), k_nope.stride(0),
          k_nope.stride(1), k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), v.stride(0), v.stride(1),
          cu_q.data_ptr(), cu_kv.data_ptr(), seq_lens.data_ptr(), B, H, Tq, Tk, entry_tokens, sm_scale,
-         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+         out.data_ptr(), lse.data_ptr(), *_space(workspace, dev))
     return out, lse
 
 
-def _norm_args(x, weight, residual, out, residual_out):
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError("x must be a [rows, d] tensor")
-    rows, d = x.shape
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    if x.dtype not in _BF16:
-        raise TypeError(f"x has dtype {x.dtype}, expected one of {_BF16}")
+_NORM_WEIGHT = _BF16 + _F32
+
+
+def _norm_args(x, weight, residual, residual_out):
+    dev = _device_of(x, "x", _BF16, (2,))
+    shape = x.shape
+    rows, d = shape
     if d > 1 and x.stride(1) != 1:
         raise ValueError("the elements of a row of x must be contiguous")
-    _need(weight, "weight", _BF16 + (torch.float32,), (d,))
+    _on(weight, "weight", _NORM_WEIGHT, (d,), dev)
     if residual is not None:
-        _need(residual, "residual", _BF16, (rows, d))
+        _on(residual, "residual", _BF16, shape, dev)
         if residual_out is None:
-            residual_out = torch.empty((rows, d), dtype=torch.bfloat16, device=x.device)
-        _need(residual_out, "residual_out", _BF16, (rows, d))
+            residual_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        else:
+            _on(residual_out, "residual_out", _BF16, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    if out is not None:
-        _need(out, "out", _BF16, (rows, d))
-    _same_device(x.device, weight=weight, residual=residual, out=out, residual_out=residual_out)
-    return rows, d, int(weight.dtype == torch.float32), residual_out
+    return dev, rows, d, int(weight.dtype == torch.float32), residual_out
 
 
 def dsa_rmsnorm(x, weight, eps: float, residual=None, out=None, residual_out=None):
@@ -556,10 +574,12 @@ def dsa_rmsnorm(x, weight, eps: float, residual=None, out=None, residual_out=Non
 
     x [rows, d] bf16 (rows may be strided, as a view of wider rows is), weight [d] bf16 or fp32.
     ``out`` and ``residual_out`` may be ``x`` and ``residual`` themselves."""
-    rows, d, w32, residual_out = _norm_args(x, weight, residual, out, residual_out)
+    dev, rows, d, w32, residual_out = _norm_args(x, weight, residual, residual_out)
     if out is None:
         out = torch.empty((rows, d), dtype=torch.bfloat16, device=x.device)
-    _run("dsa_rmsnorm", x.device, x.data_ptr(), x.stride(0), _addr(residual), weight.data_ptr(), w32, rows, d, eps,
+    else:
+        _on(out, "out", _BF16, (rows, d), dev)
+    _run(load().dsa_rmsnorm, dev, x.data_ptr(), x.stride(0), _addr(residual), weight.data_ptr(), w32, rows, d, eps,
          _addr(residual_out), out.data_ptr())
     return out, residual_out
 
@@ -570,20 +590,23 @@ def dsa_rmsnorm_fp8(x, weight, eps: float, group: int, residual=None, with_bf16:
 
     ``group`` 64 or 128 elements per scale, or 0 for one scale per row; ``out`` (bf16) is written
     when given or with ``with_bf16``.  Rows of 64 with group 64 are the fp8 index-key cache's format."""
-    rows, d, w32, residual_out = _norm_args(x, weight, residual, out, residual_out)
+    dev, rows, d, w32, residual_out = _norm_args(x, weight, residual, residual_out)
     if group not in (0, 64, 128):
         raise ValueError(f"group must be 0, 64 or 128, got {group}")
-    if out is None and with_bf16:
+    if out is not None:
+        _on(out, "out", _BF16, (rows, d), dev)
+    elif with_bf16:
         out = torch.empty((rows, d), dtype=torch.bfloat16, device=x.device)
     if codes is None:
         codes = torch.empty((rows, d), dtype=torch.float8_e4m3fn, device=x.device)
-    _need(codes, "codes", _FP8, (rows, d))
+    else:
+        _on(codes, "codes", _FP8, (rows, d), dev)
     groups = -(-d // group) if group else 1
     if scales is None:
         scales = torch.empty((rows, groups), dtype=torch.float32, device=x.device)
-    _need(scales, "scales", (torch.float32,), (rows, groups))
-    _same_device(x.device, codes=codes, scales=scales)
-    _run("dsa_rmsnorm_fp8", x.device, x.data_ptr(), x.stride(0), _addr(residual), weight.data_ptr(), w32, rows, d,
+    else:
+        _on(scales, "scales", _F32, (rows, groups), dev)
+    _run(load().dsa_rmsnorm_fp8, dev, x.data_ptr(), x.stride(0), _addr(residual), weight.data_ptr(), w32, rows, d,
          eps, group, _addr(residual_out), _addr(out), codes.data_ptr(), scales.data_ptr())
     return codes, scales, out, residual_out
 

@@ -160,14 +160,14 @@ dsa_status_t make_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int6
 }
 
 // bf16 [rows, heads, dim] with element strides (dim contiguous) as (dim, head, row): boxes of
-// 64 dims x 1 head x 128 rows, 128-byte swizzle.
+// 64 dims x 1 head x box_rows, 128-byte swizzle.
 dsa_status_t make_heads_map(CUtensorMap* map, const void* ptr, int64_t rows, int32_t heads, int32_t dim,
-                            int64_t row_stride, int64_t head_stride, const char* what) {
+                            int64_t row_stride, int64_t head_stride, uint32_t box_rows, const char* what) {
     auto enc = encode_tiled();
     if (!enc) return cuda_fail(cudaErrorNotSupported, "cuTensorMapEncodeTiled lookup");
     const cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(rows)};
     const cuuint64_t strides[2] = {cuuint64_t(head_stride) * 2, cuuint64_t(row_stride) * 2};
-    const cuuint32_t box[3] = {64, 1, 128};
+    const cuuint32_t box[3] = {64, 1, box_rows};
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
                            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -747,8 +747,8 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
         kv_rows > INT32_MAX)
         return DSA_ERR_UNSUPPORTED;
     if (!std::isfinite(sm_scale) || sm_scale < 0.f) return DSA_ERR_INVALID_ARG;
-    const int64_t slots = q_rows / 256 + batch;
-    if (slots * heads > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+    const int64_t slots = q_rows / dsa::kPrefillBlock + batch;
+    if (2 * slots * heads > INT32_MAX) return DSA_ERR_UNSUPPORTED;
     if (!cu_q || !cu_kv || !seq_lens || !aligned(cu_q, 4) || !aligned(cu_kv, 4) || !aligned(seq_lens, 4))
         return DSA_ERR_INVALID_ARG;
     if (q_rows > 0 && (!q || !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)))
@@ -766,15 +766,16 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
     if (st != DSA_OK) return st;
     if (q_rows == 0) return DSA_OK;
     CUtensorMap q_map, kn_map, kr_map, v_map;
-    st = make_heads_map(&q_map, q, q_rows, heads, DSA_PREFILL_QK_DIM, q_row_stride, q_head_stride, "prefill q");
+    st = make_heads_map(&q_map, q, q_rows, heads, DSA_PREFILL_QK_DIM, q_row_stride, q_head_stride, 128, "prefill q");
     if (st != DSA_OK) return st;
     if (kv_rows > 0) {
-        st = make_heads_map(&kn_map, k_nope, kv_rows, heads, DSA_PREFILL_NOPE_DIM, k_row_stride, k_head_stride,
+        st = make_heads_map(&kn_map, k_nope, kv_rows, heads, DSA_PREFILL_NOPE_DIM, k_row_stride, k_head_stride, 64,
                             "prefill k_nope");
         if (st != DSA_OK) return st;
-        st = make_heads_map(&v_map, v, kv_rows, heads, DSA_PREFILL_V_DIM, v_row_stride, v_head_stride, "prefill v");
+        st = make_heads_map(&v_map, v, kv_rows, heads, DSA_PREFILL_V_DIM, v_row_stride, v_head_stride, 128,
+                            "prefill v");
         if (st != DSA_OK) return st;
-        st = make_rows_map(&kr_map, k_rope, kv_rows, DSA_PREFILL_ROPE_DIM, 128, "prefill k_rope", k_rope_stride);
+        st = make_rows_map(&kr_map, k_rope, kv_rows, DSA_PREFILL_ROPE_DIM, 64, "prefill k_rope", k_rope_stride);
         if (st != DSA_OK) return st;
     } else {
         kn_map = kr_map = v_map = q_map;  // no entry: the kernel loads none

@@ -167,6 +167,7 @@ cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map
 // Latent attention over ragged prompts, expanded form: per-head 128 + 64 shared key dims, 128 value dims.
 constexpr int kPrefillQk = 192;
 constexpr int kPrefillDv = 128;
+constexpr int kPrefillBlock = 512;  // rows of a request that share a pass over its entries
 struct PrefillParams {
     const int32_t* cu_q;       // [batch + 1] first row of each request
     const int32_t* cu_kv;      // [batch + 1] first entry of each request
@@ -179,10 +180,11 @@ struct PrefillParams {
     int32_t batch;
     int32_t heads;
     int32_t entry_tokens;      // tokens per entry
-    int32_t slots;             // q_rows / 256 + batch blocks of up to 256 rows
+    int32_t slots;             // q_rows / 512 + batch blocks of up to 512 rows
     float sm_scale_log2;       // sm_scale * log2(e), above 0
 };
-// Maps of 128-byte-swizzled boxes of 128 rows x 64 dims: q, k_nope and v as (dim, head, row), k_rope as (dim, row).
+// Maps of 128-byte-swizzled boxes of 64 dims x 128 rows (q, v) or 64 rows (k_nope, k_rope): q, k_nope and v
+// as (dim, head, row), k_rope as (dim, row).
 cudaError_t launch_mla_prefill(const CUtensorMap& q_map, const CUtensorMap& kn_map, const CUtensorMap& kr_map,
                                const CUtensorMap& v_map, const PrefillParams& p, cudaStream_t stream);
 

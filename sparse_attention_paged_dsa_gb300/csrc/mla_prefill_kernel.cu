@@ -7,29 +7,34 @@
 // Row i of a request with n rows and seq_len tokens sees its first
 // ceil((seq_len - (n - 1 - i)) / entry_tokens) entries.
 //
-// One CTA per (256 rows of a request, head): two 128-row query tiles share each
-// 128-entry tile of keys and values.  Roles (320 threads):
+// A cluster of two CTAs takes 512 rows of a request and one head: two query tiles
+// of 256 rows, each CTA holding 128 rows of both.  All MMAs are cta_group::2
+// (M = 256: 128 rows in each CTA's TMEM; N = 128), issued by the leader.  Their
+// second operand is split between the two CTAs' shared memory: each loads half of
+// every 128-entry tile's keys (64 entries) and half of its values (64 dims), so a
+// tile costs an SM 40 KB of loads instead of 80, its shared memory holds three
+// tiles, and the operand reads fit its bandwidth.  Roles of a CTA (384 threads):
 //   * warps 0-3 and 4-7: softmax of query tile 0 and 1, one row per thread: the
 //     row of S from TMEM to registers, its maximum (raised only when a tile
 //     passes it by more than 2^8; the accumulator is then rescaled in TMEM),
 //     2^x, and P (bf16) back into S's columns.
-//   * warp 8: tcgen05.mma, all M = 128, N = 128.  S = Q . K^T from shared memory
-//     (12 steps); O += P . V with P from TMEM and V read in place as an MN-major
-//     operand (up to 8 steps).  Order per tile: PV of tile 0, next QK of tile 0,
-//     PV of tile 1, next QK of tile 1, so that one tile's products run while the
-//     other tile's softmax does.
+//   * warp 8 (leader): tcgen05.mma.  S = Q . K^T from shared memory (12 steps);
+//     O += P . V with P from TMEM and V read in place as an MN-major operand (up to
+//     8 steps).  Order per tile: PV of query tile 0, its next QK, PV of query tile
+//     1, its next QK, so that one tile's products run while the other's softmax does.
 //   * warp 9: TMA.  q once; keys (two 64-dim slabs of the head's own, one shared
-//     by all heads) and values (two slabs) through a ring of eight 16 KB slabs.
+//     by all heads) and values, three stages each.  Both CTAs' copies count on the
+//     leader's barriers.
+//   * warp 10: zeroes the value rows behind the last entry (see below).
 // TMEM: S/P of the two tiles 2 x 128 columns, O 2 x 128: all 512.
 //
 // The shared 64 rotary key dims are loaded from their one copy per entry, so no
 // 192-wide key is ever built, and every operand may be a strided view.
 //
-// What bounds it: the tensor cores: 20 MMAs of 128 x 128 x 16 per (128 rows, 128
-// entries), 1,280 SM cycles at full rate, of which the 12 with both operands in
-// shared memory also take all of its bandwidth.
-// Every wait is bounded (about 1 s); a timeout sets an error bit, the roles
-// drain, and TMEM is freed.
+// What bounds it: the tensor cores: 20 MMA steps of 128 x 128 x 16 per SM for each
+// (128 rows, 128 entries), 1,280 SM cycles at full rate.
+// Every wait is bounded (about 1 s) but the cluster barriers, which every thread
+// reaches; a timeout sets an error bit, the roles drain, and TMEM is freed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -43,14 +48,19 @@
 namespace dsa {
 namespace {
 
-constexpr int kTile = 128;                      // rows of a query tile, entries of a key tile
+constexpr int kTile = 128;                      // rows of a CTA's query tile, entries of a key tile
 constexpr int kSlabB = kTile * 128;             // 128 rows x 64 bf16 dims, 16 KiB
+constexpr int kHalfB = kSlabB / 2;              // 64 rows x 64 dims: a CTA's half of a key slab
 constexpr int kQkSlabs = kPrefillQk / 64;       // 3: two of the head's own, one rotary
-constexpr int kRing = 8;
+constexpr int kStages = 3;                      // key and value tiles in shared memory
+constexpr int kStageK = kQkSlabs * kHalfB;      // 24 KiB
+constexpr int kStageV = kSlabB;                 // 128 entries x this CTA's 64 value dims
 constexpr int kOffQt = 0;                       // q: 2 tiles x 3 slabs
-constexpr int kOffRing = kOffQt + 2 * kQkSlabs * kSlabB;
-constexpr int kOffCtlP = kOffRing + kRing * kSlabB;
-constexpr int kThreadsP = 320;
+constexpr int kOffK = kOffQt + 2 * kQkSlabs * kSlabB;
+constexpr int kOffV = kOffK + kStages * kStageK;
+constexpr int kOffCtlP = kOffV + kStages * kStageV;
+constexpr int kThreadsP = 384;
+constexpr int kRegsSoftmax = 200, kRegsOther = 104;  // 8 x 200 + 4 x 104 = 12 x 168 a warp lane
 constexpr uint32_t kTmemColsP = 512;
 constexpr uint32_t kColSP = 0;    // S / P of tile i at 128 i
 constexpr uint32_t kColOP = 256;  // O of tile i at 256 + 128 i
@@ -58,9 +68,9 @@ constexpr float kRaiseLog2 = 8.0f;
 constexpr float kLn2P = 0.69314718055994531f;
 
 struct __align__(8) PrefillCtl {
-    uint64_t full[kRing], empty[kRing];
+    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-    uint64_t all_done;
+    uint64_t tail_landed, tail_ready, all_done;
     uint32_t tmem_base;
     int abort;
     int req;
@@ -85,16 +95,93 @@ __device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
     return d;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], issued by one thread: A row r in TMEM lane r, column c the bf16
-// pair (2 c, 2 c + 1).
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// Two-CTA MMAs, issued by one thread of the leader: M = 256 (128 rows of A and D in each CTA), each
+// CTA's shared memory (at the same offsets) holding half of B.  A from shared memory:
+__device__ __forceinline__ void umma2_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// A from TMEM: row r in lane r, column c the bf16 pair (2 c, 2 c + 1).
+__device__ __forceinline__ void umma2_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// Arrive once on the barrier at this offset in both CTAs when every MMA this thread issued has completed.
+__device__ __forceinline__ void umma2_commit(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(uint16_t(3))
+        : "memory");
+}
+
+// TMA loads into this CTA that count on a barrier given by its shared::cluster address.
+__device__ __forceinline__ void tma2_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
+                                             int32_t z, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void tma2_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
+                                             uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// Arrive on a barrier of either CTA (shared::cluster address), ordering this thread's work before it.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// mbar_wait that also orders what the other CTA did before its arrivals.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+    const uint32_t a = smem_u32(bar);
+    const auto try_wait = [&] {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(a), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (try_wait()) return true;
+    const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+    while (true) {
+        if (try_wait()) return true;
+        if (*abort) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+    }
+}
+
+__device__ __forceinline__ void tmem2_alloc(uint32_t* dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
+                 "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem2_dealloc(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
 // Entries seen by a row whose last visible token is number `len` (from 1).
@@ -146,248 +233,248 @@ __device__ __forceinline__ void wait_landed_p(uint64_t* bar, uint32_t parity) {
     }
 }
 
-__global__ void __launch_bounds__(kThreadsP, 1)
+__global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kn_map,
                        const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap v_map,
                        const PrefillParams p) {
     extern __shared__ uint8_t smem_raw[];
+    // Dynamic shared memory starts at the same offset in both CTAs, so the operands and barriers do too.
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     PrefillCtl& ctl = *reinterpret_cast<PrefillCtl*>(tiles + kOffCtlP);
     const uint32_t s_base = smem_u32(tiles);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
+    const int rank = int(cluster_rank());  // 0: the leader
 
     // Heads vary fastest, and the last (longest) row blocks come first.
-    const int head = int(blockIdx.x % unsigned(p.heads));
-    const int slot_t = p.slots - 1 - int(blockIdx.x / unsigned(p.heads));
+    const unsigned unit = blockIdx.x >> 1;
+    const int head = int(unit % unsigned(p.heads));
+    const int slot_t = p.slots - 1 - int(unit / unsigned(p.heads));
     if (threadIdx.x == 0) ctl.req = -1;
     __syncthreads();
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
 
-    // Request b owns the slots [cu_q[b] / 256 + b, cu_q[b + 1] / 256 + b + 1): at least as many as it
-    // has blocks of 256 rows, so the launch depends on the row count and the batch alone.
+    // Request b owns the slots [cu_q[b] / 512 + b, cu_q[b + 1] / 512 + b + 1): at least as many as it
+    // has blocks of 512 rows, so the launch depends on the row count and the batch alone.
     uint32_t bad = 0;
     for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
-        const int64_t s0 = int64_t(__ldg(p.cu_q + b)) / (2 * kTile) + b;
-        const int64_t s1 = int64_t(__ldg(p.cu_q + b + 1)) / (2 * kTile) + b + 1;
+        const int64_t s0 = int64_t(__ldg(p.cu_q + b)) / kPrefillBlock + b;
+        const int64_t s1 = int64_t(__ldg(p.cu_q + b + 1)) / kPrefillBlock + b + 1;
         if (slot_t >= s0 && slot_t < s1) ctl.req = b;
         if (blockIdx.x == 0) Request(p, b, bad);  // every request is checked, also those without rows
     }
     if (bad) atomicOr(p.err, bad);
     __syncthreads();
     const int b = ctl.req;
-    if (b < 0) return;
+    if (b < 0) return;  // both CTAs alike, before any cluster barrier
     const Request rq(p, b, bad);
-    const int64_t block = slot_t - (int64_t(__ldg(p.cu_q + b)) / (2 * kTile) + b);
-    if (block < 0 || block * 2 * kTile >= rq.rows) return;
-    const int row0 = int(block) * 2 * kTile;              // of the request
-    const int nrows[2] = {min(rq.rows - row0, kTile), min(max(rq.rows - row0 - kTile, 0), kTile)};
-    int limit[2], ntiles[2];                              // entries the tile's last row sees
+    const int64_t block = slot_t - (int64_t(__ldg(p.cu_q + b)) / kPrefillBlock + b);
+    if (block < 0 || block * kPrefillBlock >= rq.rows) return;
+    // Query tile i: rows [row0 + 256 i, + 256) of the request, the second 128 of them in CTA 1.
+    const int row0 = int(block) * kPrefillBlock;
+    int limit[2], ntiles[2];  // entries that the tile's last row sees
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        limit[i] = nrows[i] > 0 ? rq.seen(row0 + i * kTile + nrows[i] - 1, p.entry_tokens) : 0;
+        const int last = min(rq.rows, row0 + (i + 1) * 2 * kTile) - 1;
+        limit[i] = last >= row0 + i * 2 * kTile ? rq.seen(last, p.entry_tokens) : 0;
         ntiles[i] = (limit[i] + kTile - 1) / kTile;
     }
     const int nt = max(ntiles[0], ntiles[1]);
     const int limit_max = max(limit[0], limit[1]);
+    // Value rows behind the last entry that any of these rows sees belong to other requests or hold
+    // nothing.  Products stop at a 16-entry step, and where that is not the end of the entries the rows
+    // up to it are zeroed (weights there are 0, but 0 x NaN is not): the last tile's values count on a
+    // barrier of each CTA, whose warp 10 zeroes them and tells the leader.
+    const bool tail = (limit_max & 15) != 0;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kRing; ++i) {
-            mbar_init(&ctl.full[i], 1);
-            mbar_init(&ctl.empty[i], 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&ctl.k_full[i], 1);
+            mbar_init(&ctl.k_empty[i], 1);
+            mbar_init(&ctl.v_full[i], 1);
+            mbar_init(&ctl.v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.q_full[i], 1);
             mbar_init(&ctl.s_full[i], 1);
-            mbar_init(&ctl.p_full[i], 4);
+            mbar_init(&ctl.p_full[i], 8);  // four warps of each CTA
             mbar_init(&ctl.o_full[i], 1);
         }
+        mbar_init(&ctl.tail_landed, 1);
+        mbar_init(&ctl.tail_ready, 2);
         mbar_init(&ctl.all_done, 1);
         ctl.abort = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
-        tmem_alloc(&ctl.tmem_base, kTmemColsP);
-        tmem_relinquish();
-    }
+    if (warp == 8) tmem2_alloc(&ctl.tmem_base, kTmemColsP);
     tc_fence_before_sync();
-    __syncthreads();
+    cluster_sync_all();
     tc_fence_after_sync();
     const uint32_t tmem_base = ctl.tmem_base;
 
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 9) {
         // ================= TMA =================
         if (lane == 0 && nt > 0) {
             const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
-            int pos = 0;  // slabs issued
             bool stop = false;
-            const auto slab = [&](const CUtensorMap* map, bool shared_dims, int x, int row) {
-                const int slot = pos & (kRing - 1);
-                if (stop || !mbar_wait(&ctl.empty[slot], uint32_t((pos / kRing) & 1) ^ 1u, &ctl.abort)) {
+            const auto load_q = [&](int i) {
+                const uint32_t bar = cluster_addr(&ctl.q_full[i], 0);
+                if (rank == 0) mbar_arrive_expect_tx(&ctl.q_full[i], uint32_t(2 * kQkSlabs * kSlabB));
+                for (int s = 0; s < kQkSlabs; ++s)
+                    tma2_load_3d(s_base + kOffQt + (i * kQkSlabs + s) * kSlabB, &q_map, bar, 64 * s, head,
+                                 rq.q0 + row0 + i * 2 * kTile + rank * kTile, pol_q);
+            };
+            const auto load_k = [&](int j) {  // this CTA's 64 entries of tile j
+                const int st = j % kStages;
+                if (stop || !mbar_wait(&ctl.k_empty[st], uint32_t((j / kStages) & 1) ^ 1u, &ctl.abort)) {
                     stop = true;
                     return;
                 }
-                mbar_arrive_expect_tx(&ctl.full[slot], uint32_t(kSlabB));
-                uint8_t* dst = tiles + kOffRing + slot * kSlabB;
-                if (shared_dims)
-                    tma_load_2d(dst, map, &ctl.full[slot], x, row, pol_kv);
-                else
-                    tma_load_3d(dst, map, &ctl.full[slot], x, head, row, pol_kv);
-                ++pos;
+                const uint32_t bar = cluster_addr(&ctl.k_full[st], 0);
+                if (rank == 0) mbar_arrive_expect_tx(&ctl.k_full[st], uint32_t(2 * kStageK));
+                const uint32_t dst = s_base + kOffK + st * kStageK;
+                const int row = rq.kv0 + j * kTile + rank * (kTile / 2);
+                tma2_load_3d(dst, &kn_map, bar, 0, head, row, pol_kv);
+                tma2_load_3d(dst + kHalfB, &kn_map, bar, 64, head, row, pol_kv);
+                tma2_load_2d(dst + 2 * kHalfB, &kr_map, bar, 0, row, pol_kv);
             };
-            const auto load_q = [&](int i) {
-                mbar_arrive_expect_tx(&ctl.q_full[i], uint32_t(kQkSlabs * kSlabB));
-                for (int s = 0; s < kQkSlabs; ++s)
-                    tma_load_3d(tiles + kOffQt + (i * kQkSlabs + s) * kSlabB, &q_map, &ctl.q_full[i], 64 * s, head,
-                                rq.q0 + row0 + i * kTile, pol_q);
-            };
-            const auto load_k = [&](int j) {
-                slab(&kn_map, false, 0, rq.kv0 + j * kTile);
-                slab(&kn_map, false, 64, rq.kv0 + j * kTile);
-                slab(&kr_map, true, 0, rq.kv0 + j * kTile);
+            const auto load_v = [&](int j) {  // this CTA's 64 value dims of tile j
+                const int st = j % kStages;
+                if (stop || !mbar_wait(&ctl.v_empty[st], uint32_t((j / kStages) & 1) ^ 1u, &ctl.abort)) {
+                    stop = true;
+                    return;
+                }
+                const bool last = tail && j == nt - 1;
+                const uint32_t bar = last ? cluster_addr(&ctl.tail_landed, uint32_t(rank)) : cluster_addr(&ctl.v_full[st], 0);
+                if (last)
+                    mbar_arrive_expect_tx(&ctl.tail_landed, uint32_t(kStageV));
+                else if (rank == 0)
+                    mbar_arrive_expect_tx(&ctl.v_full[st], uint32_t(2 * kStageV));
+                tma2_load_3d(s_base + kOffV + st * kStageV, &v_map, bar, 64 * rank, head, rq.kv0 + j * kTile, pol_kv);
             };
             if (ntiles[0] > 0) load_q(0);
             load_k(0);
             if (ntiles[1] > 0) load_q(1);
-            for (int j = 0; j < nt && !stop; ++j) {  // in the order of use: K(0) V(0) K(1) V(1) ...
-                slab(&v_map, false, 0, rq.kv0 + j * kTile);
-                slab(&v_map, false, 64, rq.kv0 + j * kTile);
+            for (int j = 0; j < nt && !stop; ++j) {
+                load_v(j);
                 if (j + 1 < nt) load_k(j + 1);
             }
             if (stop) {
                 atomicOr(p.err, kErrWaitTimeout);
                 ctl.abort = 1;
             }
-            // no copy outlives the CTA (bounded waits; they have landed unless a role gave up)
-            for (int i = pos - 1; i >= 0 && i >= pos - kRing; --i)
-                wait_landed_p(&ctl.full[i & (kRing - 1)], uint32_t(i / kRing) & 1u);
-            for (int i = 0; i < 2; ++i)
-                if (ntiles[i] > 0) wait_landed_p(&ctl.q_full[i], 0);
+            // No copy outlives the cluster (bounded waits; they have landed unless a role gave up).  The
+            // leader's barriers count both CTAs' copies, and neither CTA leaves before the other.
+            if (rank == 0) {
+                for (int j = max(nt - kStages, 0); j < nt; ++j) {
+                    wait_landed_p(&ctl.k_full[j % kStages], uint32_t(j / kStages) & 1u);
+                    if (!(tail && j == nt - 1)) wait_landed_p(&ctl.v_full[j % kStages], uint32_t(j / kStages) & 1u);
+                }
+                for (int i = 0; i < 2; ++i)
+                    if (ntiles[i] > 0) wait_landed_p(&ctl.q_full[i], 0);
+            }
+            if (tail) wait_landed_p(&ctl.tail_landed, 0);
         }
         __syncwarp();
-    } else if (warp == 8) {
-        // ================= MMA =================
-        constexpr uint32_t kIdescQk = idesc_bf16_f32(kTile, kTile);
-        constexpr uint32_t kIdescPv = idesc_bf16_f32(kTile, kPrefillDv) | (1u << 16);  // B (V) MN-major
-        bool stop = false;
-        const auto ring_wait = [&](int pos) {
-            const bool ok = mbar_wait(&ctl.full[pos & (kRing - 1)], uint32_t(pos / kRing) & 1u, &ctl.abort);
-            if (!__all_sync(0xffffffffu, ok)) stop = true;
-        };
-        const auto ring_free = [&](int pos) { umma_commit(&ctl.empty[pos & (kRing - 1)]); };
-        const auto ring_addr = [&](int pos) { return s_base + kOffRing + (pos & (kRing - 1)) * kSlabB; };
-        // S(tile i) = Q_i . K(j)^T
-        const auto qk = [&](int i, int j) {
-            if (lane == 0) {
+    } else if (warp == 10) {
+        // ================= the last tile's value rows =================
+        if (tail) {
+            const bool ok = mbar_wait(&ctl.tail_landed, 0, &ctl.abort);
+            if (__all_sync(0xffffffffu, ok)) {
+                const int valid = limit_max - (nt - 1) * kTile;
+                const int fill = 16 - (valid & 15);
+                uint8_t* v = tiles + kOffV + ((nt - 1) % kStages) * kStageV;
+                for (int i = lane; i < fill * 8; i += 32)
+                    *reinterpret_cast<uint4*>(v + (valid + (i >> 3)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                asm volatile("fence.proxy.async;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&ctl.tail_ready, 0));
+            }
+        }
+    } else if (warp == 8 && rank == 0) {
+        // ================= MMA (the leader's) =================
+        if (lane == 0) {
+            constexpr uint32_t kIdescQk = idesc_bf16_f32(2 * kTile, kTile);
+            constexpr uint32_t kIdescPv = idesc_bf16_f32(2 * kTile, kPrefillDv) | (1u << 16);  // B (V) MN-major
+            // S(tile i) = Q_i . K(j)^T
+            const auto qk = [&](int i, int j) {
 #pragma unroll
                 for (int s = 0; s < kQkSlabs; ++s) {
                     const uint64_t a = smem_desc_kmajor_sw128(s_base + kOffQt + (i * kQkSlabs + s) * kSlabB);
-                    const uint64_t bd = smem_desc_kmajor_sw128(ring_addr(5 * j + s));
+                    const uint64_t bd = smem_desc_kmajor_sw128(s_base + kOffK + (j % kStages) * kStageK + s * kHalfB);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ss(tmem_base + kColSP + 128u * i, a + 2u * kk, bd + 2u * kk, kIdescQk,
-                                     (s | kk) != 0 ? 1u : 0u);
+                        umma2_bf16_ss(tmem_base + kColSP + 128u * i, a + 2u * kk, bd + 2u * kk, kIdescQk,
+                                      (s | kk) != 0 ? 1u : 0u);
                 }
-                umma_commit(&ctl.s_full[i]);
-            }
-            __syncwarp();
-        };
-        // O(tile i) += P_i . V(j), over the 16-entry steps below the tile's limit
-        const auto pv = [&](int i, int j) {
-            if (lane == 0) {
+                umma2_commit(&ctl.s_full[i]);
+            };
+            // O(tile i) += P_i . V(j), over the 16-entry steps below the tile's limit
+            const auto pv = [&](int i, int j) {
                 const int steps = min((limit[i] - j * kTile + 15) >> 4, kTile / 16);
-                // Slabs 5 j + 3 and 5 j + 4 may sit at the two ends of the ring: one N = 64 half each.
-                const uint32_t v0 = ring_addr(5 * j + 3), v1 = ring_addr(5 * j + 4);
-                if (v1 > v0) {
-                    for (int kk = 0; kk < steps; ++kk)
-                        umma_bf16_ts(tmem_base + kColOP + 128u * i, tmem_base + kColSP + 128u * i + 8u * kk,
-                                     desc_mn_sw128(v0 + kk * 2048, kSlabB), kIdescPv, (j | kk) != 0 ? 1u : 0u);
+                const uint64_t bd = desc_mn_sw128(s_base + kOffV + (j % kStages) * kStageV, kSlabB);
+                const auto step = [&](int kk) {
+                    umma2_bf16_ts(tmem_base + kColOP + 128u * i, tmem_base + kColSP + 128u * i + 8u * kk,
+                                  bd + 128u * kk, kIdescPv, (j | kk) != 0 ? 1u : 0u);
+                };
+                if (steps == kTile / 16) {
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk) step(kk);
                 } else {
-                    constexpr uint32_t kIdescHalf = idesc_bf16_f32(kTile, 64) | (1u << 16);
-                    for (int kk = 0; kk < steps; ++kk) {
-                        umma_bf16_ts(tmem_base + kColOP + 128u * i, tmem_base + kColSP + 128u * i + 8u * kk,
-                                     desc_mn_sw128(v0 + kk * 2048, kSlabB), kIdescHalf, (j | kk) != 0 ? 1u : 0u);
-                        umma_bf16_ts(tmem_base + kColOP + 128u * i + 64u, tmem_base + kColSP + 128u * i + 8u * kk,
-                                     desc_mn_sw128(v1 + kk * 2048, kSlabB), kIdescHalf, (j | kk) != 0 ? 1u : 0u);
-                    }
+#pragma unroll 1
+                    for (int kk = 0; kk < steps; ++kk) step(kk);
                 }
-                if (j + 1 == ntiles[i]) umma_commit(&ctl.o_full[i]);
-            }
-            __syncwarp();
-        };
-        const auto wait_p = [&](int i, int j) {
-            const bool ok = mbar_wait(&ctl.p_full[i], uint32_t(j & 1), &ctl.abort);
-            if (!__all_sync(0xffffffffu, ok)) stop = true;
-            tc_fence_after_sync();
-        };
-        if (nt > 0) {
-            for (int s = 0; s < kQkSlabs && !stop; ++s) ring_wait(s);
-            for (int i = 0; i < 2 && !stop; ++i) {
-                if (ntiles[i] == 0) continue;
-                if (!__all_sync(0xffffffffu, mbar_wait(&ctl.q_full[i], 0, &ctl.abort))) {
-                    stop = true;
-                    break;
-                }
+                if (j + 1 == ntiles[i]) umma2_commit(&ctl.o_full[i]);
+            };
+            const auto wait_k = [&](int j) {
+                const bool ok = mbar_wait_cluster(&ctl.k_full[j % kStages], uint32_t(j / kStages) & 1u, &ctl.abort);
                 tc_fence_after_sync();
-                qk(i, 0);
+                return ok;
+            };
+            bool ok = nt == 0 || wait_k(0);
+            for (int i = 0; i < 2 && ok; ++i) {
+                if (ntiles[i] == 0) continue;
+                ok = mbar_wait_cluster(&ctl.q_full[i], 0, &ctl.abort);
+                tc_fence_after_sync();
+                if (ok) qk(i, 0);
             }
-            if (!stop && lane == 0)
-                for (int s = 0; s < kQkSlabs; ++s) ring_free(s);
-            __syncwarp();
-            for (int j = 0; j < nt && !stop; ++j) {
-                ring_wait(5 * j + 3);
-                if (!stop) ring_wait(5 * j + 4);
-                if (stop) break;
-                // Value rows behind the last entry that any of these rows sees belong to other requests
-                // or hold nothing: zeroed up to the end of the last step (weights there are 0, but 0 x NaN is not).
-                const int valid = limit_max - j * kTile;
-                if (valid < kTile && (valid & 15)) {
-                    const int fill = 16 - (valid & 15);
-                    for (int i = lane; i < fill * 16; i += 32) {
-                        const int row = valid + (i >> 4), half = (i >> 3) & 1, ch = i & 7;
-                        *reinterpret_cast<uint4*>(tiles + kOffRing + ((5 * j + 3 + half) & (kRing - 1)) * kSlabB +
-                                                  row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                bool next_k = false;
+            if (ok && nt > 0) umma2_commit(&ctl.k_empty[0]);
+#pragma unroll 1
+            for (int j = 0; j < nt && ok; ++j) {
+                const int st = j % kStages;
+                bool have_k = false;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (j < ntiles[i]) {
-                        wait_p(i, j);
-                        if (stop) break;
-                        pv(i, j);
+                    if (ok && j < ntiles[i]) {
+                        ok = mbar_wait_cluster(&ctl.p_full[i], uint32_t(j & 1), &ctl.abort);
+                        if (ok)
+                            ok = tail && j == nt - 1
+                                     ? mbar_wait_cluster(&ctl.tail_ready, 0, &ctl.abort)
+                                     : mbar_wait_cluster(&ctl.v_full[st], uint32_t(j / kStages) & 1u, &ctl.abort);
+                        tc_fence_after_sync();
+                        if (ok) pv(i, j);
                     }
-                    if (i == 1 && lane == 0) {
-                        ring_free(5 * j + 3);
-                        ring_free(5 * j + 4);
-                    }
-                    if (j + 1 < ntiles[i]) {
-                        if (!next_k) {
-                            next_k = true;
-                            for (int s = 0; s < kQkSlabs && !stop; ++s) ring_wait(5 * (j + 1) + s);
-                            if (stop) break;
-                            tc_fence_after_sync();
-                        }
-                        qk(i, j + 1);
+                    if (ok && i == 1) umma2_commit(&ctl.v_empty[st]);
+                    if (ok && j + 1 < ntiles[i]) {
+                        if (!have_k) ok = wait_k(j + 1);
+                        have_k = true;
+                        if (ok) qk(i, j + 1);
                     }
                 }
-                if (!stop && j + 1 < nt && lane == 0)
-                    for (int s = 0; s < kQkSlabs; ++s) ring_free(5 * (j + 1) + s);
-                __syncwarp();
+                if (ok && j + 1 < nt) umma2_commit(&ctl.k_empty[(j + 1) % kStages]);
             }
-        }
-        if (lane == 0) {
-            if (stop) {
+            if (!ok) {
                 atomicOr(p.err, kErrWaitTimeout);
                 ctl.abort = 1;
             }
-            umma_commit(&ctl.all_done);  // every MMA issued has completed when this arrives
+            umma2_commit(&ctl.all_done);
+            wait_landed_p(&ctl.all_done, 0);  // every MMA issued has completed
         }
         __syncwarp();
-    } else {
+    } else if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ================= softmax: warps 0-3 tile 0, warps 4-7 tile 1 =================
         const int i = warp >> 2;
         const int r = (warp & 3) * 32 + lane;  // row of the tile
@@ -395,8 +482,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const uint32_t s_addr = lane_addr + kColSP + 128u * i;
         const uint32_t o_addr = lane_addr + kColOP + 128u * i;
         const float c2 = p.sm_scale_log2;
-        const int row = row0 + i * kTile + r;
-        const bool live_row = r < nrows[i];
+        const int row = row0 + i * 2 * kTile + rank * kTile + r;  // of the request
+        const bool live_row = row < rq.rows;
+        const uint32_t p_bar = cluster_addr(&ctl.p_full[i], 0);
         const int see = live_row ? rq.seen(row, p.entry_tokens) : limit[i];
         float m = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
@@ -473,7 +561,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             tmem_st_wait();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.p_full[i]);
+            if (lane == 0) mbar_arrive_cluster(p_bar);
         }
         // ---- output
         if (!failed && ntiles[i] > 0) {
@@ -485,7 +573,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 atomicOr(p.err, kErrWaitTimeout);
                 ctl.abort = 1;
             }
-        } else if (nrows[i] > 0) {
+        } else if (__any_sync(0xffffffffu, live_row)) {
             tc_fence_after_sync();
             const float l = l2.x + l2.y;
             const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -519,16 +607,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         }
     }
 
+    // The leader's last arrival here: none of its earlier ones is still under way to this CTA.
+    if (warp == 8 && rank == 1) wait_landed_p(&ctl.all_done, 0);
+    __syncwarp();
     tc_fence_before_sync();
-    __syncthreads();
-    if (warp == 8) {
-        const uint32_t addr = smem_u32(&ctl.all_done);
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(addr, 0) && global_timer_ns() - t0 < kWaitLimitNs) {
-        }
-        tc_fence_after_sync();
-        tmem_dealloc(tmem_base, kTmemColsP);
-    }
+    cluster_sync_all();  // no CTA leaves while the other may read its memory or arrive on its barriers
+    tc_fence_after_sync();
+    if (warp == 8) tmem2_dealloc(tmem_base, kTmemColsP);
 }
 
 }  // namespace
@@ -545,7 +630,7 @@ cudaError_t launch_mla_prefill(const CUtensorMap& q_map, const CUtensorMap& kn_m
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(p.slots) * unsigned(p.heads));
+    cfg.gridDim = dim3(2u * unsigned(p.slots) * unsigned(p.heads));
     cfg.blockDim = dim3(kThreadsP);
     cfg.dynamicSmemBytes = size_t(kSmemP);
     cfg.stream = stream;

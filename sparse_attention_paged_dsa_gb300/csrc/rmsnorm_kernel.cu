@@ -61,6 +61,9 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[kVec],
     }
 }
 
+// A correctly rounded quotient, kept out of line: only groups at the ends of fp32's range take it.
+__device__ __noinline__ float divide(float a, float b) { return a / b; }
+
 // Sum or maximum over the `lanes` (a power of two) neighbouring lanes of each group.
 template <bool kMax>
 __device__ __forceinline__ float lanes_reduce(float x, int lanes) {
@@ -176,19 +179,23 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const RmsNormParams p) {
             amax = lanes_reduce<true>(amax, glanes);
         }
         if (!live || v >= nvec) continue;
-        float scale = amax / kE4m3Max;
+        float scale = amax * (1.f / kE4m3Max);
         if (!(scale > 0.f)) scale = 1.f;  // an all-zero group (or one below fp32's range): codes 0
-        // 448 / amax would pass fp32's range for a tiny amax: such groups divide element by element.
-        const bool tiny = !(amax > 1e-30f);
-        const float inv = kE4m3Max / amax;
         uint8_t* codes = p.codes + row * p.d + v * kVec;
+        float c[kVec];
+        if (amax > 1e-30f && amax < 1e30f) {
+            const float inv = __fdividef(kE4m3Max, amax);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) c[i] = h[j][i] * inv;
+        } else {  // 448 / amax or its approximation would leave fp32's range
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) c[i] = divide(h[j][i], scale);
+        }
         uint32_t pk[2];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float a = tiny ? h[j][2 * i] / scale : h[j][2 * i] * inv;
-            const float b = tiny ? h[j][2 * i + 1] / scale : h[j][2 * i + 1] * inv;
-            const uint32_t c = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-            pk[i >> 1] = (i & 1) ? pk[i >> 1] | (c << 16) : c;
+            const uint32_t e = __nv_cvt_float2_to_fp8x2(make_float2(c[2 * i], c[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+            pk[i >> 1] = (i & 1) ? pk[i >> 1] | (e << 16) : e;
         }
         if constexpr (kWide) {
             *reinterpret_cast<uint2*>(codes) = make_uint2(pk[0], pk[1]);

@@ -75,7 +75,8 @@ def run(lib, case, **kw):
 
 
 @pytest.mark.parametrize("e", [1, 4])
-@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 64, 100, 127, 128, 129, 130, 200, 255, 256, 257, 300, 400, 513, 1000])
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 64, 100, 127, 128, 129, 130, 200, 255, 256, 257, 300, 384, 385, 400, 511, 512, 513, 767, 768,
+                               769, 1000, 1025, 1300])
 def test_prefill_one_prompt(gpu_lib, n, e):
     """Prompts of every kind of partial tile, an entry per token or per four."""
     case = Case([n], [n], heads=2, e=e, seed=n)
