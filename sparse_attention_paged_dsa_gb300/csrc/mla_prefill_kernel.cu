@@ -143,7 +143,12 @@ __device__ __forceinline__ void tma2_load_2d(uint32_t dst, const CUtensorMap* ma
         : "memory");
 }
 
-// Arrive on a barrier of either CTA (shared::cluster address), ordering this thread's work before it.
+// Arrive on a barrier of either CTA (shared::cluster address).  What the arrivals on p_full order is
+// tensor memory, through the tcgen05 fences; the cluster-scope release and acquire below cost 250 to 470
+// cycles a time on the MMA's path and are kept for ordinary stores (the zeroed value rows).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -242,7 +247,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     PrefillCtl& ctl = *reinterpret_cast<PrefillCtl*>(tiles + kOffCtlP);
     const uint32_t s_base = smem_u32(tiles);
-    const int warp = threadIdx.x >> 5;
+    const int warp = uniform(int(threadIdx.x) >> 5);
     const int lane = threadIdx.x & 31;
     const int rank = int(cluster_rank());  // 0: the leader
 
@@ -395,29 +400,41 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp == 8 && rank == 0) {
         // ================= MMA (the leader's) =================
-        if (lane == 0) {
-            constexpr uint32_t kIdescQk = idesc_bf16_f32(2 * kTile, kTile);
-            constexpr uint32_t kIdescPv = idesc_bf16_f32(2 * kTile, kPrefillDv) | (1u << 16);  // B (V) MN-major
-            // S(tile i) = Q_i . K(j)^T
-            const auto qk = [&](int i, int j) {
+        // The whole warp runs the loop; one elected lane issues.
+        constexpr uint32_t kIdescQk = idesc_bf16_f32(2 * kTile, kTile);
+        constexpr uint32_t kIdescPv = idesc_bf16_f32(2 * kTile, kPrefillDv) | (1u << 16);  // B (V) MN-major
+        const uint32_t tmem = uint32_t(uniform(int(tmem_base)));
+        const uint32_t sb = uint32_t(uniform(int(s_base)));
+        const int n_all = uniform(nt);
+        const int n_of[2] = {uniform(ntiles[0]), uniform(ntiles[1])};
+        const int lim[2] = {uniform(limit[0]), uniform(limit[1])};
+        const uint64_t q_desc = smem_desc_kmajor_sw128(sb + kOffQt);
+        const uint64_t k_desc = smem_desc_kmajor_sw128(sb + kOffK);
+        const uint64_t v_desc = desc_mn_sw128(sb + kOffV, kSlabB);
+        const bool issuer = elect_one();
+        // S(tile i) = Q_i . K^T, keys in stage st
+        const auto qk = [&](int i, int st) {
+            if (issuer) {
+                const uint64_t a = q_desc + uint32_t(i * kQkSlabs * (kSlabB >> 4));
+                const uint64_t bd = k_desc + uint32_t(st * (kStageK >> 4));
 #pragma unroll
-                for (int s = 0; s < kQkSlabs; ++s) {
-                    const uint64_t a = smem_desc_kmajor_sw128(s_base + kOffQt + (i * kQkSlabs + s) * kSlabB);
-                    const uint64_t bd = smem_desc_kmajor_sw128(s_base + kOffK + (j % kStages) * kStageK + s * kHalfB);
+                for (int s = 0; s < kQkSlabs; ++s)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma2_bf16_ss(tmem_base + kColSP + 128u * i, a + 2u * kk, bd + 2u * kk, kIdescQk,
-                                      (s | kk) != 0 ? 1u : 0u);
-                }
+                        umma2_bf16_ss(tmem + kColSP + 128u * i, a + uint32_t(s * (kSlabB >> 4) + 2 * kk),
+                                      bd + uint32_t(s * (kHalfB >> 4) + 2 * kk), kIdescQk, (s | kk) != 0 ? 1u : 0u);
                 umma2_commit(&ctl.s_full[i]);
-            };
-            // O(tile i) += P_i . V(j), over the 16-entry steps below the tile's limit
-            const auto pv = [&](int i, int j) {
-                const int steps = min((limit[i] - j * kTile + 15) >> 4, kTile / 16);
-                const uint64_t bd = desc_mn_sw128(s_base + kOffV + (j % kStages) * kStageV, kSlabB);
+            }
+            __syncwarp();
+        };
+        // O(tile i) += P_i . V, values in stage st, over the 16-entry steps below the tile's limit
+        const auto pv = [&](int i, int j, int st) {
+            const int steps = min((lim[i] - j * kTile + 15) >> 4, kTile / 16);
+            if (issuer) {
+                const uint64_t bd = v_desc + uint32_t(st * (kStageV >> 4));
                 const auto step = [&](int kk) {
-                    umma2_bf16_ts(tmem_base + kColOP + 128u * i, tmem_base + kColSP + 128u * i + 8u * kk,
-                                  bd + 128u * kk, kIdescPv, (j | kk) != 0 ? 1u : 0u);
+                    umma2_bf16_ts(tmem + kColOP + 128u * i, tmem + kColSP + 128u * i + 8u * kk, bd + 128u * kk, kIdescPv,
+                                  (j | kk) != 0 ? 1u : 0u);
                 };
                 if (steps == kTile / 16) {
 #pragma unroll
@@ -426,52 +443,68 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll 1
                     for (int kk = 0; kk < steps; ++kk) step(kk);
                 }
-                if (j + 1 == ntiles[i]) umma2_commit(&ctl.o_full[i]);
-            };
-            const auto wait_k = [&](int j) {
-                const bool ok = mbar_wait_cluster(&ctl.k_full[j % kStages], uint32_t(j / kStages) & 1u, &ctl.abort);
-                tc_fence_after_sync();
-                return ok;
-            };
-            bool ok = nt == 0 || wait_k(0);
-            for (int i = 0; i < 2 && ok; ++i) {
-                if (ntiles[i] == 0) continue;
-                ok = mbar_wait_cluster(&ctl.q_full[i], 0, &ctl.abort);
+                if (j + 1 == n_of[i]) umma2_commit(&ctl.o_full[i]);
+            }
+            __syncwarp();
+        };
+        const auto commit = [&](uint64_t* bar) {
+            if (issuer) umma2_commit(bar);
+            __syncwarp();
+        };
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, &ctl.abort)) != 0;
+        };
+        bool ok = n_all == 0 || wait(&ctl.k_full[0], 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (ok && n_of[i] > 0) {
+                ok = wait(&ctl.q_full[i], 0);
                 tc_fence_after_sync();
                 if (ok) qk(i, 0);
             }
-            if (ok && nt > 0) umma2_commit(&ctl.k_empty[0]);
-#pragma unroll 1
-            for (int j = 0; j < nt && ok; ++j) {
-                const int st = j % kStages;
-                bool have_k = false;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (ok && j < ntiles[i]) {
-                        ok = mbar_wait_cluster(&ctl.p_full[i], uint32_t(j & 1), &ctl.abort);
-                        if (ok)
-                            ok = tail && j == nt - 1
-                                     ? mbar_wait_cluster(&ctl.tail_ready, 0, &ctl.abort)
-                                     : mbar_wait_cluster(&ctl.v_full[st], uint32_t(j / kStages) & 1u, &ctl.abort);
-                        tc_fence_after_sync();
-                        if (ok) pv(i, j);
-                    }
-                    if (ok && i == 1) umma2_commit(&ctl.v_empty[st]);
-                    if (ok && j + 1 < ntiles[i]) {
-                        if (!have_k) ok = wait_k(j + 1);
-                        have_k = true;
-                        if (ok) qk(i, j + 1);
-                    }
-                }
-                if (ok && j + 1 < nt) umma2_commit(&ctl.k_empty[(j + 1) % kStages]);
-            }
-            if (!ok) {
-                atomicOr(p.err, kErrWaitTimeout);
-                ctl.abort = 1;
-            }
-            umma2_commit(&ctl.all_done);
-            wait_landed_p(&ctl.all_done, 0);  // every MMA issued has completed
         }
+        if (ok && n_all > 0) commit(&ctl.k_empty[0]);
+        int st = 0, st_next = 1;          // stages of tiles j and j + 1, and their phases
+        uint32_t phase = 0, phase_next = 0;
+#pragma unroll 1
+        for (int j = 0; j < n_all && ok; ++j) {
+            bool have_k = false, have_v = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (ok && j < n_of[i]) {
+                    if (!have_v) {
+                        if (tail && j == n_all - 1)
+                            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.tail_ready, 0, &ctl.abort)) != 0;
+                        else
+                            ok = wait(&ctl.v_full[st], phase);
+                    }
+                    have_v = true;
+                    if (ok) ok = wait(&ctl.p_full[i], uint32_t(j & 1));
+                    tc_fence_after_sync();
+                    if (ok) pv(i, j, st);
+                }
+                if (ok && i == 1) commit(&ctl.v_empty[st]);
+                if (ok && j + 1 < n_of[i]) {
+                    if (!have_k) ok = wait(&ctl.k_full[st_next], phase_next);
+                    have_k = true;
+                    tc_fence_after_sync();
+                    if (ok) qk(i, st_next);
+                }
+            }
+            if (ok && j + 1 < n_all) commit(&ctl.k_empty[st_next]);
+            st = st_next;
+            phase = phase_next;
+            if (++st_next == kStages) {
+                st_next = 0;
+                phase_next ^= 1u;
+            }
+        }
+        if (!ok && issuer) {
+            atomicOr(p.err, kErrWaitTimeout);
+            ctl.abort = 1;
+        }
+        commit(&ctl.all_done);
+        wait_landed_p(&ctl.all_done, 0);  // every MMA issued has completed
         __syncwarp();
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -561,7 +594,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             tmem_st_wait();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(p_bar);
+            if (lane == 0) mbar_arrive_remote(p_bar);
         }
         // ---- output
         if (!failed && ntiles[i] > 0) {
