@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     DenseCtl& ctl = *reinterpret_cast<DenseCtl*>(tiles + kOffCtl);
     const uint32_t s_base = smem_u32(tiles);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = uniform(int(threadIdx.x) >> 5);
     const int lane = threadIdx.x & 31;
     const int token = blockIdx.x;  // of the group
     const int group = blockIdx.y;
@@ -340,61 +340,63 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ================= MMA1: S = Q . K^T =================
-        if (lane == 0) {
-            constexpr uint32_t kIdesc1 = idesc_bf16_f32(64, 64);
-            Walk w(ctl, p);
-            bool stop = false;
-            int n = 0, seg = 0;
-            while (!stop && w.next(p)) {
-                if (!mbar_wait(&ctl.q_full, uint32_t(seg & 1), &ctl.abort)) {
-                    stop = true;
-                    break;
-                }
-                ++seg;
+        // The whole warp runs the loop on uniform values; one elected lane issues.
+        constexpr uint32_t kIdesc1 = idesc_bf16_f32(64, 64);
+        const uint32_t tmem = uint32_t(uniform(int(tmem_base)));
+        const uint32_t sb = uint32_t(uniform(int(s_base)));
+        const uint64_t q_desc = smem_desc_kmajor_sw128(sb + kOffQ);
+        const uint64_t v_desc = smem_desc_kmajor_sw128(sb + kOffV);
+        const uint64_t r_desc = smem_desc_kmajor_sw128(sb + kOffR);
+        const bool issuer = elect_one();
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, &ctl.abort)) != 0;
+        };
+        Walk w(ctl, p);
+        bool ok = true;
+        int n = 0, seg = 0;
+        while (ok && w.next(p)) {
+            ok = wait(&ctl.q_full, uint32_t(seg & 1));
+            ++seg;
+            const int blocks = uniform(w.bhi - w.blo);
 #pragma unroll 1
-                for (int blk = w.blo; blk < w.bhi && !stop; ++blk, ++n) {
-                    const int buf = n & 1;
-                    if (!mbar_wait(&ctl.s_empty[buf], uint32_t((n >> 1) & 1) ^ 1u, &ctl.abort)) {
-                        stop = true;
-                        break;
-                    }
-                    const uint32_t s_col = tmem_base + kColS + 64u * buf;
-#pragma unroll 1
-                    for (int j = 0; j < 4; ++j) {
-                        const int pos = 4 * n + j, slot = pos & (kVRing - 1), use = pos / kVRing;
-                        if (!mbar_wait(&ctl.v_full[slot], uint32_t(use & 1), &ctl.abort)) {
-                            stop = true;
-                            break;
-                        }
-                        tc_fence_after_sync();
+            for (int i = 0; i < blocks && ok; ++i, ++n) {
+                const int buf = n & 1;  // S accumulator, half of the ring and rotary slab
+                const uint32_t phase = uint32_t((n >> 1) & 1);
+                ok = wait(&ctl.s_empty[buf], phase ^ 1u);
+                const uint32_t s_col = tmem + kColS + 64u * buf;
 #pragma unroll
-                        for (int hs = 0; hs < 2; ++hs) {
-                            const int s = 2 * j + hs;
-                            const uint64_t a = smem_desc_kmajor_sw128(s_base + kOffQ + s * kSlabBytes);
-                            const uint64_t bd =
-                                smem_desc_kmajor_sw128(s_base + kOffV + slot * kPairBytes + hs * kSlabBytes);
+                for (int j = 0; j < 4; ++j) {
+                    ok = ok && wait(&ctl.v_full[4 * buf + j], phase);
+                    tc_fence_after_sync();
+                    if (ok && issuer) {
+                        const uint64_t bd = v_desc + uint32_t(buf * (4 * kPairBytes >> 4));
+#pragma unroll
+                        for (int hs = 0; hs < 2; ++hs)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16_ss(s_col, a + 2u * kk, bd + 2u * kk, kIdesc1, (s | kk) != 0 ? 1u : 0u);
-                        }
+                                umma_bf16_ss(s_col, q_desc + uint32_t((2 * j + hs) * (kSlabBytes >> 4) + 2 * kk),
+                                             bd + uint32_t((2 * j + hs) * (kSlabBytes >> 4) + 2 * kk), kIdesc1,
+                                             (j | hs | kk) != 0 ? 1u : 0u);
                     }
-                    if (stop) break;
-                    const int slot = n & (kRRing - 1), use = n / kRRing;
-                    if (!mbar_wait(&ctl.r_full[slot], uint32_t(use & 1), &ctl.abort)) {
-                        stop = true;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint64_t a = smem_desc_kmajor_sw128(s_base + kOffQ + 8 * kSlabBytes);
-                    const uint64_t bd = smem_desc_kmajor_sw128(s_base + kOffR + slot * kSlabBytes);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) umma_bf16_ss(s_col, a + 2u * kk, bd + 2u * kk, kIdesc1, 1u);
-                    umma_commit(&ctl.r_empty[slot]);
-                    umma_commit(&ctl.s_full[buf]);
+                    __syncwarp();
                 }
-                if (!stop) umma_commit(&ctl.q_empty);
+                ok = ok && wait(&ctl.r_full[buf], phase);
+                tc_fence_after_sync();
+                if (ok && issuer) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_ss(s_col, q_desc + uint32_t(8 * (kSlabBytes >> 4) + 2 * kk),
+                                     r_desc + uint32_t(buf * (kSlabBytes >> 4) + 2 * kk), kIdesc1, 1u);
+                    umma_commit(&ctl.s_full[buf]);
+                    umma_commit(&ctl.r_empty[buf]);
+                }
+                __syncwarp();
             }
-            if (stop) {
+            if (ok && issuer) umma_commit(&ctl.q_empty);
+            __syncwarp();
+        }
+        if (issuer) {
+            if (!ok) {
                 atomicOr(p.err, kErrWaitTimeout);
                 ctl.abort = 1;
             }
@@ -404,63 +406,69 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     } else if (warp == 2) {
         // ================= MMA2: O^T += V^T . P^T =================
         constexpr uint32_t kIdesc2 = idesc_bf16_f32(128, 64) | (1u << 15);  // A (V^T) MN-major
-        const uint64_t bp = smem_desc_kmajor_sw128(s_base + kOffP);
+        const uint32_t tmem = uint32_t(uniform(int(tmem_base)));
+        const uint32_t sb = uint32_t(uniform(int(s_base)));
+        const uint64_t p_desc = smem_desc_kmajor_sw128(sb + kOffP);
+        const uint64_t v_desc = desc_mn_sw128(sb + kOffV, kSlabBytes);
+        const bool issuer = elect_one();
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, &ctl.abort)) != 0;
+        };
         Walk w(ctl, p);
-        bool stop = false;
+        bool ok = true;
         int n = 0, seg = 0;
-        while (!stop && w.next(p)) {
-            bool fresh = true;  // no product of this request yet
+        while (ok && w.next(p)) {
+            uint32_t fresh = 1;  // no product of this request yet
             uint32_t bad = 0;
+            const int blocks = uniform(w.bhi - w.blo);
 #pragma unroll 1
-            for (int blk = w.blo; blk < w.bhi; ++blk, ++n) {
-                if (((blk - w.blo) & 31) == 0)
-                    bad = __ballot_sync(0xffffffffu, page_of_lane(p, w, blk, lane) < 0);
-                const int valid = ((bad >> ((blk - w.blo) & 31)) & 1u) ? 0 : w.valid(blk, back);
-                bool ok = mbar_wait(&ctl.p_full, uint32_t(n & 1), &ctl.abort);
-                if (ok && blk == w.blo) ok = mbar_wait(&ctl.o_empty, uint32_t(seg & 1) ^ 1u, &ctl.abort);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    stop = true;
-                    break;
-                }
+            for (int i = 0; i < blocks; ++i, ++n) {
+                const int blk = w.blo + i;
+                if ((i & 31) == 0) bad = __ballot_sync(0xffffffffu, page_of_lane(p, w, blk, lane) < 0);
+                const int valid = uniform(((bad >> (i & 31)) & 1u) ? 0 : w.valid(blk, back));
+                const int buf = n & 1;  // half of the ring
+                if (i == 0) ok = wait(&ctl.o_empty, uint32_t(seg & 1) ^ 1u);
+                ok = ok && wait(&ctl.p_full, uint32_t(n & 1));
+                if (!ok) break;
                 tc_fence_after_sync();
-                const int steps = (valid + 15) >> 4;
-                if (valid & 15) {  // zero the value rows behind the live ones in the last step
-                    const int rows = 16 * steps - valid;
-                    for (int j = 0; j < 4; ++j) {  // landed long ago: orders these stores behind the copies
-                        const int pos = 4 * n + j;
-                        wait_landed(&ctl.v_full[pos & (kVRing - 1)], uint32_t(pos / kVRing) & 1u);
-                    }
-                    for (int i = lane; i < rows * 64; i += 32) {  // 8 slabs x 8 chunks of 16 bytes per row
-                        const int row = valid + (i >> 6), slab = (i >> 3) & 7, ch = i & 7;
-                        const int slot = (4 * n + (slab >> 1)) & (kVRing - 1);
-                        *reinterpret_cast<uint4*>(tiles + kOffV + slot * kPairBytes + (slab & 1) * kSlabBytes +
-                                                  row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+                if (valid & 15) {  // zero the value rows behind the live ones in the last 16-entry step
+                    const int rows = 16 - (valid & 15);
+                    for (int j = 0; j < 4; ++j)  // landed long ago: orders these stores behind the copies
+                        wait_landed(&ctl.v_full[4 * buf + j], uint32_t((n >> 1) & 1));
+                    for (int c = lane; c < rows * 64; c += 32) {  // 8 slabs x 8 chunks of 16 bytes per row
+                        const int row = valid + (c >> 6), slab = (c >> 3) & 7, ch = c & 7;
+                        *reinterpret_cast<uint4*>(tiles + kOffV + buf * 4 * kPairBytes + slab * kSlabBytes + row * 128 +
+                                                  ch * 16) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if (lane == 0) {
+                if (issuer) {
+                    const uint64_t vd = v_desc + uint32_t(buf * (4 * kPairBytes >> 4));
+                    const auto step = [&](int kk) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            umma_bf16_ss(tmem + kColO + 64u * j, vd + uint32_t(j * (kPairBytes >> 4) + kk * (2048 >> 4)),
+                                         p_desc + 2u * kk, kIdesc2, (kk == 0 && fresh) ? 0u : 1u);
+                    };
+                    if (valid > 48) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) step(kk);
+                    } else {
 #pragma unroll 1
-                    for (int kk = 0; kk < steps; ++kk) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int slot = (4 * n + j) & (kVRing - 1);
-                            umma_bf16_ss(tmem_base + kColO + 64u * j,
-                                         desc_mn_sw128(s_base + kOffV + slot * kPairBytes + kk * 2048, kSlabBytes),
-                                         bp + 2u * kk, kIdesc2, (fresh && kk == 0) ? 0u : 1u);
-                        }
+                        for (int kk = 0; 16 * kk < valid; ++kk) step(kk);
                     }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) umma_commit(&ctl.v_empty[(4 * n + j) & (kVRing - 1)]);
                     umma_commit(&ctl.pv_done);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) umma_commit(&ctl.v_empty[4 * buf + j]);
                 }
                 __syncwarp();
-                if (steps > 0) fresh = false;
+                if (valid > 0) fresh = 0;
             }
             ++seg;
         }
-        if (lane == 0) {
-            if (stop) {
+        if (issuer) {
+            if (!ok) {
                 atomicOr(p.err, kErrWaitTimeout);
                 ctl.abort = 1;
             }
