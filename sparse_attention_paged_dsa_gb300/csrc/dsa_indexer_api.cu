@@ -159,6 +159,26 @@ dsa_status_t make_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int6
     return DSA_OK;
 }
 
+// 576-wide bf16 rows as (dim in slab, row, slab of 64 dims): boxes of 64 rows x box_slabs slabs, 128-byte
+// swizzle, so that one copy fills several 64 x 64 slabs.
+dsa_status_t make_slabs_map(CUtensorMap* map, const void* ptr, int64_t rows, uint32_t box_slabs, const char* what) {
+    auto enc = encode_tiled();
+    if (!enc) return cuda_fail(cudaErrorNotSupported, "cuTensorMapEncodeTiled lookup");
+    const cuuint64_t dims[3] = {64, cuuint64_t(rows), DSA_MLA_DIM / 64};
+    const cuuint64_t strides[2] = {DSA_MLA_DIM * 2, 128};
+    const cuuint32_t box[3] = {64, 64, box_slabs};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        std::snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "cuTensorMapEncodeTiled(%s): CUresult %d", what,
+                      int(r));
+        return DSA_ERR_CUDA;
+    }
+    return DSA_OK;
+}
+
 // bf16 [rows, heads, dim] with element strides (dim contiguous) as (dim, head, row): boxes of
 // 64 dims x 1 head x box_rows, 128-byte swizzle.
 dsa_status_t make_heads_map(CUtensorMap* map, const void* ptr, int64_t rows, int32_t heads, int32_t dim,
@@ -710,10 +730,12 @@ dsa_status_t dsa_mla_decode(const void* q, const void* kv_cache, int64_t num_pag
     const int groups = dense_groups(sms, next_n);
     st = check_workspace(workspace, workspace_bytes, dense_workspace_bytes(groups, next_n));
     if (st != DSA_OK) return st;
-    CUtensorMap q_map, kv_map;
-    st = make_rows_map(&q_map, q, int64_t(batch) * next_n * DSA_MLA_HEADS, DSA_MLA_DIM, 64, "mla q");
+    CUtensorMap q_map, kv_map, kr_map;
+    st = make_slabs_map(&q_map, q, int64_t(batch) * next_n * DSA_MLA_HEADS, 3, "mla q");
     if (st != DSA_OK) return st;
-    st = make_rows_map(&kv_map, kv_cache, num_pages * dsa::kPageEntries, DSA_MLA_DIM, 64, "mla kv");
+    st = make_slabs_map(&kv_map, kv_cache, num_pages * dsa::kPageEntries, 2, "mla kv");
+    if (st != DSA_OK) return st;
+    st = make_rows_map(&kr_map, kv_cache, num_pages * dsa::kPageEntries, DSA_MLA_DIM, 64, "mla kv");
     if (st != DSA_OK) return st;
     dsa::MlaDenseParams p{};
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -732,7 +754,7 @@ dsa_status_t dsa_mla_decode(const void* q, const void* kv_cache, int64_t num_pag
     p.tokens = next_n;
     p.groups = groups;
     p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
-    e = dsa::launch_mla_dense(q_map, kv_map, p, static_cast<cudaStream_t>(stream));
+    e = dsa::launch_mla_dense(q_map, kv_map, kr_map, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA decode launch");
 }
 

@@ -159,10 +159,11 @@ struct MlaDenseParams {
     int32_t groups;            // ranges: SMs / tokens
     float sm_scale_log2;       // sm_scale * log2(e)
 };
-// q_map: q [batch * tokens * 64, 576] bf16; kv_map: the cache as [num_pages * 64, 576] bf16
-// rows; both 128-byte-swizzled boxes of 64 x 64.
-cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const MlaDenseParams& p,
-                             cudaStream_t stream);
+// q_map and kv_map: 576-wide bf16 rows (q: batch * tokens * 64 of them; the cache: num_pages * 64) as
+// (dim in slab, row, slab of 64 dims), boxes of 64 rows x 3 slabs and 64 rows x 2 slabs; kr_map: the
+// cache's rows as (dim, row), boxes of 64 x 64.  All 128-byte-swizzled.
+cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& kr_map,
+                             const MlaDenseParams& p, cudaStream_t stream);
 
 // Latent attention over ragged prompts, expanded form: per-head 128 + 64 shared key dims, 128 value dims.
 constexpr int kPrefillQk = 192;

@@ -59,6 +59,7 @@ constexpr int kPairBytes = 2 * kSlabBytes;     // value dims [128 j, 128 j + 128
 constexpr int kVRing = 8;                      // slab pairs (two blocks' values)
 constexpr int kRRing = 2;                      // slabs of the last 64 dims
 constexpr int kQSlabs = kMlaDim / 64;          // 9
+constexpr int kQBox = 3;                       // q slabs per copy
 constexpr int kOffQ = 0;
 constexpr int kOffP = kOffQ + kQSlabs * kSlabBytes;  // P [64 heads x 64 entries] bf16 (follows q's last
                                                      // slab, whose rows 64..127 an M = 64 MMA may touch)
@@ -118,6 +119,17 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
         : "r"(taddr));
 }
 
+// Rows [row, row + 64) of the map's slabs [slab, ...) (a (dim in slab, row, slab) view of 576-wide rows)
+// into consecutive 64 x 64 slabs.
+__device__ __forceinline__ void tma_load_slabs(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t row,
+                                               int32_t slab, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(slab), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 // Bounded wait for a phase of `bar`, whatever the other roles do.
 __device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
@@ -172,7 +184,7 @@ __device__ __forceinline__ int page_of_lane(const MlaDenseParams& p, const Walk&
 
 __global__ void __launch_bounds__(kThreadsD, 1)
     mla_dense_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
-                     const MlaDenseParams p) {
+                     const __grid_constant__ CUtensorMap kr_map, const MlaDenseParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     DenseCtl& ctl = *reinterpret_cast<DenseCtl*>(tiles + kOffCtl);
@@ -207,6 +219,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         fence_mbar_init();
         tma_prefetch_map(&q_map);
         tma_prefetch_map(&kv_map);
+        tma_prefetch_map(&kr_map);
     }
     if (warp == 1) {
         tmem_alloc(&ctl.tmem_base, kTmemColsD);
@@ -271,59 +284,63 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 
     if (warp == 0) {
         // ================= TMA =================
+        // The whole warp runs the loop on uniform values; one elected lane issues.
         Walk w(ctl, p);
         bool stop = false;
-        int n = 0, seg = 0;  // blocks and requests so far
+        int n = 0, seg = 0;                         // blocks and requests so far
         int last_v = -1, last_r = -1, last_q = -1;  // the last fills issued
+        const bool issuer = elect_one();
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, &ctl.abort)) != 0;
+        };
         const uint64_t pol_q = l2_policy_evict_first();
         // Tokens of a group share a page through L2; a single token reads it once.
         const uint64_t pol_kv = p.tokens > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+        const uint32_t sb = uint32_t(uniform(int(s_base)));
         while (!stop && w.next(p)) {
-            if (lane == 0) {
-                if (mbar_wait(&ctl.q_empty, uint32_t(seg & 1) ^ 1u, &ctl.abort)) {
-                    mbar_arrive_expect_tx(&ctl.q_full, uint32_t(kQSlabs * kSlabBytes));
-                    for (int s = 0; s < kQSlabs; ++s)
-                        tma_load_2d(tiles + kOffQ + s * kSlabBytes, &q_map, &ctl.q_full, s * 64,
-                                    (w.req() * p.tokens + token) * kMlaHeads, pol_q);
-                    last_q = seg;
-                } else {
-                    stop = true;
-                }
+            int page_l = page_of_lane(p, w, w.blo, lane);
+            if (w.blo + lane < w.bhi && page_l < 0) atomicOr(p.err, kErrBadPage);
+            stop = !wait(&ctl.q_empty, uint32_t(seg & 1) ^ 1u);
+            if (stop) break;
+            if (issuer) {
+                mbar_arrive_expect_tx(&ctl.q_full, uint32_t(kQSlabs * kSlabBytes));
+                const int row = (w.req() * p.tokens + token) * kMlaHeads;
+#pragma unroll
+                for (int s = 0; s < kQSlabs; s += kQBox)
+                    tma_load_slabs(sb + kOffQ + s * kSlabBytes, &q_map, &ctl.q_full, row, s, pol_q);
             }
-            stop = __any_sync(0xffffffffu, stop);
-            if (!stop) ++seg;
-            int page_l = -1;
-            for (int blk = w.blo; blk < w.bhi && !stop; ++blk, ++n) {
-                if (((blk - w.blo) & 31) == 0) {
-                    page_l = page_of_lane(p, w, blk, lane);
-                    if (blk + lane < w.bhi && page_l < 0) atomicOr(p.err, kErrBadPage);
+            __syncwarp();
+            last_q = seg++;
+            const int blocks = uniform(w.bhi - w.blo);
+#pragma unroll 1
+            for (int i = 0; i < blocks; ++i, ++n) {
+                if (i > 0 && (i & 31) == 0) {
+                    page_l = page_of_lane(p, w, w.blo + i, lane);
+                    if (w.blo + i + lane < w.bhi && page_l < 0) atomicOr(p.err, kErrBadPage);
                 }
                 // a page outside the cache: page 0 stands in, its entries are not used
-                const int page = max(__shfl_sync(0xffffffffu, page_l, (blk - w.blo) & 31), 0);
-                if (lane == 0) {
-#pragma unroll 1
-                    for (int j = 0; j < 4; ++j) {
-                        const int pos = 4 * n + j, slot = pos & (kVRing - 1), use = pos / kVRing;
-                        if (!mbar_wait(&ctl.v_empty[slot], uint32_t(use & 1) ^ 1u, &ctl.abort)) {
-                            stop = true;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(&ctl.v_full[slot], uint32_t(kPairBytes));
-                        uint8_t* dst = tiles + kOffV + slot * kPairBytes;
-                        tma_load_2d(dst, &kv_map, &ctl.v_full[slot], 128 * j, page * kBlk, pol_kv);
-                        tma_load_2d(dst + kSlabBytes, &kv_map, &ctl.v_full[slot], 128 * j + 64, page * kBlk, pol_kv);
-                        last_v = pos;
+                const int row = max(__shfl_sync(0xffffffffu, page_l, i & 31), 0) * kBlk;
+                const int buf = n & 1;  // half of the ring and rotary slab
+                const uint32_t phase = uint32_t((n >> 1) & 1) ^ 1u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    stop = stop || !wait(&ctl.v_empty[4 * buf + j], phase);
+                    if (!stop && issuer) {
+                        mbar_arrive_expect_tx(&ctl.v_full[4 * buf + j], uint32_t(kPairBytes));
+                        tma_load_slabs(sb + kOffV + (4 * buf + j) * kPairBytes, &kv_map, &ctl.v_full[4 * buf + j], row,
+                                       2 * j, pol_kv);
                     }
-                    const int slot = n & (kRRing - 1), use = n / kRRing;
-                    if (!stop && !mbar_wait(&ctl.r_empty[slot], uint32_t(use & 1) ^ 1u, &ctl.abort)) stop = true;
-                    if (!stop) {
-                        mbar_arrive_expect_tx(&ctl.r_full[slot], uint32_t(kSlabBytes));
-                        tma_load_2d(tiles + kOffR + slot * kSlabBytes, &kv_map, &ctl.r_full[slot], kMlaDv, page * kBlk,
-                                    pol_kv);
-                        last_r = n;
-                    }
+                    __syncwarp();
+                    if (!stop) last_v = 4 * n + j;
                 }
-                stop = __any_sync(0xffffffffu, stop);
+                stop = stop || !wait(&ctl.r_empty[buf], phase);
+                if (stop) break;
+                if (issuer) {
+                    mbar_arrive_expect_tx(&ctl.r_full[buf], uint32_t(kSlabBytes));
+                    tma_load_2d(tiles + kOffR + buf * kSlabBytes, &kr_map, &ctl.r_full[buf], kMlaDv, row, pol_kv);
+                }
+                __syncwarp();
+                last_r = n;
             }
         }
         if (stop && lane == 0) {
@@ -445,22 +462,23 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 }
                 if (issuer) {
                     const uint64_t vd = v_desc + uint32_t(buf * (4 * kPairBytes >> 4));
-                    const auto step = [&](int kk) {
+                    // pair by pair, so that the first slots are free (and refilled) early
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 4; ++j) {
+                        const auto step = [&](int kk) {
                             umma_bf16_ss(tmem + kColO + 64u * j, vd + uint32_t(j * (kPairBytes >> 4) + kk * (2048 >> 4)),
                                          p_desc + 2u * kk, kIdesc2, (kk == 0 && fresh) ? 0u : 1u);
-                    };
-                    if (valid > 48) {
+                        };
+                        if (valid > 48) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) step(kk);
-                    } else {
+                            for (int kk = 0; kk < 4; ++kk) step(kk);
+                        } else {
 #pragma unroll 1
-                        for (int kk = 0; 16 * kk < valid; ++kk) step(kk);
+                            for (int kk = 0; 16 * kk < valid; ++kk) step(kk);
+                        }
+                        umma_commit(&ctl.v_empty[4 * buf + j]);
                     }
                     umma_commit(&ctl.pv_done);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) umma_commit(&ctl.v_empty[4 * buf + j]);
                 }
                 __syncwarp();
                 if (valid > 0) fresh = 0;
@@ -496,7 +514,10 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                     bad = __ballot_sync(0xffffffffu, page_of_lane(p, w, blk, lane) < 0);
                 const int valid = ((bad >> ((blk - w.blo) & 31)) & 1u) ? 0 : w.valid(blk, back);
                 const int buf = n & 1;
-                bool ok = mbar_wait(&ctl.s_full[buf], uint32_t((n >> 1) & 1), &ctl.abort);
+                // The previous block's product has read P (and O^T is at rest) long before the next scores
+                // are there: waiting for it first costs nothing.
+                bool ok = n == 0 || mbar_wait(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort);
+                ok = ok && mbar_wait(&ctl.s_full[buf], uint32_t((n >> 1) & 1), &ctl.abort);
                 ok = __all_sync(0xffffffffu, ok);
                 float x[16];
                 {
@@ -548,11 +569,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                         }
                         if (half == 0 && lane % 4 == 0) ctl.alpha[h] = alpha;
                     }
-                    if (!fresh) ok = mbar_wait(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort);
-                    if (soft_bar_or(!ok)) {
-                        failed = true;
-                        break;
-                    }
+                    soft_bar_sync();
                     if (!fresh) {
                         tc_fence_after_sync();
 #pragma unroll 1
@@ -582,11 +599,6 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                         const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
                         packed[4 * r + k] = *reinterpret_cast<const uint32_t*>(&v);
                     }
-                }
-                // The P buffer is free once the previous block's product has read it.
-                if (n > 0) ok = mbar_wait(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    if (lane == 0) ctl.abort = 1;  // the other warps see it at their next wait
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
@@ -745,8 +757,8 @@ __global__ void __launch_bounds__(512) mla_dense_merge_kernel(const MlaDensePara
 
 }  // namespace
 
-cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const MlaDenseParams& p,
-                             cudaStream_t stream) {
+cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& kr_map,
+                             const MlaDenseParams& p, cudaStream_t stream) {
     static SmemLimitOnce smem_limit;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -764,7 +776,7 @@ cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, mla_dense_kernel, q_map, kv_map, p);
+    e = cudaLaunchKernelEx(&cfg, mla_dense_kernel, q_map, kv_map, kr_map, p);
     if (e != cudaSuccess) return e;
     // Few rows are split many ways: more threads per row read more partials at a time.
     const int rows = p.batch * p.tokens;
