@@ -336,7 +336,8 @@ int dense_groups(int sms, int32_t next_n) {
     const int g = sms / next_n;
     return g < 1 ? 1 : (g > dsa::kMlaMaxGroups ? dsa::kMlaMaxGroups : g);
 }
-constexpr size_t kDensePlanBytes = size_t(DSA_MAX_BATCH) * sizeof(int2);
+constexpr size_t kDenseCutBytes = size_t(dsa::kMlaMaxGroups) * sizeof(int32_t);
+constexpr size_t kDensePlanBytes = size_t(DSA_MAX_BATCH) * sizeof(int2) + kDenseCutBytes;
 size_t dense_parts(int groups, int32_t next_n) { return size_t(groups) * size_t(next_n) * 2; }
 size_t dense_workspace_bytes(int groups, int32_t next_n) {
     return dsa::kWorkspaceHeaderBytes + kDensePlanBytes +
@@ -743,7 +744,8 @@ dsa_status_t dsa_mla_decode(const void* q, const void* kv_cache, int64_t num_pag
     p.seq_lens = seq_lens;
     p.out = static_cast<__nv_bfloat16_raw*>(out);
     p.lse = lse;
-    p.plan = reinterpret_cast<int2*>(ws + dsa::kWorkspaceHeaderBytes);
+    p.cuts = reinterpret_cast<int32_t*>(ws + dsa::kWorkspaceHeaderBytes);
+    p.plan = reinterpret_cast<int2*>(ws + dsa::kWorkspaceHeaderBytes + kDenseCutBytes);
     p.o_part = reinterpret_cast<float*>(ws + dsa::kWorkspaceHeaderBytes + kDensePlanBytes);
     p.lse_part = p.o_part + dense_parts(groups, next_n) * dsa::kMlaHeads * dsa::kMlaDv;
     p.err = static_cast<uint32_t*>(workspace);
@@ -753,6 +755,7 @@ dsa_status_t dsa_mla_decode(const void* q, const void* kv_cache, int64_t num_pag
     p.batch = batch;
     p.tokens = next_n;
     p.groups = groups;
+    p.merge_by_cut = batch > groups ? 1 : 0;
     p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
     e = dsa::launch_mla_dense(q_map, kv_map, kr_map, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA decode launch");

@@ -141,13 +141,14 @@ cudaError_t launch_mla(const CUtensorMap& q_map, const CUtensorMap& kv_map, cons
 // Latent attention decode over every live entry, 1-4 tokens per request.
 constexpr int kMlaMaxGroups = 256;
 constexpr int kMlaSegUnits = 2;  // a request's fixed cost in a range (q, output), in blocks
-constexpr int kMlaMinUnits = 3;  // least units worth a range of its own
+constexpr int kMlaWholeBlocks = 4;  // requests of at most this many blocks are not split
 struct MlaDenseParams {
     const int32_t* page_table; // [batch, table_width]
     const int32_t* seq_lens;   // [batch] tokens
     __nv_bfloat16_raw* out;    // [batch, tokens, 64, 512]
     float* lse;                // [batch, tokens, 64]
-    int2* plan;                // [batch] first and last range of each request
+    int2* plan;                // [batch] first and last range of each request (equal: one)
+    int32_t* cuts;             // [groups] the request that the range is the second one of, or -1
     float* o_part;             // [groups * tokens * 2, 64, 512] partial outputs
     float* lse_part;           // [groups * tokens * 2, 64]
     uint32_t* err;             // device error word
@@ -157,6 +158,7 @@ struct MlaDenseParams {
     int32_t batch;
     int32_t tokens;            // query tokens per request
     int32_t groups;            // ranges: SMs / tokens
+    int32_t merge_by_cut;      // the merge goes by cuts (there are fewer ranges than requests)
     float sm_scale_log2;       // sm_scale * log2(e)
 };
 // q_map and kv_map: 576-wide bf16 rows (q: batch * tokens * 64 of them; the cache: num_pages * 64) as

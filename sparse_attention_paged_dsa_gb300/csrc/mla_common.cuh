@@ -1,5 +1,5 @@
 // mla_common.cuh -- what the latent attention kernels share: the MN-major
-// operand descriptor, TMEM stores and the base-2 exponential.
+// operand descriptor, TMEM stores, the base-2 exponential and bulk stores.
 #pragma once
 
 #include <cstdint>
@@ -38,6 +38,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Bulk copy of `bytes` (multiple of 16) from shared to global memory, tracked by this
+// thread's bulk-async group.
+__device__ __forceinline__ void bulk_store(void* gdst, uint32_t ssrc, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(ssrc), "r"(bytes)
+                 : "memory");
 }
 
 }  // namespace dsa

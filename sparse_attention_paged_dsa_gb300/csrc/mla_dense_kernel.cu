@@ -7,13 +7,15 @@
 // over t < ceil((seq_len - (next_n - 1 - j)) / 4).
 //
 // Work split.  A block is one page: 64 entries, 73,728 contiguous bytes.  The
-// requests' blocks, laid end to end with kSegUnits units of fixed cost before
+// requests' blocks, laid end to end with kMlaSegUnits units of fixed cost before
 // each request, are cut into equal ranges, one per group of next_n CTAs (one CTA
 // per SM; token j of a group's requests belongs to its CTA j, so the tokens read
-// a page at about the same time and all but the first from L2).  Every CTA finds
-// its range from seq_lens alone.  A request inside one range is written straight
-// to the output; one that crosses ranges leaves an fp32 partial per range, and
-// the merge kernel joins them by log-sum-exp.
+// a page at about the same time and all but the first from L2).  A cut inside a
+// request of at most kMlaWholeBlocks blocks moves to its nearer end: joining its parts
+// would cost more than reading them one after another.  Every CTA finds its range
+// from seq_lens alone.  A request inside one range is written straight to the
+// output; one that crosses ranges leaves an fp32 partial per range, and the merge
+// kernel joins them by log-sum-exp.
 //
 // Roles of a CTA (384 threads):
 //   * warp 0: TMA.  Each page into nine 64 x 64 slabs of 128-byte-swizzled rows
@@ -26,8 +28,10 @@
 //   * warps 4-11: softmax.  Warp w reads the 16 heads of TMEM quadrant w % 4 and
 //     half of the block's entries with 16-lane loads that spread them over all 32
 //     lanes: 2 heads x 8 entries per thread.  The running maximum is raised only
-//     when a block passes it by more than 2^8; then the accumulators are rescaled
-//     in TMEM.  At a request's end the warps normalise O^T and store it.
+//     when a block passes it by more than 2^20; then the accumulators are rescaled
+//     in TMEM.  At a request's end the warps normalise O^T into the ring half of its
+//     last block (released only then).
+//   * warp 3: stores from there with bulk copies; zeroes the outputs of empty requests.
 // Row sums add the unrounded fp32 weights; the weights are rounded to bf16 only
 // as the second product's operand.
 //
@@ -73,21 +77,26 @@ constexpr int kSoftThreads = 256;
 constexpr uint32_t kTmemColsD = 512;
 constexpr uint32_t kColS = 0;    // S: 2 x 64 columns
 constexpr uint32_t kColO = 128;  // O^T: 4 x 64 columns
-constexpr float kRescaleLog2 = 8.0f;
+// A weight may pass 1 by this much (its rounding is relative, so nothing is lost) before the running
+// maximum is raised: ordinary scores never rescale after the first block.  At 2^8 about every second
+// request of 256 random entries did, 2,000 cycles each.
+constexpr float kRescaleLog2 = 20.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 
-struct __align__(8) DenseCtl {
+struct __align__(16) DenseCtl {
     uint64_t v_full[kVRing], v_empty[kVRing];
     uint64_t r_full[kRRing], r_empty[kRRing];
     uint64_t s_full[2], s_empty[2];
     uint64_t q_full, q_empty, p_full, pv_done, o_empty, all_done;
+    uint64_t stage_full, stage_free;  // the output staged in the ring; its first half stored
     uint32_t tmem_base;
     int abort;
-    int first_req, first_unit;  // request of the range's first unit, and that unit within the request
-    int lo, hi;                 // the range, in units
+    int first_req, first_start;  // request of the range's first unit, and where its units start
+    int lo, hi;                  // the range, in units
+    int cut;                     // the request that this range is the second one of, or -1
     int warp_units[kWarpsD];
     float row_max[2][kMlaHeads];  // per half of the entries; the row sums at a request's end
-    float alpha[kMlaHeads];
+    alignas(16) float alpha[kMlaHeads];
 };
 constexpr int kSmemD = 1024 + kOffCtl + int(sizeof(DenseCtl));
 static_assert(kSmemD <= 232448, "fits one CTA per SM");
@@ -151,7 +160,7 @@ struct Walk {
     int b, u0, lo, hi, batch;  // request b starts at unit u0; range [lo, hi)
     int seq, nb, blo, bhi;     // current request: tokens, blocks, and this range's blocks [blo, bhi)
     __device__ __forceinline__ Walk(const DenseCtl& ctl, const MlaDenseParams& p)
-        : b(ctl.first_req), u0(ctl.lo - ctl.first_unit), lo(ctl.lo), hi(ctl.hi), batch(p.batch) {}
+        : b(ctl.first_req), u0(ctl.first_start), lo(ctl.lo), hi(ctl.hi), batch(p.batch) {}
     __device__ __forceinline__ bool next(const MlaDenseParams& p) {
         while (b < batch && u0 < hi) {
             seq = seq_tokens(p, b);
@@ -212,10 +221,13 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         mbar_init(&ctl.p_full, kSoftThreads / 32);
         mbar_init(&ctl.pv_done, 1);
         mbar_init(&ctl.o_empty, kSoftThreads / 32);
+        mbar_init(&ctl.stage_full, kSoftThreads / 32);
+        mbar_init(&ctl.stage_free, 1);
         mbar_init(&ctl.all_done, 2);
         ctl.abort = 0;
         ctl.first_req = p.batch;
-        ctl.first_unit = 0;
+        ctl.first_start = 0;
+        ctl.cut = -1;
         fence_mbar_init();
         tma_prefetch_map(&q_map);
         tma_prefetch_map(&kv_map);
@@ -252,34 +264,38 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         if (w < warp) before += ctl.warp_units[w];
         total += ctl.warp_units[w];
     }
-    int ngroups = min(p.groups, (total + kMlaMinUnits - 1) / kMlaMinUnits);
-    ngroups = ngroups < 1 ? 1 : ngroups;
+    const int ngroups = max(min(p.groups, total), 1);
     const int lo = group < ngroups ? int(int64_t(total) * group / ngroups) : total;
     const int hi = group < ngroups ? int(int64_t(total) * (group + 1) / ngroups) : total;
+    if (threadIdx.x == 0) {  // cuts at the very end lie in no request
+        if (lo == total) ctl.lo = total;
+        if (hi == total) ctl.hi = total;
+    }
     {
         int u = before + incl - mine;
         for (int b = r0; b < r1; ++b) {
             const int nb = blocks_of(seq_tokens(p, b)), n = units_of(nb);
-            if (lo < hi && lo >= u && lo < u + n) {
+            const auto settled = [&](int cut) {
+                return nb > kMlaWholeBlocks ? cut : ((cut - u) * 2 < n ? u : u + n);
+            };
+            if (lo >= u && lo < u + n) {
+                ctl.lo = settled(lo);
                 ctl.first_req = b;
-                ctl.first_unit = lo - u;
+                ctl.first_start = u;
             }
-            if (group == 0 && token == 0) {  // which groups hold the request, for the merge
-                int2 g = make_int2(0, -1);   // no entry
-                if (nb > 0) {
-                    g.x = int((int64_t(u + kMlaSegUnits + 1) * ngroups - 1) / total);
-                    g.y = int((int64_t(u + n) * ngroups - 1) / total);
-                }
-                p.plan[b] = g;
+            if (hi >= u && hi < u + n) ctl.hi = settled(hi);
+            int2 g = make_int2(0, 0);  // the first and last range that hold its blocks, for the merge
+            if (nb > kMlaWholeBlocks) {
+                g.x = int((int64_t(u + kMlaSegUnits + 1) * ngroups - 1) / total);
+                g.y = int((int64_t(u + n) * ngroups - 1) / total);
+                if (g.y > g.x && g.x + 1 == group) ctl.cut = b;
             }
+            if (group == 0 && token == 0) p.plan[b] = g;
             u += n;
         }
     }
-    if (threadIdx.x == 0) {
-        ctl.lo = lo;
-        ctl.hi = hi;
-    }
     __syncthreads();
+    if (threadIdx.x == 0 && token == 0) p.cuts[group] = ctl.cut;
     const uint32_t tmem_base = ctl.tmem_base;
 
     if (warp == 0) {
@@ -476,7 +492,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 #pragma unroll 1
                             for (int kk = 0; 16 * kk < valid; ++kk) step(kk);
                         }
-                        umma_commit(&ctl.v_empty[4 * buf + j]);
+                        if (i + 1 < blocks) umma_commit(&ctl.v_empty[4 * buf + j]);
                     }
                     umma_commit(&ctl.pv_done);
                 }
@@ -493,6 +509,54 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             umma_commit(&ctl.all_done);
         }
         __syncwarp();
+    } else if (warp == 3) {
+        // ================= output stores =================
+        // Requests without entries: out = 0, lse = -inf.
+        for (int b = group; b < p.batch; b += p.groups) {
+            if (blocks_of(seq_tokens(p, b)) > 0) continue;
+            const int64_t row = int64_t(b) * p.tokens + token;
+            uint4* o = reinterpret_cast<uint4*>(p.out + row * kMlaHeads * kMlaDv);
+            for (int i = lane; i < kMlaHeads * kMlaDv / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+            for (int h = lane; h < kMlaHeads; h += 32) p.lse[row * kMlaHeads + h] = -INFINITY;
+        }
+        const bool issuer = elect_one();
+        Walk w(ctl, p);
+        bool ok = true;
+        int n = 0, staged = 0;  // blocks so far, and stagings
+        while (ok && w.next(p)) {
+            n += w.bhi - w.blo;
+            const int buf = (n - 1) & 1;  // the ring half of the request's last block
+            const bool whole = w.blo == 0 && w.bhi == w.nb;
+            const int64_t row = int64_t(w.req()) * p.tokens + token;
+            const int64_t part = int64_t(group * p.tokens + token) * 2 + (w.blo == 0 ? 1 : 0);
+            uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(p.out + row * kMlaHeads * kMlaDv)
+                                 : reinterpret_cast<uint8_t*>(p.o_part + part * kMlaHeads * kMlaDv);
+            const int rounds = whole ? 1 : 2;  // 64 heads of bf16, or 32 of fp32 at a time
+            for (int r = 0; r < rounds && ok; ++r, ++staged) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.stage_full, uint32_t(staged & 1), &ctl.abort)) != 0;
+                if (ok && issuer) {
+                    for (int c = 0; c < 4; ++c)
+                        bulk_store(dst + r * 4 * kPairBytes + c * kPairBytes,
+                                   s_base + kOffV + (4 * buf + c) * kPairBytes, uint32_t(kPairBytes));
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    if (r + 1 < rounds) {
+                        mbar_arrive(&ctl.stage_free);
+                    } else {
+                        for (int j = 0; j < 4; ++j) mbar_arrive(&ctl.v_empty[4 * buf + j]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (issuer) {
+            if (!ok) {
+                atomicOr(p.err, kErrWaitTimeout);
+                ctl.abort = 1;
+            }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
+        __syncwarp();
     } else if (warp >= kSoftWarp0) {
         // ================= softmax and output =================
         const int quad = warp & 3;
@@ -503,7 +567,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         uint8_t* const pbuf = tiles + kOffP;
         Walk w(ctl, p);
         bool failed = false;
-        int n = 0;
+        int n = 0, halves = 0;  // blocks so far, and outputs staged in two halves
         while (!failed && w.next(p)) {
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
             bool fresh = true;  // no product of this request yet: O^T holds nothing of it
@@ -647,33 +711,63 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 }
             }
             soft_bar_sync();
-            // This warp: dims 128 j + 32 quad + lane of j = 2 half, 2 half + 1; all heads.
+            // This warp: dims 128 j + 32 quad + lane of j = 2 half, 2 half + 1.  Into the ring half of the
+            // request's last block: all heads as bf16, or (a partial) 32 heads as fp32, twice.
+            uint8_t* const stage = tiles + kOffV + ((n - 1) & 1) * 4 * kPairBytes;
+            const int rounds = whole ? 1 : 2;
 #pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                uint32_t r[32];
-                const int d = 128 * (2 * half + (j >> 1)) + 32 * quad + lane;
-                const int hb = 32 * (j & 1);
-                if (fresh) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = 0u;
-                } else {
-                    tmem_ld_32x32b_x32(lane_addr + kColO + 64u * (2 * half + (j >> 1)) + hb, r);
-                    tmem_ld_wait(r);
+            for (int rd = 0; rd < rounds; ++rd) {
+                if (rd > 0) {
+                    ok = mbar_wait(&ctl.stage_free, uint32_t(halves & 1), &ctl.abort);
+                    ++halves;
+                    if (!__all_sync(0xffffffffu, ok)) break;
                 }
-                if (whole) {
-                    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + (row * kMlaHeads + hb) * kMlaDv + d;
+#pragma unroll 1
+                for (int c = 0; c < (whole ? 4 : 2); ++c) {
+                    uint32_t r[32];
+                    const int j = 2 * half + (c & 1);
+                    const int hb = 32 * (whole ? c >> 1 : rd);
+                    if (fresh) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i * kMlaDv] = __float2bfloat16_rn(__uint_as_float(r[i]) * ctl.alpha[hb + i]);
-                } else {
-                    float* o = p.o_part + (part * kMlaHeads + hb) * kMlaDv + d;
+                        for (int i = 0; i < 32; ++i) r[i] = 0u;
+                    } else {
+                        tmem_ld_32x32b_x32(lane_addr + kColO + 64u * j + hb, r);
+                        tmem_ld_wait(r);
+                    }
+                    if (rd + 1 == rounds && c + 1 == (whole ? 4 : 2)) {  // the last of O^T is in registers
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl.o_empty);
+                    }
+                    const int d = 128 * j + 32 * quad + lane;
+                    const float4* scale = reinterpret_cast<const float4*>(ctl.alpha + hb);
+                    if (whole) {
+                        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(stage) + hb * kMlaDv + d;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i * kMlaDv] = __uint_as_float(r[i]) * ctl.alpha[hb + i];
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 f = scale[i / 4];
+                            o[i * kMlaDv] = __float2bfloat16_rn(__uint_as_float(r[i]) * f.x);
+                            o[(i + 1) * kMlaDv] = __float2bfloat16_rn(__uint_as_float(r[i + 1]) * f.y);
+                            o[(i + 2) * kMlaDv] = __float2bfloat16_rn(__uint_as_float(r[i + 2]) * f.z);
+                            o[(i + 3) * kMlaDv] = __float2bfloat16_rn(__uint_as_float(r[i + 3]) * f.w);
+                        }
+                    } else {
+                        float* o = reinterpret_cast<float*>(stage) + d;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 f = scale[i / 4];
+                            o[i * kMlaDv] = __uint_as_float(r[i]) * f.x;
+                            o[(i + 1) * kMlaDv] = __uint_as_float(r[i + 1]) * f.y;
+                            o[(i + 2) * kMlaDv] = __uint_as_float(r[i + 2]) * f.z;
+                            o[(i + 3) * kMlaDv] = __uint_as_float(r[i + 3]) * f.w;
+                        }
+                    }
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.stage_full);
             }
-            tc_fence_before_sync();
-            soft_bar_sync();  // alpha and row_max are free again
-            if (lane == 0) mbar_arrive(&ctl.o_empty);
+            // alpha and row_max are written again only behind the next block's first barrier
         }
         if (failed && threadIdx.x == kSoftWarp0 * 32) {
             atomicOr(p.err, kErrWaitTimeout);
@@ -694,24 +788,21 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 }
 
 // o[r] = sum_i exp(lse_i - lse) o_i over the partials of a split request, lse = log sum_i exp(lse_i).
-// Grid (64 heads, rows); 128 threads per 512 dims, blockDim / 128 partials at a time.
+// Grid (64 heads, requests or cuts x tokens); 128 threads per 512 dims, blockDim / 128 partials at a time.
 __global__ void __launch_bounds__(512) mla_dense_merge_kernel(const MlaDenseParams p) {
     __shared__ float wgt[kMlaMaxGroups];
     __shared__ float4 acc_s[3][128];
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
     const int h = blockIdx.x;
-    const int64_t row = blockIdx.y;
-    const int b = int(row / p.tokens), token = int(row % p.tokens);
+    const int token = int(blockIdx.y) % p.tokens;
+    const int b = p.merge_by_cut ? p.cuts[blockIdx.y / p.tokens] : int(blockIdx.y) / p.tokens;
+    if (b < 0) return;
+    const int64_t row = int64_t(b) * p.tokens + token;
     const int2 g = p.plan[b];
     if (g.x == g.y) return;  // one range: written by the decode kernel
     const int quarter = threadIdx.x >> 7, d4 = threadIdx.x & 127;
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + (row * kMlaHeads + h) * kMlaDv + 4 * d4;
-    if (g.y < g.x) {  // no entry
-        if (quarter == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0, 0);
-        if (threadIdx.x == 0) p.lse[row * kMlaHeads + h] = -INFINITY;
-        return;
-    }
     const int S = g.y - g.x + 1;
     // partial i: range g.x + i; the first one ends in the next range, the others began earlier
     const auto part = [&](int i) { return (int64_t(g.x + i) * p.tokens + token) * 2 + (i == 0 ? 1 : 0); };
@@ -778,8 +869,9 @@ cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, mla_dense_kernel, q_map, kv_map, kr_map, p);
     if (e != cudaSuccess) return e;
-    // Few rows are split many ways: more threads per row read more partials at a time.
-    const int rows = p.batch * p.tokens;
+    // One row of CTAs per request, or, where they are fewer, per cut between ranges.  Few rows are split
+    // many ways: more threads per row read more partials at a time.
+    const int rows = (p.merge_by_cut ? p.groups : p.batch) * p.tokens;
     cfg.gridDim = dim3(kMlaHeads, unsigned(rows));
     cfg.blockDim = dim3(rows <= 16 ? 512 : 256);
     cfg.dynamicSmemBytes = 0;

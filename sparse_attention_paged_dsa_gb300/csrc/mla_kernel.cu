@@ -91,13 +91,6 @@ constexpr int kSmemM = 1024 + kOffCtl + int(sizeof(MlaCtl));
 static_assert(kSmemM <= 232448, "fits one CTA per SM");
 static_assert(kVRing * kPairBytes == kMlaHeads * kMlaDv * 4, "o fits the value ring");
 
-// Bulk copy of `bytes` (multiple of 16) from shared to global memory, tracked by this
-// thread's bulk-async group.
-__device__ __forceinline__ void bulk_store(void* gdst, uint32_t ssrc, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gdst), "r"(ssrc), "r"(bytes)
-                 : "memory");
-}
-
 // TMA row gather: rows y0..y3 of a 2-D tensor map (box = one row of 64 bf16), columns
 // [x, x + 64), into 4 x 128 bytes at `dst` (swizzled by the map, like a 4-row tile).
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
