@@ -731,12 +731,14 @@ dsa_status_t dsa_mla_decode(const void* q, const void* kv_cache, int64_t num_pag
     const int groups = dense_groups(sms, next_n);
     st = check_workspace(workspace, workspace_bytes, dense_workspace_bytes(groups, next_n));
     if (st != DSA_OK) return st;
-    CUtensorMap q_map, kv_map, kr_map;
+    CUtensorMap q_map, kv_map, kr_map, o_map;
     st = make_slabs_map(&q_map, q, int64_t(batch) * next_n * DSA_MLA_HEADS, 3, "mla q");
     if (st != DSA_OK) return st;
     st = make_slabs_map(&kv_map, kv_cache, num_pages * dsa::kPageEntries, 2, "mla kv");
     if (st != DSA_OK) return st;
     st = make_rows_map(&kr_map, kv_cache, num_pages * dsa::kPageEntries, DSA_MLA_DIM, 64, "mla kv");
+    if (st != DSA_OK) return st;
+    st = make_rows_map(&o_map, out, int64_t(batch) * next_n * DSA_MLA_HEADS, DSA_MLA_DV, 64, "mla out");
     if (st != DSA_OK) return st;
     dsa::MlaDenseParams p{};
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -757,7 +759,7 @@ dsa_status_t dsa_mla_decode(const void* q, const void* kv_cache, int64_t num_pag
     p.groups = groups;
     p.merge_by_cut = batch > groups ? 1 : 0;
     p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
-    e = dsa::launch_mla_dense(q_map, kv_map, kr_map, p, static_cast<cudaStream_t>(stream));
+    e = dsa::launch_mla_dense(q_map, kv_map, kr_map, o_map, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA decode launch");
 }
 

@@ -163,9 +163,10 @@ struct MlaDenseParams {
 };
 // q_map and kv_map: 576-wide bf16 rows (q: batch * tokens * 64 of them; the cache: num_pages * 64) as
 // (dim in slab, row, slab of 64 dims), boxes of 64 rows x 3 slabs and 64 rows x 2 slabs; kr_map: the
-// cache's rows as (dim, row), boxes of 64 x 64.  All 128-byte-swizzled.
+// cache's rows as (dim, row), boxes of 64 x 64; o_map: out as [batch * tokens * 64, 512] rows, boxes of
+// 64 x 64.  All 128-byte-swizzled.
 cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& kr_map,
-                             const MlaDenseParams& p, cudaStream_t stream);
+                             const CUtensorMap& o_map, const MlaDenseParams& p, cudaStream_t stream);
 
 // Latent attention over ragged prompts, expanded form: per-head 128 + 64 shared key dims, 128 value dims.
 constexpr int kPrefillQk = 192;

@@ -128,6 +128,36 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
         : "r"(taddr));
 }
 
+// The same with 64 columns.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// Four 8 x 8 matrices of 16-bit elements, stored transposed: lane 4 i + k holds row i, columns 2 k and
+// 2 k + 1; lane 8 m + c gives the 16-byte address of column c of matrix m.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&v)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+
+// Tiled store of a box at (x, y), tracked by this thread's bulk-async group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
 // Rows [row, row + 64) of the map's slabs [slab, ...) (a (dim in slab, row, slab) view of 576-wide rows)
 // into consecutive 64 x 64 slabs.
 __device__ __forceinline__ void tma_load_slabs(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t row,
@@ -155,6 +185,19 @@ __device__ __forceinline__ int seq_tokens(const MlaDenseParams& p, int b) {
 __device__ __forceinline__ int blocks_of(int seq) { return (((seq + 3) >> 2) + kBlk - 1) / kBlk; }
 __device__ __forceinline__ int units_of(int blocks) { return blocks ? blocks + kMlaSegUnits : 0; }
 
+// Equal ranges of `total` units: range g is [cut(g), cut(g + 1)).  32-bit arithmetic only.
+struct Ranges {
+    int n, total, q, r;
+    __device__ __forceinline__ Ranges(int n_, int total_) : n(n_), total(total_), q(total_ / n_), r(total_ % n_) {}
+    __device__ __forceinline__ int cut(int g) const { return q * g + r * g / n; }  // r * g < 2^16
+    __device__ __forceinline__ int of(int unit) const {                           // the range that holds a unit
+        int g = min(int(float(unit) * float(n) / float(total)), n - 1);
+        while (g > 0 && cut(g) > unit) --g;
+        while (g + 1 < n && cut(g + 1) <= unit) ++g;
+        return g;
+    }
+};
+
 // The CTA's walk over its range: one step per request that has blocks in it.
 struct Walk {
     int b, u0, lo, hi, batch;  // request b starts at unit u0; range [lo, hi)
@@ -175,6 +218,8 @@ struct Walk {
         return false;
     }
     __device__ __forceinline__ int req() const { return b - 1; }
+    // Nothing follows the current request (false if the range ends in units without blocks).
+    __device__ __forceinline__ bool last() const { return b >= batch || u0 >= hi; }
     // Entries of block `blk` that token `back` from the end sees.
     __device__ __forceinline__ int valid(int blk, int back) const {
         const int n = (max(seq - back, 0) + 3) >> 2;
@@ -193,7 +238,8 @@ __device__ __forceinline__ int page_of_lane(const MlaDenseParams& p, const Walk&
 
 __global__ void __launch_bounds__(kThreadsD, 1)
     mla_dense_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
-                     const __grid_constant__ CUtensorMap kr_map, const MlaDenseParams p) {
+                     const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap o_map,
+                     const MlaDenseParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     DenseCtl& ctl = *reinterpret_cast<DenseCtl*>(tiles + kOffCtl);
@@ -265,8 +311,9 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         total += ctl.warp_units[w];
     }
     const int ngroups = max(min(p.groups, total), 1);
-    const int lo = group < ngroups ? int(int64_t(total) * group / ngroups) : total;
-    const int hi = group < ngroups ? int(int64_t(total) * (group + 1) / ngroups) : total;
+    const Ranges ranges(ngroups, total);
+    const int lo = group < ngroups ? ranges.cut(group) : total;
+    const int hi = group < ngroups ? ranges.cut(group + 1) : total;
     if (threadIdx.x == 0) {  // cuts at the very end lie in no request
         if (lo == total) ctl.lo = total;
         if (hi == total) ctl.hi = total;
@@ -286,8 +333,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             if (hi >= u && hi < u + n) ctl.hi = settled(hi);
             int2 g = make_int2(0, 0);  // the first and last range that hold its blocks, for the merge
             if (nb > kMlaWholeBlocks) {
-                g.x = int((int64_t(u + kMlaSegUnits + 1) * ngroups - 1) / total);
-                g.y = int((int64_t(u + n) * ngroups - 1) / total);
+                g = make_int2(ranges.of(u + kMlaSegUnits), ranges.of(u + n - 1));
                 if (g.y > g.x && g.x + 1 == group) ctl.cut = b;
             }
             if (group == 0 && token == 0) p.plan[b] = g;
@@ -529,15 +575,24 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             const bool whole = w.blo == 0 && w.bhi == w.nb;
             const int64_t row = int64_t(w.req()) * p.tokens + token;
             const int64_t part = int64_t(group * p.tokens + token) * 2 + (w.blo == 0 ? 1 : 0);
-            uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(p.out + row * kMlaHeads * kMlaDv)
-                                 : reinterpret_cast<uint8_t*>(p.o_part + part * kMlaHeads * kMlaDv);
-            const int rounds = whole ? 1 : 2;  // 64 heads of bf16, or 32 of fp32 at a time
+            uint8_t* dst = reinterpret_cast<uint8_t*>(p.o_part + part * kMlaHeads * kMlaDv);
+            const int rounds = whole || w.last() ? 1 : 2;
             for (int r = 0; r < rounds && ok; ++r, ++staged) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&ctl.stage_full, uint32_t(staged & 1), &ctl.abort)) != 0;
                 if (ok && issuer) {
-                    for (int c = 0; c < 4; ++c)
-                        bulk_store(dst + r * 4 * kPairBytes + c * kPairBytes,
-                                   s_base + kOffV + (4 * buf + c) * kPairBytes, uint32_t(kPairBytes));
+                    if (whole) {
+#pragma unroll
+                        for (int t = 0; t < 8; ++t)
+                            tma_store_2d(&o_map, s_base + kOffV + 4 * buf * kPairBytes + t * kSlabBytes, 64 * t,
+                                         int(row) * kMlaHeads);
+                    } else if (rounds == 1) {  // the whole ring
+                        for (int c = 0; c < 8; ++c)
+                            bulk_store(dst + c * kPairBytes, s_base + kOffV + c * kPairBytes, uint32_t(kPairBytes));
+                    } else {
+                        for (int c = 0; c < 4; ++c)
+                            bulk_store(dst + r * 4 * kPairBytes + c * kPairBytes,
+                                       s_base + kOffV + (4 * buf + c) * kPairBytes, uint32_t(kPairBytes));
+                    }
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     if (r + 1 < rounds) {
@@ -711,48 +766,86 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 }
             }
             soft_bar_sync();
-            // This warp: dims 128 j + 32 quad + lane of j = 2 half, 2 half + 1.  Into the ring half of the
-            // request's last block: all heads as bf16, or (a partial) 32 heads as fp32, twice.
-            uint8_t* const stage = tiles + kOffV + ((n - 1) & 1) * 4 * kPairBytes;
-            const int rounds = whole ? 1 : 2;
+            const auto o_read = [&] {  // the last of O^T is in registers
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.o_empty);
+            };
+            const auto staged = [&] {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.stage_full);
+            };
+            if (whole) {
+                // bf16, into the ring half of the request's last block: eight 128-byte-swizzled tiles of
+                // 64 heads x 64 dims.  This warp: 16-dim strips 128 j + 32 quad + 16 s of j = 2 half,
+                // 2 half + 1; each 8 x 8 (dims x heads) piece of a strip is stored transposed.
+                const uint32_t stage = s_base + kOffV + ((n - 1) & 1) * 4 * kPairBytes;
 #pragma unroll 1
-            for (int rd = 0; rd < rounds; ++rd) {
-                if (rd > 0) {
-                    ok = mbar_wait(&ctl.stage_free, uint32_t(halves & 1), &ctl.abort);
-                    ++halves;
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                }
-#pragma unroll 1
-                for (int c = 0; c < (whole ? 4 : 2); ++c) {
+                for (int c = 0; c < 4; ++c) {
                     uint32_t r[32];
-                    const int j = 2 * half + (c & 1);
-                    const int hb = 32 * (whole ? c >> 1 : rd);
+                    const int j = 2 * half + (c >> 1), s16 = c & 1;
                     if (fresh) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) r[i] = 0u;
                     } else {
-                        tmem_ld_32x32b_x32(lane_addr + kColO + 64u * j + hb, r);
+                        tmem_ld_16x256b_x8(lane_addr + (uint32_t(16 * s16) << 16) + kColO + 64u * j, r);
                         tmem_ld_wait(r);
                     }
-                    if (rd + 1 == rounds && c + 1 == (whole ? 4 : 2)) {  // the last of O^T is in registers
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ctl.o_empty);
-                    }
-                    const int d = 128 * j + 32 * quad + lane;
-                    const float4* scale = reinterpret_cast<const float4*>(ctl.alpha + hb);
-                    if (whole) {
-                        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(stage) + hb * kMlaDv + d;
+                    if (c == 3) o_read();
+                    // Tile 2 j + quad / 2, 16-byte chunks ch0 (dims 0-7 of the strip) and ch0 + 1.
+                    const uint32_t tile = stage + (2 * j + (quad >> 1)) * kSlabBytes;
+                    const int ch0 = 4 * (quad & 1) + 2 * s16;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 f = scale[i / 4];
-                            o[i * kMlaDv] = __float2bfloat16_rn(__uint_as_float(r[i]) * f.x);
-                            o[(i + 1) * kMlaDv] = __float2bfloat16_rn(__uint_as_float(r[i + 1]) * f.y);
-                            o[(i + 2) * kMlaDv] = __float2bfloat16_rn(__uint_as_float(r[i + 2]) * f.z);
-                            o[(i + 3) * kMlaDv] = __float2bfloat16_rn(__uint_as_float(r[i + 3]) * f.w);
+                    for (int k = 0; k < 8; k += 2) {  // heads [8 k, 8 k + 16)
+                        uint32_t v[4];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 f = *reinterpret_cast<const float2*>(ctl.alpha + 8 * (k + e) + 2 * (lane & 3));
+#pragma unroll
+                            for (int d8 = 0; d8 < 2; ++d8) {
+                                const int q = 4 * (k + e) + 2 * d8;
+                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(r[q]) * f.x,
+                                                                                __uint_as_float(r[q + 1]) * f.y);
+                                v[2 * e + d8] = *reinterpret_cast<const uint32_t*>(&b2);
+                            }
                         }
-                    } else {
-                        float* o = reinterpret_cast<float*>(stage) + d;
+                        // lane's row address: piece lane / 8 is (heads + 8 (piece / 2), dims + 8 (piece % 2))
+                        const int h = 8 * k + 8 * (lane >> 4) + (lane & 7);
+                        const int ch = ch0 + ((lane >> 3) & 1);
+                        stmatrix_x4_trans(tile + h * 128 + ((ch ^ (h & 7)) << 4), v);
+                    }
+                }
+                staged();
+            } else {
+                // fp32: the whole ring if nothing follows, else 32 heads at a time in the half of the
+                // request's last block.  This warp: dims 128 j + 32 quad + lane of the same j.
+                const int rounds = w.last() ? 1 : 2;
+                float* const stage =
+                    reinterpret_cast<float*>(tiles + kOffV + (rounds == 1 ? 0 : ((n - 1) & 1) * 4 * kPairBytes));
+#pragma unroll 1
+                for (int rd = 0; rd < rounds; ++rd) {
+                    if (rd > 0) {
+                        ok = mbar_wait(&ctl.stage_free, uint32_t(halves & 1), &ctl.abort);
+                        ++halves;
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                    }
+                    const int chunks = rounds == 1 ? 4 : 2;
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        uint32_t r[32];
+                        const int j = 2 * half + (c & 1);
+                        const int hb = 32 * (rounds == 1 ? c >> 1 : rd);
+                        if (fresh) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) r[i] = 0u;
+                        } else {
+                            tmem_ld_32x32b_x32(lane_addr + kColO + 64u * j + hb, r);
+                            tmem_ld_wait(r);
+                        }
+                        if (rd + 1 == rounds && c + 1 == chunks) o_read();
+                        float* o = stage + (rounds == 1 ? hb * kMlaDv : 0) + 128 * j + 32 * quad + lane;
+                        const float4* scale = reinterpret_cast<const float4*>(ctl.alpha + hb);
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             const float4 f = scale[i / 4];
@@ -762,10 +855,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                             o[(i + 3) * kMlaDv] = __uint_as_float(r[i + 3]) * f.w;
                         }
                     }
+                    staged();
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl.stage_full);
             }
             // alpha and row_max are written again only behind the next block's first barrier
         }
@@ -788,68 +879,72 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 }
 
 // o[r] = sum_i exp(lse_i - lse) o_i over the partials of a split request, lse = log sum_i exp(lse_i).
-// Grid (64 heads, requests or cuts x tokens); 128 threads per 512 dims, blockDim / 128 partials at a time.
+// 512 threads, 128 of them per 512 dims: four heads a CTA, or (few rows, each split many ways) one head
+// whose partials go to the four quarters in turn.  Grid (heads, requests or cuts x tokens).
+template <bool kOneHead>
 __global__ void __launch_bounds__(512) mla_dense_merge_kernel(const MlaDenseParams p) {
-    __shared__ float wgt[kMlaMaxGroups];
-    __shared__ float4 acc_s[3][128];
+    __shared__ float wgt[kOneHead ? 1 : 4][kMlaMaxGroups];
+    __shared__ float4 acc_s[kOneHead ? 3 : 1][128];
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
-    const int h = blockIdx.x;
+    const int quarter = threadIdx.x >> 7, d4 = threadIdx.x & 127;
+    const int h = kOneHead ? int(blockIdx.x) : int(blockIdx.x) * 4 + quarter;
     const int token = int(blockIdx.y) % p.tokens;
     const int b = p.merge_by_cut ? p.cuts[blockIdx.y / p.tokens] : int(blockIdx.y) / p.tokens;
     if (b < 0) return;
     const int64_t row = int64_t(b) * p.tokens + token;
     const int2 g = p.plan[b];
     if (g.x == g.y) return;  // one range: written by the decode kernel
-    const int quarter = threadIdx.x >> 7, d4 = threadIdx.x & 127;
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + (row * kMlaHeads + h) * kMlaDv + 4 * d4;
     const int S = g.y - g.x + 1;
     // partial i: range g.x + i; the first one ends in the next range, the others began earlier
     const auto part = [&](int i) { return (int64_t(g.x + i) * p.tokens + token) * 2 + (i == 0 ? 1 : 0); };
-    if (threadIdx.x < 32) {
+    if ((threadIdx.x & 127) < 32 && (!kOneHead || quarter == 0)) {
+        float* const w = wgt[kOneHead ? 0 : quarter];
+        const int lane = threadIdx.x & 31;
         float mx = -INFINITY;
-        for (int i = threadIdx.x; i < S; i += 32) {
-            wgt[i] = p.lse_part[part(i) * kMlaHeads + h];
-            mx = fmaxf(mx, wgt[i]);
+        for (int i = lane; i < S; i += 32) {
+            w[i] = p.lse_part[part(i) * kMlaHeads + h];
+            mx = fmaxf(mx, w[i]);
         }
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         float sum = 0.f;
-        for (int i = threadIdx.x; i < S; i += 32) {
-            const float e = mx == -INFINITY ? 0.f : expf(wgt[i] - mx);
-            wgt[i] = e;
+        for (int i = lane; i < S; i += 32) {
+            const float e = mx == -INFINITY ? 0.f : expf(w[i] - mx);
+            w[i] = e;
             sum += e;
         }
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        for (int i = threadIdx.x; i < S; i += 32) wgt[i] *= inv;
-        if (threadIdx.x == 0) p.lse[row * kMlaHeads + h] = mx == -INFINITY ? -INFINITY : mx + logf(sum);
+        for (int i = lane; i < S; i += 32) w[i] *= inv;
+        if (lane == 0) p.lse[row * kMlaHeads + h] = mx == -INFINITY ? -INFINITY : mx + logf(sum);
     }
     __syncthreads();
+    const float* const w = wgt[kOneHead ? 0 : quarter];
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int step = blockDim.x >> 7;
 #pragma unroll 8
-    for (int i = quarter; i < S; i += step) {
+    for (int i = kOneHead ? quarter : 0; i < S; i += kOneHead ? 4 : 1) {
         const float4 v = *reinterpret_cast<const float4*>(p.o_part + (part(i) * kMlaHeads + h) * kMlaDv + 4 * d4);
-        const float wt = wgt[i];
-        acc.x = fmaf(wt, v.x, acc.x), acc.y = fmaf(wt, v.y, acc.y);
-        acc.z = fmaf(wt, v.z, acc.z), acc.w = fmaf(wt, v.w, acc.w);
+        acc.x = fmaf(w[i], v.x, acc.x), acc.y = fmaf(w[i], v.y, acc.y);
+        acc.z = fmaf(w[i], v.z, acc.z), acc.w = fmaf(w[i], v.w, acc.w);
     }
-    if (quarter > 0) acc_s[quarter - 1][d4] = acc;
-    __syncthreads();
-    if (quarter > 0) return;
-    for (int q = 1; q < step; ++q) {
-        const float4 v = acc_s[q - 1][d4];
-        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    if constexpr (kOneHead) {
+        if (quarter > 0) acc_s[quarter - 1][d4] = acc;
+        __syncthreads();
+        if (quarter > 0) return;
+        for (int q = 0; q < 3; ++q) {
+            const float4 v = acc_s[q][d4];
+            acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
     }
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-    *reinterpret_cast<uint2*>(out) =
+    *reinterpret_cast<uint2*>(p.out + (row * kMlaHeads + h) * kMlaDv + 4 * d4) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 }  // namespace
 
 cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& kr_map,
-                             const MlaDenseParams& p, cudaStream_t stream) {
+                             const CUtensorMap& o_map, const MlaDenseParams& p, cudaStream_t stream) {
     static SmemLimitOnce smem_limit;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -867,15 +962,17 @@ cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, mla_dense_kernel, q_map, kv_map, kr_map, p);
+    e = cudaLaunchKernelEx(&cfg, mla_dense_kernel, q_map, kv_map, kr_map, o_map, p);
     if (e != cudaSuccess) return e;
     // One row of CTAs per request, or, where they are fewer, per cut between ranges.  Few rows are split
     // many ways: more threads per row read more partials at a time.
     const int rows = (p.merge_by_cut ? p.groups : p.batch) * p.tokens;
-    cfg.gridDim = dim3(kMlaHeads, unsigned(rows));
-    cfg.blockDim = dim3(rows <= 16 ? 512 : 256);
+    const bool one_head = rows <= 16;
+    cfg.gridDim = dim3(one_head ? kMlaHeads : kMlaHeads / 4, unsigned(rows));
+    cfg.blockDim = dim3(512);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, mla_dense_merge_kernel, p);
+    return one_head ? cudaLaunchKernelEx(&cfg, mla_dense_merge_kernel<true>, p)
+                    : cudaLaunchKernelEx(&cfg, mla_dense_merge_kernel<false>, p);
 }
 
 }  // namespace dsa
