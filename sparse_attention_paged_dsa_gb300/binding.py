@@ -404,35 +404,42 @@ def dsa_sparse_mla_decode(q, kv_cache, page_table, seq_lens, max_context: int, t
 
 def _run(fn, device: int, *args):
     """Call the C entry point ``fn`` with ``args`` and the current stream of ``device``, on that device."""
-    if device == torch.cuda.current_device():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    stream = torch._C._cuda_getCurrentRawStream(device)
+    if device == torch._C._cuda_getDevice():
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(device))
-    if st != DSA_OK:
+            st = fn(*args, stream)
+    if st:
         raise DsaError(st, fn.__name__)
 
 
 def _on(t, name, dtypes, shape, device: int):
     """``_need`` for a tensor that must also be on ``device`` (one test on the path of a good call)."""
-    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == device
-            and t.is_contiguous()):
-        return
+    try:
+        if t.dtype in dtypes and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
     _need(t, name, dtypes, shape)
     raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
 
 
 def _device_of(t, name, dtypes, dims) -> int:
     """The device index of the call's leading tensor, after its own checks but for the layout."""
+    try:
+        device = t.get_device()
+        if device >= 0 and t.dtype in dtypes and t.dim() in dims:
+            return device
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.dim() not in dims:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}")
-    return t.get_device()
+    raise ValueError(f"{name} has shape {tuple(t.shape)}")
 
 
 def _addr(t):
@@ -476,7 +483,7 @@ def dsa_mla_decode(q, kv_cache, page_table, seq_lens, max_context: int, sm_scale
     lead = q.shape[:-2]
     B, Q = lead[0], (lead[1] if len(lead) == 2 else 1)
     _on(q, "q", _BF16, (*lead, MLA_HEADS, MLA_DIM), dev)
-    pages = kv_cache.shape[0] if isinstance(kv_cache, torch.Tensor) and kv_cache.dim() else 0
+    pages = kv_cache.shape[0] if isinstance(kv_cache, torch.Tensor) and kv_cache.dim() == 3 else 0
     _on(kv_cache, "kv_cache", _BF16, (pages, PAGE_ENTRIES, MLA_DIM), dev)
     _on(page_table, "page_table", _I32, (B, max_context // PAGE_TOKENS), dev)
     _on(seq_lens, "seq_lens", _I32, (B,), dev)

@@ -358,13 +358,18 @@ dsa_status_t run_rmsnorm(dsa::RmsNormParams p, void* stream) {
         return DSA_ERR_INVALID_ARG;
     if (p.out && p.out == p.residual_out) return DSA_ERR_INVALID_ARG;
     if ((p.out == p.x || p.residual_out == p.x) && p.x_stride != p.d) return DSA_ERR_INVALID_ARG;
-    const bool wide = p.d % 8 == 0 && p.x_stride % 8 == 0 && aligned(p.x, 16) && aligned(p.residual, 16) &&
-                      aligned(p.weight, 16) && aligned(p.residual_out, 16) && aligned(p.out, 16) &&
-                      aligned(p.codes, 8);
+    // The boundary that every 16-element unit of every array starts on (its codes: half of it), in bytes.
+    const auto on = [&](uintptr_t bytes) {
+        const int64_t n = int64_t(bytes) / 2;
+        return p.d % n == 0 && p.x_stride % n == 0 && aligned(p.x, bytes) && aligned(p.residual, bytes) &&
+               aligned(p.weight, p.weight_fp32 ? 16 : bytes) && aligned(p.residual_out, bytes) &&
+               aligned(p.out, bytes) && aligned(p.codes, bytes / 2);
+    };
+    const int align = on(32) ? 32 : on(16) ? 16 : 2;
     int sms = 0;
     cudaError_t e = sm_count(&sms);
     if (e != cudaSuccess) return cuda_fail(e, "device query");
-    e = dsa::launch_rmsnorm(p, wide, sms, static_cast<cudaStream_t>(stream));
+    e = dsa::launch_rmsnorm(p, align, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "RMS norm launch");
 }
 

@@ -207,9 +207,12 @@ struct RmsNormParams {
     int32_t group;            // 64, 128 or 0 (one scale per row)
     int32_t weight_fp32;
     int32_t row_threads;      // threads that share a row (set by the launch)
+    int32_t log2_threads;     // of row_threads, where several rows share a CTA
+    int32_t ahead;            // how many rows ahead a CTA fetches into L2 (set by the launch)
     float eps;
 };
-// wide: 16-byte vectors of every array are aligned and d is a multiple of 8.
-cudaError_t launch_rmsnorm(RmsNormParams p, bool wide, int sms, cudaStream_t stream);
+// align: 32, 16 or 2, the boundary in bytes of every 16-element unit (codes: half of it); d is a multiple
+// of align / 2.
+cudaError_t launch_rmsnorm(RmsNormParams p, int align, int sms, cudaStream_t stream);
 
 }  // namespace dsa

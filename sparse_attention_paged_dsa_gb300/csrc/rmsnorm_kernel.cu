@@ -9,9 +9,16 @@
 // the unrounded sum; each output is rounded once), so a row is read and written
 // once: HBM-bound for many rows, launch latency for few.
 //
-// A row belongs to T threads; vector v (8 consecutive elements, one 16-byte load)
-// belongs to thread v % T, so neighbouring lanes hold neighbouring vectors and a
-// quantisation group of 64 or 128 elements is 8 or 16 neighbouring lanes.
+// A row belongs to T threads; unit v (16 consecutive elements, one 32-byte load)
+// belongs to thread v % T, so neighbouring lanes hold neighbouring units and a
+// quantisation group of 64 or 128 elements is 4 or 8 neighbouring lanes.
+//
+// What bounds it.  16384 x 7168, residual, e4m3 out: 123 us, 0.99 of the measured
+// copy rate (bf16 out: 140 us, 0.99).  Steps there: 8-element units, reductions over
+// run-time lane counts and scalar arithmetic, 35 instructions an element: 242 us;
+// 16-element units and packed fp32 pairs: 156; 40 registers, so that three CTAs of
+// one unit a thread are resident: 143; the next row fetched into L2: 123.  Without
+// a residual the e4m3 output is bound by its instructions (73 us, 0.72).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -24,193 +31,340 @@
 namespace dsa {
 namespace {
 
-constexpr int kVec = 8;           // elements per vector
+constexpr int kUnit = 16;         // elements per unit
+constexpr int kPairs = kUnit / 2;
 constexpr int kCta = 256;         // threads of a CTA whose rows have at most one warp each
 constexpr float kE4m3Max = 448.f;
 
-__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-
-// Eight consecutive bf16 from `p`; the last `kVec - n` read as 0.  Wide: one 16-byte load.
-template <bool kWide>
-__device__ __forceinline__ void load8(float (&v)[kVec], const __nv_bfloat16* p, int n) {
-    if constexpr (kWide) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-        v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.f;
-    }
+__device__ __forceinline__ float2 unpack_bf16(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float2 v) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-template <bool kWide>
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[kVec], int n) {
-    if constexpr (kWide) {
-        uint32_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            if (i < n) p[i] = __float2bfloat16_rn(v[i]);
+__device__ __forceinline__ void load_v8(uint32_t (&u)[kPairs], const void* p) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void store_v8(void* p, const uint32_t (&u)[kPairs]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]),
+                 "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+
+// A row's rows of the arrays, moved by its T threads.  kAlign: the boundary, in bytes, that every unit of
+// every array starts on.  32: one access a unit; 16: two (d a multiple of 8).  2: the row passes through
+// shared memory, so that global accesses are of neighbouring elements (unit by unit, 32 lanes touch
+// 32 sectors an access: 16384 x 7001 took 891 us, now 520).
+template <int kNV, bool kCtaRow, int kAlign>
+struct RowIo {
+    int T, t, d, units;  // units: 0 for threads past the last row
+    uint16_t* stage;     // kAlign 2: T x kNV x 16 elements of shared memory
+
+    __device__ __forceinline__ int unit(int j) const { return j * T + t; }
+    // Where the 8-element half `f` of this thread's unit j starts.  With 16-byte accesses two neighbouring
+    // threads share their units' halves alternately, so that each access is of whole sectors.
+    __device__ __forceinline__ int half_at(int j, int f) const {
+        const int v = unit(j);
+        return kAlign == 16 ? ((v >> 1) * 4 + (v & 1) + 2 * f) * 8 : v * kUnit + 8 * f;
     }
+    __device__ __forceinline__ void sync() const {
+        if constexpr (kCtaRow)
+            __syncthreads();
+        else
+            __syncwarp();
+    }
+    // Elements past the row read as 0.
+    __device__ __forceinline__ void load(float2 (&v)[kNV][kPairs], const uint16_t* p) const {
+        if constexpr (kAlign == 2) {
+#pragma unroll 4
+            for (int i = 0; i < kNV * kUnit; ++i) {
+                const int e = i * T + t;
+                stage[e] = units && e < d ? p[e] : uint16_t(0);
+            }
+            sync();
+        }
+#pragma unroll
+        for (int j = 0; j < kNV; ++j) {
+            uint32_t u[kPairs] = {};
+            if constexpr (kAlign == 2) {
+                const uint4* q = reinterpret_cast<const uint4*>(stage + unit(j) * kUnit);
+                const uint4 a = q[0], b = q[1];
+                u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w, u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
+            } else if constexpr (kAlign == 32) {
+                if (unit(j) < units) load_v8(u, p + unit(j) * kUnit);
+            } else {
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    uint4 a = make_uint4(0, 0, 0, 0);
+                    if (units && half_at(j, f) < d) a = *reinterpret_cast<const uint4*>(p + half_at(j, f));
+                    u[4 * f] = a.x, u[4 * f + 1] = a.y, u[4 * f + 2] = a.z, u[4 * f + 3] = a.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) v[j][i] = unpack_bf16(u[i]);
+        }
+        if constexpr (kAlign == 2) sync();
+    }
+    __device__ __forceinline__ void store(uint16_t* p, const float2 (&v)[kNV][kPairs]) const {
+#pragma unroll
+        for (int j = 0; j < kNV; ++j) {
+            uint32_t u[kPairs];
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) u[i] = pack_bf16(v[j][i]);
+            if constexpr (kAlign == 32) {
+                if (unit(j) < units) store_v8(p + unit(j) * kUnit, u);
+            } else {
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    if (kAlign == 2 || (units && half_at(j, f) < d))
+                        *reinterpret_cast<uint4*>((kAlign == 2 ? stage : p) + half_at(j, f)) =
+                            make_uint4(u[4 * f], u[4 * f + 1], u[4 * f + 2], u[4 * f + 3]);
+            }
+        }
+        if constexpr (kAlign == 2) {
+            sync();
+#pragma unroll 4
+            for (int i = 0; i < kNV * kUnit; ++i) {
+                const int e = i * T + t;
+                if (units && e < d) p[e] = stage[e];
+            }
+            sync();
+        }
+    }
+    __device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&pk)[kNV][4]) const {
+        uint8_t* const bytes = reinterpret_cast<uint8_t*>(stage);
+#pragma unroll
+        for (int j = 0; j < kNV; ++j) {
+            if constexpr (kAlign == 16) {
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    if (units && half_at(j, f) < d)
+                        *reinterpret_cast<uint2*>(p + half_at(j, f)) = make_uint2(pk[j][2 * f], pk[j][2 * f + 1]);
+            } else if (kAlign == 2 || unit(j) < units) {
+                *reinterpret_cast<uint4*>((kAlign == 2 ? bytes : p) + unit(j) * kUnit) =
+                    make_uint4(pk[j][0], pk[j][1], pk[j][2], pk[j][3]);
+            }
+        }
+        if constexpr (kAlign == 2) {
+            sync();
+#pragma unroll 4
+            for (int i = 0; i < kNV * kUnit; ++i) {
+                const int e = i * T + t;
+                if (units && e < d) p[e] = bytes[e];
+            }
+        }
+    }
+    __device__ __forceinline__ void load_weight_fp32(float2 (&v)[kNV][kPairs], const float* w) const {
+#pragma unroll
+        for (int j = 0; j < kNV; ++j) {
+#pragma unroll
+            for (int i = 0; i < kPairs; i += 2) {
+                const int e = half_at(j, i >> 2) + 2 * (i & 3);
+                const int n = units ? d - e : 0;
+                if constexpr (kAlign == 2) {
+                    v[j][i] = make_float2(0 < n ? w[e] : 0.f, 1 < n ? w[e + 1] : 0.f);
+                    v[j][i + 1] = make_float2(2 < n ? w[e + 2] : 0.f, 3 < n ? w[e + 3] : 0.f);
+                } else {
+                    const float4 a =
+                        0 < n ? __ldg(reinterpret_cast<const float4*>(w + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    v[j][i] = make_float2(a.x, a.y), v[j][i + 1] = make_float2(a.z, a.w);
+                }
+            }
+        }
+    }
+};
+
+// max(m, |v.x|, |v.y|); a NaN loses.
+__device__ __forceinline__ float max_abs3(float m, float2 v) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(v.x), "f"(v.y));
+    return r;
+}
+
+// Fetch `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // A correctly rounded quotient, kept out of line: only groups at the ends of fp32's range take it.
 __device__ __noinline__ float divide(float a, float b) { return a / b; }
 
-// Sum or maximum over the `lanes` (a power of two) neighbouring lanes of each group.
-template <bool kMax>
-__device__ __forceinline__ float lanes_reduce(float x, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) {
+constexpr int kResident = 3;  // CTAs of up to 512 threads per SM (40 registers; two at 64 were slower throughout)
+
+// Sum or maximum over each group of kLanes neighbouring lanes.
+template <bool kMax, int kLanes>
+__device__ __forceinline__ float lanes_reduce(float x) {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
         const float y = __shfl_xor_sync(0xffffffffu, x, o);
         x = kMax ? fmaxf(x, y) : x + y;
     }
     return x;
 }
-
-// The same over the row's T threads (T <= 32: part of a warp; else the whole CTA).
+// The same over T lanes (a power of two up to 32).  0 is neutral: the maxima are of |y|.
 template <bool kMax>
+__device__ __forceinline__ float part_reduce(float x, int T) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        float y = __shfl_xor_sync(0xffffffffu, x, o);
+        y = o < T ? y : 0.f;
+        x = kMax ? fmaxf(x, y) : x + y;
+    }
+    return x;
+}
+// Over a row's T threads: part of a warp, or (kCtaRow) the whole CTA.
+template <bool kMax, bool kCtaRow>
 __device__ __forceinline__ float row_reduce(float x, int T, float* scratch) {
-    if (T <= 32) return lanes_reduce<kMax>(x, T);
-    x = lanes_reduce<kMax>(x, 32);
+    if constexpr (!kCtaRow) return part_reduce<kMax>(x, T);
+    x = lanes_reduce<kMax, 32>(x);
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
     __syncthreads();
     const int lane = threadIdx.x & 31;
-    return lanes_reduce<kMax>(lane < (T >> 5) ? scratch[lane] : 0.f, 32);  // sums and |y| maxima: 0 is neutral
+    return lanes_reduce<kMax, 32>(lane < (T >> 5) ? scratch[lane] : 0.f);
 }
 
-// kNV vectors per thread.  kWide: every row of every array starts on a 16-byte
-// boundary (codes: 8-byte) and d is a multiple of 8.
-template <int kNV, bool kWide>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const RmsNormParams p) {
-    __shared__ float scratch[2][32];
-    const int T = p.row_threads;
-    const int t = T <= 32 ? int(threadIdx.x) & (T - 1) : int(threadIdx.x);
-    const int64_t row = T <= 32 ? int64_t(blockIdx.x) * (kCta / T) + int(threadIdx.x) / T : int64_t(blockIdx.x);
-    const bool live = row < p.rows;  // every thread takes part in the shuffles
-    const int nvec = (p.d + kVec - 1) / kVec;
-    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(p.x) + row * p.x_stride;
-    const __nv_bfloat16* res = reinterpret_cast<const __nv_bfloat16*>(p.residual) + row * p.d;
-
-    float h[kNV][kVec];
-    pdl_wait_prior_grid();
+// The 8-bit output of a row: one scale per group of kGroupLanes lanes (4 or 8), or (32) per row.
+template <int kNV, bool kCtaRow, int kGroupLanes, typename Io>
+__device__ __forceinline__ void quantise(const RmsNormParams& p, const Io& io, float2 (&h)[kNV][kPairs], int64_t row,
+                                         float* scratch) {
+    float amax[kNV];
 #pragma unroll
-    for (int j = 0; j < kNV; ++j) {
-        const int v = j * T + t;
-        if (live && v < nvec) {
-            load8<kWide>(h[j], x + v * kVec, p.d - v * kVec);
-        } else {
+    for (int j = 0; j < kNV; ++j) {  // units past the row hold zeros
+        float a = 0.f, b = 0.f;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) h[j][i] = 0.f;
-        }
+        for (int i = 0; i < kPairs; i += 2) a = max_abs3(a, h[j][i]), b = max_abs3(b, h[j][i + 1]);
+        amax[j] = fmaxf(a, b);
     }
-    if (p.residual) {
+    if constexpr (kGroupLanes == 32) {
+#pragma unroll
+        for (int j = 1; j < kNV; ++j) amax[0] = fmaxf(amax[0], amax[j]);
+        amax[0] = row_reduce<true, kCtaRow>(amax[0], io.T, scratch);
+#pragma unroll
+        for (int j = 1; j < kNV; ++j) amax[j] = amax[0];
+    } else {
 #pragma unroll
         for (int j = 0; j < kNV; ++j) {
-            const int v = j * T + t;
-            if (live && v < nvec) {
-                float r[kVec];
-                load8<kWide>(r, res + v * kVec, p.d - v * kVec);
+            if constexpr (kCtaRow)
+                amax[j] = lanes_reduce<true, kGroupLanes>(amax[j]);
+            else  // a row shorter than a group lies in its T lanes
+                amax[j] = part_reduce<true>(amax[j], min(io.T, kGroupLanes));
+        }
+    }
+    const int nscale = kGroupLanes == 32 ? 1 : (p.d + kGroupLanes * kUnit - 1) / (kGroupLanes * kUnit);
+    uint32_t pk[kNV][4];
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) h[j][i] += r[i];
-            }
+    for (int j = 0; j < kNV; ++j) {
+        float scale = amax[j] * (1.f / kE4m3Max);
+        if (!(scale > 0.f)) scale = 1.f;  // an all-zero group (or one below fp32's range): codes 0
+        if (amax[j] > 1e-30f && amax[j] < 1e30f) {
+            const float inv = __fdividef(kE4m3Max, amax[j]);
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) h[j][i] = mul_f32x2(h[j][i], make_float2(inv, inv));
+        } else {  // 448 / amax or its approximation would leave fp32's range
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i)
+                h[j][i] = make_float2(divide(h[j][i].x, scale), divide(h[j][i].y, scale));
+        }
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const uint32_t e = __nv_cvt_float2_to_fp8x2(h[j][i], __NV_SATFINITE, __NV_E4M3);
+            pk[j][i >> 1] = (i & 1) ? pk[j][i >> 1] | (e << 16) : e;
+        }
+        const int v = io.unit(j);
+        const bool first = kGroupLanes == 32 ? v == 0 : (v & (kGroupLanes - 1)) == 0;
+        if (v < io.units && first) p.scales[row * nscale + (kGroupLanes == 32 ? 0 : v / kGroupLanes)] = scale;
+    }
+    io.store_codes(p.codes + row * p.d, pk);
+}
+
+// kNV units per thread; kCtaRow: one row per CTA, else rows of T <= 32 threads.  kGroupLanes: lanes of a
+// quantisation group (4 or 8), 32 for one scale per row, 0 without 8-bit output.
+template <int kNV, bool kCtaRow, int kGroupLanes, int kAlign, int kMaxT>
+__global__ void __launch_bounds__(kMaxT, kMaxT == 512 ? kResident : 1) rmsnorm_kernel(const RmsNormParams p) {
+    __shared__ float scratch[2][32];
+    const int T = p.row_threads;
+    const int t = kCtaRow ? int(threadIdx.x) : int(threadIdx.x) & (T - 1);
+    const int64_t row =
+        kCtaRow ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * (kCta >> p.log2_threads) + (threadIdx.x >> p.log2_threads);
+    const bool live = kCtaRow || row < p.rows;  // every thread takes part in the shuffles
+    extern __shared__ uint4 stage_raw[];
+    uint16_t* const stage = reinterpret_cast<uint16_t*>(stage_raw) + (int(threadIdx.x) - t) * kNV * kUnit;
+    const RowIo<kNV, kCtaRow, kAlign> io{T, t, p.d, live ? (p.d + kUnit - 1) / kUnit : 0, stage};
+    const int64_t at = row * p.d;
+
+    float2 h[kNV][kPairs];
+    pdl_wait_prior_grid();
+    // The row that takes this CTA's place is fetched into L2 now: what is in flight no longer ends with
+    // the resident CTAs' registers.
+    if (kCtaRow && kAlign >= 16 && threadIdx.x == 0 && row + p.ahead < p.rows) {
+        const uint32_t bytes = uint32_t(p.d) * 2u;
+        l2_prefetch(static_cast<const uint16_t*>(p.x) + (row + p.ahead) * p.x_stride, bytes);
+        if (p.residual) l2_prefetch(static_cast<const uint16_t*>(p.residual) + (row + p.ahead) * p.d, bytes);
+    }
+    {
+        float2 r[kNV][kPairs];
+        io.load(h, static_cast<const uint16_t*>(p.x) + row * p.x_stride);
+        if (p.residual) {
+            io.load(r, static_cast<const uint16_t*>(p.residual) + at);
+#pragma unroll
+            for (int j = 0; j < kNV; ++j)
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) h[j][i] = add_f32x2(h[j][i], r[j][i]);
         }
     }
     pdl_allow_next_grid();
 
-    float sq = 0.f;
+    float2 sq2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < kNV; ++j)
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) sq = fmaf(h[j][i], h[j][i], sq);
-    sq = row_reduce<false>(sq, T, scratch[0]);
+        for (int i = 0; i < kPairs; ++i) sq2 = fma_f32x2(h[j][i], h[j][i], sq2);
+    const float sq = row_reduce<false, kCtaRow>(sq2.x + sq2.y, T, scratch[0]);
     const float rstd = rsqrtf(sq / float(p.d) + p.eps);
+    const float2 rstd2 = make_float2(rstd, rstd);
 
-    float row_max = 0.f;
-#pragma unroll
-    for (int j = 0; j < kNV; ++j) {
-        const int v = j * T + t;
-        if (!live || v >= nvec) continue;
-        const int n = p.d - v * kVec;
-        if (p.residual_out) store8<kWide>(reinterpret_cast<__nv_bfloat16*>(p.residual_out) + row * p.d + v * kVec, h[j], n);
-        float g[kVec];
-        if (p.weight_fp32) {
-            const float* w = static_cast<const float*>(p.weight) + v * kVec;
-            if constexpr (kWide) {
-                const float4 a = __ldg(reinterpret_cast<const float4*>(w)), b = __ldg(reinterpret_cast<const float4*>(w) + 1);
-                g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w, g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) g[i] = i < n ? w[i] : 0.f;
-            }
-        } else {
-            load8<kWide>(g, static_cast<const __nv_bfloat16*>(p.weight) + v * kVec, n);
-        }
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) h[j][i] = h[j][i] * rstd * g[i];
-        if (p.out) store8<kWide>(reinterpret_cast<__nv_bfloat16*>(p.out) + row * p.d + v * kVec, h[j], n);
-    }
-    if (!p.codes) return;
-
-    // 8-bit output: one scale per group of 64 or 128 elements (8 or 16 lanes) or per row.
-    if (p.group == 0) {
+    if (p.residual_out) io.store(static_cast<uint16_t*>(p.residual_out) + at, h);
+    {
+        float2 g[kNV][kPairs];
+        if (p.weight_fp32)
+            io.load_weight_fp32(g, static_cast<const float*>(p.weight));
+        else
+            io.load(g, static_cast<const uint16_t*>(p.weight));
 #pragma unroll
         for (int j = 0; j < kNV; ++j)
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) row_max = fmaxf(row_max, fabsf(h[j][i]));
-        row_max = row_reduce<true>(row_max, T, scratch[1]);
+            for (int i = 0; i < kPairs; ++i) h[j][i] = mul_f32x2(mul_f32x2(h[j][i], rstd2), g[j][i]);
     }
-    const int glanes = min(p.group / kVec, T);  // a row shorter than a group lies in its T lanes
-    const int nscale = p.group ? (p.d + p.group - 1) / p.group : 1;
-#pragma unroll
-    for (int j = 0; j < kNV; ++j) {
-        const int v = j * T + t;
-        float amax = row_max;
-        if (p.group) {
-            amax = 0.f;  // vectors past the row hold zeros
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) amax = fmaxf(amax, fabsf(h[j][i]));
-            amax = lanes_reduce<true>(amax, glanes);
+    if (p.out) io.store(static_cast<uint16_t*>(p.out) + at, h);
+    if constexpr (kGroupLanes > 0) {
+        quantise<kNV, kCtaRow, kGroupLanes>(p, io, h, row, scratch[1]);
+    }
+}
+template <int kNV, bool kCtaRow, int kGroupLanes, int kMaxT>
+cudaError_t launch_aligned(const RmsNormParams& p, int align, cudaLaunchConfig_t cfg) {
+    if (align == 2) {  // the rows' staging; above 48 KB the limit is raised once
+        cfg.dynamicSmemBytes = size_t(cfg.blockDim.x) * kNV * kUnit * sizeof(uint16_t);
+        if (kNV > 1 && cfg.dynamicSmemBytes > 48 * 1024) {
+            static SmemLimitOnce limit;
+            int dev = 0;
+            cudaError_t e = cudaGetDevice(&dev);
+            if (e == cudaSuccess) e = limit.apply(dev, rmsnorm_kernel<kNV, kCtaRow, kGroupLanes, 2, kMaxT>, 65536);
+            if (e != cudaSuccess) return e;
         }
-        if (!live || v >= nvec) continue;
-        float scale = amax * (1.f / kE4m3Max);
-        if (!(scale > 0.f)) scale = 1.f;  // an all-zero group (or one below fp32's range): codes 0
-        uint8_t* codes = p.codes + row * p.d + v * kVec;
-        float c[kVec];
-        if (amax > 1e-30f && amax < 1e30f) {
-            const float inv = __fdividef(kE4m3Max, amax);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) c[i] = h[j][i] * inv;
-        } else {  // 448 / amax or its approximation would leave fp32's range
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) c[i] = divide(h[j][i], scale);
-        }
-        uint32_t pk[2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t e = __nv_cvt_float2_to_fp8x2(make_float2(c[2 * i], c[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-            pk[i >> 1] = (i & 1) ? pk[i >> 1] | (e << 16) : e;
-        }
-        if constexpr (kWide) {
-            *reinterpret_cast<uint2*>(codes) = make_uint2(pk[0], pk[1]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kVec; ++i)
-                if (v * kVec + i < p.d) codes[i] = uint8_t(pk[i >> 2] >> (8 * (i & 3)));
-        }
-        const bool first = p.group ? (v * kVec) % p.group == 0 : v == 0;
-        if (first) p.scales[row * nscale + (p.group ? (v * kVec) / p.group : 0)] = scale;
+    }
+    switch (align) {
+        case 32: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<kNV, kCtaRow, kGroupLanes, 32, kMaxT>, p);
+        case 16: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<kNV, kCtaRow, kGroupLanes, 16, kMaxT>, p);
+        default: return cudaLaunchKernelEx(&cfg, rmsnorm_kernel<kNV, kCtaRow, kGroupLanes, 2, kMaxT>, p);
     }
 }
 
-template <int kNV>
-cudaError_t launch_nv(const RmsNormParams& p, bool wide, unsigned grid, unsigned threads, cudaStream_t stream) {
+template <int kNV, bool kCtaRow, int kMaxT>
+cudaError_t launch_nv(const RmsNormParams& p, int align, unsigned grid, unsigned threads, cudaStream_t stream) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -220,38 +374,34 @@ cudaError_t launch_nv(const RmsNormParams& p, bool wide, unsigned grid, unsigned
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return wide ? cudaLaunchKernelEx(&cfg, rmsnorm_kernel<kNV, true>, p)
-                : cudaLaunchKernelEx(&cfg, rmsnorm_kernel<kNV, false>, p);
+    if (!p.codes) return launch_aligned<kNV, kCtaRow, 0, kMaxT>(p, align, cfg);
+    switch (p.group) {
+        case 64: return launch_aligned<kNV, kCtaRow, 64 / kUnit, kMaxT>(p, align, cfg);
+        case 128: return launch_aligned<kNV, kCtaRow, 128 / kUnit, kMaxT>(p, align, cfg);
+        default: return launch_aligned<kNV, kCtaRow, 32, kMaxT>(p, align, cfg);
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_rmsnorm(RmsNormParams p, bool wide, int sms, cudaStream_t stream) {
-    const int nvec = (p.d + kVec - 1) / kVec;
-    int nv;
-    if (nvec <= 32) {  // a row in part of a warp
-        nv = 1;
-        p.row_threads = 1;
-        while (p.row_threads < nvec) p.row_threads *= 2;
-    } else if (nvec <= 128) {  // one warp per row
-        p.row_threads = 32;
-        nv = nvec <= 64 ? 2 : 4;
-    } else {
-        // One CTA per row.  Few rows: as many threads as vectors (one load each, shortest chain);
-        // many rows: four vectors per thread (smaller CTAs, more of them resident).
-        const int least = p.rows > 4 * int64_t(sms) ? 4 : 1;
-        nv = least;
-        while ((nvec + nv - 1) / nv > 1024) nv *= 2;
-        p.row_threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+cudaError_t launch_rmsnorm(RmsNormParams p, int align, int sms, cudaStream_t stream) {
+    const int units = (p.d + kUnit - 1) / kUnit;
+    if (units <= 64) {  // at most one warp per row, two units a thread above 32
+        int T = align == 16 ? 2 : 1;  // 16-byte halves are shared by pairs of threads
+        while (T < units && T < 32) T *= 2;
+        p.row_threads = T;
+        p.log2_threads = 31 - __builtin_clz(unsigned(T));
+        const unsigned grid = unsigned((p.rows + kCta / T - 1) / (kCta / T));
+        return units <= 32 ? launch_nv<1, false, kCta>(p, align, grid, kCta, stream)
+                           : launch_nv<2, false, kCta>(p, align, grid, kCta, stream);
     }
-    const int T = p.row_threads;
-    const int64_t grid = T <= 32 ? (p.rows + kCta / T - 1) / (kCta / T) : p.rows;
-    const unsigned threads = T <= 32 ? kCta : T;
-    switch (nv) {
-        case 1: return launch_nv<1>(p, wide, unsigned(grid), threads, stream);
-        case 2: return launch_nv<2>(p, wide, unsigned(grid), threads, stream);
-        default: return launch_nv<4>(p, wide, unsigned(grid), threads, stream);
-    }
+    const int nv = units <= 1024 ? 1 : 2;  // one CTA per row
+    const unsigned T = unsigned((units + nv - 1) / nv + 31) / 32 * 32, grid = unsigned(p.rows);
+    p.row_threads = int(T);
+    p.ahead = sms * (T <= 512 ? kResident : 1);  // the CTAs resident at a time
+    if (nv == 2) return launch_nv<2, true, 1024>(p, align, grid, T, stream);
+    return T <= 512 ? launch_nv<1, true, 512>(p, align, grid, T, stream)
+                    : launch_nv<1, true, 1024>(p, align, grid, T, stream);
 }
 
 }  // namespace dsa
