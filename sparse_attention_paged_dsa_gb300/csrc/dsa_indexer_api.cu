@@ -825,6 +825,7 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
     p.heads = heads;
     p.entry_tokens = entry_tokens;
     p.slots = int32_t(slots);
+    p.out_aligned32 = aligned(out, 32) ? 1 : 0;
     // A scale of 0 becomes one whose products vanish next to 1: hidden scores stay -inf times it.
     p.sm_scale_log2 = std::fmax(sm_scale * 1.4426950408889634f, 1e-30f);
     const cudaError_t e = dsa::launch_mla_prefill(q_map, kn_map, kr_map, v_map, p, static_cast<cudaStream_t>(stream));

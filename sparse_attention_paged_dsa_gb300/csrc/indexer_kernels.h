@@ -185,6 +185,7 @@ struct PrefillParams {
     int32_t heads;
     int32_t entry_tokens;      // tokens per entry
     int32_t slots;             // q_rows / 512 + batch blocks of up to 512 rows
+    int32_t out_aligned32;     // out starts on a 32-byte boundary
     float sm_scale_log2;       // sm_scale * log2(e), above 0
 };
 // Maps of 128-byte-swizzled boxes of 64 dims x 128 rows (q, v) or 64 rows (k_nope, k_rope): q, k_nope and v

@@ -73,7 +73,7 @@ struct __align__(8) PrefillCtl {
     uint64_t tail_landed, tail_ready, all_done;
     uint32_t tmem_base;
     int abort;
-    int req;
+    int req, block;  // this slot's request (-1: none) and block of rows
 };
 constexpr int kSmemP = 1024 + kOffCtlP + int(sizeof(PrefillCtl));
 static_assert(kSmemP <= 232448, "fits one CTA per SM");
@@ -238,45 +238,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     const unsigned unit = blockIdx.x >> 1;
     const int head = int(unit % unsigned(p.heads));
     const int slot_t = p.slots - 1 - int(unit / unsigned(p.heads));
-    if (threadIdx.x == 0) ctl.req = -1;
-    __syncthreads();
-    pdl_wait_prior_grid();
-    pdl_allow_next_grid();
-
-    // Request b owns the slots [cu_q[b] / 512 + b, cu_q[b + 1] / 512 + b + 1): at least as many as it
-    // has blocks of 512 rows, so the launch depends on the row count and the batch alone.
-    uint32_t bad = 0;
-    for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
-        const int64_t s0 = int64_t(__ldg(p.cu_q + b)) / kPrefillBlock + b;
-        const int64_t s1 = int64_t(__ldg(p.cu_q + b + 1)) / kPrefillBlock + b + 1;
-        if (slot_t >= s0 && slot_t < s1) ctl.req = b;
-        if (blockIdx.x == 0) Request(p, b, bad);  // every request is checked, also those without rows
-    }
-    if (bad) atomicOr(p.err, bad);
-    __syncthreads();
-    const int b = ctl.req;
-    if (b < 0) return;  // both CTAs alike, before any cluster barrier
-    const Request rq(p, b, bad);
-    const int64_t block = slot_t - (int64_t(__ldg(p.cu_q + b)) / kPrefillBlock + b);
-    if (block < 0 || block * kPrefillBlock >= rq.rows) return;
-    // Query tile i: rows [row0 + 256 i, + 256) of the request, the second 128 of them in CTA 1.
-    const int row0 = int(block) * kPrefillBlock;
-    int limit[2], ntiles[2];  // entries that the tile's last row sees
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int last = min(rq.rows, row0 + (i + 1) * 2 * kTile) - 1;
-        limit[i] = last >= row0 + i * 2 * kTile ? rq.seen(last, p.entry_tokens) : 0;
-        ntiles[i] = (limit[i] + kTile - 1) / kTile;
-    }
-    const int nt = max(ntiles[0], ntiles[1]);
-    const int limit_max = max(limit[0], limit[1]);
-    // Value rows behind the last entry that any of these rows sees belong to other requests or hold
-    // nothing.  Products stop at a 16-entry step, and where that is not the end of the entries the rows
-    // up to it are zeroed (weights there are 0, but 0 x NaN is not): the last tile's values count on a
-    // barrier of each CTA, whose warp 10 zeroes them and tells the leader.
-    const bool tail = (limit_max & 15) != 0;
-
     if (threadIdx.x == 0) {
+        ctl.req = -1;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&ctl.k_full[i], 1);
             mbar_init(&ctl.k_empty[i], 1);
@@ -294,12 +257,60 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         mbar_init(&ctl.all_done, 1);
         ctl.abort = 0;
         fence_mbar_init();
+        tma_prefetch_map(&q_map);
+        tma_prefetch_map(&kn_map);
+        tma_prefetch_map(&kr_map);
+        tma_prefetch_map(&v_map);
     }
     if (warp == 8) tmem2_alloc(&ctl.tmem_base, kTmemColsP);
+    __syncwarp();
     tc_fence_before_sync();
-    cluster_sync_all();
+    cluster_arrive();
+    __syncthreads();
+    pdl_wait_prior_grid();
+    pdl_allow_next_grid();
+
+    // Request b owns the slots [cu_q[b] / 512 + b, cu_q[b + 1] / 512 + b + 1): at least as many as it
+    // has blocks of 512 rows, so the launch depends on the row count and the batch alone.
+    uint32_t bad = 0;
+    for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
+        const Request r(p, b, bad);  // loaded by the way, so that the owner's lines are in L1 below
+        const int64_t s0 = int64_t(__ldg(p.cu_q + b)) / kPrefillBlock + b;
+        const int64_t s1 = int64_t(__ldg(p.cu_q + b + 1)) / kPrefillBlock + b + 1;
+        if (slot_t >= s0 && slot_t < s1 && slot_t - s0 < (r.rows + kPrefillBlock - 1) / kPrefillBlock) {
+            ctl.req = b;
+            ctl.block = int(slot_t - s0);
+        }
+    }
+    if (bad && blockIdx.x == 0) atomicOr(p.err, bad);  // every request is checked, also those without rows
+    __syncwarp();
+    cluster_wait();  // the other CTA's barriers are set up too
+    __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = ctl.tmem_base;
+    const int b = ctl.req;
+    if (b < 0) {  // a slot without rows; both CTAs alike
+        cluster_sync_all();
+        if (warp == 8) tmem2_dealloc(tmem_base, kTmemColsP);
+        return;
+    }
+    const Request rq(p, b, bad);
+    // Query tile i: rows [row0 + 256 i, + 256) of the request, the second 128 of them in CTA 1.
+    const int row0 = ctl.block * kPrefillBlock;
+    int limit[2], ntiles[2];  // entries that the tile's last row sees
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int last = min(rq.rows, row0 + (i + 1) * 2 * kTile) - 1;
+        limit[i] = last >= row0 + i * 2 * kTile ? rq.seen(last, p.entry_tokens) : 0;
+        ntiles[i] = (limit[i] + kTile - 1) / kTile;
+    }
+    const int nt = max(ntiles[0], ntiles[1]);
+    const int limit_max = max(limit[0], limit[1]);
+    // Value rows behind the last entry that any of these rows sees belong to other requests or hold
+    // nothing.  Products stop at a 16-entry step, and where that is not the end of the entries the rows
+    // up to it are zeroed (weights there are 0, but 0 x NaN is not): the last tile's values count on a
+    // barrier of each CTA, whose warp 10 zeroes them and tells the leader.
+    const bool tail = (limit_max & 15) != 0;
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 9) {
@@ -608,15 +619,21 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                 }
                 if (live_row) {
 #pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        uint32_t u[4];
+                    for (int q4 = 0; q4 < 2; ++q4) {  // a whole sector a lane
+                        uint32_t u[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[8 * q4 + 2 * k]) * inv,
-                                                                           __uint_as_float(o[8 * q4 + 2 * k + 1]) * inv);
+                        for (int k = 0; k < 8; ++k) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[16 * q4 + 2 * k]) * inv,
+                                                                           __uint_as_float(o[16 * q4 + 2 * k + 1]) * inv);
                             u[k] = *reinterpret_cast<const uint32_t*>(&v);
                         }
-                        *reinterpret_cast<uint4*>(o_row + 32 * c + 8 * q4) = make_uint4(u[0], u[1], u[2], u[3]);
+                        if (p.out_aligned32) {
+                            st_global_v8(o_row + 32 * c + 16 * q4, u);
+                        } else {
+                            uint4* d = reinterpret_cast<uint4*>(o_row + 32 * c + 16 * q4);
+                            d[0] = make_uint4(u[0], u[1], u[2], u[3]);
+                            d[1] = make_uint4(u[4], u[5], u[6], u[7]);
+                        }
                     }
                 }
             }

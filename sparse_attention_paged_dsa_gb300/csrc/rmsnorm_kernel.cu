@@ -44,17 +44,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float2 v) {
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-__device__ __forceinline__ void load_v8(uint32_t (&u)[kPairs], const void* p) {
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
-                 : "l"(p));
-}
-__device__ __forceinline__ void store_v8(void* p, const uint32_t (&u)[kPairs]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]),
-                 "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
-                 : "memory");
-}
-
 // A row's rows of the arrays, moved by its T threads.  kAlign: the boundary, in bytes, that every unit of
 // every array starts on.  32: one access a unit; 16: two (d a multiple of 8).  2: the row passes through
 // shared memory, so that global accesses are of neighbouring elements (unit by unit, 32 lanes touch
@@ -95,7 +84,7 @@ struct RowIo {
                 const uint4 a = q[0], b = q[1];
                 u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w, u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
             } else if constexpr (kAlign == 32) {
-                if (unit(j) < units) load_v8(u, p + unit(j) * kUnit);
+                if (unit(j) < units) ld_global_v8(u, p + unit(j) * kUnit);
             } else {
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
@@ -116,7 +105,7 @@ struct RowIo {
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) u[i] = pack_bf16(v[j][i]);
             if constexpr (kAlign == 32) {
-                if (unit(j) < units) store_v8(p + unit(j) * kUnit, u);
+                if (unit(j) < units) st_global_v8(p + unit(j) * kUnit, u);
             } else {
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
