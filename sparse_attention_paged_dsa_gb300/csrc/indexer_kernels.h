@@ -184,7 +184,7 @@ struct PrefillParams {
     int32_t batch;
     int32_t heads;
     int32_t entry_tokens;      // tokens per entry
-    int32_t slots;             // q_rows / 512 + batch blocks of up to 512 rows
+    int32_t slots;             // q_rows / 512 + batch: at least the blocks of up to 512 rows
     int32_t out_aligned32;     // out starts on a 32-byte boundary
     float sm_scale_log2;       // sm_scale * log2(e), above 0
 };

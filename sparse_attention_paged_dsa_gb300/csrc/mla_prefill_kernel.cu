@@ -7,25 +7,34 @@
 // Row i of a request with n rows and seq_len tokens sees its first
 // ceil((seq_len - (n - 1 - i)) / entry_tokens) entries.
 //
-// A cluster of two CTAs takes 512 rows of a request and one head: two query tiles
-// of 256 rows, each CTA holding 128 rows of both.  All MMAs are cta_group::2
-// (M = 256: 128 rows in each CTA's TMEM; N = 128), issued by the leader.  Their
-// second operand is split between the two CTAs' shared memory: each loads half of
-// every 128-entry tile's keys (64 entries) and half of its values (64 dims), so a
-// tile costs an SM 40 KB of loads instead of 80, its shared memory holds three
-// tiles, and the operand reads fit its bandwidth.  Roles of a CTA (384 threads):
+// A cluster of two CTAs works on two query tiles of 256 rows at a time, each CTA
+// holding 128 rows of both.  All MMAs are cta_group::2 (M = 256: 128 rows in each
+// CTA's TMEM; N = 128), issued by the leader.  Their second operand is split between
+// the two CTAs' shared memory: each loads half of every 128-entry tile's keys (64
+// entries) and half of its values (64 dims), so a tile costs an SM 40 KB of loads
+// instead of 80, its shared memory holds three tiles, and the operand reads fit its
+// bandwidth.
+//
+// Work.  A unit is 512 rows of a request and one head, whose two tiles share the
+// keys and values; or, where a request has at most 256 rows left, those rows and two
+// heads, one a tile.  Clusters are persistent: the units, longest requests and their
+// last rows first, are dealt out back and forth over the clusters that fit the
+// device, and the next unit's loads and first product run under the end of the one
+// before (a unit's own set-up and tail cost 9 us without that).  A scheduler warp
+// looks the units up.  Roles of a CTA (384 threads):
 //   * warps 0-3 and 4-7: softmax of query tile 0 and 1, one row per thread: the
 //     row of S from TMEM to registers, its maximum (raised only when a tile
-//     passes it by more than 2^8; the accumulator is then rescaled in TMEM),
-//     2^x, and P (bf16) back into S's columns.
+//     passes it by more than 2^20; the accumulator is then rescaled in TMEM),
+//     2^x, and P (bf16) back into S's columns; at the end the output.
 //   * warp 8 (leader): tcgen05.mma.  S = Q . K^T from shared memory (12 steps);
 //     O += P . V with P from TMEM and V read in place as an MN-major operand (up to
 //     8 steps).  Order per tile: PV of query tile 0, its next QK, PV of query tile
 //     1, its next QK, so that one tile's products run while the other's softmax does.
-//   * warp 9: TMA.  q once; keys (two 64-dim slabs of the head's own, one shared
+//   * warp 9: TMA.  q; keys (two 64-dim slabs of the head's own, one shared
 //     by all heads) and values, three stages each.  Both CTAs' copies count on the
 //     leader's barriers.
-//   * warp 10: zeroes the value rows behind the last entry (see below).
+//   * warp 10: zeroes the value rows behind the last entry (see Unit::tail).
+//   * warp 11: the scheduler.
 // TMEM: S/P of the two tiles 2 x 128 columns, O 2 x 128: all 512.
 //
 // The shared 64 rotary key dims are loaded from their one copy per entry, so no
@@ -39,6 +48,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "indexer_kernels.h"
@@ -64,16 +74,53 @@ constexpr int kRegsSoftmax = 200, kRegsOther = 104;  // 8 x 200 + 4 x 104 = 12 x
 constexpr uint32_t kTmemColsP = 512;
 constexpr uint32_t kColSP = 0;    // S / P of tile i at 128 i
 constexpr uint32_t kColOP = 256;  // O of tile i at 256 + 128 i
-constexpr float kRaiseLog2 = 8.0f;
+constexpr float kRaiseLog2 = 20.0f;  // rounding is relative: weights may pass 1 by this much
 constexpr float kLn2P = 0.69314718055994531f;
+
+constexpr int kSortMost = 256;       // requests that are ordered by length (more: as they come)
+constexpr int kInfoSlots = 2;
+constexpr int kInfoReaders = 11;     // every warp but the scheduler
+
+// What a cluster works on: two query tiles, or fewer.  Tile i is rows [i step_row, + 256) of the block
+// (those of them below `rows`) of head `head` + i step_head.
+struct Unit {
+    int q_row;               // row of q where the block starts
+    int row0;                // the same within the request
+    int rows;                // of the block
+    int req_rows, seq, live; // of the request: rows, tokens, entries
+    int kv0;                 // its first entry
+    int head;
+    int step_row, step_head; // (256, 0): the tiles share keys and values; (0, 1)
+    int limit[2];            // entries that the tile's last row sees; 0 without a tile
+    int last;                // no unit: the list is at its end
+
+    __device__ __forceinline__ bool shared() const { return step_head == 0; }
+    __device__ __forceinline__ int tiles(int i) const { return (limit[i] + kTile - 1) / kTile; }
+    // Streams of keys and values, and tiles in each.
+    __device__ __forceinline__ int streams() const { return shared() || limit[1] == 0 ? 1 : 2; }
+    __device__ __forceinline__ int nt() const { return max(tiles(0), tiles(1)); }
+    __device__ __forceinline__ int limit_max() const { return max(limit[0], limit[1]); }
+    // Value rows behind the last entry that any of these rows sees belong to other requests or hold
+    // nothing.  Products stop at a 16-entry step, and where that is not the end of the entries the rows
+    // up to it are zeroed (weights there are 0, but 0 x NaN is not): such a last tile's values count on
+    // a barrier of each CTA, whose warp 10 zeroes them and tells the leader.
+    __device__ __forceinline__ bool tail() const { return (limit_max() & 15) != 0; }
+};
 
 struct __align__(8) PrefillCtl {
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-    uint64_t tail_landed, tail_ready, all_done;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
+    uint64_t tail_landed[2], tail_ready[2];
+    uint64_t info_full[kInfoSlots], info_empty[kInfoSlots];
+    uint64_t all_done;
     uint32_t tmem_base;
     int abort;
-    int req, block;  // this slot's request (-1: none) and block of rows
+    int total;                         // units
+    int warp_units[kThreadsP / 32];
+    Unit info[kInfoSlots];
+    int first[kMaxBatch];              // first unit of the i-th request in the order
+    int16_t order[kMaxBatch];          // that request
+    int key[kSortMost];
 };
 constexpr int kSmemP = 1024 + kOffCtlP + int(sizeof(PrefillCtl));
 static_assert(kSmemP <= 232448, "fits one CTA per SM");
@@ -221,6 +268,14 @@ __device__ __forceinline__ void wait_landed_p(uint64_t* bar, uint32_t parity) {
     }
 }
 
+// Units of a request with n rows: blocks of 512 rows, one per head, and, where at most 256 rows are
+// left, one per two heads for those.
+__device__ __forceinline__ bool short_end(int n) { return n % kPrefillBlock > 0 && n % kPrefillBlock <= 2 * kTile; }
+__device__ __forceinline__ int long_blocks(int n) { return (n + 2 * kTile - 1) / kPrefillBlock; }
+__device__ __forceinline__ int units_of_rows(int n, int heads) {
+    return long_blocks(n) * heads + (short_end(n) ? (heads + 1) / 2 : 0);
+}
+
 __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kn_map,
                        const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap v_map,
@@ -234,12 +289,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     const int lane = threadIdx.x & 31;
     const int rank = int(cluster_rank());  // 0: the leader
 
-    // Heads vary fastest, and the last (longest) row blocks come first.
-    const unsigned unit = blockIdx.x >> 1;
-    const int head = int(unit % unsigned(p.heads));
-    const int slot_t = p.slots - 1 - int(unit / unsigned(p.heads));
     if (threadIdx.x == 0) {
-        ctl.req = -1;
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&ctl.k_full[i], 1);
             mbar_init(&ctl.k_empty[i], 1);
@@ -248,12 +298,18 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.q_full[i], 1);
+            mbar_init(&ctl.q_empty[i], 1);
             mbar_init(&ctl.s_full[i], 1);
-            mbar_init(&ctl.p_full[i], 8);  // four warps of each CTA
+            mbar_init(&ctl.p_full[i], 8);   // four warps of each CTA
             mbar_init(&ctl.o_full[i], 1);
+            mbar_init(&ctl.o_empty[i], 8);  // the same
+            mbar_init(&ctl.tail_landed[i], 1);
+            mbar_init(&ctl.tail_ready[i], 2);
         }
-        mbar_init(&ctl.tail_landed, 1);
-        mbar_init(&ctl.tail_ready, 2);
+        for (int i = 0; i < kInfoSlots; ++i) {
+            mbar_init(&ctl.info_full[i], 1);
+            mbar_init(&ctl.info_empty[i], kInfoReaders);
+        }
         mbar_init(&ctl.all_done, 1);
         ctl.abort = 0;
         fence_mbar_init();
@@ -266,382 +322,561 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     __syncwarp();
     tc_fence_before_sync();
     cluster_arrive();
-    __syncthreads();
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
 
-    // Request b owns the slots [cu_q[b] / 512 + b, cu_q[b + 1] / 512 + b + 1): at least as many as it
-    // has blocks of 512 rows, so the launch depends on the row count and the batch alone.
+    // The order of the requests (longest first, where they are few) and where their units start.
     uint32_t bad = 0;
-    for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
-        const Request r(p, b, bad);  // loaded by the way, so that the owner's lines are in L1 below
-        const int64_t s0 = int64_t(__ldg(p.cu_q + b)) / kPrefillBlock + b;
-        const int64_t s1 = int64_t(__ldg(p.cu_q + b + 1)) / kPrefillBlock + b + 1;
-        if (slot_t >= s0 && slot_t < s1 && slot_t - s0 < (r.rows + kPrefillBlock - 1) / kPrefillBlock) {
-            ctl.req = b;
-            ctl.block = int(slot_t - s0);
+    const bool sorted = p.batch <= kSortMost;
+    if (sorted) {
+        for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
+            const Request r(p, b, bad);
+            ctl.key[b] = r.rows > 0 ? r.live : -1;
         }
+        __syncthreads();
+        for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
+            const int key = ctl.key[b];
+            int at = 0;
+            for (int o = 0; o < p.batch; ++o) at += ctl.key[o] > key || (ctl.key[o] == key && o < b);
+            ctl.order[at] = int16_t(b);
+        }
+        __syncthreads();
     }
-    if (bad && blockIdx.x == 0) atomicOr(p.err, bad);  // every request is checked, also those without rows
+    const int per = (p.batch + kThreadsP - 1) / kThreadsP;
+    const int i0 = min(int(threadIdx.x) * per, p.batch), i1 = min(i0 + per, p.batch);
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) {
+        const int b = sorted ? int(ctl.order[i]) : i;
+        if (!sorted) ctl.order[i] = int16_t(i);
+        mine += units_of_rows(Request(p, b, bad).rows, p.heads);
+    }
+    if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) ctl.warp_units[warp] = incl;
+    __syncthreads();
+    {
+        int before = incl - mine, total = 0;
+        for (int w = 0; w < kThreadsP / 32; ++w) {
+            if (w < warp) before += ctl.warp_units[w];
+            total += ctl.warp_units[w];
+        }
+        for (int i = i0; i < i1; ++i) {
+            ctl.first[i] = before;
+            uint32_t ignored = 0;
+            before += units_of_rows(Request(p, int(ctl.order[i]), ignored).rows, p.heads);
+        }
+        if (threadIdx.x == 0) ctl.total = total;
+    }
     __syncwarp();
     cluster_wait();  // the other CTA's barriers are set up too
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem_base = ctl.tmem_base;
-    const int b = ctl.req;
-    if (b < 0) {  // a slot without rows; both CTAs alike
-        cluster_sync_all();
-        if (warp == 8) tmem2_dealloc(tmem_base, kTmemColsP);
-        return;
-    }
-    const Request rq(p, b, bad);
-    // Query tile i: rows [row0 + 256 i, + 256) of the request, the second 128 of them in CTA 1.
-    const int row0 = ctl.block * kPrefillBlock;
-    int limit[2], ntiles[2];  // entries that the tile's last row sees
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int last = min(rq.rows, row0 + (i + 1) * 2 * kTile) - 1;
-        limit[i] = last >= row0 + i * 2 * kTile ? rq.seen(last, p.entry_tokens) : 0;
-        ntiles[i] = (limit[i] + kTile - 1) / kTile;
-    }
-    const int nt = max(ntiles[0], ntiles[1]);
-    const int limit_max = max(limit[0], limit[1]);
-    // Value rows behind the last entry that any of these rows sees belong to other requests or hold
-    // nothing.  Products stop at a 16-entry step, and where that is not the end of the entries the rows
-    // up to it are zeroed (weights there are 0, but 0 x NaN is not): the last tile's values count on a
-    // barrier of each CTA, whose warp 10 zeroes them and tells the leader.
-    const bool tail = (limit_max & 15) != 0;
+
+    // A warp's next unit; false at the end of the list or when a role has given up.
+    int taken = 0;
+    const auto next_unit = [&](Unit& u) {
+        const int slot = taken & (kInfoSlots - 1);
+        const bool ok = mbar_wait(&ctl.info_full[slot], uint32_t(taken / kInfoSlots) & 1u, &ctl.abort);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        u = ctl.info[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.info_empty[slot]);
+        ++taken;
+        return u.last == 0;
+    };
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 9) {
-        // ================= TMA =================
-        if (lane == 0 && nt > 0) {
-            const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
-            bool stop = false;
-            const auto load_q = [&](int i) {
-                const uint32_t bar = cluster_addr(&ctl.q_full[i], 0);
-                if (rank == 0) mbar_arrive_expect_tx(&ctl.q_full[i], uint32_t(2 * kQkSlabs * kSlabB));
-                for (int s = 0; s < kQkSlabs; ++s)
-                    tma2_load_3d(s_base + kOffQt + (i * kQkSlabs + s) * kSlabB, &q_map, bar, 64 * s, head,
-                                 rq.q0 + row0 + i * 2 * kTile + rank * kTile, pol_q);
-            };
-            const auto load_k = [&](int j) {  // this CTA's 64 entries of tile j
-                const int st = j % kStages;
-                if (stop || !mbar_wait(&ctl.k_empty[st], uint32_t((j / kStages) & 1) ^ 1u, &ctl.abort)) {
-                    stop = true;
-                    return;
+    if (warp == 11) {
+        // ================= scheduler =================
+        const int clusters = int(gridDim.x >> 1), cluster = int(blockIdx.x >> 1);
+        bool ok = true, more = true;
+        for (int k = 0; ok && more; ++k) {
+            const int slot = k & (kInfoSlots - 1);
+            // dealt back and forth: what is longer in one round meets what is shorter in the next
+            const int64_t n = int64_t(k) * clusters + ((k & 1) ? clusters - 1 - cluster : cluster);
+            more = n < ctl.total;
+            Unit u = {};
+            u.last = more ? 0 : 1;
+            if (more) {
+                int lo = 0;  // the last request (in the order) that starts at or before n: 32-way, twice
+                for (int span = 32; span >= 1; span /= 32) {
+                    const int at = lo + lane * span;
+                    const bool before = at < p.batch && ctl.first[at] <= int(n);
+                    lo += span * (__popc(__ballot_sync(0xffffffffu, before)) - 1);
                 }
-                const uint32_t bar = cluster_addr(&ctl.k_full[st], 0);
-                if (rank == 0) mbar_arrive_expect_tx(&ctl.k_full[st], uint32_t(2 * kStageK));
-                const uint32_t dst = s_base + kOffK + st * kStageK;
-                const int row = rq.kv0 + j * kTile + rank * (kTile / 2);
-                tma2_load_3d(dst, &kn_map, bar, 0, head, row, pol_kv);
-                tma2_load_3d(dst + kHalfB, &kn_map, bar, 64, head, row, pol_kv);
-                tma2_load_2d(dst + 2 * kHalfB, &kr_map, bar, 0, row, pol_kv);
-            };
-            const auto load_v = [&](int j) {  // this CTA's 64 value dims of tile j
-                const int st = j % kStages;
-                if (stop || !mbar_wait(&ctl.v_empty[st], uint32_t((j / kStages) & 1) ^ 1u, &ctl.abort)) {
-                    stop = true;
-                    return;
+                // requests without rows start where the next one does: the last of them is the owner
+                uint32_t ignored = 0;
+                const Request rq(p, int(ctl.order[lo]), ignored);
+                int at = int(n) - ctl.first[lo];
+                const int ends = short_end(rq.rows) ? (p.heads + 1) / 2 : 0;
+                int block;
+                if (at < ends) {
+                    block = long_blocks(rq.rows);
+                    u.head = 2 * at;
+                    u.step_head = 1;
+                } else {
+                    at -= ends;
+                    block = long_blocks(rq.rows) - 1 - at / p.heads;
+                    u.head = at % p.heads;
+                    u.step_row = 2 * kTile;
                 }
-                const bool last = tail && j == nt - 1;
-                const uint32_t bar = last ? cluster_addr(&ctl.tail_landed, uint32_t(rank)) : cluster_addr(&ctl.v_full[st], 0);
-                if (last)
-                    mbar_arrive_expect_tx(&ctl.tail_landed, uint32_t(kStageV));
-                else if (rank == 0)
-                    mbar_arrive_expect_tx(&ctl.v_full[st], uint32_t(2 * kStageV));
-                tma2_load_3d(s_base + kOffV + st * kStageV, &v_map, bar, 64 * rank, head, rq.kv0 + j * kTile, pol_kv);
-            };
-            if (ntiles[0] > 0) load_q(0);
-            load_k(0);
-            if (ntiles[1] > 0) load_q(1);
-            for (int j = 0; j < nt && !stop; ++j) {
-                load_v(j);
-                if (j + 1 < nt) load_k(j + 1);
+                u.row0 = block * kPrefillBlock;
+                u.q_row = rq.q0 + u.row0;
+                u.rows = min(rq.rows - u.row0, kPrefillBlock);
+                u.req_rows = rq.rows, u.seq = rq.seq, u.live = rq.live, u.kv0 = rq.kv0;
+                for (int i = 0; i < 2; ++i) {
+                    const int from = i * u.step_row, to = min(u.rows, from + 2 * kTile);
+                    const bool there = to > from && u.head + i * u.step_head < p.heads;
+                    u.limit[i] = there ? rq.seen(u.row0 + to - 1, p.entry_tokens) : 0;
+                }
             }
-            if (stop) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.info_empty[slot], (uint32_t(k / kInfoSlots) & 1u) ^ 1u,
+                                                   &ctl.abort)) != 0;
+            if (ok && lane == 0) {
+                ctl.info[slot] = u;
+                mbar_arrive(&ctl.info_full[slot]);
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) {
+            atomicOr(p.err, kErrWaitTimeout);
+            ctl.abort = 1;
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ================= TMA =================
+        const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
+        const bool issuer = elect_one();
+        const uint32_t sb = uint32_t(uniform(int(s_base)));
+        bool ok = true;
+        int nk = 0, nv = 0;                       // key and value tiles so far
+        int nq[2] = {0, 0}, ntail[2] = {0, 0};    // q tiles and zeroed ends
+        uint32_t v_tail = 0;                      // value stages whose last fill counts on a tail barrier
+        const auto wait = [&](uint64_t* bar, int fills) {  // the stage's `fills` earlier contents are used
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t(fills) & 1u) ^ 1u, &ctl.abort));
+            return ok;
+        };
+        Unit u;
+        while (ok && next_unit(u)) {
+            const int streams = u.streams(), nt = u.nt();
+            const auto load_q = [&](int i) {
+                if (u.limit[i] == 0 || !wait(&ctl.q_empty[i], nq[i])) return;
+                if (issuer) {
+                    const uint32_t bar = cluster_addr(&ctl.q_full[i], 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&ctl.q_full[i], uint32_t(2 * kQkSlabs * kSlabB));
+#pragma unroll
+                    for (int s = 0; s < kQkSlabs; ++s)
+                        tma2_load_3d(sb + kOffQt + (i * kQkSlabs + s) * kSlabB, &q_map, bar, 64 * s,
+                                     u.head + i * u.step_head, u.q_row + i * u.step_row + rank * kTile, pol_q);
+                }
+                __syncwarp();
+                ++nq[i];
+            };
+            const auto load_k = [&](int l, int j) {  // this CTA's 64 entries of tile j of stream l
+                const int st = nk % kStages;
+                if (!wait(&ctl.k_empty[st], nk / kStages)) return;
+                if (issuer) {
+                    const uint32_t bar = cluster_addr(&ctl.k_full[st], 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&ctl.k_full[st], uint32_t(2 * kStageK));
+                    const uint32_t dst = sb + kOffK + st * kStageK;
+                    const int row = u.kv0 + j * kTile + rank * (kTile / 2), head = u.head + l;
+                    tma2_load_3d(dst, &kn_map, bar, 0, head, row, pol_kv);
+                    tma2_load_3d(dst + kHalfB, &kn_map, bar, 64, head, row, pol_kv);
+                    tma2_load_2d(dst + 2 * kHalfB, &kr_map, bar, 0, row, pol_kv);
+                }
+                __syncwarp();
+                ++nk;
+            };
+            const auto load_v = [&](int l, int j) {  // this CTA's 64 value dims of tile j of stream l
+                const int st = nv % kStages;
+                if (!wait(&ctl.v_empty[st], nv / kStages)) return;
+                const bool end = u.tail() && j == nt - 1;
+                if (issuer) {
+                    const uint32_t bar = end ? cluster_addr(&ctl.tail_landed[l], uint32_t(rank))
+                                             : cluster_addr(&ctl.v_full[st], 0);
+                    if (end) {
+                        mbar_arrive_expect_tx(&ctl.tail_landed[l], uint32_t(kStageV));
+                        if (rank == 0) mbar_arrive(&ctl.v_full[st]);  // the stage's phases go on
+                    } else if (rank == 0) {
+                        mbar_arrive_expect_tx(&ctl.v_full[st], uint32_t(2 * kStageV));
+                    }
+                    tma2_load_3d(sb + kOffV + st * kStageV, &v_map, bar, 64 * rank, u.head + l, u.kv0 + j * kTile,
+                                 pol_kv);
+                }
+                __syncwarp();
+                v_tail = (v_tail & ~(1u << st)) | (uint32_t(end) << st);
+                if (end) ++ntail[l];
+                ++nv;
+            };
+            if (nt > 0) {
+                load_q(0);
+                load_k(0, 0);
+                load_q(1);
+                if (streams == 2) load_k(1, 0);
+                for (int j = 0; j < nt && ok; ++j) {  // in the order of use
+                    for (int l = 0; l < streams; ++l) load_v(l, j);
+                    if (j + 1 < nt)
+                        for (int l = 0; l < streams; ++l) load_k(l, j + 1);
+                }
+            }
+        }
+        if (lane == 0) {
+            if (!ok) {
                 atomicOr(p.err, kErrWaitTimeout);
                 ctl.abort = 1;
             }
             // No copy outlives the cluster (bounded waits; they have landed unless a role gave up).  The
             // leader's barriers count both CTAs' copies, and neither CTA leaves before the other.
             if (rank == 0) {
-                for (int j = max(nt - kStages, 0); j < nt; ++j) {
-                    wait_landed_p(&ctl.k_full[j % kStages], uint32_t(j / kStages) & 1u);
-                    if (!(tail && j == nt - 1)) wait_landed_p(&ctl.v_full[j % kStages], uint32_t(j / kStages) & 1u);
-                }
+                for (int n = max(nk - kStages, 0); n < nk; ++n)
+                    wait_landed_p(&ctl.k_full[n % kStages], uint32_t(n / kStages) & 1u);
+                for (int n = max(nv - kStages, 0); n < nv; ++n)
+                    if (!((v_tail >> (n % kStages)) & 1u))
+                        wait_landed_p(&ctl.v_full[n % kStages], uint32_t(n / kStages) & 1u);
                 for (int i = 0; i < 2; ++i)
-                    if (ntiles[i] > 0) wait_landed_p(&ctl.q_full[i], 0);
+                    if (nq[i] > 0) wait_landed_p(&ctl.q_full[i], uint32_t(nq[i] - 1) & 1u);
             }
-            if (tail) wait_landed_p(&ctl.tail_landed, 0);
+            for (int i = 0; i < 2; ++i)
+                if (ntail[i] > 0) wait_landed_p(&ctl.tail_landed[i], uint32_t(ntail[i] - 1) & 1u);
         }
         __syncwarp();
     } else if (warp == 10) {
-        // ================= the last tile's value rows =================
-        if (tail) {
-            const bool ok = mbar_wait(&ctl.tail_landed, 0, &ctl.abort);
-            if (__all_sync(0xffffffffu, ok)) {
-                const int valid = limit_max - (nt - 1) * kTile;
-                const int fill = 16 - (valid & 15);
-                uint8_t* v = tiles + kOffV + ((nt - 1) % kStages) * kStageV;
+        // ================= the last tiles' value rows =================
+        int nv = 0, ntail[2] = {0, 0};
+        bool ok = true;
+        Unit u;
+        while (ok && next_unit(u)) {
+            const int streams = u.streams(), nt = u.nt();
+            nv += nt * streams;
+            if (!u.tail()) continue;
+            const int valid = u.limit_max() - (nt - 1) * kTile, fill = 16 - (valid & 15);
+            for (int l = 0; l < streams && ok; ++l) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.tail_landed[l], uint32_t(ntail[l]) & 1u, &ctl.abort)) != 0;
+                ++ntail[l];
+                if (!ok) break;
+                uint8_t* v = tiles + kOffV + ((nv - streams + l) % kStages) * kStageV;
                 for (int i = lane; i < fill * 8; i += 32)
                     *reinterpret_cast<uint4*>(v + (valid + (i >> 3)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                 asm volatile("fence.proxy.async;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&ctl.tail_ready, 0));
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&ctl.tail_ready[l], 0));
             }
         }
-    } else if (warp == 8 && rank == 0) {
+        __syncwarp();
+    } else if (warp == 8) {
         // ================= MMA (the leader's) =================
-        // The whole warp runs the loop; one elected lane issues.
+        // The whole warp runs the loop on uniform values; one elected lane issues.
         constexpr uint32_t kIdescQk = idesc_bf16_f32(2 * kTile, kTile);
         constexpr uint32_t kIdescPv = idesc_bf16_f32(2 * kTile, kPrefillDv) | (1u << 16);  // B (V) MN-major
         const uint32_t tmem = uint32_t(uniform(int(tmem_base)));
         const uint32_t sb = uint32_t(uniform(int(s_base)));
-        const int n_all = uniform(nt);
-        const int n_of[2] = {uniform(ntiles[0]), uniform(ntiles[1])};
-        const int lim[2] = {uniform(limit[0]), uniform(limit[1])};
         const uint64_t q_desc = smem_desc_kmajor_sw128(sb + kOffQt);
         const uint64_t k_desc = smem_desc_kmajor_sw128(sb + kOffK);
         const uint64_t v_desc = desc_mn_sw128(sb + kOffV, kSlabB);
         const bool issuer = elect_one();
-        // S(tile i) = Q_i . K^T, keys in stage st
-        const auto qk = [&](int i, int st) {
-            if (issuer) {
-                const uint64_t a = q_desc + uint32_t(i * kQkSlabs * (kSlabB >> 4));
-                const uint64_t bd = k_desc + uint32_t(st * (kStageK >> 4));
-#pragma unroll
-                for (int s = 0; s < kQkSlabs; ++s)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma2_bf16_ss(tmem + kColSP + 128u * i, a + uint32_t(s * (kSlabB >> 4) + 2 * kk),
-                                      bd + uint32_t(s * (kHalfB >> 4) + 2 * kk), kIdescQk, (s | kk) != 0 ? 1u : 0u);
-                umma2_commit(&ctl.s_full[i]);
-            }
-            __syncwarp();
-        };
-        // O(tile i) += P_i . V, values in stage st, over the 16-entry steps below the tile's limit
-        const auto pv = [&](int i, int j, int st) {
-            const int steps = min((lim[i] - j * kTile + 15) >> 4, kTile / 16);
-            if (issuer) {
-                const uint64_t bd = v_desc + uint32_t(st * (kStageV >> 4));
-                const auto step = [&](int kk) {
-                    umma2_bf16_ts(tmem + kColOP + 128u * i, tmem + kColSP + 128u * i + 8u * kk, bd + 128u * kk, kIdescPv,
-                                  (j | kk) != 0 ? 1u : 0u);
-                };
-                if (steps == kTile / 16) {
-#pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk) step(kk);
-                } else {
-#pragma unroll 1
-                    for (int kk = 0; kk < steps; ++kk) step(kk);
-                }
-                if (j + 1 == n_of[i]) umma2_commit(&ctl.o_full[i]);
-            }
-            __syncwarp();
+        bool ok = true;
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, &ctl.abort));
+            return ok;
         };
         const auto commit = [&](uint64_t* bar) {
             if (issuer) umma2_commit(bar);
             __syncwarp();
         };
-        const auto wait = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, &ctl.abort)) != 0;
-        };
-        bool ok = n_all == 0 || wait(&ctl.k_full[0], 0);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (ok && n_of[i] > 0) {
-                ok = wait(&ctl.q_full[i], 0);
-                tc_fence_after_sync();
-                if (ok) qk(i, 0);
+        // Rings of key and value stages, in the order of the loads: a stage and its phase.
+        struct Ring {
+            int st = 0;
+            uint32_t phase = 0;
+            __device__ __forceinline__ void next() {
+                if (++st == kStages) st = 0, phase ^= 1u;
             }
-        }
-        if (ok && n_all > 0) commit(&ctl.k_empty[0]);
-        int st = 0, st_next = 1;          // stages of tiles j and j + 1, and their phases
-        uint32_t phase = 0, phase_next = 0;
+        };
+        Ring kr, vr;
+        uint32_t np[2] = {0, 0}, no[2] = {0, 0}, nq[2] = {0, 0}, ntail[2] = {0, 0};  // phases
+        Unit info;
+        while (ok && next_unit(info)) {
+            if (rank != 0) continue;  // the leader issues for both
+            const int lim[2] = {uniform(info.limit[0]), uniform(info.limit[1])};
+            const int n_of[2] = {(lim[0] + kTile - 1) / kTile, (lim[1] + kTile - 1) / kTile};
+            const int nt = max(n_of[0], n_of[1]);
+            const bool shared = uniform(info.step_head) == 0;
+            const bool tail = (max(lim[0], lim[1]) & 15) != 0;
+            // S(tile i) = Q_i . K^T, keys in stage st
+            const auto qk = [&](int i, int st, bool last) {
+                if (issuer) {
+                    const uint64_t a = q_desc + uint32_t(i * kQkSlabs * (kSlabB >> 4));
+                    const uint64_t bd = k_desc + uint32_t(st * (kStageK >> 4));
+#pragma unroll
+                    for (int s = 0; s < kQkSlabs; ++s)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma2_bf16_ss(tmem + kColSP + 128u * i, a + uint32_t(s * (kSlabB >> 4) + 2 * kk),
+                                          bd + uint32_t(s * (kHalfB >> 4) + 2 * kk), kIdescQk,
+                                          (s | kk) != 0 ? 1u : 0u);
+                    umma2_commit(&ctl.s_full[i]);
+                    if (last) umma2_commit(&ctl.q_empty[i]);
+                }
+                __syncwarp();
+            };
+            // O(tile i) += P_i . V, values in stage st, over the 16-entry steps below the tile's limit
+            const auto pv = [&](int i, int j, int st) {
+                const int steps = min((lim[i] - j * kTile + 15) >> 4, kTile / 16);
+                if (issuer) {
+                    const uint64_t bd = v_desc + uint32_t(st * (kStageV >> 4));
+                    const auto step = [&](int kk) {
+                        umma2_bf16_ts(tmem + kColOP + 128u * i, tmem + kColSP + 128u * i + 8u * kk, bd + 128u * kk,
+                                      kIdescPv, (j | kk) != 0 ? 1u : 0u);
+                    };
+                    if (steps == kTile / 16) {
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; ++kk) step(kk);
+                    } else {
 #pragma unroll 1
-        for (int j = 0; j < n_all && ok; ++j) {
-            bool have_k = false, have_v = false;
+                        for (int kk = 0; kk < steps; ++kk) step(kk);
+                    }
+                    if (j + 1 == n_of[i]) umma2_commit(&ctl.o_full[i]);
+                }
+                __syncwarp();
+            };
+            // First scores of both tiles.
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (ok && j < n_of[i]) {
-                    if (!have_v) {
-                        if (tail && j == n_all - 1)
-                            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.tail_ready, 0, &ctl.abort)) != 0;
-                        else
-                            ok = wait(&ctl.v_full[st], phase);
+                if (!ok || n_of[i] == 0) continue;
+                if (!shared || i == 0 || n_of[0] == 0) wait(&ctl.k_full[kr.st], kr.phase);
+                wait(&ctl.q_full[i], nq[i] & 1u);
+                ++nq[i];
+                tc_fence_after_sync();
+                if (ok) qk(i, kr.st, n_of[i] == 1);
+                if (ok && (!shared || i == 1)) {
+                    commit(&ctl.k_empty[kr.st]);
+                    kr.next();
+                }
+            }
+#pragma unroll 1
+            for (int j = 0; j < nt && ok; ++j) {
+                bool have_k = false, have_v = false;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int l = shared ? 0 : i;
+                    if (ok && j < n_of[i]) {
+                        if (!shared || !have_v) {
+                            if (tail && j == nt - 1) {
+                                ok = __all_sync(0xffffffffu,
+                                                mbar_wait_cluster(&ctl.tail_ready[l], ntail[l] & 1u, &ctl.abort)) != 0;
+                                ++ntail[l];
+                            } else {
+                                wait(&ctl.v_full[vr.st], vr.phase);
+                            }
+                        }
+                        have_v = true;
+                        if (j == 0) {
+                            wait(&ctl.o_empty[i], (no[i] & 1u) ^ 1u);
+                            ++no[i];
+                        }
+                        wait(&ctl.p_full[i], np[i] & 1u);
+                        ++np[i];
+                        tc_fence_after_sync();
+                        if (ok) pv(i, j, vr.st);
+                        if (ok && !shared) {
+                            commit(&ctl.v_empty[vr.st]);
+                            vr.next();
+                        }
                     }
-                    have_v = true;
-                    if (ok) ok = wait(&ctl.p_full[i], uint32_t(j & 1));
-                    tc_fence_after_sync();
-                    if (ok) pv(i, j, st);
+                    if (ok && shared && i == 1) {
+                        commit(&ctl.v_empty[vr.st]);
+                        vr.next();
+                    }
+                    if (ok && j + 1 < n_of[i]) {
+                        if (!shared || !have_k) wait(&ctl.k_full[kr.st], kr.phase);
+                        have_k = true;
+                        tc_fence_after_sync();
+                        if (ok) qk(i, kr.st, j + 2 == n_of[i]);
+                        if (ok && !shared) {
+                            commit(&ctl.k_empty[kr.st]);
+                            kr.next();
+                        }
+                    }
                 }
-                if (ok && i == 1) commit(&ctl.v_empty[st]);
-                if (ok && j + 1 < n_of[i]) {
-                    if (!have_k) ok = wait(&ctl.k_full[st_next], phase_next);
-                    have_k = true;
-                    tc_fence_after_sync();
-                    if (ok) qk(i, st_next);
+                if (ok && shared && j + 1 < nt) {
+                    commit(&ctl.k_empty[kr.st]);
+                    kr.next();
                 }
             }
-            if (ok && j + 1 < n_all) commit(&ctl.k_empty[st_next]);
-            st = st_next;
-            phase = phase_next;
-            if (++st_next == kStages) {
-                st_next = 0;
-                phase_next ^= 1u;
+        }
+        if (rank == 0) {
+            if (!ok && issuer) {
+                atomicOr(p.err, kErrWaitTimeout);
+                ctl.abort = 1;
             }
+            commit(&ctl.all_done);
         }
-        if (!ok && issuer) {
-            atomicOr(p.err, kErrWaitTimeout);
-            ctl.abort = 1;
-        }
-        commit(&ctl.all_done);
-        wait_landed_p(&ctl.all_done, 0);  // every MMA issued has completed
+        wait_landed_p(&ctl.all_done, 0);  // every MMA has completed, and every arrival is here
         __syncwarp();
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ================= softmax: warps 0-3 tile 0, warps 4-7 tile 1 =================
         const int i = warp >> 2;
-        const int r = (warp & 3) * 32 + lane;  // row of the tile
+        const int r = rank * kTile + (warp & 3) * 32 + lane;  // row of the tile
         const uint32_t lane_addr = tmem_base + (uint32_t((warp & 3) * 32) << 16);
         const uint32_t s_addr = lane_addr + kColSP + 128u * i;
         const uint32_t o_addr = lane_addr + kColOP + 128u * i;
         const float c2 = p.sm_scale_log2;
-        const int row = row0 + i * 2 * kTile + rank * kTile + r;  // of the request
-        const bool live_row = row < rq.rows;
         const uint32_t p_bar = cluster_addr(&ctl.p_full[i], 0);
-        const int see = live_row ? rq.seen(row, p.entry_tokens) : limit[i];
-        float m = -INFINITY;
-        float2 l2 = make_float2(0.f, 0.f);
+        const uint32_t o_bar = cluster_addr(&ctl.o_empty[i], 0);
         bool failed = false;
+        uint32_t ns = 0, no = 0;  // score tiles and outputs so far
+        Unit u;
+        while (!failed && next_unit(u)) {
+            const int head = u.head + i * u.step_head;
+            const bool live_row = i * u.step_row + r < u.rows && head < p.heads;
+            const int ntiles = u.tiles(i);
+            int see = u.limit[i];
+            if (live_row) {
+                const int64_t len = int64_t(u.seq) - (int64_t(u.req_rows) - 1 - (u.row0 + i * u.step_row + r));
+                see = min(entries_seen(len > 0 ? int(len) : 0, p.entry_tokens), u.live);
+            }
+            float m = -INFINITY;
+            float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll 1
-        for (int j = 0; j < ntiles[i]; ++j) {
-            const bool ok = mbar_wait(&ctl.s_full[i], uint32_t(j & 1), &ctl.abort);
+            for (int j = 0; j < ntiles; ++j, ++ns) {
+                const bool ok = mbar_wait(&ctl.s_full[i], ns & 1u, &ctl.abort);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    failed = true;
+                    break;
+                }
+                tc_fence_after_sync();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + 32u * c, s[c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
+                const int here = see - j * kTile;  // entries of this tile that the row sees
+                if (__any_sync(0xffffffffu, here < kTile)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k >= here) s[c][k] = 0xFF800000u;  // -inf
+                }
+                float mx4[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mx4[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+                    for (int k = 1; k < 32; ++k) mx4[c] = fmaxf(mx4[c], __uint_as_float(s[c][k]));
+                }
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c2;
+                const bool need = mx > m + kRaiseLog2;
+                if (__any_sync(0xffffffffu, need)) {  // rare after the first tile
+                    float alpha = 1.f;
+                    if (need) {
+                        alpha = exp2f(m - mx);
+                        m = mx;
+                        l2.x *= alpha;
+                        l2.y *= alpha;
+                    }
+                    // S(j) full means that PV(j - 1), issued before it, has completed: O is at rest.
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(o_addr + 32u * c, o);
+                            tmem_ld_wait(o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                            tmem_st_x32(o_addr + 32u * c, o);
+                        }
+                    }
+                }
+                const float2 cc = make_float2(c2, c2);
+                const float nm = m == -INFINITY ? 0.f : -m;
+                const float2 mm = make_float2(nm, nm);
+#pragma unroll
+                for (int hp = 0; hp < 2; ++hp) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int c = 2 * hp + (k >> 4), e = 2 * (k & 15);
+                        float2 x =
+                            fma_f32x2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), cc, mm);
+                        x.x = ex2_approx(x.x);
+                        x.y = ex2_approx(x.y);
+                        l2 = add_f32x2(l2, x);
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(x.x, x.y);
+                        pk[k] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                    tmem_st_x32(s_addr + 32u * hp, pk);
+                }
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(p_bar);
+            }
+            if (failed) break;
+            // ---- output
+            const int64_t token = int64_t(u.q_row) + i * u.step_row + r;
+            __nv_bfloat16* o_row = reinterpret_cast<__nv_bfloat16*>(p.out) + (token * p.heads + head) * kPrefillDv;
+            if (ntiles == 0) {  // rows that see nothing
+                if (live_row) {
+                    for (int c = 0; c < kPrefillDv / 8; ++c)
+                        *reinterpret_cast<uint4*>(o_row + 8 * c) = make_uint4(0, 0, 0, 0);
+                    p.lse[token * p.heads + head] = -INFINITY;
+                }
+                __syncwarp();
+                continue;
+            }
+            const bool ok = mbar_wait(&ctl.o_full[i], no & 1u, &ctl.abort);
             if (!__all_sync(0xffffffffu, ok)) {
                 failed = true;
                 break;
             }
-            tc_fence_after_sync();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + 32u * c, s[c]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
-            const int here = see - j * kTile;  // entries of this tile that the row sees
-            if (__any_sync(0xffffffffu, here < kTile)) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (32 * c + k >= here) s[c][k] = 0xFF800000u;  // -inf
-            }
-            float mx4[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mx4[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-                for (int k = 1; k < 32; ++k) mx4[c] = fmaxf(mx4[c], __uint_as_float(s[c][k]));
-            }
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c2;
-            const bool need = mx > m + kRaiseLog2;
-            if (__any_sync(0xffffffffu, need)) {  // rare after the first tile
-                float alpha = 1.f;
-                if (need) {
-                    alpha = exp2f(m - mx);
-                    m = mx;
-                    l2.x *= alpha;
-                    l2.y *= alpha;
-                }
-                // S(j) full means that PV(j - 1), issued before it, has completed: O is at rest.
-                if (j > 0) {
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(o_addr + 32u * c, o);
-                        tmem_ld_wait(o);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                        tmem_st_x32(o_addr + 32u * c, o);
-                    }
-                }
-            }
-            const float2 cc = make_float2(c2, c2);
-            const float nm = m == -INFINITY ? 0.f : -m;
-            const float2 mm = make_float2(nm, nm);
-#pragma unroll
-            for (int hp = 0; hp < 2; ++hp) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const int c = 2 * hp + (k >> 4), e = 2 * (k & 15);
-                    float2 x = fma_f32x2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), cc, mm);
-                    x.x = ex2_approx(x.x);
-                    x.y = ex2_approx(x.y);
-                    l2 = add_f32x2(l2, x);
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(x.x, x.y);
-                    pk[k] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-                tmem_st_x32(s_addr + 32u * hp, pk);
-            }
-            tmem_st_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(p_bar);
-        }
-        // ---- output
-        if (!failed && ntiles[i] > 0) {
-            const bool ok = mbar_wait(&ctl.o_full[i], 0, &ctl.abort);
-            failed = !__all_sync(0xffffffffu, ok);
-        }
-        if (failed) {
-            if (lane == 0) {
-                atomicOr(p.err, kErrWaitTimeout);
-                ctl.abort = 1;
-            }
-        } else if (__any_sync(0xffffffffu, live_row)) {
+            ++no;
             tc_fence_after_sync();
             const float l = l2.x + l2.y;
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            const int64_t token = int64_t(rq.q0) + row;
-            __nv_bfloat16* o_row = reinterpret_cast<__nv_bfloat16*>(p.out) + (token * p.heads + head) * kPrefillDv;
             if (live_row) p.lse[token * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2P : -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                if (ntiles[i] > 0) {
-                    tmem_ld_32x32b_x32(o_addr + 32u * c, o);
-                    tmem_ld_wait(o);
-                } else {
+            uint32_t o[4][32];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = 0u;
-                }
-                if (live_row) {
+            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(o_addr + 32u * c, o[c]);
 #pragma unroll
-                    for (int q4 = 0; q4 < 2; ++q4) {  // a whole sector a lane
-                        uint32_t u[8];
+            for (int c = 0; c < 4; ++c) tmem_ld_wait(o[c]);
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(o_bar);  // O may be overwritten
+            if (live_row) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[16 * q4 + 2 * k]) * inv,
-                                                                           __uint_as_float(o[16 * q4 + 2 * k + 1]) * inv);
-                            u[k] = *reinterpret_cast<const uint32_t*>(&v);
-                        }
-                        if (p.out_aligned32) {
-                            st_global_v8(o_row + 32 * c + 16 * q4, u);
-                        } else {
-                            uint4* d = reinterpret_cast<uint4*>(o_row + 32 * c + 16 * q4);
-                            d[0] = make_uint4(u[0], u[1], u[2], u[3]);
-                            d[1] = make_uint4(u[4], u[5], u[6], u[7]);
-                        }
+                for (int q4 = 0; q4 < 8; ++q4) {  // a whole sector a lane
+                    uint32_t w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int c = q4 >> 1, e = 16 * (q4 & 1) + 2 * k;
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[c][e]) * inv,
+                                                                       __uint_as_float(o[c][e + 1]) * inv);
+                        w[k] = *reinterpret_cast<const uint32_t*>(&v);
+                    }
+                    if (p.out_aligned32) {
+                        st_global_v8(o_row + 16 * q4, w);
+                    } else {
+                        uint4* d = reinterpret_cast<uint4*>(o_row + 16 * q4);
+                        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
                     }
                 }
             }
+            __syncwarp();
+        }
+        if (failed && lane == 0) {
+            atomicOr(p.err, kErrWaitTimeout);
+            ctl.abort = 1;
         }
     }
 
-    // The leader's last arrival here: none of its earlier ones is still under way to this CTA.
-    if (warp == 8 && rank == 1) wait_landed_p(&ctl.all_done, 0);
     __syncwarp();
     tc_fence_before_sync();
     cluster_sync_all();  // no CTA leaves while the other may read its memory or arrive on its barriers
@@ -659,16 +894,30 @@ cudaError_t launch_mla_prefill(const CUtensorMap& q_map, const CUtensorMap& kn_m
     if (e != cudaSuccess) return e;
     e = smem_limit.apply(dev, mla_prefill_kernel, kSmemP);
     if (e != cudaSuccess) return e;
+    // Persistent clusters: as many as the device holds (its SMs do not all pair up), or one per unit.
+    static std::atomic<int> resident[kMaxDevices];
+    int fit = resident[dev].load(std::memory_order_relaxed);
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2u * unsigned(p.slots) * unsigned(p.heads));
+    cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreadsP);
     cfg.dynamicSmemBytes = size_t(kSmemP);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (fit == 0) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        e = cudaOccupancyMaxActiveClusters(&fit, mla_prefill_kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        if (fit < 1) return cudaErrorInvalidConfiguration;
+        resident[dev].store(fit, std::memory_order_relaxed);
+    }
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const int64_t most = int64_t(p.slots) * p.heads;  // at least the number of units
+    cfg.gridDim = dim3(2u * unsigned(most < fit ? most : fit));
     return cudaLaunchKernelEx(&cfg, mla_prefill_kernel, q_map, kn_map, kr_map, v_map, p);
 }
 
