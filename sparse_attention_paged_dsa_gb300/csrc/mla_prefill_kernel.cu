@@ -70,7 +70,7 @@ constexpr int kOffK = kOffQt + 2 * kQkSlabs * kSlabB;
 constexpr int kOffV = kOffK + kStages * kStageK;
 constexpr int kOffCtlP = kOffV + kStages * kStageV;
 constexpr int kThreadsP = 384;
-constexpr int kRegsSoftmax = 200, kRegsOther = 104;  // 8 x 200 + 4 x 104 = 12 x 168 a warp lane
+constexpr int kRegsSoftmax = 192, kRegsOther = 120;  // 8 x 192 + 4 x 120 = 12 x 168 a warp lane
 constexpr uint32_t kTmemColsP = 512;
 constexpr uint32_t kColSP = 0;    // S / P of tile i at 128 i
 constexpr uint32_t kColOP = 256;  // O of tile i at 256 + 128 i
@@ -78,7 +78,7 @@ constexpr float kRaiseLog2 = 20.0f;  // rounding is relative: weights may pass 1
 constexpr float kLn2P = 0.69314718055994531f;
 
 constexpr int kSortMost = 256;       // requests that are ordered by length (more: as they come)
-constexpr int kInfoSlots = 2;
+constexpr int kInfoSlots = 4;
 constexpr int kInfoReaders = 11;     // every warp but the scheduler
 
 // What a cluster works on: two query tiles, or fewer.  Tile i is rows [i step_row, + 256) of the block
@@ -103,14 +103,15 @@ struct Unit {
     // Value rows behind the last entry that any of these rows sees belong to other requests or hold
     // nothing.  Products stop at a 16-entry step, and where that is not the end of the entries the rows
     // up to it are zeroed (weights there are 0, but 0 x NaN is not): such a last tile's values count on
-    // a barrier of each CTA, whose warp 10 zeroes them and tells the leader.
+    // a barrier of each CTA, whose warp 10 zeroes them and tells the leader.  Those barriers are the
+    // stage's: the loads run ahead of the products by units, and a barrier takes one fill at a time.
     __device__ __forceinline__ bool tail() const { return (limit_max() & 15) != 0; }
 };
 
 struct __align__(8) PrefillCtl {
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
-    uint64_t tail_landed[2], tail_ready[2];
+    uint64_t tail_landed[kStages], tail_ready[kStages];  // per value stage
     uint64_t info_full[kInfoSlots], info_empty[kInfoSlots];
     uint64_t all_done;
     uint32_t tmem_base;
@@ -124,6 +125,12 @@ struct __align__(8) PrefillCtl {
 };
 constexpr int kSmemP = 1024 + kOffCtlP + int(sizeof(PrefillCtl));
 static_assert(kSmemP <= 232448, "fits one CTA per SM");
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // Two-CTA MMAs, issued by one thread of the leader: M = 256 (128 rows of A and D in each CTA), each
 // CTA's shared memory (at the same offsets) holding half of B.  A from shared memory:
@@ -295,6 +302,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&ctl.k_empty[i], 1);
             mbar_init(&ctl.v_full[i], 1);
             mbar_init(&ctl.v_empty[i], 1);
+            mbar_init(&ctl.tail_landed[i], 1);
+            mbar_init(&ctl.tail_ready[i], 2);  // one arrival of each CTA
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.q_full[i], 1);
@@ -303,8 +312,6 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             mbar_init(&ctl.p_full[i], 8);   // four warps of each CTA
             mbar_init(&ctl.o_full[i], 1);
             mbar_init(&ctl.o_empty[i], 8);  // the same
-            mbar_init(&ctl.tail_landed[i], 1);
-            mbar_init(&ctl.tail_ready[i], 2);
         }
         for (int i = 0; i < kInfoSlots; ++i) {
             mbar_init(&ctl.info_full[i], 1);
@@ -430,6 +437,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                 u.q_row = rq.q0 + u.row0;
                 u.rows = min(rq.rows - u.row0, kPrefillBlock);
                 u.req_rows = rq.rows, u.seq = rq.seq, u.live = rq.live, u.kv0 = rq.kv0;
+#pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int from = i * u.step_row, to = min(u.rows, from + 2 * kTile);
                     const bool there = to > from && u.head + i * u.step_head < p.heads;
@@ -456,8 +464,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         const uint32_t sb = uint32_t(uniform(int(s_base)));
         bool ok = true;
         int nk = 0, nv = 0;                       // key and value tiles so far
-        int nq[2] = {0, 0}, ntail[2] = {0, 0};    // q tiles and zeroed ends
-        uint32_t v_tail = 0;                      // value stages whose last fill counts on a tail barrier
+        int nq[2] = {0, 0};                       // q tiles
+        uint32_t v_tail = 0, tail_phase = 0;      // value stages whose last fill counts on the tail barrier; its phases
         const auto wait = [&](uint64_t* bar, int fills) {  // the stage's `fills` earlier contents are used
             ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t(fills) & 1u) ^ 1u, &ctl.abort));
             return ok;
@@ -498,10 +506,10 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                 if (!wait(&ctl.v_empty[st], nv / kStages)) return;
                 const bool end = u.tail() && j == nt - 1;
                 if (issuer) {
-                    const uint32_t bar = end ? cluster_addr(&ctl.tail_landed[l], uint32_t(rank))
+                    const uint32_t bar = end ? cluster_addr(&ctl.tail_landed[st], uint32_t(rank))
                                              : cluster_addr(&ctl.v_full[st], 0);
                     if (end) {
-                        mbar_arrive_expect_tx(&ctl.tail_landed[l], uint32_t(kStageV));
+                        mbar_arrive_expect_tx(&ctl.tail_landed[st], uint32_t(kStageV));
                         if (rank == 0) mbar_arrive(&ctl.v_full[st]);  // the stage's phases go on
                     } else if (rank == 0) {
                         mbar_arrive_expect_tx(&ctl.v_full[st], uint32_t(2 * kStageV));
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                 }
                 __syncwarp();
                 v_tail = (v_tail & ~(1u << st)) | (uint32_t(end) << st);
-                if (end) ++ntail[l];
+                if (end) tail_phase ^= 1u << st;
                 ++nv;
             };
             if (nt > 0) {
@@ -542,13 +550,21 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                 for (int i = 0; i < 2; ++i)
                     if (nq[i] > 0) wait_landed_p(&ctl.q_full[i], uint32_t(nq[i] - 1) & 1u);
             }
-            for (int i = 0; i < 2; ++i)
-                if (ntail[i] > 0) wait_landed_p(&ctl.tail_landed[i], uint32_t(ntail[i] - 1) & 1u);
+            for (int st = 0; st < kStages; ++st)
+                if ((v_tail >> st) & 1u) wait_landed_p(&ctl.tail_landed[st], ((tail_phase >> st) & 1u) ^ 1u);
+            // After a timeout the two CTAs may have issued different copies, and what only the other counts
+            // cannot be waited for here: a millisecond, a thousand times a copy's latency.
+            if (*const_cast<volatile int*>(&ctl.abort)) {
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000 * 1000) {
+                }
+            }
         }
         __syncwarp();
     } else if (warp == 10) {
         // ================= the last tiles' value rows =================
-        int nv = 0, ntail[2] = {0, 0};
+        int nv = 0;
+        uint32_t tail_phase = 0;  // per value stage
         bool ok = true;
         Unit u;
         while (ok && next_unit(u)) {
@@ -557,15 +573,16 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             if (!u.tail()) continue;
             const int valid = u.limit_max() - (nt - 1) * kTile, fill = 16 - (valid & 15);
             for (int l = 0; l < streams && ok; ++l) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.tail_landed[l], uint32_t(ntail[l]) & 1u, &ctl.abort)) != 0;
-                ++ntail[l];
+                const int st = (nv - streams + l) % kStages;
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.tail_landed[st], (tail_phase >> st) & 1u, &ctl.abort)) != 0;
+                tail_phase ^= 1u << st;
                 if (!ok) break;
-                uint8_t* v = tiles + kOffV + ((nv - streams + l) % kStages) * kStageV;
+                uint8_t* v = tiles + kOffV + st * kStageV;
                 for (int i = lane; i < fill * 8; i += 32)
                     *reinterpret_cast<uint4*>(v + (valid + (i >> 3)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                 asm volatile("fence.proxy.async;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&ctl.tail_ready[l], 0));
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&ctl.tail_ready[st], 0));
             }
         }
         __syncwarp();
@@ -598,116 +615,173 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             }
         };
         Ring kr, vr;
-        uint32_t np[2] = {0, 0}, no[2] = {0, 0}, nq[2] = {0, 0}, ntail[2] = {0, 0};  // phases
-        Unit info;
-        while (ok && next_unit(info)) {
-            if (rank != 0) continue;  // the leader issues for both
-            const int lim[2] = {uniform(info.limit[0]), uniform(info.limit[1])};
-            const int n_of[2] = {(lim[0] + kTile - 1) / kTile, (lim[1] + kTile - 1) / kTile};
-            const int nt = max(n_of[0], n_of[1]);
-            const bool shared = uniform(info.step_head) == 0;
-            const bool tail = (max(lim[0], lim[1]) & 15) != 0;
-            // S(tile i) = Q_i . K^T, keys in stage st
-            const auto qk = [&](int i, int st, bool last) {
-                if (issuer) {
-                    const uint64_t a = q_desc + uint32_t(i * kQkSlabs * (kSlabB >> 4));
-                    const uint64_t bd = k_desc + uint32_t(st * (kStageK >> 4));
+        uint32_t np[2] = {0, 0}, no[2] = {0, 0}, nq[2] = {0, 0}, tail_phase = 0;  // phases
+        // What the loop needs of a unit; fetched a unit ahead.
+        struct Plan {
+            int lim[2], n_of[2], nt;
+            bool shared, tail;
+        };
+        const auto fetch = [&](Plan& w) {
+            Unit u;
+            if (!next_unit(u)) return false;
+            w.lim[0] = uniform(u.limit[0]), w.lim[1] = uniform(u.limit[1]);
+            w.n_of[0] = (w.lim[0] + kTile - 1) / kTile, w.n_of[1] = (w.lim[1] + kTile - 1) / kTile;
+            w.nt = max(w.n_of[0], w.n_of[1]);
+            w.shared = uniform(u.step_head) == 0;
+            w.tail = (max(w.lim[0], w.lim[1]) & 15) != 0;
+            return true;
+        };
+        // S(tile i) = Q_i . K^T, keys in stage st
+        const auto qk = [&](int i, int st, bool last) {
+            if (issuer) {
+                const uint64_t a = q_desc + uint32_t(i * kQkSlabs * (kSlabB >> 4));
+                const uint64_t bd = k_desc + uint32_t(st * (kStageK >> 4));
 #pragma unroll
-                    for (int s = 0; s < kQkSlabs; ++s)
+                for (int s = 0; s < kQkSlabs; ++s)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma2_bf16_ss(tmem + kColSP + 128u * i, a + uint32_t(s * (kSlabB >> 4) + 2 * kk),
-                                          bd + uint32_t(s * (kHalfB >> 4) + 2 * kk), kIdescQk,
-                                          (s | kk) != 0 ? 1u : 0u);
-                    umma2_commit(&ctl.s_full[i]);
-                    if (last) umma2_commit(&ctl.q_empty[i]);
-                }
-                __syncwarp();
-            };
-            // O(tile i) += P_i . V, values in stage st, over the 16-entry steps below the tile's limit
-            const auto pv = [&](int i, int j, int st) {
-                const int steps = min((lim[i] - j * kTile + 15) >> 4, kTile / 16);
-                if (issuer) {
-                    const uint64_t bd = v_desc + uint32_t(st * (kStageV >> 4));
-                    const auto step = [&](int kk) {
-                        umma2_bf16_ts(tmem + kColOP + 128u * i, tmem + kColSP + 128u * i + 8u * kk, bd + 128u * kk,
-                                      kIdescPv, (j | kk) != 0 ? 1u : 0u);
-                    };
-                    if (steps == kTile / 16) {
-#pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk) step(kk);
-                    } else {
-#pragma unroll 1
-                        for (int kk = 0; kk < steps; ++kk) step(kk);
-                    }
-                    if (j + 1 == n_of[i]) umma2_commit(&ctl.o_full[i]);
-                }
-                __syncwarp();
-            };
-            // First scores of both tiles.
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (!ok || n_of[i] == 0) continue;
-                if (!shared || i == 0 || n_of[0] == 0) wait(&ctl.k_full[kr.st], kr.phase);
-                wait(&ctl.q_full[i], nq[i] & 1u);
-                ++nq[i];
-                tc_fence_after_sync();
-                if (ok) qk(i, kr.st, n_of[i] == 1);
-                if (ok && (!shared || i == 1)) {
-                    commit(&ctl.k_empty[kr.st]);
-                    kr.next();
-                }
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma2_bf16_ss(tmem + kColSP + 128u * i, a + uint32_t(s * (kSlabB >> 4) + 2 * kk),
+                                      bd + uint32_t(s * (kHalfB >> 4) + 2 * kk), kIdescQk, (s | kk) != 0 ? 1u : 0u);
+                umma2_commit(&ctl.s_full[i]);
+                if (last) umma2_commit(&ctl.q_empty[i]);
             }
-#pragma unroll 1
-            for (int j = 0; j < nt && ok; ++j) {
-                bool have_k = false, have_v = false;
+            __syncwarp();
+        };
+        // O(tile i) += P_i . V, values in stage st, over the 16-entry steps below the tile's limit
+        const auto pv = [&](int i, int j, int st, int lim, bool last) {
+            const int steps = min((lim - j * kTile + 15) >> 4, kTile / 16);
+            if (issuer) {
+                const uint64_t bd = v_desc + uint32_t(st * (kStageV >> 4));
+                const auto step = [&](int kk) {
+                    umma2_bf16_ts(tmem + kColOP + 128u * i, tmem + kColSP + 128u * i + 8u * kk, bd + 128u * kk, kIdescPv,
+                                  (j | kk) != 0 ? 1u : 0u);
+                };
+                if (steps == kTile / 16) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int l = shared ? 0 : i;
-                    if (ok && j < n_of[i]) {
-                        if (!shared || !have_v) {
-                            if (tail && j == nt - 1) {
-                                ok = __all_sync(0xffffffffu,
-                                                mbar_wait_cluster(&ctl.tail_ready[l], ntail[l] & 1u, &ctl.abort)) != 0;
-                                ++ntail[l];
-                            } else {
-                                wait(&ctl.v_full[vr.st], vr.phase);
-                            }
-                        }
-                        have_v = true;
+                    for (int kk = 0; kk < kTile / 16; ++kk) step(kk);
+                } else {
+#pragma unroll 1
+                    for (int kk = 0; kk < steps; ++kk) step(kk);
+                }
+                if (last) umma2_commit(&ctl.o_full[i]);
+            }
+            __syncwarp();
+        };
+        // A unit's first scores of tile i: its S is free once the products issued so far have read P.
+        const auto first_scores = [&](const Plan& w, int i) {
+            if (!ok || w.n_of[i] == 0) return;
+            if (!w.shared || i == 0 || w.n_of[0] == 0) wait(&ctl.k_full[kr.st], kr.phase);
+            wait(&ctl.q_full[i], nq[i] & 1u);
+            ++nq[i];
+            tc_fence_after_sync();
+            if (ok) qk(i, kr.st, w.n_of[i] == 1);
+            if (ok && (!w.shared || i == 1)) {
+                commit(&ctl.k_empty[kr.st]);
+                kr.next();
+            }
+        };
+        Plan w, next;
+        bool more = fetch(w);
+        if (rank == 0) {
+            if (more)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) first_scores(w, i);
+            while (ok && more) {
+                if (w.nt == 0) {
+                    more = fetch(next);
+                    if (more)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) first_scores(next, i);
+                }
+                int j = 0;
+                // Tiles that both query tiles see whole, with another one to come: the long part of a long
+                // unit, as straight as it can be (an MMA issued late is tensor core time lost).
+                const int whole = w.shared ? min(w.n_of[0], w.n_of[1]) - 1 : 0;
+#pragma unroll 1
+                for (; j < whole && ok; ++j) {
+                    wait(&ctl.v_full[vr.st], vr.phase);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
                         if (j == 0) {
                             wait(&ctl.o_empty[i], (no[i] & 1u) ^ 1u);
                             ++no[i];
                         }
+                        if (i == 0) wait(&ctl.k_full[kr.st], kr.phase);
                         wait(&ctl.p_full[i], np[i] & 1u);
                         ++np[i];
                         tc_fence_after_sync();
-                        if (ok) pv(i, j, vr.st);
-                        if (ok && !shared) {
+                        if (ok && issuer) {
+                            const uint64_t bd = v_desc + uint32_t(vr.st * (kStageV >> 4));
+#pragma unroll
+                            for (int kk = 0; kk < kTile / 16; ++kk)
+                                umma2_bf16_ts(tmem + kColOP + 128u * i, tmem + kColSP + 128u * i + 8u * kk, bd + 128u * kk,
+                                              kIdescPv, (j | kk) != 0 ? 1u : 0u);
+                            if (i == 1) umma2_commit(&ctl.v_empty[vr.st]);
+                        }
+                        if (ok) qk(i, kr.st, j + 2 == w.n_of[i]);
+                    }
+                    if (ok) commit(&ctl.k_empty[kr.st]);
+                    kr.next();
+                    vr.next();
+                }
+#pragma unroll 1
+                for (; j < w.nt && ok; ++j) {
+                    const bool end = j == w.nt - 1;
+                    bool have_k = false, have_v = false;
+                    if (end) more = fetch(next);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (ok && j < w.n_of[i]) {
+                            if (!w.shared || !have_v) {
+                                if (w.tail && end) {
+                                    ok = __all_sync(0xffffffffu,
+                                                    mbar_wait_cluster(&ctl.tail_ready[vr.st],
+                                                                      (tail_phase >> vr.st) & 1u, &ctl.abort)) != 0;
+                                    tail_phase ^= 1u << vr.st;
+                                } else {
+                                    wait(&ctl.v_full[vr.st], vr.phase);
+                                }
+                            }
+                            have_v = true;
+                            if (j == 0) {
+                                wait(&ctl.o_empty[i], (no[i] & 1u) ^ 1u);
+                                ++no[i];
+                            }
+                            wait(&ctl.p_full[i], np[i] & 1u);
+                            ++np[i];
+                            tc_fence_after_sync();
+                            if (ok) pv(i, j, vr.st, w.lim[i], j + 1 == w.n_of[i]);
+                            if (ok && !w.shared) {
+                                commit(&ctl.v_empty[vr.st]);
+                                vr.next();
+                            }
+                        }
+                        if (ok && w.shared && i == 1) {
                             commit(&ctl.v_empty[vr.st]);
                             vr.next();
                         }
-                    }
-                    if (ok && shared && i == 1) {
-                        commit(&ctl.v_empty[vr.st]);
-                        vr.next();
-                    }
-                    if (ok && j + 1 < n_of[i]) {
-                        if (!shared || !have_k) wait(&ctl.k_full[kr.st], kr.phase);
-                        have_k = true;
-                        tc_fence_after_sync();
-                        if (ok) qk(i, kr.st, j + 2 == n_of[i]);
-                        if (ok && !shared) {
-                            commit(&ctl.k_empty[kr.st]);
-                            kr.next();
+                        if (ok && j + 1 < w.n_of[i]) {
+                            if (!w.shared || !have_k) wait(&ctl.k_full[kr.st], kr.phase);
+                            have_k = true;
+                            tc_fence_after_sync();
+                            if (ok) qk(i, kr.st, j + 2 == w.n_of[i]);
+                            if (ok && !w.shared) {
+                                commit(&ctl.k_empty[kr.st]);
+                                kr.next();
+                            }
                         }
+                        // All keys of this unit are used: on to the next one's.
+                        if (end && more) first_scores(next, i);
+                    }
+                    if (ok && w.shared && !end) {
+                        commit(&ctl.k_empty[kr.st]);
+                        kr.next();
                     }
                 }
-                if (ok && shared && j + 1 < nt) {
-                    commit(&ctl.k_empty[kr.st]);
-                    kr.next();
-                }
+                w = next;
             }
+        } else {
+            while (more) more = fetch(w);  // the leader issues for both
         }
         if (rank == 0) {
             if (!ok && issuer) {
@@ -732,11 +806,13 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         bool failed = false;
         uint32_t ns = 0, no = 0;  // score tiles and outputs so far
         Unit u;
-        while (!failed && next_unit(u)) {
+        bool more = next_unit(u);
+        while (more) {
             const int head = u.head + i * u.step_head;
             const bool live_row = i * u.step_row + r < u.rows && head < p.heads;
-            const int ntiles = u.tiles(i);
-            int see = u.limit[i];
+            const int limit = i ? u.limit[1] : u.limit[0], ntiles = (limit + kTile - 1) / kTile;
+            const int64_t token = int64_t(u.q_row) + i * u.step_row + r;
+            int see = limit;
             if (live_row) {
                 const int64_t len = int64_t(u.seq) - (int64_t(u.req_rows) - 1 - (u.row0 + i * u.step_row + r));
                 see = min(entries_seen(len > 0 ? int(len) : 0, p.entry_tokens), u.live);
@@ -751,67 +827,101 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                     break;
                 }
                 tc_fence_after_sync();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + 32u * c, s[c]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
                 const int here = see - j * kTile;  // entries of this tile that the row sees
-                if (__any_sync(0xffffffffu, here < kTile)) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * c + k >= here) s[c][k] = 0xFF800000u;  // -inf
-                }
-                float mx4[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    mx4[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-                    for (int k = 1; k < 32; ++k) mx4[c] = fmaxf(mx4[c], __uint_as_float(s[c][k]));
-                }
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * c2;
-                const bool need = mx > m + kRaiseLog2;
-                if (__any_sync(0xffffffffu, need)) {  // rare after the first tile
-                    float alpha = 1.f;
-                    if (need) {
-                        alpha = exp2f(m - mx);
-                        m = mx;
-                        l2.x *= alpha;
-                        l2.y *= alpha;
-                    }
-                    // S(j) full means that PV(j - 1), issued before it, has completed: O is at rest.
-                    if (j > 0) {
+                const float2 cc = make_float2(c2, c2);
+                // The row's maximum so far, and O and the sum with it (rare after the first tile).
+                const auto raise = [&](float mx) {
+                    const bool need = mx > m + kRaiseLog2;
+                    if (__any_sync(0xffffffffu, need)) {
+                        float alpha = 1.f;
+                        if (need) {
+                            alpha = exp2f(m - mx);
+                            m = mx;
+                            l2.x *= alpha;
+                            l2.y *= alpha;
+                        }
+                        // S(j) full means that PV(j - 1), issued before it, has completed: O is at rest.
+                        if (j > 0) {
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t o[32];
-                            tmem_ld_32x32b_x32(o_addr + 32u * c, o);
-                            tmem_ld_wait(o);
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t o[32];
+                                tmem_ld_32x32b_x32(o_addr + 32u * c, o);
+                                tmem_ld_wait(o);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                            tmem_st_x32(o_addr + 32u * c, o);
+                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                                tmem_st_x32(o_addr + 32u * c, o);
+                            }
                         }
                     }
-                }
-                const float2 cc = make_float2(c2, c2);
-                const float nm = m == -INFINITY ? 0.f : -m;
-                const float2 mm = make_float2(nm, nm);
+                };
+                // The weights of 32 columns, as 16 pairs of bf16 from pk[at] on.
+                const auto weights = [&](const uint32_t (&v)[32], auto& pk, int at, float2 mm) {
 #pragma unroll
-                for (int hp = 0; hp < 2; ++hp) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int c = 2 * hp + (k >> 4), e = 2 * (k & 15);
+                    for (int k = 0; k < 16; ++k) {
                         float2 x =
-                            fma_f32x2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), cc, mm);
+                            fma_f32x2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), cc, mm);
                         x.x = ex2_approx(x.x);
                         x.y = ex2_approx(x.y);
                         l2 = add_f32x2(l2, x);
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(x.x, x.y);
-                        pk[k] = *reinterpret_cast<const uint32_t*>(&v);
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+                        pk[at + k] = *reinterpret_cast<const uint32_t*>(&b);
                     }
-                    tmem_st_x32(s_addr + 32u * hp, pk);
+                };
+                if (__all_sync(0xffffffffu, here >= kTile)) {
+                    uint32_t s[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + 32u * c, s[c]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
+                    float mx[4];  // four independent chains
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+                    for (int k = 1; k < 31; k += 2)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            mx[c] = max3(mx[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
+                    raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2);
+                    const float nm = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+                        weights(s[2 * h], pk, 0, make_float2(nm, nm));
+                        weights(s[2 * h + 1], pk, 16, make_float2(nm, nm));
+                        tmem_st_x32(s_addr + 32u * h, pk);
+                    }
+                } else {
+                    // A tile that some row sees in part: 32 columns at a time, read twice; the products read
+                    // none past the tile's limit, so chunks that start behind it are left out.
+                    const int chunks = min((limit - j * kTile + 31) >> 5, 4);
+                    uint32_t v[32];
+                    const auto chunk = [&](int c) {
+                        tmem_ld_32x32b_x32(s_addr + 32u * c, v);
+                        tmem_ld_wait(v);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k >= here) v[k] = 0xFF800000u;  // -inf
+                    };
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        chunk(c);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            mx = max3(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                    }
+                    raise(mx * c2);
+                    const float nm = m == -INFINITY ? 0.f : -m;
+                    // P's chunk c covers S's columns [16 c, 16 c + 16): behind what later chunks still read.
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        chunk(c);
+                        uint32_t pk[16];
+                        weights(v, pk, 0, make_float2(nm, nm));
+                        tmem_st_x16(s_addr + 16u * c, pk);
+                    }
                 }
                 tmem_st_wait();
                 tc_fence_before_sync();
@@ -819,8 +929,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                 if (lane == 0) mbar_arrive_remote(p_bar);
             }
             if (failed) break;
+            more = next_unit(u);
             // ---- output
-            const int64_t token = int64_t(u.q_row) + i * u.step_row + r;
             __nv_bfloat16* o_row = reinterpret_cast<__nv_bfloat16*>(p.out) + (token * p.heads + head) * kPrefillDv;
             if (ntiles == 0) {  // rows that see nothing
                 if (live_row) {
@@ -838,12 +948,12 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             }
             ++no;
             tc_fence_after_sync();
-            const float l = l2.x + l2.y;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            if (live_row) p.lse[token * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2P : -INFINITY;
             uint32_t o[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(o_addr + 32u * c, o[c]);
+            const float l = l2.x + l2.y;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            if (live_row) p.lse[token * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2P : -INFINITY;
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_wait(o[c]);
             tc_fence_before_sync();
