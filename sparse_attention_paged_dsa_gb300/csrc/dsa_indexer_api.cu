@@ -797,20 +797,23 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
     dsa_status_t st = check_workspace(workspace, workspace_bytes, DSA_PREFILL_WORKSPACE_BYTES);
     if (st != DSA_OK) return st;
     if (q_rows == 0) return DSA_OK;
-    CUtensorMap q_map, kn_map, kr_map, v_map;
-    st = make_heads_map(&q_map, q, q_rows, heads, DSA_PREFILL_QK_DIM, q_row_stride, q_head_stride, 128, "prefill q");
+    dsa::PrefillMaps m;
+    st = make_heads_map(&m.q, q, q_rows, heads, DSA_PREFILL_QK_DIM, q_row_stride, q_head_stride, 128, "prefill q");
     if (st != DSA_OK) return st;
     if (kv_rows > 0) {
-        st = make_heads_map(&kn_map, k_nope, kv_rows, heads, DSA_PREFILL_NOPE_DIM, k_row_stride, k_head_stride, 64,
-                            "prefill k_nope");
-        if (st != DSA_OK) return st;
-        st = make_heads_map(&v_map, v, kv_rows, heads, DSA_PREFILL_V_DIM, v_row_stride, v_head_stride, 128,
-                            "prefill v");
-        if (st != DSA_OK) return st;
-        st = make_rows_map(&kr_map, k_rope, kv_rows, DSA_PREFILL_ROPE_DIM, 64, "prefill k_rope", k_rope_stride);
-        if (st != DSA_OK) return st;
+        for (uint32_t few : {0u, 16u}) {  // whole tiles, and the 16 entries that the last ones are loaded by
+            st = make_heads_map(few ? &m.kn16 : &m.kn, k_nope, kv_rows, heads, DSA_PREFILL_NOPE_DIM, k_row_stride,
+                                k_head_stride, few ? few : 64, "prefill k_nope");
+            if (st != DSA_OK) return st;
+            st = make_heads_map(few ? &m.v16 : &m.v, v, kv_rows, heads, DSA_PREFILL_V_DIM, v_row_stride, v_head_stride,
+                                few ? few : 128, "prefill v");
+            if (st != DSA_OK) return st;
+            st = make_rows_map(few ? &m.kr16 : &m.kr, k_rope, kv_rows, DSA_PREFILL_ROPE_DIM, few ? few : 64,
+                               "prefill k_rope", k_rope_stride);
+            if (st != DSA_OK) return st;
+        }
     } else {
-        kn_map = kr_map = v_map = q_map;  // no entry: the kernel loads none
+        m.kn = m.kr = m.v = m.kn16 = m.kr16 = m.v16 = m.q;  // no entry: the kernel loads none
     }
     dsa::PrefillParams p{};
     p.cu_q = cu_q;
@@ -828,7 +831,7 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
     p.out_aligned32 = aligned(out, 32) ? 1 : 0;
     // A scale of 0 becomes one whose products vanish next to 1: hidden scores stay -inf times it.
     p.sm_scale_log2 = std::fmax(sm_scale * 1.4426950408889634f, 1e-30f);
-    const cudaError_t e = dsa::launch_mla_prefill(q_map, kn_map, kr_map, v_map, p, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = dsa::launch_mla_prefill(m, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA prefill launch");
 }
 

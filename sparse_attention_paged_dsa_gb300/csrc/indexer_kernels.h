@@ -188,10 +188,12 @@ struct PrefillParams {
     int32_t out_aligned32;     // out starts on a 32-byte boundary
     float sm_scale_log2;       // sm_scale * log2(e), above 0
 };
-// Maps of 128-byte-swizzled boxes of 64 dims x 128 rows (q, v) or 64 rows (k_nope, k_rope): q, k_nope and v
-// as (dim, head, row), k_rope as (dim, row).
-cudaError_t launch_mla_prefill(const CUtensorMap& q_map, const CUtensorMap& kn_map, const CUtensorMap& kr_map,
-                               const CUtensorMap& v_map, const PrefillParams& p, cudaStream_t stream);
+// 128-byte-swizzled boxes of 64 dims x 128 rows (q, v) or 64 rows (kn, kr), and of 16 rows for a request's
+// last tile; q, k_nope and v as (dim, head, row), k_rope as (dim, row).
+struct PrefillMaps {
+    CUtensorMap q, kn, kr, v, kn16, kr16, v16;
+};
+cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t stream);
 
 // Residual addition + RMS norm of bf16 rows.
 struct RmsNormParams {

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         int last_v = -1, last_r = -1, last_q = -1;  // the last fills issued
         const bool issuer = elect_one();
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, &ctl.abort)) != 0;
+            return __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort)) != 0;
         };
         const uint64_t pol_q = l2_policy_evict_first();
         // Tokens of a group share a page through L2; a single token reads it once.
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         const uint64_t r_desc = smem_desc_kmajor_sw128(sb + kOffR);
         const bool issuer = elect_one();
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, &ctl.abort)) != 0;
+            return __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort)) != 0;
         };
         Walk w(ctl, p);
         bool ok = true;
@@ -448,13 +448,15 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                     ok = ok && wait(&ctl.v_full[4 * buf + j], phase);
                     tc_fence_after_sync();
                     if (ok && issuer) {
-                        const uint64_t bd = v_desc + uint32_t(buf * (4 * kPairBytes >> 4));
+                        const uint64_t a = refreshed(q_desc + uint32_t(2 * j * (kSlabBytes >> 4)));
+                        const uint64_t bd = refreshed(v_desc + uint32_t((buf * 4 + j) * (kPairBytes >> 4)));
+                        const uint32_t d = refreshed(s_col);
 #pragma unroll
                         for (int hs = 0; hs < 2; ++hs)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16_ss(s_col, q_desc + uint32_t((2 * j + hs) * (kSlabBytes >> 4) + 2 * kk),
-                                             bd + uint32_t((2 * j + hs) * (kSlabBytes >> 4) + 2 * kk), kIdesc1,
+                                umma_bf16_ss(d, a + uint32_t(hs * (kSlabBytes >> 4) + 2 * kk),
+                                             bd + uint32_t(hs * (kSlabBytes >> 4) + 2 * kk), kIdesc1,
                                              (j | hs | kk) != 0 ? 1u : 0u);
                     }
                     __syncwarp();
@@ -462,10 +464,11 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 ok = ok && wait(&ctl.r_full[buf], phase);
                 tc_fence_after_sync();
                 if (ok && issuer) {
+                    const uint64_t a = refreshed(q_desc + uint32_t(8 * (kSlabBytes >> 4)));
+                    const uint64_t bd = refreshed(r_desc + uint32_t(buf * (kSlabBytes >> 4)));
+                    const uint32_t d = refreshed(s_col);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16_ss(s_col, q_desc + uint32_t(8 * (kSlabBytes >> 4) + 2 * kk),
-                                     r_desc + uint32_t(buf * (kSlabBytes >> 4) + 2 * kk), kIdesc1, 1u);
+                    for (int kk = 0; kk < 4; ++kk) umma_bf16_ss(d, a + 2u * kk, bd + 2u * kk, kIdesc1, 1u);
                     umma_commit(&ctl.s_full[buf]);
                     umma_commit(&ctl.r_empty[buf]);
                 }
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         const uint64_t v_desc = desc_mn_sw128(sb + kOffV, kSlabBytes);
         const bool issuer = elect_one();
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, &ctl.abort)) != 0;
+            return __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort)) != 0;
         };
         Walk w(ctl, p);
         bool ok = true;
@@ -523,13 +526,15 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                     __syncwarp();
                 }
                 if (issuer) {
-                    const uint64_t vd = v_desc + uint32_t(buf * (4 * kPairBytes >> 4));
                     // pair by pair, so that the first slots are free (and refilled) early
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        const uint64_t vd = refreshed(v_desc + uint32_t((buf * 4 + j) * (kPairBytes >> 4)));
+                        const uint64_t pd = refreshed(p_desc);
+                        const uint32_t d = refreshed(tmem + kColO + 64u * j);
                         const auto step = [&](int kk) {
-                            umma_bf16_ss(tmem + kColO + 64u * j, vd + uint32_t(j * (kPairBytes >> 4) + kk * (2048 >> 4)),
-                                         p_desc + 2u * kk, kIdesc2, (kk == 0 && fresh) ? 0u : 1u);
+                            umma_bf16_ss(d, vd + uint32_t(kk * (2048 >> 4)), pd + 2u * kk, kIdesc2,
+                                         (kk == 0 && fresh) ? 0u : 1u);
                         };
                         if (valid > 48) {
 #pragma unroll
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             uint8_t* dst = reinterpret_cast<uint8_t*>(p.o_part + part * kMlaHeads * kMlaDv);
             const int rounds = whole || w.last() ? 1 : 2;
             for (int r = 0; r < rounds && ok; ++r, ++staged) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.stage_full, uint32_t(staged & 1), &ctl.abort)) != 0;
+                ok = __all_sync(0xffffffffu, mbar_await(&ctl.stage_full, uint32_t(staged & 1), &ctl.abort)) != 0;
                 if (ok && issuer) {
                     if (whole) {
 #pragma unroll
@@ -635,8 +640,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 const int buf = n & 1;
                 // The previous block's product has read P (and O^T is at rest) long before the next scores
                 // are there: waiting for it first costs nothing.
-                bool ok = n == 0 || mbar_wait(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort);
-                ok = ok && mbar_wait(&ctl.s_full[buf], uint32_t((n >> 1) & 1), &ctl.abort);
+                bool ok = n == 0 || mbar_await(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort);
+                ok = ok && mbar_await(&ctl.s_full[buf], uint32_t((n >> 1) & 1), &ctl.abort);
                 ok = __all_sync(0xffffffffu, ok);
                 float x[16];
                 {
@@ -734,7 +739,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             }
             if (failed) break;
             // ---- the request's output (or partial)
-            bool ok = mbar_wait(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort);
+            bool ok = mbar_await(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -826,7 +831,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 #pragma unroll 1
                 for (int rd = 0; rd < rounds; ++rd) {
                     if (rd > 0) {
-                        ok = mbar_wait(&ctl.stage_free, uint32_t(halves & 1), &ctl.abort);
+                        ok = mbar_await(&ctl.stage_free, uint32_t(halves & 1), &ctl.abort);
                         ++halves;
                         if (!__all_sync(0xffffffffu, ok)) break;
                     }

@@ -16,8 +16,7 @@
 // bandwidth.
 //
 // Work.  A unit is 512 rows of a request and one head, whose two tiles share the
-// keys and values; or, where a request has at most 256 rows left, those rows and two
-// heads, one a tile.  Clusters are persistent: the units, longest requests and their
+// keys and values; or 256 rows and two heads, one a tile (see Cut).  Clusters are persistent: the units, longest requests and their
 // last rows first, are dealt out back and forth over the clusters that fit the
 // device, and the next unit's loads and first product run under the end of the one
 // before (a unit's own set-up and tail cost 9 us without that).  A scheduler warp
@@ -70,14 +69,15 @@ constexpr int kOffK = kOffQt + 2 * kQkSlabs * kSlabB;
 constexpr int kOffV = kOffK + kStages * kStageK;
 constexpr int kOffCtlP = kOffV + kStages * kStageV;
 constexpr int kThreadsP = 384;
-constexpr int kRegsSoftmax = 192, kRegsOther = 120;  // 8 x 192 + 4 x 120 = 12 x 168 a warp lane
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;  // 8 x 208 + 4 x 88 = 12 x 168 a warp lane
 constexpr uint32_t kTmemColsP = 512;
 constexpr uint32_t kColSP = 0;    // S / P of tile i at 128 i
 constexpr uint32_t kColOP = 256;  // O of tile i at 256 + 128 i
 constexpr float kRaiseLog2 = 20.0f;  // rounding is relative: weights may pass 1 by this much
 constexpr float kLn2P = 0.69314718055994531f;
 
-constexpr int kSortMost = 256;       // requests that are ordered by length (more: as they come)
+constexpr int kFewEntries = 768;     // see Cut: two heads a unit up to here (512: 146 us against 155), one above (1024: 80, 100)
+constexpr int kSortMost = 256;       // requests that are ordered by length, one a thread (more: as they come)
 constexpr int kInfoSlots = 4;
 constexpr int kInfoReaders = 11;     // every warp but the scheduler
 
@@ -204,16 +204,14 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
             : "memory");
         return ok != 0;
     };
+    uint64_t t0 = 0;
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (try_wait()) return true;
-    const uint64_t t0 = global_timer_ns();
-#pragma unroll 1
-    while (true) {
-        if (try_wait()) return true;
-        if (*abort) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) return false;
+    for (uint32_t n = 0; !try_wait(); ++n) {
+        if (n < 64) continue;
+        if (n == 64) t0 = global_timer_ns();
+        if (*abort || global_timer_ns() - t0 > kWaitLimitNs) return false;
     }
+    return true;
 }
 
 __device__ __forceinline__ void tmem2_alloc(uint32_t* dst_smem, uint32_t ncols) {
@@ -275,18 +273,26 @@ __device__ __forceinline__ void wait_landed_p(uint64_t* bar, uint32_t parity) {
     }
 }
 
-// Units of a request with n rows: blocks of 512 rows, one per head, and, where at most 256 rows are
-// left, one per two heads for those.
-__device__ __forceinline__ bool short_end(int n) { return n % kPrefillBlock > 0 && n % kPrefillBlock <= 2 * kTile; }
-__device__ __forceinline__ int long_blocks(int n) { return (n + 2 * kTile - 1) / kPrefillBlock; }
-__device__ __forceinline__ int units_of_rows(int n, int heads) {
-    return long_blocks(n) * heads + (short_end(n) ? (heads + 1) / 2 : 0);
-}
+// How a request's rows are cut.  Few entries: 256 rows at a time, two heads a unit, whose tiles run for
+// equally many key tiles (the halves of 512 rows do not, and a tile alone waits out its own softmax).
+// Many: 512 rows of one head, whose tiles share keys and values, and at most 256 rows left as above.
+struct Cut {
+    int rows, heads, pair_blocks, long_blocks;  // blocks of 256 rows for two heads, and of 512 for one
+    __device__ __forceinline__ Cut(const Request& r, int heads_) : rows(r.rows), heads(heads_) {
+        const bool few = r.live <= kFewEntries && heads_ > 1;
+        const int left = few ? r.rows : r.rows % kPrefillBlock;
+        pair_blocks = few || left <= 2 * kTile ? (left + 2 * kTile - 1) / (2 * kTile) : 0;
+        long_blocks = few ? 0 : (r.rows + 2 * kTile - 1) / kPrefillBlock;
+    }
+    __device__ __forceinline__ int pairs() const { return (heads + 1) / 2; }
+    __device__ __forceinline__ int units() const { return pair_blocks * pairs() + long_blocks * heads; }
+};
 
 __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kn_map,
                        const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap v_map,
-                       const PrefillParams p) {
+                       const __grid_constant__ CUtensorMap kn16_map, const __grid_constant__ CUtensorMap kr16_map,
+                       const __grid_constant__ CUtensorMap v16_map, const PrefillParams p) {
     extern __shared__ uint8_t smem_raw[];
     // Dynamic shared memory starts at the same offset in both CTAs, so the operands and barriers do too.
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -324,6 +330,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         tma_prefetch_map(&kn_map);
         tma_prefetch_map(&kr_map);
         tma_prefetch_map(&v_map);
+        tma_prefetch_map(&kn16_map);
+        tma_prefetch_map(&kr16_map);
+        tma_prefetch_map(&v16_map);
     }
     if (warp == 8) tmem2_alloc(&ctl.tmem_base, kTmemColsP);
     __syncwarp();
@@ -334,30 +343,33 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
 
     // The order of the requests (longest first, where they are few) and where their units start.
     uint32_t bad = 0;
-    const bool sorted = p.batch <= kSortMost;
-    if (sorted) {
-        for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
-            const Request r(p, b, bad);
-            ctl.key[b] = r.rows > 0 ? r.live : -1;
+    for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
+        const Request r(p, b, bad);
+        ctl.first[b] = Cut(r, p.heads).units();
+        ctl.order[b] = int16_t(b);
+        if (b < kSortMost) ctl.key[b] = r.rows > 0 ? r.live : -1;
+    }
+    if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
+    __syncthreads();
+    if (p.batch > 1 && p.batch <= kSortMost) {
+        const int b = threadIdx.x;
+        int at = 0, units = 0;
+        if (b < p.batch) {
+            const int key = ctl.key[b];
+            units = ctl.first[b];
+            for (int o = 0; o < p.batch; ++o) at += ctl.key[o] > key || (ctl.key[o] == key && o < b);
         }
         __syncthreads();
-        for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
-            const int key = ctl.key[b];
-            int at = 0;
-            for (int o = 0; o < p.batch; ++o) at += ctl.key[o] > key || (ctl.key[o] == key && o < b);
+        if (b < p.batch) {
             ctl.order[at] = int16_t(b);
+            ctl.first[at] = units;
         }
         __syncthreads();
     }
     const int per = (p.batch + kThreadsP - 1) / kThreadsP;
     const int i0 = min(int(threadIdx.x) * per, p.batch), i1 = min(i0 + per, p.batch);
     int mine = 0;
-    for (int i = i0; i < i1; ++i) {
-        const int b = sorted ? int(ctl.order[i]) : i;
-        if (!sorted) ctl.order[i] = int16_t(i);
-        mine += units_of_rows(Request(p, b, bad).rows, p.heads);
-    }
-    if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
+    for (int i = i0; i < i1; ++i) mine += ctl.first[i];
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -373,9 +385,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             total += ctl.warp_units[w];
         }
         for (int i = i0; i < i1; ++i) {
+            const int units = ctl.first[i];
             ctl.first[i] = before;
-            uint32_t ignored = 0;
-            before += units_of_rows(Request(p, int(ctl.order[i]), ignored).rows, p.heads);
+            before += units;
         }
         if (threadIdx.x == 0) ctl.total = total;
     }
@@ -385,17 +397,19 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     tc_fence_after_sync();
     const uint32_t tmem_base = ctl.tmem_base;
 
-    // A warp's next unit; false at the end of the list or when a role has given up.
+    // A warp's next unit, of which `read` takes what the warp needs; false at the end of the list or when
+    // a role has given up.
     int taken = 0;
-    const auto next_unit = [&](Unit& u) {
+    const auto next_unit = [&](auto&& read) {
         const int slot = taken & (kInfoSlots - 1);
-        const bool ok = mbar_wait(&ctl.info_full[slot], uint32_t(taken / kInfoSlots) & 1u, &ctl.abort);
+        const bool ok = mbar_await(&ctl.info_full[slot], uint32_t(taken / kInfoSlots) & 1u, &ctl.abort);
         if (!__all_sync(0xffffffffu, ok)) return false;
-        u = ctl.info[slot];
+        read(ctl.info[slot]);
+        const bool more = ctl.info[slot].last == 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.info_empty[slot]);
         ++taken;
-        return u.last == 0;
+        return more;
     };
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -421,21 +435,21 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                 uint32_t ignored = 0;
                 const Request rq(p, int(ctl.order[lo]), ignored);
                 int at = int(n) - ctl.first[lo];
-                const int ends = short_end(rq.rows) ? (p.heads + 1) / 2 : 0;
-                int block;
-                if (at < ends) {
-                    block = long_blocks(rq.rows);
-                    u.head = 2 * at;
+                const Cut cut(rq, p.heads);
+                // last rows (the longest) first: the blocks for two heads lie behind the long ones
+                if (at < cut.pair_blocks * cut.pairs()) {
+                    u.row0 = cut.long_blocks * kPrefillBlock + (cut.pair_blocks - 1 - at / cut.pairs()) * 2 * kTile;
+                    u.rows = min(rq.rows - u.row0, 2 * kTile);
+                    u.head = at % cut.pairs() * 2;
                     u.step_head = 1;
                 } else {
-                    at -= ends;
-                    block = long_blocks(rq.rows) - 1 - at / p.heads;
+                    at -= cut.pair_blocks * cut.pairs();
+                    u.row0 = (cut.long_blocks - 1 - at / p.heads) * kPrefillBlock;
+                    u.rows = min(rq.rows - u.row0, kPrefillBlock);
                     u.head = at % p.heads;
                     u.step_row = 2 * kTile;
                 }
-                u.row0 = block * kPrefillBlock;
                 u.q_row = rq.q0 + u.row0;
-                u.rows = min(rq.rows - u.row0, kPrefillBlock);
                 u.req_rows = rq.rows, u.seq = rq.seq, u.live = rq.live, u.kv0 = rq.kv0;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                     u.limit[i] = there ? rq.seen(u.row0 + to - 1, p.entry_tokens) : 0;
                 }
             }
-            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.info_empty[slot], (uint32_t(k / kInfoSlots) & 1u) ^ 1u,
+            ok = __all_sync(0xffffffffu, mbar_await(&ctl.info_empty[slot], (uint32_t(k / kInfoSlots) & 1u) ^ 1u,
                                                    &ctl.abort)) != 0;
             if (ok && lane == 0) {
                 ctl.info[slot] = u;
@@ -467,36 +481,53 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         int nq[2] = {0, 0};                       // q tiles
         uint32_t v_tail = 0, tail_phase = 0;      // value stages whose last fill counts on the tail barrier; its phases
         const auto wait = [&](uint64_t* bar, int fills) {  // the stage's `fills` earlier contents are used
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t(fills) & 1u) ^ 1u, &ctl.abort));
+            ok = ok && __all_sync(0xffffffffu, mbar_await(bar, (uint32_t(fills) & 1u) ^ 1u, &ctl.abort));
             return ok;
         };
         Unit u;
-        while (ok && next_unit(u)) {
+        while (ok && next_unit([&](const Unit& from) { u = from; })) {
             const int streams = u.streams(), nt = u.nt();
-            const auto load_q = [&](int i) {
+            const int limit = u.limit_max();
+            const auto load_q = [&](int i) {  // a CTA whose 128 rows are all past the block loads none
                 if (u.limit[i] == 0 || !wait(&ctl.q_empty[i], nq[i])) return;
                 if (issuer) {
                     const uint32_t bar = cluster_addr(&ctl.q_full[i], 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&ctl.q_full[i], uint32_t(2 * kQkSlabs * kSlabB));
+                    const int rows = u.rows - i * u.step_row;
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(&ctl.q_full[i], uint32_t((rows > kTile ? 2 : 1) * kQkSlabs * kSlabB));
+                    if (rank == 0 || rows > kTile) {
 #pragma unroll
-                    for (int s = 0; s < kQkSlabs; ++s)
-                        tma2_load_3d(sb + kOffQt + (i * kQkSlabs + s) * kSlabB, &q_map, bar, 64 * s,
-                                     u.head + i * u.step_head, u.q_row + i * u.step_row + rank * kTile, pol_q);
+                        for (int s = 0; s < kQkSlabs; ++s)
+                            tma2_load_3d(sb + kOffQt + (i * kQkSlabs + s) * kSlabB, &q_map, bar, 64 * s,
+                                         u.head + i * u.step_head, u.q_row + i * u.step_row + rank * kTile, pol_q);
+                    }
                 }
                 __syncwarp();
                 ++nq[i];
             };
+            // Of a request's last tile only what lies before the limit is loaded, 16 entries at a time; the
+            // rest of the stage keeps what it held (scores there are masked, value steps left out).
             const auto load_k = [&](int l, int j) {  // this CTA's 64 entries of tile j of stream l
                 const int st = nk % kStages;
                 if (!wait(&ctl.k_empty[st], nk / kStages)) return;
                 if (issuer) {
                     const uint32_t bar = cluster_addr(&ctl.k_full[st], 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&ctl.k_full[st], uint32_t(2 * kStageK));
+                    const int steps = min((limit - j * kTile + 15) >> 4, kTile / 16);  // of the tile, both CTAs
+                    if (rank == 0) mbar_arrive_expect_tx(&ctl.k_full[st], uint32_t(steps * (2 * kStageK / (kTile / 16))));
                     const uint32_t dst = sb + kOffK + st * kStageK;
                     const int row = u.kv0 + j * kTile + rank * (kTile / 2), head = u.head + l;
-                    tma2_load_3d(dst, &kn_map, bar, 0, head, row, pol_kv);
-                    tma2_load_3d(dst + kHalfB, &kn_map, bar, 64, head, row, pol_kv);
-                    tma2_load_2d(dst + 2 * kHalfB, &kr_map, bar, 0, row, pol_kv);
+                    const int mine = min(max(steps - rank * (kTile / 32), 0), kTile / 32);
+                    if (mine == kTile / 32) {
+                        tma2_load_3d(dst, &kn_map, bar, 0, head, row, pol_kv);
+                        tma2_load_3d(dst + kHalfB, &kn_map, bar, 64, head, row, pol_kv);
+                        tma2_load_2d(dst + 2 * kHalfB, &kr_map, bar, 0, row, pol_kv);
+                    } else {
+                        for (int s = 0; s < mine; ++s) {
+                            tma2_load_3d(dst + s * 2048, &kn16_map, bar, 0, head, row + 16 * s, pol_kv);
+                            tma2_load_3d(dst + kHalfB + s * 2048, &kn16_map, bar, 64, head, row + 16 * s, pol_kv);
+                            tma2_load_2d(dst + 2 * kHalfB + s * 2048, &kr16_map, bar, 0, row + 16 * s, pol_kv);
+                        }
+                    }
                 }
                 __syncwarp();
                 ++nk;
@@ -508,30 +539,41 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                 if (issuer) {
                     const uint32_t bar = end ? cluster_addr(&ctl.tail_landed[st], uint32_t(rank))
                                              : cluster_addr(&ctl.v_full[st], 0);
+                    const int steps = min((limit - j * kTile + 15) >> 4, kTile / 16);
+                    const uint32_t bytes = uint32_t(steps * (kStageV / (kTile / 16)));
                     if (end) {
-                        mbar_arrive_expect_tx(&ctl.tail_landed[st], uint32_t(kStageV));
+                        mbar_arrive_expect_tx(&ctl.tail_landed[st], bytes);
                         if (rank == 0) mbar_arrive(&ctl.v_full[st]);  // the stage's phases go on
                     } else if (rank == 0) {
-                        mbar_arrive_expect_tx(&ctl.v_full[st], uint32_t(2 * kStageV));
+                        mbar_arrive_expect_tx(&ctl.v_full[st], 2 * bytes);
                     }
-                    tma2_load_3d(sb + kOffV + st * kStageV, &v_map, bar, 64 * rank, u.head + l, u.kv0 + j * kTile,
-                                 pol_kv);
+                    const uint32_t dst = sb + kOffV + st * kStageV;
+                    const int row = u.kv0 + j * kTile, head = u.head + l;
+                    if (steps == kTile / 16) {
+                        tma2_load_3d(dst, &v_map, bar, 64 * rank, head, row, pol_kv);
+                    } else {
+                        for (int s = 0; s < steps; ++s)
+                            tma2_load_3d(dst + s * 2048, &v16_map, bar, 64 * rank, head, row + 16 * s, pol_kv);
+                    }
                 }
                 __syncwarp();
                 v_tail = (v_tail & ~(1u << st)) | (uint32_t(end) << st);
                 if (end) tail_phase ^= 1u << st;
                 ++nv;
             };
-            if (nt > 0) {
-                load_q(0);
-                load_k(0, 0);
-                load_q(1);
-                if (streams == 2) load_k(1, 0);
-                for (int j = 0; j < nt && ok; ++j) {  // in the order of use
-                    for (int l = 0; l < streams; ++l) load_v(l, j);
-                    if (j + 1 < nt)
-                        for (int l = 0; l < streams; ++l) load_k(l, j + 1);
+            // In the order of use: q and K(0) of each stream, then V(j) and K(j + 1) of each.  Rolled, so that
+            // every kind of load is in the code once.
+#pragma unroll 1
+            for (int j = -1; j < nt && nt > 0 && ok; ++j) {
+#pragma unroll 1
+                for (int l = 0; l < 2; ++l) {
+                    if (j < 0) load_q(l);
+                    if (j >= 0 && l < streams) load_v(l, j);
+                    if (j < 0 && l < streams) load_k(l, 0);
                 }
+                if (j >= 0 && j + 1 < nt)
+#pragma unroll 1
+                    for (int l = 0; l < streams; ++l) load_k(l, j + 1);
             }
         }
         if (lane == 0) {
@@ -566,15 +608,15 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         int nv = 0;
         uint32_t tail_phase = 0;  // per value stage
         bool ok = true;
-        Unit u;
-        while (ok && next_unit(u)) {
-            const int streams = u.streams(), nt = u.nt();
+        int streams = 0, limit = 0;
+        while (ok && next_unit([&](const Unit& from) { streams = from.streams(), limit = from.limit_max(); })) {
+            const int nt = (limit + kTile - 1) / kTile;
             nv += nt * streams;
-            if (!u.tail()) continue;
-            const int valid = u.limit_max() - (nt - 1) * kTile, fill = 16 - (valid & 15);
+            if ((limit & 15) == 0) continue;  // Unit::tail
+            const int valid = limit - (nt - 1) * kTile, fill = 16 - (valid & 15);
             for (int l = 0; l < streams && ok; ++l) {
                 const int st = (nv - streams + l) % kStages;
-                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.tail_landed[st], (tail_phase >> st) & 1u, &ctl.abort)) != 0;
+                ok = __all_sync(0xffffffffu, mbar_await(&ctl.tail_landed[st], (tail_phase >> st) & 1u, &ctl.abort)) != 0;
                 tail_phase ^= 1u << st;
                 if (!ok) break;
                 uint8_t* v = tiles + kOffV + st * kStageV;
@@ -599,7 +641,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         const bool issuer = elect_one();
         bool ok = true;
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, &ctl.abort));
+            ok = ok && __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort));
             return ok;
         };
         const auto commit = [&](uint64_t* bar) {
@@ -615,85 +657,71 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             }
         };
         Ring kr, vr;
-        uint32_t np[2] = {0, 0}, no[2] = {0, 0}, nq[2] = {0, 0}, tail_phase = 0;  // phases
+        uint32_t p_phase = 0, o_phase = 3, q_phase = 0, tail_phase = 0;  // bit i: of tile (stage) i
         // What the loop needs of a unit; fetched a unit ahead.
         struct Plan {
             int lim[2], n_of[2], nt;
             bool shared, tail;
         };
         const auto fetch = [&](Plan& w) {
-            Unit u;
-            if (!next_unit(u)) return false;
-            w.lim[0] = uniform(u.limit[0]), w.lim[1] = uniform(u.limit[1]);
+            int step = 0;
+            if (!next_unit([&](const Unit& from) {
+                    w.lim[0] = uniform(from.limit[0]), w.lim[1] = uniform(from.limit[1]);
+                    step = uniform(from.step_head);
+                }))
+                return false;
             w.n_of[0] = (w.lim[0] + kTile - 1) / kTile, w.n_of[1] = (w.lim[1] + kTile - 1) / kTile;
             w.nt = max(w.n_of[0], w.n_of[1]);
-            w.shared = uniform(u.step_head) == 0;
+            w.shared = step == 0;
             w.tail = (max(w.lim[0], w.lim[1]) & 15) != 0;
             return true;
+        };
+        const auto flip = [](uint32_t& phases, int i) {  // the tile's phase, and on to the next
+            const uint32_t phase = (phases >> i) & 1u;
+            phases ^= 1u << i;
+            return phase;
         };
         // S(tile i) = Q_i . K^T, keys in stage st
         const auto qk = [&](int i, int st, bool last) {
             if (issuer) {
-                const uint64_t a = q_desc + uint32_t(i * kQkSlabs * (kSlabB >> 4));
-                const uint64_t bd = k_desc + uint32_t(st * (kStageK >> 4));
+                const uint64_t a = refreshed(q_desc + uint32_t(i * kQkSlabs * (kSlabB >> 4)));
+                const uint64_t bd = refreshed(k_desc + uint32_t(st * (kStageK >> 4)));
+                const uint32_t d = refreshed(tmem + kColSP + 128u * i);
 #pragma unroll
                 for (int s = 0; s < kQkSlabs; ++s)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma2_bf16_ss(tmem + kColSP + 128u * i, a + uint32_t(s * (kSlabB >> 4) + 2 * kk),
+                        umma2_bf16_ss(d, a + uint32_t(s * (kSlabB >> 4) + 2 * kk),
                                       bd + uint32_t(s * (kHalfB >> 4) + 2 * kk), kIdescQk, (s | kk) != 0 ? 1u : 0u);
                 umma2_commit(&ctl.s_full[i]);
                 if (last) umma2_commit(&ctl.q_empty[i]);
             }
             __syncwarp();
         };
-        // O(tile i) += P_i . V, values in stage st, over the 16-entry steps below the tile's limit
-        const auto pv = [&](int i, int j, int st, int lim, bool last) {
-            const int steps = min((lim - j * kTile + 15) >> 4, kTile / 16);
-            if (issuer) {
-                const uint64_t bd = v_desc + uint32_t(st * (kStageV >> 4));
-                const auto step = [&](int kk) {
-                    umma2_bf16_ts(tmem + kColOP + 128u * i, tmem + kColSP + 128u * i + 8u * kk, bd + 128u * kk, kIdescPv,
-                                  (j | kk) != 0 ? 1u : 0u);
-                };
-                if (steps == kTile / 16) {
+        // O(tile i) (+)= P_i . V, values in stage st
+        const auto pv = [&](int i, int st, int steps, bool first) {
+            const uint64_t bd = refreshed(v_desc + uint32_t(st * (kStageV >> 4)));
+            const uint32_t d = refreshed(tmem + kColOP + 128u * i), a = refreshed(tmem + kColSP + 128u * i);
+            const auto step = [&](int kk) {
+                umma2_bf16_ts(d, a + 8u * kk, bd + 128u * kk, kIdescPv, kk == 0 && first ? 0u : 1u);
+            };
+            if (steps == kTile / 16) {
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk) step(kk);
-                } else {
+                for (int kk = 0; kk < kTile / 16; ++kk) step(kk);
+            } else {
 #pragma unroll 1
-                    for (int kk = 0; kk < steps; ++kk) step(kk);
-                }
-                if (last) umma2_commit(&ctl.o_full[i]);
-            }
-            __syncwarp();
-        };
-        // A unit's first scores of tile i: its S is free once the products issued so far have read P.
-        const auto first_scores = [&](const Plan& w, int i) {
-            if (!ok || w.n_of[i] == 0) return;
-            if (!w.shared || i == 0 || w.n_of[0] == 0) wait(&ctl.k_full[kr.st], kr.phase);
-            wait(&ctl.q_full[i], nq[i] & 1u);
-            ++nq[i];
-            tc_fence_after_sync();
-            if (ok) qk(i, kr.st, w.n_of[i] == 1);
-            if (ok && (!w.shared || i == 1)) {
-                commit(&ctl.k_empty[kr.st]);
-                kr.next();
+                for (int kk = 0; kk < steps; ++kk) step(kk);
             }
         };
-        Plan w, next;
-        bool more = fetch(w);
+        Plan w = {}, next = {};
+        bool more = fetch(next);
         if (rank == 0) {
-            if (more)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) first_scores(w, i);
-            while (ok && more) {
-                if (w.nt == 0) {
-                    more = fetch(next);
-                    if (more)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) first_scores(next, i);
-                }
-                int j = 0;
+            // One round per key tile: the products of both query tiles with it, each followed by that
+            // tile's next scores, be they this unit's or (its keys are all used) the next one's.  The first
+            // round is of no unit and has scores only.  Rolled over the tiles: this code runs once or twice
+            // a unit where units are short, and out of the instruction cache it is twice as slow.
+            int j = 0;
+            while (ok && (w.nt > 0 || more)) {
                 // Tiles that both query tiles see whole, with another one to come: the long part of a long
                 // unit, as straight as it can be (an MMA issued late is tensor core time lost).
                 const int whole = w.shared ? min(w.n_of[0], w.n_of[1]) - 1 : 0;
@@ -702,20 +730,12 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                     wait(&ctl.v_full[vr.st], vr.phase);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        if (j == 0) {
-                            wait(&ctl.o_empty[i], (no[i] & 1u) ^ 1u);
-                            ++no[i];
-                        }
+                        if (j == 0) wait(&ctl.o_empty[i], flip(o_phase, i));
                         if (i == 0) wait(&ctl.k_full[kr.st], kr.phase);
-                        wait(&ctl.p_full[i], np[i] & 1u);
-                        ++np[i];
+                        wait(&ctl.p_full[i], flip(p_phase, i));
                         tc_fence_after_sync();
                         if (ok && issuer) {
-                            const uint64_t bd = v_desc + uint32_t(vr.st * (kStageV >> 4));
-#pragma unroll
-                            for (int kk = 0; kk < kTile / 16; ++kk)
-                                umma2_bf16_ts(tmem + kColOP + 128u * i, tmem + kColSP + 128u * i + 8u * kk, bd + 128u * kk,
-                                              kIdescPv, (j | kk) != 0 ? 1u : 0u);
+                            pv(i, vr.st, kTile / 16, j == 0);
                             if (i == 1) umma2_commit(&ctl.v_empty[vr.st]);
                         }
                         if (ok) qk(i, kr.st, j + 2 == w.n_of[i]);
@@ -724,61 +744,60 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                     kr.next();
                     vr.next();
                 }
+                const bool end = j >= w.nt - 1;
+                if (end && w.nt > 0) more = fetch(next);
+                // Whose scores come next: of tile j + 1 of this unit, or of the first of the next one.
+                const int first_n = more ? next.n_of[0] : 0, second_n = more ? next.n_of[1] : 0;
+                const bool s_shared = end ? next.shared : w.shared;
+                bool have_k = false, have_v = false;
 #pragma unroll 1
-                for (; j < w.nt && ok; ++j) {
-                    const bool end = j == w.nt - 1;
-                    bool have_k = false, have_v = false;
-                    if (end) more = fetch(next);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (ok && j < w.n_of[i]) {
-                            if (!w.shared || !have_v) {
-                                if (w.tail && end) {
-                                    ok = __all_sync(0xffffffffu,
-                                                    mbar_wait_cluster(&ctl.tail_ready[vr.st],
-                                                                      (tail_phase >> vr.st) & 1u, &ctl.abort)) != 0;
-                                    tail_phase ^= 1u << vr.st;
-                                } else {
-                                    wait(&ctl.v_full[vr.st], vr.phase);
-                                }
-                            }
-                            have_v = true;
-                            if (j == 0) {
-                                wait(&ctl.o_empty[i], (no[i] & 1u) ^ 1u);
-                                ++no[i];
-                            }
-                            wait(&ctl.p_full[i], np[i] & 1u);
-                            ++np[i];
-                            tc_fence_after_sync();
-                            if (ok) pv(i, j, vr.st, w.lim[i], j + 1 == w.n_of[i]);
-                            if (ok && !w.shared) {
-                                commit(&ctl.v_empty[vr.st]);
-                                vr.next();
-                            }
+                for (int i = 0; i < 2; ++i) {
+                    const int n = i ? w.n_of[1] : w.n_of[0], lim = i ? w.lim[1] : w.lim[0];
+                    if (ok && j < n) {
+                        if (!w.shared || !have_v) {
+                            if (w.tail && end)
+                                ok = __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.tail_ready[vr.st],
+                                                                               flip(tail_phase, vr.st), &ctl.abort)) != 0;
+                            else
+                                wait(&ctl.v_full[vr.st], vr.phase);
                         }
-                        if (ok && w.shared && i == 1) {
-                            commit(&ctl.v_empty[vr.st]);
-                            vr.next();
+                        have_v = true;
+                        if (j == 0) wait(&ctl.o_empty[i], flip(o_phase, i));
+                        wait(&ctl.p_full[i], flip(p_phase, i));
+                        tc_fence_after_sync();
+                        if (ok && issuer) {
+                            pv(i, vr.st, min((lim - j * kTile + 15) >> 4, kTile / 16), j == 0);
+                            if (j + 1 == n) umma2_commit(&ctl.o_full[i]);
                         }
-                        if (ok && j + 1 < w.n_of[i]) {
-                            if (!w.shared || !have_k) wait(&ctl.k_full[kr.st], kr.phase);
-                            have_k = true;
-                            tc_fence_after_sync();
-                            if (ok) qk(i, kr.st, j + 2 == w.n_of[i]);
-                            if (ok && !w.shared) {
-                                commit(&ctl.k_empty[kr.st]);
-                                kr.next();
-                            }
-                        }
-                        // All keys of this unit are used: on to the next one's.
-                        if (end && more) first_scores(next, i);
+                        __syncwarp();
                     }
-                    if (ok && w.shared && !end) {
+                    if (ok && w.nt > 0 && (w.shared ? i == 1 : j < n)) {
+                        commit(&ctl.v_empty[vr.st]);
+                        vr.next();
+                    }
+                    const int to_come = end ? (i ? second_n : first_n) : n - (j + 1);  // key tiles
+                    if (ok && to_come > 0) {
+                        if (!s_shared || !have_k) wait(&ctl.k_full[kr.st], kr.phase);
+                        have_k = true;
+                        if (end) wait(&ctl.q_full[i], flip(q_phase, i));
+                        tc_fence_after_sync();
+                        if (ok) qk(i, kr.st, to_come == 1);
+                    }
+                    if (ok && have_k && (s_shared ? i == 1 : to_come > 0)) {
                         commit(&ctl.k_empty[kr.st]);
                         kr.next();
                     }
                 }
-                w = next;
+                ++j;
+                if (end) {
+                    j = 0;
+                    if (more) {
+                        w = next;
+                        if (w.nt == 0) more = fetch(next);
+                    } else {
+                        w.nt = 0;
+                    }
+                }
             }
         } else {
             while (more) more = fetch(w);  // the leader issues for both
@@ -806,7 +825,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         bool failed = false;
         uint32_t ns = 0, no = 0;  // score tiles and outputs so far
         Unit u;
-        bool more = next_unit(u);
+        const auto copy = [&](const Unit& from) { u = from; };
+        bool more = next_unit(copy);
         while (more) {
             const int head = u.head + i * u.step_head;
             const bool live_row = i * u.step_row + r < u.rows && head < p.heads;
@@ -821,7 +841,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll 1
             for (int j = 0; j < ntiles; ++j, ++ns) {
-                const bool ok = mbar_wait(&ctl.s_full[i], ns & 1u, &ctl.abort);
+                const bool ok = mbar_await(&ctl.s_full[i], ns & 1u, &ctl.abort);
                 if (!__all_sync(0xffffffffu, ok)) {
                     failed = true;
                     break;
@@ -904,23 +924,25 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                         for (int k = 0; k < 32; ++k)
                             if (32 * c + k >= here) v[k] = 0xFF800000u;  // -inf
                     };
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < chunks; ++c) {
-                        chunk(c);
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2)
-                            mx = max3(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                    }
-                    raise(mx * c2);
-                    const float nm = m == -INFINITY ? 0.f : -m;
+                    float mx = -INFINITY, nm = 0.f;
                     // P's chunk c covers S's columns [16 c, 16 c + 16): behind what later chunks still read.
 #pragma unroll 1
-                    for (int c = 0; c < chunks; ++c) {
+                    for (int it = 0; it < 2 * chunks; ++it) {
+                        const int c = it < chunks ? it : it - chunks;
                         chunk(c);
-                        uint32_t pk[16];
-                        weights(v, pk, 0, make_float2(nm, nm));
-                        tmem_st_x16(s_addr + 16u * c, pk);
+                        if (it < chunks) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2)
+                                mx = max3(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                            if (it == chunks - 1) {
+                                raise(mx * c2);
+                                nm = m == -INFINITY ? 0.f : -m;
+                            }
+                        } else {
+                            uint32_t pk[16];
+                            weights(v, pk, 0, make_float2(nm, nm));
+                            tmem_st_x16(s_addr + 16u * c, pk);
+                        }
                     }
                 }
                 tmem_st_wait();
@@ -929,7 +951,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                 if (lane == 0) mbar_arrive_remote(p_bar);
             }
             if (failed) break;
-            more = next_unit(u);
+            more = next_unit(copy);
             // ---- output
             __nv_bfloat16* o_row = reinterpret_cast<__nv_bfloat16*>(p.out) + (token * p.heads + head) * kPrefillDv;
             if (ntiles == 0) {  // rows that see nothing
@@ -941,41 +963,43 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                 __syncwarp();
                 continue;
             }
-            const bool ok = mbar_wait(&ctl.o_full[i], no & 1u, &ctl.abort);
+            const bool ok = mbar_await(&ctl.o_full[i], no & 1u, &ctl.abort);
             if (!__all_sync(0xffffffffu, ok)) {
                 failed = true;
                 break;
             }
             ++no;
             tc_fence_after_sync();
-            uint32_t o[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(o_addr + 32u * c, o[c]);
             const float l = l2.x + l2.y;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             if (live_row) p.lse[token * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2P : -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(o_addr + 32u * c, o);
+                tmem_ld_wait(o);
+                if (c == 3) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(o_bar);  // O may be overwritten
+                }
+                if (live_row) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_wait(o[c]);
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(o_bar);  // O may be overwritten
-            if (live_row) {
+                    for (int h = 0; h < 2; ++h) {  // a whole sector a lane
+                        uint32_t w[8];
 #pragma unroll
-                for (int q4 = 0; q4 < 8; ++q4) {  // a whole sector a lane
-                    uint32_t w[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int c = q4 >> 1, e = 16 * (q4 & 1) + 2 * k;
-                        const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[c][e]) * inv,
-                                                                       __uint_as_float(o[c][e + 1]) * inv);
-                        w[k] = *reinterpret_cast<const uint32_t*>(&v);
-                    }
-                    if (p.out_aligned32) {
-                        st_global_v8(o_row + 16 * q4, w);
-                    } else {
-                        uint4* d = reinterpret_cast<uint4*>(o_row + 16 * q4);
-                        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        for (int k = 0; k < 8; ++k) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[16 * h + 2 * k]) * inv,
+                                                                           __uint_as_float(o[16 * h + 2 * k + 1]) * inv);
+                            w[k] = *reinterpret_cast<const uint32_t*>(&v);
+                        }
+                        __nv_bfloat16* d = o_row + 32 * c + 16 * h;
+                        if (p.out_aligned32) {
+                            st_global_v8(d, w);
+                        } else {
+                            reinterpret_cast<uint4*>(d)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4*>(d)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
                     }
                 }
             }
@@ -996,8 +1020,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
 
 }  // namespace
 
-cudaError_t launch_mla_prefill(const CUtensorMap& q_map, const CUtensorMap& kn_map, const CUtensorMap& kr_map,
-                               const CUtensorMap& v_map, const PrefillParams& p, cudaStream_t stream) {
+cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t stream) {
     static SmemLimitOnce smem_limit;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1028,7 +1051,7 @@ cudaError_t launch_mla_prefill(const CUtensorMap& q_map, const CUtensorMap& kn_m
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     const int64_t most = int64_t(p.slots) * p.heads;  // at least the number of units
     cfg.gridDim = dim3(2u * unsigned(most < fit ? most : fit));
-    return cudaLaunchKernelEx(&cfg, mla_prefill_kernel, q_map, kn_map, kr_map, v_map, p);
+    return cudaLaunchKernelEx(&cfg, mla_prefill_kernel, m.q, m.kn, m.kr, m.v, m.kn16, m.kr16, m.v16, p);
 }
 
 }  // namespace dsa

@@ -25,8 +25,18 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 // tcgen05.mma takes its operands from uniform registers.  In a branch of one lane, reached by
 // conditions the compiler cannot prove uniform, every operand is moved there per instruction (about 90
 // cycles an MMA in all); a warp that runs the loop together on values made uniform here, and lets one
-// elected lane issue, avoids that.
+// elected lane issue, avoids that.  Descriptors that do not change in a loop are another trap: their sums
+// with each instruction's offset are computed once, kept in ordinary registers and moved back each
+// time (10 to 30 instructions an MMA); `refreshed` hides that they do not change (3 instructions).
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+__device__ __forceinline__ uint32_t refreshed(uint32_t x) {
+    asm volatile("" : "+r"(x));
+    return x;
+}
+__device__ __forceinline__ uint64_t refreshed(uint64_t desc) {
+    return (desc & ~uint64_t(0xFFFFFFFFu)) | refreshed(uint32_t(desc));
+}
 
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -84,6 +94,20 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
         if (*abort) return false;
         if (global_timer_ns() - t0 > kWaitLimitNs) return false;
     }
+}
+
+// The same in less code: in a kernel with many waits the loops above are a good part of its instructions,
+// and what a role runs once a request then comes from far out of the instruction caches.
+__device__ __forceinline__ bool mbar_await(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+    const uint32_t a = smem_u32(bar);
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 0; !mbar_try_wait(a, parity); ++n) {
+        if (n < 64) continue;  // the timer is slow to read
+        if (n == 64) t0 = global_timer_ns();
+        if (*abort || global_timer_ns() - t0 > kWaitLimitNs) return false;
+    }
+    return true;
 }
 
 // Make this thread's ordinary shared-memory stores visible to the async proxy
