@@ -331,12 +331,12 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 ctl.first_start = u;
             }
             if (hi >= u && hi < u + n) ctl.hi = settled(hi);
-            int2 g = make_int2(0, 0);  // the first and last range that hold its blocks, for the merge
-            if (nb > kMlaWholeBlocks) {
-                g = make_int2(ranges.of(u + kMlaSegUnits), ranges.of(u + n - 1));
-                if (g.y > g.x && g.x + 1 == group) ctl.cut = b;
-            }
-            if (group == 0 && token == 0) p.plan[b] = g;
+            // Is this the request's second range?  Its first block lies in the one before.
+            if (nb > kMlaWholeBlocks && lo > u + kMlaSegUnits && lo < u + n && ranges.cut(group - 1) <= u + kMlaSegUnits)
+                ctl.cut = b;
+            if (group == 0 && token == 0)  // the first and last range that hold its blocks, for the merge
+                p.plan[b] = nb > kMlaWholeBlocks ? make_int2(ranges.of(u + kMlaSegUnits), ranges.of(u + n - 1))
+                                                 : make_int2(0, 0);
             u += n;
         }
     }
@@ -884,16 +884,18 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 }
 
 // o[r] = sum_i exp(lse_i - lse) o_i over the partials of a split request, lse = log sum_i exp(lse_i).
-// 512 threads, 128 of them per 512 dims: four heads a CTA, or (few rows, each split many ways) one head
-// whose partials go to the four quarters in turn.  Grid (heads, requests or cuts x tokens).
+// 512 threads.  128 of them per 512 dims, four heads a CTA; or (kOneHead: few rows, each split many ways)
+// 64 per 256 dims, half a head a CTA, whose partials go to the eight groups in turn.  Grid (heads / 4 or
+// heads x 2, requests or cuts x tokens).
 template <bool kOneHead>
 __global__ void __launch_bounds__(512) mla_dense_merge_kernel(const MlaDenseParams p) {
     __shared__ float wgt[kOneHead ? 1 : 4][kMlaMaxGroups];
-    __shared__ float4 acc_s[kOneHead ? 3 : 1][128];
+    __shared__ float4 acc_s[kOneHead ? 7 : 1][64];
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
-    const int quarter = threadIdx.x >> 7, d4 = threadIdx.x & 127;
-    const int h = kOneHead ? int(blockIdx.x) : int(blockIdx.x) * 4 + quarter;
+    const int quarter = threadIdx.x >> (kOneHead ? 6 : 7);
+    const int d4 = kOneHead ? (int(blockIdx.x) & 1) * 64 + (threadIdx.x & 63) : threadIdx.x & 127;
+    const int h = kOneHead ? int(blockIdx.x) >> 1 : int(blockIdx.x) * 4 + quarter;
     const int token = int(blockIdx.y) % p.tokens;
     const int b = p.merge_by_cut ? p.cuts[blockIdx.y / p.tokens] : int(blockIdx.y) / p.tokens;
     if (b < 0) return;
@@ -921,23 +923,25 @@ __global__ void __launch_bounds__(512) mla_dense_merge_kernel(const MlaDensePara
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         for (int i = lane; i < S; i += 32) w[i] *= inv;
-        if (lane == 0) p.lse[row * kMlaHeads + h] = mx == -INFINITY ? -INFINITY : mx + logf(sum);
+        if (lane == 0 && (!kOneHead || (blockIdx.x & 1) == 0))
+            p.lse[row * kMlaHeads + h] = mx == -INFINITY ? -INFINITY : mx + logf(sum);
     }
     __syncthreads();
     const float* const w = wgt[kOneHead ? 0 : quarter];
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int i = kOneHead ? quarter : 0; i < S; i += kOneHead ? 4 : 1) {
+    for (int i = kOneHead ? quarter : 0; i < S; i += kOneHead ? 8 : 1) {
         const float4 v = *reinterpret_cast<const float4*>(p.o_part + (part(i) * kMlaHeads + h) * kMlaDv + 4 * d4);
         acc.x = fmaf(w[i], v.x, acc.x), acc.y = fmaf(w[i], v.y, acc.y);
         acc.z = fmaf(w[i], v.z, acc.z), acc.w = fmaf(w[i], v.w, acc.w);
     }
     if constexpr (kOneHead) {
-        if (quarter > 0) acc_s[quarter - 1][d4] = acc;
+        if (quarter > 0) acc_s[quarter - 1][threadIdx.x & 63] = acc;
         __syncthreads();
         if (quarter > 0) return;
-        for (int q = 0; q < 3; ++q) {
-            const float4 v = acc_s[q][d4];
+#pragma unroll
+        for (int q = 0; q < 7; ++q) {
+            const float4 v = acc_s[q][threadIdx.x & 63];
             acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
         }
     }
@@ -973,7 +977,7 @@ cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map
     // many ways: more threads per row read more partials at a time.
     const int rows = (p.merge_by_cut ? p.groups : p.batch) * p.tokens;
     const bool one_head = rows <= 16;
-    cfg.gridDim = dim3(one_head ? kMlaHeads : kMlaHeads / 4, unsigned(rows));
+    cfg.gridDim = dim3(one_head ? kMlaHeads * 2 : kMlaHeads / 4, unsigned(rows));
     cfg.blockDim = dim3(512);
     cfg.dynamicSmemBytes = 0;
     return one_head ? cudaLaunchKernelEx(&cfg, mla_dense_merge_kernel<true>, p)
