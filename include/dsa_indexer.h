@@ -416,12 +416,13 @@ DSA_API dsa_status_t dsa_mla_prefill(const void *q, int64_t q_row_stride, int64_
  * dsa_indexer_qw_proj, 8-bit rows for an 8-bit product), or index keys in the
  * fp8 cache's format.  Per row of d elements, in fp32:
  *     h = x + residual (x where residual_opt is NULL)
- *     y = h / sqrt(mean(h^2) + eps) * weight
+ *     y = h * weight / sqrt(mean(h^2) + eps)           (the product first)
  *     residual_out = h,  out = y                       (bf16, one rounding each)
  *     scale_G = max_G |y| / 448,  code = y / scale_G    (e4m3, one rounding)
  * with one scale per group of 64 or 128 consecutive elements (the last group of
  * a row may be short) or per row (group 0).  A group whose maximum is 0 (or so
- * small that the scale is) has scale 1.  For finite rows every scale is positive and finite.
+ * small that the scale is) has scale 1.  Where h * weight and the sum of squares are
+ * finite in fp32, every scale is positive and finite.
  *
  *   x            bf16 [rows, d], rows x_stride >= 0 elements apart (a view of
  *                wider rows, or 0: the same row every time)
@@ -430,7 +431,8 @@ DSA_API dsa_status_t dsa_mla_prefill(const void *q, int64_t q_row_stride, int64_
  *   out          bf16 [rows, d] (dsa_rmsnorm_fp8: may be NULL)
  *   codes        uint8 [rows, d];  scales fp32 [rows, ceil(d / group)] or [rows]
  * No alignment beyond the element's is asked for; 16-byte aligned rows (and a
- * d that is a multiple of 8) are faster.  out and residual_out may be x or
+ * d that is a multiple of 8) are faster.  The aligned 16-byte blocks in which a
+ * row's ends lie are read whole; nothing beside the outputs is written.  out and residual_out may be x or
  * residual themselves (x only with x_stride == d); otherwise outputs overlap
  * neither inputs nor each other.  rows = 0 launches nothing.  1 <= d <= 32768
  * (above: DSA_ERR_UNSUPPORTED), rows < 2^31, eps finite and >= 0.  The result of

@@ -213,6 +213,7 @@ struct RmsNormParams {
     int32_t log2_threads;     // of row_threads, where several rows share a CTA
     int32_t ahead;            // how many rows ahead a CTA fetches into L2 (set by the launch)
     float eps;
+    float inv_d;              // 1 / d (set by the launch)
 };
 // align: 32, 16 or 2, the boundary in bytes of every 16-element unit (codes: half of it); d is a multiple
 // of align / 2.

@@ -101,6 +101,43 @@ def test_norm_strided_rows(gpu_lib, d, stride):
         check_bf16(out, reference(x, None, w)[1], f"start {start}")
 
 
+@pytest.mark.parametrize("d, offset", [(1, 1), (7, 2), (24, 1), (65, 3), (72, 5), (333, 7), (1000, 4), (1037, 1), (1040, 3),
+                                       (7001, 6), (8192, 1), (9001, 5), (16403, 2)])
+def test_norm_offset_arrays(gpu_lib, d, offset):
+    """Arrays that start anywhere, each at its own offset: the same values, and nothing beside them."""
+    import torch
+    rows = 37
+    x, r, w = rows_of(24, rows, d), rows_of(25, rows, d, scale=2.0), rows_of(26, 1, d)[0]
+    h, y = reference(x, r, w)
+    u8 = torch.uint8
+    buffers = {}
+
+    def at(name, k, data=None, dtype=torch.bfloat16):
+        buf = torch.full((rows * d + 64,), 0x5A, dtype=u8, device="cuda").to(dtype) if dtype is u8 else \
+            torch.full((rows * d + 64,), 77.0, dtype=dtype, device="cuda")
+        buffers[name] = (buf, k, rows * d)
+        view = buf[k:k + rows * d].view(rows, d)
+        if data is not None:
+            view.copy_(data)
+        return view
+
+    args = at("x", offset, x), torch.cat([w[:1], w]).cuda()[1:], EPS
+    kw = dict(residual=at("r", (3 * offset) % 16, r), residual_out=at("ro", (5 * offset + 1) % 16))
+    for group in (-1, 0, 64, 128):
+        out = at("out", (7 * offset + 2) % 16)
+        if group < 0:
+            gpu_lib.dsa_rmsnorm(*args, out=out, **kw)
+        else:
+            codes = at("codes", (11 * offset + 3) % 16, dtype=u8)
+            _, scales, _, _ = gpu_lib.dsa_rmsnorm_fp8(*args, group, out=out, codes=codes, **kw)
+            check_codes(codes, scales, y, group)
+        check_bf16(out, y, "out")
+        assert torch.equal(kw["residual_out"].cpu(), (x.float() + r.float()).to(torch.bfloat16))
+        for name, (buf, k, n) in buffers.items():
+            beside = torch.cat([buf[:k], buf[k + n:]])
+            assert torch.all(beside == (0x5A if buf.dtype is u8 else 77.0)), name
+
+
 def test_norm_broadcast_row(gpu_lib):
     """Stride 0: the same row every time."""
     x, w = rows_of(9, 1, 640), rows_of(10, 1, 640)[0]
