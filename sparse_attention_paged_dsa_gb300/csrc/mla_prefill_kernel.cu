@@ -913,9 +913,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                         tmem_st_x32(s_addr + 32u * h, pk);
                     }
                 } else {
-                    // A tile that some row sees in part: 32 columns at a time, read twice; the products read
-                    // none past the tile's limit, so chunks that start behind it are left out.
-                    const int chunks = min((limit - j * kTile + 31) >> 5, 4);
+                    // A tile that some row sees in part: 32 columns at a time, read twice (all of them at once
+                    // do not fit beside their masks).  Columns that no row of the warp sees are not read, and
+                    // their weights are 0 as far as the tile's limit (the products read none past it).
+                    const int most = __reduce_max_sync(0xffffffffu, here);
+                    const int chunks = min((limit - j * kTile + 31) >> 5, 4), seen = min(max(most + 31, 0) >> 5, chunks);
                     uint32_t v[32];
                     const auto chunk = [&](int c) {
                         tmem_ld_32x32b_x32(s_addr + 32u * c, v);
@@ -927,14 +929,14 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                     float mx = -INFINITY, nm = 0.f;
                     // P's chunk c covers S's columns [16 c, 16 c + 16): behind what later chunks still read.
 #pragma unroll 1
-                    for (int it = 0; it < 2 * chunks; ++it) {
-                        const int c = it < chunks ? it : it - chunks;
+                    for (int it = 0; it < 2 * seen; ++it) {
+                        const int c = it < seen ? it : it - seen;
                         chunk(c);
-                        if (it < chunks) {
+                        if (it < seen) {
 #pragma unroll
                             for (int k = 0; k < 32; k += 2)
                                 mx = max3(mx, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                            if (it == chunks - 1) {
+                            if (it == seen - 1) {
                                 raise(mx * c2);
                                 nm = m == -INFINITY ? 0.f : -m;
                             }
@@ -943,6 +945,13 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                             weights(v, pk, 0, make_float2(nm, nm));
                             tmem_st_x16(s_addr + 16u * c, pk);
                         }
+                    }
+#pragma unroll 1
+                    for (int c = seen; c < chunks; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) pk[k] = 0;
+                        tmem_st_x16(s_addr + 16u * c, pk);
                     }
                 }
                 tmem_st_wait();
