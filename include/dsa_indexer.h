@@ -383,7 +383,10 @@ DSA_API dsa_status_t dsa_mla_decode(const void *q, const void *kv_cache, int64_t
  *           multiples of 8 below 2^39 elements.
  *   cu_q, cu_kv int32 [batch + 1], non-decreasing; seq_lens int32 [batch]
  *   out     bf16 [q_rows, heads, 128] 16-byte aligned, lse fp32 [q_rows, heads], both contiguous
- *   workspace >= DSA_PREFILL_WORKSPACE_BYTES, 256-byte aligned, zeroed once: the error word
+ *   workspace >= DSA_PREFILL_WORKSPACE_BYTES, 256-byte aligned, header zeroed once (the error
+ *           word).  With dsa_mla_prefill_workspace_size() bytes (sized for the current
+ *           device; any larger one will do) few rows over many entries are split along the
+ *           entries and joined by log-sum-exp.
  *
  * 1 <= batch <= 1024, 1 <= heads <= 128, 1 <= entry_tokens <= 64, sm_scale finite
  * and >= 0, q_rows and kv_rows below 2^31 (0 rows: nothing is launched; 0 entries: every
@@ -392,8 +395,10 @@ DSA_API dsa_status_t dsa_mla_decode(const void *q, const void *kv_cache, int64_t
  * whatever they hold; q and the entries that some row of a request sees must be
  * finite.  Device data out of contract (DSA_DEVERR_BAD_RANGE, DSA_DEVERR_SEQ_LEN_CLAMPED)
  * is never dereferenced: such rows are left out, or see the entries that there are.
- * A row's result depends on its request alone.  The launch depends on (q_rows,
- * batch, heads).  Asynchronous on `stream`, allocates nothing, capture-safe.
+ * Where requests are split, the order of a row's sums depends on the batch's row counts and
+ * lengths; otherwise a row's result depends on its request alone.  For the same arguments
+ * results are the same bits.  The launch depends on (q_rows, kv_rows, batch,
+ * heads, workspace_bytes).  Asynchronous on `stream`, allocates nothing, capture-safe.
  */
 #define DSA_PREFILL_QK_DIM 192
 #define DSA_PREFILL_NOPE_DIM 128
@@ -401,6 +406,8 @@ DSA_API dsa_status_t dsa_mla_decode(const void *q, const void *kv_cache, int64_t
 #define DSA_PREFILL_V_DIM 128
 #define DSA_PREFILL_MAX_HEADS 128
 #define DSA_PREFILL_WORKSPACE_BYTES 256
+
+DSA_API size_t dsa_mla_prefill_workspace_size(void);
 
 DSA_API dsa_status_t dsa_mla_prefill(const void *q, int64_t q_row_stride, int64_t q_head_stride, const void *k_nope,
                                      int64_t k_row_stride, int64_t k_head_stride, const void *k_rope,

@@ -81,6 +81,8 @@ def load():
     lib.dsa_mla_decode_workspace_size.restype = sz
     lib.dsa_mla_decode.argtypes = [p, p, i64, p, p, i32, i32, i64, ctypes.c_float, p, p, p, sz, p]
     lib.dsa_mla_decode.restype = st
+    lib.dsa_mla_prefill_workspace_size.argtypes = []
+    lib.dsa_mla_prefill_workspace_size.restype = sz
     lib.dsa_mla_prefill.argtypes = [p, i64, i64, p, i64, i64, p, i64, p, i64, i64, p, p, p, i32, i32, i64, i64, i32,
                                     ctypes.c_float, p, p, p, sz, p]
     lib.dsa_mla_prefill.restype = st
@@ -464,13 +466,18 @@ def mla_decode_workspace_size(batch: int, next_n: int = 1) -> int:
 
 
 def new_mla_workspace(batch: int, next_n: int = 1, device="cuda") -> torch.Tensor:
-    """A zeroed workspace for ``dsa_mla_decode`` calls of this shape (and for ``dsa_mla_prefill``)."""
+    """A zeroed workspace for ``dsa_mla_decode`` calls of this shape, and for ``dsa_mla_prefill``."""
     device = torch.device(device)
     with torch.cuda.device(device):
         n = mla_decode_workspace_size(batch, next_n)
         if n == 0:
             raise ValueError("invalid shape for a workspace")
-        return torch.zeros(n, dtype=torch.uint8, device=device)
+        return torch.zeros(max(n, prefill_workspace_size()), dtype=torch.uint8, device=device)
+
+
+def prefill_workspace_size() -> int:
+    """Workspace bytes with which ``dsa_mla_prefill`` splits few rows over many entries (current device)."""
+    return int(load().dsa_mla_prefill_workspace_size())
 
 
 def dsa_mla_decode(q, kv_cache, page_table, seq_lens, max_context: int, sm_scale: float, out=None, lse=None,
@@ -526,7 +533,8 @@ def dsa_mla_prefill(q, k_nope, k_rope, v, cu_q, cu_kv, seq_lens, sm_scale: float
     q [Tq, H, 192] bf16, k_nope [Tk, H, 128], k_rope [Tk, 64], v [Tk, H, 128] (strided views are
     fine); cu_q, cu_kv int32 [B + 1]; seq_lens int32 [B] tokens per request, the new rows included;
     ``entry_tokens`` tokens per key entry (1: an entry per token).  out [Tq, H, 128] bf16 and lse
-    [Tq, H] fp32; rows outside [cu_q[0], cu_q[B]) are left as they are."""
+    [Tq, H] fp32; rows outside [cu_q[0], cu_q[B]) are left as they are.  ``workspace``: at least 256
+    bytes, zeroed once; of ``prefill_workspace_size()`` (the default), few rows over many entries are split."""
     dev = _device_of(q, "q", _BF16, (3,))
     _device_of(v, "v", _BF16, (3,))
     Tq, H, Tk = q.shape[0], q.shape[1], v.shape[0]
@@ -547,7 +555,9 @@ def dsa_mla_prefill(q, k_nope, k_rope, v, cu_q, cu_kv, seq_lens, sm_scale: float
     else:
         _on(lse, "lse", _F32, (Tq, H), dev)
     if workspace is None:
-        workspace = torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=q.device)
+        with torch.cuda.device(q.device):
+            workspace = torch.empty(prefill_workspace_size(), dtype=torch.uint8, device=q.device)
+        workspace[:WORKSPACE_HEADER_BYTES].zero_()
     _run(load().dsa_mla_prefill, dev, q.data_ptr(), q.stride(0), q.stride(1), k_nope.data_ptr(), k_nope.stride(0),
          k_nope.stride(1), k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), v.stride(0), v.stride(1),
          cu_q.data_ptr(), cu_kv.data_ptr(), seq_lens.data_ptr(), B, H, Tq, Tk, entry_tokens, sm_scale,

@@ -768,6 +768,12 @@ dsa_status_t dsa_mla_decode(const void* q, const void* kv_cache, int64_t num_pag
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA decode launch");
 }
 
+size_t dsa_mla_prefill_workspace_size(void) {
+    int sms = 0;
+    if (sm_count(&sms) != cudaSuccess) sms = 160;  // no device: what a large part needs
+    return dsa::kWorkspaceHeaderBytes + dsa::prefill_split_bytes(sms);
+}
+
 dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k_nope,
                              int64_t k_row_stride, int64_t k_head_stride, const void* k_rope, int64_t k_rope_stride,
                              const void* v, int64_t v_row_stride, int64_t v_head_stride, const int32_t* cu_q,
@@ -831,7 +837,18 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
     p.out_aligned32 = aligned(out, 32) ? 1 : 0;
     // A scale of 0 becomes one whose products vanish next to 1: hidden scores stay -inf times it.
     p.sm_scale_log2 = std::fmax(sm_scale * 1.4426950408889634f, 1e-30f);
-    const cudaError_t e = dsa::launch_mla_prefill(m, p, static_cast<cudaStream_t>(stream));
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    if (workspace_bytes >= dsa::kWorkspaceHeaderBytes + dsa::prefill_split_bytes(sms)) {
+        uint8_t* ws = static_cast<uint8_t*>(workspace) + dsa::kWorkspaceHeaderBytes;
+        p.split = reinterpret_cast<int2*>(ws);
+        p.split_units = reinterpret_cast<dsa::SplitUnit*>(ws + 16);
+        p.o_part = reinterpret_cast<float*>(ws + dsa::prefill_part_offset(sms));
+        p.max_parts = sms / 2;
+        p.lse_part = p.o_part + size_t(p.max_parts) * dsa::kPrefillBlock * DSA_PREFILL_V_DIM;
+    }
+    e = dsa::launch_mla_prefill(m, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA prefill launch");
 }
 

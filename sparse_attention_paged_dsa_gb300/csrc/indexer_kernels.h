@@ -172,6 +172,9 @@ cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map
 constexpr int kPrefillQk = 192;
 constexpr int kPrefillDv = 128;
 constexpr int kPrefillBlock = 512;  // rows of a request that share a pass over its entries
+struct SplitUnit {             // rows that several parts of their entries leave outputs for
+    int32_t q_row, rows, head, step_row, step_head;
+};
 struct PrefillParams {
     const int32_t* cu_q;       // [batch + 1] first row of each request
     const int32_t* cu_kv;      // [batch + 1] first entry of each request
@@ -185,6 +188,11 @@ struct PrefillParams {
     int32_t heads;
     int32_t entry_tokens;      // tokens per entry
     int32_t slots;             // q_rows / 512 + batch: at least the blocks of up to 512 rows
+    int2* split;               // units, and parts of each (0 or 1: written directly)
+    SplitUnit* split_units;    // [clusters / 2]
+    float* o_part;             // [parts, 2 tiles, 256 rows, 128]; null: no splitting
+    float* lse_part;           // [parts, 2, 256]
+    int32_t max_parts;         // of all units
     int32_t out_aligned32;     // out starts on a 32-byte boundary
     float sm_scale_log2;       // sm_scale * log2(e), above 0
 };
@@ -193,6 +201,8 @@ struct PrefillParams {
 struct PrefillMaps {
     CUtensorMap q, kn, kr, v, kn16, kr16, v16;
 };
+size_t prefill_split_bytes(int sms);  // workspace behind the header, with splitting
+size_t prefill_part_offset(int sms);  // where in it the parts' outputs start
 cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t stream);
 
 // Residual addition + RMS norm of bf16 rows.

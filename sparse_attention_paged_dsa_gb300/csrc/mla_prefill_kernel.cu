@@ -16,11 +16,15 @@
 // bandwidth.
 //
 // Work.  A unit is 512 rows of a request and one head, whose two tiles share the
-// keys and values; or 256 rows and two heads, one a tile (see Cut).  Clusters are persistent: the units, longest requests and their
-// last rows first, are dealt out back and forth over the clusters that fit the
-// device, and the next unit's loads and first product run under the end of the one
-// before (a unit's own set-up and tail cost 9 us without that).  A scheduler warp
-// looks the units up.  Roles of a CTA (384 threads):
+// keys and values; or 256 rows and two heads, one a tile (see Cut).  Clusters are
+// persistent: the units, longest requests and their last rows first, are dealt out
+// back and forth over the clusters that fit the device, and the next unit's loads and
+// first product run under the end of the one before (a unit's own set-up and tail cost
+// 9 us without that).  Where the units are at most half the clusters, each is cut along
+// its entries into as many parts as there is room for; parts leave fp32 outputs and a
+// second kernel joins them by log-sum-exp (one row of 64 heads over 16,385 entries:
+// 138 us, uncut 249; 300 rows of two heads over 33,068: 41, uncut 386).  A scheduler
+// warp looks the units up.  Roles of a CTA (384 threads):
 //   * warps 0-3 and 4-7: softmax of query tile 0 and 1, one row per thread: the
 //     row of S from TMEM to registers, its maximum (raised only when a tile
 //     passes it by more than 2^20; the accumulator is then rescaled in TMEM),
@@ -76,6 +80,8 @@ constexpr uint32_t kColOP = 256;  // O of tile i at 256 + 128 i
 constexpr float kRaiseLog2 = 20.0f;  // rounding is relative: weights may pass 1 by this much
 constexpr float kLn2P = 0.69314718055994531f;
 
+constexpr int kPartTiles = 4;        // key tiles a part has at least, in the longest request (2: no faster; 8: 20 heads,
+                                     // 2,064 entries 29 us, now 23)
 constexpr int kFewEntries = 768;     // see Cut: two heads a unit up to here (512: 146 us against 155), one above (1024: 80, 100)
 constexpr int kSortMost = 256;       // requests that are ordered by length, one a thread (more: as they come)
 constexpr int kInfoSlots = 4;
@@ -92,6 +98,8 @@ struct Unit {
     int head;
     int step_row, step_head; // (256, 0): the tiles share keys and values; (0, 1)
     int limit[2];            // entries that the tile's last row sees; 0 without a tile
+    int skip;                // entries before this part's first one (kv0 and limit are the part's)
+    int part;                // where its output goes, -1: the output itself
     int last;                // no unit: the list is at its end
 
     __device__ __forceinline__ bool shared() const { return step_head == 0; }
@@ -116,8 +124,8 @@ struct __align__(8) PrefillCtl {
     uint64_t all_done;
     uint32_t tmem_base;
     int abort;
-    int total;                         // units
-    int warp_units[kThreadsP / 32];
+    int total, parts;                  // units, and parts of each
+    int warp_units[kThreadsP / 32], warp_live[kThreadsP / 32];
     Unit info[kInfoSlots];
     int first[kMaxBatch];              // first unit of the i-th request in the order
     int16_t order[kMaxBatch];          // that request
@@ -288,6 +296,9 @@ struct Cut {
     __device__ __forceinline__ int units() const { return pair_blocks * pairs() + long_blocks * heads; }
 };
 
+// kSplit: units may be cut into parts.  (In a kernel of its own: the choice made at run time in one took
+// 64 prompts of 100 rows, which are not cut, from 119 to 131 us.)
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kn_map,
                        const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap v_map,
@@ -343,11 +354,13 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
 
     // The order of the requests (longest first, where they are few) and where their units start.
     uint32_t bad = 0;
+    int most_live = 0;  // entries of the longest request
     for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
         const Request r(p, b, bad);
         ctl.first[b] = Cut(r, p.heads).units();
         ctl.order[b] = int16_t(b);
         if (b < kSortMost) ctl.key[b] = r.rows > 0 ? r.live : -1;
+        if (kSplit && r.rows > 0) most_live = max(most_live, r.live);
     }
     if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
     __syncthreads();
@@ -376,7 +389,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
-    if (lane == 31) ctl.warp_units[warp] = incl;
+    if constexpr (kSplit) most_live = __reduce_max_sync(0xffffffffu, most_live);
+    if (lane == 31) ctl.warp_units[warp] = incl, ctl.warp_live[warp] = most_live;
     __syncthreads();
     {
         int before = incl - mine, total = 0;
@@ -389,7 +403,19 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             ctl.first[i] = before;
             before += units;
         }
-        if (threadIdx.x == 0) ctl.total = total;
+        if (threadIdx.x == 0) {
+            // Parts: as many as give every cluster one, but none of less than kPartTiles key tiles in the
+            // longest request.
+            int parts = 1;
+            if (kSplit && total > 0) {
+                for (int w = 0; w < kThreadsP / 32; ++w) most_live = max(most_live, ctl.warp_live[w]);
+                parts = max(min(min(int(gridDim.x >> 1) / total, p.max_parts / total),
+                                (most_live + kTile - 1) / kTile / kPartTiles), 1);
+            }
+            ctl.parts = parts;
+            ctl.total = total * parts;
+            if (kSplit && blockIdx.x == 0) *p.split = make_int2(total, parts);
+        }
     }
     __syncwarp();
     cluster_wait();  // the other CTA's barriers are set up too
@@ -425,16 +451,18 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             Unit u = {};
             u.last = more ? 0 : 1;
             if (more) {
-                int lo = 0;  // the last request (in the order) that starts at or before n: 32-way, twice
+                const int parts = kSplit ? ctl.parts : 1;
+                const int whole = int(n) / parts, part = int(n) % parts;
+                int lo = 0;  // the last request (in the order) that starts at or before it: 32-way, twice
                 for (int span = 32; span >= 1; span /= 32) {
                     const int at = lo + lane * span;
-                    const bool before = at < p.batch && ctl.first[at] <= int(n);
+                    const bool before = at < p.batch && ctl.first[at] <= whole;
                     lo += span * (__popc(__ballot_sync(0xffffffffu, before)) - 1);
                 }
                 // requests without rows start where the next one does: the last of them is the owner
                 uint32_t ignored = 0;
                 const Request rq(p, int(ctl.order[lo]), ignored);
-                int at = int(n) - ctl.first[lo];
+                int at = whole - ctl.first[lo];
                 const Cut cut(rq, p.heads);
                 // last rows (the longest) first: the blocks for two heads lie behind the long ones
                 if (at < cut.pair_blocks * cut.pairs()) {
@@ -456,6 +484,20 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                     const int from = i * u.step_row, to = min(u.rows, from + 2 * kTile);
                     const bool there = to > from && u.head + i * u.step_head < p.heads;
                     u.limit[i] = there ? rq.seen(u.row0 + to - 1, p.entry_tokens) : 0;
+                }
+                u.part = -1;
+                if (parts > 1) {
+                    u.part = int(n);
+                    if (part == 0 && rank == 0 && lane == 0) {
+                        SplitUnit& out = p.split_units[whole];
+                        out.q_row = u.q_row, out.rows = u.rows, out.head = u.head;
+                        out.step_row = u.step_row, out.step_head = u.step_head;
+                    }
+                    const int nt = u.nt(), j0 = nt * part / parts, j1 = nt * (part + 1) / parts;
+                    u.skip = j0 * kTile;
+                    u.kv0 += u.skip;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) u.limit[i] = min(max(u.limit[i] - u.skip, 0), (j1 - j0) * kTile);
                 }
             }
             ok = __all_sync(0xffffffffu, mbar_await(&ctl.info_empty[slot], (uint32_t(k / kInfoSlots) & 1u) ^ 1u,
@@ -832,10 +874,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             const bool live_row = i * u.step_row + r < u.rows && head < p.heads;
             const int limit = i ? u.limit[1] : u.limit[0], ntiles = (limit + kTile - 1) / kTile;
             const int64_t token = int64_t(u.q_row) + i * u.step_row + r;
+            const int64_t part_row = kSplit && u.part >= 0 ? (int64_t(u.part) * 2 + i) * (2 * kTile) + r : -1;
             int see = limit;
             if (live_row) {
                 const int64_t len = int64_t(u.seq) - (int64_t(u.req_rows) - 1 - (u.row0 + i * u.step_row + r));
-                see = min(entries_seen(len > 0 ? int(len) : 0, p.entry_tokens), u.live);
+                see = min(entries_seen(len > 0 ? int(len) : 0, p.entry_tokens), u.live) - (kSplit ? u.skip : 0);
             }
             float m = -INFINITY;
             float2 l2 = make_float2(0.f, 0.f);
@@ -964,7 +1007,9 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             // ---- output
             __nv_bfloat16* o_row = reinterpret_cast<__nv_bfloat16*>(p.out) + (token * p.heads + head) * kPrefillDv;
             if (ntiles == 0) {  // rows that see nothing
-                if (live_row) {
+                if (kSplit && live_row && part_row >= 0) {
+                    p.lse_part[part_row] = -INFINITY;
+                } else if (live_row) {
                     for (int c = 0; c < kPrefillDv / 8; ++c)
                         *reinterpret_cast<uint4*>(o_row + 8 * c) = make_uint4(0, 0, 0, 0);
                     p.lse[token * p.heads + head] = -INFINITY;
@@ -981,7 +1026,12 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             tc_fence_after_sync();
             const float l = l2.x + l2.y;
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            if (live_row) p.lse[token * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2P : -INFINITY;
+            const float lse = l > 0.f ? (m + log2f(l)) * kLn2P : -INFINITY;
+            if (kSplit && live_row && part_row >= 0) {
+                p.lse_part[part_row] = lse;
+            } else if (live_row) {
+                p.lse[token * p.heads + head] = lse;
+            }
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
@@ -992,7 +1042,16 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(o_bar);  // O may be overwritten
                 }
-                if (live_row) {
+                if (kSplit && live_row && part_row >= 0) {
+                    float* d = p.o_part + part_row * kPrefillDv + 32 * c;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(__uint_as_float(o[8 * h + k]) * inv);
+                        st_global_v8(d + 8 * h, w);
+                    }
+                } else if (live_row) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {  // a whole sector a lane
                         uint32_t w[8];
@@ -1027,14 +1086,59 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     if (warp == 8) tmem2_dealloc(tmem_base, kTmemColsP);
 }
 
+// out = sum_s exp(lse_s - lse) o_s over a unit's parts, lse = log sum_s exp(lse_s).  One warp per row; grid
+// (units, 64 groups of 8 rows).
+__global__ void __launch_bounds__(256) mla_prefill_merge_kernel(const PrefillParams p) {
+    pdl_wait_prior_grid();
+    pdl_allow_next_grid();
+    const int2 split = *p.split;  // units, parts of each
+    const int unit = blockIdx.x, parts = split.y;
+    if (unit >= split.x || parts < 2) return;
+    const SplitUnit u = p.split_units[unit];
+    const int lane = threadIdx.x & 31;
+    const int at = int(blockIdx.y) * 8 + (threadIdx.x >> 5), i = at / (2 * kTile), r = at % (2 * kTile);
+    const int head = u.head + i * u.step_head;
+    if (i * u.step_row + r >= u.rows || head >= p.heads) return;
+    const auto part_row = [&](int s) { return (int64_t(unit) * parts + s) * 4 * kTile + at; };
+    float mx = -INFINITY, sum = 0.f;
+    for (int s = lane; s < parts; s += 32) mx = fmaxf(mx, p.lse_part[part_row(s)]);
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+        const float w = mx == -INFINITY ? 0.f : expf(p.lse_part[part_row(s)] - mx);
+        if (w == 0.f) continue;  // a part without entries has written no output
+        sum += w;
+        const float4 v = *reinterpret_cast<const float4*>(p.o_part + part_row(s) * kPrefillDv + 4 * lane);
+        acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t row = (int64_t(u.q_row) + i * u.step_row + r) * p.heads + head;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(p.out + row * kPrefillDv + 4 * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    if (lane == 0) p.lse[row] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+}
+
 }  // namespace
 
+size_t prefill_split_bytes(int sms) {
+    const size_t parts = size_t(sms) / 2;
+    return prefill_part_offset(sms) + parts * 4 * kTile * (kPrefillDv + 1) * sizeof(float);
+}
+size_t prefill_part_offset(int sms) {  // the pair of counts and the units, before the parts
+    return (16 + size_t(sms) / 2 * sizeof(SplitUnit) + 255) / 256 * 256;
+}
+
 cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t stream) {
-    static SmemLimitOnce smem_limit;
+    static SmemLimitOnce smem_limit, smem_limit_split;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    e = smem_limit.apply(dev, mla_prefill_kernel, kSmemP);
+    e = smem_limit.apply(dev, mla_prefill_kernel<false>, kSmemP);
+    if (e == cudaSuccess) e = smem_limit_split.apply(dev, mla_prefill_kernel<true>, kSmemP);
     if (e != cudaSuccess) return e;
     // Persistent clusters: as many as the device holds (its SMs do not all pair up), or one per unit.
     static std::atomic<int> resident[kMaxDevices];
@@ -1051,7 +1155,7 @@ cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cud
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        e = cudaOccupancyMaxActiveClusters(&fit, mla_prefill_kernel, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&fit, mla_prefill_kernel<false>, &cfg);
         if (e != cudaSuccess) return e;
         if (fit < 1) return cudaErrorInvalidConfiguration;
         resident[dev].store(fit, std::memory_order_relaxed);
@@ -1059,8 +1163,19 @@ cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cud
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     const int64_t most = int64_t(p.slots) * p.heads;  // at least the number of units
-    cfg.gridDim = dim3(2u * unsigned(most < fit ? most : fit));
-    return cudaLaunchKernelEx(&cfg, mla_prefill_kernel, m.q, m.kn, m.kr, m.v, m.kn16, m.kr16, m.v16, p);
+    // Splitting needs units that leave half the clusters without one and a request of two parts' entries;
+    // the kernel, which sees the lengths, decides.  Where the arguments rule it out, the second launch (2 us)
+    // is not made.
+    const int64_t least = int64_t(p.q_rows) * p.heads / kPrefillBlock;  // units, where every row is used
+    const bool split = p.o_part && most <= 2 * fit && least <= fit / 2 && p.kv_rows >= 2 * kPartTiles * kTile;
+    cfg.gridDim = dim3(2u * unsigned(most < fit && !split ? most : fit));
+    if (!split) return cudaLaunchKernelEx(&cfg, mla_prefill_kernel<false>, m.q, m.kn, m.kr, m.v, m.kn16, m.kr16, m.v16, p);
+    e = cudaLaunchKernelEx(&cfg, mla_prefill_kernel<true>, m.q, m.kn, m.kr, m.v, m.kn16, m.kr16, m.v16, p);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(unsigned(fit) / 2u, 4 * kTile / 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, mla_prefill_merge_kernel, p);
 }
 
 }  // namespace dsa

@@ -66,9 +66,9 @@ class Case:
                 assert torch.all(dl <= 2.0 ** -11 + 2.0 ** -20 * l.abs()[~none]), f"request {b} head {h}: lse"
 
 
-def run(lib, case, **kw):
+def run(lib, case, split=False, **kw):
     import torch
-    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    ws = lib.new_mla_workspace(1) if split else torch.zeros(256, dtype=torch.uint8, device="cuda")
     out, lse = lib.dsa_mla_prefill(*case.args(), entry_tokens=case.e, workspace=ws, **kw)
     assert lib.get_error(ws) == 0
     return out, lse
@@ -89,6 +89,56 @@ def test_prefill_chunks(gpu_lib, n, seq, e):
     """New rows on top of earlier tokens."""
     case = Case([n], [seq], heads=3, e=e, seed=n + seq)
     case.check(*run(gpu_lib, case))
+
+
+@pytest.mark.parametrize("n, seq, e, heads", [(1, 1024, 1, 1), (1, 30000, 4, 1), (3, 4097, 1, 2), (64, 9001, 1, 5),
+                                              (130, 5000, 4, 3), (256, 20000, 4, 18), (257, 3000, 1, 1),
+                                              (400, 8191, 1, 7), (512, 12000, 4, 20), (700, 6000, 1, 3),
+                                              (1100, 1100, 1, 1), (5, 600, 1, 1), (20, 66000, 1, 3)])
+def test_prefill_split(gpu_lib, n, seq, e, heads):
+    """Few units over many entries: parts of each on clusters of their own, joined by the merge; and the
+    same call unsplit.  One row, both kinds of unit, units of unlike length, parts that some rows (and one
+    of two tiles) see nothing of."""
+    case = Case([n], [seq], heads=heads, e=e, seed=n + heads)
+    case.check(*run(gpu_lib, case, split=True))
+    case.check(*run(gpu_lib, case))
+
+
+def test_prefill_split_ragged(gpu_lib):
+    """A long and a short request, one without rows and one shorter than its rows, in parts; the workspace
+    reused by calls of other splits, the same bits again."""
+    import torch
+    case = Case([40, 0, 300, 9], [20000, 50, 310, 5], heads=3, e=1, seed=21)
+    ws = gpu_lib.new_mla_workspace(1)
+    f = lambda c: [t.clone() for t in gpu_lib.dsa_mla_prefill(*c.args(), entry_tokens=c.e, workspace=ws)]  # noqa: E731
+    first = f(case)
+    case.check(*first)
+    other = Case([2], [70000], heads=1, e=4, seed=22)
+    other.check(*f(other))
+    again = f(case)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1]) and gpu_lib.get_error(ws) == 0
+
+
+def test_prefill_split_graph_lengths(gpu_lib):
+    """Captured on one batch, replayed on lengths that are split otherwise, or not at all."""
+    import torch
+    case = Case([6, 50], [30000, 2000], heads=2, e=1, seed=23)
+    ws = gpu_lib.new_mla_workspace(1)
+    out = torch.empty(56, 2, 128, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(56, 2, device="cuda")
+    args = case.args()
+    gpu_lib.dsa_mla_prefill(*args, entry_tokens=1, out=out, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gpu_lib.dsa_mla_prefill(*args, entry_tokens=1, out=out, lse=lse, workspace=ws)
+    for seqs in ([30000, 2000], [100, 60], [6, 1999], [29000, 50]):
+        case.seqs = seqs
+        case.seq.copy_(torch.tensor(seqs, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        case.check(out, lse)
+    assert gpu_lib.get_error(ws) == 0
 
 
 @pytest.mark.parametrize("heads", [1, 2, 5, 64, 128])
