@@ -385,8 +385,8 @@ DSA_API dsa_status_t dsa_mla_decode(const void *q, const void *kv_cache, int64_t
  *   out     bf16 [q_rows, heads, 128] 16-byte aligned, lse fp32 [q_rows, heads], both contiguous
  *   workspace >= DSA_PREFILL_WORKSPACE_BYTES, 256-byte aligned, header zeroed once (the error
  *           word).  With dsa_mla_prefill_workspace_size() bytes (sized for the current
- *           device; any larger one will do) few rows over many entries are split along the
- *           entries and joined by log-sum-exp.
+ *           device; any larger one will do) rows that would leave a part of the device idle are
+ *           split along the entries and joined by log-sum-exp.
  *
  * 1 <= batch <= 1024, 1 <= heads <= 128, 1 <= entry_tokens <= 64, sm_scale finite
  * and >= 0, q_rows and kv_rows below 2^31 (0 rows: nothing is launched; 0 entries: every
@@ -398,7 +398,7 @@ DSA_API dsa_status_t dsa_mla_decode(const void *q, const void *kv_cache, int64_t
  * Where requests are split, the order of a row's sums depends on the batch's row counts and
  * lengths; otherwise a row's result depends on its request alone.  For the same arguments
  * results are the same bits.  The launch depends on (q_rows, kv_rows, batch,
- * heads, workspace_bytes).  Asynchronous on `stream`, allocates nothing, capture-safe.
+ * heads, entry_tokens, workspace_bytes).  Asynchronous on `stream`, allocates nothing, capture-safe.
  */
 #define DSA_PREFILL_QK_DIM 192
 #define DSA_PREFILL_NOPE_DIM 128

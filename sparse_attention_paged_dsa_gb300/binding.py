@@ -476,7 +476,7 @@ def new_mla_workspace(batch: int, next_n: int = 1, device="cuda") -> torch.Tenso
 
 
 def prefill_workspace_size() -> int:
-    """Workspace bytes with which ``dsa_mla_prefill`` splits few rows over many entries (current device)."""
+    """Workspace bytes with which ``dsa_mla_prefill`` may split rows along their entries (current device)."""
     return int(load().dsa_mla_prefill_workspace_size())
 
 
@@ -534,7 +534,7 @@ def dsa_mla_prefill(q, k_nope, k_rope, v, cu_q, cu_kv, seq_lens, sm_scale: float
     fine); cu_q, cu_kv int32 [B + 1]; seq_lens int32 [B] tokens per request, the new rows included;
     ``entry_tokens`` tokens per key entry (1: an entry per token).  out [Tq, H, 128] bf16 and lse
     [Tq, H] fp32; rows outside [cu_q[0], cu_q[B]) are left as they are.  ``workspace``: at least 256
-    bytes, zeroed once; of ``prefill_workspace_size()`` (the default), few rows over many entries are split."""
+    bytes, zeroed once; with ``prefill_workspace_size()`` (the default) few rows may be split along their entries."""
     dev = _device_of(q, "q", _BF16, (3,))
     _device_of(v, "v", _BF16, (3,))
     Tq, H, Tk = q.shape[0], q.shape[1], v.shape[0]

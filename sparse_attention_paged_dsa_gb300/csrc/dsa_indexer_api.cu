@@ -845,8 +845,7 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
         p.split = reinterpret_cast<int2*>(ws);
         p.split_units = reinterpret_cast<dsa::SplitUnit*>(ws + 16);
         p.o_part = reinterpret_cast<float*>(ws + dsa::prefill_part_offset(sms));
-        p.max_parts = sms / 2;
-        p.lse_part = p.o_part + size_t(p.max_parts) * dsa::kPrefillBlock * DSA_PREFILL_V_DIM;
+        p.lse_part = p.o_part + dsa::prefill_max_parts(sms) * dsa::kPrefillBlock * DSA_PREFILL_V_DIM;
     }
     e = dsa::launch_mla_prefill(m, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA prefill launch");

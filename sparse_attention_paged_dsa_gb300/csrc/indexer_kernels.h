@@ -188,11 +188,10 @@ struct PrefillParams {
     int32_t heads;
     int32_t entry_tokens;      // tokens per entry
     int32_t slots;             // q_rows / 512 + batch: at least the blocks of up to 512 rows
-    int2* split;               // units, and parts of each (0 or 1: written directly)
-    SplitUnit* split_units;    // [clusters / 2]
+    int2* split;               // cut units, and parts of each (1: none is cut)
+    SplitUnit* split_units;    // [clusters]
     float* o_part;             // [parts, 2 tiles, 256 rows, 128]; null: no splitting
     float* lse_part;           // [parts, 2, 256]
-    int32_t max_parts;         // of all units
     int32_t out_aligned32;     // out starts on a 32-byte boundary
     float sm_scale_log2;       // sm_scale * log2(e), above 0
 };
@@ -203,6 +202,7 @@ struct PrefillMaps {
 };
 size_t prefill_split_bytes(int sms);  // workspace behind the header, with splitting
 size_t prefill_part_offset(int sms);  // where in it the parts' outputs start
+size_t prefill_max_parts(int sms);
 cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t stream);
 
 // Residual addition + RMS norm of bf16 rows.

@@ -20,11 +20,13 @@
 // persistent: the units, longest requests and their last rows first, are dealt out
 // back and forth over the clusters that fit the device, and the next unit's loads and
 // first product run under the end of the one before (a unit's own set-up and tail cost
-// 9 us without that).  Where the units are at most half the clusters, each is cut along
-// its entries into as many parts as there is room for; parts leave fp32 outputs and a
-// second kernel joins them by log-sum-exp (one row of 64 heads over 16,385 entries:
-// 138 us, uncut 249; 300 rows of two heads over 33,068: 41, uncut 386).  A scheduler
-// warp looks the units up.  Roles of a CTA (384 threads):
+// 9 us without that).  The units behind the last whole round of the clusters are cut
+// along their entries where that pays (parts_of); parts leave fp32 outputs and a second
+// kernel joins them by log-sum-exp (one row of 64 heads over 16,385 entries: 136 us,
+// uncut 249; 300 rows of two heads over 33,068: 42, uncut 386; 128 units of 256 key
+// tiles: 756, uncut 805).  Units of equal cost laid end to end and cut once per cluster
+// balance better, but cost more to find and to join: 735 there, 8192 rows of 32 heads
+// 484 against 407.  A scheduler warp looks the units up.  Roles of a CTA (384 threads):
 //   * warps 0-3 and 4-7: softmax of query tile 0 and 1, one row per thread: the
 //     row of S from TMEM to registers, its maximum (raised only when a tile
 //     passes it by more than 2^20; the accumulator is then rescaled in TMEM),
@@ -80,8 +82,7 @@ constexpr uint32_t kColOP = 256;  // O of tile i at 256 + 128 i
 constexpr float kRaiseLog2 = 20.0f;  // rounding is relative: weights may pass 1 by this much
 constexpr float kLn2P = 0.69314718055994531f;
 
-constexpr int kPartTiles = 4;        // key tiles a part has at least, in the longest request (2: no faster; 8: 20 heads,
-                                     // 2,064 entries 29 us, now 23)
+constexpr int kPartTiles = 4;        // key tiles a part has at least (2: no faster; 8: 20 heads, 2,064 entries 29 us, now 22)
 constexpr int kFewEntries = 768;     // see Cut: two heads a unit up to here (512: 146 us against 155), one above (1024: 80, 100)
 constexpr int kSortMost = 256;       // requests that are ordered by length, one a thread (more: as they come)
 constexpr int kInfoSlots = 4;
@@ -124,8 +125,8 @@ struct __align__(8) PrefillCtl {
     uint64_t all_done;
     uint32_t tmem_base;
     int abort;
-    int total, parts;                  // units, and parts of each
-    int warp_units[kThreadsP / 32], warp_live[kThreadsP / 32];
+    int total, parts;                  // pieces of work; parts of each unit behind the whole ones
+    int warp_units[kThreadsP / 32];
     Unit info[kInfoSlots];
     int first[kMaxBatch];              // first unit of the i-th request in the order
     int16_t order[kMaxBatch];          // that request
@@ -286,15 +287,74 @@ __device__ __forceinline__ void wait_landed_p(uint64_t* bar, uint32_t parity) {
 // Many: 512 rows of one head, whose tiles share keys and values, and at most 256 rows left as above.
 struct Cut {
     int rows, heads, pair_blocks, long_blocks;  // blocks of 256 rows for two heads, and of 512 for one
-    __device__ __forceinline__ Cut(const Request& r, int heads_) : rows(r.rows), heads(heads_) {
-        const bool few = r.live <= kFewEntries && heads_ > 1;
-        const int left = few ? r.rows : r.rows % kPrefillBlock;
+    __host__ __device__ __forceinline__ Cut(int rows_, int live, int heads_) : rows(rows_), heads(heads_) {
+        const bool few = live <= kFewEntries && heads_ > 1;
+        const int left = few ? rows : rows % kPrefillBlock;
         pair_blocks = few || left <= 2 * kTile ? (left + 2 * kTile - 1) / (2 * kTile) : 0;
-        long_blocks = few ? 0 : (r.rows + 2 * kTile - 1) / kPrefillBlock;
+        long_blocks = few ? 0 : (rows + 2 * kTile - 1) / kPrefillBlock;
     }
-    __device__ __forceinline__ int pairs() const { return (heads + 1) / 2; }
-    __device__ __forceinline__ int units() const { return pair_blocks * pairs() + long_blocks * heads; }
+    __device__ __forceinline__ Cut(const Request& r, int heads_) : Cut(r.rows, r.live, heads_) {}
+    __host__ __device__ __forceinline__ int pairs() const { return (heads + 1) / 2; }
+    __host__ __device__ __forceinline__ int units() const { return pair_blocks * pairs() + long_blocks * heads; }
 };
+
+// The last request (in the order) that starts at or before unit n: 32-way, twice.  (Requests without rows
+// start where the next one does: the last of them is the owner.)
+__device__ __forceinline__ int request_at(const PrefillParams& p, const PrefillCtl& ctl, int n, int lane) {
+    int lo = 0;
+    for (int span = 32; span >= 1; span /= 32) {
+        const int at = lo + lane * span;
+        const bool before = at < p.batch && ctl.first[at] <= n;
+        lo += span * (__popc(__ballot_sync(0xffffffffu, before)) - 1);
+    }
+    return lo;
+}
+
+// The request's unit number `at`, last rows (the longest) first: the blocks for two heads lie behind the
+// long ones.
+__device__ __forceinline__ Unit unit_of(const PrefillParams& p, const Request& rq, int at) {
+    const Cut cut(rq, p.heads);
+    Unit u = {};
+    if (at < cut.pair_blocks * cut.pairs()) {
+        u.row0 = cut.long_blocks * kPrefillBlock + (cut.pair_blocks - 1 - at / cut.pairs()) * 2 * kTile;
+        u.rows = min(rq.rows - u.row0, 2 * kTile);
+        u.head = at % cut.pairs() * 2;
+        u.step_head = 1;
+    } else {
+        at -= cut.pair_blocks * cut.pairs();
+        u.row0 = (cut.long_blocks - 1 - at / p.heads) * kPrefillBlock;
+        u.rows = min(rq.rows - u.row0, kPrefillBlock);
+        u.head = at % p.heads;
+        u.step_row = 2 * kTile;
+    }
+    u.q_row = rq.q0 + u.row0;
+    u.req_rows = rq.rows, u.seq = rq.seq, u.live = rq.live, u.kv0 = rq.kv0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int from = i * u.step_row, to = min(u.rows, from + 2 * kTile);
+        const bool there = to > from && u.head + i * u.step_head < p.heads;
+        u.limit[i] = there ? rq.seen(u.row0 + to - 1, p.entry_tokens) : 0;
+    }
+    u.part = -1;
+    return u;
+}
+
+// Into how many parts to cut each of `units` units of `tiles` key tiles, the last ones, which would leave
+// some of the clusters idle.  In key tiles: a unit costs 3 beside its own, a second launch and its reading
+// 6 and 1 for every 36 parts.  Parts go round the clusters at most kRounds times.
+constexpr int kRounds = 3;
+__host__ __device__ __forceinline__ int parts_of(int units, int tiles, int clusters) {
+    int best = 1, least = tiles + 3;
+    for (int rounds = 1; units > 0 && rounds <= kRounds; ++rounds) {
+        int parts = rounds * clusters / units;
+        if (parts > tiles / kPartTiles) parts = tiles / kPartTiles;
+        if (parts < 2) continue;
+        const int goes = (units * parts + clusters - 1) / clusters;
+        const int cost = goes * ((tiles + parts - 1) / parts + 3) + 6 + units * parts / 36;
+        if (cost < least) best = parts, least = cost;
+    }
+    return best;
+}
 
 // kSplit: units may be cut into parts.  (In a kernel of its own: the choice made at run time in one took
 // 64 prompts of 100 rows, which are not cut, from 119 to 131 us.)
@@ -354,13 +414,11 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
 
     // The order of the requests (longest first, where they are few) and where their units start.
     uint32_t bad = 0;
-    int most_live = 0;  // entries of the longest request
     for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
         const Request r(p, b, bad);
         ctl.first[b] = Cut(r, p.heads).units();
         ctl.order[b] = int16_t(b);
         if (b < kSortMost) ctl.key[b] = r.rows > 0 ? r.live : -1;
-        if (kSplit && r.rows > 0) most_live = max(most_live, r.live);
     }
     if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
     __syncthreads();
@@ -389,8 +447,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
-    if constexpr (kSplit) most_live = __reduce_max_sync(0xffffffffu, most_live);
-    if (lane == 31) ctl.warp_units[warp] = incl, ctl.warp_live[warp] = most_live;
+    if (lane == 31) ctl.warp_units[warp] = incl;
     __syncthreads();
     {
         int before = incl - mine, total = 0;
@@ -403,19 +460,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             ctl.first[i] = before;
             before += units;
         }
-        if (threadIdx.x == 0) {
-            // Parts: as many as give every cluster one, but none of less than kPartTiles key tiles in the
-            // longest request.
-            int parts = 1;
-            if (kSplit && total > 0) {
-                for (int w = 0; w < kThreadsP / 32; ++w) most_live = max(most_live, ctl.warp_live[w]);
-                parts = max(min(min(int(gridDim.x >> 1) / total, p.max_parts / total),
-                                (most_live + kTile - 1) / kTile / kPartTiles), 1);
-            }
-            ctl.parts = parts;
-            ctl.total = total * parts;
-            if (kSplit && blockIdx.x == 0) *p.split = make_int2(total, parts);
-        }
+        if (threadIdx.x == 0) ctl.total = total;
     }
     __syncwarp();
     cluster_wait();  // the other CTA's barriers are set up too
@@ -442,54 +487,36 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     if (warp == 11) {
         // ================= scheduler =================
         const int clusters = int(gridDim.x >> 1), cluster = int(blockIdx.x >> 1);
+        // Units that go round the clusters whole times, then the parts of the others.
+        int total = ctl.total, whole = total, parts = 1;
+        if (kSplit && total > 0) {
+            const int left = total % clusters;
+            uint32_t ignored = 0;
+            const int lo = request_at(p, ctl, total - left, lane);
+            const Request rq(p, int(ctl.order[lo]), ignored);
+            if (left > 0) parts = parts_of(left, unit_of(p, rq, total - left - ctl.first[lo]).nt(), clusters);
+            if (parts > 1) whole = total - left, total = whole + left * parts;
+        }
+        if (kSplit && blockIdx.x == 0 && lane == 0) *p.split = make_int2(ctl.total - whole, parts);
         bool ok = true, more = true;
         for (int k = 0; ok && more; ++k) {
             const int slot = k & (kInfoSlots - 1);
             // dealt back and forth: what is longer in one round meets what is shorter in the next
             const int64_t n = int64_t(k) * clusters + ((k & 1) ? clusters - 1 - cluster : cluster);
-            more = n < ctl.total;
+            more = n < total;
             Unit u = {};
             u.last = more ? 0 : 1;
             if (more) {
-                const int parts = kSplit ? ctl.parts : 1;
-                const int whole = int(n) / parts, part = int(n) % parts;
-                int lo = 0;  // the last request (in the order) that starts at or before it: 32-way, twice
-                for (int span = 32; span >= 1; span /= 32) {
-                    const int at = lo + lane * span;
-                    const bool before = at < p.batch && ctl.first[at] <= whole;
-                    lo += span * (__popc(__ballot_sync(0xffffffffu, before)) - 1);
-                }
-                // requests without rows start where the next one does: the last of them is the owner
+                const int past = max(int(n) - whole, 0), part = past % parts;  // (1 part: 0)
+                const int at = min(int(n), whole) + past / parts;
+                const int lo = request_at(p, ctl, at, lane);
                 uint32_t ignored = 0;
                 const Request rq(p, int(ctl.order[lo]), ignored);
-                int at = whole - ctl.first[lo];
-                const Cut cut(rq, p.heads);
-                // last rows (the longest) first: the blocks for two heads lie behind the long ones
-                if (at < cut.pair_blocks * cut.pairs()) {
-                    u.row0 = cut.long_blocks * kPrefillBlock + (cut.pair_blocks - 1 - at / cut.pairs()) * 2 * kTile;
-                    u.rows = min(rq.rows - u.row0, 2 * kTile);
-                    u.head = at % cut.pairs() * 2;
-                    u.step_head = 1;
-                } else {
-                    at -= cut.pair_blocks * cut.pairs();
-                    u.row0 = (cut.long_blocks - 1 - at / p.heads) * kPrefillBlock;
-                    u.rows = min(rq.rows - u.row0, kPrefillBlock);
-                    u.head = at % p.heads;
-                    u.step_row = 2 * kTile;
-                }
-                u.q_row = rq.q0 + u.row0;
-                u.req_rows = rq.rows, u.seq = rq.seq, u.live = rq.live, u.kv0 = rq.kv0;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int from = i * u.step_row, to = min(u.rows, from + 2 * kTile);
-                    const bool there = to > from && u.head + i * u.step_head < p.heads;
-                    u.limit[i] = there ? rq.seen(u.row0 + to - 1, p.entry_tokens) : 0;
-                }
-                u.part = -1;
-                if (parts > 1) {
-                    u.part = int(n);
+                u = unit_of(p, rq, at - ctl.first[lo]);
+                if (kSplit && parts > 1 && int(n) >= whole) {
+                    u.part = past;
                     if (part == 0 && rank == 0 && lane == 0) {
-                        SplitUnit& out = p.split_units[whole];
+                        SplitUnit& out = p.split_units[at - whole];
                         out.q_row = u.q_row, out.rows = u.rows, out.head = u.head;
                         out.step_row = u.step_row, out.step_head = u.step_head;
                     }
@@ -1124,13 +1151,13 @@ __global__ void __launch_bounds__(256) mla_prefill_merge_kernel(const PrefillPar
 
 }  // namespace
 
-size_t prefill_split_bytes(int sms) {
-    const size_t parts = size_t(sms) / 2;
-    return prefill_part_offset(sms) + parts * 4 * kTile * (kPrefillDv + 1) * sizeof(float);
+size_t prefill_split_bytes(int sms) {  // a slot of 512 rows for each part
+    return prefill_part_offset(sms) + prefill_max_parts(sms) * 4 * kTile * (kPrefillDv + 1) * sizeof(float);
 }
 size_t prefill_part_offset(int sms) {  // the pair of counts and the units, before the parts
     return (16 + size_t(sms) / 2 * sizeof(SplitUnit) + 255) / 256 * 256;
 }
+size_t prefill_max_parts(int sms) { return size_t(sms) / 2 * kRounds; }
 
 cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t stream) {
     static SmemLimitOnce smem_limit, smem_limit_split;
@@ -1163,16 +1190,20 @@ cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cud
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     const int64_t most = int64_t(p.slots) * p.heads;  // at least the number of units
-    // Splitting needs units that leave half the clusters without one and a request of two parts' entries;
-    // the kernel, which sees the lengths, decides.  Where the arguments rule it out, the second launch (2 us)
-    // is not made.
-    const int64_t least = int64_t(p.q_rows) * p.heads / kPrefillBlock;  // units, where every row is used
-    const bool split = p.o_part && most <= 2 * fit && least <= fit / 2 && p.kv_rows >= 2 * kPartTiles * kTile;
+    // Cut where a batch of this batch's average request would be; the kernel, which sees the lengths, decides.
+    bool split = false;
+    if (p.o_part) {
+        const int rows = int((p.q_rows + p.batch - 1) / p.batch), entries = int(p.kv_rows / p.batch);
+        const int64_t units = Cut(rows, entries, p.heads).units() * int64_t(p.batch);
+        const int first = units > fit && rows > kPrefillBlock ? kPrefillBlock : rows;  // the last units are of
+        const int tiles = (entries - (rows - first) / p.entry_tokens + kTile - 1) / kTile;  // a prompt's first rows
+        split = parts_of(int(units % fit), tiles, fit) > 1;
+    }
     cfg.gridDim = dim3(2u * unsigned(most < fit && !split ? most : fit));
     if (!split) return cudaLaunchKernelEx(&cfg, mla_prefill_kernel<false>, m.q, m.kn, m.kr, m.v, m.kn16, m.kr16, m.v16, p);
     e = cudaLaunchKernelEx(&cfg, mla_prefill_kernel<true>, m.q, m.kn, m.kr, m.v, m.kn16, m.kr16, m.v16, p);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(unsigned(fit) / 2u, 4 * kTile / 8);
+    cfg.gridDim = dim3(unsigned(fit), 4 * kTile / 8);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, mla_prefill_merge_kernel, p);

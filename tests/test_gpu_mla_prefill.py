@@ -104,6 +104,16 @@ def test_prefill_split(gpu_lib, n, seq, e, heads):
     case.check(*run(gpu_lib, case))
 
 
+@pytest.mark.parametrize("new, seqs, e, heads", [([520], [9000], 1, 80), ([1024], [40000], 4, 64),
+                                                 ([300, 40, 513], [7000, 5000, 6600], 1, 33)])
+def test_prefill_split_last_round(gpu_lib, new, seqs, e, heads):
+    """More units than clusters: the ones behind the last whole round in parts, the others whole."""
+    case = Case(new, seqs, heads=heads, e=e, seed=heads)
+    some = [0, 1, heads // 2, heads - 2, heads - 1]
+    case.check(*run(gpu_lib, case, split=True), heads=some)
+    case.check(*run(gpu_lib, case), heads=some)
+
+
 def test_prefill_split_ragged(gpu_lib):
     """A long and a short request, one without rows and one shorter than its rows, in parts; the workspace
     reused by calls of other splits, the same bits again."""
