@@ -973,6 +973,8 @@ cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, mla_dense_kernel, q_map, kv_map, kr_map, o_map, p);
     if (e != cudaSuccess) return e;
+    // No request is split where none can have more blocks than are kept together.
+    if (p.table_width <= kMlaWholeBlocks) return cudaSuccess;
     // One row of CTAs per request, or, where they are fewer, per cut between ranges.  Few rows are split
     // many ways: more threads per row read more partials at a time.
     const int rows = (p.merge_by_cut ? p.groups : p.batch) * p.tokens;
