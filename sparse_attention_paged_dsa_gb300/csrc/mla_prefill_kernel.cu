@@ -46,7 +46,10 @@
 // 192-wide key is ever built, and every operand may be a strided view.
 //
 // What bounds it: the tensor cores: 20 MMA steps of 128 x 128 x 16 per SM for each
-// (128 rows, 128 entries), 1,280 SM cycles at full rate.
+// (128 rows, 128 entries), 1,280 SM cycles at full rate.  8192 rows of 32 heads: 407 us,
+// 1690 TFLOP/s, 0.88 of the measured bf16 rate; 1024 rows of 64 heads over 32,768
+// entries: 756 us, 0.94.  Short prompts are bound by a unit's ends: 32 prompts of 512
+// rows and 32 heads 143 us (0.62), 64 of 100 rows and 64 heads 120 (0.39 of the bytes).
 // Every wait is bounded (about 1 s) but the cluster barriers, which every thread
 // reaches; a timeout sets an error bit, the roles drain, and TMEM is freed.
 #include <cuda.h>
@@ -82,8 +85,10 @@ constexpr uint32_t kColOP = 256;  // O of tile i at 256 + 128 i
 constexpr float kRaiseLog2 = 20.0f;  // rounding is relative: weights may pass 1 by this much
 constexpr float kLn2P = 0.69314718055994531f;
 
-constexpr int kPartTiles = 4;        // key tiles a part has at least (2: no faster; 8: 20 heads, 2,064 entries 29 us, now 22)
-constexpr int kFewEntries = 768;     // see Cut: two heads a unit up to here (512: 146 us against 155), one above (1024: 80, 100)
+constexpr int kPartTiles = 4;        // key tiles a part has at least (2: no faster; 8: 64 rows of 20 heads
+                                     // over 2,064 entries took 29 us, now 24)
+constexpr int kFewEntries = 768;     // see Cut: two heads a unit up to here (prompts of 512 rows: 146 us
+                                     // against 155), one above (of 1024: 80 against 100)
 constexpr int kSortMost = 256;       // requests that are ordered by length, one a thread (more: as they come)
 constexpr int kInfoSlots = 4;
 constexpr int kInfoReaders = 11;     // every warp but the scheduler
