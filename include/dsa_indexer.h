@@ -59,11 +59,12 @@
  *     page id outside [0, num_pages) is not read and its positions score -inf.
  *     Each case sets a bit in the workspace error word (DSA_DEVERR_*).
  *   - Workspace: a caller-owned device buffer, 256-byte aligned, of at least
- *     dsa_indexer_workspace_size() bytes (every entry point accepts that
- *     size), zeroed once before first use (dsa_indexer_workspace_init or any
- *     memset to 0).  Its first 256 bytes hold the sticky device error word;
- *     the rest of them is reserved and stays zero.  Calls that share a
- *     workspace must be ordered on one stream.
+ *     dsa_indexer_workspace_size() bytes (every indexer entry point accepts
+ *     that size; the attention ones name theirs), zeroed once before first
+ *     use (dsa_indexer_workspace_init or any memset to 0).  Its first 256
+ *     bytes hold the sticky device error word; the rest of them is reserved
+ *     and stays zero.  Calls that share a workspace, replayed graphs too,
+ *     must be ordered on one stream.
  */
 #ifndef DSA_INDEXER_H
 #define DSA_INDEXER_H

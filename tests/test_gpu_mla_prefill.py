@@ -129,6 +129,52 @@ def test_prefill_split_ragged(gpu_lib):
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1]) and gpu_lib.get_error(ws) == 0
 
 
+@pytest.mark.parametrize("n, seq, e, heads", [(100, 30000, 4, 3), (300, 3001, 1, 2), (1, 9999, 1, 1)])
+def test_prefill_split_beside_nan(gpu_lib, n, seq, e, heads):
+    """Split, between rows and entries that belong to nobody: NaN there reaches nothing, and their
+    outputs stay as they are."""
+    import torch
+    pad = 9
+    case = Case([n], [seq], heads=heads, e=e, seed=n, pad=pad)
+    m = case.entries[0]
+    for t, rows in ((case.q, n), (case.kn, m), (case.v, m), (case.kr, m)):
+        t[:pad] = float("nan")
+        t[pad + rows:] = float("nan")
+    out = torch.full((n + 2 * pad, heads, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n + 2 * pad, heads), 7.0, device="cuda")
+    case.check(*run(gpu_lib, case, split=True, out=out, lse=lse))
+    for t in (out, lse):
+        assert torch.all(t[:pad] == 7.0) and torch.all(t[pad + n:] == 7.0)
+
+
+def test_prefill_and_decode_share_a_workspace(gpu_lib):
+    """One after another on one stream, captured and replayed: the same bits as on workspaces of their own."""
+    import torch
+    case = Case([50], [30000], heads=4, e=4, seed=31)
+    g = torch.Generator().manual_seed(32)
+    q = torch.randn(2, 64, 576, generator=g).to(torch.bfloat16).cuda()
+    kv = torch.randn(40, 64, 576, generator=g).to(torch.bfloat16).cuda()
+    table = torch.arange(64, dtype=torch.int32).remainder(40).view(2, 32).cuda()
+    seq = torch.tensor([8000, 3000], dtype=torch.int32).cuda()
+    ws = [gpu_lib.new_mla_workspace(2) for _ in range(3)]
+
+    def both(a, b):
+        o = gpu_lib.dsa_mla_prefill(*case.args(), entry_tokens=4, workspace=a)
+        d = gpu_lib.dsa_mla_decode(q, kv, table, seq, 8192, SCALE, workspace=b)
+        return [*o, *d, *gpu_lib.dsa_mla_prefill(*case.args(), entry_tokens=4, workspace=a)]
+
+    want = both(ws[0], ws[1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(ws[2], ws[2])
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert all(gpu_lib.get_error(w) == 0 for w in ws)
+
+
 def test_prefill_split_graph_lengths(gpu_lib):
     """Captured on one batch, replayed on lengths that are split otherwise, or not at all."""
     import torch

@@ -71,3 +71,11 @@ def call():
 ])
 def test_prefill_rejects_bad_arguments(call, over, status):
     assert call(**over) == status
+
+
+def test_prefill_workspace_size():
+    """More than the error word's header: room for the parts that rows are split into."""
+    from sparse_attention_paged_dsa_gb300 import build
+    f = ctypes.CDLL(build.build()).dsa_mla_prefill_workspace_size
+    f.argtypes, f.restype = [], SZ
+    assert f() > 256 + 64 * 512 * 129 * 4
