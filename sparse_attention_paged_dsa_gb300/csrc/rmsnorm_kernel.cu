@@ -21,8 +21,8 @@
 // 16-element units and packed fp32 pairs: 156; 40 registers, so that three CTAs of
 // one unit a thread are resident: 143; the next row fetched into L2: 123.  Without
 // a residual the e4m3 output is bound by its instructions (63 us, 0.83; one unit a
-// thread, and the codes after the norm: 73).  Rows off 16-byte boundaries are, too:
-// 16384 x 7001, residual, e4m3 out: 232 us, 0.51.
+// thread, and the codes after the norm: 73; 131072 x 512: 36 us, 0.82, from 46).  Rows
+// off 16-byte boundaries are, too: 16384 x 7001, residual, e4m3 out: 231 us, 0.51.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -320,11 +320,17 @@ __global__ void __launch_bounds__(kMaxT, kResidentOf<kNV, kMaxT, kAlign>) rmsnor
     float2 h[kNV][kPairs];
     uint32_t g[kNV][kPairs];
     pdl_wait_prior_grid();
-    // The row that takes this CTA's place is fetched into L2 now: what is in flight no longer ends with
-    // the resident CTAs' registers.
-    if (kCtaRow && threadIdx.x == 0 && row + p.ahead < p.rows) {
-        l2_prefetch(static_cast<const uint16_t*>(p.x) + (row + p.ahead) * p.x_stride, p.d);
-        if (p.residual) l2_prefetch(static_cast<const uint16_t*>(p.residual) + (row + p.ahead) * p.d, p.d);
+    // The rows of the CTA that takes this one's place are fetched into L2 now: what is in flight no longer
+    // ends with the resident CTAs' registers.  (Short rows without codes leave by themselves soon enough:
+    // 131072 x 512 44 us with it, 41 without; with codes 36 against 42.)
+    if ((kCtaRow || kGroupLanes > 0) && threadIdx.x == 0) {
+        const int64_t rows = kCtaRow ? 1 : kCta >> p.log2_threads, next = int64_t(blockIdx.x) * rows + p.ahead;
+        if (next < p.rows && (kCtaRow || p.x_stride < 2 * p.d)) {
+            const int64_t more = (rows < p.rows - next ? rows : p.rows - next) - 1;
+            l2_prefetch(static_cast<const uint16_t*>(p.x) + next * p.x_stride, int(more * p.x_stride) + p.d);
+            if (p.residual)
+                l2_prefetch(static_cast<const uint16_t*>(p.residual) + next * p.d, int(more + 1) * p.d);
+        }
     }
     {
         uint32_t x[kNV][kPairs], r[kNV][kPairs];
@@ -447,19 +453,23 @@ cudaError_t launch_nv(const RmsNormParams& p, int align, unsigned grid, unsigned
 cudaError_t launch_rmsnorm(RmsNormParams p, int align, int sms, cudaStream_t stream) {
     const int units = (p.d + kUnit - 1) / kUnit;
     p.inv_d = 1.f / float(p.d);
+    const bool bare = p.codes && !p.residual;  // little to load for what there is to compute
     if (units <= 64) {  // at most one warp per row, two units a thread above 32
-        int T = align == 16 ? 4 : 1;  // 16-byte halves are shared by four threads
-        while (T < units && T < 32) T *= 2;
+        const int nv = units > 32 || (bare && units > 8) ? 2 : 1;  // (see below)
+        // 16-byte halves are shared by four threads; a group of 128 elements is eight with a unit each
+        int T = nv == 2 ? 8 : align == 16 ? 4 : 1;
+        while (T * nv < units && T < 32) T *= 2;
         p.row_threads = T;
         p.log2_threads = 31 - __builtin_clz(unsigned(T));
         const unsigned grid = unsigned((p.rows + kCta / T - 1) / (kCta / T));
-        return units <= 32 ? launch_nv<1, false, kCta>(p, align, grid, kCta, stream)
-                           : launch_nv<2, false, kCta>(p, align, grid, kCta, stream);
+        p.ahead = sms * (nv == 1 ? kResidentOf<1, kCta, 32> : kResidentOf<2, kCta, 32>) * (kCta / T);
+        return nv == 1 ? launch_nv<1, false, kCta>(p, align, grid, kCta, stream)
+                       : launch_nv<2, false, kCta>(p, align, grid, kCta, stream);
     }
     // One CTA per row.  Two units a thread where a row does not fit one, and where instructions are the
-    // bound, which two share (16384 x 7168 without a residual, e4m3 out: 64 us against 71; with one, and so
-    // more to load, 129 against 123).
-    const int nv = units > 1024 || (units <= 512 && p.codes && !p.residual) ? 2 : 1;
+    // bound, which two share (16384 x 7168 without a residual, e4m3 out: 63 us against 71, 262144 x 256 39
+    // against 43; with one, and so more to load, 129 against 123).
+    const int nv = units > 1024 || (units <= 512 && bare) ? 2 : 1;
     const unsigned T = unsigned((units + nv - 1) / nv + 31) / 32 * 32, grid = unsigned(p.rows);
     p.row_threads = int(T);
     const auto run = [&](auto kernel_nv, auto max_t) {
