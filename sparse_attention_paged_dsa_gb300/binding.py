@@ -514,10 +514,11 @@ PREFILL_QK, PREFILL_NOPE, PREFILL_ROPE, PREFILL_DV = 192, 128, 64, 128
 
 
 def _strided(t, name, shape, device: int):
-    """A bf16 tensor of ``shape`` on ``device`` whose last dimension is contiguous (other strides are free)."""
-    if (isinstance(t, torch.Tensor) and t.dtype in _BF16 and t.shape == shape and t.get_device() == device
-            and t.stride(-1) == 1):
-        return
+    """The strides of a bf16 tensor of ``shape`` on ``device`` whose last dimension is contiguous (others are free)."""
+    if isinstance(t, torch.Tensor) and t.dtype in _BF16 and t.shape == shape and t.get_device() == device:
+        strides = t.stride()  # (one call for all: stride(i) costs more than the tuple)
+        if strides[-1] == 1:
+            return strides
     _device_of(t, name, _BF16, (len(shape),))
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
@@ -537,11 +538,11 @@ def dsa_mla_prefill(q, k_nope, k_rope, v, cu_q, cu_kv, seq_lens, sm_scale: float
     bytes, zeroed once; with ``prefill_workspace_size()`` (the default) few rows may be split along their entries."""
     dev = _device_of(q, "q", _BF16, (3,))
     _device_of(v, "v", _BF16, (3,))
-    Tq, H, Tk = q.shape[0], q.shape[1], v.shape[0]
-    _strided(q, "q", (Tq, H, PREFILL_QK), dev)
-    _strided(k_nope, "k_nope", (Tk, H, PREFILL_NOPE), dev)
-    _strided(k_rope, "k_rope", (Tk, PREFILL_ROPE), dev)
-    _strided(v, "v", (Tk, H, PREFILL_DV), dev)
+    (Tq, H, _), Tk = q.shape, v.shape[0]
+    q_row, q_head, _ = _strided(q, "q", (Tq, H, PREFILL_QK), dev)
+    k_row, k_head, _ = _strided(k_nope, "k_nope", (Tk, H, PREFILL_NOPE), dev)
+    r_row, _ = _strided(k_rope, "k_rope", (Tk, PREFILL_ROPE), dev)
+    v_row, v_head, _ = _strided(v, "v", (Tk, H, PREFILL_DV), dev)
     B = seq_lens.numel() if isinstance(seq_lens, torch.Tensor) else 0
     _on(seq_lens, "seq_lens", _I32, (B,), dev)
     _on(cu_q, "cu_q", _I32, (B + 1,), dev)
@@ -558,10 +559,10 @@ def dsa_mla_prefill(q, k_nope, k_rope, v, cu_q, cu_kv, seq_lens, sm_scale: float
         with torch.cuda.device(q.device):
             workspace = torch.empty(prefill_workspace_size(), dtype=torch.uint8, device=q.device)
         workspace[:WORKSPACE_HEADER_BYTES].zero_()
-    _run(load().dsa_mla_prefill, dev, q.data_ptr(), q.stride(0), q.stride(1), k_nope.data_ptr(), k_nope.stride(0),
-         k_nope.stride(1), k_rope.data_ptr(), k_rope.stride(0), v.data_ptr(), v.stride(0), v.stride(1),
-         cu_q.data_ptr(), cu_kv.data_ptr(), seq_lens.data_ptr(), B, H, Tq, Tk, entry_tokens, sm_scale,
-         out.data_ptr(), lse.data_ptr(), *_space(workspace, dev))
+    _run(load().dsa_mla_prefill, dev, q.data_ptr(), q_row, q_head, k_nope.data_ptr(), k_row, k_head,
+         k_rope.data_ptr(), r_row, v.data_ptr(), v_row, v_head, cu_q.data_ptr(), cu_kv.data_ptr(),
+         seq_lens.data_ptr(), B, H, Tq, Tk, entry_tokens, sm_scale, out.data_ptr(), lse.data_ptr(),
+         *_space(workspace, dev))
     return out, lse
 
 
@@ -572,18 +573,19 @@ def _norm_args(x, weight, residual, residual_out):
     dev = _device_of(x, "x", _BF16, (2,))
     shape = x.shape
     rows, d = shape
-    if d > 1 and x.stride(1) != 1:
+    stride, inner = x.stride()
+    if inner != 1 and d > 1:
         raise ValueError("the elements of a row of x must be contiguous")
     _on(weight, "weight", _NORM_WEIGHT, (d,), dev)
     if residual is not None:
         _on(residual, "residual", _BF16, shape, dev)
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+            residual_out = torch.empty_like(residual)
         else:
             _on(residual_out, "residual_out", _BF16, shape, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    return dev, rows, d, int(weight.dtype == torch.float32), residual_out
+    return dev, rows, d, stride, int(weight.dtype == torch.float32), residual_out
 
 
 def dsa_rmsnorm(x, weight, eps: float, residual=None, out=None, residual_out=None):
@@ -591,12 +593,12 @@ def dsa_rmsnorm(x, weight, eps: float, residual=None, out=None, residual_out=Non
 
     x [rows, d] bf16 (rows may be strided, as a view of wider rows is), weight [d] bf16 or fp32.
     ``out`` and ``residual_out`` may be ``x`` and ``residual`` themselves."""
-    dev, rows, d, w32, residual_out = _norm_args(x, weight, residual, residual_out)
+    dev, rows, d, stride, w32, residual_out = _norm_args(x, weight, residual, residual_out)
     if out is None:
         out = torch.empty((rows, d), dtype=torch.bfloat16, device=x.device)
     else:
         _on(out, "out", _BF16, (rows, d), dev)
-    _run(load().dsa_rmsnorm, dev, x.data_ptr(), x.stride(0), _addr(residual), weight.data_ptr(), w32, rows, d, eps,
+    _run(load().dsa_rmsnorm, dev, x.data_ptr(), stride, _addr(residual), weight.data_ptr(), w32, rows, d, eps,
          _addr(residual_out), out.data_ptr())
     return out, residual_out
 
@@ -607,7 +609,7 @@ def dsa_rmsnorm_fp8(x, weight, eps: float, group: int, residual=None, with_bf16:
 
     ``group`` 64 or 128 elements per scale, or 0 for one scale per row; ``out`` (bf16) is written
     when given or with ``with_bf16``.  Rows of 64 with group 64 are the fp8 index-key cache's format."""
-    dev, rows, d, w32, residual_out = _norm_args(x, weight, residual, residual_out)
+    dev, rows, d, stride, w32, residual_out = _norm_args(x, weight, residual, residual_out)
     if group not in (0, 64, 128):
         raise ValueError(f"group must be 0, 64 or 128, got {group}")
     if out is not None:
@@ -623,7 +625,7 @@ def dsa_rmsnorm_fp8(x, weight, eps: float, group: int, residual=None, with_bf16:
         scales = torch.empty((rows, groups), dtype=torch.float32, device=x.device)
     else:
         _on(scales, "scales", _F32, (rows, groups), dev)
-    _run(load().dsa_rmsnorm_fp8, dev, x.data_ptr(), x.stride(0), _addr(residual), weight.data_ptr(), w32, rows, d,
+    _run(load().dsa_rmsnorm_fp8, dev, x.data_ptr(), stride, _addr(residual), weight.data_ptr(), w32, rows, d,
          eps, group, _addr(residual_out), _addr(out), codes.data_ptr(), scales.data_ptr())
     return codes, scales, out, residual_out
 
