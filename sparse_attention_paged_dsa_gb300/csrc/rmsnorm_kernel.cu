@@ -454,7 +454,9 @@ cudaError_t launch_rmsnorm(RmsNormParams p, int align, int sms, cudaStream_t str
     const int units = (p.d + kUnit - 1) / kUnit;
     p.inv_d = 1.f / float(p.d);
     const bool bare = p.codes && !p.residual;  // little to load for what there is to compute
-    if (units <= 64) {  // at most one warp per row, two units a thread above 32
+    // At most one warp per row, two units a thread above 32; with a residual, rows that fill two warps take
+    // them (65536 x 1024, e4m3 out: 70 us against 76; 131072 x 640 135 against 89).
+    if (units <= (p.residual ? 48 : 64)) {
         const int nv = units > 32 || (bare && units > 8) ? 2 : 1;  // (see below)
         // 16-byte halves are shared by four threads; a group of 128 elements is eight with a unit each
         int T = nv == 2 ? 8 : align == 16 ? 4 : 1;
