@@ -24,7 +24,7 @@
 // along their entries where that pays (parts_of); parts leave fp32 outputs and a second
 // kernel joins them by log-sum-exp (one row of 64 heads over 16,385 entries: 136 us,
 // uncut 249; 300 rows of two heads over 33,068: 42, uncut 386; 128 units of 256 key
-// tiles: 756, uncut 805).  Units of equal cost laid end to end and cut once per cluster
+// tiles: 750, uncut 805).  Units of equal cost laid end to end and cut once per cluster
 // balance better, but cost more to find and to join: 735 there, 8192 rows of 32 heads
 // 484 against 407.  A scheduler warp looks the units up.  Roles of a CTA (384 threads):
 //   * warps 0-3 and 4-7: softmax of query tile 0 and 1, one row per thread: the
@@ -48,7 +48,7 @@
 // What bounds it: the tensor cores: 20 MMA steps of 128 x 128 x 16 per SM for each
 // (128 rows, 128 entries), 1,280 SM cycles at full rate.  8192 rows of 32 heads: 407 us,
 // 1690 TFLOP/s, 0.88 of the measured bf16 rate; 1024 rows of 64 heads over 32,768
-// entries: 756 us, 0.94.  Short prompts are bound by a unit's ends: 32 prompts of 512
+// entries: 750 us, 0.95.  Short prompts are bound by a unit's ends: 32 prompts of 512
 // rows and 32 heads 143 us (0.62), 64 of 100 rows and 64 heads 120 (0.39 of the bytes).
 // Every wait is bounded (about 1 s) but the cluster barriers, which every thread
 // reaches; a timeout sets an error bit, the roles drain, and TMEM is freed.
@@ -327,9 +327,14 @@ __device__ __forceinline__ Unit unit_of(const PrefillParams& p, const Request& r
         u.step_head = 1;
     } else {
         at -= cut.pair_blocks * cut.pairs();
-        u.row0 = (cut.long_blocks - 1 - at / p.heads) * kPrefillBlock;
+        // Where the blocks see about equally many entries (a chunk on a long past), a head's blocks follow one
+        // another, so that its keys and values are in L2 for all but the first (1024 rows of 64 heads over
+        // 32,768 entries in a long run, which power limits: 871 -> 838 us; alone 756 -> 750).
+        const bool alike = rq.seen(kPrefillBlock - 1, p.entry_tokens) >= rq.live - rq.live / 4;
+        const int block = alike ? at % cut.long_blocks : at / p.heads;
+        u.row0 = (cut.long_blocks - 1 - block) * kPrefillBlock;
         u.rows = min(rq.rows - u.row0, kPrefillBlock);
-        u.head = at % p.heads;
+        u.head = alike ? at / cut.long_blocks : at % p.heads;
         u.step_row = 2 * kTile;
     }
     u.q_row = rq.q0 + u.row0;
