@@ -130,12 +130,15 @@ struct __align__(8) PrefillCtl {
     uint64_t all_done;
     uint32_t tmem_base;
     int abort;
-    int total, parts;                  // pieces of work; parts of each unit behind the whole ones
+    int total, list;                   // units; entries of the list below
     int warp_units[kThreadsP / 32];
     Unit info[kInfoSlots];
-    int first[kMaxBatch];              // first unit of the i-th request in the order
-    int16_t order[kMaxBatch];          // that request
-    int key[kSortMost];
+    int first[kMaxBatch];              // first unit of the i-th entry of the list
+    int order[kMaxBatch];              // its request, the kind of order, and its first unit there (ListEntry)
+    union {
+        int live[kSortMost];
+        uint16_t tiles[2 * kSortMost];
+    } key;
 };
 constexpr int kSmemP = 1024 + kOffCtlP + int(sizeof(PrefillCtl));
 static_assert(kSmemP <= 232448, "fits one CTA per SM");
@@ -303,21 +306,30 @@ struct Cut {
     __host__ __device__ __forceinline__ int units() const { return pair_blocks * pairs() + long_blocks * heads; }
 };
 
-// The last request (in the order) that starts at or before unit n: 32-way, twice.  (Requests without rows
-// start where the next one does: the last of them is the owner.)
-__device__ __forceinline__ int request_at(const PrefillParams& p, const PrefillCtl& ctl, int n, int lane) {
-    int lo = 0;
-    for (int span = 32; span >= 1; span /= 32) {
-        const int at = lo + lane * span;
-        const bool before = at < p.batch && ctl.first[at] <= n;
-        lo += span * (__popc(__ballot_sync(0xffffffffu, before)) - 1);
-    }
-    return lo;
+// Do a request's blocks of 512 rows see about equally many entries (a chunk on a long past)?  A head's
+// blocks then follow one another, so that its keys and values are in L2 for all but the first (1024 rows of
+// 64 heads over 32,768 entries in a long run, which power limits: 871 -> 838 us; alone 756 -> 750).
+__device__ __forceinline__ bool blocks_alike(const PrefillParams& p, const Request& rq) {
+    return rq.seen(kPrefillBlock - 1, p.entry_tokens) >= rq.live - rq.live / 4;
+}
+// Groups of a request's units, in their order: a block each, or all the alike ones.
+__device__ __forceinline__ int groups_of(const PrefillParams& p, const Request& rq, const Cut& cut) {
+    return cut.pair_blocks + (cut.long_blocks > 1 && blocks_alike(p, rq) ? 1 : cut.long_blocks);
+}
+__device__ __forceinline__ int group_start(const Cut& cut, int group) {
+    return min(group, cut.pair_blocks) * cut.pairs() + max(group - cut.pair_blocks, 0) * cut.heads;
+}
+// Key tiles of a group's (longest) units.
+__device__ __forceinline__ int group_tiles(const PrefillParams& p, const Request& rq, const Cut& cut, int group) {
+    const int pair = cut.pair_blocks - 1 - group;
+    const int end = pair >= 0 ? cut.long_blocks * kPrefillBlock + (pair + 1) * 2 * kTile
+                              : (cut.long_blocks + pair + 1) * kPrefillBlock;
+    return (rq.seen(min(end, rq.rows) - 1, p.entry_tokens) + kTile - 1) / kTile;
 }
 
 // The request's unit number `at`, last rows (the longest) first: the blocks for two heads lie behind the
 // long ones.
-__device__ __forceinline__ Unit unit_of(const PrefillParams& p, const Request& rq, int at) {
+__device__ __forceinline__ Unit unit_of(const PrefillParams& p, const Request& rq, bool alike, int at) {
     const Cut cut(rq, p.heads);
     Unit u = {};
     if (at < cut.pair_blocks * cut.pairs()) {
@@ -327,10 +339,6 @@ __device__ __forceinline__ Unit unit_of(const PrefillParams& p, const Request& r
         u.step_head = 1;
     } else {
         at -= cut.pair_blocks * cut.pairs();
-        // Where the blocks see about equally many entries (a chunk on a long past), a head's blocks follow one
-        // another, so that its keys and values are in L2 for all but the first (1024 rows of 64 heads over
-        // 32,768 entries in a long run, which power limits: 871 -> 838 us; alone 756 -> 750).
-        const bool alike = rq.seen(kPrefillBlock - 1, p.entry_tokens) >= rq.live - rq.live / 4;
         const int block = alike ? at % cut.long_blocks : at / p.heads;
         u.row0 = (cut.long_blocks - 1 - block) * kPrefillBlock;
         u.rows = min(rq.rows - u.row0, kPrefillBlock);
@@ -347,6 +355,24 @@ __device__ __forceinline__ Unit unit_of(const PrefillParams& p, const Request& r
     }
     u.part = -1;
     return u;
+}
+
+// An entry of the list: units of a request from number `start` on (16 bits: of at most 384 groups of 128).
+__device__ __forceinline__ int list_entry(int request, bool alike, int start) {
+    return request << 17 | int(alike) << 16 | start;
+}
+// Unit n of the list, for a whole warp.
+__device__ __forceinline__ Unit unit_at(const PrefillParams& p, const PrefillCtl& ctl, int n, int lane) {
+    int lo = 0;  // the last entry that starts at or before it: 32-way, twice
+    for (int span = 32; span >= 1; span /= 32) {
+        const int at = lo + lane * span;
+        const bool before = at < ctl.list && ctl.first[at] <= n;
+        lo += span * (__popc(__ballot_sync(0xffffffffu, before)) - 1);
+    }
+    // requests without rows start where the next one does: the last of them is the owner
+    const int entry = ctl.order[lo];
+    uint32_t ignored = 0;
+    return unit_of(p, Request(p, entry >> 17, ignored), (entry >> 16) & 1, n - ctl.first[lo] + (entry & 0xFFFF));
 }
 
 // Into how many parts to cut each of `units` units of `tiles` key tiles, the last ones, which would leave
@@ -368,7 +394,8 @@ __host__ __device__ __forceinline__ int parts_of(int units, int tiles, int clust
 
 // kSplit: units may be cut into parts.  (In a kernel of its own: the choice made at run time in one took
 // 64 prompts of 100 rows, which are not cut, from 119 to 131 us.)
-template <bool kSplit>
+// kGroups: several long prompts, whose units are ordered by their groups.
+template <bool kSplit, bool kGroups>
 __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kn_map,
                        const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap v_map,
@@ -422,56 +449,97 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
 
-    // The order of the requests (longest first, where they are few) and where their units start.
+    // The list of the units: longest requests first, their last rows first; several long prompts by their
+    // groups of units instead, longest first (four prompts of 2048 rows, 8 heads: 52 us, by requests 56; of
+    // 5378 rows, 5 heads: 138, 175).  Many requests as they come.
     uint32_t bad = 0;
-    for (int b = threadIdx.x; b < p.batch; b += kThreadsP) {
+    const int me = threadIdx.x;
+    int groups = 0;
+    for (int b = me; b < p.batch; b += kThreadsP) {
         const Request r(p, b, bad);
-        ctl.first[b] = Cut(r, p.heads).units();
-        ctl.order[b] = int16_t(b);
-        if (b < kSortMost) ctl.key[b] = r.rows > 0 ? r.live : -1;
+        const Cut cut(r, p.heads);
+        ctl.first[b] = cut.units();
+        ctl.order[b] = list_entry(b, blocks_alike(p, r), 0);
+        if (b < kSortMost) ctl.key.live[b] = r.rows > 0 ? r.live : -1;
+        if constexpr (kGroups) groups = groups_of(p, r, cut);  // (a thread has one request)
     }
     if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
-    __syncthreads();
-    if (p.batch > 1 && p.batch <= kSortMost) {
-        const int b = threadIdx.x;
-        int at = 0, units = 0;
-        if (b < p.batch) {
-            const int key = ctl.key[b];
-            units = ctl.first[b];
-            for (int o = 0; o < p.batch; ++o) at += ctl.key[o] > key || (ctl.key[o] == key && o < b);
-        }
-        __syncthreads();
-        if (b < p.batch) {
-            ctl.order[at] = int16_t(b);
-            ctl.first[at] = units;
-        }
-        __syncthreads();
-    }
-    const int per = (p.batch + kThreadsP - 1) / kThreadsP;
-    const int i0 = min(int(threadIdx.x) * per, p.batch), i1 = min(i0 + per, p.batch);
-    int mine = 0;
-    for (int i = i0; i < i1; ++i) mine += ctl.first[i];
-    int incl = mine;
+    // Sum over the threads before this one, and over all of them.
+    const auto scan = [&](int mine, int& total) {
+        int incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) ctl.warp_units[warp] = incl;
-    __syncthreads();
-    {
-        int before = incl - mine, total = 0;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) ctl.warp_units[warp] = incl;
+        __syncthreads();
+        int before = incl - mine;
+        total = 0;
         for (int w = 0; w < kThreadsP / 32; ++w) {
             if (w < warp) before += ctl.warp_units[w];
             total += ctl.warp_units[w];
         }
-        for (int i = i0; i < i1; ++i) {
-            const int units = ctl.first[i];
-            ctl.first[i] = before;
-            before += units;
+        return before;
+    };
+    int list = p.batch;
+    if (p.batch > 1 && p.batch <= kSortMost) {
+        bool by_groups = false;
+        if constexpr (kGroups) {
+            int all = 0;
+            const int start = scan(groups, all);
+            by_groups = all <= kThreadsP;
+            if (by_groups) {
+                if (me < p.batch) ctl.order[me] = start;
+                list = all;
+            }
         }
-        if (threadIdx.x == 0) ctl.total = total;
+        __syncthreads();
+        int entry = 0, units = 0, key = 0, at = 0;
+        if (me < list) {
+            if (by_groups) {
+                int b = 0;
+                for (int step = kSortMost / 2; step > 0; step >>= 1)
+                    if (b + step < p.batch && ctl.order[b + step] <= me) b += step;
+                const int group = me - ctl.order[b];
+                uint32_t ignored = 0;
+                const Request r(p, b, ignored);
+                const Cut cut(r, p.heads);
+                const bool last = group + 1 == groups_of(p, r, cut);
+                const int from = group_start(cut, group);
+                units = (last ? cut.units() : group_start(cut, group + 1)) - from;
+                key = min(group_tiles(p, r, cut, group), 0xFFFF);
+                entry = list_entry(b, blocks_alike(p, r), from);
+            } else {
+                units = ctl.first[me], entry = ctl.order[me], key = ctl.key.live[me];
+            }
+        }
+        if (by_groups) {
+            if (me < list) ctl.key.tiles[me] = uint16_t(key);
+            __syncthreads();
+            if (me < list)
+                for (int o = 0; o < list; ++o) at += ctl.key.tiles[o] > key || (ctl.key.tiles[o] == key && o < me);
+        } else if (me < list) {
+            for (int o = 0; o < list; ++o) at += ctl.key.live[o] > key || (ctl.key.live[o] == key && o < me);
+        }
+        __syncthreads();
+        if (me < list) {
+            ctl.order[at] = entry;
+            ctl.first[at] = units;
+        }
     }
+    __syncthreads();
+    const int per = (list + kThreadsP - 1) / kThreadsP;
+    const int i0 = min(me * per, list), i1 = min(i0 + per, list);
+    int mine = 0, total_units = 0;
+    for (int i = i0; i < i1; ++i) mine += ctl.first[i];
+    int before = scan(mine, total_units);
+    for (int i = i0; i < i1; ++i) {
+        const int units = ctl.first[i];
+        ctl.first[i] = before;
+        before += units;
+    }
+    if (me == 0) ctl.total = total_units, ctl.list = list;
     __syncwarp();
     cluster_wait();  // the other CTA's barriers are set up too
     __syncthreads();
@@ -501,10 +569,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
         int total = ctl.total, whole = total, parts = 1;
         if (kSplit && total > 0) {
             const int left = total % clusters;
-            uint32_t ignored = 0;
-            const int lo = request_at(p, ctl, total - left, lane);
-            const Request rq(p, int(ctl.order[lo]), ignored);
-            if (left > 0) parts = parts_of(left, unit_of(p, rq, total - left - ctl.first[lo]).nt(), clusters);
+            if (left > 0) parts = parts_of(left, unit_at(p, ctl, total - left, lane).nt(), clusters);
             if (parts > 1) whole = total - left, total = whole + left * parts;
         }
         if (kSplit && blockIdx.x == 0 && lane == 0) *p.split = make_int2(ctl.total - whole, parts);
@@ -519,10 +584,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             if (more) {
                 const int past = max(int(n) - whole, 0), part = past % parts;  // (1 part: 0)
                 const int at = min(int(n), whole) + past / parts;
-                const int lo = request_at(p, ctl, at, lane);
-                uint32_t ignored = 0;
-                const Request rq(p, int(ctl.order[lo]), ignored);
-                u = unit_of(p, rq, at - ctl.first[lo]);
+                u = unit_at(p, ctl, at, lane);
                 if (kSplit && parts > 1 && int(n) >= whole) {
                     u.part = past;
                     if (part == 0 && rank == 0 && lane == 0) {
@@ -1170,12 +1232,13 @@ size_t prefill_part_offset(int sms) {  // the pair of counts and the units, befo
 size_t prefill_max_parts(int sms) { return size_t(sms) / 2 * kRounds; }
 
 cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t stream) {
-    static SmemLimitOnce smem_limit, smem_limit_split;
+    static SmemLimitOnce smem_limit, smem_limit_split, smem_limit_groups;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    e = smem_limit.apply(dev, mla_prefill_kernel<false>, kSmemP);
-    if (e == cudaSuccess) e = smem_limit_split.apply(dev, mla_prefill_kernel<true>, kSmemP);
+    e = smem_limit.apply(dev, mla_prefill_kernel<false, false>, kSmemP);
+    if (e == cudaSuccess) e = smem_limit_split.apply(dev, mla_prefill_kernel<true, false>, kSmemP);
+    if (e == cudaSuccess) e = smem_limit_groups.apply(dev, mla_prefill_kernel<false, true>, kSmemP);
     if (e != cudaSuccess) return e;
     // Persistent clusters: as many as the device holds (its SMs do not all pair up), or one per unit.
     static std::atomic<int> resident[kMaxDevices];
@@ -1192,7 +1255,7 @@ cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cud
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        e = cudaOccupancyMaxActiveClusters(&fit, mla_prefill_kernel<false>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&fit, mla_prefill_kernel<false, false>, &cfg);
         if (e != cudaSuccess) return e;
         if (fit < 1) return cudaErrorInvalidConfiguration;
         resident[dev].store(fit, std::memory_order_relaxed);
@@ -1210,8 +1273,13 @@ cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cud
         split = parts_of(int(units % fit), tiles, fit) > 1;
     }
     cfg.gridDim = dim3(2u * unsigned(most < fit && !split ? most : fit));
-    if (!split) return cudaLaunchKernelEx(&cfg, mla_prefill_kernel<false>, m.q, m.kn, m.kr, m.v, m.kn16, m.kr16, m.v16, p);
-    e = cudaLaunchKernelEx(&cfg, mla_prefill_kernel<true>, m.q, m.kn, m.kr, m.v, m.kn16, m.kr16, m.v16, p);
+    if (!split) {
+        // Several prompts of more than a block on average (shorter ones lose what finding the groups takes).
+        const bool groups = p.batch > 1 && p.batch <= kSortMost && p.q_rows > p.batch * kPrefillBlock;
+        return cudaLaunchKernelEx(&cfg, groups ? mla_prefill_kernel<false, true> : mla_prefill_kernel<false, false>, m.q,
+                                  m.kn, m.kr, m.v, m.kn16, m.kr16, m.v16, p);
+    }
+    e = cudaLaunchKernelEx(&cfg, mla_prefill_kernel<true, false>, m.q, m.kn, m.kr, m.v, m.kn16, m.kr16, m.v16, p);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(unsigned(fit), 4 * kTile / 8);
     cfg.blockDim = dim3(256);

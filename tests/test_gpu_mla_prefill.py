@@ -114,6 +114,22 @@ def test_prefill_split_last_round(gpu_lib, new, seqs, e, heads):
     case.check(*run(gpu_lib, case), heads=some)
 
 
+@pytest.mark.parametrize("new, seqs, e, heads", [([1500, 700, 0, 2100, 600], [1500, 700, 5, 2100, 650], 1, 3),
+                                                 ([1300, 900, 1100], [60000, 900, 4000], 4, 2),
+                                                 ([2049, 1, 513, 2000], [2049, 3000, 513, 1500], 1, 7)])
+def test_prefill_long_prompts(gpu_lib, new, seqs, e, heads):
+    """Several prompts of more than a block of rows: their units ordered across requests, those of a chunk
+    on a long past head by head."""
+    case = Case(new, seqs, heads=heads, e=e, seed=sum(new))
+    case.check(*run(gpu_lib, case))
+
+
+def test_prefill_long_prompts_many(gpu_lib):
+    """More groups of units than there are threads to order them."""
+    case = Case([520 + b % 3 for b in range(200)], [520 + b % 7 for b in range(200)], heads=1, e=1, seed=41)
+    case.check(*run(gpu_lib, case), requests=range(0, 200, 9))
+
+
 def test_prefill_split_ragged(gpu_lib):
     """A long and a short request, one without rows and one shorter than its rows, in parts; the workspace
     reused by calls of other splits, the same bits again."""
