@@ -367,6 +367,55 @@ def test_prefill_bad_ranges(gpu_lib):
     assert torch.equal(out[rows(2)], good[0][rows(2)])
 
 
+@pytest.mark.parametrize("new, seqs", [([60, 40, 30], [9000, 5000, 7000]), ([700, 900, 1200], [700, 900, 1200])])
+def test_prefill_bad_ranges_split_and_ordered(gpu_lib, new, seqs):
+    """The same where rows are split along their entries, and where units are ordered across requests."""
+    import torch
+    case = Case(new, seqs, heads=2, seed=15)
+    run(gpu_lib, case, split=True)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = gpu_lib.new_mla_workspace(1)
+    cu_q, cu_kv = case.cu_q_l, case.cu_kv_l
+    for bad_q, bad_kv, bad_seq, wrong in ((cu_q[:3] + [1 << 30], cu_kv, seqs, 2), ([-5] + cu_q[1:], cu_kv, seqs, 0),
+                                          (cu_q, cu_kv[:3] + [case.v.shape[0] + 1], seqs, 2),
+                                          (cu_q, cu_kv, [seqs[0] + 1] + seqs[1:], 0), (cu_q, cu_kv, [-3] + seqs[1:], 0)):
+        out = torch.full((sum(new), 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((sum(new), 2), 7.0, device="cuda")
+        gpu_lib.dsa_mla_prefill(case.q, case.kn, case.kr, case.v, i32(bad_q), i32(bad_kv), i32(bad_seq), case.scale,
+                                entry_tokens=1, out=out, lse=lse, workspace=ws)
+        want = gpu_lib.DEVERR_SEQ_LEN_CLAMPED if bad_seq[0] < 0 else gpu_lib.DEVERR_BAD_RANGE
+        assert gpu_lib.get_error(ws) == want
+        case.check(out, lse, requests=[b for b in range(3) if b != wrong])
+
+
+def test_prefill_split_two_streams(gpu_lib):
+    """Two split calls, a decode and a norm at once on their own streams and workspaces: the same bits as alone."""
+    import torch
+    a, b = Case([9], [40000], heads=2, e=1, seed=16), Case([300], [20000], heads=3, e=4, seed=17)
+    g = torch.Generator().manual_seed(18)
+    q, kv = (torch.randn(*s, generator=g).to(torch.bfloat16).cuda() for s in ((4, 64, 576), (64, 64, 576)))
+    table = torch.arange(128, dtype=torch.int32).remainder(64).view(4, 32).cuda()
+    seq = torch.tensor([8000, 100, 3000, 0], dtype=torch.int32).cuda()
+    x = torch.randn(3000, 512, generator=g).to(torch.bfloat16).cuda()
+    calls = [lambda ws: gpu_lib.dsa_mla_prefill(*a.args(), entry_tokens=1, workspace=ws),
+             lambda ws: gpu_lib.dsa_mla_prefill(*b.args(), entry_tokens=4, workspace=ws),
+             lambda ws: gpu_lib.dsa_mla_decode(q, kv, table, seq, 8192, SCALE, workspace=ws),
+             lambda ws: gpu_lib.dsa_rmsnorm_fp8(x, x[0].contiguous(), 1e-6, 128)[:2]]
+    spaces = [gpu_lib.new_mla_workspace(4) for _ in calls]
+    want = [[t.clone() for t in f(ws)] for f, ws in zip(calls, spaces)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(10):
+        got = []
+        for f, ws, s in zip(calls, spaces, streams):
+            with torch.cuda.stream(s):
+                got.append(f(ws))
+        torch.cuda.synchronize()
+        for p, r in zip(want, got):
+            assert all(torch.equal(m.view(torch.uint8), n.view(torch.uint8)) for m, n in zip(p, r))
+    assert all(gpu_lib.get_error(ws) == 0 for ws in spaces)
+
+
 def test_prefill_no_entries(gpu_lib):
     """No entry at all, and no row at all."""
     import torch
