@@ -44,9 +44,11 @@
 // softmax, MMA2; the ring holds two blocks, all the shared memory beside q.  64
 // requests of 131072 tokens: 373 us, 6480 GB/s, 0.96 of the measured copy rate; one
 // of 1M: 66 us, 0.68 (ramp, tail, and 11 us of launch and merge); 64 of 8192: 46.
-// Several tokens are bound by the chain alone, 1.43 us a block and token (64 x 131072,
-// four tokens: 1230 us, tensor pipe 53 % active).  Tokens of a request in one cluster,
-// its pages loaded once and multicast, took 1352: the bytes are not their bound.
+// Several tokens are bound by the MMAs' rate: 52 a block at about 50 cycles each (their
+// operands' reads of shared memory), 2,750 cycles a block and token, of which they run
+// 2,270 (64 x 131072, four tokens: 1230 us; the pipe's own figure is 53 %).  Tokens of a
+// request in one cluster, its pages loaded once and multicast, took 1352, pages fetched
+// into L2 ahead of the ring 1225 (and one token up to 10 % more): bytes are not the bound.
 // Shares of at least 2, 3 or 4 units for small batches were slower throughout.
 // Every wait is bounded (about 1 s); a timeout sets an error bit, the roles
 // drain, and TMEM is freed.
