@@ -140,8 +140,6 @@ cudaError_t launch_mla(const CUtensorMap& q_map, const CUtensorMap& kv_map, cons
 
 // Latent attention decode over every live entry, 1-4 tokens per request.
 constexpr int kMlaMaxGroups = 256;
-constexpr int kMlaSegUnits = 2;  // a request's fixed cost in a range (q, output), in blocks
-constexpr int kMlaWholeBlocks = 4;  // requests of at most this many blocks are not split
 struct MlaDenseParams {
     const int32_t* page_table; // [batch, table_width]
     const int32_t* seq_lens;   // [batch] tokens

@@ -30,7 +30,8 @@
 //     lanes: 2 heads x 8 entries per thread.  The running maximum is raised only
 //     when a block passes it by more than 2^20; then the accumulators are rescaled
 //     in TMEM.  At a request's end the warps normalise O^T into the ring half of its
-//     last block (released only then).
+//     last block (released only then), a range's last partial into the whole ring
+//     (stage_whole_ring: where the other half is known to be at rest).
 //   * warp 3: stores from there with bulk copies; zeroes the outputs of empty requests.
 // Row sums add the unrounded fp32 weights; the weights are rounded to bf16 only
 // as the second product's operand.
@@ -60,6 +61,7 @@
 
 #include "indexer_kernels.h"
 #include "mla_common.cuh"
+#include "mla_dense_plan.h"
 #include "sm103_ptx.cuh"
 
 namespace dsa {
@@ -191,20 +193,6 @@ __device__ __forceinline__ int seq_tokens(const MlaDenseParams& p, int b) {
     return seq < 0 ? 0 : (int64_t(seq) > p.max_context ? int(p.max_context) : seq);
 }
 __device__ __forceinline__ int blocks_of(int seq) { return (((seq + 3) >> 2) + kBlk - 1) / kBlk; }
-__device__ __forceinline__ int units_of(int blocks) { return blocks ? blocks + kMlaSegUnits : 0; }
-
-// Equal ranges of `total` units: range g is [cut(g), cut(g + 1)).  32-bit arithmetic only.
-struct Ranges {
-    int n, total, q, r;
-    __device__ __forceinline__ Ranges(int n_, int total_) : n(n_), total(total_), q(total_ / n_), r(total_ % n_) {}
-    __device__ __forceinline__ int cut(int g) const { return q * g + r * g / n; }  // r * g < 2^16
-    __device__ __forceinline__ int of(int unit) const {                           // the range that holds a unit
-        int g = min(int(float(unit) * float(n) / float(total)), n - 1);
-        while (g > 0 && cut(g) > unit) --g;
-        while (g + 1 < n && cut(g + 1) <= unit) ++g;
-        return g;
-    }
-};
 
 // The CTA's walk over its range: one step per request that has blocks in it.
 struct Walk {
@@ -330,15 +318,12 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         int u = before + incl - mine;
         for (int b = r0; b < r1; ++b) {
             const int nb = blocks_of(seq_tokens(p, b)), n = units_of(nb);
-            const auto settled = [&](int cut) {
-                return nb > kMlaWholeBlocks ? cut : ((cut - u) * 2 < n ? u : u + n);
-            };
             if (lo >= u && lo < u + n) {
-                ctl.lo = settled(lo);
+                ctl.lo = settled_cut(lo, u, nb);
                 ctl.first_req = b;
                 ctl.first_start = u;
             }
-            if (hi >= u && hi < u + n) ctl.hi = settled(hi);
+            if (hi >= u && hi < u + n) ctl.hi = settled_cut(hi, u, nb);
             // Is this the request's second range?  Its first block lies in the one before.
             if (nb > kMlaWholeBlocks && lo > u + kMlaSegUnits && lo < u + n && ranges.cut(group - 1) <= u + kMlaSegUnits)
                 ctl.cut = b;
@@ -589,7 +574,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             const int64_t row = int64_t(w.req()) * p.tokens + token;
             const int64_t part = int64_t(group * p.tokens + token) * 2 + (w.blo == 0 ? 1 : 0);
             uint8_t* dst = reinterpret_cast<uint8_t*>(p.o_part + part * kMlaHeads * kMlaDv);
-            const int rounds = whole || w.last() ? 1 : 2;
+            const int rounds = whole || stage_whole_ring(w.last(), w.bhi - w.blo, n) ? 1 : 2;
             for (int r = 0; r < rounds && ok; ++r, ++staged) {
                 ok = __all_sync(0xffffffffu, mbar_await(&ctl.stage_full, uint32_t(staged & 1), &ctl.abort)) != 0;
                 if (ok && issuer) {
@@ -831,9 +816,9 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 }
                 staged();
             } else {
-                // fp32: the whole ring if nothing follows, else 32 heads at a time in the half of the
+                // fp32: the whole ring (stage_whole_ring), or 32 heads at a time in the half of the
                 // request's last block.  This warp: dims 128 j + 32 quad + lane of the same j.
-                const int rounds = w.last() ? 1 : 2;
+                const int rounds = stage_whole_ring(w.last(), w.bhi - w.blo, n) ? 1 : 2;
                 float* const stage =
                     reinterpret_cast<float*>(tiles + kOffV + (rounds == 1 ? 0 : ((n - 1) & 1) * 4 * kPairBytes));
 #pragma unroll 1
