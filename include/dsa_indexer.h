@@ -349,7 +349,8 @@ DSA_API dsa_status_t dsa_sparse_mla_decode(const void *q, const void *kv_cache, 
  * log-sum-exp; the launch depends on (batch, next_n, device) only.  Softmax
  * weights are rounded to bf16 for the second product, sums are fp32.  Entries
  * past n_bj are never used, whatever they hold; the entries a token sees, and
- * q, must be finite.  An entry on a live page id outside [0, num_pages) is
+ * q, must be finite (a score that is NaN or +inf makes that head's out and lse
+ * NaN, of that token only).  An entry on a live page id outside [0, num_pages) is
  * left out, and DSA_DEVERR_BAD_PAGE is set.  The order of a request's sums
  * depends on the batch's lengths; for the same arguments results are the same
  * bits.  1 <= next_n <= 4, finite sm_scale; num_pages above 2^25 - 1 returns

@@ -755,8 +755,9 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 for (int r = 0; r < 2; ++r) {
                     const int h = h0 + 8 * r;
                     const float sum = ctl.row_max[0][h] + ctl.row_max[1][h];
-                    ctl.alpha[h] = sum > 0.f ? 1.f / sum : 0.f;
-                    const float lse = sum > 0.f ? (m[r] + log2f(sum)) * kLn2 : -INFINITY;
+                    // (0: nothing was seen; a NaN goes on to both outputs)
+                    ctl.alpha[h] = sum == 0.f ? 0.f : 1.f / sum;
+                    const float lse = sum == 0.f ? -INFINITY : (m[r] + log2f(sum)) * kLn2;
                     if (whole)
                         p.lse[row * kMlaHeads + h] = lse;
                     else
@@ -909,15 +910,15 @@ __global__ void __launch_bounds__(512) mla_dense_merge_kernel(const MlaDensePara
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         float sum = 0.f;
         for (int i = lane; i < S; i += 32) {
-            const float e = mx == -INFINITY ? 0.f : expf(w[i] - mx);
+            const float e = w[i] == -INFINITY ? 0.f : expf(w[i] - mx);  // (a NaN, which the maximum passes by, stays)
             w[i] = e;
             sum += e;
         }
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         for (int i = lane; i < S; i += 32) w[i] *= inv;
         if (lane == 0 && (!kOneHead || (blockIdx.x & 1) == 0))
-            p.lse[row * kMlaHeads + h] = mx == -INFINITY ? -INFINITY : mx + logf(sum);
+            p.lse[row * kMlaHeads + h] = sum == 0.f ? -INFINITY : mx + logf(sum);
     }
     __syncthreads();
     const float* const w = wgt[kOneHead ? 0 : quarter];
