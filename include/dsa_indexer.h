@@ -395,7 +395,8 @@ DSA_API dsa_status_t dsa_mla_decode(const void *q, const void *kv_cache, int64_t
  * row sees nothing).  Softmax weights are rounded to bf16 for the second product,
  * sums are fp32.  Entries that no row of their request sees are never used,
  * whatever they hold; q and the entries that some row of a request sees must be
- * finite.  Device data out of contract (DSA_DEVERR_BAD_RANGE, DSA_DEVERR_SEQ_LEN_CLAMPED)
+ * finite (a score that is NaN or +inf makes that row's and head's out and lse NaN,
+ * split or not).  Device data out of contract (DSA_DEVERR_BAD_RANGE, DSA_DEVERR_SEQ_LEN_CLAMPED)
  * is never dereferenced: such rows are left out, or see the entries that there are.
  * Where requests are split, the order of a row's sums depends on the batch's row counts and
  * lengths; otherwise a row's result depends on its request alone.  For the same arguments

@@ -1124,8 +1124,8 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
             ++no;
             tc_fence_after_sync();
             const float l = l2.x + l2.y;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            const float lse = l > 0.f ? (m + log2f(l)) * kLn2P : -INFINITY;
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // (0: nothing was seen; a NaN goes on to both outputs)
+            const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2P;
             if (kSplit && live_row && part_row >= 0) {
                 p.lse_part[part_row] = lse;
             } else if (live_row) {
@@ -1205,20 +1205,21 @@ __global__ void __launch_bounds__(256) mla_prefill_merge_kernel(const PrefillPar
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int s = 0; s < parts; ++s) {
-        const float w = mx == -INFINITY ? 0.f : expf(p.lse_part[part_row(s)] - mx);
-        if (w == 0.f) continue;  // a part without entries has written no output
+        const float lse = p.lse_part[part_row(s)];
+        if (lse == -INFINITY) continue;  // a part without entries has written no output
+        const float w = expf(lse - mx);  // (a NaN, which the maximum passes by, stays)
         sum += w;
         const float4 v = *reinterpret_cast<const float4*>(p.o_part + part_row(s) * kPrefillDv + 4 * lane);
         acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y);
         acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int64_t row = (int64_t(u.q_row) + i * u.step_row + r) * p.heads + head;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
     *reinterpret_cast<uint2*>(p.out + row * kPrefillDv + 4 * lane) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    if (lane == 0) p.lse[row] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+    if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : mx + logf(sum);
 }
 
 }  // namespace
