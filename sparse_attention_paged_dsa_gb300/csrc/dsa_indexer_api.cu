@@ -14,6 +14,7 @@
 #include "../../include/dsa_indexer.h"
 #include "api_checks.h"
 #include "indexer_kernels.h"
+#include "mla_prefill_plan.h"
 
 namespace {
 
@@ -785,8 +786,8 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
         kv_rows > INT32_MAX)
         return DSA_ERR_UNSUPPORTED;
     if (!std::isfinite(sm_scale) || sm_scale < 0.f) return DSA_ERR_INVALID_ARG;
-    const int64_t slots = q_rows / dsa::kPrefillBlock + batch;
-    if (2 * slots * heads > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+    const int64_t slots = dsa::prefill_slots(q_rows, batch);
+    if (2 * dsa::prefill_most_units(slots, heads) > INT32_MAX) return DSA_ERR_UNSUPPORTED;
     if (!cu_q || !cu_kv || !seq_lens || !aligned(cu_q, 4) || !aligned(cu_kv, 4) || !aligned(seq_lens, 4))
         return DSA_ERR_INVALID_ARG;
     if (q_rows > 0 && (!q || !out || !lse || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)))

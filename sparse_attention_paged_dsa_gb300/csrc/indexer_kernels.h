@@ -169,7 +169,6 @@ cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map
 // Latent attention over ragged prompts, expanded form: per-head 128 + 64 shared key dims, 128 value dims.
 constexpr int kPrefillQk = 192;
 constexpr int kPrefillDv = 128;
-constexpr int kPrefillBlock = 512;  // rows of a request that share a pass over its entries
 struct SplitUnit {             // rows that several parts of their entries leave outputs for
     int32_t q_row, rows, head, step_row, step_head;
 };
@@ -185,7 +184,7 @@ struct PrefillParams {
     int32_t batch;
     int32_t heads;
     int32_t entry_tokens;      // tokens per entry
-    int32_t slots;             // q_rows / 512 + batch: at least the blocks of up to 512 rows
+    int32_t slots;             // prefill_slots: at least the blocks of up to 512 rows
     int2* split;               // cut units, and parts of each (1: none is cut)
     SplitUnit* split_units;    // [clusters]
     float* o_part;             // [parts, 2 tiles, 256 rows, 128]; null: no splitting

@@ -61,6 +61,7 @@
 
 #include "indexer_kernels.h"
 #include "mla_common.cuh"
+#include "mla_prefill_plan.h"
 #include "sm103_ptx.cuh"
 
 namespace dsa {
@@ -78,6 +79,7 @@ constexpr int kOffK = kOffQt + 2 * kQkSlabs * kSlabB;
 constexpr int kOffV = kOffK + kStages * kStageK;
 constexpr int kOffCtlP = kOffV + kStages * kStageV;
 constexpr int kThreadsP = 384;
+static_assert(2 * kTile == kPrefillPair, "a cluster's query tile");
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;  // 8 x 208 + 4 x 88 = 12 x 168 a warp lane
 constexpr uint32_t kTmemColsP = 512;
 constexpr uint32_t kColSP = 0;    // S / P of tile i at 128 i
@@ -87,8 +89,6 @@ constexpr float kLn2P = 0.69314718055994531f;
 
 constexpr int kPartTiles = 4;        // key tiles a part has at least (2: no faster; 8: 64 rows of 20 heads
                                      // over 2,064 entries took 29 us, now 24)
-constexpr int kFewEntries = 768;     // see Cut: two heads a unit up to here (prompts of 512 rows: 146 us
-                                     // against 155), one above (of 1024: 80 against 100)
 constexpr int kSortMost = 256;       // requests that are ordered by length, one a thread (more: as they come)
 constexpr int kInfoSlots = 4;
 constexpr int kInfoReaders = 11;     // every warp but the scheduler
@@ -290,22 +290,6 @@ __device__ __forceinline__ void wait_landed_p(uint64_t* bar, uint32_t parity) {
     }
 }
 
-// How a request's rows are cut.  Few entries: 256 rows at a time, two heads a unit, whose tiles run for
-// equally many key tiles (the halves of 512 rows do not, and a tile alone waits out its own softmax).
-// Many: 512 rows of one head, whose tiles share keys and values, and at most 256 rows left as above.
-struct Cut {
-    int rows, heads, pair_blocks, long_blocks;  // blocks of 256 rows for two heads, and of 512 for one
-    __host__ __device__ __forceinline__ Cut(int rows_, int live, int heads_) : rows(rows_), heads(heads_) {
-        const bool few = live <= kFewEntries && heads_ > 1;
-        const int left = few ? rows : rows % kPrefillBlock;
-        pair_blocks = few || left <= 2 * kTile ? (left + 2 * kTile - 1) / (2 * kTile) : 0;
-        long_blocks = few ? 0 : (rows + 2 * kTile - 1) / kPrefillBlock;
-    }
-    __device__ __forceinline__ Cut(const Request& r, int heads_) : Cut(r.rows, r.live, heads_) {}
-    __host__ __device__ __forceinline__ int pairs() const { return (heads + 1) / 2; }
-    __host__ __device__ __forceinline__ int units() const { return pair_blocks * pairs() + long_blocks * heads; }
-};
-
 // Do a request's blocks of 512 rows see about equally many entries (a chunk on a long past)?  A head's
 // blocks then follow one another, so that its keys and values are in L2 for all but the first (1024 rows of
 // 64 heads over 32,768 entries in a long run, which power limits: 871 -> 838 us; alone 756 -> 750).
@@ -330,7 +314,7 @@ __device__ __forceinline__ int group_tiles(const PrefillParams& p, const Request
 // The request's unit number `at`, last rows (the longest) first: the blocks for two heads lie behind the
 // long ones.
 __device__ __forceinline__ Unit unit_of(const PrefillParams& p, const Request& rq, bool alike, int at) {
-    const Cut cut(rq, p.heads);
+    const Cut cut(rq.rows, rq.live, p.heads);
     Unit u = {};
     if (at < cut.pair_blocks * cut.pairs()) {
         u.row0 = cut.long_blocks * kPrefillBlock + (cut.pair_blocks - 1 - at / cut.pairs()) * 2 * kTile;
@@ -457,7 +441,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
     int groups = 0;
     for (int b = me; b < p.batch; b += kThreadsP) {
         const Request r(p, b, bad);
-        const Cut cut(r, p.heads);
+        const Cut cut(r.rows, r.live, p.heads);
         ctl.first[b] = cut.units();
         ctl.order[b] = list_entry(b, blocks_alike(p, r), 0);
         if (b < kSortMost) ctl.key.live[b] = r.rows > 0 ? r.live : -1;
@@ -504,7 +488,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                 const int group = me - ctl.order[b];
                 uint32_t ignored = 0;
                 const Request r(p, b, ignored);
-                const Cut cut(r, p.heads);
+                const Cut cut(r.rows, r.live, p.heads);
                 const bool last = group + 1 == groups_of(p, r, cut);
                 const int from = group_start(cut, group);
                 units = (last ? cut.units() : group_start(cut, group + 1)) - from;
@@ -1263,7 +1247,7 @@ cudaError_t launch_mla_prefill(const PrefillMaps& m, const PrefillParams& p, cud
     }
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    const int64_t most = int64_t(p.slots) * p.heads;  // at least the number of units
+    const int64_t most = prefill_most_units(p.slots, p.heads);
     // Cut where a batch of this batch's average request would be; the kernel, which sees the lengths, decides.
     bool split = false;
     if (p.o_part) {
