@@ -480,12 +480,24 @@ def prefill_workspace_size() -> int:
     return int(load().dsa_mla_prefill_workspace_size())
 
 
+def _workspace_of(device, size, *shape) -> torch.Tensor:
+    """A workspace of ``size(*shape)`` bytes for one call: of it only the header has to be zero."""
+    with torch.cuda.device(device):
+        n = size(*shape)
+        if n == 0:
+            raise ValueError("invalid shape for a workspace")
+        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    workspace[:WORKSPACE_HEADER_BYTES].zero_()
+    return workspace
+
+
 def dsa_mla_decode(q, kv_cache, page_table, seq_lens, max_context: int, sm_scale: float, out=None, lse=None,
                    workspace=None):
     """(out, lse): attention of q over every live entry of the paged latent cache.
 
     q [B, 64, 576] bf16, or [B, next_n, 64, 576] for next_n query tokens per request (token j sees
-    seq_len - (next_n - 1 - j) tokens); kv_cache [P, 64, 576] bf16; out bf16 [..., 64, 512]; lse fp32."""
+    seq_len - (next_n - 1 - j) tokens); kv_cache [P, 64, 576] bf16; out bf16 [..., 64, 512]; lse fp32.
+    ``workspace``: of ``new_mla_workspace(B, next_n)``; without one the call makes its own."""
     dev = _device_of(q, "q", _BF16, (3, 4))
     lead = q.shape[:-2]
     B, Q = lead[0], (lead[1] if len(lead) == 2 else 1)
@@ -503,7 +515,7 @@ def dsa_mla_decode(q, kv_cache, page_table, seq_lens, max_context: int, sm_scale
     else:
         _on(lse, "lse", _F32, (*lead, MLA_HEADS), dev)
     if workspace is None:
-        workspace = new_mla_workspace(B, Q, q.device)
+        workspace = _workspace_of(q.device, mla_decode_workspace_size, B, Q)
     _run(load().dsa_mla_decode, dev, q.data_ptr(), kv_cache.data_ptr(), pages, page_table.data_ptr(),
          seq_lens.data_ptr(), B, Q, max_context, sm_scale, out.data_ptr(), lse.data_ptr(),
          *_space(workspace, dev))
@@ -556,9 +568,7 @@ def dsa_mla_prefill(q, k_nope, k_rope, v, cu_q, cu_kv, seq_lens, sm_scale: float
     else:
         _on(lse, "lse", _F32, (Tq, H), dev)
     if workspace is None:
-        with torch.cuda.device(q.device):
-            workspace = torch.empty(prefill_workspace_size(), dtype=torch.uint8, device=q.device)
-        workspace[:WORKSPACE_HEADER_BYTES].zero_()
+        workspace = _workspace_of(q.device, prefill_workspace_size)
     _run(load().dsa_mla_prefill, dev, q.data_ptr(), q_row, q_head, k_nope.data_ptr(), k_row, k_head,
          k_rope.data_ptr(), r_row, v.data_ptr(), v_row, v_head, cu_q.data_ptr(), cu_kv.data_ptr(),
          seq_lens.data_ptr(), B, H, Tq, Tk, entry_tokens, sm_scale, out.data_ptr(), lse.data_ptr(),
