@@ -431,8 +431,9 @@ DSA_API dsa_status_t dsa_mla_prefill(const void *q, int64_t q_row_stride, int64_
  *     scale_G = max_G |y| / 448,  code = y / scale_G    (e4m3, one rounding)
  * with one scale per group of 64 or 128 consecutive elements (the last group of
  * a row may be short) or per row (group 0).  A group whose maximum is 0 (or so
- * small that the scale is) has scale 1.  Where h * weight and the sum of squares are
- * finite in fp32, every scale is positive and finite.
+ * small that the scale is), or that has no finite scale (h * weight or the norm is not
+ * finite in fp32), has scale 1: every scale is positive and finite.  Below 2^-126,
+ * where a scale's own rounding counts, codes are of y over the scale as stored.
  *
  *   x            bf16 [rows, d], rows x_stride >= 0 elements apart (a view of
  *                wider rows, or 0: the same row every time)

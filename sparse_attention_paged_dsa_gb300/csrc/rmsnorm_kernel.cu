@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 #include <type_traits>
 
@@ -216,9 +217,6 @@ __device__ __forceinline__ void l2_prefetch(const uint16_t* p, int n) {
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(uint32_t(to - from)) : "memory");
 }
 
-// A correctly rounded quotient, kept out of line: only groups at the ends of fp32's range take it.
-__device__ __noinline__ float divide(float a, float b) { return a / b; }
-
 // CTAs per SM that the registers have to allow: 40 a thread with one unit (with 56, and fewer CTAs, 131072
 // x 512 took 46 us, now 42), 64 with two; more for shifting.
 template <int kNV, int kMaxT, int kAlign>
@@ -289,18 +287,21 @@ __device__ __forceinline__ void pack_e4m3(uint32_t (&pk)[4], const float2 (&u)[k
 // parts, so that the result is off by little more than its last rounding (a one-part quotient moves half
 // as many more codes to a neighbour: they lie where u is just between two).
 __device__ __forceinline__ void codes_of(uint32_t (&pk)[4], const float2 (&u)[kPairs], float amax) {
-    if (amax > 1e-30f && amax < 1e30f) {
-        const float q = __fdividef(kE4m3Max, amax);
-        const float lo = fmaf(-q, amax, kE4m3Max) * (q * (1.f / kE4m3Max));
+    const auto quotients = [&](float most, auto&& value) {
+        const float q = __fdividef(kE4m3Max, most);
+        const float lo = fmaf(-q, most, kE4m3Max) * (q * (1.f / kE4m3Max));
         pack_e4m3(pk, u, [&](float2 v) {
+            v = value(v);
             return fma_f32x2(v, make_float2(q, q), mul_f32x2(v, make_float2(lo, lo)));
         });
+    };
+    if (amax > 1e-30f && amax < 1e30f) {
+        quotients(amax, [](float2 v) { return v; });
     } else if (!(amax > 0.f)) {  // zeros (a row's last warp may hold nothing else) and NaN
         pack_e4m3(pk, u, [](float2 v) { return v; });
-    } else {  // a quotient that would leave fp32's range
-        float scale = amax * (1.f / kE4m3Max);
-        if (!(scale > 0.f)) scale = 1.f;
-        pack_e4m3(pk, u, [&](float2 v) { return make_float2(divide(v.x, scale), divide(v.y, scale)); });
+    } else {  // a quotient that would leave fp32's range: moved by 2^64, which is exact where it counts
+        const float by = amax < 1.f ? 0x1p64f : 0x1p-64f;
+        quotients(amax * by, [&](float2 v) { return mul_f32x2(v, make_float2(by, by)); });
     }
 }
 
@@ -408,9 +409,21 @@ __global__ void __launch_bounds__(kMaxT, kResidentOf<kNV, kMaxT, kAlign>) rmsnor
 #pragma unroll
         for (int j = 0; j < kNV; ++j) {
             float scale = amax[j] * rstd * (1.f / kE4m3Max);
-            if (!(scale > 0.f)) {  // all zeros, below fp32's range, or no finite norm: the codes of y itself
-                scale = 1.f;
-                pack_e4m3(pk[j], h[j], [&](float2 v) { return mul_f32x2(v, make_float2(rstd, rstd)); });
+            if (__float_as_uint(scale) - 0x00800000u >= 0x7F000000u) {  // not a positive normal number
+                if (amax[j] == 0.f && rstd <= FLT_MAX) {  // zeros: their codes stand
+                    scale = 1.f;
+                } else {  // an end of fp32's range, or no finite norm
+                    const bool over = scale > FLT_MAX;  // y alone may pass fp32's range: these codes stand
+                    if (over) scale = amax[j] * (1.f / kE4m3Max) * rstd;
+                    const bool one = !(scale > 0.f && scale <= FLT_MAX);
+                    if (one) scale = 1.f;
+                    if (one || !over) {  // the codes of y / scale itself, whose rounding counts below 2^-126
+                        const float by = one ? rstd : rstd * 0x1p64f, inv = one ? 1.f : __fdividef(1.f, scale * 0x1p64f);
+                        pack_e4m3(pk[j], h[j], [&](float2 v) {
+                            return mul_f32x2(mul_f32x2(v, make_float2(by, by)), make_float2(inv, inv));
+                        });
+                    }
+                }
             }
             const int v = io.unit(j);
             const bool first = kRowScale ? v == 0 : (v & (kGroupLanes - 1)) == 0;
