@@ -334,7 +334,8 @@ DSA_API dsa_status_t dsa_sparse_mla_decode(const void *q, const void *kv_cache, 
  * The absorbed form without a top-k row: each of next_n query tokens per request
  * attends to every entry it sees, by the rule of the multi-token indexer (token
  * j of the request sees L_j = seq_len - (next_n - 1 - j) tokens, i.e. n_bj =
- * ceil(max(L_j, 0) / 4) entries):
+ * ceil(max(L_j, 0) / 4) entries; the last one may hold later tokens of the
+ * request's too, as its maker left it):
  *     s_t = sm_scale * q[b, j, h, :] . kv_t[:]                     (576 dims)
  *     out[b, j, h] = sum_t softmax_t(s) * kv_t[0:512]              (t < n_bj)
  *     lse[b, j, h] = log sum_t exp(s_t)
@@ -346,7 +347,7 @@ DSA_API dsa_status_t dsa_sparse_mla_decode(const void *q, const void *kv_cache, 
  *              aligned, header zeroed once; holds the error word, the plan of the
  *              split and the partial outputs (sized for the current device).
  * The requests' entries are split over the whole device by length and joined by
- * log-sum-exp; the launch depends on (batch, next_n, device) only.  Softmax
+ * log-sum-exp; the launch depends on (batch, next_n, max_context) and the device.  Softmax
  * weights are rounded to bf16 for the second product, sums are fp32.  Entries
  * past n_bj are never used, whatever they hold; the entries a token sees, and
  * q, must be finite (a score that is NaN or +inf makes that head's out and lse
@@ -369,9 +370,12 @@ DSA_API dsa_status_t dsa_mla_decode(const void *q, const void *kv_cache, int64_t
  * caller's up-projection, for a ragged batch of new rows per request.  Request b
  * has rows cu_q[b] .. cu_q[b + 1] of q and entries cu_kv[b] .. cu_kv[b + 1] of the
  * keys and values; seq_lens[b] counts its tokens, its new rows included.  Row i
- * of its n rows sees the entries of its causal prefix, by the same rule as the
- * multi-token indexer and decode: L = seq_len - (n - 1 - i) tokens, the first
- * ceil(max(L, 0) / entry_tokens) entries.
+ * of its n rows sees, by the same rule as the multi-token indexer and decode, the
+ * first ceil(max(L, 0) / entry_tokens) entries of L = seq_len - (n - 1 - i) tokens:
+ * every entry that holds one of its tokens.  With entry_tokens > 1 the last of them
+ * may hold up to entry_tokens - 1 tokens behind the row too, so that attention is
+ * causal by entries: by tokens only for rows at the end of an entry, or where the
+ * caller's entry was made from the row's prefix alone (a decode step's last entry).
  *     s_t = sm_scale * (q[i, h, 0:128] . k_nope[t, h] + q[i, h, 128:192] . k_rope[t])
  *     out[i, h] = sum_t softmax_t(s) * v[t, h],   lse[i, h] = log sum_t exp(s_t)
  * A row that sees nothing gets out = 0 and lse = -inf.  Rows of q outside
@@ -401,7 +405,7 @@ DSA_API dsa_status_t dsa_mla_decode(const void *q, const void *kv_cache, int64_t
  * Where requests are split, the order of a row's sums depends on the batch's row counts and
  * lengths; otherwise a row's result depends on its request alone.  For the same arguments
  * results are the same bits.  The launch depends on (q_rows, kv_rows, batch,
- * heads, entry_tokens, workspace_bytes).  Asynchronous on `stream`, allocates nothing, capture-safe.
+ * heads, entry_tokens, workspace_bytes) and the device.  Asynchronous on `stream`, allocates nothing, capture-safe.
  */
 #define DSA_PREFILL_QK_DIM 192
 #define DSA_PREFILL_NOPE_DIM 128

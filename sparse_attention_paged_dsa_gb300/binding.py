@@ -541,11 +541,12 @@ def _strided(t, name, shape, device: int):
 
 def dsa_mla_prefill(q, k_nope, k_rope, v, cu_q, cu_kv, seq_lens, sm_scale: float, entry_tokens: int = 4, out=None,
                     lse=None, workspace=None):
-    """(out, lse): causal attention of a ragged batch of prompt rows, expanded latent form.
+    """(out, lse): attention of a ragged batch of prompt rows, expanded latent form, causal by entries.
 
     q [Tq, H, 192] bf16, k_nope [Tk, H, 128], k_rope [Tk, 64], v [Tk, H, 128] (strided views are
     fine); cu_q, cu_kv int32 [B + 1]; seq_lens int32 [B] tokens per request, the new rows included;
-    ``entry_tokens`` tokens per key entry (1: an entry per token).  out [Tq, H, 128] bf16 and lse
+    ``entry_tokens`` tokens per key entry (1: an entry per token; more: a row sees the whole entry that its
+    own token is in, with what that holds of tokens behind it).  out [Tq, H, 128] bf16 and lse
     [Tq, H] fp32; rows outside [cu_q[0], cu_q[B]) are left as they are.  ``workspace``: at least 256
     bytes, zeroed once; with ``prefill_workspace_size()`` (the default) few rows may be split along their entries."""
     dev = _device_of(q, "q", _BF16, (3,))

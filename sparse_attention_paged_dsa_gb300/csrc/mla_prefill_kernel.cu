@@ -5,7 +5,8 @@
 //     o[i, h] = sum_t softmax_t(s[i, :]) v[t, h],   lse[i, h] = log sum_t exp(s[i, t])
 //
 // Row i of a request with n rows and seq_len tokens sees its first
-// ceil((seq_len - (n - 1 - i)) / entry_tokens) entries.
+// ceil((seq_len - (n - 1 - i)) / entry_tokens) entries: whole ones, whatever tokens
+// behind the row's own the last of them holds.
 //
 // A cluster of two CTAs works on two query tiles of 256 rows at a time, each CTA
 // holding 128 rows of both.  All MMAs are cta_group::2 (M = 256: 128 rows in each

@@ -22,7 +22,8 @@
 // one unit a thread are resident: 143; the next row fetched into L2: 123.  Without
 // a residual the e4m3 output is bound by its instructions (63 us, 0.83; one unit a
 // thread, and the codes after the norm: 73; 131072 x 512: 36 us, 0.82, from 46).  Rows
-// off 16-byte boundaries are, too: 16384 x 7001, residual, e4m3 out: 231 us, 0.51.
+// off 16-byte boundaries are, too: 16384 x 7001, residual, e4m3 out: 231 us, 0.51, 750
+// instructions a unit and warp for 300, the ALU pipe at 71 % and DRAM at 39.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -323,7 +324,8 @@ __global__ void __launch_bounds__(kMaxT, kResidentOf<kNV, kMaxT, kAlign>) rmsnor
     pdl_wait_prior_grid();
     // The rows of the CTA that takes this one's place are fetched into L2 now: what is in flight no longer
     // ends with the resident CTAs' registers.  (Short rows without codes leave by themselves soon enough:
-    // 131072 x 512 44 us with it, 41 without; with codes 36 against 42.)
+    // 131072 x 512 44 us with it, 41 without; with codes 36 against 42.  `ahead` counts on the variant's
+    // largest CTAs: of smaller ones more are resident, and part of what is fetched is under way already.)
     if ((kCtaRow || kGroupLanes > 0) && threadIdx.x == 0) {
         const int64_t rows = kCtaRow ? 1 : kCta >> p.log2_threads, next = int64_t(blockIdx.x) * rows + p.ahead;
         if (next < p.rows && (kCtaRow || p.x_stride < 2 * p.d)) {
