@@ -63,7 +63,7 @@
  *     that size; the attention ones name theirs), zeroed once before first
  *     use (dsa_indexer_workspace_init or any memset to 0).  Its first 256
  *     bytes hold the sticky device error word; the rest of them is reserved
- *     and stays zero.  Calls that share a workspace, replayed graphs too,
+ *     and is zero between calls.  Calls that share a workspace, replayed graphs too,
  *     must be ordered on one stream.
  */
 #ifndef DSA_INDEXER_H
@@ -95,7 +95,11 @@ typedef enum {
 #define DSA_DEVERR_BAD_PAGE        0x2u /* a live page id was outside [0, num_pages) */
 #define DSA_DEVERR_WAIT_TIMEOUT    0x4u /* an in-kernel pipeline wait gave up (about 1 s) */
 #define DSA_DEVERR_BAD_RANGE       0x8u /* prefill: a request's rows or entries are out of order or out of the
-                                           tensor, or fewer entries than its seq_len needs */
+                                           tensor, or fewer entries than its seq_len needs; tree decode: a
+                                           token count outside [0, tokens]; append: a position outside the
+                                           rotation's table; page update: a count of free pages outside
+                                           [0, num_pages], or more pages returned than there are */
+#define DSA_DEVERR_NO_PAGES        0x10u /* page update: a request was not served (too few free pages or slots) */
 
 #define DSA_HEADS 32
 #define DSA_HEAD_DIM 64
@@ -463,6 +467,123 @@ DSA_API dsa_status_t dsa_rmsnorm(const void *x, int64_t x_stride, const void *re
 DSA_API dsa_status_t dsa_rmsnorm_fp8(const void *x, int64_t x_stride, const void *residual_opt, const void *weight,
                                      int32_t weight_fp32, int64_t rows, int32_t d, float eps, int32_t group,
                                      void *residual_out, void *out_opt, void *codes, float *scales, void *stream);
+
+/* ---- Latent attention decode for a tree of drafted tokens ------------------------
+ *
+ * The absorbed form for the verification of drafted tokens whose entries are not in
+ * the cache yet: drafted token j of request b attends to the request's live entries
+ * t < n_b = ceil(seq_len / 4) (seq_len counts what is in the cache, no drafted token)
+ * and to the drafted entries i with bit i of tree_mask[b, j] set (a tree's ancestors
+ * and the token itself; any mask will do):
+ *     s_e = sm_scale * q[b, j, h, :] . e[:]                        (576 dims)
+ *     out[b, j, h] = sum_e softmax_e(s) * e[0:512],  lse[b, j, h] = log sum_e exp(s_e)
+ * A token that sees nothing gets out = 0 and lse = -inf.  Layouts (C-contiguous):
+ *   q          [batch, tokens, 64, 576] bf16; kv_cache [num_pages, 64, 576] bf16;
+ *   draft_kv   [batch, tokens, 576] bf16, one entry per drafted token; all 16-byte aligned
+ *   tree_mask  [batch, tokens] 64-bit words; page_table, seq_lens as above
+ *   token_counts_opt int32 [batch]: request b has that many tokens, the others are padding
+ *              (their entries are not seen, their rows of out and lse not written); NULL: all
+ *   out        [batch, tokens, 64, 512] bf16 16-byte aligned, lse [batch, tokens, 64] fp32
+ *   workspace  >= dsa_mla_tree_decode_workspace_size(batch, tokens) bytes, 256-byte
+ *              aligned, header zeroed once; holds the error word, the plan of the split
+ *              and the partial outputs (sized for the current device).
+ * 1 <= tokens <= 64, finite sm_scale; num_pages above 2^25 - 1 returns DSA_ERR_UNSUPPORTED.
+ * Mask bits at or past the request's tokens are ignored.  Entries that no token of the
+ * request sees are never used, whatever they hold; q and the entries that some token sees
+ * must be finite (a score that is NaN or +inf makes that head's out and lse NaN; a value
+ * that is not finite makes those of every token of the request).  Softmax weights are
+ * rounded to bf16 for the second product, sums are fp32.  A live page id outside
+ * [0, num_pages) is left out and sets DSA_DEVERR_BAD_PAGE; a count outside [0, tokens] is
+ * held to it (DSA_DEVERR_BAD_RANGE).  The order of a request's sums depends on the batch's
+ * lengths; for the same arguments results are the same bits.  The launch depends on
+ * (batch, tokens, max_context) and the device.  Asynchronous on `stream`, allocates
+ * nothing, capture-safe.
+ */
+#define DSA_MAX_TREE_TOKENS 64
+
+DSA_API size_t dsa_mla_tree_decode_workspace_size(int32_t batch, int32_t tokens);
+
+DSA_API dsa_status_t dsa_mla_tree_decode(const void *q, const void *kv_cache, int64_t num_pages,
+                                         const int32_t *page_table, const int32_t *seq_lens, const void *draft_kv,
+                                         const uint64_t *tree_mask, const int32_t *token_counts_opt, int32_t batch,
+                                         int32_t tokens, int64_t max_context, float sm_scale, void *out, float *lse,
+                                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Page tables, free pages and slots ------------------------------------------
+ *
+ * What the entry points above are given, kept on the device: request b goes from
+ * seq_lens[b] to new_lens[b] tokens.
+ *   - Fewer tokens (0: it ends): its pages behind the new length return to the free
+ *     pages, request by request, in the order of its table's row (whose words stay).
+ *   - More: it takes pages from the top of the free pages, one after another, into its
+ *     row behind the old ones, and gets a slot for each entry that is to be written:
+ *     entries [seq_len / 4, ceil(new_len / 4)), the old last one again where it is not
+ *     full.  Entry e has the slot page_table[b, e / 64] x 64 + e % 64 and the position e.
+ * All pages returned by the call are on top before any is taken.  Requests are served in
+ * order; one that grows for which there are too few pages, or slots, stays as it was,
+ * and so does every later one that grows (DSA_DEVERR_NO_PAGES).
+ *   seq_lens, new_lens int32 [batch]; page_table int32 [batch, max_context / 256], updated
+ *   free_pages   int32 [num_pages], updated: free_count of them from the bottom of a stack;
+ *                words at and past the new count are left as they were
+ *   free_count   int32 [1];  free_count_out int32 [1], seq_lens_out int32 [batch]: the count
+ *                and the lengths afterwards; may be free_count and seq_lens themselves
+ *   cu_slots     int32 [batch + 1]: request b's slots are [cu_slots[b], cu_slots[b + 1])
+ *   slots        int64 [max_slots], positions int32 [max_slots], 16-byte aligned: the
+ *                entries', in order, then -1 (a fixed shape for dsa_cache_append)
+ *   workspace    >= 256 bytes, 256-byte aligned, header zeroed once
+ * The outputs do not overlap the inputs or one another but as said.  0 <= max_slots < 2^31;
+ * num_pages < 2^31.  Lengths outside [0, max_context] are held to it
+ * (DSA_DEVERR_SEQ_LEN_CLAMPED).  A free or a returned page outside [0, num_pages) is handed
+ * on as -1, and an entry on one gets the slot -1 (DSA_DEVERR_BAD_PAGE).  Integers only:
+ * results are the same bits for the same arguments.  Asynchronous on `stream`, allocates
+ * nothing, capture-safe; calls that share a workspace must be ordered on one stream.
+ */
+DSA_API dsa_status_t dsa_pages_update(const int32_t *seq_lens, const int32_t *new_lens, int32_t batch,
+                                      int64_t max_context, int32_t *page_table, int32_t *free_pages,
+                                      int64_t num_pages, const int32_t *free_count, int64_t max_slots,
+                                      int32_t *seq_lens_out, int32_t *free_count_out, int32_t *cu_slots,
+                                      int64_t *slots, int32_t *positions, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+/* ---- New entries into the paged caches ------------------------------------------
+ *
+ * Row i goes to slot slots[i] of the caches: entry slot % 64 of page slot / 64.
+ * A slot of -1 skips the row.  In fp32, one rounding per output:
+ *   latent entries  x = latent[i, 0:576]:
+ *     kv_cache[slot, 0:512] = x[0:512] * weight / sqrt(mean(x[0:512]^2) + eps)
+ *                             (x itself without a weight)
+ *     kv_cache[slot, 512 + 2 j], [513 + 2 j] = a cos - b sin, a sin + b cos  (j < 32)
+ *                             of a, b = x[512 + 2 j], x[513 + 2 j], with cos and sin =
+ *                             cos_sin[positions[i], j] and [.., 32 + j] (x without a table)
+ *   index keys      k = index_keys[i, 0:64], y = k * weight / sqrt(mean(k^2) + eps)
+ *                   (k without a weight):
+ *     key_pool[slot] = y (bf16), or key_scales[slot] = max|y| / 448 and key_codes[slot] =
+ *     e4m3(y / scale), the fp8 index-key cache's format; scale 1 where max|y| / 448 is 0
+ *     or not finite
+ * Either part may be left out (latent_opt and kv_cache NULL; index_keys_opt and the key
+ * caches NULL); keys go to exactly one of key_pool and (key_codes, key_scales).
+ *   latent_opt     bf16 [rows, 576], rows latent_stride >= 0 elements apart, a multiple of 8;
+ *                  16-byte aligned, as kv_cache bf16 [num_pages, 64, 576] is
+ *   index_keys_opt bf16 [rows, 64], rows key_stride >= 0 apart, a multiple of 2; 4-byte
+ *                  aligned, as key_pool bf16 [num_pages, 64, 64] is
+ *   weights        bf16 or fp32 (.._weight_fp32 0 or 1), [512] and [64]
+ *   cos_sin_opt    fp32 [cos_rows, 64] (32 cosines, then 32 sines), positions int32 [rows]
+ *   key_codes_opt  uint8 [num_pages, 64, 64], key_scales_opt fp32 [num_pages, 64]
+ *   slots          int64 [rows];  workspace >= 256 bytes, header zeroed once (the error word)
+ * Slots other than -1 are distinct (rows that share one leave a mix of them there), and the
+ * caches overlap none of the inputs.  A slot outside [-1, num_pages x 64) or a position
+ * outside the table leaves out its row and sets DSA_DEVERR_BAD_PAGE or
+ * DSA_DEVERR_BAD_RANGE.  Other entries are left as they were.  rows < 2^31, 0 launches
+ * nothing; eps finite and >= 0.  Asynchronous on `stream`, allocates nothing, capture-safe.
+ */
+DSA_API dsa_status_t dsa_cache_append(const int64_t *slots, int64_t rows, const void *latent_opt,
+                                      int64_t latent_stride, const void *latent_weight_opt,
+                                      int32_t latent_weight_fp32, const float *cos_sin_opt, int64_t cos_rows,
+                                      const int32_t *positions, void *kv_cache, const void *index_keys_opt,
+                                      int64_t key_stride, const void *index_weight_opt, int32_t index_weight_fp32,
+                                      void *key_pool_opt, void *key_codes_opt, float *key_scales_opt,
+                                      int64_t num_pages, float eps, void *workspace, size_t workspace_bytes,
+                                      void *stream);
 
 /*
  * Read the sticky device error word into *code (host pointer).  Synchronises

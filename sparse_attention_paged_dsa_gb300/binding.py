@@ -21,7 +21,7 @@ WORKSPACE_HEADER_BYTES = 256
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE, DSA_ERR_CUDA = range(5)
 DEVERR_SEQ_LEN_CLAMPED, DEVERR_BAD_PAGE, DEVERR_WAIT_TIMEOUT = 0x1, 0x2, 0x4
-DEVERR_BAD_RANGE = 0x8
+DEVERR_BAD_RANGE, DEVERR_NO_PAGES = 0x8, 0x10
 
 _lib = None
 
@@ -90,6 +90,15 @@ def load():
     lib.dsa_rmsnorm.restype = st
     lib.dsa_rmsnorm_fp8.argtypes = [p, i64, p, p, i32, i64, i32, ctypes.c_float, i32, p, p, p, p, p]
     lib.dsa_rmsnorm_fp8.restype = st
+    lib.dsa_mla_tree_decode_workspace_size.argtypes = [i32, i32]
+    lib.dsa_mla_tree_decode_workspace_size.restype = sz
+    lib.dsa_mla_tree_decode.argtypes = [p, p, i64, p, p, p, p, p, i32, i32, i64, ctypes.c_float, p, p, p, sz, p]
+    lib.dsa_mla_tree_decode.restype = st
+    lib.dsa_pages_update.argtypes = [p, p, i32, i64, p, p, i64, p, i64, p, p, p, p, p, p, sz, p]
+    lib.dsa_pages_update.restype = st
+    lib.dsa_cache_append.argtypes = [p, i64, p, i64, p, i32, p, i64, p, p, p, i64, p, i32, p, p, p, i64,
+                                     ctypes.c_float, p, sz, p]
+    lib.dsa_cache_append.restype = st
     lib.dsa_indexer_get_error.argtypes = [p, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int, p]
     lib.dsa_indexer_get_error.restype = st
     lib.dsa_status_string.argtypes = [st]
@@ -520,6 +529,160 @@ def dsa_mla_decode(q, kv_cache, page_table, seq_lens, max_context: int, sm_scale
          seq_lens.data_ptr(), B, Q, max_context, sm_scale, out.data_ptr(), lse.data_ptr(),
          *_space(workspace, dev))
     return out, lse
+
+
+MAX_TREE_TOKENS = 64
+_I64 = (torch.int64,)
+_MASK = (torch.int64, torch.uint64) if hasattr(torch, "uint64") else _I64
+
+
+def tree_workspace_size(batch: int, tokens: int) -> int:
+    """Workspace bytes of ``dsa_mla_tree_decode`` on the current device (0 for an invalid shape)."""
+    return int(load().dsa_mla_tree_decode_workspace_size(batch, tokens))
+
+
+def new_tree_workspace(batch: int, tokens: int, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for ``dsa_mla_tree_decode`` calls of this shape."""
+    device = torch.device(device)
+    with torch.cuda.device(device):
+        n = tree_workspace_size(batch, tokens)
+        if n == 0:
+            raise ValueError("invalid shape for a workspace")
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def dsa_mla_tree_decode(q, kv_cache, page_table, seq_lens, max_context: int, draft_kv, tree_mask, sm_scale: float,
+                        token_counts=None, out=None, lse=None, workspace=None):
+    """(out, lse): attention of a tree of drafted tokens over the paged latent cache and their own entries.
+
+    q [B, T, 64, 576] bf16 of T <= 64 drafted tokens per request; kv_cache [P, 64, 576] bf16, all of whose
+    ceil(seq_len / 4) live entries every token sees (seq_lens counts no drafted token); draft_kv [B, T, 576]
+    bf16, one entry per drafted token; tree_mask [B, T] 64-bit words: bit i of word j is set where token j
+    sees drafted entry i.  ``token_counts`` int32 [B]: the request's tokens, where they are fewer (rows of
+    padding are left as they are).  out bf16 [B, T, 64, 512]; lse fp32.  ``workspace``: of
+    ``new_tree_workspace(B, T)``; without one the call makes its own."""
+    dev = _device_of(q, "q", _BF16, (4,))
+    B, T = q.shape[:2]
+    _on(q, "q", _BF16, (B, T, MLA_HEADS, MLA_DIM), dev)
+    pages = kv_cache.shape[0] if isinstance(kv_cache, torch.Tensor) and kv_cache.dim() == 3 else 0
+    _on(kv_cache, "kv_cache", _BF16, (pages, PAGE_ENTRIES, MLA_DIM), dev)
+    _on(page_table, "page_table", _I32, (B, max_context // PAGE_TOKENS), dev)
+    _on(seq_lens, "seq_lens", _I32, (B,), dev)
+    _on(draft_kv, "draft_kv", _BF16, (B, T, MLA_DIM), dev)
+    _on(tree_mask, "tree_mask", _MASK, (B, T), dev)
+    if token_counts is not None:
+        _on(token_counts, "token_counts", _I32, (B,), dev)
+    if out is None:
+        out = torch.empty((B, T, MLA_HEADS, MLA_DV), dtype=torch.bfloat16, device=q.device)
+    else:
+        _on(out, "out", _BF16, (B, T, MLA_HEADS, MLA_DV), dev)
+    if lse is None:
+        lse = torch.empty((B, T, MLA_HEADS), dtype=torch.float32, device=q.device)
+    else:
+        _on(lse, "lse", _F32, (B, T, MLA_HEADS), dev)
+    if workspace is None:
+        workspace = _workspace_of(q.device, tree_workspace_size, B, T)
+    _run(load().dsa_mla_tree_decode, dev, q.data_ptr(), kv_cache.data_ptr(), pages, page_table.data_ptr(),
+         seq_lens.data_ptr(), draft_kv.data_ptr(), tree_mask.data_ptr(), _addr(token_counts), B, T, max_context,
+         sm_scale, out.data_ptr(), lse.data_ptr(), *_space(workspace, dev))
+    return out, lse
+
+
+def _header_workspace(device) -> torch.Tensor:
+    return torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=device)
+
+
+def dsa_pages_update(seq_lens, new_lens, max_context: int, page_table, free_pages, free_count, max_slots: int,
+                     seq_lens_out=None, free_count_out=None, cu_slots=None, slots=None, positions=None,
+                     workspace=None):
+    """(seq_lens_out, free_count_out, cu_slots, slots, positions) of requests that go to ``new_lens`` tokens.
+
+    Updates page_table [B, max_context / 256] and the stack of free pages, free_pages [P] with free_count [1]
+    of them (all int32), in place: requests that shrink return pages, those that grow take some, in order,
+    and get a slot (int64, page x 64 + entry) and a position for each entry to be written; [max_slots] of
+    both, -1 behind the last.  Request b's are cu_slots[b] to cu_slots[b + 1].  Requests that cannot be
+    served keep their length.  ``seq_lens_out`` and ``free_count_out`` may be ``seq_lens`` and ``free_count``
+    themselves.  ``workspace``: any of this package's; without one the call makes its own."""
+    dev = _device_of(seq_lens, "seq_lens", _I32, (1,))
+    B = seq_lens.shape[0]
+    _on(seq_lens, "seq_lens", _I32, (B,), dev)
+    _on(new_lens, "new_lens", _I32, (B,), dev)
+    _on(page_table, "page_table", _I32, (B, max_context // PAGE_TOKENS), dev)
+    pages = free_pages.shape[0] if isinstance(free_pages, torch.Tensor) and free_pages.dim() == 1 else 0
+    _on(free_pages, "free_pages", _I32, (pages,), dev)
+    _on(free_count, "free_count", _I32, (1,), dev)
+    given = dict(seq_lens_out=(seq_lens_out, _I32, (B,)), free_count_out=(free_count_out, _I32, (1,)),
+                 cu_slots=(cu_slots, _I32, (B + 1,)), slots=(slots, _I64, (max_slots,)),
+                 positions=(positions, _I32, (max_slots,)))
+    outs = []
+    for name, (t, dtypes, shape) in given.items():
+        if t is None:
+            t = torch.empty(shape, dtype=dtypes[0], device=seq_lens.device)
+        else:
+            _on(t, name, dtypes, shape, dev)
+        outs.append(t)
+    if workspace is None:
+        workspace = _header_workspace(seq_lens.device)
+    _run(load().dsa_pages_update, dev, seq_lens.data_ptr(), new_lens.data_ptr(), B, max_context,
+         page_table.data_ptr(), free_pages.data_ptr(), pages, free_count.data_ptr(), max_slots,
+         *(t.data_ptr() for t in outs), *_space(workspace, dev))
+    return tuple(outs)
+
+
+def dsa_cache_append(slots, latent=None, latent_weight=None, cos_sin=None, positions=None, kv_cache=None,
+                     index_keys=None, index_weight=None, key_pool=None, key_codes=None, key_scales=None,
+                     eps: float = 1e-6, workspace=None) -> None:
+    """Write row i to slot ``slots[i]`` (page x 64 + entry; -1 skips it) of the paged caches, in one launch.
+
+    latent [N, 576] bf16 to kv_cache [P, 64, 576]: the first 512 dims RMS-normed with ``latent_weight`` [512],
+    the last 64 rotated (neighbouring dims a pair) by row ``positions[i]`` of ``cos_sin`` [R, 64] (fp32: 32
+    cosines, then 32 sines); either is left out where it is not given.  index_keys [N, 64] bf16, RMS-normed
+    with ``index_weight`` [64] where it is given, to key_pool [P, 64, 64] bf16 or to the fp8 cache key_codes
+    [P, 64, 64] with key_scales [P, 64].  Rows of both may be views of wider ones.  Weights are bf16 or fp32.
+    ``workspace`` (any of this package's) takes the error word; without one the call makes its own."""
+    dev = _device_of(slots, "slots", _I64, (1,))
+    N = slots.shape[0]
+    _on(slots, "slots", _I64, (N,), dev)
+    if (latent is None) != (kv_cache is None):
+        raise ValueError("latent and kv_cache come together")
+    if (key_codes is None) != (key_scales is None):
+        raise ValueError("key_codes and key_scales come together")
+    if (index_keys is None) != (key_pool is None and key_codes is None) or (key_pool is not None and key_codes is not None):
+        raise ValueError("index_keys goes with one of key_pool and (key_codes, key_scales)")
+    pages = row = key_row = cos_rows = 0
+    if latent is not None:
+        row, _ = _strided(latent, "latent", (N, MLA_DIM), dev)
+        pages = kv_cache.shape[0] if isinstance(kv_cache, torch.Tensor) else 0
+        _on(kv_cache, "kv_cache", _BF16, (pages, PAGE_ENTRIES, MLA_DIM), dev)
+        if latent_weight is not None:
+            _on(latent_weight, "latent_weight", _NORM_WEIGHT, (MLA_DV,), dev)
+        if cos_sin is not None:
+            cos_rows = cos_sin.shape[0] if isinstance(cos_sin, torch.Tensor) and cos_sin.dim() == 2 else 0
+            _on(cos_sin, "cos_sin", _F32, (cos_rows, MLA_DIM - MLA_DV), dev)
+            _on(positions, "positions", _I32, (N,), dev)
+    elif latent_weight is not None or cos_sin is not None:
+        raise ValueError("latent_weight and cos_sin are for latent entries")
+    if index_keys is not None:
+        key_row, _ = _strided(index_keys, "index_keys", (N, HEAD_DIM), dev)
+        keys_to = key_pool if key_pool is not None else key_codes
+        if latent is None:
+            pages = keys_to.shape[0] if isinstance(keys_to, torch.Tensor) else 0
+        if key_pool is not None:
+            _on(key_pool, "key_pool", _BF16, (pages, PAGE_ENTRIES, HEAD_DIM), dev)
+        else:
+            _on(key_codes, "key_codes", _FP8, (pages, PAGE_ENTRIES, HEAD_DIM), dev)
+            _on(key_scales, "key_scales", _F32, (pages, PAGE_ENTRIES), dev)
+        if index_weight is not None:
+            _on(index_weight, "index_weight", _NORM_WEIGHT, (HEAD_DIM,), dev)
+    elif index_weight is not None:
+        raise ValueError("index_weight is for index keys")
+    if workspace is None:
+        workspace = _header_workspace(slots.device)
+    _run(load().dsa_cache_append, dev, slots.data_ptr(), N, _addr(latent), row, _addr(latent_weight),
+         int(latent_weight is not None and latent_weight.dtype == torch.float32), _addr(cos_sin), cos_rows,
+         _addr(positions), _addr(kv_cache), _addr(index_keys), key_row, _addr(index_weight),
+         int(index_weight is not None and index_weight.dtype == torch.float32), _addr(key_pool), _addr(key_codes),
+         _addr(key_scales), pages, eps, *_space(workspace, dev))
 
 
 PREFILL_QK, PREFILL_NOPE, PREFILL_ROPE, PREFILL_DV = 192, 128, 64, 128

@@ -1,0 +1,182 @@
+// append_kernel.cu -- new entries into the paged caches at their slots: RMS norm of
+// the latent part, rotation of the rotary part, RMS norm and 8-bit quantisation of
+// the index key.  One pass, one launch.
+//
+//     c = x[0:512] * weight / sqrt(mean(x[0:512]^2) + eps)           (without a weight: x)
+//     r[2j], r[2j + 1] = a cos - b sin, a sin + b cos                 (a, b = x[512 + 2j], x[513 + 2j])
+//     y = k * key_weight / sqrt(mean(k^2) + eps),  scale = max|y| / 448,  code = y / scale
+//
+// A warp has a row at a time: 8-element chunks lane and lane + 32 of the latent part
+// (16-byte accesses, whole 512-byte lines of the warp), one pair of the rotary dims and
+// of the key a lane; the sums are butterflies over the warp.  fp32 throughout, one
+// rounding per output.  Weights stay in registers, and the next row's loads are under
+// way while this one is computed and stored.
+//
+// What bounds it: HBM for many rows, launch latency for few.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "indexer_kernels.h"
+#include "sm103_ptx.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kWarpsA = 8;
+constexpr float kE4m3Max = 448.0f;
+
+__device__ __forceinline__ float2 widen(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t narrow(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+struct Row {
+    int64_t slot;
+    uint4 c[2];     // latent chunks
+    uint32_t r, k;  // rotary pair, key pair
+    float cs, sn;
+    bool bad_pos;   // its position is outside the table
+};
+
+__global__ void __launch_bounds__(kWarpsA * 32) append_kernel(const AppendParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = int64_t(blockIdx.x) * kWarpsA + (threadIdx.x >> 5), warps = int64_t(gridDim.x) * kWarpsA;
+    pdl_wait_prior_grid();
+    pdl_allow_next_grid();
+    if (warp >= p.rows) return;
+
+    const auto load = [&](int64_t i) {
+        Row row;
+        row.slot = __ldg(p.slots + i);
+        row.cs = 1.f, row.sn = 0.f;
+        row.bad_pos = false;
+        if (p.latent) {
+            const uint8_t* x = p.latent + i * p.latent_stride * 2;
+            row.c[0] = __ldg(reinterpret_cast<const uint4*>(x) + lane);
+            row.c[1] = __ldg(reinterpret_cast<const uint4*>(x) + 32 + lane);
+            row.r = __ldg(reinterpret_cast<const uint32_t*>(x + kMlaDv * 2) + lane);
+            if (p.cos_sin) {
+                const int pos = __ldg(p.positions + i);
+                row.bad_pos = pos < 0 || int64_t(pos) >= p.cos_rows;
+                if (!row.bad_pos) {
+                    row.cs = __ldg(p.cos_sin + int64_t(pos) * 64 + lane);
+                    row.sn = __ldg(p.cos_sin + int64_t(pos) * 64 + 32 + lane);
+                }
+            }
+        }
+        if (p.keys) row.k = __ldg(reinterpret_cast<const uint32_t*>(p.keys + i * p.key_stride * 2) + lane);
+        return row;
+    };
+    const auto weight_at = [&](const void* w, int fp32, int i) {
+        return fp32 ? __ldg(static_cast<const float*>(w) + i)
+                    : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + i));
+    };
+    float wc[16], wk[2];
+    if (p.latent_weight)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) wc[i] = weight_at(p.latent_weight, p.latent_weight_fp32, (i >> 3) * 256 + lane * 8 + (i & 7));
+    if (p.key_weight)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wk[i] = weight_at(p.key_weight, p.key_weight_fp32, lane * 2 + i);
+
+    Row row = load(warp);
+    for (int64_t i = warp; i < p.rows; i += warps) {
+        const Row now = row;
+        if (i + warps < p.rows) row = load(i + warps);
+        if (now.slot == -1) continue;
+        const bool bad_slot = now.slot < -1 || now.slot >= p.num_pages * kPageEntries;
+        if (bad_slot || now.bad_pos) {
+            if (lane == 0) atomicOr(p.err, (bad_slot ? kErrBadPage : 0u) | (now.bad_pos ? kErrBadRange : 0u));
+            continue;
+        }
+        if (p.latent) {
+            uint4 c[2] = {now.c[0], now.c[1]};
+            if (p.latent_weight) {
+                uint32_t* u = reinterpret_cast<uint32_t*>(c);
+                float ss = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 v = widen(u[j]);
+                    ss = fmaf(v.x, v.x, fmaf(v.y, v.y, ss));
+                }
+                const float inv = 1.f / sqrtf(warp_sum(ss) * (1.f / kMlaDv) + p.eps);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 v = widen(u[j]);
+                    u[j] = narrow(v.x * wc[2 * j] * inv, v.y * wc[2 * j + 1] * inv);
+                }
+            }
+            uint32_t r = now.r;
+            if (p.cos_sin) {
+                const float2 v = widen(r);
+                r = narrow(v.x * now.cs - v.y * now.sn, v.x * now.sn + v.y * now.cs);
+            }
+            uint8_t* out = p.kv_cache + now.slot * (kMlaDim * 2);
+            reinterpret_cast<uint4*>(out)[lane] = c[0];
+            reinterpret_cast<uint4*>(out)[32 + lane] = c[1];
+            reinterpret_cast<uint32_t*>(out + kMlaDv * 2)[lane] = r;
+        }
+        if (p.keys) {
+            float2 y = widen(now.k);
+            uint32_t bits = now.k;
+            if (p.key_weight) {
+                const float inv = 1.f / sqrtf(warp_sum(fmaf(y.x, y.x, y.y * y.y)) * (1.f / kHeadDim) + p.eps);
+                y = make_float2(y.x * wk[0] * inv, y.y * wk[1] * inv);
+                bits = narrow(y.x, y.y);
+            }
+            if (p.key_pool) {
+                reinterpret_cast<uint32_t*>(p.key_pool + now.slot * (kHeadDim * 2))[lane] = bits;
+            } else {
+                float top = fmaxf(fabsf(y.x), fabsf(y.y));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                float scale = top / kE4m3Max;
+                if (!(scale > 0.f) || scale > 3.0e38f) scale = 1.f;
+                uint16_t code;
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(code) : "f"(y.y / scale), "f"(y.x / scale));
+                reinterpret_cast<uint16_t*>(p.key_codes + now.slot * kHeadDim)[lane] = code;
+                if (lane == 0) p.key_scales[now.slot] = scale;
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream) {
+    static std::atomic<int> resident[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    int per_sm = resident[dev].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, append_kernel, kWarpsA * 32, 0);
+        if (e != cudaSuccess) return e;
+        resident[dev].store(per_sm, std::memory_order_relaxed);
+    }
+    const int64_t ctas = (p.rows + kWarpsA - 1) / kWarpsA, most = int64_t(sms) * per_sm;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(ctas < most ? ctas : most));
+    cfg.blockDim = dim3(kWarpsA * 32);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, append_kernel, p);
+}
+
+}  // namespace dsa

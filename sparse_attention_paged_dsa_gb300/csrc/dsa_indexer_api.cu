@@ -15,6 +15,7 @@
 #include "api_checks.h"
 #include "indexer_kernels.h"
 #include "mla_prefill_plan.h"
+#include "mla_tree_plan.h"
 
 namespace {
 
@@ -201,6 +202,26 @@ dsa_status_t make_heads_map(CUtensorMap* map, const void* ptr, int64_t rows, int
     return DSA_OK;
 }
 
+// Drafted entries [batch, tokens, 576] bf16 as (dim in slab, token, slab of 64 dims, request): boxes of one slab of
+// 64 tokens, those behind the request's arriving as zeros.
+dsa_status_t make_drafts_map(CUtensorMap* map, const void* ptr, int32_t batch, int32_t tokens) {
+    auto enc = encode_tiled();
+    if (!enc) return cuda_fail(cudaErrorNotSupported, "cuTensorMapEncodeTiled lookup");
+    const cuuint64_t dims[4] = {64, cuuint64_t(tokens), DSA_MLA_DIM / 64, cuuint64_t(batch)};
+    const cuuint64_t strides[3] = {DSA_MLA_DIM * 2, 128, cuuint64_t(tokens) * DSA_MLA_DIM * 2};
+    const cuuint32_t box[4] = {64, 64, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box,
+                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        std::snprintf(g_last_cuda_error, sizeof g_last_cuda_error, "cuTensorMapEncodeTiled(drafts): CUresult %d",
+                      int(r));
+        return DSA_ERR_CUDA;
+    }
+    return DSA_OK;
+}
+
 constexpr int kProjMaxSplit = 8;  // CTAs per cluster (portable size)
 constexpr int kProjQTiles = (DSA_HEADS * DSA_HEAD_DIM) / 128;
 constexpr int64_t kProjMaxModel = 65536;
@@ -343,6 +364,16 @@ size_t dense_parts(int groups, int32_t next_n) { return size_t(groups) * size_t(
 size_t dense_workspace_bytes(int groups, int32_t next_n) {
     return dsa::kWorkspaceHeaderBytes + kDensePlanBytes +
            dense_parts(groups, next_n) * dsa::kMlaHeads * (dsa::kMlaDv + 1) * sizeof(float);
+}
+
+constexpr int kTicketWord = 32;  // of the workspace header: the page update's, 0 between calls
+
+// Tree decode: header, cuts, plan, then two partial outputs per range and token.
+constexpr size_t kTreePlanBytes = size_t(dsa::kTreeMaxRanges) * sizeof(int32_t) + size_t(DSA_MAX_BATCH) * sizeof(int2);
+size_t tree_parts(int ranges, int32_t tokens) { return size_t(ranges) * size_t(tokens) * 2; }
+size_t tree_workspace_bytes(int ranges, int32_t tokens) {
+    return dsa::kWorkspaceHeaderBytes + kTreePlanBytes +
+           tree_parts(ranges, tokens) * dsa::kMlaHeads * (dsa::kMlaDv + 1) * sizeof(float);
 }
 
 dsa_status_t run_rmsnorm(dsa::RmsNormParams p, void* stream) {
@@ -850,6 +881,179 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
     }
     e = dsa::launch_mla_prefill(m, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA prefill launch");
+}
+
+size_t dsa_mla_tree_decode_workspace_size(int32_t batch, int32_t tokens) {
+    int pairs = 0;
+    if (batch < 1 || batch > DSA_MAX_BATCH || tokens < 1 || tokens > DSA_MAX_TREE_TOKENS) return 0;
+    if (dsa::mla_tree_pairs(&pairs) != cudaSuccess) pairs = 80;  // no device: what a large part needs
+    return tree_workspace_bytes(dsa::tree_ranges(tokens, pairs), tokens);
+}
+
+dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t num_pages, const int32_t* page_table,
+                                 const int32_t* seq_lens, const void* draft_kv, const uint64_t* tree_mask,
+                                 const int32_t* token_counts_opt, int32_t batch, int32_t tokens, int64_t max_context,
+                                 float sm_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    dsa_status_t st = check_shape(batch, max_context);
+    if (st != DSA_OK) return st;
+    if (tokens < 1) return DSA_ERR_INVALID_ARG;
+    if (tokens > DSA_MAX_TREE_TOKENS) return DSA_ERR_UNSUPPORTED;
+    if (!q || !kv_cache || !page_table || !seq_lens || !draft_kv || !tree_mask || !out || !lse)
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(draft_kv, 16) || !aligned(page_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(token_counts_opt, 4) || !aligned(tree_mask, 8) || !aligned(out, 16) ||
+        !aligned(lse, 4))
+        return DSA_ERR_INVALID_ARG;
+    if (num_pages < 1 || num_pages > kMaxPages || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+    // The tile loads address cache rows with 32-bit coordinates.
+    if (num_pages > (int64_t(1) << 31) / dsa::kPageEntries - 1) return DSA_ERR_UNSUPPORTED;
+    st = check_workspace(workspace, workspace_bytes, dsa::kWorkspaceHeaderBytes);
+    if (st != DSA_OK) return st;
+    int pairs = 0;
+    cudaError_t e = dsa::mla_tree_pairs(&pairs);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    const int ranges = dsa::tree_ranges(tokens, pairs), tiles = dsa::tree_tiles(tokens);
+    if (ranges * tiles > dsa::kTreeMaxRounds * pairs) return DSA_ERR_UNSUPPORTED;  // a device with very few SMs
+    st = check_workspace(workspace, workspace_bytes, tree_workspace_bytes(ranges, tokens));
+    if (st != DSA_OK) return st;
+    dsa::MlaTreeMaps m;
+    st = make_slabs_map(&m.q, q, int64_t(batch) * tokens * DSA_MLA_HEADS, 3, "mla q");
+    if (st != DSA_OK) return st;
+    st = make_slabs_map(&m.kv, kv_cache, num_pages * dsa::kPageEntries, 2, "mla kv");
+    if (st != DSA_OK) return st;
+    st = make_rows_map(&m.kr, kv_cache, num_pages * dsa::kPageEntries, DSA_MLA_DIM, 64, "mla kv");
+    if (st != DSA_OK) return st;
+    st = make_drafts_map(&m.d, draft_kv, batch, tokens);
+    if (st != DSA_OK) return st;
+    dsa::MlaTreeParams p{};
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.page_table = page_table;
+    p.seq_lens = seq_lens;
+    p.mask = tree_mask;
+    p.counts = token_counts_opt;
+    p.out = static_cast<__nv_bfloat16_raw*>(out);
+    p.lse = lse;
+    p.cuts = reinterpret_cast<int32_t*>(ws + dsa::kWorkspaceHeaderBytes);
+    p.plan = reinterpret_cast<int2*>(p.cuts + dsa::kTreeMaxRanges);
+    p.o_part = reinterpret_cast<float*>(ws + dsa::kWorkspaceHeaderBytes + kTreePlanBytes);
+    p.lse_part = p.o_part + tree_parts(ranges, tokens) * dsa::kMlaHeads * dsa::kMlaDv;
+    p.err = static_cast<uint32_t*>(workspace);
+    p.num_pages = num_pages;
+    p.max_context = max_context;
+    p.table_width = int32_t(max_context / DSA_PAGE_TOKENS);
+    p.batch = batch;
+    p.tokens = tokens;
+    p.tiles = tiles;
+    p.ranges = ranges;
+    p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+    e = dsa::launch_mla_tree(m, p, pairs, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA tree decode launch");
+}
+
+dsa_status_t dsa_pages_update(const int32_t* seq_lens, const int32_t* new_lens, int32_t batch, int64_t max_context,
+                              int32_t* page_table, int32_t* free_pages, int64_t num_pages, const int32_t* free_count,
+                              int64_t max_slots, int32_t* seq_lens_out, int32_t* free_count_out, int32_t* cu_slots,
+                              int64_t* slots, int32_t* positions, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+    dsa_status_t st = check_shape(batch, max_context);
+    if (st != DSA_OK) return st;
+    if (!seq_lens || !new_lens || !page_table || !free_pages || !free_count || !seq_lens_out || !free_count_out ||
+        !cu_slots || max_slots < 0 || (max_slots > 0 && (!slots || !positions)))
+        return DSA_ERR_INVALID_ARG;
+    for (const void* a : {static_cast<const void*>(seq_lens), static_cast<const void*>(new_lens),
+                          static_cast<const void*>(page_table), static_cast<const void*>(free_pages),
+                          static_cast<const void*>(free_count), static_cast<const void*>(seq_lens_out),
+                          static_cast<const void*>(free_count_out), static_cast<const void*>(cu_slots)})
+        if (!aligned(a, 4)) return DSA_ERR_INVALID_ARG;
+    if (!aligned(slots, 16) || !aligned(positions, 16)) return DSA_ERR_INVALID_ARG;
+    if (num_pages < 1 || num_pages > kMaxPages) return DSA_ERR_INVALID_ARG;
+    if (max_slots > kMaxPages) return DSA_ERR_UNSUPPORTED;
+    st = check_workspace(workspace, workspace_bytes, dsa::kWorkspaceHeaderBytes);
+    if (st != DSA_OK) return st;
+    dsa::PagesParams p{};
+    p.seq_lens = seq_lens;
+    p.new_lens = new_lens;
+    p.page_table = page_table;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.seq_lens_out = seq_lens_out;
+    p.free_count_out = free_count_out;
+    p.cu_slots = cu_slots;
+    p.slots = slots;
+    p.positions = positions;
+    p.err = static_cast<uint32_t*>(workspace);
+    p.ticket = p.err + kTicketWord;
+    p.num_pages = num_pages;
+    p.max_context = max_context;
+    p.max_slots = max_slots;
+    p.table_width = int32_t(max_context / DSA_PAGE_TOKENS);
+    p.batch = batch;
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    e = dsa::launch_pages_update(p, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DSA_OK : cuda_fail(e, "page update launch");
+}
+
+dsa_status_t dsa_cache_append(const int64_t* slots, int64_t rows, const void* latent_opt, int64_t latent_stride,
+                              const void* latent_weight_opt, int32_t latent_weight_fp32, const float* cos_sin_opt,
+                              int64_t cos_rows, const int32_t* positions, void* kv_cache, const void* index_keys_opt,
+                              int64_t key_stride, const void* index_weight_opt, int32_t index_weight_fp32,
+                              void* key_pool_opt, void* key_codes_opt, float* key_scales_opt, int64_t num_pages,
+                              float eps, void* workspace, size_t workspace_bytes, void* stream) {
+    const auto flag = [](int32_t v) { return v == 0 || v == 1; };
+    if (rows < 0 || num_pages < 1 || num_pages > kMaxPages || !std::isfinite(eps) || eps < 0.f ||
+        !flag(latent_weight_fp32) || !flag(index_weight_fp32))
+        return DSA_ERR_INVALID_ARG;
+    if (rows > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+    if (rows == 0) return DSA_OK;
+    // What each part comes with.
+    if (!slots || (!latent_opt && !index_keys_opt)) return DSA_ERR_INVALID_ARG;
+    if (latent_opt && !kv_cache) return DSA_ERR_INVALID_ARG;
+    if (!latent_opt && (kv_cache || latent_weight_opt || cos_sin_opt)) return DSA_ERR_INVALID_ARG;
+    if (cos_sin_opt && (cos_rows < 1 || !positions)) return DSA_ERR_INVALID_ARG;
+    if ((key_codes_opt == nullptr) != (key_scales_opt == nullptr) || (key_pool_opt && key_codes_opt))
+        return DSA_ERR_INVALID_ARG;
+    if (index_keys_opt ? !key_pool_opt && !key_codes_opt : key_pool_opt || key_codes_opt || index_weight_opt)
+        return DSA_ERR_INVALID_ARG;
+    if (rows == 1) latent_stride = DSA_MLA_DIM, key_stride = DSA_HEAD_DIM;  // no second row: no stride
+    if ((latent_opt && (latent_stride < 0 || latent_stride % 8 != 0)) ||
+        (index_keys_opt && (key_stride < 0 || key_stride % 2 != 0)))
+        return DSA_ERR_INVALID_ARG;
+    if (!aligned(slots, 8) || !aligned(latent_opt, 16) || !aligned(kv_cache, 16) || !aligned(index_keys_opt, 4) ||
+        !aligned(key_pool_opt, 4) || !aligned(key_codes_opt, 2) || !aligned(key_scales_opt, 4) ||
+        !aligned(cos_sin_opt, 4) || !aligned(positions, 4) ||
+        !aligned(latent_weight_opt, latent_weight_fp32 ? 4 : 2) || !aligned(index_weight_opt, index_weight_fp32 ? 4 : 2))
+        return DSA_ERR_INVALID_ARG;
+    dsa_status_t st = check_workspace(workspace, workspace_bytes, dsa::kWorkspaceHeaderBytes);
+    if (st != DSA_OK) return st;
+    dsa::AppendParams p{};
+    p.slots = slots;
+    p.latent = static_cast<const uint8_t*>(latent_opt);
+    p.latent_weight = latent_weight_opt;
+    p.cos_sin = cos_sin_opt;
+    p.positions = positions;
+    p.keys = static_cast<const uint8_t*>(index_keys_opt);
+    p.key_weight = index_weight_opt;
+    p.kv_cache = static_cast<uint8_t*>(kv_cache);
+    p.key_pool = static_cast<uint8_t*>(key_pool_opt);
+    p.key_codes = static_cast<uint8_t*>(key_codes_opt);
+    p.key_scales = key_scales_opt;
+    p.err = static_cast<uint32_t*>(workspace);
+    p.rows = rows;
+    p.latent_stride = latent_stride;
+    p.key_stride = key_stride;
+    p.cos_rows = cos_rows;
+    p.num_pages = num_pages;
+    p.latent_weight_fp32 = latent_weight_fp32;
+    p.key_weight_fp32 = index_weight_fp32;
+    p.eps = eps;
+    int sms = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    e = dsa::launch_append(p, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DSA_OK : cuda_fail(e, "cache append launch");
 }
 
 }  // extern "C"

@@ -47,6 +47,7 @@ constexpr uint32_t kErrSeqLenClamped = 0x1u;
 constexpr uint32_t kErrBadPage = 0x2u;
 constexpr uint32_t kErrWaitTimeout = 0x4u;
 constexpr uint32_t kErrBadRange = 0x8u;
+constexpr uint32_t kErrNoPages = 0x10u;
 
 struct ScoresParams {
     const int32_t* page_table;  // [batch, table_width]
@@ -166,6 +167,51 @@ struct MlaDenseParams {
 cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& kr_map,
                              const CUtensorMap& o_map, const MlaDenseParams& p, cudaStream_t stream);
 
+// The log-sum-exp merge of requests that cross ranges (of the dense and the tree decode).
+struct MlaMergeParams {
+    const int2* plan;          // [batch] first and last range of each request (equal: one)
+    const int32_t* cuts;       // [ranges] the request that the range is the second one of, or -1
+    const float* o_part;       // [ranges * tokens * 2, 64, 512] partial outputs: of a range and token the one
+    const float* lse_part;     // [ranges * tokens * 2, 64]      that began earlier, then the one that begins here
+    __nv_bfloat16_raw* out;    // [batch, tokens, 64, 512]
+    float* lse;                // [batch, tokens, 64]
+    const int32_t* counts;     // [batch] tokens of each request, or null: all
+    int32_t tokens;
+    int32_t by_cut;            // rows go by cuts (there are fewer ranges than requests)
+};
+cudaError_t launch_mla_merge(const MlaMergeParams& p, int batch, int ranges, cudaStream_t stream);
+
+// Latent attention decode for a tree of drafted tokens, 1-64 of them per request.
+struct MlaTreeParams {
+    const int32_t* page_table; // [batch, table_width]
+    const int32_t* seq_lens;   // [batch] tokens in the cache
+    const uint64_t* mask;      // [batch, tokens] bit i: the token sees drafted entry i
+    const int32_t* counts;     // [batch] drafted tokens, or null: all `tokens`
+    __nv_bfloat16_raw* out;    // [batch, tokens, 64, 512]
+    float* lse;                // [batch, tokens, 64]
+    int2* plan;                // as for the merge
+    int32_t* cuts;
+    float* o_part;
+    float* lse_part;
+    uint32_t* err;             // device error word
+    int64_t num_pages;
+    int64_t max_context;
+    int32_t table_width;
+    int32_t batch;
+    int32_t tokens;
+    int32_t tiles;             // pairs of tokens
+    int32_t ranges;            // tree_ranges
+    float sm_scale_log2;       // sm_scale * log2(e)
+};
+// q: batch * tokens * 64 rows and kv, the cache's: 576-wide bf16 rows as (dim in slab, row, slab), boxes of 64
+// rows x 3 and 2 slabs; kr: the cache's rows as (dim, row), boxes of 64 x 64; d: the drafted entries as (dim in
+// slab, token, slab, request), boxes of 64 tokens x 1 slab.  All 128-byte-swizzled.
+struct MlaTreeMaps {
+    CUtensorMap q, kv, kr, d;
+};
+cudaError_t mla_tree_pairs(int* pairs);  // CTA pairs that the current device holds
+cudaError_t launch_mla_tree(const MlaTreeMaps& m, const MlaTreeParams& p, int pairs, cudaStream_t stream);
+
 // Latent attention over ragged prompts, expanded form: per-head 128 + 64 shared key dims, 128 value dims.
 constexpr int kPrefillQk = 192;
 constexpr int kPrefillDv = 128;
@@ -225,5 +271,52 @@ struct RmsNormParams {
 // align: 32, 16 or 2, the boundary in bytes of every 16-element unit (codes: half of it); d is a multiple
 // of align / 2.
 cudaError_t launch_rmsnorm(RmsNormParams p, int align, int sms, cudaStream_t stream);
+
+// Page tables, lengths, free pages and slots, from the lengths now and those wanted.
+struct PagesParams {
+    const int32_t* seq_lens;   // [batch] tokens now
+    const int32_t* new_lens;   // [batch] tokens wanted
+    int32_t* page_table;       // [batch, table_width]
+    int32_t* free_pages;       // [num_pages] a stack
+    const int32_t* free_count; // [1]
+    int32_t* seq_lens_out;     // [batch] (may be seq_lens)
+    int32_t* free_count_out;   // [1] (may be free_count)
+    int32_t* cu_slots;         // [batch + 1]
+    int64_t* slots;            // [max_slots], 16-byte aligned like positions
+    int32_t* positions;        // [max_slots]
+    uint32_t* err;             // device error word
+    uint32_t* ticket;          // in the workspace header, 0 between calls
+    int64_t num_pages;
+    int64_t max_context;
+    int64_t max_slots;
+    int32_t table_width;
+    int32_t batch;
+};
+cudaError_t launch_pages_update(const PagesParams& p, int sms, cudaStream_t stream);
+
+// New entries into the paged caches at their slots.
+struct AppendParams {
+    const int64_t* slots;      // [rows], -1: skipped
+    const uint8_t* latent;     // bf16 [rows, 576], rows latent_stride elements apart, or null
+    const void* latent_weight; // [512] bf16 or fp32, or null: no norm
+    const float* cos_sin;      // [cos_rows, 64], or null: no rotation
+    const int32_t* positions;  // [rows]
+    const uint8_t* keys;       // bf16 [rows, 64], rows key_stride elements apart, or null
+    const void* key_weight;    // [64] bf16 or fp32, or null: no norm
+    uint8_t* kv_cache;         // bf16 [num_pages, 64, 576]
+    uint8_t* key_pool;         // bf16 [num_pages, 64, 64], or null: the two below
+    uint8_t* key_codes;        // e4m3 [num_pages, 64, 64]
+    float* key_scales;         // [num_pages, 64]
+    uint32_t* err;             // device error word
+    int64_t rows;
+    int64_t latent_stride;
+    int64_t key_stride;
+    int64_t cos_rows;
+    int64_t num_pages;
+    int32_t latent_weight_fp32;
+    int32_t key_weight_fp32;
+    float eps;
+};
+cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream);
 
 }  // namespace dsa

@@ -1,0 +1,102 @@
+// mla_merge_kernel.cu -- joins the partial outputs of requests whose entries the
+// dense and the tree decode cut between ranges.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "indexer_kernels.h"
+#include "sm103_ptx.cuh"
+
+namespace dsa {
+namespace {
+
+// o[r] = sum_i exp(lse_i - lse) o_i over the partials of a split request, lse = log sum_i exp(lse_i).
+// 512 threads.  128 of them per 512 dims, four heads a CTA; or (kOneHead: few rows, each split many ways)
+// 64 per 256 dims, half a head a CTA, whose partials go to the eight groups in turn.  Grid (heads / 4 or
+// heads x 2, requests or cuts x tokens).
+template <bool kOneHead>
+__global__ void __launch_bounds__(512) mla_merge_kernel(const MlaMergeParams p) {
+    __shared__ float wgt[kOneHead ? 1 : 4][kMlaMaxGroups];
+    __shared__ float4 acc_s[kOneHead ? 7 : 1][64];
+    pdl_wait_prior_grid();
+    pdl_allow_next_grid();
+    const int quarter = threadIdx.x >> (kOneHead ? 6 : 7);
+    const int d4 = kOneHead ? (int(blockIdx.x) & 1) * 64 + (threadIdx.x & 63) : threadIdx.x & 127;
+    const int h = kOneHead ? int(blockIdx.x) >> 1 : int(blockIdx.x) * 4 + quarter;
+    const int token = int(blockIdx.y) % p.tokens;
+    const int b = p.by_cut ? p.cuts[blockIdx.y / p.tokens] : int(blockIdx.y) / p.tokens;
+    if (b < 0) return;
+    if (p.counts && token >= __ldg(p.counts + b)) return;  // (a count out of range is held to it: no more tokens than these)
+    const int64_t row = int64_t(b) * p.tokens + token;
+    const int2 g = p.plan[b];
+    if (g.x == g.y) return;  // one range: written by the attention kernel
+    const int S = g.y - g.x + 1;
+    // partial i: range g.x + i; the first one ends in the next range, the others began earlier
+    const auto part = [&](int i) { return (int64_t(g.x + i) * p.tokens + token) * 2 + (i == 0 ? 1 : 0); };
+    if ((threadIdx.x & 127) < 32 && (!kOneHead || quarter == 0)) {
+        float* const w = wgt[kOneHead ? 0 : quarter];
+        const int lane = threadIdx.x & 31;
+        float mx = -INFINITY;
+        for (int i = lane; i < S; i += 32) {
+            w[i] = p.lse_part[part(i) * kMlaHeads + h];
+            mx = fmaxf(mx, w[i]);
+        }
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        float sum = 0.f;
+        for (int i = lane; i < S; i += 32) {
+            const float e = w[i] == -INFINITY ? 0.f : expf(w[i] - mx);  // (a NaN, which the maximum passes by, stays)
+            w[i] = e;
+            sum += e;
+        }
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        for (int i = lane; i < S; i += 32) w[i] *= inv;
+        if (lane == 0 && (!kOneHead || (blockIdx.x & 1) == 0))
+            p.lse[row * kMlaHeads + h] = sum == 0.f ? -INFINITY : mx + logf(sum);
+    }
+    __syncthreads();
+    const float* const w = wgt[kOneHead ? 0 : quarter];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = kOneHead ? quarter : 0; i < S; i += kOneHead ? 8 : 1) {
+        const float4 v = *reinterpret_cast<const float4*>(p.o_part + (part(i) * kMlaHeads + h) * kMlaDv + 4 * d4);
+        acc.x = fmaf(w[i], v.x, acc.x), acc.y = fmaf(w[i], v.y, acc.y);
+        acc.z = fmaf(w[i], v.z, acc.z), acc.w = fmaf(w[i], v.w, acc.w);
+    }
+    if constexpr (kOneHead) {
+        if (quarter > 0) acc_s[quarter - 1][threadIdx.x & 63] = acc;
+        __syncthreads();
+        if (quarter > 0) return;
+#pragma unroll
+        for (int q = 0; q < 7; ++q) {
+            const float4 v = acc_s[q][threadIdx.x & 63];
+            acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+    *reinterpret_cast<uint2*>(p.out + (row * kMlaHeads + h) * kMlaDv + 4 * d4) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+}  // namespace
+
+cudaError_t launch_mla_merge(const MlaMergeParams& p, int batch, int ranges, cudaStream_t stream) {
+    // One row of CTAs per request, or, where they are fewer, per cut between ranges.  Few rows are split
+    // many ways: more threads per row read more partials at a time.
+    const int rows = (p.by_cut ? ranges : batch) * p.tokens;
+    const bool one_head = rows <= 16;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(one_head ? kMlaHeads * 2 : kMlaHeads / 4, unsigned(rows));
+    cfg.blockDim = dim3(512);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return one_head ? cudaLaunchKernelEx(&cfg, mla_merge_kernel<true>, p)
+                    : cudaLaunchKernelEx(&cfg, mla_merge_kernel<false>, p);
+}
+
+}  // namespace dsa

@@ -1,0 +1,46 @@
+// mla_tree_plan.h -- how the tree decode cuts a batch's blocks into ranges, and how many ranges a call has.
+// Plain arithmetic, compiled for the device and, by the tests, for the host.
+#pragma once
+
+#include "mla_dense_plan.h"
+
+namespace dsa {
+
+constexpr int kTreeSegUnits = 2;     // a request's fixed cost in a range (q, first products, output), in blocks
+constexpr int kTreeWholeBlocks = 3;  // requests of at most this many blocks are not split
+constexpr int kTreeMaxRanges = 256;
+constexpr int kTreeMaxRounds = 8;    // units of a CTA pair, at most
+constexpr int kTreePlanRounds = 3;   // rounds that are tried for a full device
+
+// A request's pages: the live ones of the cache and one of its drafted tokens, where it has any.
+DSA_PLAN int tree_cache_pages(int tokens) { return (((tokens + 3) >> 2) + 63) >> 6; }
+// Its blocks of two pages.
+DSA_PLAN int tree_blocks(int cache_pages, int drafted) { return drafted > 0 ? (cache_pages + 2) >> 1 : 0; }
+DSA_PLAN int tree_units(int blocks) { return blocks ? blocks + kTreeSegUnits : 0; }
+
+// Where a cut inside a request of `blocks` blocks, whose units start at u, comes to lie.
+DSA_PLAN int tree_settled_cut(int cut, int u, int blocks) {
+    const int n = tree_units(blocks);
+    return blocks > kTreeWholeBlocks ? cut : ((cut - u) * 2 < n ? u : u + n);
+}
+
+// Pairs of drafted tokens, each a unit in every range.
+DSA_PLAN int tree_tiles(int tokens) { return (tokens + 1) / 2; }
+
+// Ranges of a call on `pairs` CTA pairs: as many as fill them in few rounds.  A round more is worth it for
+// a twentieth of the device.
+DSA_PLAN int tree_ranges(int tokens, int pairs) {
+    const int tiles = tree_tiles(tokens);
+    int best = 1, best_rounds = 0, best_units = 0;  // units: of best_rounds * pairs places
+    for (int k = 1; k <= kTreePlanRounds; ++k) {
+        int r = k * pairs / tiles;
+        if (r > kTreeMaxRanges) r = kTreeMaxRanges;
+        if (r < 1) continue;
+        // r tiles / (k pairs) against best_units / (best_rounds pairs) + 1 / 20
+        if (best_rounds == 0 || 20 * (r * tiles * best_rounds - best_units * k) > k * best_rounds * pairs)
+            best = r, best_rounds = k, best_units = r * tiles;
+    }
+    return best;
+}
+
+}  // namespace dsa
