@@ -161,14 +161,15 @@ dsa_status_t make_rows_map(CUtensorMap* map, const void* ptr, int64_t rows, int6
     return DSA_OK;
 }
 
-// 576-wide bf16 rows as (dim in slab, row, slab of 64 dims): boxes of 64 rows x box_slabs slabs, 128-byte
-// swizzle, so that one copy fills several 64 x 64 slabs.
-dsa_status_t make_slabs_map(CUtensorMap* map, const void* ptr, int64_t rows, uint32_t box_slabs, const char* what) {
+// 576-wide bf16 rows as (dim in slab, row, slab of 64 dims): boxes of box_rows rows x box_slabs slabs, 128-byte
+// swizzle, so that one copy fills several slabs.
+dsa_status_t make_slabs_map(CUtensorMap* map, const void* ptr, int64_t rows, uint32_t box_slabs, const char* what,
+                            uint32_t box_rows = 64) {
     auto enc = encode_tiled();
     if (!enc) return cuda_fail(cudaErrorNotSupported, "cuTensorMapEncodeTiled lookup");
     const cuuint64_t dims[3] = {64, cuuint64_t(rows), DSA_MLA_DIM / 64};
     const cuuint64_t strides[2] = {DSA_MLA_DIM * 2, 128};
-    const cuuint32_t box[3] = {64, 64, box_slabs};
+    const cuuint32_t box[3] = {64, box_rows, box_slabs};
     const cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
                            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -203,13 +204,13 @@ dsa_status_t make_heads_map(CUtensorMap* map, const void* ptr, int64_t rows, int
 }
 
 // Drafted entries [batch, tokens, 576] bf16 as (dim in slab, token, slab of 64 dims, request): boxes of one slab of
-// 64 tokens, those behind the request's arriving as zeros.
-dsa_status_t make_drafts_map(CUtensorMap* map, const void* ptr, int32_t batch, int32_t tokens) {
+// box_rows tokens, those behind the request's arriving as zeros.
+dsa_status_t make_drafts_map(CUtensorMap* map, const void* ptr, int32_t batch, int32_t tokens, uint32_t box_rows) {
     auto enc = encode_tiled();
     if (!enc) return cuda_fail(cudaErrorNotSupported, "cuTensorMapEncodeTiled lookup");
     const cuuint64_t dims[4] = {64, cuuint64_t(tokens), DSA_MLA_DIM / 64, cuuint64_t(batch)};
     const cuuint64_t strides[3] = {DSA_MLA_DIM * 2, 128, cuuint64_t(tokens) * DSA_MLA_DIM * 2};
-    const cuuint32_t box[4] = {64, 64, 1, 1};
+    const cuuint32_t box[4] = {64, box_rows, 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box,
                            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -368,13 +369,25 @@ size_t dense_workspace_bytes(int groups, int32_t next_n) {
 
 constexpr int kTicketWord = 32;  // of the workspace header: the page update's, 0 between calls
 
-// Tree decode: header, cuts, plan, then two partial outputs per range and token.
-constexpr size_t kTreePlanBytes = size_t(dsa::kTreeMaxRanges) * sizeof(int32_t) + size_t(DSA_MAX_BATCH) * sizeof(int2);
-size_t tree_parts(int ranges, int32_t tokens) { return size_t(ranges) * size_t(tokens) * 2; }
-size_t tree_workspace_bytes(int ranges, int32_t tokens) {
-    return dsa::kWorkspaceHeaderBytes + kTreePlanBytes +
-           tree_parts(ranges, tokens) * dsa::kMlaHeads * (dsa::kMlaDv + 1) * sizeof(float);
-}
+// Tree decode: header, cuts, plan, flags, then two partial outputs per range and token.
+constexpr size_t kTreeFlagBytes = size_t(dsa::kTreeMaxFlags + 64) * sizeof(uint32_t);
+constexpr size_t kTreePlanBytes =
+    size_t(dsa::kTreeMaxRanges) * sizeof(int32_t) + size_t(DSA_MAX_BATCH) * sizeof(int2) + kTreeFlagBytes;
+struct TreeShape {
+    int pairs, quads;                                     // clusters of two and of four CTAs that fit the device
+    int pair_tiles, pair_ranges, quad_tiles, quad_ranges;
+    TreeShape(int32_t tokens, int pairs_, int quads_) : pairs(pairs_), quads(quads_) {
+        pair_tiles = dsa::tree_tiles(tokens, 2), pair_ranges = dsa::tree_ranges(pair_tiles, pairs);
+        quad_tiles = dsa::tree_tiles(tokens, 4), quad_ranges = dsa::tree_ranges(quad_tiles, quads);
+    }
+    size_t parts(int32_t tokens) const {
+        return size_t(pair_ranges > quad_ranges ? pair_ranges : quad_ranges) * size_t(tokens) * 2;
+    }
+    size_t workspace_bytes(int32_t tokens) const {
+        return dsa::kWorkspaceHeaderBytes + kTreePlanBytes +
+               parts(tokens) * dsa::kMlaHeads * (dsa::kMlaDv + 1) * sizeof(float);
+    }
+};
 
 dsa_status_t run_rmsnorm(dsa::RmsNormParams p, void* stream) {
     if (p.rows < 0 || p.rows > INT32_MAX || p.d < 1 || p.x_stride < 0 || !std::isfinite(p.eps) || p.eps < 0.f ||
@@ -884,10 +897,11 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
 }
 
 size_t dsa_mla_tree_decode_workspace_size(int32_t batch, int32_t tokens) {
-    int pairs = 0;
+    int pairs = 0, quads = 0;
     if (batch < 1 || batch > DSA_MAX_BATCH || tokens < 1 || tokens > DSA_MAX_TREE_TOKENS) return 0;
-    if (dsa::mla_tree_pairs(&pairs) != cudaSuccess) pairs = 80;  // no device: what a large part needs
-    return tree_workspace_bytes(dsa::tree_ranges(tokens, pairs), tokens);
+    if (dsa::mla_tree_pairs(&pairs) != cudaSuccess || dsa::mla_tree_quads(&quads) != cudaSuccess)
+        pairs = 80, quads = 40;  // no device: what a large part needs
+    return TreeShape(tokens, pairs, quads).workspace_bytes(tokens);
 }
 
 dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t num_pages, const int32_t* page_table,
@@ -910,44 +924,62 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
     if (num_pages > (int64_t(1) << 31) / dsa::kPageEntries - 1) return DSA_ERR_UNSUPPORTED;
     st = check_workspace(workspace, workspace_bytes, dsa::kWorkspaceHeaderBytes);
     if (st != DSA_OK) return st;
-    int pairs = 0;
+    int pairs = 0, quads = 0;
     cudaError_t e = dsa::mla_tree_pairs(&pairs);
+    if (e == cudaSuccess) e = dsa::mla_tree_quads(&quads);
     if (e != cudaSuccess) return cuda_fail(e, "device query");
-    const int ranges = dsa::tree_ranges(tokens, pairs), tiles = dsa::tree_tiles(tokens);
-    if (ranges * tiles > dsa::kTreeMaxRounds * pairs) return DSA_ERR_UNSUPPORTED;  // a device with very few SMs
-    st = check_workspace(workspace, workspace_bytes, tree_workspace_bytes(ranges, tokens));
+    const TreeShape shape(tokens, pairs, quads);
+    if (shape.pair_ranges * shape.pair_tiles > dsa::kTreeMaxRounds * pairs) return DSA_ERR_UNSUPPORTED;  // few SMs
+    st = check_workspace(workspace, workspace_bytes, shape.workspace_bytes(tokens));
     if (st != DSA_OK) return st;
-    dsa::MlaTreeMaps m;
-    st = make_slabs_map(&m.q, q, int64_t(batch) * tokens * DSA_MLA_HEADS, 3, "mla q");
-    if (st != DSA_OK) return st;
-    st = make_slabs_map(&m.kv, kv_cache, num_pages * dsa::kPageEntries, 2, "mla kv");
-    if (st != DSA_OK) return st;
-    st = make_rows_map(&m.kr, kv_cache, num_pages * dsa::kPageEntries, DSA_MLA_DIM, 64, "mla kv");
-    if (st != DSA_OK) return st;
-    st = make_drafts_map(&m.d, draft_kv, batch, tokens);
-    if (st != DSA_OK) return st;
+    const bool quad = tokens > 2 && max_context > 4096 && shape.quad_ranges * shape.quad_tiles <= dsa::kTreeMaxRounds * quads;
     dsa::MlaTreeParams p{};
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.page_table = page_table;
     p.seq_lens = seq_lens;
+    p.q = static_cast<const __nv_bfloat16_raw*>(q);
     p.mask = tree_mask;
     p.counts = token_counts_opt;
     p.out = static_cast<__nv_bfloat16_raw*>(out);
     p.lse = lse;
     p.cuts = reinterpret_cast<int32_t*>(ws + dsa::kWorkspaceHeaderBytes);
     p.plan = reinterpret_cast<int2*>(p.cuts + dsa::kTreeMaxRanges);
+    p.flags = reinterpret_cast<uint32_t*>(p.plan + DSA_MAX_BATCH);
+    p.again = p.flags + dsa::kTreeMaxFlags;
     p.o_part = reinterpret_cast<float*>(ws + dsa::kWorkspaceHeaderBytes + kTreePlanBytes);
-    p.lse_part = p.o_part + tree_parts(ranges, tokens) * dsa::kMlaHeads * dsa::kMlaDv;
+    p.lse_part = p.o_part + shape.parts(tokens) * dsa::kMlaHeads * dsa::kMlaDv;
     p.err = static_cast<uint32_t*>(workspace);
     p.num_pages = num_pages;
     p.max_context = max_context;
     p.table_width = int32_t(max_context / DSA_PAGE_TOKENS);
     p.batch = batch;
     p.tokens = tokens;
-    p.tiles = tiles;
-    p.ranges = ranges;
     p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
-    e = dsa::launch_mla_tree(m, p, pairs, static_cast<cudaStream_t>(stream));
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    dsa::MlaTreeMaps m;
+    const int64_t q_rows = int64_t(batch) * tokens * DSA_MLA_HEADS, kv_rows = num_pages * dsa::kPageEntries;
+    if (quad) {
+        p.tile_tokens = 4;
+        p.tiles = shape.quad_tiles;
+        p.ranges = shape.quad_ranges;
+        st = make_slabs_map(&m.q, q, q_rows, 1, "mla q", 128);
+        if (st == DSA_OK) st = make_slabs_map(&m.kv, kv_cache, kv_rows, 2, "mla kv");
+        if (st == DSA_OK) st = make_slabs_map(&m.kr, kv_cache, kv_rows, 3, "mla kv", 32);
+        if (st == DSA_OK) st = make_drafts_map(&m.d, draft_kv, batch, tokens, 32);
+        if (st != DSA_OK) return st;
+        e = dsa::launch_mla_tree_quad(m, p, quads, cs);
+        if (e != cudaSuccess) return cuda_fail(e, "MLA tree decode launch");
+        p.redo = 4 * (p.ranges * p.tiles < quads ? p.ranges * p.tiles : quads);
+    }
+    p.tile_tokens = 2;
+    p.tiles = shape.pair_tiles;
+    p.ranges = shape.pair_ranges;
+    st = make_slabs_map(&m.q, q, q_rows, 3, "mla q");
+    if (st == DSA_OK) st = make_slabs_map(&m.kv, kv_cache, kv_rows, 2, "mla kv");
+    if (st == DSA_OK) st = make_rows_map(&m.kr, kv_cache, kv_rows, DSA_MLA_DIM, 64, "mla kv");
+    if (st == DSA_OK) st = make_drafts_map(&m.d, draft_kv, batch, tokens, 64);
+    if (st != DSA_OK) return st;
+    e = dsa::launch_mla_tree(m, p, pairs, cs);
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA tree decode launch");
 }
 

@@ -176,6 +176,7 @@ struct MlaMergeParams {
     __nv_bfloat16_raw* out;    // [batch, tokens, 64, 512]
     float* lse;                // [batch, tokens, 64]
     const int32_t* counts;     // [batch] tokens of each request, or null: all
+    const uint32_t* run;       // 0 there: nothing is to be done (null: there is)
     int32_t tokens;
     int32_t by_cut;            // rows go by cuts (there are fewer ranges than requests)
 };
@@ -183,6 +184,7 @@ cudaError_t launch_mla_merge(const MlaMergeParams& p, int batch, int ranges, cud
 
 // Latent attention decode for a tree of drafted tokens, 1-64 of them per request.
 struct MlaTreeParams {
+    const __nv_bfloat16_raw* q; // [batch, tokens, 64, 576]
     const int32_t* page_table; // [batch, table_width]
     const int32_t* seq_lens;   // [batch] tokens in the cache
     const uint64_t* mask;      // [batch, tokens] bit i: the token sees drafted entry i
@@ -199,18 +201,25 @@ struct MlaTreeParams {
     int32_t table_width;
     int32_t batch;
     int32_t tokens;
-    int32_t tiles;             // pairs of tokens
+    int32_t tile_tokens;       // tokens of a tile: 2, a cluster of two CTAs; 4, one of four
+    int32_t tiles;
     int32_t ranges;            // tree_ranges
+    uint32_t* flags;           // [kTreeMaxFlags] of the larger kernel's CTAs: its outputs are not to be used
+    uint32_t* again;           // did the smaller kernel do the call again?
+    int32_t redo;              // (smaller kernel) flags to look at: leave if none is set; 0: the call is its own
     float sm_scale_log2;       // sm_scale * log2(e)
 };
-// q: batch * tokens * 64 rows and kv, the cache's: 576-wide bf16 rows as (dim in slab, row, slab), boxes of 64
-// rows x 3 and 2 slabs; kr: the cache's rows as (dim, row), boxes of 64 x 64; d: the drafted entries as (dim in
-// slab, token, slab, request), boxes of 64 tokens x 1 slab.  All 128-byte-swizzled.
+// 576-wide bf16 rows as (dim in slab, row, slab), the drafted entries as (dim in slab, token, slab, request), all
+// 128-byte-swizzled.  Boxes of the smaller kernel: q 64 rows x 3 slabs, kv 64 x 2, d 64 x 1, kr 64 x 64 of the
+// cache's rows as (dim, row); of the larger: q 128 x 1, kv 64 x 2, kr 32 x 3, d 32 x 1.
 struct MlaTreeMaps {
     CUtensorMap q, kv, kr, d;
 };
-cudaError_t mla_tree_pairs(int* pairs);  // CTA pairs that the current device holds
+cudaError_t mla_tree_pairs(int* pairs);  // clusters that the current device holds
+cudaError_t mla_tree_quads(int* quads);
+// Each with its merge.
 cudaError_t launch_mla_tree(const MlaTreeMaps& m, const MlaTreeParams& p, int pairs, cudaStream_t stream);
+cudaError_t launch_mla_tree_quad(const MlaTreeMaps& m, const MlaTreeParams& p, int quads, cudaStream_t stream);
 
 // Latent attention over ragged prompts, expanded form: per-head 128 + 64 shared key dims, 128 value dims.
 constexpr int kPrefillQk = 192;

@@ -21,6 +21,7 @@ __global__ void __launch_bounds__(512) mla_merge_kernel(const MlaMergeParams p) 
     __shared__ float4 acc_s[kOneHead ? 7 : 1][64];
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
+    if (p.run && *p.run == 0) return;
     const int quarter = threadIdx.x >> (kOneHead ? 6 : 7);
     const int d4 = kOneHead ? (int(blockIdx.x) & 1) * 64 + (threadIdx.x & 63) : threadIdx.x & 127;
     const int h = kOneHead ? int(blockIdx.x) >> 1 : int(blockIdx.x) * 4 + quarter;

@@ -53,13 +53,13 @@
 #include "cta_pair.cuh"
 #include "indexer_kernels.h"
 #include "mla_common.cuh"
-#include "mla_tree_plan.h"
+#include "mla_tree_common.cuh"
 #include "sm103_ptx.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kPg = kPageEntries;             // entries of a page, rows of a CTA (a token's heads)
+constexpr int kThreadsT = 384;
 constexpr int kSlabT = kPg * 128;             // 64 rows x 64 bf16 dims, 8 KiB
 constexpr int kSlabsT = kMlaDim / 64;         // 9
 constexpr int kKeyGroups = 5;                 // slab pairs of the value dims, and the last slab
@@ -70,19 +70,10 @@ constexpr int kOffKT = kOffQT + kSlabsT * kSlabT;
 constexpr int kOffVT = kOffKT + kSlabsT * kSlabT;
 constexpr int kOffPT = kOffVT + kValGroups * kGroupV;  // P: 64 rows x 64 entries of each page
 constexpr int kOffCtlT = kOffPT + 2 * kSlabT;
-constexpr int kThreadsT = 384;
-constexpr int kWarpsT = kThreadsT / 32;
-constexpr int kSoftWarps = 8;
 constexpr uint32_t kTmemColsT = 512;
 constexpr uint32_t kColST = 0;    // S: 2 x 64 columns
 constexpr uint32_t kColOT = 128;  // O: 2 x 128 columns
 constexpr float kRaise = 20.0f;   // log2; a weight's rounding is relative, so nothing is lost below it
-constexpr float kLn2T = 0.69314718055994531f;
-
-struct UnitT {
-    int lo, hi;                  // the range, in units of the plan
-    int first_req, first_start;  // request of its first unit, and where that request's units start
-};
 
 struct __align__(16) TreeCtl {
     uint64_t k_full[kKeyGroups], k_empty[kKeyGroups];  // full: the leader's, of both CTAs' copies
@@ -92,105 +83,11 @@ struct __align__(16) TreeCtl {
     uint64_t q_full, q_empty, p_full, pv_done, o_empty, all_done;
     uint32_t tmem_base;
     int abort;
-    int warp_units[kWarpsT];
-    UnitT unit[kTreeMaxRounds];
-    int cut[kTreeMaxRounds];     // the request that the range is the second one of, or -1
+    TreePlan plan;
     float part[4][kPg];          // per row and quarter of the block: maxima, at the end sums
 };
 constexpr int kSmemT = 1024 + kOffCtlT + int(sizeof(TreeCtl));
 static_assert(kSmemT <= 232448, "fits one CTA per SM");
-
-__device__ __forceinline__ bool soft_or(bool v) {  // over the 256 softmax threads
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred pi, po;\n\t"
-        "setp.ne.u32 pi, %1, 0;\n\t"
-        "bar.red.or.pred po, 1, 256, pi;\n\t"
-        "selp.u32 %0, 1, 0, po;\n\t}"
-        : "=r"(r)
-        : "r"(v ? 1u : 0u)
-        : "memory");
-    return r != 0;
-}
-
-// Rows [0, 64) of one slab of a request's drafted entries (rows behind them arrive as zeros).
-__device__ __forceinline__ void tma2_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t slab,
-                                             int32_t request, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(slab), "r"(request), "r"(bar), "l"(policy)
-        : "memory");
-}
-
-__device__ __forceinline__ void wait_landed_t(uint64_t* bar, uint32_t parity) {
-    const uint32_t a = smem_u32(bar);
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(a, parity) && global_timer_ns() - t0 < kWaitLimitNs) {
-    }
-}
-
-__device__ __forceinline__ int tree_tokens(const MlaTreeParams& p, int b) {  // cached, in [0, max_context]
-    const int seq = __ldg(p.seq_lens + b);
-    return seq < 0 ? 0 : (int64_t(seq) > p.max_context ? int(p.max_context) : seq);
-}
-__device__ __forceinline__ int tree_drafted(const MlaTreeParams& p, int b) {  // in [0, tokens]
-    if (!p.counts) return p.tokens;
-    return min(max(__ldg(p.counts + b), 0), p.tokens);
-}
-__device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1; }
-
-// The CTA pair's walk over its units: one step per request that has blocks in a unit's range and tokens
-// in its pair.
-struct TreeWalk {
-    int k, rounds, first, step;  // units first, first + step, ...
-    int b, u0, lo, hi;
-    int range, tile;
-    int np, live, drafted, nb, blo, bhi;  // current request: cache pages, entries, drafted tokens, blocks
-    __device__ __forceinline__ TreeWalk(int first_, int step_, int units)
-        : k(-1), rounds(first_ < units ? (units - first_ + step_ - 1) / step_ : 0), first(first_), step(step_), b(0),
-          u0(0), lo(0), hi(0) {}
-    __device__ __forceinline__ bool next(const MlaTreeParams& p, const TreeCtl& ctl) {
-        while (true) {
-            while (b < p.batch && u0 < hi) {
-                const int seq = tree_tokens(p, b);
-                live = (seq + 3) >> 2;
-                np = tree_cache_pages(seq);
-                drafted = tree_drafted(p, b);
-                nb = tree_blocks(np, drafted);
-                const int base = u0 + kTreeSegUnits, end = u0 + tree_units(nb);
-                blo = max(lo, base) - base;
-                bhi = min(hi, end) - base;
-                ++b;
-                u0 = end;
-                if (nb > 0 && bhi > blo && 2 * tile < drafted) return true;
-            }
-            if (++k >= rounds) return false;
-            const int u = first + k * step;
-            range = u / p.tiles;
-            tile = u - range * p.tiles;
-            lo = ctl.unit[k].lo, hi = ctl.unit[k].hi, b = ctl.unit[k].first_req, u0 = ctl.unit[k].first_start;
-        }
-    }
-    __device__ __forceinline__ int req() const { return b - 1; }
-    // Entries of a page that somebody may see, if its id is good.
-    __device__ __forceinline__ int valid(int page) const {
-        return page < np ? min(live - page * kPg, kPg) : (page == np ? drafted : 0);
-    }
-    // Has a page value rows to zero?  (The drafted page always, by the masks.)
-    __device__ __forceinline__ bool zeroes(int page) const {
-        return page == np || (page < np && ((live - page * kPg) < kPg) && ((live & 15) != 0));
-    }
-};
-
-// Ids of pages [page0, page0 + 32) of the current request, a lane each: -1 where the table's is outside the
-// cache, -2 for the drafted page and those behind it.
-__device__ __forceinline__ int tree_page_of_lane(const MlaTreeParams& p, const TreeWalk& w, int page0, int lane) {
-    const int page = page0 + lane;
-    if (page >= w.np) return -2;
-    const int id = __ldg(p.page_table + int64_t(w.req()) * p.table_width + page);
-    return (id >= 0 && int64_t(id) < p.num_pages) ? id : -1;
-}
 
 __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
     mla_tree_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
@@ -206,6 +103,12 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
     const int rank = int(cluster_rank());  // 0: the leader
     const int cluster = int(blockIdx.x) >> 1, clusters = int(gridDim.x) >> 1;
 
+    if (p.redo > 0) {  // the larger kernel's call: only if a CTA of it has given up
+        pdl_wait_prior_grid();
+        const int any = __syncthreads_or(int(threadIdx.x) < p.redo && p.flags[threadIdx.x] != 0);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *p.again = any ? 1 : 0;
+        if (!any) return;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kKeyGroups; ++i) {
             mbar_init(&ctl.k_full[i], 1);
@@ -228,10 +131,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
         mbar_init(&ctl.o_empty, 2 * kSoftWarps);
         mbar_init(&ctl.all_done, 1);
         ctl.abort = 0;
-        for (int k = 0; k < kTreeMaxRounds; ++k) {
-            ctl.unit[k] = {0, 0, p.batch, 0};
-            ctl.cut[k] = -1;
-        }
+        clear_plan(p, ctl.plan);
         fence_mbar_init();
         tma_prefetch_map(&q_map);
         tma_prefetch_map(&kv_map);
@@ -243,72 +143,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
 
-    // This pair's ranges, from the prefix sums of the requests' units.
-    const int per = (p.batch + kThreadsT - 1) / kThreadsT;
-    const int r0 = min(int(threadIdx.x) * per, p.batch), r1 = min(r0 + per, p.batch);
-    int mine = 0;
-    for (int b = r0; b < r1; ++b) {
-        if (blockIdx.x == 0) {
-            const int seq = __ldg(p.seq_lens + b);
-            if (seq < 0 || int64_t(seq) > p.max_context) atomicOr(p.err, kErrSeqLenClamped);
-            if (p.counts && tree_drafted(p, b) != __ldg(p.counts + b)) atomicOr(p.err, kErrBadRange);
-        }
-        mine += tree_units(tree_blocks(tree_cache_pages(tree_tokens(p, b)), tree_drafted(p, b)));
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) ctl.warp_units[warp] = incl;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < kWarpsT; ++w) {
-        if (w < warp) before += ctl.warp_units[w];
-        total += ctl.warp_units[w];
-    }
-    const int nranges = max(min(p.ranges, total), 1);
-    const int units = nranges * p.tiles;
-    const Ranges ranges(nranges, total);
-    if (threadIdx.x == 0)  // cuts at the very end lie in no request
-        for (int k = 0; cluster + k * clusters < units; ++k) {
-            const int range = (cluster + k * clusters) / p.tiles;
-            if (ranges.cut(range) == total) ctl.unit[k].lo = total;
-            if (ranges.cut(range + 1) == total) ctl.unit[k].hi = total;
-        }
-    {
-        int u = before + incl - mine;
-        for (int b = r0; b < r1; ++b) {
-            const int nb = tree_blocks(tree_cache_pages(tree_tokens(p, b)), tree_drafted(p, b)), n = tree_units(nb);
-            for (int k = 0; cluster + k * clusters < units; ++k) {
-                const int range = (cluster + k * clusters) / p.tiles;
-                const int lo = ranges.cut(range), hi = ranges.cut(range + 1);
-                if (lo >= u && lo < u + n) {
-                    ctl.unit[k].lo = tree_settled_cut(lo, u, nb);
-                    ctl.unit[k].first_req = b;
-                    ctl.unit[k].first_start = u;
-                }
-                if (hi >= u && hi < u + n) ctl.unit[k].hi = tree_settled_cut(hi, u, nb);
-                // Is this the request's second range?  Its first block lies in the one before.
-                if (nb > kTreeWholeBlocks && lo > u + kTreeSegUnits && lo < u + n &&
-                    ranges.cut(range - 1) <= u + kTreeSegUnits)
-                    ctl.cut[k] = b;
-            }
-            if (blockIdx.x == 0)  // the first and last range that hold its blocks, for the merge
-                p.plan[b] = nb > kTreeWholeBlocks ? make_int2(ranges.of(u + kTreeSegUnits), ranges.of(u + n - 1))
-                                                  : make_int2(0, 0);
-            u += n;
-        }
-    }
+    const int units = find_units<kThreadsT>(p, ctl.plan, cluster, clusters);
     tc_fence_before_sync();
     cluster_sync_all();  // the barriers and the plan are there, in both CTAs
     tc_fence_after_sync();
-    if (threadIdx.x == 0 && rank == 0)
-        for (int k = 0; cluster + k * clusters < p.ranges * p.tiles; ++k) {  // ranges without work too
-            const int u = cluster + k * clusters;
-            if (u % p.tiles == 0) p.cuts[u / p.tiles] = k < kTreeMaxRounds && u < units ? ctl.cut[k] : -1;
-        }
+    if (threadIdx.x == 0 && rank == 0) write_cuts(p, ctl.plan, cluster, clusters, units);
     const uint32_t tmem_base = ctl.tmem_base;
     TreeWalk w(cluster, clusters, units);
 
@@ -325,7 +164,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
             return ok;
         };
         uint32_t issued = 0;  // fills of each key group beyond the n whole blocks (bit j), for the drain
-        while (ok && w.next(p, ctl)) {
+        while (ok && w.next(p, ctl.plan)) {
             int id_l = tree_page_of_lane(p, w, 2 * w.blo, lane);
             if (id_l == -1 && 2 * w.blo + lane < 2 * w.bhi) atomicOr(p.err, kErrBadPage);
             if (!wait(&ctl.q_empty, uint32_t(seg & 1) ^ 1u)) break;
@@ -399,7 +238,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
             return ok;
         };
         uint32_t issued = 0;
-        while (ok && w.next(p, ctl)) {
+        while (ok && w.next(p, ctl.plan)) {
             int id_l = 0;
             const int blocks = uniform(w.bhi - w.blo);
 #pragma unroll 1
@@ -466,7 +305,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
         // ================= value rows that nobody sees =================
         bool ok = true;
         uint32_t phase = 0;  // bit pg
-        while (ok && w.next(p, ctl)) {
+        while (ok && w.next(p, ctl.plan)) {
             for (int page = max(w.np - 1, 0); page <= w.np && ok; ++page) {
                 if (page < 2 * w.blo || page >= 2 * w.bhi || !w.zeroes(page)) continue;
                 uint64_t used = low_bits(w.valid(page));
@@ -546,7 +385,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
                 }
                 ++nq;
             };
-            while (ok && w.next(p, ctl)) {
+            while (ok && w.next(p, ctl.plan)) {
                 if (!wait(&ctl.q_full, uint32_t(seg & 1))) break;
                 const int blocks = uniform(w.bhi - w.blo);
                 uint32_t fresh = 1, bad = 0;
@@ -623,7 +462,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
         uint8_t* const pbuf = tiles + kOffPT + pg * kSlabT + row * 128;
         bool failed = false;
         int n = 0;
-        while (!failed && w.next(p, ctl)) {
+        while (!failed && w.next(p, ctl.plan)) {
             const int token = 2 * w.tile + rank;
             const bool live_token = token < w.drafted;
             const int64_t q_row = int64_t(w.req()) * p.tokens + min(token, p.tokens - 1);
@@ -717,7 +556,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
                 for (int k = 0; k < 4; ++k)
                     *reinterpret_cast<uint4*>(pbuf + (((4 * half + k) ^ (row & 7)) << 4)) =
                         make_uint4(packed[4 * k], packed[4 * k + 1], packed[4 * k + 2], packed[4 * k + 3]);
-                asm volatile("fence.proxy.async;" ::: "memory");
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(p_bar);
                 if (w.valid(2 * blk) > 0 && !(bad_here & 1u)) fresh = false;
@@ -842,19 +681,7 @@ cudaError_t launch_mla_tree(const MlaTreeMaps& m, const MlaTreeParams& p, int pa
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tree_kernel, m.q, m.kv, m.kr, m.d, p);
     if (e != cudaSuccess) return e;
-    // No request is split where none can have more blocks than are kept together.
-    if (tree_blocks(p.table_width, 1) <= kTreeWholeBlocks) return cudaSuccess;
-    MlaMergeParams mp{};
-    mp.plan = p.plan;
-    mp.cuts = p.cuts;
-    mp.o_part = p.o_part;
-    mp.lse_part = p.lse_part;
-    mp.out = p.out;
-    mp.lse = p.lse;
-    mp.counts = p.counts;
-    mp.tokens = p.tokens;
-    mp.by_cut = p.batch > p.ranges;
-    return launch_mla_merge(mp, p.batch, p.ranges, stream);
+    return merge_tree(p, stream);
 }
 
 }  // namespace dsa

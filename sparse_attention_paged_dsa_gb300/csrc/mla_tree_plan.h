@@ -9,8 +9,9 @@ namespace dsa {
 constexpr int kTreeSegUnits = 2;     // a request's fixed cost in a range (q, first products, output), in blocks
 constexpr int kTreeWholeBlocks = 3;  // requests of at most this many blocks are not split
 constexpr int kTreeMaxRanges = 256;
-constexpr int kTreeMaxRounds = 8;    // units of a CTA pair, at most
-constexpr int kTreePlanRounds = 3;   // rounds that are tried for a full device
+constexpr int kTreeMaxFlags = 256;    // CTAs of the larger kernel
+constexpr int kTreeMaxRounds = 8;    // units of a cluster, at most
+constexpr int kTreePlanRounds = 4;   // rounds that are tried for a full device
 
 // A request's pages: the live ones of the cache and one of its drafted tokens, where it has any.
 DSA_PLAN int tree_cache_pages(int tokens) { return (((tokens + 3) >> 2) + 63) >> 6; }
@@ -24,20 +25,19 @@ DSA_PLAN int tree_settled_cut(int cut, int u, int blocks) {
     return blocks > kTreeWholeBlocks ? cut : ((cut - u) * 2 < n ? u : u + n);
 }
 
-// Pairs of drafted tokens, each a unit in every range.
-DSA_PLAN int tree_tiles(int tokens) { return (tokens + 1) / 2; }
+// Tiles of drafted tokens, each a unit in every range.
+DSA_PLAN int tree_tiles(int tokens, int tile_tokens) { return (tokens + tile_tokens - 1) / tile_tokens; }
 
-// Ranges of a call on `pairs` CTA pairs: as many as fill them in few rounds.  A round more is worth it for
+// Ranges of a call on `clusters` clusters: as many as fill them in few rounds.  A round more is worth it for
 // a twentieth of the device.
-DSA_PLAN int tree_ranges(int tokens, int pairs) {
-    const int tiles = tree_tiles(tokens);
-    int best = 1, best_rounds = 0, best_units = 0;  // units: of best_rounds * pairs places
+DSA_PLAN int tree_ranges(int tiles, int clusters) {
+    int best = 1, best_rounds = 0, best_units = 0;  // units: of best_rounds * clusters places
     for (int k = 1; k <= kTreePlanRounds; ++k) {
-        int r = k * pairs / tiles;
+        int r = k * clusters / tiles;
         if (r > kTreeMaxRanges) r = kTreeMaxRanges;
         if (r < 1) continue;
-        // r tiles / (k pairs) against best_units / (best_rounds pairs) + 1 / 20
-        if (best_rounds == 0 || 20 * (r * tiles * best_rounds - best_units * k) > k * best_rounds * pairs)
+        // r tiles / (k clusters) against best_units / (best_rounds clusters) + 1 / 20
+        if (best_rounds == 0 || 20 * (r * tiles * best_rounds - best_units * k) > k * best_rounds * clusters)
             best = r, best_rounds = k, best_units = r * tiles;
     }
     return best;

@@ -1,0 +1,786 @@
+// mla_tree_quad_kernel.cu -- the tree decode (mla_tree_kernel.cu) on clusters of four
+// CTAs and four drafted tokens, for calls whose time is products, sm_103a.
+//
+// What an SM takes in bounds the smaller kernel: 33 bytes a cycle, multicast or not
+// (measured), so a 64-row tile's 1,088 bytes an entry cost twice its multiply-adds.  Here:
+//   * rows: tokens 0 and 1 of the tile are CTAs 0 and 2's 128 rows, tokens 2 and 3 CTAs 1
+//     and 3's.  CTAs 0, 1 and CTAs 2, 3 are pairs (cta_group::2, M = 256: all four tokens);
+//   * S = Q . K^T    pair p takes page p of a block of two: N = 64, 32 entries in each CTA;
+//   * O += P . V     pair p takes value dims [256 p, 256 p + 256) of both pages: N = 256, 128
+//                    dims in each CTA.  P of its own page comes from tensor memory, P of the
+//                    other page from the CTA with the same rows in the other pair, through
+//                    distributed shared memory.
+// An entry then costs an SM 288 bytes as key, 256 as value and 128 of weights for 128 rows'
+// scores and half a row's values: 672 bytes, 20 cycles, for 17 of multiply-adds.
+//
+// No running maximum.  Both CTAs that hold a row must use one reference, and agreeing
+// on a new one block by block would cost a round trip each.  They agree once, on the
+// first block's maximum.  Weights may then pass 1 as far as fp32 and bf16 reach (their
+// rounding is relative: nothing is lost).  A CTA whose sums pass 2^58, or any of
+// whose outputs is not finite, sets its flag, and the smaller kernel, which keeps a running
+// maximum, then does the whole call again (launch_mla_tree): it leaves at once where no flag is set.
+//
+// Shared memory holds q (147 KB), eight of a block's nine key slabs, its values, and the other page's
+// weights.  Roles as in the smaller kernel (384 threads): warps 0-7 softmax, one row and 32 entries a
+// thread; warp 8 of each pair's leader MMAs; 9 and 10 TMA; 11 zeroes value rows that nobody sees.
+// Every wait is bounded (about 1 s) but the cluster barriers, which every thread reaches.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "cta_pair.cuh"
+#include "indexer_kernels.h"
+#include "mla_common.cuh"
+#include "mla_tree_common.cuh"
+#include "sm103_ptx.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kThreadsQ = 416;
+constexpr int kRowsQ = 128;                     // rows of a CTA: two tokens' heads
+constexpr int kHalfPg = kPg / 2;                // entries of a CTA's half page
+constexpr int kSlabsQ = kMlaDim / 64;           // 9
+constexpr int kSlabQ = kRowsQ * 128;            // 16 KiB
+constexpr int kSlabK = kHalfPg * 128;           // 4 KiB
+constexpr int kSlabsTm = 4;                     // of q in tensor memory, the last ones
+constexpr int kSlabsSm = kSlabsQ - kSlabsTm;    // in shared memory
+constexpr int kSlabsK = 3;                      // key slabs that are loaded together
+constexpr int kGroupK = kSlabsK * kSlabK;
+constexpr int kGroupsK = kSlabsQ / kSlabsK;     // of a block
+constexpr int kRingK = 4;                       // groups in shared memory
+constexpr int kSlabV = kPg * 128;               // values of a page: two slabs of 64 entries x 64 dims
+constexpr int kGroupQ = 2 * kSlabV;
+constexpr int kOffQq = 0;
+constexpr int kOffKq = kOffQq + kSlabsSm * kSlabQ;
+constexpr int kOffVq = kOffKq + kRingK * kGroupK;
+constexpr int kOffRq = kOffVq + 2 * kGroupQ;    // weights of the other page, 128 rows x 64 entries
+constexpr int kOffPq = kOffRq + 2 * kSlabQ;     // and of the own page; two blocks' of both
+constexpr int kOffCtlQ = kOffPq + 2 * kSlabQ;
+constexpr uint32_t kColSQ = 0;     // S: 2 x 64 columns
+constexpr uint32_t kColQQ = 128;   // q: 32 columns a slab
+constexpr uint32_t kColOQ = 256;   // O: 256 columns
+constexpr float kSumMost = 288230376151711744.0f;  // 2^58: times 2^18 entries and values below 2^50
+constexpr float kSumLeast = 8.4703294725430034e-22f;  // 2^-70, where the reference is not the row's own
+
+struct __align__(16) QuadCtl {
+    uint64_t k_full[kRingK], k_empty[kRingK];  // full: the pair's leader's, of both CTAs' copies
+    uint64_t v_full[2], v_empty[2];            // per page of a block
+    uint64_t vz_full[2], vz_ready[2];
+    uint64_t s_full[2], s_empty[2];
+    uint64_t q_full, q_empty, qt_full, o_empty, all_done;
+    uint64_t p_own[2], p_other[2], r_full[2], pv_done[2];  // of every other block
+    uint64_t m_full, l_full;                   // the other pair's row maxima, and sums, are here
+    uint32_t tmem_base;
+    int abort;
+    TreePlan plan;
+    float part[2][kRowsQ];                     // per half of the entries: maxima of the first block, then sums
+    float peer[2][kRowsQ];                     // the other pair's maxima, and sums
+};
+constexpr int kSmemQ = kOffCtlQ + int(sizeof(QuadCtl));
+static_assert(kSmemQ <= 232448, "fits one CTA per SM");
+
+// Arrive once on the barrier at this offset in the CTAs of `mask` when every MMA this thread issued has completed.
+__device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(mask)
+        : "memory");
+}
+
+// Copy to another CTA's shared memory, counted on a barrier there.
+__device__ __forceinline__ void bulk_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// 32 rows of one slab of a request's drafted entries (rows behind the last arrive as zeros).
+__device__ __forceinline__ void load_drafts(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t row, int32_t slab,
+                                            int32_t request, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(slab), "r"(request), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+__global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
+    mla_tree_quad_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                         const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap d_map,
+                         const MlaTreeParams p) {
+    extern __shared__ uint8_t smem_raw[];  // at the same offset in all CTAs; on a 1,024-byte boundary, checked below
+    uint8_t* tiles = smem_raw;
+    QuadCtl& ctl = *reinterpret_cast<QuadCtl*>(tiles + kOffCtlQ);
+    const uint32_t s_base = smem_u32(tiles);
+    const int warp = uniform(int(threadIdx.x) >> 5);
+    const int lane = threadIdx.x & 31;
+    const int rank = int(cluster_rank());
+    const int pair = rank >> 1, side = rank & 1;   // side 0: the pair's leader
+    const uint32_t leader = uint32_t(rank & 2);
+    const uint16_t both = uint16_t(3u << (rank & 2));
+    const int cluster = int(blockIdx.x) >> 2, clusters = int(gridDim.x) >> 2;
+
+    if (s_base & 1023u) {  // (the same in every CTA; shared memory has started on such a boundary on every part)
+        if (threadIdx.x == 0) p.flags[blockIdx.x] = 1;
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRingK; ++i) {
+            mbar_init(&ctl.k_full[i], 1);
+            mbar_init(&ctl.k_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.v_full[i], 1);
+            mbar_init(&ctl.v_empty[i], 1);
+            mbar_init(&ctl.vz_full[i], 1);
+            mbar_init(&ctl.vz_ready[i], 2);  // one arrival of each CTA of the pair
+            mbar_init(&ctl.s_full[i], 1);
+            mbar_init(&ctl.p_own[i], 2 * kSoftWarps);
+            mbar_init(&ctl.p_other[i], 1);   // the other CTA of the pair has its part
+            mbar_init(&ctl.r_full[i], 1);
+            mbar_init(&ctl.pv_done[i], 2);   // of both pairs
+            mbar_init(&ctl.s_empty[i], 2 * kSoftWarps);
+        }
+        mbar_init(&ctl.q_full, 1);
+        mbar_init(&ctl.q_empty, 1);
+        mbar_init(&ctl.qt_full, 2 * kSoftWarps);
+        mbar_init(&ctl.o_empty, 2 * kSoftWarps);
+        mbar_init(&ctl.all_done, 4);         // of both pairs' two issuing warps
+        mbar_init(&ctl.m_full, kSoftWarps / 2);
+        mbar_init(&ctl.l_full, kSoftWarps / 2);
+        ctl.abort = 0;
+        clear_plan(p, ctl.plan);
+        fence_mbar_init();
+        tma_prefetch_map(&q_map);
+        tma_prefetch_map(&k_map);
+        tma_prefetch_map(&v_map);
+        tma_prefetch_map(&d_map);
+    }
+    if (warp == 8) tmem2_alloc(&ctl.tmem_base, 512);
+    __syncwarp();
+    pdl_wait_prior_grid();
+    pdl_allow_next_grid();
+
+    const int units = find_units<kThreadsQ>(p, ctl.plan, cluster, clusters);
+    tc_fence_before_sync();
+    cluster_sync_all();  // the barriers and the plan are there, in all CTAs
+    tc_fence_after_sync();
+    if (threadIdx.x == 0 && rank == 0) write_cuts(p, ctl.plan, cluster, clusters, units);
+    const uint32_t tmem_base = ctl.tmem_base;
+    TreeWalk w(cluster, clusters, units);
+    bool flagged = false;
+
+    if (warp == 9) {
+        // ================= TMA: q and keys =================
+        // Whole warps run the loops on uniform values; one elected lane issues.
+        const bool issuer = elect_one();
+        const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
+        const uint32_t sb = uint32_t(uniform(int(s_base)));
+        bool ok = true;
+        int n = 0, seg = 0, slot = 0;  // key groups, requests so far; the ring's place
+        uint32_t phase = 0;
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort));
+            return ok;
+        };
+        while (ok && w.next(p, ctl.plan)) {
+            int id_l = tree_page_of_lane(p, w, 2 * w.blo, lane);
+            if (id_l == -1 && 2 * w.blo + lane < 2 * w.bhi) atomicOr(p.err, kErrBadPage);
+            if (!wait(&ctl.q_empty, uint32_t(seg & 1) ^ 1u)) break;
+            if (issuer) {
+                const uint32_t bar = cluster_addr(&ctl.q_full, leader);
+                if (side == 0) mbar_arrive_expect_tx(&ctl.q_full, uint32_t(2 * kSlabsSm * kSlabQ));
+                // (rows behind the request's tokens are others' or zeros, and are not written)
+                const int row = (w.req() * p.tokens + 4 * w.tile + 2 * side) * kMlaHeads;
+#pragma unroll
+                for (int s = 0; s < kSlabsSm; ++s) tma2_load_3d(sb + kOffQq + s * kSlabQ, &q_map, bar, 0, row, s, pol_q);
+            }
+            __syncwarp();
+            ++seg;
+            const int blocks = uniform(w.bhi - w.blo);
+#pragma unroll 1
+            for (int i = 0; i < blocks && ok; ++i) {
+                if (i > 0 && (i & 15) == 0) {
+                    id_l = tree_page_of_lane(p, w, 2 * (w.blo + i), lane);
+                    if (id_l == -1 && 2 * (w.blo + i) + lane < 2 * w.bhi) atomicOr(p.err, kErrBadPage);
+                }
+                // the pair's page; -1: page 0 stands in, its entries are not used
+                const int id = __shfl_sync(0xffffffffu, id_l, 2 * (i & 15) + pair);
+                const int row = max(id, 0) * kPg + kHalfPg * side;
+#pragma unroll 1
+                for (int j = 0; j < kGroupsK; ++j, ++n) {
+                    if (!wait(&ctl.k_empty[slot], phase ^ 1u)) break;
+                    if (issuer) {
+                        const uint32_t bar = cluster_addr(&ctl.k_full[slot], leader), dst = sb + kOffKq + slot * kGroupK;
+                        if (side == 0) mbar_arrive_expect_tx(&ctl.k_full[slot], uint32_t(2 * kGroupK));
+                        if (id == -2) {
+#pragma unroll
+                            for (int k = 0; k < kSlabsK; ++k)
+                                load_drafts(dst + k * kSlabK, &d_map, bar, kHalfPg * side, kSlabsK * j + k, w.req(), pol_kv);
+                        } else {
+                            tma2_load_3d(dst, &k_map, bar, 0, row, kSlabsK * j, pol_kv);
+                        }
+                    }
+                    __syncwarp();
+                    if (++slot == kRingK) slot = 0, phase ^= 1u;
+                }
+            }
+        }
+        if (lane == 0) {
+            if (!ok) {
+                atomicOr(p.err, kErrWaitTimeout);
+                ctl.abort = 1;
+            }
+            // No copy outlives the cluster (bounded waits; they have landed unless a role gave up).
+            if (side == 0) {
+                for (int i = max(n - kRingK, 0); i < n; ++i)
+                    wait_landed_t(&ctl.k_full[i % kRingK], uint32_t(i / kRingK) & 1u);
+                if (seg > 0) wait_landed_t(&ctl.q_full, uint32_t(seg - 1) & 1u);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 10) {
+        // ================= TMA: values =================
+        const bool issuer = elect_one();
+        const uint64_t pol_kv = l2_policy_evict_last();
+        const uint32_t sb = uint32_t(uniform(int(s_base)));
+        bool ok = true;
+        int n = 0;
+        uint32_t zero_fills[2] = {0, 0}, issued = 0;
+        const auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort));
+            return ok;
+        };
+        while (ok && w.next(p, ctl.plan)) {
+            int id_l = 0;
+            const int blocks = uniform(w.bhi - w.blo);
+#pragma unroll 1
+            for (int i = 0; i < blocks; ++i, ++n) {
+                if ((i & 15) == 0) id_l = tree_page_of_lane(p, w, 2 * (w.blo + i), lane);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {  // the pair's own page first, as its product goes
+                    const int pg = s ^ pair;
+                    const int id = __shfl_sync(0xffffffffu, id_l, 2 * (i & 15) + pg);
+                    const bool zeroes = id != -1 && w.zeroes(2 * (w.blo + i) + pg);
+                    if (!wait(&ctl.v_empty[pg], uint32_t(n & 1) ^ 1u)) break;
+                    if (issuer) {
+                        uint32_t bar = cluster_addr(&ctl.v_full[pg], leader);
+                        if (zeroes) {
+                            bar = cluster_addr(&ctl.vz_full[pg], uint32_t(rank));
+                            mbar_arrive_expect_tx(&ctl.vz_full[pg], uint32_t(kGroupQ));
+                            if (side == 0) mbar_arrive(&ctl.v_full[pg]);  // the page's phases go on
+                        } else if (side == 0) {
+                            mbar_arrive_expect_tx(&ctl.v_full[pg], uint32_t(2 * kGroupQ));
+                        }
+                        const uint32_t dst = sb + kOffVq + pg * kGroupQ;
+                        const int slab = 4 * pair + 2 * side;  // dims 256 pair + 128 side
+                        if (id == -2) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)  // 32 entries of a slab at a time
+                                load_drafts(dst + k * kSlabK, &d_map, bar, kHalfPg * (k & 1), slab + (k >> 1), w.req(),
+                                            pol_kv);
+                        } else {
+                            tma2_load_3d(dst, &v_map, bar, 0, max(id, 0) * kPg, slab, pol_kv);
+                        }
+                    }
+                    __syncwarp();
+                    issued |= 1u << pg;
+                    if (ok && zeroes) ++zero_fills[pg];
+                }
+                if (!ok) break;
+                issued = 0;
+            }
+        }
+        if (lane == 0) {
+            if (!ok) {
+                atomicOr(p.err, kErrWaitTimeout);
+                ctl.abort = 1;
+            }
+            if (side == 0)
+                for (int g = 0; g < 2; ++g) {
+                    const int fills = n + int((issued >> g) & 1u);
+                    if (fills > 0) wait_landed_t(&ctl.v_full[g], uint32_t(fills - 1) & 1u);
+                }
+            for (int pg = 0; pg < 2; ++pg)
+                if (zero_fills[pg] > 0) wait_landed_t(&ctl.vz_full[pg], (zero_fills[pg] - 1) & 1u);
+            // After a timeout the CTAs may have issued different copies, and what only another counts
+            // cannot be waited for here: a millisecond, a thousand times a copy's latency.
+            if (*const_cast<volatile int*>(&ctl.abort)) {
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000 * 1000) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 11) {
+        // ================= value rows that nobody sees =================
+        bool ok = true;
+        uint32_t phase = 0;  // bit pg
+        while (ok && w.next(p, ctl.plan)) {
+            for (int page = max(w.np - 1, 0); page <= w.np && ok; ++page) {
+                if (page < 2 * w.blo || page >= 2 * w.bhi || !w.zeroes(page)) continue;
+                uint64_t used = low_bits(w.valid(page));
+                if (page == w.np) {
+                    uint64_t any = 0;
+                    for (int j = lane; j < w.drafted; j += 32) any |= __ldg(p.mask + int64_t(w.req()) * p.tokens + j);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) any |= __shfl_xor_sync(0xffffffffu, any, o);
+                    used &= any;
+                } else if (tree_page_of_lane(p, w, page, 0) == -1) {
+                    continue;  // page 0 stands in: no product reads it
+                }
+                const int pg = page & 1;
+                ok = __all_sync(0xffffffffu, mbar_await(&ctl.vz_full[pg], (phase >> pg) & 1u, &ctl.abort)) != 0;
+                phase ^= 1u << pg;
+                if (!ok) break;
+                const int rows = (w.valid(page) + 15) & ~15;
+                for (int c = lane; c < rows * 8; c += 32) {
+                    const int r = c >> 3;
+                    if ((used >> r) & 1u) continue;
+                    uint8_t* v = tiles + kOffVq + pg * kGroupQ + r * 128 + (c & 7) * 16;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) *reinterpret_cast<uint4*>(v + s * kSlabV) = make_uint4(0, 0, 0, 0);
+                }
+                asm volatile("fence.proxy.async;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&ctl.vz_ready[pg], leader));
+            }
+        }
+        __syncwarp();
+    } else if (warp == 8 || (warp == 12 && side == 0)) {
+        // ================= MMA (the pairs' leaders'), scores =================
+        // In a warp of their own: one that issued both products was late with every one of them (4,650
+        // cycles a block, of them 2,000 in barriers that were complete).
+        if (side == 0) {
+            constexpr uint32_t kIdescQk = idesc_bf16_f32(256, 64);
+            constexpr uint32_t kIdescPv = idesc_bf16_f32(256, 256) | (1u << 16);  // B (V) MN-major
+            const uint32_t tmem = uint32_t(uniform(int(tmem_base)));
+            const uint32_t sb = uint32_t(uniform(int(s_base)));
+            const bool issuer = elect_one();
+            bool ok = true;
+            const auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort));
+                return ok;
+            };
+            int n = 0, seg = 0;  // blocks, requests so far
+            if (warp == 8) {
+                const uint64_t q_desc = smem_desc_kmajor_sw128(sb + kOffQq);
+                const uint64_t k_desc = smem_desc_kmajor_sw128(sb + kOffKq);
+                int slot = 0;
+                uint32_t phase = 0;
+                while (ok && w.next(p, ctl.plan)) {
+                    if (!wait(&ctl.q_full, uint32_t(seg & 1)) || !wait(&ctl.qt_full, uint32_t(seg & 1))) break;
+                    const int blocks = uniform(w.bhi - w.blo);
+#pragma unroll 1
+                    for (int i = 0; i < blocks && ok; ++i, ++n) {
+                        const int buf = n & 1;
+                        const uint32_t d = tmem + kColSQ + 64u * buf;
+                        wait(&ctl.s_empty[buf], (uint32_t(n >> 1) & 1u) ^ 1u);
+#pragma unroll
+                        for (int j = 0; j < kGroupsK; ++j) {
+                            wait(&ctl.k_full[slot], phase);
+                            tc_fence_after_sync();
+                            if (ok && issuer) {
+                                const uint64_t bd = refreshed(k_desc + uint32_t(slot * (kGroupK >> 4)));
+                                const uint64_t a = refreshed(q_desc + uint32_t(kSlabsK * j * (kSlabQ >> 4)));
+                                const uint32_t at = refreshed(tmem + kColQQ), dd = refreshed(d);
+#pragma unroll
+                                for (int k = 0; k < kSlabsK; ++k)
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk) {
+                                        const uint64_t b = bd + uint32_t(k * (kSlabK >> 4) + 2 * kk);
+                                        if (kSlabsK * j + k < kSlabsSm)
+                                            umma2_bf16_ss(dd, a + uint32_t(k * (kSlabQ >> 4) + 2 * kk), b, kIdescQk,
+                                                          (j | k | kk) != 0 ? 1u : 0u);
+                                        else
+                                            umma2_bf16_ts(dd, at + uint32_t(32 * (kSlabsK * j + k - kSlabsSm) + 8 * kk), b, kIdescQk, 1u);
+                                    }
+                                commit_to(&ctl.k_empty[slot], both);
+                                if (j == kGroupsK - 1) {
+                                    commit_to(&ctl.s_full[buf], both);
+                                    if (i + 1 == blocks) commit_to(&ctl.q_empty, both);
+                                }
+                            }
+                            __syncwarp();
+                            if (++slot == kRingK) slot = 0, phase ^= 1u;
+                        }
+                    }
+                    ++seg;
+                }
+            } else {
+                // ---- outputs
+                const uint64_t r_desc = smem_desc_kmajor_sw128(sb + kOffRq), p_desc = smem_desc_kmajor_sw128(sb + kOffPq);
+                const uint64_t v_desc = desc_mn_sw128(sb + kOffVq, kSlabV);
+                uint32_t zero_phase = 0;
+                while (ok && w.next(p, ctl.plan)) {
+                    const int blocks = uniform(w.bhi - w.blo);
+                    uint32_t fresh = 1, bad = 0;
+#pragma unroll 1
+                    for (int i = 0; i < blocks && ok; ++i, ++n) {
+                        if ((i & 15) == 0)
+                            bad = __ballot_sync(0xffffffffu, tree_page_of_lane(p, w, 2 * (w.blo + i), lane) == -1);
+                        const int buf = n & 1;
+                        const uint32_t phase = uint32_t(n >> 1) & 1u;
+                        if (issuer) mbar_arrive_expect_tx(&ctl.r_full[buf], uint32_t(kSlabQ));
+                        __syncwarp();
+                        if (i == 0) wait(&ctl.o_empty, uint32_t(seg & 1) ^ 1u);
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {  // the own page, then the other
+                            const int pg = s ^ pair;
+                            const int page = 2 * (w.blo + i) + pg;
+                            const bool good = !((bad >> (2 * (i & 15) + pg)) & 1u);
+                            const int steps = good ? uniform((w.valid(page) + 15) >> 4) : 0;
+                            if (good && w.zeroes(page)) {
+                                ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u,
+                                                                                     &ctl.abort));
+                                zero_phase ^= 1u << pg;
+                            }
+                            wait(&ctl.v_full[pg], uint32_t(n & 1));
+                            if (s == 0) {
+                                ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.p_own[buf], phase, &ctl.abort));  // (the other CTA's stores)
+                            } else {
+                                wait(&ctl.r_full[buf], phase);
+                                ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.p_other[buf], phase, &ctl.abort));
+                            }
+                            tc_fence_after_sync();
+                            if (ok && issuer) {
+                                const uint64_t bd = refreshed(v_desc + uint32_t(pg * (kGroupQ >> 4)));
+                                const uint32_t d = refreshed(tmem + kColOQ);
+                                const uint64_t a = refreshed((s == 0 ? p_desc : r_desc) + uint32_t(buf * (kSlabQ >> 4)));
+                                const auto step = [&](int kk) {
+                                    umma2_bf16_ss(d, a + 2u * kk, bd + uint32_t(kk * (2048 >> 4)), kIdescPv,
+                                                  (kk == 0 && fresh) ? 0u : 1u);
+                                };
+                                if (steps == 4) {
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk) step(kk);
+                                } else {
+#pragma unroll 1
+                                    for (int kk = 0; kk < steps; ++kk) step(kk);
+                                }
+                                commit_to(&ctl.v_empty[pg], both);
+                                if (s == 1) commit_to(&ctl.pv_done[buf], uint16_t(15));
+                            }
+                            __syncwarp();
+                            if (steps > 0) fresh = 0;
+                        }
+                    }
+                    ++seg;
+                }
+            }
+            if (issuer) {
+                if (!ok) {
+                    atomicOr(p.err, kErrWaitTimeout);
+                    ctl.abort = 1;
+                }
+                commit_to(&ctl.all_done, uint16_t(15));  // every MMA this thread issued has completed when this arrives
+            }
+            __syncwarp();
+        } else {
+            // ---- the other CTA's: tells the leader of the weights that have come here
+            const bool issuer = elect_one();
+            bool ok = true;
+            int n = 0;
+            while (ok && w.next(p, ctl.plan)) {
+                const int blocks = uniform(w.bhi - w.blo);
+#pragma unroll 1
+                for (int i = 0; i < blocks && ok; ++i, ++n) {
+                    if (issuer) mbar_arrive_expect_tx(&ctl.r_full[n & 1], uint32_t(kSlabQ));
+                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, mbar_await(&ctl.r_full[n & 1], uint32_t(n >> 1) & 1u, &ctl.abort)) != 0;
+                    if (ok && issuer) mbar_arrive_cluster(cluster_addr(&ctl.p_other[n & 1], leader));
+                    __syncwarp();
+                }
+            }
+        }
+    } else if (warp < kSoftWarps) {
+        // ================= softmax and output =================
+        const int quad = warp & 3, half = warp >> 2;     // entries [32 half, 32 half + 32) of the pair's page
+        const int row = quad * 32 + lane;
+        const uint32_t lane_addr = tmem_base + (uint32_t(quad * 32) << 16);
+        const uint32_t peer = uint32_t(rank ^ 2);        // the same rows, the other page and value dims
+        const uint32_t s_bar = cluster_addr(ctl.s_empty, leader), p_bar = cluster_addr(ctl.p_own, leader),
+                       o_bar = cluster_addr(&ctl.o_empty, leader), qt_bar = cluster_addr(&ctl.qt_full, leader);
+        const uint32_t r_rows = cluster_addr(tiles + kOffRq, peer) + quad * 4096, r_bar = cluster_addr(ctl.r_full, peer);
+        uint8_t* const pbuf = tiles + kOffPq + row * 128;
+        const uint32_t peer_max = cluster_addr(ctl.peer[0], peer) + 4 * row, peer_sum = cluster_addr(ctl.peer[1], peer) + 4 * row;
+        const uint32_t m_bar = cluster_addr(&ctl.m_full, peer), l_bar = cluster_addr(&ctl.l_full, peer);
+        const float c2 = p.sm_scale_log2;
+        bool failed = false;
+        int n = 0, seg = 0;
+        while (!failed && w.next(p, ctl.plan)) {
+            const int token = 4 * w.tile + 2 * side + (row >> 6);
+            const bool live_token = token < w.drafted;
+            const int64_t q_row = int64_t(w.req()) * p.tokens + min(token, p.tokens - 1);
+            const uint64_t drafts = __ldg(p.mask + q_row) & low_bits(w.drafted);
+            // The last slabs of q, once the products of the request before have read them: 128 dims a thread.
+            bool ok = mbar_await(&ctl.q_empty, uint32_t(seg & 1) ^ 1u, &ctl.abort);
+            if (!__all_sync(0xffffffffu, ok)) {
+                failed = true;  // (met by all warps at the next barrier)
+                if (lane == 0) ctl.abort = 1;
+            }
+            {
+                const uint4* q = reinterpret_cast<const uint4*>(p.q + (q_row * kMlaHeads + (row & 63)) * kMlaDim +
+                                                                64 * kSlabsSm + 32 * kSlabsTm * half);
+                tc_fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < kSlabsTm; ++c) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 v = __ldg(q + 4 * c + k);
+                        r[4 * k] = v.x, r[4 * k + 1] = v.y, r[4 * k + 2] = v.z, r[4 * k + 3] = v.w;
+                    }
+                    tmem_st_x16(lane_addr + kColQQ + 16u * kSlabsTm * half + 16u * c, r);
+                }
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(qt_bar);
+            }
+            float m = 0.f, l = 0.f;
+            bool own = true;    // the reference is a score of the row's
+            uint32_t any = 0;   // entries seen
+            bool fresh = true;  // no product of this request yet: O holds nothing of it
+            uint32_t bad = 0;
+#pragma unroll 1
+            for (int blk = w.blo; blk < w.bhi; ++blk, ++n) {
+                if (((blk - w.blo) & 15) == 0)
+                    bad = __ballot_sync(0xffffffffu, tree_page_of_lane(p, w, 2 * blk, lane) == -1);
+                const uint32_t bad_here = bad >> (2 * ((blk - w.blo) & 15));
+                const int page = 2 * blk + pair;
+                uint64_t seen = page == w.np ? drafts : low_bits(w.valid(page));
+                if ((bad_here >> pair) & 1u) seen = 0;
+                const uint32_t bits = uint32_t(seen >> (32 * half));
+                any |= bits;
+                const int buf = n & 1;
+                ok = __all_sync(0xffffffffu, mbar_await(&ctl.s_full[buf], uint32_t(n >> 1) & 1u, &ctl.abort)) != 0;
+                float x[32];
+                {
+                    uint32_t r[32];
+                    tc_fence_after_sync();
+                    tmem_ld_32x32b_x32(lane_addr + kColSQ + 64u * buf + 32u * half, r);
+                    tmem_ld_wait(r);
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(s_bar + 8u * buf);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+                }
+                if (blk == w.blo) {  // the reference: the block's maximum, of both pages
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if ((bits >> i) & 1u) mx = fmaxf(mx, x[i] * c2);
+                    ctl.part[half][row] = mx;
+                    soft_or(false);
+                    mx = fmaxf(ctl.part[0][row], ctl.part[1][row]);
+                    if (half == 0) {
+                        st_cluster_f32(peer_max, mx);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(m_bar);
+                    }
+                    ok = ok && mbar_wait_cluster(&ctl.m_full, uint32_t(seg & 1), &ctl.abort);
+                    if (soft_or(!ok)) {
+                        failed = true;
+                        break;
+                    }
+                    m = fmaxf(mx, *const_cast<volatile float*>(&ctl.peer[0][row]));
+                    own = m != -INFINITY;
+                    if (!own) m = 0.f;
+                }
+                uint32_t packed[16];
+                float2 sum = make_float2(0.f, 0.f);
+                const float2 c22 = make_float2(c2, c2), m2 = make_float2(-m, -m);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 y = fma_f32x2(make_float2(x[2 * i], x[2 * i + 1]), c22, m2);
+                    x[2 * i] = y.x, x[2 * i + 1] = y.y;
+                }
+                if (__any_sync(0xffffffffu, bits != 0xffffffffu)) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!((bits >> i) & 1u)) x[i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float p0 = ex2_approx(x[2 * i]), p1 = ex2_approx(x[2 * i + 1]);
+                    sum = add_f32x2(sum, make_float2(p0, p1));
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
+                    packed[i] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+                l += sum.x + sum.y;
+                // The products of the block before the last, of both pairs, have read their weights.
+                if (!__all_sync(0xffffffffu, ok && mbar_await(&ctl.pv_done[buf], (uint32_t(n >> 1) & 1u) ^ 1u, &ctl.abort))) {
+                    failed = true;  // (the others' waits end the same way; the barriers are met by all)
+                    if (lane == 0) ctl.abort = 1;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    *reinterpret_cast<uint4*>(pbuf + buf * kSlabQ + (((4 * half + k) ^ (row & 7)) << 4)) =
+                        make_uint4(packed[4 * k], packed[4 * k + 1], packed[4 * k + 2], packed[4 * k + 3]);
+                fence_proxy_async_smem();
+                // both halves of these 32 rows are there
+                asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
+                if (lane == 0) {
+                    if (half == 0)
+                        bulk_to_cta(r_rows + buf * kSlabQ, s_base + kOffPq + buf * kSlabQ + quad * 4096, 4096u, r_bar + 8u * buf);
+                    mbar_arrive_cluster(p_bar + 8u * buf);
+                }
+                if (w.valid(2 * blk) > 0 && !(bad_here & 1u)) fresh = false;
+                if (w.valid(2 * blk + 1) > 0 && !(bad_here & 2u)) fresh = false;
+            }
+            // ---- the request's output (or partial)
+            bool done = !failed && mbar_await(&ctl.pv_done[(n - 1) & 1], uint32_t((n - 1) >> 1) & 1u, &ctl.abort);
+            ctl.part[half][row] = l;
+            if (soft_or(!done)) {
+                failed = true;
+                break;
+            }
+            tc_fence_after_sync();
+            float sum = ctl.part[0][row] + ctl.part[1][row];
+            if (half == 0) {
+                st_cluster_f32(peer_sum, sum);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(l_bar);
+            }
+            done = mbar_wait_cluster(&ctl.l_full, uint32_t(seg & 1), &ctl.abort);
+            if (soft_or(!done)) {  // (and the sums are read)
+                failed = true;
+                break;
+            }
+            ++seg;
+            {   // in one order, so that both pairs have the same sum
+                const float other = *const_cast<volatile float*>(&ctl.peer[1][row]);
+                sum = pair == 0 ? sum + other : other + sum;
+            }
+            if (live_token && (!(sum <= kSumMost) || (!own && any != 0 && !(sum >= kSumLeast)))) flagged = true;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const bool whole = w.blo == 0 && w.bhi == w.nb;
+            const int64_t at = whole ? q_row : (int64_t(w.range) * p.tokens + token) * 2 + (w.blo == 0 ? 1 : 0);
+            const int head = row & 63;
+            if (live_token && pair == 0 && half == 0)
+                (whole ? p.lse : p.lse_part)[at * kMlaHeads + head] =
+                    sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2T;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                if (fresh) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0u;
+                } else {
+                    tmem_ld_32x32b_x32(lane_addr + kColOQ + 128u * half + 32u * c, o);
+                    tmem_ld_wait(o);
+                }
+                if (c == 3) {
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(o_bar);  // O may be overwritten
+                }
+                if (!live_token) continue;
+                const int64_t d = (at * kMlaHeads + head) * kMlaDv + 256 * pair + 128 * half + 32 * c;
+                bool finite = true;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float v = __uint_as_float(o[i]) * inv;
+                    finite = finite && fabsf(v) <= 3.3e38f;
+                    o[i] = __float_as_uint(v);
+                }
+                if (!finite) flagged = true;
+                if (whole) {
+                    uint4* out = reinterpret_cast<uint4*>(p.out + d);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]),
+                                                                            __uint_as_float(o[8 * k + 2 * e + 1]));
+                            v[e] = *reinterpret_cast<const uint32_t*>(&b2);
+                        }
+                        out[k] = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                } else {
+                    uint4* out = reinterpret_cast<uint4*>(p.o_part + d);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) out[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+            }
+        }
+        if (failed && lane == 0) {
+            atomicOr(p.err, kErrWaitTimeout);
+            ctl.abort = 1;
+        }
+        __syncwarp();
+    }
+
+    __syncwarp();
+    tc_fence_before_sync();
+    flagged = __syncthreads_or(flagged) != 0;
+    if (threadIdx.x == 0) p.flags[blockIdx.x] = flagged ? 1 : 0;
+    cluster_sync_all();  // no CTA leaves while another may read its memory or arrive on its barriers
+    tc_fence_after_sync();
+    if (warp == 8) {
+        wait_landed_t(&ctl.all_done, 0);  // the leaders' last arrivals here
+        __syncwarp();
+        tmem2_dealloc(tmem_base, 512);
+    }
+}
+
+}  // namespace
+
+cudaError_t mla_tree_quads(int* quads) {
+    static SmemLimitOnce smem_limit;
+    static std::atomic<int> resident[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    e = smem_limit.apply(dev, mla_tree_quad_kernel, kSmemQ);
+    if (e != cudaSuccess) return e;
+    *quads = resident[dev].load(std::memory_order_relaxed);
+    if (*quads > 0) return cudaSuccess;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 4;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(4);
+    cfg.blockDim = dim3(kThreadsQ);
+    cfg.dynamicSmemBytes = size_t(kSmemQ);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(quads, mla_tree_quad_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (*quads < 1) return cudaErrorInvalidConfiguration;
+    if (*quads > kTreeMaxFlags / 4) *quads = kTreeMaxFlags / 4;
+    resident[dev].store(*quads, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+cudaError_t launch_mla_tree_quad(const MlaTreeMaps& m, const MlaTreeParams& p, int quads, cudaStream_t stream) {
+    const int units = p.ranges * p.tiles;
+    if (p.ranges < 1 || p.ranges > kTreeMaxRanges || units > kTreeMaxRounds * quads) return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(4u * unsigned(units < quads ? units : quads));
+    cfg.blockDim = dim3(kThreadsQ);
+    cfg.dynamicSmemBytes = size_t(kSmemQ);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tree_quad_kernel, m.q, m.kr, m.kv, m.d, p);
+    return e == cudaSuccess ? merge_tree(p, stream) : e;
+}
+
+}  // namespace dsa
