@@ -369,24 +369,20 @@ size_t dense_workspace_bytes(int groups, int32_t next_n) {
 
 constexpr int kTicketWord = 32;  // of the workspace header: the page update's, 0 between calls
 
-// Tree decode: header, cuts, plan, flags, then two partial outputs per range and token.
-constexpr size_t kTreeFlagBytes = size_t(dsa::kTreeMaxFlags + 64) * sizeof(uint32_t);
-constexpr size_t kTreePlanBytes =
-    size_t(dsa::kTreeMaxRanges) * sizeof(int32_t) + size_t(DSA_MAX_BATCH) * sizeof(int2) + kTreeFlagBytes;
+// Tree decode: header, cuts, plan, flags, then two partial outputs per range and token.  Two kernels share it
+// (the second one works where the first has not, or again): their plans lie apart, their partials do not.
 struct TreeShape {
-    int pairs, quads;                                     // clusters of two and of four CTAs that fit the device
-    int pair_tiles, pair_ranges, quad_tiles, quad_ranges;
-    TreeShape(int32_t tokens, int pairs_, int quads_) : pairs(pairs_), quads(quads_) {
-        pair_tiles = dsa::tree_tiles(tokens, 2), pair_ranges = dsa::tree_ranges(pair_tiles, pairs);
-        quad_tiles = dsa::tree_tiles(tokens, 4), quad_ranges = dsa::tree_ranges(quad_tiles, quads);
+    int groups, quads, tiles, ranges;  // of the dense kernel; of the kernel on clusters of four CTAs
+    TreeShape(int32_t tokens, int sms, int quads_) : groups(dense_groups(sms, tokens)), quads(quads_) {
+        tiles = dsa::tree_tiles(tokens), ranges = dsa::tree_ranges(tiles, quads);
     }
-    size_t parts(int32_t tokens) const {
-        return size_t(pair_ranges > quad_ranges ? pair_ranges : quad_ranges) * size_t(tokens) * 2;
-    }
+    size_t parts(int32_t tokens) const { return dense_parts(groups > ranges ? groups : ranges, tokens); }
     size_t workspace_bytes(int32_t tokens) const {
         return dsa::kWorkspaceHeaderBytes + kTreePlanBytes +
                parts(tokens) * dsa::kMlaHeads * (dsa::kMlaDv + 1) * sizeof(float);
     }
+    static constexpr size_t kTreePlanBytes =
+        kDensePlanBytes + size_t(dsa::kTreeMaxFlags + 64) * sizeof(uint32_t);
 };
 
 dsa_status_t run_rmsnorm(dsa::RmsNormParams p, void* stream) {
@@ -897,11 +893,11 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
 }
 
 size_t dsa_mla_tree_decode_workspace_size(int32_t batch, int32_t tokens) {
-    int pairs = 0, quads = 0;
+    int sms = 0, quads = 0;
     if (batch < 1 || batch > DSA_MAX_BATCH || tokens < 1 || tokens > DSA_MAX_TREE_TOKENS) return 0;
-    if (dsa::mla_tree_pairs(&pairs) != cudaSuccess || dsa::mla_tree_quads(&quads) != cudaSuccess)
-        pairs = 80, quads = 40;  // no device: what a large part needs
-    return TreeShape(tokens, pairs, quads).workspace_bytes(tokens);
+    if (sm_count(&sms) != cudaSuccess || dsa::mla_tree_quads(&quads) != cudaSuccess)
+        sms = 160, quads = 40;  // no device: what a large part needs
+    return TreeShape(tokens, sms, quads).workspace_bytes(tokens);
 }
 
 dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t num_pages, const int32_t* page_table,
@@ -924,29 +920,27 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
     if (num_pages > (int64_t(1) << 31) / dsa::kPageEntries - 1) return DSA_ERR_UNSUPPORTED;
     st = check_workspace(workspace, workspace_bytes, dsa::kWorkspaceHeaderBytes);
     if (st != DSA_OK) return st;
-    int pairs = 0, quads = 0;
-    cudaError_t e = dsa::mla_tree_pairs(&pairs);
+    int sms = 0, quads = 0;
+    cudaError_t e = sm_count(&sms);
     if (e == cudaSuccess) e = dsa::mla_tree_quads(&quads);
     if (e != cudaSuccess) return cuda_fail(e, "device query");
-    const TreeShape shape(tokens, pairs, quads);
-    if (shape.pair_ranges * shape.pair_tiles > dsa::kTreeMaxRounds * pairs) return DSA_ERR_UNSUPPORTED;  // few SMs
+    const TreeShape shape(tokens, sms, quads);
     st = check_workspace(workspace, workspace_bytes, shape.workspace_bytes(tokens));
     if (st != DSA_OK) return st;
-    const bool quad = tokens > 2 && max_context > 4096 && shape.quad_ranges * shape.quad_tiles <= dsa::kTreeMaxRounds * quads;
-    dsa::MlaTreeParams p{};
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint8_t* ws = static_cast<uint8_t*>(workspace) + dsa::kWorkspaceHeaderBytes;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int64_t q_rows = int64_t(batch) * tokens * DSA_MLA_HEADS, kv_rows = num_pages * dsa::kPageEntries;
+    dsa::MlaDenseParams p{};
     p.page_table = page_table;
     p.seq_lens = seq_lens;
-    p.q = static_cast<const __nv_bfloat16_raw*>(q);
-    p.mask = tree_mask;
-    p.counts = token_counts_opt;
     p.out = static_cast<__nv_bfloat16_raw*>(out);
     p.lse = lse;
-    p.cuts = reinterpret_cast<int32_t*>(ws + dsa::kWorkspaceHeaderBytes);
-    p.plan = reinterpret_cast<int2*>(p.cuts + dsa::kTreeMaxRanges);
-    p.flags = reinterpret_cast<uint32_t*>(p.plan + DSA_MAX_BATCH);
-    p.again = p.flags + dsa::kTreeMaxFlags;
-    p.o_part = reinterpret_cast<float*>(ws + dsa::kWorkspaceHeaderBytes + kTreePlanBytes);
+    p.cuts = reinterpret_cast<int32_t*>(ws);
+    p.plan = reinterpret_cast<int2*>(ws + kDenseCutBytes);
+    uint32_t* flags = reinterpret_cast<uint32_t*>(ws + kDensePlanBytes);
+    p.flags = flags;
+    p.again = flags + dsa::kTreeMaxFlags;
+    p.o_part = reinterpret_cast<float*>(ws + TreeShape::kTreePlanBytes);
     p.lse_part = p.o_part + shape.parts(tokens) * dsa::kMlaHeads * dsa::kMlaDv;
     p.err = static_cast<uint32_t*>(workspace);
     p.num_pages = num_pages;
@@ -954,32 +948,52 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
     p.table_width = int32_t(max_context / DSA_PAGE_TOKENS);
     p.batch = batch;
     p.tokens = tokens;
+    p.groups = shape.groups;
+    p.merge_by_cut = batch > shape.groups ? 1 : 0;
     p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
-    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    dsa::MlaTreeMaps m;
-    const int64_t q_rows = int64_t(batch) * tokens * DSA_MLA_HEADS, kv_rows = num_pages * dsa::kPageEntries;
-    if (quad) {
-        p.tile_tokens = 4;
-        p.tiles = shape.quad_tiles;
-        p.ranges = shape.quad_ranges;
+    p.mask = tree_mask;
+    p.counts = token_counts_opt;
+    if (tokens > 2 && max_context > 2048 && shape.ranges * shape.tiles <= dsa::kTreeMaxRounds * quads) {
+        dsa::MlaTreeParams t{};
+        t.q = static_cast<const __nv_bfloat16_raw*>(q);
+        t.page_table = page_table;
+        t.seq_lens = seq_lens;
+        t.mask = tree_mask;
+        t.counts = token_counts_opt;
+        t.out = p.out;
+        t.lse = lse;
+        t.plan = p.plan;
+        t.cuts = p.cuts;
+        t.o_part = p.o_part;
+        t.lse_part = p.lse_part;
+        t.err = p.err;
+        t.flags = flags;
+        t.num_pages = num_pages;
+        t.max_context = max_context;
+        t.table_width = p.table_width;
+        t.batch = batch;
+        t.tokens = tokens;
+        t.tiles = shape.tiles;
+        t.ranges = shape.ranges;
+        t.sm_scale_log2 = p.sm_scale_log2;
+        dsa::MlaTreeMaps m;
         st = make_slabs_map(&m.q, q, q_rows, 1, "mla q", 128);
-        if (st == DSA_OK) st = make_slabs_map(&m.kv, kv_cache, kv_rows, 2, "mla kv");
-        if (st == DSA_OK) st = make_slabs_map(&m.kr, kv_cache, kv_rows, 3, "mla kv", 32);
+        if (st == DSA_OK) st = make_slabs_map(&m.k, kv_cache, kv_rows, 3, "mla kv", 32);
+        if (st == DSA_OK) st = make_slabs_map(&m.v, kv_cache, kv_rows, 2, "mla kv");
         if (st == DSA_OK) st = make_drafts_map(&m.d, draft_kv, batch, tokens, 32);
         if (st != DSA_OK) return st;
-        e = dsa::launch_mla_tree_quad(m, p, quads, cs);
+        e = dsa::launch_mla_tree(m, t, quads, cs);
         if (e != cudaSuccess) return cuda_fail(e, "MLA tree decode launch");
-        p.redo = 4 * (p.ranges * p.tiles < quads ? p.ranges * p.tiles : quads);
+        p.redo = dsa::mla_tree_ctas(t, quads);
     }
-    p.tile_tokens = 2;
-    p.tiles = shape.pair_tiles;
-    p.ranges = shape.pair_ranges;
-    st = make_slabs_map(&m.q, q, q_rows, 3, "mla q");
-    if (st == DSA_OK) st = make_slabs_map(&m.kv, kv_cache, kv_rows, 2, "mla kv");
-    if (st == DSA_OK) st = make_rows_map(&m.kr, kv_cache, kv_rows, DSA_MLA_DIM, 64, "mla kv");
-    if (st == DSA_OK) st = make_drafts_map(&m.d, draft_kv, batch, tokens, 64);
+    CUtensorMap q_map, kv_map, kr_map, o_map, d_map;
+    st = make_slabs_map(&q_map, q, q_rows, 3, "mla q");
+    if (st == DSA_OK) st = make_slabs_map(&kv_map, kv_cache, kv_rows, 2, "mla kv");
+    if (st == DSA_OK) st = make_rows_map(&kr_map, kv_cache, kv_rows, DSA_MLA_DIM, 64, "mla kv");
+    if (st == DSA_OK) st = make_rows_map(&o_map, out, q_rows, DSA_MLA_DV, 64, "mla out");
+    if (st == DSA_OK) st = make_drafts_map(&d_map, draft_kv, batch, tokens, 64);
     if (st != DSA_OK) return st;
-    e = dsa::launch_mla_tree(m, p, pairs, cs);
+    e = dsa::launch_mla_dense_tree(q_map, kv_map, kr_map, o_map, d_map, p, cs);
     return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA tree decode launch");
 }
 

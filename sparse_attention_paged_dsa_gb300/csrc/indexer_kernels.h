@@ -159,6 +159,12 @@ struct MlaDenseParams {
     int32_t groups;            // ranges: SMs / tokens
     int32_t merge_by_cut;      // the merge goes by cuts (there are fewer ranges than requests)
     float sm_scale_log2;       // sm_scale * log2(e)
+    // of a tree of drafted tokens:
+    const uint64_t* mask;      // [batch, tokens] bit i: the token sees drafted entry i
+    const int32_t* counts;     // [batch] drafted tokens, or null: all `tokens`
+    const uint32_t* flags;     // of another kernel's CTAs, which has done the call: its outputs are not to be used
+    uint32_t* again;           // was the call done again?
+    int32_t redo;              // flags to look at: leave if none is set; 0: the call is this kernel's own
 };
 // q_map and kv_map: 576-wide bf16 rows (q: batch * tokens * 64 of them; the cache: num_pages * 64) as
 // (dim in slab, row, slab of 64 dims), boxes of 64 rows x 3 slabs and 64 rows x 2 slabs; kr_map: the
@@ -166,6 +172,12 @@ struct MlaDenseParams {
 // 64 x 64.  All 128-byte-swizzled.
 cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& kr_map,
                              const CUtensorMap& o_map, const MlaDenseParams& p, cudaStream_t stream);
+
+// The same for a tree of drafted tokens (1-64 per request), each of which sees all of the cache and the drafted
+// entries of its mask.  d_map: the drafted entries as (dim in slab, token, slab, request), boxes of 64 tokens x 1 slab.
+cudaError_t launch_mla_dense_tree(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& kr_map,
+                                  const CUtensorMap& o_map, const CUtensorMap& d_map, const MlaDenseParams& p,
+                                  cudaStream_t stream);
 
 // The log-sum-exp merge of requests that cross ranges (of the dense and the tree decode).
 struct MlaMergeParams {
@@ -182,7 +194,7 @@ struct MlaMergeParams {
 };
 cudaError_t launch_mla_merge(const MlaMergeParams& p, int batch, int ranges, cudaStream_t stream);
 
-// Latent attention decode for a tree of drafted tokens, 1-64 of them per request.
+// Latent attention decode for a tree of drafted tokens, on clusters of four CTAs.
 struct MlaTreeParams {
     const __nv_bfloat16_raw* q; // [batch, tokens, 64, 576]
     const int32_t* page_table; // [batch, table_width]
@@ -191,35 +203,29 @@ struct MlaTreeParams {
     const int32_t* counts;     // [batch] drafted tokens, or null: all `tokens`
     __nv_bfloat16_raw* out;    // [batch, tokens, 64, 512]
     float* lse;                // [batch, tokens, 64]
-    int2* plan;                // as for the merge
+    int2* plan;                // these four as for the merge
     int32_t* cuts;
     float* o_part;
     float* lse_part;
     uint32_t* err;             // device error word
+    uint32_t* flags;           // [kTreeMaxFlags] a CTA each: its outputs are not to be used
     int64_t num_pages;
     int64_t max_context;
     int32_t table_width;
     int32_t batch;
     int32_t tokens;
-    int32_t tile_tokens;       // tokens of a tile: 2, a cluster of two CTAs; 4, one of four
-    int32_t tiles;
+    int32_t tiles;             // tree_tiles: of four tokens
     int32_t ranges;            // tree_ranges
-    uint32_t* flags;           // [kTreeMaxFlags] of the larger kernel's CTAs: its outputs are not to be used
-    uint32_t* again;           // did the smaller kernel do the call again?
-    int32_t redo;              // (smaller kernel) flags to look at: leave if none is set; 0: the call is its own
     float sm_scale_log2;       // sm_scale * log2(e)
 };
-// 576-wide bf16 rows as (dim in slab, row, slab), the drafted entries as (dim in slab, token, slab, request), all
-// 128-byte-swizzled.  Boxes of the smaller kernel: q 64 rows x 3 slabs, kv 64 x 2, d 64 x 1, kr 64 x 64 of the
-// cache's rows as (dim, row); of the larger: q 128 x 1, kv 64 x 2, kr 32 x 3, d 32 x 1.
+// 576-wide bf16 rows as (dim in slab, row, slab), boxes of rows x slabs: q 128 x 1; the cache's, k 32 x 3, v 64 x
+// 2; the drafted entries as (dim in slab, token, slab, request), d 32 tokens x 1.  All 128-byte-swizzled.
 struct MlaTreeMaps {
-    CUtensorMap q, kv, kr, d;
+    CUtensorMap q, k, v, d;
 };
-cudaError_t mla_tree_pairs(int* pairs);  // clusters that the current device holds
-cudaError_t mla_tree_quads(int* quads);
-// Each with its merge.
-cudaError_t launch_mla_tree(const MlaTreeMaps& m, const MlaTreeParams& p, int pairs, cudaStream_t stream);
-cudaError_t launch_mla_tree_quad(const MlaTreeMaps& m, const MlaTreeParams& p, int quads, cudaStream_t stream);
+cudaError_t mla_tree_quads(int* quads);                    // clusters that the current device holds
+int mla_tree_ctas(const MlaTreeParams& p, int quads);      // CTAs of a call
+cudaError_t launch_mla_tree(const MlaTreeMaps& m, const MlaTreeParams& p, int quads, cudaStream_t stream);
 
 // Latent attention over ragged prompts, expanded form: per-head 128 + 64 shared key dims, 128 value dims.
 constexpr int kPrefillQk = 192;

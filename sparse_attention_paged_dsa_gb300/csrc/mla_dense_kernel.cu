@@ -179,6 +179,17 @@ __device__ __forceinline__ void tma_load_slabs(uint32_t dst, const CUtensorMap* 
         : "memory");
 }
 
+// 64 rows of one slab of a request's drafted entries (rows behind the last arrive as zeros).
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t slab,
+                                            int32_t request, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(slab), "r"(request), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1; }
+
 // Bounded wait for a phase of `bar`, whatever the other roles do.
 __device__ __forceinline__ void wait_landed(uint64_t* bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
@@ -192,51 +203,77 @@ __device__ __forceinline__ int seq_tokens(const MlaDenseParams& p, int b) {
     const int seq = __ldg(p.seq_lens + b);
     return seq < 0 ? 0 : (int64_t(seq) > p.max_context ? int(p.max_context) : seq);
 }
-__device__ __forceinline__ int blocks_of(int seq) { return (((seq + 3) >> 2) + kBlk - 1) / kBlk; }
+__device__ __forceinline__ int cache_blocks(int seq) { return (((seq + 3) >> 2) + kBlk - 1) / kBlk; }
+// A tree's tokens of a request, held to [0, tokens].
+__device__ __forceinline__ int drafted_tokens(const MlaDenseParams& p, int b) {
+    return p.counts ? min(max(__ldg(p.counts + b), 0), p.tokens) : p.tokens;
+}
+// A request's blocks: its pages, and of a tree (if it has any tokens) one of their own entries behind them.
+template <bool kTree>
+__device__ __forceinline__ int blocks_of(const MlaDenseParams& p, int b) {
+    const int nb = cache_blocks(seq_tokens(p, b));
+    if constexpr (kTree) return drafted_tokens(p, b) > 0 ? nb + 1 : 0;
+    return nb;
+}
 
 // The CTA's walk over its range: one step per request that has blocks in it.
+template <bool kTree>
 struct Walk {
     int b, u0, lo, hi, batch;  // request b starts at unit u0; range [lo, hi)
     int seq, nb, blo, bhi;     // current request: tokens, blocks, and this range's blocks [blo, bhi)
+    int token, drafted;        // of a tree: this CTA's, and the request's tokens
     __device__ __forceinline__ Walk(const DenseCtl& ctl, const MlaDenseParams& p)
-        : b(ctl.first_req), u0(ctl.first_start), lo(ctl.lo), hi(ctl.hi), batch(p.batch) {}
+        : b(ctl.first_req), u0(ctl.first_start), lo(ctl.lo), hi(ctl.hi), batch(p.batch), token(blockIdx.x) {}
     __device__ __forceinline__ bool next(const MlaDenseParams& p) {
         while (b < batch && u0 < hi) {
             seq = seq_tokens(p, b);
-            nb = blocks_of(seq);
+            nb = blocks_of<kTree>(p, b);
+            drafted = kTree ? drafted_tokens(p, b) : 0;
             const int base = u0 + kMlaSegUnits, end = u0 + units_of(nb);
             blo = max(lo, base) - base;
             bhi = min(hi, end) - base;
             ++b;
             u0 = end;
-            if (nb > 0 && bhi > blo) return true;
+            if (nb > 0 && bhi > blo && (!kTree || token < drafted)) return true;
         }
         return false;
     }
     __device__ __forceinline__ int req() const { return b - 1; }
     // Nothing follows the current request (false if the range ends in units without blocks).
     __device__ __forceinline__ bool last() const { return b >= batch || u0 >= hi; }
-    // Entries of block `blk` that token `back` from the end sees.
+    // The block of a tree's own entries.
+    __device__ __forceinline__ bool own(int blk) const { return kTree && blk == nb - 1; }
+    // Entries of block `blk` that token `back` from the end sees (of a tree's own block: that some token may).
     __device__ __forceinline__ int valid(int blk, int back) const {
+        if (own(blk)) return drafted;
         const int n = (max(seq - back, 0) + 3) >> 2;
         return min(max(n - blk * kBlk, 0), kBlk);
     }
 };
 
 // The pages of blocks [blk0, blk0 + 32) of the current request: lane's page id, -1 when outside
-// the cache or past the range.
-__device__ __forceinline__ int page_of_lane(const MlaDenseParams& p, const Walk& w, int blk0, int lane) {
+// the cache or past the range, -2 of a tree's own block.
+template <bool kTree>
+__device__ __forceinline__ int page_of_lane(const MlaDenseParams& p, const Walk<kTree>& w, int blk0, int lane) {
     const int blk = blk0 + lane;
     if (blk >= w.bhi) return -1;
+    if (w.own(blk)) return -2;
     const int page = __ldg(p.page_table + int64_t(w.req()) * p.table_width + blk);
     return (page >= 0 && int64_t(page) < p.num_pages) ? page : -1;
 }
 
+template <bool kTree>
 __global__ void __launch_bounds__(kThreadsD, 1)
     mla_dense_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
                      const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap o_map,
-                     const MlaDenseParams p) {
+                     const __grid_constant__ CUtensorMap d_map, const MlaDenseParams p) {
     extern __shared__ uint8_t smem_raw[];
+    if (kTree && p.redo > 0) {  // the call of another kernel: only if a CTA of it has given up
+        pdl_wait_prior_grid();
+        const int any = __syncthreads_or(int(threadIdx.x) < p.redo && p.flags[threadIdx.x] != 0);
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.again = any ? 1 : 0;
+        if (!any) return;
+    }
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     DenseCtl& ctl = *reinterpret_cast<DenseCtl*>(tiles + kOffCtl);
     const uint32_t s_base = smem_u32(tiles);
@@ -245,7 +282,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     const int lane = threadIdx.x & 31;
     const int token = blockIdx.x;  // of the group
     const int group = blockIdx.y;
-    const int back = p.tokens - 1 - token;
+    const int back = kTree ? 0 : p.tokens - 1 - token;  // (a tree's tokens are not in the cache)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kVRing; ++i) {
@@ -274,6 +311,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         tma_prefetch_map(&q_map);
         tma_prefetch_map(&kv_map);
         tma_prefetch_map(&kr_map);
+        if (kTree) tma_prefetch_map(&d_map);
     }
     if (warp == 1) {
         tmem_alloc(&ctl.tmem_base, kTmemColsD);
@@ -289,7 +327,9 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     for (int b = r0; b < r1; ++b) {
         const int seq = __ldg(p.seq_lens + b);
         if ((seq < 0 || int64_t(seq) > p.max_context) && group == 0 && token == 0) atomicOr(p.err, kErrSeqLenClamped);
-        mine += units_of(blocks_of(seq_tokens(p, b)));
+        if (kTree && p.counts && __ldg(p.counts + b) != drafted_tokens(p, b) && group == 0 && token == 0)
+            atomicOr(p.err, kErrBadRange);
+        mine += units_of(blocks_of<kTree>(p, b));
     }
     int incl = mine;
 #pragma unroll
@@ -317,7 +357,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     {
         int u = before + incl - mine;
         for (int b = r0; b < r1; ++b) {
-            const int nb = blocks_of(seq_tokens(p, b)), n = units_of(nb);
+            const int nb = blocks_of<kTree>(p, b), n = units_of(nb);
             if (lo >= u && lo < u + n) {
                 ctl.lo = settled_cut(lo, u, nb);
                 ctl.first_req = b;
@@ -340,7 +380,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     if (warp == 0) {
         // ================= TMA =================
         // The whole warp runs the loop on uniform values; one elected lane issues.
-        Walk w(ctl, p);
+        Walk<kTree> w(ctl, p);
         bool stop = false;
         int n = 0, seg = 0;                         // blocks and requests so far
         int last_v = -1, last_r = -1, last_q = -1;  // the last fills issued
@@ -354,7 +394,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         const uint32_t sb = uint32_t(uniform(int(s_base)));
         while (!stop && w.next(p)) {
             int page_l = page_of_lane(p, w, w.blo, lane);
-            if (w.blo + lane < w.bhi && page_l < 0) atomicOr(p.err, kErrBadPage);
+            if (w.blo + lane < w.bhi && page_l == -1) atomicOr(p.err, kErrBadPage);
             stop = !wait(&ctl.q_empty, uint32_t(seg & 1) ^ 1u);
             if (stop) break;
             if (issuer) {
@@ -371,10 +411,12 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             for (int i = 0; i < blocks; ++i, ++n) {
                 if (i > 0 && (i & 31) == 0) {
                     page_l = page_of_lane(p, w, w.blo + i, lane);
-                    if (w.blo + i + lane < w.bhi && page_l < 0) atomicOr(p.err, kErrBadPage);
+                    if (w.blo + i + lane < w.bhi && page_l == -1) atomicOr(p.err, kErrBadPage);
                 }
                 // a page outside the cache: page 0 stands in, its entries are not used
-                const int row = max(__shfl_sync(0xffffffffu, page_l, i & 31), 0) * kBlk;
+                const int page = __shfl_sync(0xffffffffu, page_l, i & 31);
+                const int row = max(page, 0) * kBlk;
+                const bool own = kTree && page == -2;
                 const int buf = n & 1;  // half of the ring and rotary slab
                 const uint32_t phase = uint32_t((n >> 1) & 1) ^ 1u;
 #pragma unroll
@@ -382,8 +424,13 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                     stop = stop || !wait(&ctl.v_empty[4 * buf + j], phase);
                     if (!stop && issuer) {
                         mbar_arrive_expect_tx(&ctl.v_full[4 * buf + j], uint32_t(kPairBytes));
-                        tma_load_slabs(sb + kOffV + (4 * buf + j) * kPairBytes, &kv_map, &ctl.v_full[4 * buf + j], row,
-                                       2 * j, pol_kv);
+                        const uint32_t dst = sb + kOffV + (4 * buf + j) * kPairBytes;
+                        if (own) {
+                            tma_load_4d(dst, &d_map, &ctl.v_full[4 * buf + j], 2 * j, w.req(), pol_kv);
+                            tma_load_4d(dst + kSlabBytes, &d_map, &ctl.v_full[4 * buf + j], 2 * j + 1, w.req(), pol_kv);
+                        } else {
+                            tma_load_slabs(dst, &kv_map, &ctl.v_full[4 * buf + j], row, 2 * j, pol_kv);
+                        }
                     }
                     __syncwarp();
                     if (!stop) last_v = 4 * n + j;
@@ -392,7 +439,10 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 if (stop) break;
                 if (issuer) {
                     mbar_arrive_expect_tx(&ctl.r_full[buf], uint32_t(kSlabBytes));
-                    tma_load_2d(tiles + kOffR + buf * kSlabBytes, &kr_map, &ctl.r_full[buf], kMlaDv, row, pol_kv);
+                    if (own)
+                        tma_load_4d(sb + kOffR + buf * kSlabBytes, &d_map, &ctl.r_full[buf], 8, w.req(), pol_kv);
+                    else
+                        tma_load_2d(tiles + kOffR + buf * kSlabBytes, &kr_map, &ctl.r_full[buf], kMlaDv, row, pol_kv);
                 }
                 __syncwarp();
                 last_r = n;
@@ -423,7 +473,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort)) != 0;
         };
-        Walk w(ctl, p);
+        Walk<kTree> w(ctl, p);
         bool ok = true;
         int n = 0, seg = 0;
         while (ok && w.next(p)) {
@@ -489,7 +539,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort)) != 0;
         };
-        Walk w(ctl, p);
+        Walk<kTree> w(ctl, p);
         bool ok = true;
         int n = 0, seg = 0;
         while (ok && w.next(p)) {
@@ -499,14 +549,32 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 #pragma unroll 1
             for (int i = 0; i < blocks; ++i, ++n) {
                 const int blk = w.blo + i;
-                if ((i & 31) == 0) bad = __ballot_sync(0xffffffffu, page_of_lane(p, w, blk, lane) < 0);
+                if ((i & 31) == 0) bad = __ballot_sync(0xffffffffu, page_of_lane(p, w, blk, lane) == -1);
                 const int valid = uniform(((bad >> (i & 31)) & 1u) ? 0 : w.valid(blk, back));
                 const int buf = n & 1;  // half of the ring
                 if (i == 0) ok = wait(&ctl.o_empty, uint32_t(seg & 1) ^ 1u);
                 ok = ok && wait(&ctl.p_full, uint32_t(n & 1));
                 if (!ok) break;
                 tc_fence_after_sync();
-                if (valid & 15) {  // zero the value rows behind the live ones in the last 16-entry step
+                const bool own = w.own(blk);
+                if (own) {  // zero the value rows of drafted entries that nobody sees
+                    uint64_t used = 0;
+                    for (int j = lane; j < w.drafted; j += 32) used |= __ldg(p.mask + int64_t(w.req()) * p.tokens + j);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) used |= __shfl_xor_sync(0xffffffffu, used, o);
+                    used &= low_bits(w.drafted);
+                    for (int j = 0; j < 4; ++j)
+                        wait_landed(&ctl.v_full[4 * buf + j], uint32_t((n >> 1) & 1));
+                    for (int c = lane; c < ((valid + 15) & ~15) * 8; c += 32) {
+                        if ((used >> (c >> 3)) & 1u) continue;
+#pragma unroll
+                        for (int s = 0; s < 8; ++s)
+                            *reinterpret_cast<uint4*>(tiles + kOffV + buf * 4 * kPairBytes + s * kSlabBytes + c * 16) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                } else if (valid & 15) {  // zero the value rows behind the live ones in the last 16-entry step
                     const int rows = 16 - (valid & 15);
                     for (int j = 0; j < 4; ++j)  // landed long ago: orders these stores behind the copies
                         wait_landed(&ctl.v_full[4 * buf + j], uint32_t((n >> 1) & 1));
@@ -556,15 +624,15 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     } else if (warp == 3) {
         // ================= output stores =================
         // Requests without entries: out = 0, lse = -inf.
-        for (int b = group; b < p.batch; b += p.groups) {
-            if (blocks_of(seq_tokens(p, b)) > 0) continue;
+        for (int b = group; b < p.batch && !kTree; b += p.groups) {
+            if (blocks_of<kTree>(p, b) > 0) continue;
             const int64_t row = int64_t(b) * p.tokens + token;
             uint4* o = reinterpret_cast<uint4*>(p.out + row * kMlaHeads * kMlaDv);
             for (int i = lane; i < kMlaHeads * kMlaDv / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
             for (int h = lane; h < kMlaHeads; h += 32) p.lse[row * kMlaHeads + h] = -INFINITY;
         }
         const bool issuer = elect_one();
-        Walk w(ctl, p);
+        Walk<kTree> w(ctl, p);
         bool ok = true;
         int n = 0, staged = 0;  // blocks so far, and stagings
         while (ok && w.next(p)) {
@@ -618,17 +686,19 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         const uint32_t lane_addr = tmem_base + (uint32_t(quad * 32) << 16);
         const float c2 = p.sm_scale_log2;
         uint8_t* const pbuf = tiles + kOffP;
-        Walk w(ctl, p);
+        Walk<kTree> w(ctl, p);
         bool failed = false;
         int n = 0, halves = 0;  // blocks so far, and outputs staged in two halves
         while (!failed && w.next(p)) {
+            const uint64_t drafts =
+                kTree ? __ldg(p.mask + int64_t(w.req()) * p.tokens + token) & low_bits(w.drafted) : 0;
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
             bool fresh = true;  // no product of this request yet: O^T holds nothing of it
             uint32_t bad = 0;
 #pragma unroll 1
             for (int blk = w.blo; blk < w.bhi; ++blk, ++n) {
                 if (((blk - w.blo) & 31) == 0)
-                    bad = __ballot_sync(0xffffffffu, page_of_lane(p, w, blk, lane) < 0);
+                    bad = __ballot_sync(0xffffffffu, page_of_lane(p, w, blk, lane) == -1);
                 const int valid = ((bad >> ((blk - w.blo) & 31)) & 1u) ? 0 : w.valid(blk, back);
                 const int buf = n & 1;
                 // The previous block's product has read P (and O^T is at rest) long before the next scores
@@ -648,7 +718,12 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]) * c2;
                 }
-                if (valid < kBlk) {
+                if (w.own(blk)) {
+                    const uint32_t bits = uint32_t(drafts >> (32 * half)) >> (2 * (lane & 3));
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (!((bits >> (8 * (i >> 2) + (i & 1))) & 1u)) x[i] = -INFINITY;
+                } else if (valid < kBlk) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int col = 32 * half + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
@@ -879,13 +954,16 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 
 }  // namespace
 
-cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& kr_map,
-                             const CUtensorMap& o_map, const MlaDenseParams& p, cudaStream_t stream) {
+namespace {
+
+template <bool kTree>
+cudaError_t launch(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& kr_map,
+                   const CUtensorMap& o_map, const CUtensorMap& d_map, const MlaDenseParams& p, cudaStream_t stream) {
     static SmemLimitOnce smem_limit;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    e = smem_limit.apply(dev, mla_dense_kernel, kSmemD);
+    e = smem_limit.apply(dev, mla_dense_kernel<kTree>, kSmemD);
     if (e != cudaSuccess) return e;
     if (p.groups < 1 || p.groups > kMlaMaxGroups || p.tokens < 1) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
@@ -898,10 +976,10 @@ cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, mla_dense_kernel, q_map, kv_map, kr_map, o_map, p);
+    e = cudaLaunchKernelEx(&cfg, mla_dense_kernel<kTree>, q_map, kv_map, kr_map, o_map, d_map, p);
     if (e != cudaSuccess) return e;
     // No request is split where none can have more blocks than are kept together.
-    if (p.table_width <= kMlaWholeBlocks) return cudaSuccess;
+    if (p.table_width + (kTree ? 1 : 0) <= kMlaWholeBlocks) return cudaSuccess;
     MlaMergeParams m{};
     m.plan = p.plan;
     m.cuts = p.cuts;
@@ -909,9 +987,24 @@ cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map
     m.lse_part = p.lse_part;
     m.out = p.out;
     m.lse = p.lse;
+    m.counts = p.counts;
+    m.run = p.redo > 0 ? p.again : nullptr;
     m.tokens = p.tokens;
     m.by_cut = p.merge_by_cut;
     return launch_mla_merge(m, p.batch, p.groups, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_mla_dense(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& kr_map,
+                             const CUtensorMap& o_map, const MlaDenseParams& p, cudaStream_t stream) {
+    return launch<false>(q_map, kv_map, kr_map, o_map, q_map, p, stream);
+}
+
+cudaError_t launch_mla_dense_tree(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CUtensorMap& kr_map,
+                                  const CUtensorMap& o_map, const CUtensorMap& d_map, const MlaDenseParams& p,
+                                  cudaStream_t stream) {
+    return launch<true>(q_map, kv_map, kr_map, o_map, d_map, p, stream);
 }
 
 }  // namespace dsa

@@ -1,48 +1,29 @@
-// mla_tree_kernel.cu -- latent attention decode (absorbed form) for a tree of
-// drafted tokens, sm_103a.
+// mla_tree_kernel.cu -- the tree decode (mla_tree_kernel.cu) on clusters of four
+// CTAs and four drafted tokens, for calls whose time is products, sm_103a.
 //
-//     s[h, t] = sm_scale * q[b, j, h] . e_t                  (576-wide entries)
-//     o[b, j, h] = sum_t softmax_t(s[h, :]) e_t[:512],  lse = log sum_t exp(s[h, t])
+// What an SM takes in bounds the smaller kernel: 33 bytes a cycle, multicast or not
+// (measured), so a 64-row tile's 1,088 bytes an entry cost twice its multiply-adds.  Here:
+//   * rows: tokens 0 and 1 of the tile are CTAs 0 and 2's 128 rows, tokens 2 and 3 CTAs 1
+//     and 3's.  CTAs 0, 1 and CTAs 2, 3 are pairs (cta_group::2, M = 256: all four tokens);
+//   * S = Q . K^T    pair p takes page p of a block of two: N = 64, 32 entries in each CTA;
+//   * O += P . V     pair p takes value dims [256 p, 256 p + 256) of both pages: N = 256, 128
+//                    dims in each CTA.  P of its own page comes from tensor memory, P of the
+//                    other page from the CTA with the same rows in the other pair, through
+//                    distributed shared memory.
+// An entry then costs an SM 288 bytes as key, 256 as value and 128 of weights for 128 rows'
+// scores and half a row's values: 672 bytes, 20 cycles, for 17 of multiply-adds.
 //
-// over the ceil(seq_len / 4) live entries of the request's paged cache and the drafted
-// entries i whose bit of the token's mask is set.
+// No running maximum.  Both CTAs that hold a row must use one reference, and agreeing
+// on a new one block by block would cost a round trip each.  They agree once, on the
+// first block's maximum.  Weights may then pass 1 as far as fp32 and bf16 reach (their
+// rounding is relative: nothing is lost).  A CTA whose sums pass 2^58, or any of
+// whose outputs is not finite, sets its flag, and the smaller kernel, which keeps a running
+// maximum, then does the whole call again (launch_mla_tree): it leaves at once where no flag is set.
 //
-// A token's 64 heads fill half of a tensor core's rows, and its accumulators (64 x 512)
-// half of an SM's tensor memory; two tokens' q do not fit an SM's shared memory beside
-// the entries.  So a cluster of two CTAs works on two tokens, one in each, with
-// cta_group::2 MMAs (M = 128: 64 rows of a token in each CTA) whose second operand is
-// split between the CTAs' shared memory:
-//     S = Q . K^T    N = 128 entries: a block of two pages, one page's 576 dims in each CTA
-//     O += P . V     N = 256 dims, twice: of both pages 2 x 128 dims in each CTA, read
-//                    in place as an MN-major operand
-// An entry is thus read as key in one of the CTAs and as value in both: 1,088 bytes of
-// loads an SM and entry for two tokens (1,152 for one otherwise), and the operands' reads
-// of shared memory, which bound a CTA with one token, fall from 60 to 30 bytes a
-// thousand multiply-adds.  D of an M = 128 pair lies in each CTA as 64 rows x two halves
-// of the columns: lanes 0-63 the first half, 64-127 the second.
-//
-// Work.  A request's blocks are those of its pages followed by a page of its drafted
-// entries.  Requests laid end to end, kTreeSegUnits units of fixed cost before each, are cut
-// into ranges; a unit is a range and a pair of tokens.  Units are dealt out range by range,
-// so that the pairs of one request run at the same time and all but the first read
-// its pages from L2.  A request inside one range is written straight to the output,
-// one that crosses ranges leaves fp32 partials that a second kernel joins.
-//
-// Roles of a CTA (384 threads):
-//   * warps 0-7: softmax.  Warp w reads TMEM quadrant w % 4 (rows 32 (w & 1) + lane of
-//     page (w >> 1) & 1) and half of the page's entries: one row and 32 entries a
-//     thread.  The running maximum is raised only when a block passes it by more than
-//     2^20; O is then rescaled in TMEM.  At the end the output, from TMEM to global memory.
-//   * warp 8 (of the leader): MMAs.  The next block's S before this one's O, so that
-//     the softmax runs under a product.
-//   * warps 9 and 10: TMA of q and keys, and of values.
-//   * warp 11: zeroes the value rows of entries that nobody sees (behind the last live
-//     one, drafted ones outside every mask): their weights are 0, but 0 x NaN is not.
-// Row sums add the unrounded fp32 weights; the weights are rounded to bf16 only as the
-// second product's operand.
-//
-// Every wait is bounded (about 1 s) but the cluster barriers, which every thread
-// reaches; a timeout sets an error bit, the roles drain, and TMEM is freed.
+// Shared memory holds q (147 KB), eight of a block's nine key slabs, its values, and the other page's
+// weights.  Roles as in the smaller kernel (384 threads): warps 0-7 softmax, one row and 32 entries a
+// thread; warp 8 of each pair's leader MMAs; 9 and 10 TMA; 11 zeroes value rows that nobody sees.
+// Every wait is bounded (about 1 s) but the cluster barriers, which every thread reaches.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -53,103 +34,327 @@
 #include "cta_pair.cuh"
 #include "indexer_kernels.h"
 #include "mla_common.cuh"
-#include "mla_tree_common.cuh"
+#include "mla_tree_plan.h"
 #include "sm103_ptx.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kThreadsT = 384;
-constexpr int kSlabT = kPg * 128;             // 64 rows x 64 bf16 dims, 8 KiB
-constexpr int kSlabsT = kMlaDim / 64;         // 9
-constexpr int kKeyGroups = 5;                 // slab pairs of the value dims, and the last slab
-constexpr int kValGroups = 4;                 // (page, 256 dims): 2 page + half
-constexpr int kGroupV = 2 * kSlabT;           // this CTA's 128 of a group's 256 dims
-constexpr int kOffQT = 0;
-constexpr int kOffKT = kOffQT + kSlabsT * kSlabT;
-constexpr int kOffVT = kOffKT + kSlabsT * kSlabT;
-constexpr int kOffPT = kOffVT + kValGroups * kGroupV;  // P: 64 rows x 64 entries of each page
-constexpr int kOffCtlT = kOffPT + 2 * kSlabT;
-constexpr uint32_t kTmemColsT = 512;
-constexpr uint32_t kColST = 0;    // S: 2 x 64 columns
-constexpr uint32_t kColOT = 128;  // O: 2 x 128 columns
-constexpr float kRaise = 20.0f;   // log2; a weight's rounding is relative, so nothing is lost below it
+constexpr int kThreadsQ = 416;
+constexpr int kPg = kPageEntries;      // entries of a page, heads of a token
+constexpr int kSoftWarps = 8;
+constexpr float kLn2T = 0.69314718055994531f;
 
-struct __align__(16) TreeCtl {
-    uint64_t k_full[kKeyGroups], k_empty[kKeyGroups];  // full: the leader's, of both CTAs' copies
-    uint64_t v_full[kValGroups], v_empty[kValGroups];
-    uint64_t vz_full[2], vz_ready[2];  // of pages with rows to zero: landed in this CTA; zeroed in both
+struct UnitT {
+    int lo, hi;                  // the range, in units of the plan
+    int first_req, first_start;  // request of its first unit, and where that request's units start
+};
+
+// In shared memory: a cluster's units.
+struct TreePlan {
+    UnitT unit[kTreeMaxRounds];
+    int cut[kTreeMaxRounds];     // the request that the range is the second one of, or -1
+    int warp_units[16];
+};
+
+__device__ __forceinline__ bool soft_or(bool v) {  // over the 256 softmax threads
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred pi, po;\n\t"
+        "setp.ne.u32 pi, %1, 0;\n\t"
+        "bar.red.or.pred po, 1, 256, pi;\n\t"
+        "selp.u32 %0, 1, 0, po;\n\t}"
+        : "=r"(r)
+        : "r"(v ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void wait_landed_t(uint64_t* bar, uint32_t parity) {
+    const uint32_t a = smem_u32(bar);
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(a, parity) && global_timer_ns() - t0 < kWaitLimitNs) {
+    }
+}
+
+__device__ __forceinline__ int tree_tokens(const MlaTreeParams& p, int b) {  // cached, in [0, max_context]
+    const int seq = __ldg(p.seq_lens + b);
+    return seq < 0 ? 0 : (int64_t(seq) > p.max_context ? int(p.max_context) : seq);
+}
+__device__ __forceinline__ int tree_drafted(const MlaTreeParams& p, int b) {  // in [0, tokens]
+    if (!p.counts) return p.tokens;
+    return min(max(__ldg(p.counts + b), 0), p.tokens);
+}
+__device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1; }
+
+// The cluster's walk over its units: one step per request that has blocks in a unit's range and tokens
+// in its tile.
+struct TreeWalk {
+    int k, rounds, first, step;  // units first, first + step, ...
+    int b, u0, lo, hi;
+    int range, tile;
+    int np, live, drafted, nb, blo, bhi;  // current request: cache pages, entries, drafted tokens, blocks
+    __device__ __forceinline__ TreeWalk(int first_, int step_, int units)
+        : k(-1), rounds(first_ < units ? (units - first_ + step_ - 1) / step_ : 0), first(first_), step(step_), b(0),
+          u0(0), lo(0), hi(0) {}
+    __device__ __forceinline__ bool next(const MlaTreeParams& p, const TreePlan& plan) {
+        while (true) {
+            while (b < p.batch && u0 < hi) {
+                const int seq = tree_tokens(p, b);
+                live = (seq + 3) >> 2;
+                np = tree_cache_pages(seq);
+                drafted = tree_drafted(p, b);
+                nb = tree_blocks(np, drafted);
+                const int base = u0 + kTreeSegUnits, end = u0 + tree_units(nb);
+                blo = max(lo, base) - base;
+                bhi = min(hi, end) - base;
+                ++b;
+                u0 = end;
+                if (nb > 0 && bhi > blo && kTileTokens * tile < drafted) return true;
+            }
+            if (++k >= rounds) return false;
+            const int u = first + k * step;
+            range = u / p.tiles;
+            tile = u - range * p.tiles;
+            lo = plan.unit[k].lo, hi = plan.unit[k].hi, b = plan.unit[k].first_req, u0 = plan.unit[k].first_start;
+        }
+    }
+    __device__ __forceinline__ int req() const { return b - 1; }
+    // Entries of a page that somebody may see, if its id is good.
+    __device__ __forceinline__ int valid(int page) const {
+        return page < np ? min(live - page * kPg, kPg) : (page == np ? drafted : 0);
+    }
+    // Has a page value rows to zero?  (The drafted page always, by the masks.)
+    __device__ __forceinline__ bool zeroes(int page) const {
+        return page == np || (page < np && ((live - page * kPg) < kPg) && ((live & 15) != 0));
+    }
+};
+
+// Ids of pages [page0, page0 + 32) of the current request, a lane each: -1 where the table's is outside the
+// cache, -2 for the drafted page and those behind it.
+__device__ __forceinline__ int tree_page_of_lane(const MlaTreeParams& p, const TreeWalk& w, int page0, int lane) {
+    const int page = page0 + lane;
+    if (page >= w.np) return -2;
+    const int id = __ldg(p.page_table + int64_t(w.req()) * p.table_width + page);
+    return (id >= 0 && int64_t(id) < p.num_pages) ? id : -1;
+}
+
+
+__device__ __forceinline__ void clear_plan(const MlaTreeParams& p, TreePlan& plan) {
+    for (int k = 0; k < kTreeMaxRounds; ++k) {
+        plan.unit[k] = {0, 0, p.batch, 0};
+        plan.cut[k] = -1;
+    }
+}
+
+// Finds the cluster's units, from the prefix sums of the requests' plan units; returns how many the call
+// has.  For all threads, the plan cleared; it is there after the caller's next barrier.
+template <int kThreads>
+__device__ __forceinline__ int find_units(const MlaTreeParams& p, TreePlan& plan, int cluster, int clusters) {
+    const int warp = int(threadIdx.x) >> 5, lane = threadIdx.x & 31;
+    const int per = (p.batch + kThreads - 1) / kThreads;
+    const int r0 = min(int(threadIdx.x) * per, p.batch), r1 = min(r0 + per, p.batch);
+    int mine = 0;
+    for (int b = r0; b < r1; ++b) {
+        if (blockIdx.x == 0) {
+            const int seq = __ldg(p.seq_lens + b);
+            if (seq < 0 || int64_t(seq) > p.max_context) atomicOr(p.err, kErrSeqLenClamped);
+            if (p.counts && tree_drafted(p, b) != __ldg(p.counts + b)) atomicOr(p.err, kErrBadRange);
+        }
+        mine += tree_units(tree_blocks(tree_cache_pages(tree_tokens(p, b)), tree_drafted(p, b)));
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) plan.warp_units[warp] = incl;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += plan.warp_units[w];
+        total += plan.warp_units[w];
+    }
+    const int nranges = max(min(p.ranges, total), 1);
+    const int units = nranges * p.tiles;
+    const Ranges ranges(nranges, total);
+    if (threadIdx.x == 0)  // cuts at the very end lie in no request
+        for (int k = 0; cluster + k * clusters < units; ++k) {
+            const int range = (cluster + k * clusters) / p.tiles;
+            if (ranges.cut(range) == total) plan.unit[k].lo = total;
+            if (ranges.cut(range + 1) == total) plan.unit[k].hi = total;
+        }
+    int u = before + incl - mine;
+    for (int b = r0; b < r1; ++b) {
+        const int nb = tree_blocks(tree_cache_pages(tree_tokens(p, b)), tree_drafted(p, b)), n = tree_units(nb);
+        for (int k = 0; cluster + k * clusters < units; ++k) {
+            const int range = (cluster + k * clusters) / p.tiles;
+            const int lo = ranges.cut(range), hi = ranges.cut(range + 1);
+            if (lo >= u && lo < u + n) {
+                plan.unit[k].lo = tree_settled_cut(lo, u, nb);
+                plan.unit[k].first_req = b;
+                plan.unit[k].first_start = u;
+            }
+            if (hi >= u && hi < u + n) plan.unit[k].hi = tree_settled_cut(hi, u, nb);
+            // Is this the request's second range?  Its first block lies in the one before.
+            if (nb > kTreeWholeBlocks && lo > u + kTreeSegUnits && lo < u + n &&
+                ranges.cut(range - 1) <= u + kTreeSegUnits)
+                plan.cut[k] = b;
+        }
+        if (blockIdx.x == 0)  // the first and last range that hold its blocks, for the merge
+            p.plan[b] = nb > kTreeWholeBlocks ? make_int2(ranges.of(u + kTreeSegUnits), ranges.of(u + n - 1))
+                                              : make_int2(0, 0);
+        u += n;
+    }
+    return units;
+}
+
+// The cuts of the cluster's ranges, for the merge; by one thread.
+__device__ __forceinline__ void write_cuts(const MlaTreeParams& p, const TreePlan& plan, int cluster, int clusters,
+                                           int units) {
+    for (int k = 0; cluster + k * clusters < p.ranges * p.tiles; ++k) {  // ranges without work too
+        const int u = cluster + k * clusters;
+        if (u % p.tiles == 0) p.cuts[u / p.tiles] = u < units ? plan.cut[k] : -1;
+    }
+}
+
+constexpr int kRowsQ = 128;                     // rows of a CTA: two tokens' heads
+constexpr int kHalfPg = kPg / 2;                // entries of a CTA's half page
+constexpr int kSlabsQ = kMlaDim / 64;           // 9
+constexpr int kSlabQ = kRowsQ * 128;            // 16 KiB
+constexpr int kSlabK = kHalfPg * 128;           // 4 KiB
+constexpr int kSlabsTm = 4;                     // of q in tensor memory, the last ones
+constexpr int kSlabsSm = kSlabsQ - kSlabsTm;    // in shared memory
+constexpr int kSlabsK = 3;                      // key slabs that are loaded together
+constexpr int kGroupK = kSlabsK * kSlabK;
+constexpr int kGroupsK = kSlabsQ / kSlabsK;     // of a block
+constexpr int kRingK = 4;                       // groups in shared memory
+constexpr int kSlabV = kPg * 128;               // values of a page: two slabs of 64 entries x 64 dims
+constexpr int kGroupQ = 2 * kSlabV;
+constexpr int kOffQq = 0;
+constexpr int kOffKq = kOffQq + kSlabsSm * kSlabQ;
+constexpr int kOffVq = kOffKq + kRingK * kGroupK;
+constexpr int kOffRq = kOffVq + 2 * kGroupQ;    // weights of the other page, 128 rows x 64 entries
+constexpr int kOffPq = kOffRq + 2 * kSlabQ;     // and of the own page; two blocks' of both
+constexpr int kOffCtlQ = kOffPq + 2 * kSlabQ;
+constexpr uint32_t kColSQ = 0;     // S: 2 x 64 columns
+constexpr uint32_t kColQQ = 128;   // q: 32 columns a slab
+constexpr uint32_t kColOQ = 256;   // O: 256 columns
+constexpr float kSumMost = 288230376151711744.0f;  // 2^58: times 2^18 entries and values below 2^50
+constexpr float kSumLeast = 8.4703294725430034e-22f;  // 2^-70, where the reference is not the row's own
+
+struct __align__(16) QuadCtl {
+    uint64_t k_full[kRingK], k_empty[kRingK];  // full: the pair's leader's, of both CTAs' copies
+    uint64_t v_full[2], v_empty[2];            // per page of a block
+    uint64_t vz_full[2], vz_ready[2];
     uint64_t s_full[2], s_empty[2];
-    uint64_t q_full, q_empty, p_full, pv_done, o_empty, all_done;
+    uint64_t q_full, q_empty, qt_full, o_empty, all_done;
+    uint64_t p_own[2], p_other[2], r_full[2], pv_done[2];  // of every other block
+    uint64_t m_full, l_full;                   // the other pair's row maxima, and sums, are here
     uint32_t tmem_base;
     int abort;
     TreePlan plan;
-    float part[4][kPg];          // per row and quarter of the block: maxima, at the end sums
+    float part[2][kRowsQ];                     // per half of the entries: maxima of the first block, then sums
+    float peer[2][kRowsQ];                     // the other pair's maxima, and sums
 };
-constexpr int kSmemT = 1024 + kOffCtlT + int(sizeof(TreeCtl));
-static_assert(kSmemT <= 232448, "fits one CTA per SM");
+constexpr int kSmemQ = kOffCtlQ + int(sizeof(QuadCtl));
+static_assert(kSmemQ <= 232448, "fits one CTA per SM");
 
-__global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
-    mla_tree_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
-                    const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap d_map,
-                    const MlaTreeParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    // Dynamic shared memory starts at the same offset in both CTAs, so the operands and barriers do too.
-    uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    TreeCtl& ctl = *reinterpret_cast<TreeCtl*>(tiles + kOffCtlT);
+// Arrive once on the barrier at this offset in the CTAs of `mask` when every MMA this thread issued has completed.
+__device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(mask)
+        : "memory");
+}
+
+// Copy to another CTA's shared memory, counted on a barrier there.
+__device__ __forceinline__ void bulk_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// 32 rows of one slab of a request's drafted entries (rows behind the last arrive as zeros).
+__device__ __forceinline__ void load_drafts(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t row, int32_t slab,
+                                            int32_t request, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(slab), "r"(request), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+__global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
+    mla_tree_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                         const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap d_map,
+                         const MlaTreeParams p) {
+    extern __shared__ uint8_t smem_raw[];  // at the same offset in all CTAs; on a 1,024-byte boundary, checked below
+    uint8_t* tiles = smem_raw;
+    QuadCtl& ctl = *reinterpret_cast<QuadCtl*>(tiles + kOffCtlQ);
     const uint32_t s_base = smem_u32(tiles);
     const int warp = uniform(int(threadIdx.x) >> 5);
     const int lane = threadIdx.x & 31;
-    const int rank = int(cluster_rank());  // 0: the leader
-    const int cluster = int(blockIdx.x) >> 1, clusters = int(gridDim.x) >> 1;
+    const int rank = int(cluster_rank());
+    const int pair = rank >> 1, side = rank & 1;   // side 0: the pair's leader
+    const uint32_t leader = uint32_t(rank & 2);
+    const uint16_t both = uint16_t(3u << (rank & 2));
+    const int cluster = int(blockIdx.x) >> 2, clusters = int(gridDim.x) >> 2;
 
-    if (p.redo > 0) {  // the larger kernel's call: only if a CTA of it has given up
-        pdl_wait_prior_grid();
-        const int any = __syncthreads_or(int(threadIdx.x) < p.redo && p.flags[threadIdx.x] != 0);
-        if (blockIdx.x == 0 && threadIdx.x == 0) *p.again = any ? 1 : 0;
-        if (!any) return;
+    if (s_base & 1023u) {  // (the same in every CTA; shared memory has started on such a boundary on every part)
+        if (threadIdx.x == 0) p.flags[blockIdx.x] = 1;
+        return;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kKeyGroups; ++i) {
+        for (int i = 0; i < kRingK; ++i) {
             mbar_init(&ctl.k_full[i], 1);
             mbar_init(&ctl.k_empty[i], 1);
         }
-        for (int i = 0; i < kValGroups; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.v_full[i], 1);
             mbar_init(&ctl.v_empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.vz_full[i], 1);
-            mbar_init(&ctl.vz_ready[i], 2);  // one arrival of each CTA
+            mbar_init(&ctl.vz_ready[i], 2);  // one arrival of each CTA of the pair
             mbar_init(&ctl.s_full[i], 1);
+            mbar_init(&ctl.p_own[i], 2 * kSoftWarps);
+            mbar_init(&ctl.p_other[i], 1);   // the other CTA of the pair has its part
+            mbar_init(&ctl.r_full[i], 1);
+            mbar_init(&ctl.pv_done[i], 2);   // of both pairs
             mbar_init(&ctl.s_empty[i], 2 * kSoftWarps);
         }
         mbar_init(&ctl.q_full, 1);
         mbar_init(&ctl.q_empty, 1);
-        mbar_init(&ctl.p_full, 2 * kSoftWarps);
-        mbar_init(&ctl.pv_done, 1);
+        mbar_init(&ctl.qt_full, 2 * kSoftWarps);
         mbar_init(&ctl.o_empty, 2 * kSoftWarps);
-        mbar_init(&ctl.all_done, 1);
+        mbar_init(&ctl.all_done, 4);         // of both pairs' two issuing warps
+        mbar_init(&ctl.m_full, kSoftWarps / 2);
+        mbar_init(&ctl.l_full, kSoftWarps / 2);
         ctl.abort = 0;
         clear_plan(p, ctl.plan);
         fence_mbar_init();
         tma_prefetch_map(&q_map);
-        tma_prefetch_map(&kv_map);
-        tma_prefetch_map(&kr_map);
+        tma_prefetch_map(&k_map);
+        tma_prefetch_map(&v_map);
         tma_prefetch_map(&d_map);
     }
-    if (warp == 8) tmem2_alloc(&ctl.tmem_base, kTmemColsT);
+    if (warp == 8) tmem2_alloc(&ctl.tmem_base, 512);
     __syncwarp();
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
 
-    const int units = find_units<kThreadsT>(p, ctl.plan, cluster, clusters);
+    const int units = find_units<kThreadsQ>(p, ctl.plan, cluster, clusters);
     tc_fence_before_sync();
-    cluster_sync_all();  // the barriers and the plan are there, in both CTAs
+    cluster_sync_all();  // the barriers and the plan are there, in all CTAs
     tc_fence_after_sync();
     if (threadIdx.x == 0 && rank == 0) write_cuts(p, ctl.plan, cluster, clusters, units);
     const uint32_t tmem_base = ctl.tmem_base;
     TreeWalk w(cluster, clusters, units);
+    bool flagged = false;
 
     if (warp == 9) {
         // ================= TMA: q and keys =================
@@ -158,56 +363,53 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
         const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
         const uint32_t sb = uint32_t(uniform(int(s_base)));
         bool ok = true;
-        int n = 0, seg = 0;
+        int n = 0, seg = 0, slot = 0;  // key groups, requests so far; the ring's place
+        uint32_t phase = 0;
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = ok && __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort));
             return ok;
         };
-        uint32_t issued = 0;  // fills of each key group beyond the n whole blocks (bit j), for the drain
         while (ok && w.next(p, ctl.plan)) {
             int id_l = tree_page_of_lane(p, w, 2 * w.blo, lane);
             if (id_l == -1 && 2 * w.blo + lane < 2 * w.bhi) atomicOr(p.err, kErrBadPage);
             if (!wait(&ctl.q_empty, uint32_t(seg & 1) ^ 1u)) break;
             if (issuer) {
-                const uint32_t bar = cluster_addr(&ctl.q_full, 0);
-                if (rank == 0) mbar_arrive_expect_tx(&ctl.q_full, uint32_t(2 * kSlabsT * kSlabT));
-                const int token = min(2 * w.tile + rank, p.tokens - 1);  // (an odd last one twice)
-                const int row = (w.req() * p.tokens + token) * kMlaHeads;
+                const uint32_t bar = cluster_addr(&ctl.q_full, leader);
+                if (side == 0) mbar_arrive_expect_tx(&ctl.q_full, uint32_t(2 * kSlabsSm * kSlabQ));
+                // (rows behind the request's tokens are others' or zeros, and are not written)
+                const int row = (w.req() * p.tokens + 4 * w.tile + 2 * side) * kMlaHeads;
 #pragma unroll
-                for (int s = 0; s < kSlabsT; s += 3) tma2_load_3d(sb + kOffQT + s * kSlabT, &q_map, bar, 0, row, s, pol_q);
+                for (int s = 0; s < kSlabsSm; ++s) tma2_load_3d(sb + kOffQq + s * kSlabQ, &q_map, bar, 0, row, s, pol_q);
             }
             __syncwarp();
             ++seg;
             const int blocks = uniform(w.bhi - w.blo);
 #pragma unroll 1
-            for (int i = 0; i < blocks; ++i, ++n) {
+            for (int i = 0; i < blocks && ok; ++i) {
                 if (i > 0 && (i & 15) == 0) {
                     id_l = tree_page_of_lane(p, w, 2 * (w.blo + i), lane);
                     if (id_l == -1 && 2 * (w.blo + i) + lane < 2 * w.bhi) atomicOr(p.err, kErrBadPage);
                 }
-                // this CTA's page; -1: page 0 stands in, its entries are not used
-                const int id = __shfl_sync(0xffffffffu, id_l, 2 * (i & 15) + rank);
-                const int row = max(id, 0) * kPg;
-#pragma unroll
-                for (int j = 0; j < kKeyGroups; ++j) {
-                    if (!wait(&ctl.k_empty[j], uint32_t(n & 1) ^ 1u)) break;
+                // the pair's page; -1: page 0 stands in, its entries are not used
+                const int id = __shfl_sync(0xffffffffu, id_l, 2 * (i & 15) + pair);
+                const int row = max(id, 0) * kPg + kHalfPg * side;
+#pragma unroll 1
+                for (int j = 0; j < kGroupsK; ++j, ++n) {
+                    if (!wait(&ctl.k_empty[slot], phase ^ 1u)) break;
                     if (issuer) {
-                        const uint32_t bar = cluster_addr(&ctl.k_full[j], 0), dst = sb + kOffKT + 2 * j * kSlabT;
-                        if (rank == 0) mbar_arrive_expect_tx(&ctl.k_full[j], uint32_t((j < 4 ? 4 : 2) * kSlabT));
+                        const uint32_t bar = cluster_addr(&ctl.k_full[slot], leader), dst = sb + kOffKq + slot * kGroupK;
+                        if (side == 0) mbar_arrive_expect_tx(&ctl.k_full[slot], uint32_t(2 * kGroupK));
                         if (id == -2) {
-                            tma2_load_4d(dst, &d_map, bar, 2 * j, w.req(), pol_kv);
-                            if (j < 4) tma2_load_4d(dst + kSlabT, &d_map, bar, 2 * j + 1, w.req(), pol_kv);
-                        } else if (j < 4) {
-                            tma2_load_3d(dst, &kv_map, bar, 0, row, 2 * j, pol_kv);
+#pragma unroll
+                            for (int k = 0; k < kSlabsK; ++k)
+                                load_drafts(dst + k * kSlabK, &d_map, bar, kHalfPg * side, kSlabsK * j + k, w.req(), pol_kv);
                         } else {
-                            tma2_load_2d(dst, &kr_map, bar, kMlaDv, row, pol_kv);
+                            tma2_load_3d(dst, &k_map, bar, 0, row, kSlabsK * j, pol_kv);
                         }
                     }
                     __syncwarp();
-                    issued |= 1u << j;
+                    if (++slot == kRingK) slot = 0, phase ^= 1u;
                 }
-                if (!ok) break;
-                issued = 0;
             }
         }
         if (lane == 0) {
@@ -216,11 +418,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
                 ctl.abort = 1;
             }
             // No copy outlives the cluster (bounded waits; they have landed unless a role gave up).
-            if (rank == 0) {
-                for (int j = 0; j < kKeyGroups; ++j) {
-                    const int fills = n + int((issued >> j) & 1u);
-                    if (fills > 0) wait_landed_t(&ctl.k_full[j], uint32_t(fills - 1) & 1u);
-                }
+            if (side == 0) {
+                for (int i = max(n - kRingK, 0); i < n; ++i)
+                    wait_landed_t(&ctl.k_full[i % kRingK], uint32_t(i / kRingK) & 1u);
                 if (seg > 0) wait_landed_t(&ctl.q_full, uint32_t(seg - 1) & 1u);
             }
         }
@@ -232,12 +432,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
         const uint32_t sb = uint32_t(uniform(int(s_base)));
         bool ok = true;
         int n = 0;
-        uint32_t zero_fills[2] = {0, 0};
+        uint32_t zero_fills[2] = {0, 0}, issued = 0;
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = ok && __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort));
             return ok;
         };
-        uint32_t issued = 0;
         while (ok && w.next(p, ctl.plan)) {
             int id_l = 0;
             const int blocks = uniform(w.bhi - w.blo);
@@ -245,35 +444,33 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
             for (int i = 0; i < blocks; ++i, ++n) {
                 if ((i & 15) == 0) id_l = tree_page_of_lane(p, w, 2 * (w.blo + i), lane);
 #pragma unroll
-                for (int pg = 0; pg < 2; ++pg) {
+                for (int s = 0; s < 2; ++s) {  // the pair's own page first, as its product goes
+                    const int pg = s ^ pair;
                     const int id = __shfl_sync(0xffffffffu, id_l, 2 * (i & 15) + pg);
-                    const int row = max(id, 0) * kPg;
                     const bool zeroes = id != -1 && w.zeroes(2 * (w.blo + i) + pg);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int g = 2 * pg + h;
-                        if (!wait(&ctl.v_empty[g], uint32_t(n & 1) ^ 1u)) break;
-                        if (issuer) {
-                            uint32_t bar = cluster_addr(&ctl.v_full[g], 0);
-                            if (zeroes) {
-                                bar = cluster_addr(&ctl.vz_full[pg], uint32_t(rank));
-                                if (h == 0) mbar_arrive_expect_tx(&ctl.vz_full[pg], uint32_t(2 * kGroupV));
-                                if (rank == 0) mbar_arrive(&ctl.v_full[g]);  // the group's phases go on
-                            } else if (rank == 0) {
-                                mbar_arrive_expect_tx(&ctl.v_full[g], uint32_t(2 * kGroupV));
-                            }
-                            const uint32_t dst = sb + kOffVT + g * kGroupV;
-                            const int slab = 4 * h + 2 * rank;  // dims 256 h + 128 rank
-                            if (id == -2) {
-                                tma2_load_4d(dst, &d_map, bar, slab, w.req(), pol_kv);
-                                tma2_load_4d(dst + kSlabT, &d_map, bar, slab + 1, w.req(), pol_kv);
-                            } else {
-                                tma2_load_3d(dst, &kv_map, bar, 0, row, slab, pol_kv);
-                            }
+                    if (!wait(&ctl.v_empty[pg], uint32_t(n & 1) ^ 1u)) break;
+                    if (issuer) {
+                        uint32_t bar = cluster_addr(&ctl.v_full[pg], leader);
+                        if (zeroes) {
+                            bar = cluster_addr(&ctl.vz_full[pg], uint32_t(rank));
+                            mbar_arrive_expect_tx(&ctl.vz_full[pg], uint32_t(kGroupQ));
+                            if (side == 0) mbar_arrive(&ctl.v_full[pg]);  // the page's phases go on
+                        } else if (side == 0) {
+                            mbar_arrive_expect_tx(&ctl.v_full[pg], uint32_t(2 * kGroupQ));
                         }
-                        __syncwarp();
-                        issued |= 1u << g;
+                        const uint32_t dst = sb + kOffVq + pg * kGroupQ;
+                        const int slab = 4 * pair + 2 * side;  // dims 256 pair + 128 side
+                        if (id == -2) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)  // 32 entries of a slab at a time
+                                load_drafts(dst + k * kSlabK, &d_map, bar, kHalfPg * (k & 1), slab + (k >> 1), w.req(),
+                                            pol_kv);
+                        } else {
+                            tma2_load_3d(dst, &v_map, bar, 0, max(id, 0) * kPg, slab, pol_kv);
+                        }
                     }
+                    __syncwarp();
+                    issued |= 1u << pg;
                     if (ok && zeroes) ++zero_fills[pg];
                 }
                 if (!ok) break;
@@ -285,14 +482,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
                 atomicOr(p.err, kErrWaitTimeout);
                 ctl.abort = 1;
             }
-            if (rank == 0)
-                for (int g = 0; g < kValGroups; ++g) {
+            if (side == 0)
+                for (int g = 0; g < 2; ++g) {
                     const int fills = n + int((issued >> g) & 1u);
                     if (fills > 0) wait_landed_t(&ctl.v_full[g], uint32_t(fills - 1) & 1u);
                 }
             for (int pg = 0; pg < 2; ++pg)
                 if (zero_fills[pg] > 0) wait_landed_t(&ctl.vz_full[pg], (zero_fills[pg] - 1) & 1u);
-            // After a timeout the two CTAs may have issued different copies, and what only the other counts
+            // After a timeout the CTAs may have issued different copies, and what only another counts
             // cannot be waited for here: a millisecond, a thousand times a copy's latency.
             if (*const_cast<volatile int*>(&ctl.abort)) {
                 const uint64_t t0 = global_timer_ns();
@@ -323,100 +520,119 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
                 phase ^= 1u << pg;
                 if (!ok) break;
                 const int rows = (w.valid(page) + 15) & ~15;
-                uint8_t* v = tiles + kOffVT + 2 * pg * kGroupV;
                 for (int c = lane; c < rows * 8; c += 32) {
-                    if ((used >> (c >> 3)) & 1u) continue;
+                    const int r = c >> 3;
+                    if ((used >> r) & 1u) continue;
+                    uint8_t* v = tiles + kOffVq + pg * kGroupQ + r * 128 + (c & 7) * 16;
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        *reinterpret_cast<uint4*>(v + s * kSlabT + c * 16) = make_uint4(0, 0, 0, 0);
+                    for (int s = 0; s < 2; ++s) *reinterpret_cast<uint4*>(v + s * kSlabV) = make_uint4(0, 0, 0, 0);
                 }
                 asm volatile("fence.proxy.async;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&ctl.vz_ready[pg], 0));
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&ctl.vz_ready[pg], leader));
             }
         }
         __syncwarp();
-    } else if (warp == 8) {
-        // ================= MMA (the leader's) =================
-        if (rank == 0) {
-            constexpr uint32_t kIdescQk = idesc_bf16_f32(128, 128);
-            constexpr uint32_t kIdescPv = idesc_bf16_f32(128, 256) | (1u << 16);  // B (V) MN-major
+    } else if (warp == 8 || (warp == 12 && side == 0)) {
+        // ================= MMA (the pairs' leaders'), scores =================
+        // In a warp of their own: one that issued both products was late with every one of them (4,650
+        // cycles a block, of them 2,000 in barriers that were complete).
+        if (side == 0) {
+            constexpr uint32_t kIdescQk = idesc_bf16_f32(256, 64);
+            constexpr uint32_t kIdescPv = idesc_bf16_f32(256, 256) | (1u << 16);  // B (V) MN-major
             const uint32_t tmem = uint32_t(uniform(int(tmem_base)));
             const uint32_t sb = uint32_t(uniform(int(s_base)));
-            const uint64_t q_desc = smem_desc_kmajor_sw128(sb + kOffQT);
-            const uint64_t k_desc = smem_desc_kmajor_sw128(sb + kOffKT);
-            const uint64_t p_desc = smem_desc_kmajor_sw128(sb + kOffPT);
-            const uint64_t v_desc = desc_mn_sw128(sb + kOffVT, kSlabT);
             const bool issuer = elect_one();
             bool ok = true;
             const auto wait = [&](uint64_t* bar, uint32_t parity) {
                 ok = ok && __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort));
                 return ok;
             };
-            int nq = 0, nv = 0, seg = 0;  // S products, O products, requests so far
-            uint32_t zero_phase = 0;
-            // S of the next block
-            const auto qk = [&](bool last) {
-                const int buf = nq & 1;
-                const uint32_t phase = uint32_t(nq & 1);
-                wait(&ctl.s_empty[buf], (uint32_t(nq >> 1) & 1u) ^ 1u);
-                const uint32_t d = tmem + kColST + 64u * buf;
+            int n = 0, seg = 0;  // blocks, requests so far
+            if (warp == 8) {
+                const uint64_t q_desc = smem_desc_kmajor_sw128(sb + kOffQq);
+                const uint64_t k_desc = smem_desc_kmajor_sw128(sb + kOffKq);
+                int slot = 0;
+                uint32_t phase = 0;
+                while (ok && w.next(p, ctl.plan)) {
+                    if (!wait(&ctl.q_full, uint32_t(seg & 1)) || !wait(&ctl.qt_full, uint32_t(seg & 1))) break;
+                    const int blocks = uniform(w.bhi - w.blo);
+#pragma unroll 1
+                    for (int i = 0; i < blocks && ok; ++i, ++n) {
+                        const int buf = n & 1;
+                        const uint32_t d = tmem + kColSQ + 64u * buf;
+                        wait(&ctl.s_empty[buf], (uint32_t(n >> 1) & 1u) ^ 1u);
 #pragma unroll
-                for (int j = 0; j < kKeyGroups; ++j) {
-                    if (!wait(&ctl.k_full[j], phase)) return;
-                    tc_fence_after_sync();
-                    if (issuer) {
-                        const uint64_t a = refreshed(q_desc + uint32_t(2 * j * (kSlabT >> 4)));
-                        const uint64_t bd = refreshed(k_desc + uint32_t(2 * j * (kSlabT >> 4)));
+                        for (int j = 0; j < kGroupsK; ++j) {
+                            wait(&ctl.k_full[slot], phase);
+                            tc_fence_after_sync();
+                            if (ok && issuer) {
+                                const uint64_t bd = refreshed(k_desc + uint32_t(slot * (kGroupK >> 4)));
+                                const uint64_t a = refreshed(q_desc + uint32_t(kSlabsK * j * (kSlabQ >> 4)));
+                                const uint32_t at = refreshed(tmem + kColQQ), dd = refreshed(d);
 #pragma unroll
-                        for (int hs = 0; hs < (j < 4 ? 2 : 1); ++hs)
+                                for (int k = 0; k < kSlabsK; ++k)
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma2_bf16_ss(refreshed(d), a + uint32_t(hs * (kSlabT >> 4) + 2 * kk),
-                                              bd + uint32_t(hs * (kSlabT >> 4) + 2 * kk), kIdescQk,
-                                              (j | hs | kk) != 0 ? 1u : 0u);
-                        umma2_commit(&ctl.k_empty[j]);
-                        if (j == kKeyGroups - 1) {
-                            umma2_commit(&ctl.s_full[buf]);
-                            if (last) umma2_commit(&ctl.q_empty);
+                                    for (int kk = 0; kk < 4; ++kk) {
+                                        const uint64_t b = bd + uint32_t(k * (kSlabK >> 4) + 2 * kk);
+                                        if (kSlabsK * j + k < kSlabsSm)
+                                            umma2_bf16_ss(dd, a + uint32_t(k * (kSlabQ >> 4) + 2 * kk), b, kIdescQk,
+                                                          (j | k | kk) != 0 ? 1u : 0u);
+                                        else
+                                            umma2_bf16_ts(dd, at + uint32_t(32 * (kSlabsK * j + k - kSlabsSm) + 8 * kk), b, kIdescQk, 1u);
+                                    }
+                                commit_to(&ctl.k_empty[slot], both);
+                                if (j == kGroupsK - 1) {
+                                    commit_to(&ctl.s_full[buf], both);
+                                    if (i + 1 == blocks) commit_to(&ctl.q_empty, both);
+                                }
+                            }
+                            __syncwarp();
+                            if (++slot == kRingK) slot = 0, phase ^= 1u;
                         }
                     }
-                    __syncwarp();
+                    ++seg;
                 }
-                ++nq;
-            };
-            while (ok && w.next(p, ctl.plan)) {
-                if (!wait(&ctl.q_full, uint32_t(seg & 1))) break;
-                const int blocks = uniform(w.bhi - w.blo);
-                uint32_t fresh = 1, bad = 0;
-                qk(blocks == 1);
+            } else {
+                // ---- outputs
+                const uint64_t r_desc = smem_desc_kmajor_sw128(sb + kOffRq), p_desc = smem_desc_kmajor_sw128(sb + kOffPq);
+                const uint64_t v_desc = desc_mn_sw128(sb + kOffVq, kSlabV);
+                uint32_t zero_phase = 0;
+                while (ok && w.next(p, ctl.plan)) {
+                    const int blocks = uniform(w.bhi - w.blo);
+                    uint32_t fresh = 1, bad = 0;
 #pragma unroll 1
-                for (int i = 0; i < blocks && ok; ++i, ++nv) {
-                    if ((i & 15) == 0)
-                        bad = __ballot_sync(0xffffffffu, tree_page_of_lane(p, w, 2 * (w.blo + i), lane) == -1);
-                    if (i + 1 < blocks) qk(i + 2 == blocks);
-                    if (i == 0) wait(&ctl.o_empty, uint32_t(seg & 1) ^ 1u);
-                    // (cluster scope: the weights are the other CTA's ordinary stores too)
-                    ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.p_full, uint32_t(nv & 1), &ctl.abort));
+                    for (int i = 0; i < blocks && ok; ++i, ++n) {
+                        if ((i & 15) == 0)
+                            bad = __ballot_sync(0xffffffffu, tree_page_of_lane(p, w, 2 * (w.blo + i), lane) == -1);
+                        const int buf = n & 1;
+                        const uint32_t phase = uint32_t(n >> 1) & 1u;
+                        if (issuer) mbar_arrive_expect_tx(&ctl.r_full[buf], uint32_t(kSlabQ));
+                        __syncwarp();
+                        if (i == 0) wait(&ctl.o_empty, uint32_t(seg & 1) ^ 1u);
 #pragma unroll
-                    for (int pg = 0; pg < 2; ++pg) {
-                        const int page = 2 * (w.blo + i) + pg;
-                        const bool good = !((bad >> (2 * (i & 15) + pg)) & 1u);
-                        const int steps = good ? uniform((w.valid(page) + 15) >> 4) : 0;
-                        if (good && w.zeroes(page)) {
-                            ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u,
-                                                                                 &ctl.abort));
-                            zero_phase ^= 1u << pg;
-                        }
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int g = 2 * pg + h;
-                            if (!wait(&ctl.v_full[g], uint32_t(nv & 1))) break;
+                        for (int s = 0; s < 2; ++s) {  // the own page, then the other
+                            const int pg = s ^ pair;
+                            const int page = 2 * (w.blo + i) + pg;
+                            const bool good = !((bad >> (2 * (i & 15) + pg)) & 1u);
+                            const int steps = good ? uniform((w.valid(page) + 15) >> 4) : 0;
+                            if (good && w.zeroes(page)) {
+                                ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u,
+                                                                                     &ctl.abort));
+                                zero_phase ^= 1u << pg;
+                            }
+                            wait(&ctl.v_full[pg], uint32_t(n & 1));
+                            if (s == 0) {
+                                ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.p_own[buf], phase, &ctl.abort));  // (the other CTA's stores)
+                            } else {
+                                wait(&ctl.r_full[buf], phase);
+                                ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.p_other[buf], phase, &ctl.abort));
+                            }
                             tc_fence_after_sync();
-                            if (issuer) {
-                                const uint64_t a = refreshed(p_desc + uint32_t(pg * (kSlabT >> 4)));
-                                const uint64_t bd = refreshed(v_desc + uint32_t(g * (kGroupV >> 4)));
-                                const uint32_t d = refreshed(tmem + kColOT + 128u * h);
+                            if (ok && issuer) {
+                                const uint64_t bd = refreshed(v_desc + uint32_t(pg * (kGroupQ >> 4)));
+                                const uint32_t d = refreshed(tmem + kColOQ);
+                                const uint64_t a = refreshed((s == 0 ? p_desc : r_desc) + uint32_t(buf * (kSlabQ >> 4)));
                                 const auto step = [&](int kk) {
                                     umma2_bf16_ss(d, a + 2u * kk, bd + uint32_t(kk * (2048 >> 4)), kIdescPv,
                                                   (kk == 0 && fresh) ? 0u : 1u);
@@ -428,46 +644,89 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll 1
                                     for (int kk = 0; kk < steps; ++kk) step(kk);
                                 }
-                                umma2_commit(&ctl.v_empty[g]);
-                                if (g == kValGroups - 1) umma2_commit(&ctl.pv_done);
+                                commit_to(&ctl.v_empty[pg], both);
+                                if (s == 1) commit_to(&ctl.pv_done[buf], uint16_t(15));
                             }
                             __syncwarp();
+                            if (steps > 0) fresh = 0;
                         }
-                        if (steps > 0) fresh = 0;
                     }
+                    ++seg;
                 }
-                ++seg;
             }
             if (issuer) {
                 if (!ok) {
                     atomicOr(p.err, kErrWaitTimeout);
                     ctl.abort = 1;
                 }
-                umma2_commit(&ctl.all_done);  // every MMA this thread issued has completed when this arrives
+                commit_to(&ctl.all_done, uint16_t(15));  // every MMA this thread issued has completed when this arrives
             }
             __syncwarp();
-            wait_landed_t(&ctl.all_done, 0);
-            __syncwarp();
+        } else {
+            // ---- the other CTA's: tells the leader of the weights that have come here
+            const bool issuer = elect_one();
+            bool ok = true;
+            int n = 0;
+            while (ok && w.next(p, ctl.plan)) {
+                const int blocks = uniform(w.bhi - w.blo);
+#pragma unroll 1
+                for (int i = 0; i < blocks && ok; ++i, ++n) {
+                    if (issuer) mbar_arrive_expect_tx(&ctl.r_full[n & 1], uint32_t(kSlabQ));
+                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, mbar_await(&ctl.r_full[n & 1], uint32_t(n >> 1) & 1u, &ctl.abort)) != 0;
+                    if (ok && issuer) mbar_arrive_cluster(cluster_addr(&ctl.p_other[n & 1], leader));
+                    __syncwarp();
+                }
+            }
         }
-    } else {
+    } else if (warp < kSoftWarps) {
         // ================= softmax and output =================
-        const int quad = warp & 3, half = warp >> 2;     // entries [32 half, 32 half + 32) of the page
-        const int pg = quad >> 1;
-        const int row = (quad & 1) * 32 + lane;          // the head
-        const int part = 2 * pg + half;
+        const int quad = warp & 3, half = warp >> 2;     // entries [32 half, 32 half + 32) of the pair's page
+        const int row = quad * 32 + lane;
         const uint32_t lane_addr = tmem_base + (uint32_t(quad * 32) << 16);
-        const uint32_t s_bar = cluster_addr(ctl.s_empty, 0), p_bar = cluster_addr(&ctl.p_full, 0),
-                       o_bar = cluster_addr(&ctl.o_empty, 0);
+        const uint32_t peer = uint32_t(rank ^ 2);        // the same rows, the other page and value dims
+        const uint32_t s_bar = cluster_addr(ctl.s_empty, leader), p_bar = cluster_addr(ctl.p_own, leader),
+                       o_bar = cluster_addr(&ctl.o_empty, leader), qt_bar = cluster_addr(&ctl.qt_full, leader);
+        const uint32_t r_rows = cluster_addr(tiles + kOffRq, peer) + quad * 4096, r_bar = cluster_addr(ctl.r_full, peer);
+        uint8_t* const pbuf = tiles + kOffPq + row * 128;
+        const uint32_t peer_max = cluster_addr(ctl.peer[0], peer) + 4 * row, peer_sum = cluster_addr(ctl.peer[1], peer) + 4 * row;
+        const uint32_t m_bar = cluster_addr(&ctl.m_full, peer), l_bar = cluster_addr(&ctl.l_full, peer);
         const float c2 = p.sm_scale_log2;
-        uint8_t* const pbuf = tiles + kOffPT + pg * kSlabT + row * 128;
         bool failed = false;
-        int n = 0;
+        int n = 0, seg = 0;
         while (!failed && w.next(p, ctl.plan)) {
-            const int token = 2 * w.tile + rank;
+            const int token = 4 * w.tile + 2 * side + (row >> 6);
             const bool live_token = token < w.drafted;
             const int64_t q_row = int64_t(w.req()) * p.tokens + min(token, p.tokens - 1);
             const uint64_t drafts = __ldg(p.mask + q_row) & low_bits(w.drafted);
-            float m = -INFINITY, l = 0.f;
+            // The last slabs of q, once the products of the request before have read them: 128 dims a thread.
+            bool ok = mbar_await(&ctl.q_empty, uint32_t(seg & 1) ^ 1u, &ctl.abort);
+            if (!__all_sync(0xffffffffu, ok)) {
+                failed = true;  // (met by all warps at the next barrier)
+                if (lane == 0) ctl.abort = 1;
+            }
+            {
+                const uint4* q = reinterpret_cast<const uint4*>(p.q + (q_row * kMlaHeads + (row & 63)) * kMlaDim +
+                                                                64 * kSlabsSm + 32 * kSlabsTm * half);
+                tc_fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < kSlabsTm; ++c) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 v = __ldg(q + 4 * c + k);
+                        r[4 * k] = v.x, r[4 * k + 1] = v.y, r[4 * k + 2] = v.z, r[4 * k + 3] = v.w;
+                    }
+                    tmem_st_x16(lane_addr + kColQQ + 16u * kSlabsTm * half + 16u * c, r);
+                }
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(qt_bar);
+            }
+            float m = 0.f, l = 0.f;
+            bool own = true;    // the reference is a score of the row's
+            uint32_t any = 0;   // entries seen
             bool fresh = true;  // no product of this request yet: O holds nothing of it
             uint32_t bad = 0;
 #pragma unroll 1
@@ -475,107 +734,119 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
                 if (((blk - w.blo) & 15) == 0)
                     bad = __ballot_sync(0xffffffffu, tree_page_of_lane(p, w, 2 * blk, lane) == -1);
                 const uint32_t bad_here = bad >> (2 * ((blk - w.blo) & 15));
-                const int page = 2 * blk + pg;
+                const int page = 2 * blk + pair;
                 uint64_t seen = page == w.np ? drafts : low_bits(w.valid(page));
-                if ((bad_here >> pg) & 1u) seen = 0;
+                if ((bad_here >> pair) & 1u) seen = 0;
                 const uint32_t bits = uint32_t(seen >> (32 * half));
+                any |= bits;
                 const int buf = n & 1;
-                bool ok = mbar_await(&ctl.s_full[buf], uint32_t(n >> 1) & 1u, &ctl.abort);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu, mbar_await(&ctl.s_full[buf], uint32_t(n >> 1) & 1u, &ctl.abort)) != 0;
                 float x[32];
                 {
                     uint32_t r[32];
                     tc_fence_after_sync();
-                    tmem_ld_32x32b_x32(lane_addr + kColST + 64u * buf + 32u * half, r);
+                    tmem_ld_32x32b_x32(lane_addr + kColSQ + 64u * buf + 32u * half, r);
                     tmem_ld_wait(r);
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(s_bar + 8u * buf);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]) * c2;
+                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
                 }
-                if (bits != 0xffffffffu) {
+                if (blk == w.blo) {  // the reference: the block's maximum, of both pages
+                    float mx = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (!((bits >> i) & 1u)) x[i] = -INFINITY;
-                }
-                float mx = x[0];
-#pragma unroll
-                for (int i = 1; i < 32; ++i) mx = fmaxf(mx, x[i]);
-                const bool need = mx > m + kRaise;
-                if (soft_or(need || !ok)) {  // raise the running maximum (rare), or give up
-                    ctl.part[part][row] = mx;
-                    // O is at rest behind the previous block's product
-                    ok = ok && (n == 0 || mbar_await(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort));
+                        if ((bits >> i) & 1u) mx = fmaxf(mx, x[i] * c2);
+                    ctl.part[half][row] = mx;
+                    soft_or(false);
+                    mx = fmaxf(ctl.part[0][row], ctl.part[1][row]);
+                    if (half == 0) {
+                        st_cluster_f32(peer_max, mx);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(m_bar);
+                    }
+                    ok = ok && mbar_wait_cluster(&ctl.m_full, uint32_t(seg & 1), &ctl.abort);
                     if (soft_or(!ok)) {
                         failed = true;
                         break;
                     }
-                    const float top = fmaxf(fmaxf(ctl.part[0][row], ctl.part[1][row]),
-                                            fmaxf(ctl.part[2][row], ctl.part[3][row]));
-                    float alpha = 1.f;
-                    if (top > m + kRaise) {
-                        alpha = exp2f(m - top);
-                        m = top;
-                        l *= alpha;
-                    }
-                    if (!fresh) {
-                        tc_fence_after_sync();
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t r[32];
-                            const uint32_t col = kColOT + 128u * half + 32u * c;
-                            tmem_ld_32x32b_x32(lane_addr + col, r);
-                            tmem_ld_wait(r);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-                            tmem_st_x32(lane_addr + col, r);
-                        }
-                        tmem_st_wait();
-                        tc_fence_before_sync();
-                    }
-                    soft_or(false);  // the maxima are read
+                    m = fmaxf(mx, *const_cast<volatile float*>(&ctl.peer[0][row]));
+                    own = m != -INFINITY;
+                    if (!own) m = 0.f;
                 }
                 uint32_t packed[16];
-                const float mr = m == -INFINITY ? 0.f : m;
                 float2 sum = make_float2(0.f, 0.f);
+                const float2 c22 = make_float2(c2, c2), m2 = make_float2(-m, -m);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float p0 = ex2_approx(x[2 * i] - mr), p1 = ex2_approx(x[2 * i + 1] - mr);
+                    const float2 y = fma_f32x2(make_float2(x[2 * i], x[2 * i + 1]), c22, m2);
+                    x[2 * i] = y.x, x[2 * i + 1] = y.y;
+                }
+                if (__any_sync(0xffffffffu, bits != 0xffffffffu)) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!((bits >> i) & 1u)) x[i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float p0 = ex2_approx(x[2 * i]), p1 = ex2_approx(x[2 * i + 1]);
                     sum = add_f32x2(sum, make_float2(p0, p1));
                     const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
                     packed[i] = *reinterpret_cast<const uint32_t*>(&v);
                 }
                 l += sum.x + sum.y;
-                // The previous block's product has read P.
-                if (!__all_sync(0xffffffffu, n == 0 || mbar_await(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort))) {
-                    failed = true;  // (the others' waits end the same way)
+                // The products of the block before the last, of both pairs, have read their weights.
+                if (!__all_sync(0xffffffffu, ok && mbar_await(&ctl.pv_done[buf], (uint32_t(n >> 1) & 1u) ^ 1u, &ctl.abort))) {
+                    failed = true;  // (the others' waits end the same way; the barriers are met by all)
                     if (lane == 0) ctl.abort = 1;
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    *reinterpret_cast<uint4*>(pbuf + (((4 * half + k) ^ (row & 7)) << 4)) =
+                    *reinterpret_cast<uint4*>(pbuf + buf * kSlabQ + (((4 * half + k) ^ (row & 7)) << 4)) =
                         make_uint4(packed[4 * k], packed[4 * k + 1], packed[4 * k + 2], packed[4 * k + 3]);
                 fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(p_bar);
+                // both halves of these 32 rows are there
+                asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
+                if (lane == 0) {
+                    if (half == 0)
+                        bulk_to_cta(r_rows + buf * kSlabQ, s_base + kOffPq + buf * kSlabQ + quad * 4096, 4096u, r_bar + 8u * buf);
+                    mbar_arrive_cluster(p_bar + 8u * buf);
+                }
                 if (w.valid(2 * blk) > 0 && !(bad_here & 1u)) fresh = false;
                 if (w.valid(2 * blk + 1) > 0 && !(bad_here & 2u)) fresh = false;
             }
             // ---- the request's output (or partial)
-            const bool done = !failed && mbar_await(&ctl.pv_done, uint32_t(n & 1) ^ 1u, &ctl.abort);
-            ctl.part[part][row] = l;
+            bool done = !failed && mbar_await(&ctl.pv_done[(n - 1) & 1], uint32_t((n - 1) >> 1) & 1u, &ctl.abort);
+            ctl.part[half][row] = l;
             if (soft_or(!done)) {
                 failed = true;
                 break;
             }
             tc_fence_after_sync();
-            const float sum = (ctl.part[0][row] + ctl.part[1][row]) + (ctl.part[2][row] + ctl.part[3][row]);
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (0: nothing was seen; a NaN goes on to both outputs)
+            float sum = ctl.part[0][row] + ctl.part[1][row];
+            if (half == 0) {
+                st_cluster_f32(peer_sum, sum);
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(l_bar);
+            }
+            done = mbar_wait_cluster(&ctl.l_full, uint32_t(seg & 1), &ctl.abort);
+            if (soft_or(!done)) {  // (and the sums are read)
+                failed = true;
+                break;
+            }
+            ++seg;
+            {   // in one order, so that both pairs have the same sum
+                const float other = *const_cast<volatile float*>(&ctl.peer[1][row]);
+                sum = pair == 0 ? sum + other : other + sum;
+            }
+            if (live_token && (!(sum <= kSumMost) || (!own && any != 0 && !(sum >= kSumLeast)))) flagged = true;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const bool whole = w.blo == 0 && w.bhi == w.nb;
             const int64_t at = whole ? q_row : (int64_t(w.range) * p.tokens + token) * 2 + (w.blo == 0 ? 1 : 0);
-            if (live_token && part == 0)
-                (whole ? p.lse : p.lse_part)[at * kMlaHeads + row] =
+            const int head = row & 63;
+            if (live_token && pair == 0 && half == 0)
+                (whole ? p.lse : p.lse_part)[at * kMlaHeads + head] =
                     sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2T;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -584,7 +855,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
                 } else {
-                    tmem_ld_32x32b_x32(lane_addr + kColOT + 128u * half + 32u * c, o);
+                    tmem_ld_32x32b_x32(lane_addr + kColOQ + 128u * half + 32u * c, o);
                     tmem_ld_wait(o);
                 }
                 if (c == 3) {
@@ -593,7 +864,15 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
                     if (lane == 0) mbar_arrive_remote(o_bar);  // O may be overwritten
                 }
                 if (!live_token) continue;
-                const int64_t d = (at * kMlaHeads + row) * kMlaDv + 256 * half + 128 * pg + 32 * c;
+                const int64_t d = (at * kMlaHeads + head) * kMlaDv + 256 * pair + 128 * half + 32 * c;
+                bool finite = true;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float v = __uint_as_float(o[i]) * inv;
+                    finite = finite && fabsf(v) <= 3.3e38f;
+                    o[i] = __float_as_uint(v);
+                }
+                if (!finite) flagged = true;
                 if (whole) {
                     uint4* out = reinterpret_cast<uint4*>(p.out + d);
 #pragma unroll
@@ -601,22 +880,18 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
                         uint32_t v[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const __nv_bfloat162 b2 =
-                                __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]) * inv,
-                                                      __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]),
+                                                                            __uint_as_float(o[8 * k + 2 * e + 1]));
                             v[e] = *reinterpret_cast<const uint32_t*>(&b2);
                         }
                         out[k] = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 } else {
-                    float4* out = reinterpret_cast<float4*>(p.o_part + d);
+                    uint4* out = reinterpret_cast<uint4*>(p.o_part + d);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        out[k] = make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
-                                             __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
+                    for (int k = 0; k < 8; ++k) out[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 }
             }
-            soft_or(false);  // the sums are read
         }
         if (failed && lane == 0) {
             atomicOr(p.err, kErrWaitTimeout);
@@ -627,61 +902,81 @@ __global__ void __launch_bounds__(kThreadsT, 1) __cluster_dims__(2, 1, 1)
 
     __syncwarp();
     tc_fence_before_sync();
-    cluster_sync_all();  // no CTA leaves while the other may read its memory or arrive on its barriers
+    flagged = __syncthreads_or(flagged) != 0;
+    if (threadIdx.x == 0) p.flags[blockIdx.x] = flagged ? 1 : 0;
+    cluster_sync_all();  // no CTA leaves while another may read its memory or arrive on its barriers
     tc_fence_after_sync();
     if (warp == 8) {
-        if (rank != 0) wait_landed_t(&ctl.all_done, 0);  // the leader's last arrival here
+        wait_landed_t(&ctl.all_done, 0);  // the leaders' last arrivals here
         __syncwarp();
-        tmem2_dealloc(tmem_base, kTmemColsT);
+        tmem2_dealloc(tmem_base, 512);
     }
 }
 
 }  // namespace
 
-cudaError_t mla_tree_pairs(int* pairs) {
+cudaError_t mla_tree_quads(int* quads) {
     static SmemLimitOnce smem_limit;
     static std::atomic<int> resident[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    e = smem_limit.apply(dev, mla_tree_kernel, kSmemT);
+    e = smem_limit.apply(dev, mla_tree_kernel, kSmemQ);
     if (e != cudaSuccess) return e;
-    *pairs = resident[dev].load(std::memory_order_relaxed);
-    if (*pairs > 0) return cudaSuccess;
+    *quads = resident[dev].load(std::memory_order_relaxed);
+    if (*quads > 0) return cudaSuccess;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = 4;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kThreadsT);
-    cfg.dynamicSmemBytes = size_t(kSmemT);
+    cfg.gridDim = dim3(4);
+    cfg.blockDim = dim3(kThreadsQ);
+    cfg.dynamicSmemBytes = size_t(kSmemQ);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(pairs, mla_tree_kernel, &cfg);
+    e = cudaOccupancyMaxActiveClusters(quads, mla_tree_kernel, &cfg);
     if (e != cudaSuccess) return e;
-    if (*pairs < 1) return cudaErrorInvalidConfiguration;
-    resident[dev].store(*pairs, std::memory_order_relaxed);
+    if (*quads < 1) return cudaErrorInvalidConfiguration;
+    if (*quads > kTreeMaxFlags / 4) *quads = kTreeMaxFlags / 4;
+    resident[dev].store(*quads, std::memory_order_relaxed);
     return cudaSuccess;
 }
 
-cudaError_t launch_mla_tree(const MlaTreeMaps& m, const MlaTreeParams& p, int pairs, cudaStream_t stream) {
+int mla_tree_ctas(const MlaTreeParams& p, int quads) {
     const int units = p.ranges * p.tiles;
-    if (p.ranges < 1 || p.ranges > kTreeMaxRanges || units > kTreeMaxRounds * pairs) return cudaErrorInvalidValue;
+    return 4 * (units < quads ? units : quads);
+}
+
+cudaError_t launch_mla_tree(const MlaTreeMaps& m, const MlaTreeParams& p, int quads, cudaStream_t stream) {
+    const int units = p.ranges * p.tiles;
+    if (p.ranges < 1 || p.ranges > kTreeMaxRanges || units > kTreeMaxRounds * quads) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2u * unsigned(units < pairs ? units : pairs));
-    cfg.blockDim = dim3(kThreadsT);
-    cfg.dynamicSmemBytes = size_t(kSmemT);
+    cfg.gridDim = dim3(unsigned(mla_tree_ctas(p, quads)));
+    cfg.blockDim = dim3(kThreadsQ);
+    cfg.dynamicSmemBytes = size_t(kSmemQ);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tree_kernel, m.q, m.kv, m.kr, m.d, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tree_kernel, m.q, m.k, m.v, m.d, p);
     if (e != cudaSuccess) return e;
-    return merge_tree(p, stream);
+    // No request is split where none can have more blocks than are kept together.
+    if (tree_blocks(p.table_width, 1) <= kTreeWholeBlocks) return cudaSuccess;
+    MlaMergeParams mp{};
+    mp.plan = p.plan;
+    mp.cuts = p.cuts;
+    mp.o_part = p.o_part;
+    mp.lse_part = p.lse_part;
+    mp.out = p.out;
+    mp.lse = p.lse;
+    mp.counts = p.counts;
+    mp.tokens = p.tokens;
+    mp.by_cut = p.batch > p.ranges;
+    return launch_mla_merge(mp, p.batch, p.ranges, stream);
 }
 
 }  // namespace dsa

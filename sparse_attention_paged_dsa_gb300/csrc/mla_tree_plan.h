@@ -9,7 +9,7 @@ namespace dsa {
 constexpr int kTreeSegUnits = 2;     // a request's fixed cost in a range (q, first products, output), in blocks
 constexpr int kTreeWholeBlocks = 3;  // requests of at most this many blocks are not split
 constexpr int kTreeMaxRanges = 256;
-constexpr int kTreeMaxFlags = 256;    // CTAs of the larger kernel
+constexpr int kTreeMaxFlags = 256;    // CTAs of a call
 constexpr int kTreeMaxRounds = 8;    // units of a cluster, at most
 constexpr int kTreePlanRounds = 4;   // rounds that are tried for a full device
 
@@ -26,7 +26,8 @@ DSA_PLAN int tree_settled_cut(int cut, int u, int blocks) {
 }
 
 // Tiles of drafted tokens, each a unit in every range.
-DSA_PLAN int tree_tiles(int tokens, int tile_tokens) { return (tokens + tile_tokens - 1) / tile_tokens; }
+constexpr int kTileTokens = 4;
+DSA_PLAN int tree_tiles(int tokens) { return (tokens + kTileTokens - 1) / kTileTokens; }
 
 // Ranges of a call on `clusters` clusters: as many as fill them in few rounds.  A round more is worth it for
 // a twentieth of the device.
