@@ -190,9 +190,10 @@ struct MlaMergeParams {
     const int32_t* counts;     // [batch] tokens of each request, or null: all
     const uint32_t* run;       // 0 there: nothing is to be done (null: there is)
     int32_t tokens;
+    int32_t rows;              // (set by the launch)
     int32_t by_cut;            // rows go by cuts (there are fewer ranges than requests)
 };
-cudaError_t launch_mla_merge(const MlaMergeParams& p, int batch, int ranges, cudaStream_t stream);
+cudaError_t launch_mla_merge(MlaMergeParams p, int batch, int ranges, cudaStream_t stream);
 
 // Latent attention decode for a tree of drafted tokens, on clusters of four CTAs.
 struct MlaTreeParams {
@@ -215,7 +216,8 @@ struct MlaTreeParams {
     int32_t batch;
     int32_t tokens;
     int32_t tiles;             // tree_tiles: of four tokens
-    int32_t ranges;            // tree_ranges
+    int32_t ranges;            // tree_ranges: at most
+    int32_t quads;             // clusters of the device (set by the launch)
     float sm_scale_log2;       // sm_scale * log2(e)
 };
 // 576-wide bf16 rows as (dim in slab, row, slab), boxes of rows x slabs: q 128 x 1; the cache's, k 32 x 3, v 64 x
@@ -225,7 +227,7 @@ struct MlaTreeMaps {
 };
 cudaError_t mla_tree_quads(int* quads);                    // clusters that the current device holds
 int mla_tree_ctas(const MlaTreeParams& p, int quads);      // CTAs of a call
-cudaError_t launch_mla_tree(const MlaTreeMaps& m, const MlaTreeParams& p, int quads, cudaStream_t stream);
+cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cudaStream_t stream);
 
 // Latent attention over ragged prompts, expanded form: per-head 128 + 64 shared key dims, 128 value dims.
 constexpr int kPrefillQk = 192;

@@ -11,24 +11,23 @@
 namespace dsa {
 namespace {
 
+constexpr int kAgainRows = 16;  // rows of CTAs where the call is hardly ever done again
+
 // o[r] = sum_i exp(lse_i - lse) o_i over the partials of a split request, lse = log sum_i exp(lse_i).
 // 512 threads.  128 of them per 512 dims, four heads a CTA; or (kOneHead: few rows, each split many ways)
 // 64 per 256 dims, half a head a CTA, whose partials go to the eight groups in turn.  Grid (heads / 4 or
 // heads x 2, requests or cuts x tokens).
 template <bool kOneHead>
-__global__ void __launch_bounds__(512) mla_merge_kernel(const MlaMergeParams p) {
+__device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at) {
     __shared__ float wgt[kOneHead ? 1 : 4][kMlaMaxGroups];
     __shared__ float4 acc_s[kOneHead ? 7 : 1][64];
-    pdl_wait_prior_grid();
-    pdl_allow_next_grid();
-    if (p.run && *p.run == 0) return;
     const int quarter = threadIdx.x >> (kOneHead ? 6 : 7);
     const int d4 = kOneHead ? (int(blockIdx.x) & 1) * 64 + (threadIdx.x & 63) : threadIdx.x & 127;
     const int h = kOneHead ? int(blockIdx.x) >> 1 : int(blockIdx.x) * 4 + quarter;
-    const int token = int(blockIdx.y) % p.tokens;
-    const int b = p.by_cut ? p.cuts[blockIdx.y / p.tokens] : int(blockIdx.y) / p.tokens;
+    const int token = at % p.tokens;
+    const int b = p.by_cut ? p.cuts[at / p.tokens] : at / p.tokens;
     if (b < 0) return;
-    if (p.counts && token >= __ldg(p.counts + b)) return;  // (a count out of range is held to it: no more tokens than these)
+    if (p.counts && token >= __ldg(p.counts + b)) return;
     const int64_t row = int64_t(b) * p.tokens + token;
     const int2 g = p.plan[b];
     if (g.x == g.y) return;  // one range: written by the attention kernel
@@ -80,18 +79,30 @@ __global__ void __launch_bounds__(512) mla_merge_kernel(const MlaMergeParams p) 
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
+// Rows of CTAs take the rows in turn (each one its own, but where nothing is likely to be done).
+template <bool kOneHead>
+__global__ void __launch_bounds__(512) mla_merge_kernel(const MlaMergeParams p) {
+    pdl_wait_prior_grid();
+    pdl_allow_next_grid();
+    if (p.run && *p.run == 0) return;
+    for (int at = blockIdx.y; at < p.rows; at += gridDim.y) {
+        merge_row<kOneHead>(p, at);
+        __syncthreads();
+    }
+}
+
 }  // namespace
 
-cudaError_t launch_mla_merge(const MlaMergeParams& p, int batch, int ranges, cudaStream_t stream) {
+cudaError_t launch_mla_merge(MlaMergeParams p, int batch, int ranges, cudaStream_t stream) {
     // One row of CTAs per request, or, where they are fewer, per cut between ranges.  Few rows are split
     // many ways: more threads per row read more partials at a time.
-    const int rows = (p.by_cut ? ranges : batch) * p.tokens;
+    const int rows = p.rows = (p.by_cut ? ranges : batch) * p.tokens;
     const bool one_head = rows <= 16;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(one_head ? kMlaHeads * 2 : kMlaHeads / 4, unsigned(rows));
+    cfg.gridDim = dim3(one_head ? kMlaHeads * 2 : kMlaHeads / 4, unsigned(p.run && rows > kAgainRows ? kAgainRows : rows));
     cfg.blockDim = dim3(512);
     cfg.stream = stream;
     cfg.attrs = attr;

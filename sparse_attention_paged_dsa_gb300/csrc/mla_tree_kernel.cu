@@ -55,6 +55,7 @@ struct TreePlan {
     UnitT unit[kTreeMaxRounds];
     int cut[kTreeMaxRounds];     // the request that the range is the second one of, or -1
     int warp_units[16];
+    uint64_t warp_best[16];
 };
 
 __device__ __forceinline__ bool soft_or(bool v) {  // over the 256 softmax threads
@@ -176,7 +177,21 @@ __device__ __forceinline__ int find_units(const MlaTreeParams& p, TreePlan& plan
         if (w < warp) before += plan.warp_units[w];
         total += plan.warp_units[w];
     }
-    const int nranges = max(min(p.ranges, total), 1);
+    // How many ranges: a thread for each number.
+    uint64_t best = ~uint64_t(0);
+    for (int r = int(threadIdx.x) + 1; r <= min(p.ranges, total); r += kThreads) {
+        const uint64_t cost = uint64_t(tree_cost(r, total, p.tiles, p.quads, p.tokens)) << 16 | uint64_t(r);
+        best = cost < best ? cost : best;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t y = __shfl_xor_sync(0xffffffffu, best, o);
+        best = y < best ? y : best;
+    }
+    if (lane == 0) plan.warp_best[warp] = best;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) best = plan.warp_best[w] < best ? plan.warp_best[w] : best;
+    const int nranges = total > 0 ? int(best & 0xFFFF) : 1;
     const int units = nranges * p.tiles;
     const Ranges ranges(nranges, total);
     if (threadIdx.x == 0)  // cuts at the very end lie in no request
@@ -623,10 +638,10 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                             }
                             wait(&ctl.v_full[pg], uint32_t(n & 1));
                             if (s == 0) {
-                                ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.p_own[buf], phase, &ctl.abort));  // (the other CTA's stores)
+                                wait(&ctl.p_own[buf], phase);
                             } else {
                                 wait(&ctl.r_full[buf], phase);
-                                ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.p_other[buf], phase, &ctl.abort));
+                                wait(&ctl.p_other[buf], phase);
                             }
                             tc_fence_after_sync();
                             if (ok && issuer) {
@@ -674,7 +689,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                     if (issuer) mbar_arrive_expect_tx(&ctl.r_full[n & 1], uint32_t(kSlabQ));
                     __syncwarp();
                     ok = __all_sync(0xffffffffu, mbar_await(&ctl.r_full[n & 1], uint32_t(n >> 1) & 1u, &ctl.abort)) != 0;
-                    if (ok && issuer) mbar_arrive_cluster(cluster_addr(&ctl.p_other[n & 1], leader));
+                    if (ok && issuer) mbar_arrive_remote(cluster_addr(&ctl.p_other[n & 1], leader));
                     __syncwarp();
                 }
             }
@@ -692,38 +707,47 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
         const uint32_t peer_max = cluster_addr(ctl.peer[0], peer) + 4 * row, peer_sum = cluster_addr(ctl.peer[1], peer) + 4 * row;
         const uint32_t m_bar = cluster_addr(&ctl.m_full, peer), l_bar = cluster_addr(&ctl.l_full, peer);
         const float c2 = p.sm_scale_log2;
+        const bool out_aligned = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         bool failed = false;
         int n = 0, seg = 0;
-        while (!failed && w.next(p, ctl.plan)) {
-            const int token = 4 * w.tile + 2 * side + (row >> 6);
+        int q_seg = 0;
+        // The last slabs of the current request's q, once the products of the one before have read theirs: 128
+        // dims a thread.
+        const auto load_q = [&] {
+            const bool ok = mbar_await(&ctl.q_empty, uint32_t(q_seg & 1) ^ 1u, &ctl.abort);
+            ++q_seg;
+            if (!__all_sync(0xffffffffu, ok)) {
+                failed = true;  // (all warps meet at the next barrier)
+                if (lane == 0) ctl.abort = 1;
+            }
+            const int token = min(kTileTokens * w.tile + 2 * side + (row >> 6), p.tokens - 1);
+            const uint4* q = reinterpret_cast<const uint4*>(
+                p.q + ((int64_t(w.req()) * p.tokens + token) * kMlaHeads + (row & 63)) * kMlaDim + 64 * kSlabsSm +
+                32 * kSlabsTm * half);
+            tc_fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < kSlabsTm; ++c) {
+                uint32_t r[16];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 v = __ldg(q + 4 * c + k);
+                    r[4 * k] = v.x, r[4 * k + 1] = v.y, r[4 * k + 2] = v.z, r[4 * k + 3] = v.w;
+                }
+                tmem_st_x16(lane_addr + kColQQ + 16u * kSlabsTm * half + 16u * c, r);
+            }
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(qt_bar);
+        };
+        bool more = w.next(p, ctl.plan);
+        if (more) load_q();
+        while (more && !failed) {
+            const int token = kTileTokens * w.tile + 2 * side + (row >> 6);
             const bool live_token = token < w.drafted;
             const int64_t q_row = int64_t(w.req()) * p.tokens + min(token, p.tokens - 1);
             const uint64_t drafts = __ldg(p.mask + q_row) & low_bits(w.drafted);
-            // The last slabs of q, once the products of the request before have read them: 128 dims a thread.
-            bool ok = mbar_await(&ctl.q_empty, uint32_t(seg & 1) ^ 1u, &ctl.abort);
-            if (!__all_sync(0xffffffffu, ok)) {
-                failed = true;  // (met by all warps at the next barrier)
-                if (lane == 0) ctl.abort = 1;
-            }
-            {
-                const uint4* q = reinterpret_cast<const uint4*>(p.q + (q_row * kMlaHeads + (row & 63)) * kMlaDim +
-                                                                64 * kSlabsSm + 32 * kSlabsTm * half);
-                tc_fence_after_sync();
-#pragma unroll
-                for (int c = 0; c < kSlabsTm; ++c) {
-                    uint32_t r[16];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint4 v = __ldg(q + 4 * c + k);
-                        r[4 * k] = v.x, r[4 * k + 1] = v.y, r[4 * k + 2] = v.z, r[4 * k + 3] = v.w;
-                    }
-                    tmem_st_x16(lane_addr + kColQQ + 16u * kSlabsTm * half + 16u * c, r);
-                }
-                tmem_st_wait();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(qt_bar);
-            }
+            bool ok = true;
             float m = 0.f, l = 0.f;
             bool own = true;    // the reference is a score of the row's
             uint32_t any = 0;   // entries seen
@@ -806,35 +830,42 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                     *reinterpret_cast<uint4*>(pbuf + buf * kSlabQ + (((4 * half + k) ^ (row & 7)) << 4)) =
                         make_uint4(packed[4 * k], packed[4 * k + 1], packed[4 * k + 2], packed[4 * k + 3]);
                 fence_proxy_async_smem();
-                // both halves of these 32 rows are there
+                // Both halves of these 32 rows are there, for the async proxy too: the products and the copy read them in
+                // this SM, behind each writer's fence.  (No thread of another CTA does: the arrivals need no
+                // cluster-scope release, which took 1,900 cycles here and bound the loop: 1662 us for 16 x 32
+                // tokens at 128K context.)
                 asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
                 if (lane == 0) {
                     if (half == 0)
                         bulk_to_cta(r_rows + buf * kSlabQ, s_base + kOffPq + buf * kSlabQ + quad * 4096, 4096u, r_bar + 8u * buf);
-                    mbar_arrive_cluster(p_bar + 8u * buf);
+                    mbar_arrive_remote(p_bar + 8u * buf);
                 }
                 if (w.valid(2 * blk) > 0 && !(bad_here & 1u)) fresh = false;
                 if (w.valid(2 * blk + 1) > 0 && !(bad_here & 2u)) fresh = false;
             }
             // ---- the request's output (or partial)
-            bool done = !failed && mbar_await(&ctl.pv_done[(n - 1) & 1], uint32_t((n - 1) >> 1) & 1u, &ctl.abort);
             ctl.part[half][row] = l;
-            if (soft_or(!done)) {
+            if (soft_or(failed)) {
                 failed = true;
                 break;
             }
-            tc_fence_after_sync();
             float sum = ctl.part[0][row] + ctl.part[1][row];
             if (half == 0) {
                 st_cluster_f32(peer_sum, sum);
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(l_bar);
             }
-            done = mbar_wait_cluster(&ctl.l_full, uint32_t(seg & 1), &ctl.abort);
-            if (soft_or(!done)) {  // (and the sums are read)
+            const bool whole = w.blo == 0 && w.bhi == w.nb;
+            const int64_t at = whole ? q_row : (int64_t(w.range) * p.tokens + token) * 2 + (w.blo == 0 ? 1 : 0);
+            more = w.next(p, ctl.plan);
+            if (more) load_q();  // the next one's first scores run beside this one's last products
+            bool done = mbar_await(&ctl.pv_done[(n - 1) & 1], uint32_t((n - 1) >> 1) & 1u, &ctl.abort);
+            done = done && mbar_wait_cluster(&ctl.l_full, uint32_t(seg & 1), &ctl.abort);
+            if (soft_or(!done || failed)) {  // (and the sums are read)
                 failed = true;
                 break;
             }
+            tc_fence_after_sync();
             ++seg;
             {   // in one order, so that both pairs have the same sum
                 const float other = *const_cast<volatile float*>(&ctl.peer[1][row]);
@@ -842,8 +873,6 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
             }
             if (live_token && (!(sum <= kSumMost) || (!own && any != 0 && !(sum >= kSumLeast)))) flagged = true;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const bool whole = w.blo == 0 && w.bhi == w.nb;
-            const int64_t at = whole ? q_row : (int64_t(w.range) * p.tokens + token) * 2 + (w.blo == 0 ? 1 : 0);
             const int head = row & 63;
             if (live_token && pair == 0 && half == 0)
                 (whole ? p.lse : p.lse_part)[at * kMlaHeads + head] =
@@ -873,23 +902,32 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                     o[i] = __float_as_uint(v);
                 }
                 if (!finite) flagged = true;
-                if (whole) {
-                    uint4* out = reinterpret_cast<uint4*>(p.out + d);
+                if (whole) {  // a whole sector a lane, where it starts on one
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t v[4];
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t v[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]),
-                                                                            __uint_as_float(o[8 * k + 2 * e + 1]));
+                        for (int e = 0; e < 8; ++e) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[16 * k + 2 * e]),
+                                                                            __uint_as_float(o[16 * k + 2 * e + 1]));
                             v[e] = *reinterpret_cast<const uint32_t*>(&b2);
                         }
-                        out[k] = make_uint4(v[0], v[1], v[2], v[3]);
+                        __nv_bfloat16_raw* out = p.out + d + 16 * k;
+                        if (out_aligned) {
+                            st_global_v8(out, v);
+                        } else {
+                            reinterpret_cast<uint4*>(out)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+                            reinterpret_cast<uint4*>(out)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+                        }
                     }
                 } else {
-                    uint4* out = reinterpret_cast<uint4*>(p.o_part + d);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) out[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = o[8 * k + e];
+                        st_global_v8(p.o_part + d + 8 * k, v);
+                    }
                 }
             }
         }
@@ -949,7 +987,8 @@ int mla_tree_ctas(const MlaTreeParams& p, int quads) {
     return 4 * (units < quads ? units : quads);
 }
 
-cudaError_t launch_mla_tree(const MlaTreeMaps& m, const MlaTreeParams& p, int quads, cudaStream_t stream) {
+cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cudaStream_t stream) {
+    p.quads = quads;
     const int units = p.ranges * p.tiles;
     if (p.ranges < 1 || p.ranges > kTreeMaxRanges || units > kTreeMaxRounds * quads) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];

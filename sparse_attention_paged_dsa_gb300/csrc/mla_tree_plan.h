@@ -29,8 +29,8 @@ DSA_PLAN int tree_settled_cut(int cut, int u, int blocks) {
 constexpr int kTileTokens = 4;
 DSA_PLAN int tree_tiles(int tokens) { return (tokens + kTileTokens - 1) / kTileTokens; }
 
-// Ranges of a call on `clusters` clusters: as many as fill them in few rounds.  A round more is worth it for
-// a twentieth of the device.
+// The most ranges of a call on `clusters` clusters: as many as fill them in few rounds.  A round more is worth
+// it for a twentieth of the device.
 DSA_PLAN int tree_ranges(int tiles, int clusters) {
     int best = 1, best_rounds = 0, best_units = 0;  // units: of best_rounds * clusters places
     for (int k = 1; k <= kTreePlanRounds; ++k) {
@@ -42,6 +42,14 @@ DSA_PLAN int tree_ranges(int tiles, int clusters) {
             best = r, best_rounds = k, best_units = r * tiles;
     }
     return best;
+}
+
+// What `ranges` of `total` plan units cost, in sixteenths of a block: the units that a cluster does one after
+// another, each with its own start and end, and the partial outputs that the merge reads.
+constexpr int kTreeUnitCost = 32, kTreeMergeCost = 48;
+DSA_PLAN long long tree_cost(int ranges, int total, int tiles, int clusters, int tokens) {
+    const long long rounds = (ranges * tiles + clusters - 1) / clusters, each = (total + ranges - 1) / ranges;
+    return rounds * (16 * each + kTreeUnitCost) + (ranges > 1 ? kTreeMergeCost + ranges * tokens / 4 : 0);
 }
 
 }  // namespace dsa
