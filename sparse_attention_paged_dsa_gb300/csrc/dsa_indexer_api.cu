@@ -369,6 +369,8 @@ size_t dense_workspace_bytes(int groups, int32_t next_n) {
 
 constexpr int kTicketWord = 32;  // of the workspace header: the page update's, 0 between calls
 
+constexpr int64_t kTreeWork = int64_t(1) << 19;
+
 // Tree decode: header, cuts, plan, flags, then two partial outputs per range and token.  Two kernels share it
 // (the second one works where the first has not, or again): their plans lie apart, their partials do not.
 struct TreeShape {
@@ -953,7 +955,7 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
     p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
     p.mask = tree_mask;
     p.counts = token_counts_opt;
-    if (tokens > 2 && max_context > 2048 && shape.ranges * shape.tiles <= dsa::kTreeMaxRounds * quads) {
+    if (tokens > 2 && int64_t(batch) * tokens * max_context > kTreeWork && shape.ranges * shape.tiles <= dsa::kTreeMaxRounds * quads) {
         dsa::MlaTreeParams t{};
         t.q = static_cast<const __nv_bfloat16_raw*>(q);
         t.page_table = page_table;

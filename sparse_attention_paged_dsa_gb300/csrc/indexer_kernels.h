@@ -191,6 +191,7 @@ struct MlaMergeParams {
     const uint32_t* run;       // 0 there: nothing is to be done (null: there is)
     int32_t tokens;
     int32_t rows;              // (set by the launch)
+    int32_t many;              // ranges per request from which on one is split many ways
     int32_t by_cut;            // rows go by cuts (there are fewer ranges than requests)
 };
 cudaError_t launch_mla_merge(MlaMergeParams p, int batch, int ranges, cudaStream_t stream);

@@ -11,6 +11,7 @@
 namespace dsa {
 namespace {
 
+constexpr int kEarly = 4;
 constexpr int kAgainRows = 16;  // rows of CTAs where the call is hardly ever done again
 
 // o[r] = sum_i exp(lse_i - lse) o_i over the partials of a split request, lse = log sum_i exp(lse_i).
@@ -34,6 +35,16 @@ __device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at) {
     const int S = g.y - g.x + 1;
     // partial i: range g.x + i; the first one ends in the next range, the others began earlier
     const auto part = [&](int i) { return (int64_t(g.x + i) * p.tokens + token) * 2 + (i == 0 ? 1 : 0); };
+    // The first partials are on their way while the weights are made.
+    const auto value = [&](int i) {
+        return *reinterpret_cast<const float4*>(p.o_part + (part(i) * kMlaHeads + h) * kMlaDv + 4 * d4);
+    };
+    constexpr int kStep = kOneHead ? 8 : 1;
+    const int first = kOneHead ? quarter : 0;
+    float4 early[kEarly];
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k)
+        if (first + k * kStep < S) early[k] = value(first + k * kStep);
     if ((threadIdx.x & 127) < 32 && (!kOneHead || quarter == 0)) {
         float* const w = wgt[kOneHead ? 0 : quarter];
         const int lane = threadIdx.x & 31;
@@ -58,12 +69,15 @@ __device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at) {
     __syncthreads();
     const float* const w = wgt[kOneHead ? 0 : quarter];
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = kOneHead ? quarter : 0; i < S; i += kOneHead ? 8 : 1) {
-        const float4 v = *reinterpret_cast<const float4*>(p.o_part + (part(i) * kMlaHeads + h) * kMlaDv + 4 * d4);
+    const auto add = [&](int i, const float4& v) {
         acc.x = fmaf(w[i], v.x, acc.x), acc.y = fmaf(w[i], v.y, acc.y);
         acc.z = fmaf(w[i], v.z, acc.z), acc.w = fmaf(w[i], v.w, acc.w);
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k)
+        if (first + k * kStep < S) add(first + k * kStep, early[k]);
+#pragma unroll 8
+    for (int i = first + kEarly * kStep; i < S; i += kStep) add(i, value(i));
     if constexpr (kOneHead) {
         if (quarter > 0) acc_s[quarter - 1][threadIdx.x & 63] = acc;
         __syncthreads();
@@ -94,10 +108,10 @@ __global__ void __launch_bounds__(512) mla_merge_kernel(const MlaMergeParams p) 
 }  // namespace
 
 cudaError_t launch_mla_merge(MlaMergeParams p, int batch, int ranges, cudaStream_t stream) {
-    // One row of CTAs per request, or, where they are fewer, per cut between ranges.  Few rows are split
+    // One row of CTAs per request, or, where they are fewer, per cut between ranges.  Few rows that are split
     // many ways: more threads per row read more partials at a time.
     const int rows = p.rows = (p.by_cut ? ranges : batch) * p.tokens;
-    const bool one_head = rows <= 16;
+    const bool one_head = rows <= 16 && ranges >= p.many * batch;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

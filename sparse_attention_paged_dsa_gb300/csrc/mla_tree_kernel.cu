@@ -1015,6 +1015,7 @@ cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cu
     mp.counts = p.counts;
     mp.tokens = p.tokens;
     mp.by_cut = p.batch > p.ranges;
+    mp.many = 32;
     return launch_mla_merge(mp, p.batch, p.ranges, stream);
 }
 

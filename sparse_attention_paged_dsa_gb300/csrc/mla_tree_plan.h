@@ -6,7 +6,7 @@
 
 namespace dsa {
 
-constexpr int kTreeSegUnits = 2;     // a request's fixed cost in a range (q, first products, output), in blocks
+constexpr int kTreeSegUnits = 4;     // a request's fixed cost in a range (q, first products, output), in blocks
 constexpr int kTreeWholeBlocks = 3;  // requests of at most this many blocks are not split
 constexpr int kTreeMaxRanges = 256;
 constexpr int kTreeMaxFlags = 256;    // CTAs of a call
@@ -46,10 +46,10 @@ DSA_PLAN int tree_ranges(int tiles, int clusters) {
 
 // What `ranges` of `total` plan units cost, in sixteenths of a block: the units that a cluster does one after
 // another, each with its own start and end, and the partial outputs that the merge reads.
-constexpr int kTreeUnitCost = 32, kTreeMergeCost = 48;
+constexpr int kTreeUnitCost = 96, kTreeMergeCost = 64;
 DSA_PLAN long long tree_cost(int ranges, int total, int tiles, int clusters, int tokens) {
     const long long rounds = (ranges * tiles + clusters - 1) / clusters, each = (total + ranges - 1) / ranges;
-    return rounds * (16 * each + kTreeUnitCost) + (ranges > 1 ? kTreeMergeCost + ranges * tokens / 4 : 0);
+    return rounds * (16 * each + kTreeUnitCost) + (ranges > 1 ? kTreeMergeCost + ranges * tokens * 3 / 4 : 0);
 }
 
 }  // namespace dsa
