@@ -983,6 +983,7 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
         if (st == DSA_OK) st = make_slabs_map(&m.k, kv_cache, kv_rows, 3, "mla kv", 32);
         if (st == DSA_OK) st = make_slabs_map(&m.v, kv_cache, kv_rows, 2, "mla kv");
         if (st == DSA_OK) st = make_drafts_map(&m.d, draft_kv, batch, tokens, 32);
+        if (st == DSA_OK) st = make_rows_map(&m.o, out, q_rows, DSA_MLA_DV, 64, "mla out");
         if (st != DSA_OK) return st;
         e = dsa::launch_mla_tree(m, t, quads, cs);
         if (e != cudaSuccess) return cuda_fail(e, "MLA tree decode launch");

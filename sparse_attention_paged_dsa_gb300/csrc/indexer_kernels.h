@@ -193,7 +193,12 @@ struct MlaMergeParams {
     int32_t rows;              // (set by the launch)
     int32_t many;              // ranges per request from which on one is split many ways
     int32_t by_cut;            // rows go by cuts (there are fewer ranges than requests)
+    int32_t tiled;             // the partials lie as tiled_part says, not row by row
 };
+// Where a dim (a multiple of 4) of a head lies in a tiled partial: eight dims of all 64 heads after one another.
+__host__ __device__ inline int64_t tiled_part(int64_t part, int head, int dim) {
+    return ((part * (kMlaDv / 8) + dim / 8) * kMlaHeads + head) * 8 + dim % 8;
+}
 cudaError_t launch_mla_merge(MlaMergeParams p, int batch, int ranges, cudaStream_t stream);
 
 // Latent attention decode for a tree of drafted tokens, on clusters of four CTAs.
@@ -222,9 +227,10 @@ struct MlaTreeParams {
     float sm_scale_log2;       // sm_scale * log2(e)
 };
 // 576-wide bf16 rows as (dim in slab, row, slab), boxes of rows x slabs: q 128 x 1; the cache's, k 32 x 3, v 64 x
-// 2; the drafted entries as (dim in slab, token, slab, request), d 32 tokens x 1.  All 128-byte-swizzled.
+// 2; the drafted entries as (dim in slab, token, slab, request), d 32 tokens x 1; o, out as [batch * tokens * 64, 512] rows, boxes of
+// 64 x 64.  All 128-byte-swizzled.
 struct MlaTreeMaps {
-    CUtensorMap q, k, v, d;
+    CUtensorMap q, k, v, d, o;
 };
 cudaError_t mla_tree_quads(int* quads);                    // clusters that the current device holds
 int mla_tree_ctas(const MlaTreeParams& p, int quads);      // CTAs of a call

@@ -160,14 +160,6 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t 
                  : "memory");
 }
 
-// Tiled store of a box at (x, y), tracked by this thread's bulk-async group.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(src)
-                 : "memory");
-}
-
 // Rows [row, row + 64) of the map's slabs [slab, ...) (a (dim in slab, row, slab) view of 576-wide rows)
 // into consecutive 64 x 64 slabs.
 __device__ __forceinline__ void tma_load_slabs(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t row,

@@ -18,7 +18,7 @@ constexpr int kAgainRows = 16;  // rows of CTAs where the call is hardly ever do
 // 512 threads.  128 of them per 512 dims, four heads a CTA; or (kOneHead: few rows, each split many ways)
 // 64 per 256 dims, half a head a CTA, whose partials go to the eight groups in turn.  Grid (heads / 4 or
 // heads x 2, requests or cuts x tokens).
-template <bool kOneHead>
+template <bool kOneHead, bool kTiled>
 __device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at) {
     __shared__ float wgt[kOneHead ? 1 : 4][kMlaMaxGroups];
     __shared__ float4 acc_s[kOneHead ? 7 : 1][64];
@@ -37,7 +37,8 @@ __device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at) {
     const auto part = [&](int i) { return (int64_t(g.x + i) * p.tokens + token) * 2 + (i == 0 ? 1 : 0); };
     // The first partials are on their way while the weights are made.
     const auto value = [&](int i) {
-        return *reinterpret_cast<const float4*>(p.o_part + (part(i) * kMlaHeads + h) * kMlaDv + 4 * d4);
+        return *reinterpret_cast<const float4*>(p.o_part + (kTiled ? tiled_part(part(i), h, 4 * d4)
+                                                                   : (part(i) * kMlaHeads + h) * kMlaDv + 4 * d4));
     };
     constexpr int kStep = kOneHead ? 8 : 1;
     const int first = kOneHead ? quarter : 0;
@@ -94,13 +95,13 @@ __device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at) {
 }
 
 // Rows of CTAs take the rows in turn (each one its own, but where nothing is likely to be done).
-template <bool kOneHead>
+template <bool kOneHead, bool kTiled>
 __global__ void __launch_bounds__(512) mla_merge_kernel(const MlaMergeParams p) {
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
     if (p.run && *p.run == 0) return;
     for (int at = blockIdx.y; at < p.rows; at += gridDim.y) {
-        merge_row<kOneHead>(p, at);
+        merge_row<kOneHead, kTiled>(p, at);
         __syncthreads();
     }
 }
@@ -121,8 +122,11 @@ cudaError_t launch_mla_merge(MlaMergeParams p, int batch, int ranges, cudaStream
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return one_head ? cudaLaunchKernelEx(&cfg, mla_merge_kernel<true>, p)
-                    : cudaLaunchKernelEx(&cfg, mla_merge_kernel<false>, p);
+    if (p.tiled)
+        return one_head ? cudaLaunchKernelEx(&cfg, mla_merge_kernel<true, true>, p)
+                        : cudaLaunchKernelEx(&cfg, mla_merge_kernel<false, true>, p);
+    return one_head ? cudaLaunchKernelEx(&cfg, mla_merge_kernel<true, false>, p)
+                    : cudaLaunchKernelEx(&cfg, mla_merge_kernel<false, false>, p);
 }
 
 }  // namespace dsa

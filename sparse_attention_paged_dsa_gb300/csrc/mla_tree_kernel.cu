@@ -40,7 +40,7 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreadsQ = 416;
+constexpr int kThreadsQ = 384;  // (twelve warps: a thirteenth would leave the softmax 128 registers)
 constexpr int kPg = kPageEntries;      // entries of a page, heads of a token
 constexpr int kSoftWarps = 8;
 constexpr float kLn2T = 0.69314718055994531f;
@@ -291,8 +291,11 @@ __device__ __forceinline__ void bulk_to_cta(uint32_t dst, uint32_t src, uint32_t
                  "r"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Store to another CTA's shared memory, counted (four bytes) on a barrier there: no release to wait for.
+__device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(addr), "f"(v),
+                 "r"(bar)
+                 : "memory");
 }
 
 // 32 rows of one slab of a request's drafted entries (rows behind the last arrive as zeros).
@@ -305,10 +308,34 @@ __device__ __forceinline__ void load_drafts(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// Zeroes the value rows of a page (in buffer pg) that nobody sees, up to the last 16-entry step of the product:
+// their weights are 0, but 0 x NaN is not.  By a whole warp, once the page has landed.  Out of line: the loops of
+// the roles run side by side and share an instruction cache.
+__device__ __noinline__ void zero_unseen(const uint64_t* masks, int drafted, int valid, uint8_t* v) {
+    const int lane = threadIdx.x & 31;
+    uint64_t used = low_bits(valid);
+    if (masks) {  // the drafted page: what some token sees
+        uint64_t any = 0;
+        for (int j = lane; j < drafted; j += 32) any |= __ldg(masks + j);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) any |= __shfl_xor_sync(0xffffffffu, any, o);
+        used &= any;
+    }
+    const int rows = (valid + 15) & ~15;
+#pragma unroll 1
+    for (int c = lane; c < rows * 8; c += 32) {
+        if ((used >> (c >> 3)) & 1u) continue;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) *reinterpret_cast<uint4*>(v + s * kSlabV + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
     mla_tree_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                          const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap d_map,
-                         const MlaTreeParams p) {
+                         const __grid_constant__ CUtensorMap o_map, const MlaTreeParams p) {
     extern __shared__ uint8_t smem_raw[];  // at the same offset in all CTAs; on a 1,024-byte boundary, checked below
     uint8_t* tiles = smem_raw;
     QuadCtl& ctl = *reinterpret_cast<QuadCtl*>(tiles + kOffCtlQ);
@@ -334,7 +361,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
             mbar_init(&ctl.v_full[i], 1);
             mbar_init(&ctl.v_empty[i], 1);
             mbar_init(&ctl.vz_full[i], 1);
-            mbar_init(&ctl.vz_ready[i], 2);  // one arrival of each CTA of the pair
+            mbar_init(&ctl.vz_ready[i], 1);  // the leader's: of the other CTA
             mbar_init(&ctl.s_full[i], 1);
             mbar_init(&ctl.p_own[i], 2 * kSoftWarps);
             mbar_init(&ctl.p_other[i], 1);   // the other CTA of the pair has its part
@@ -347,8 +374,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
         mbar_init(&ctl.qt_full, 2 * kSoftWarps);
         mbar_init(&ctl.o_empty, 2 * kSoftWarps);
         mbar_init(&ctl.all_done, 4);         // of both pairs' two issuing warps
-        mbar_init(&ctl.m_full, kSoftWarps / 2);
-        mbar_init(&ctl.l_full, kSoftWarps / 2);
+        mbar_init(&ctl.m_full, 1);
+        mbar_init(&ctl.l_full, 1);
         ctl.abort = 0;
         clear_plan(p, ctl.plan);
         fence_mbar_init();
@@ -387,12 +414,21 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
         while (ok && w.next(p, ctl.plan)) {
             int id_l = tree_page_of_lane(p, w, 2 * w.blo, lane);
             if (id_l == -1 && 2 * w.blo + lane < 2 * w.bhi) atomicOr(p.err, kErrBadPage);
+            const int row = (w.req() * p.tokens + 4 * w.tile + 2 * side) * kMlaHeads;
+            if (issuer) {  // into L2, the slabs that the softmax warps read too
+#pragma unroll 1
+                for (int s = 0; s < kSlabsQ; ++s)
+                    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                                     reinterpret_cast<uint64_t>(&q_map)),
+                                 "r"(0), "r"(row), "r"(s)
+                                 : "memory");
+            }
+            __syncwarp();
             if (!wait(&ctl.q_empty, uint32_t(seg & 1) ^ 1u)) break;
             if (issuer) {
                 const uint32_t bar = cluster_addr(&ctl.q_full, leader);
                 if (side == 0) mbar_arrive_expect_tx(&ctl.q_full, uint32_t(2 * kSlabsSm * kSlabQ));
                 // (rows behind the request's tokens are others' or zeros, and are not written)
-                const int row = (w.req() * p.tokens + 4 * w.tile + 2 * side) * kMlaHeads;
 #pragma unroll
                 for (int s = 0; s < kSlabsSm; ++s) tma2_load_3d(sb + kOffQq + s * kSlabQ, &q_map, bar, 0, row, s, pol_q);
             }
@@ -513,42 +549,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 11) {
-        // ================= value rows that nobody sees =================
-        bool ok = true;
-        uint32_t phase = 0;  // bit pg
-        while (ok && w.next(p, ctl.plan)) {
-            for (int page = max(w.np - 1, 0); page <= w.np && ok; ++page) {
-                if (page < 2 * w.blo || page >= 2 * w.bhi || !w.zeroes(page)) continue;
-                uint64_t used = low_bits(w.valid(page));
-                if (page == w.np) {
-                    uint64_t any = 0;
-                    for (int j = lane; j < w.drafted; j += 32) any |= __ldg(p.mask + int64_t(w.req()) * p.tokens + j);
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) any |= __shfl_xor_sync(0xffffffffu, any, o);
-                    used &= any;
-                } else if (tree_page_of_lane(p, w, page, 0) == -1) {
-                    continue;  // page 0 stands in: no product reads it
-                }
-                const int pg = page & 1;
-                ok = __all_sync(0xffffffffu, mbar_await(&ctl.vz_full[pg], (phase >> pg) & 1u, &ctl.abort)) != 0;
-                phase ^= 1u << pg;
-                if (!ok) break;
-                const int rows = (w.valid(page) + 15) & ~15;
-                for (int c = lane; c < rows * 8; c += 32) {
-                    const int r = c >> 3;
-                    if ((used >> r) & 1u) continue;
-                    uint8_t* v = tiles + kOffVq + pg * kGroupQ + r * 128 + (c & 7) * 16;
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) *reinterpret_cast<uint4*>(v + s * kSlabV) = make_uint4(0, 0, 0, 0);
-                }
-                asm volatile("fence.proxy.async;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&ctl.vz_ready[pg], leader));
-            }
-        }
-        __syncwarp();
-    } else if (warp == 8 || (warp == 12 && side == 0)) {
+    } else if (warp == 8 || warp == 11) {
         // ================= MMA (the pairs' leaders'), scores =================
         // In a warp of their own: one that issued both products was late with every one of them (4,650
         // cycles a block, of them 2,000 in barriers that were complete).
@@ -625,15 +626,17 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                         if (issuer) mbar_arrive_expect_tx(&ctl.r_full[buf], uint32_t(kSlabQ));
                         __syncwarp();
                         if (i == 0) wait(&ctl.o_empty, uint32_t(seg & 1) ^ 1u);
-#pragma unroll
+#pragma unroll 1
                         for (int s = 0; s < 2; ++s) {  // the own page, then the other
                             const int pg = s ^ pair;
                             const int page = 2 * (w.blo + i) + pg;
                             const bool good = !((bad >> (2 * (i & 15) + pg)) & 1u);
                             const int steps = good ? uniform((w.valid(page) + 15) >> 4) : 0;
                             if (good && w.zeroes(page)) {
-                                ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u,
-                                                                                     &ctl.abort));
+                                wait(&ctl.vz_full[pg], (zero_phase >> pg) & 1u);
+                                zero_unseen(page == w.np ? p.mask + int64_t(w.req()) * p.tokens : nullptr, w.drafted, w.valid(page),
+                                            tiles + kOffVq + pg * kGroupQ);
+                                wait(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u);  // (as p_own: nobody here reads those rows)
                                 zero_phase ^= 1u << pg;
                             }
                             wait(&ctl.v_full[pg], uint32_t(n & 1));
@@ -677,18 +680,36 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                 commit_to(&ctl.all_done, uint16_t(15));  // every MMA this thread issued has completed when this arrives
             }
             __syncwarp();
-        } else {
-            // ---- the other CTA's: tells the leader of the weights that have come here
+        } else if (warp == 11) {
+            // ---- the other CTA's: zeroes its value rows that nobody sees, and tells the leader of that and of
+            // the weights that have come here
             const bool issuer = elect_one();
             bool ok = true;
+            const auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort));
+                return ok;
+            };
             int n = 0;
+            uint32_t zero_phase = 0, bad = 0;
             while (ok && w.next(p, ctl.plan)) {
                 const int blocks = uniform(w.bhi - w.blo);
 #pragma unroll 1
                 for (int i = 0; i < blocks && ok; ++i, ++n) {
+                    if ((i & 15) == 0)
+                        bad = __ballot_sync(0xffffffffu, tree_page_of_lane(p, w, 2 * (w.blo + i), lane) == -1);
                     if (issuer) mbar_arrive_expect_tx(&ctl.r_full[n & 1], uint32_t(kSlabQ));
                     __syncwarp();
-                    ok = __all_sync(0xffffffffu, mbar_await(&ctl.r_full[n & 1], uint32_t(n >> 1) & 1u, &ctl.abort)) != 0;
+#pragma unroll 1
+                    for (int s = 0; s < 2; ++s) {
+                        const int pg = s ^ pair, page = 2 * (w.blo + i) + pg;
+                        if (((bad >> (2 * (i & 15) + pg)) & 1u) || !w.zeroes(page)) continue;
+                        if (!wait(&ctl.vz_full[pg], (zero_phase >> pg) & 1u)) break;
+                        zero_phase ^= 1u << pg;
+                        zero_unseen(page == w.np ? p.mask + int64_t(w.req()) * p.tokens : nullptr, w.drafted, w.valid(page),
+                                            tiles + kOffVq + pg * kGroupQ);
+                        if (issuer) mbar_arrive_remote(cluster_addr(&ctl.vz_ready[pg], leader));
+                    }
+                    wait(&ctl.r_full[n & 1], uint32_t(n >> 1) & 1u);
                     if (ok && issuer) mbar_arrive_remote(cluster_addr(&ctl.p_other[n & 1], leader));
                     __syncwarp();
                 }
@@ -707,51 +728,168 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
         const uint32_t peer_max = cluster_addr(ctl.peer[0], peer) + 4 * row, peer_sum = cluster_addr(ctl.peer[1], peer) + 4 * row;
         const uint32_t m_bar = cluster_addr(&ctl.m_full, peer), l_bar = cluster_addr(&ctl.l_full, peer);
         const float c2 = p.sm_scale_log2;
-        const bool out_aligned = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+        const bool q_aligned = (reinterpret_cast<uintptr_t>(p.q) & 31) == 0;
         bool failed = false;
         int n = 0, seg = 0;
+        // One request after another; its start is under the last products of the one before, and the code is there
+        // once: the roles' loops share an instruction cache, and 0.25 of the time went to it when they passed it.
+        bool more = w.next(p, ctl.plan), had = false;
         int q_seg = 0;
-        // The last slabs of the current request's q, once the products of the one before have read theirs: 128
-        // dims a thread.
-        const auto load_q = [&] {
-            const bool ok = mbar_await(&ctl.q_empty, uint32_t(q_seg & 1) ^ 1u, &ctl.abort);
-            ++q_seg;
-            if (!__all_sync(0xffffffffu, ok)) {
-                failed = true;  // (all warps meet at the next barrier)
-                if (lane == 0) ctl.abort = 1;
+        // of the request before: its sums, where its outputs go, and what is known of them
+        float m = 0.f, l = 0.f;
+        bool own = true, fresh = true, live_token = false, whole = false;
+        uint32_t any = 0;
+        int64_t at = 0, first_row = 0;
+        int tokens_here = 0;
+        while (true) {
+            float sum = 0.f;
+            if (had) {
+                ctl.part[half][row] = l;
+                if (soft_or(failed)) break;
+                sum = ctl.part[0][row] + ctl.part[1][row];
+                if (half == 0) st_async_f32(peer_sum, sum, l_bar);
             }
-            const int token = min(kTileTokens * w.tile + 2 * side + (row >> 6), p.tokens - 1);
-            const uint4* q = reinterpret_cast<const uint4*>(
-                p.q + ((int64_t(w.req()) * p.tokens + token) * kMlaHeads + (row & 63)) * kMlaDim + 64 * kSlabsSm +
-                32 * kSlabsTm * half);
-            tc_fence_after_sync();
+            // The last slabs of q, 128 dims a thread: fetched here, ...
+            uint32_t q_regs[kSlabsTm][16];
+            if (more) {
+                const int token = min(kTileTokens * w.tile + 2 * side + (row >> 6), p.tokens - 1);
+                const __nv_bfloat16_raw* q =
+                    p.q + ((int64_t(w.req()) * p.tokens + token) * kMlaHeads + (row & 63)) * kMlaDim + 64 * kSlabsSm +
+                    32 * kSlabsTm * half;
+                if (q_aligned) {  // a sector a lane (16 bytes a lane took twice as long)
 #pragma unroll
-            for (int c = 0; c < kSlabsTm; ++c) {
-                uint32_t r[16];
+                    for (int c = 0; c < kSlabsTm; ++c)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint4 v = __ldg(q + 4 * c + k);
-                    r[4 * k] = v.x, r[4 * k + 1] = v.y, r[4 * k + 2] = v.z, r[4 * k + 3] = v.w;
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t v[8];
+                            ld_global_v8(v, q + 32 * c + 16 * k);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) q_regs[c][8 * k + e] = v[e];
+                        }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kSlabsTm; ++c)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + 4 * c + k);
+                            q_regs[c][4 * k] = v.x, q_regs[c][4 * k + 1] = v.y, q_regs[c][4 * k + 2] = v.z,
+                            q_regs[c][4 * k + 3] = v.w;
+                        }
                 }
-                tmem_st_x16(lane_addr + kColQQ + 16u * kSlabsTm * half + 16u * c, r);
             }
-            tmem_st_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(qt_bar);
-        };
-        bool more = w.next(p, ctl.plan);
-        if (more) load_q();
-        while (more && !failed) {
+            if (more) {  // ... and put into tensor memory once the products of the request before have read theirs
+                const bool ok = mbar_await(&ctl.q_empty, uint32_t(q_seg & 1) ^ 1u, &ctl.abort);
+                ++q_seg;
+                if (!__all_sync(0xffffffffu, ok)) {
+                    failed = true;  // (all warps meet at the next barrier)
+                    if (lane == 0) ctl.abort = 1;
+                }
+                tc_fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < kSlabsTm; ++c)
+                    tmem_st_x16(lane_addr + kColQQ + 16u * kSlabsTm * half + 16u * c, q_regs[c]);
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(qt_bar);
+            }
+            if (had) {
+                // ---- the output (or partial)
+                bool done = mbar_await(&ctl.pv_done[(n - 1) & 1], uint32_t((n - 1) >> 1) & 1u, &ctl.abort);
+                done = done && mbar_wait_cluster(&ctl.l_full, uint32_t(seg & 1), &ctl.abort);
+                if (soft_or(!done || failed)) {  // (and the sums are read)
+                    failed = true;
+                    break;
+                }
+                tc_fence_after_sync();
+                ++seg;
+                {   // in one order, so that both pairs have the same sum
+                    const float other = *const_cast<volatile float*>(&ctl.peer[1][row]);
+                    sum = pair == 0 ? sum + other : other + sum;
+                }
+                if (live_token && (!(sum <= kSumMost) || (!own && any != 0 && !(sum >= kSumLeast)))) flagged = true;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const int head = row & 63;
+                if (live_token && pair == 0 && half == 0)
+                    (whole ? p.lse : p.lse_part)[at * kMlaHeads + head] =
+                        sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2T;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    if (fresh) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0u;
+                    } else {
+                        tmem_ld_32x32b_x32(lane_addr + kColOQ + 128u * half + 32u * c, o);
+                        tmem_ld_wait(o);
+                    }
+                    if (c == 3) {
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(o_bar);  // O may be overwritten
+                    }
+                    if (!live_token) continue;
+                    float most = 0.f;  // (0 x inf and 0 x NaN are NaN, and any other product 0)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float v = __uint_as_float(o[i]) * inv;
+                        most = fmaf(v, 0.f, most);
+                        o[i] = __float_as_uint(v);
+                    }
+                    if (most != 0.f) flagged = true;
+                    if (whole) {  // 64 heads x 64 dims a tile, 128-byte-swizzled, where the weights were
+                        uint8_t* const tile = tiles + kOffRq + ((row >> 6) * 4 + 2 * half + (c >> 1)) * kSlabV + head * 128;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[8 * k + 2 * e]),
+                                                                                __uint_as_float(o[8 * k + 2 * e + 1]));
+                                v[e] = *reinterpret_cast<const uint32_t*>(&b2);
+                            }
+                            *reinterpret_cast<uint4*>(tile + (((4 * (c & 1) + k) ^ (head & 7)) << 4)) =
+                                make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    } else {  // eight dims of a head after those of the head before: a warp's stores are contiguous
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t v[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = o[8 * k + e];
+                            st_global_v8(p.o_part + tiled_part(at, head, 256 * pair + 128 * half + 32 * c + 8 * k), v);
+                        }
+                    }
+                }
+                if (whole) {
+                    fence_proxy_async_smem();
+                    soft_or(false);
+                    if (threadIdx.x == 0) {
+#pragma unroll 1
+                        for (int i = 0; i < 4 * tokens_here; ++i)
+                            tma_store_2d(&o_map, s_base + kOffRq + i * kSlabV, 256 * pair + 64 * (i & 3),
+                                         int(first_row + (i >> 2)) * kMlaHeads);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!more) break;
+
+            // ---- the request's weights
             const int token = kTileTokens * w.tile + 2 * side + (row >> 6);
-            const bool live_token = token < w.drafted;
+            live_token = token < w.drafted;
             const int64_t q_row = int64_t(w.req()) * p.tokens + min(token, p.tokens - 1);
             const uint64_t drafts = __ldg(p.mask + q_row) & low_bits(w.drafted);
             bool ok = true;
-            float m = 0.f, l = 0.f;
-            bool own = true;    // the reference is a score of the row's
-            uint32_t any = 0;   // entries seen
-            bool fresh = true;  // no product of this request yet: O holds nothing of it
+            if (threadIdx.x == 0) {  // what the other pair will send: a maximum and a sum of each row
+                mbar_arrive_expect_tx(&ctl.m_full, uint32_t(kRowsQ * sizeof(float)));
+                mbar_arrive_expect_tx(&ctl.l_full, uint32_t(kRowsQ * sizeof(float)));
+            }
+            m = l = 0.f;
+            own = true;    // the reference is a score of the row's
+            any = 0;       // entries seen
+            fresh = true;  // no product of this request yet: O holds nothing of it
             uint32_t bad = 0;
 #pragma unroll 1
             for (int blk = w.blo; blk < w.bhi; ++blk, ++n) {
@@ -775,21 +913,29 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(s_bar + 8u * buf);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 y = mul_f32x2(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                                                   make_float2(c2, c2));
+                        x[i] = y.x, x[i + 1] = y.y;
+                    }
                 }
-                if (blk == w.blo) {  // the reference: the block's maximum, of both pages
-                    float mx = -INFINITY;
+                if (__any_sync(0xffffffffu, bits != 0xffffffffu)) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if ((bits >> i) & 1u) mx = fmaxf(mx, x[i] * c2);
+                        if (!((bits >> i) & 1u)) x[i] = -INFINITY;
+                }
+                if (blk == w.blo) {  // the reference: the block's maximum, of both pages
+                    float mx = x[0];
+#pragma unroll
+                    for (int i = 1; i < 32; ++i) mx = fmaxf(mx, x[i]);
                     ctl.part[half][row] = mx;
+                    // The outputs of the request before have left the buffers that weights come to again, this CTA's
+                    // own and, once its maxima are sent, the other pair's.
+                    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
                     soft_or(false);
                     mx = fmaxf(ctl.part[0][row], ctl.part[1][row]);
-                    if (half == 0) {
-                        st_cluster_f32(peer_max, mx);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(m_bar);
-                    }
+                    if (half == 0) st_async_f32(peer_max, mx, m_bar);
                     ok = ok && mbar_wait_cluster(&ctl.m_full, uint32_t(seg & 1), &ctl.abort);
                     if (soft_or(!ok)) {
                         failed = true;
@@ -800,26 +946,17 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                     if (!own) m = 0.f;
                 }
                 uint32_t packed[16];
-                float2 sum = make_float2(0.f, 0.f);
-                const float2 c22 = make_float2(c2, c2), m2 = make_float2(-m, -m);
+                float2 sums = make_float2(0.f, 0.f);
+                const float2 m2 = make_float2(-m, -m);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 y = fma_f32x2(make_float2(x[2 * i], x[2 * i + 1]), c22, m2);
-                    x[2 * i] = y.x, x[2 * i + 1] = y.y;
-                }
-                if (__any_sync(0xffffffffu, bits != 0xffffffffu)) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!((bits >> i) & 1u)) x[i] = -INFINITY;
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float p0 = ex2_approx(x[2 * i]), p1 = ex2_approx(x[2 * i + 1]);
-                    sum = add_f32x2(sum, make_float2(p0, p1));
+                    const float2 y = add_f32x2(make_float2(x[2 * i], x[2 * i + 1]), m2);
+                    const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+                    sums = add_f32x2(sums, make_float2(p0, p1));
                     const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
                     packed[i] = *reinterpret_cast<const uint32_t*>(&v);
                 }
-                l += sum.x + sum.y;
+                l += sums.x + sums.y;
                 // The products of the block before the last, of both pairs, have read their weights.
                 if (!__all_sync(0xffffffffu, ok && mbar_await(&ctl.pv_done[buf], (uint32_t(n >> 1) & 1u) ^ 1u, &ctl.abort))) {
                     failed = true;  // (the others' waits end the same way; the barriers are met by all)
@@ -843,94 +980,14 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                 if (w.valid(2 * blk) > 0 && !(bad_here & 1u)) fresh = false;
                 if (w.valid(2 * blk + 1) > 0 && !(bad_here & 2u)) fresh = false;
             }
-            // ---- the request's output (or partial)
-            ctl.part[half][row] = l;
-            if (soft_or(failed)) {
-                failed = true;
-                break;
-            }
-            float sum = ctl.part[0][row] + ctl.part[1][row];
-            if (half == 0) {
-                st_cluster_f32(peer_sum, sum);
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(l_bar);
-            }
-            const bool whole = w.blo == 0 && w.bhi == w.nb;
-            const int64_t at = whole ? q_row : (int64_t(w.range) * p.tokens + token) * 2 + (w.blo == 0 ? 1 : 0);
+            whole = w.blo == 0 && w.bhi == w.nb;
+            at = whole ? q_row : (int64_t(w.range) * p.tokens + token) * 2 + (w.blo == 0 ? 1 : 0);
+            tokens_here = min(w.drafted - kTileTokens * w.tile - 2 * side, 2);  // of this CTA's two
+            first_row = int64_t(w.req()) * p.tokens + kTileTokens * w.tile + 2 * side;
+            had = true;
             more = w.next(p, ctl.plan);
-            if (more) load_q();  // the next one's first scores run beside this one's last products
-            bool done = mbar_await(&ctl.pv_done[(n - 1) & 1], uint32_t((n - 1) >> 1) & 1u, &ctl.abort);
-            done = done && mbar_wait_cluster(&ctl.l_full, uint32_t(seg & 1), &ctl.abort);
-            if (soft_or(!done || failed)) {  // (and the sums are read)
-                failed = true;
-                break;
-            }
-            tc_fence_after_sync();
-            ++seg;
-            {   // in one order, so that both pairs have the same sum
-                const float other = *const_cast<volatile float*>(&ctl.peer[1][row]);
-                sum = pair == 0 ? sum + other : other + sum;
-            }
-            if (live_token && (!(sum <= kSumMost) || (!own && any != 0 && !(sum >= kSumLeast)))) flagged = true;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const int head = row & 63;
-            if (live_token && pair == 0 && half == 0)
-                (whole ? p.lse : p.lse_part)[at * kMlaHeads + head] =
-                    sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2T;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                if (fresh) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0u;
-                } else {
-                    tmem_ld_32x32b_x32(lane_addr + kColOQ + 128u * half + 32u * c, o);
-                    tmem_ld_wait(o);
-                }
-                if (c == 3) {
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(o_bar);  // O may be overwritten
-                }
-                if (!live_token) continue;
-                const int64_t d = (at * kMlaHeads + head) * kMlaDv + 256 * pair + 128 * half + 32 * c;
-                bool finite = true;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float v = __uint_as_float(o[i]) * inv;
-                    finite = finite && fabsf(v) <= 3.3e38f;
-                    o[i] = __float_as_uint(v);
-                }
-                if (!finite) flagged = true;
-                if (whole) {  // a whole sector a lane, where it starts on one
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[16 * k + 2 * e]),
-                                                                            __uint_as_float(o[16 * k + 2 * e + 1]));
-                            v[e] = *reinterpret_cast<const uint32_t*>(&b2);
-                        }
-                        __nv_bfloat16_raw* out = p.out + d + 16 * k;
-                        if (out_aligned) {
-                            st_global_v8(out, v);
-                        } else {
-                            reinterpret_cast<uint4*>(out)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-                            reinterpret_cast<uint4*>(out)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = o[8 * k + e];
-                        st_global_v8(p.o_part + d + 8 * k, v);
-                    }
-                }
-            }
         }
+        if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (failed && lane == 0) {
             atomicOr(p.err, kErrWaitTimeout);
             ctl.abort = 1;
@@ -1001,7 +1058,7 @@ cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cu
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tree_kernel, m.q, m.k, m.v, m.d, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tree_kernel, m.q, m.k, m.v, m.d, m.o, p);
     if (e != cudaSuccess) return e;
     // No request is split where none can have more blocks than are kept together.
     if (tree_blocks(p.table_width, 1) <= kTreeWholeBlocks) return cudaSuccess;
@@ -1016,6 +1073,7 @@ cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cu
     mp.tokens = p.tokens;
     mp.by_cut = p.batch > p.ranges;
     mp.many = 32;
+    mp.tiled = 1;
     return launch_mla_merge(mp, p.batch, p.ranges, stream);
 }
 
