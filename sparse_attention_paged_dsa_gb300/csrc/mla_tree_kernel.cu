@@ -247,6 +247,8 @@ constexpr int kGroupsK = kSlabsQ / kSlabsK;     // of a block
 constexpr int kRingK = 4;                       // groups in shared memory
 constexpr int kSlabV = kPg * 128;               // values of a page: two slabs of 64 entries x 64 dims
 constexpr int kGroupQ = 2 * kSlabV;
+constexpr int kSlabsLand = kRingK * kGroupK / kSlabQ;  // of q's slabs for tensor memory, by way of the idle ring
+static_assert(kSlabsLand == kSlabsTm - 1, "the last one goes through registers");
 constexpr int kOffQq = 0;
 constexpr int kOffKq = kOffQq + kSlabsSm * kSlabQ;
 constexpr int kOffVq = kOffKq + kRingK * kGroupK;
@@ -264,7 +266,7 @@ struct __align__(16) QuadCtl {
     uint64_t v_full[2], v_empty[2];            // per page of a block
     uint64_t vz_full[2], vz_ready[2];
     uint64_t s_full[2], s_empty[2];
-    uint64_t q_full, q_empty, qt_full, o_empty, all_done;
+    uint64_t q_full, q_empty, ql_full, ql_read, qt_full, o_empty, all_done;
     uint64_t p_own[2], p_other[2], r_full[2], pv_done[2];  // of every other block
     uint64_t m_full, l_full;                   // the other pair's row maxima, and sums, are here
     uint32_t tmem_base;
@@ -308,19 +310,20 @@ __device__ __forceinline__ void load_drafts(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// What some token of the current request sees of its drafted entries; by a whole warp.
+__device__ __forceinline__ uint64_t drafts_seen(const MlaTreeParams& p, const TreeWalk& w, int lane) {
+    uint64_t any = 0;
+    for (int j = lane; j < w.drafted; j += 32) any |= __ldg(p.mask + int64_t(w.req()) * p.tokens + j);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) any |= __shfl_xor_sync(0xffffffffu, any, o);
+    return any & low_bits(w.drafted);
+}
+
 // Zeroes the value rows of a page (in buffer pg) that nobody sees, up to the last 16-entry step of the product:
 // their weights are 0, but 0 x NaN is not.  By a whole warp, once the page has landed.  Out of line: the loops of
 // the roles run side by side and share an instruction cache.
-__device__ __noinline__ void zero_unseen(const uint64_t* masks, int drafted, int valid, uint8_t* v) {
+__device__ __noinline__ void zero_unseen(uint64_t used, int valid, uint8_t* v) {
     const int lane = threadIdx.x & 31;
-    uint64_t used = low_bits(valid);
-    if (masks) {  // the drafted page: what some token sees
-        uint64_t any = 0;
-        for (int j = lane; j < drafted; j += 32) any |= __ldg(masks + j);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) any |= __shfl_xor_sync(0xffffffffu, any, o);
-        used &= any;
-    }
     const int rows = (valid + 15) & ~15;
 #pragma unroll 1
     for (int c = lane; c < rows * 8; c += 32) {
@@ -371,6 +374,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
         }
         mbar_init(&ctl.q_full, 1);
         mbar_init(&ctl.q_empty, 1);
+        mbar_init(&ctl.ql_full, 1);          // slabs for tensor memory landed in this CTA's key ring; read from it
+        mbar_init(&ctl.ql_read, kSoftWarps);
         mbar_init(&ctl.qt_full, 2 * kSoftWarps);
         mbar_init(&ctl.o_empty, 2 * kSoftWarps);
         mbar_init(&ctl.all_done, 4);         // of both pairs' two issuing warps
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
             int id_l = tree_page_of_lane(p, w, 2 * w.blo, lane);
             if (id_l == -1 && 2 * w.blo + lane < 2 * w.bhi) atomicOr(p.err, kErrBadPage);
             const int row = (w.req() * p.tokens + 4 * w.tile + 2 * side) * kMlaHeads;
-            if (issuer) {  // into L2, the slabs that the softmax warps read too
+            if (issuer) {  // into L2, while the products of the request before use its q
 #pragma unroll 1
                 for (int s = 0; s < kSlabsQ; ++s)
                     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
@@ -429,11 +434,17 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                 const uint32_t bar = cluster_addr(&ctl.q_full, leader);
                 if (side == 0) mbar_arrive_expect_tx(&ctl.q_full, uint32_t(2 * kSlabsSm * kSlabQ));
                 // (rows behind the request's tokens are others' or zeros, and are not written)
-#pragma unroll
+                // those for tensor memory first, by way of the ring: its keys are used
+                mbar_arrive_expect_tx(&ctl.ql_full, uint32_t(kSlabsLand * kSlabQ));
+#pragma unroll 1
+                for (int s = 0; s < kSlabsLand; ++s)
+                    tma_load_3d(tiles + kOffKq + s * kSlabQ, &q_map, &ctl.ql_full, 0, row, kSlabsSm + s, pol_q);
+#pragma unroll 1
                 for (int s = 0; s < kSlabsSm; ++s) tma2_load_3d(sb + kOffQq + s * kSlabQ, &q_map, bar, 0, row, s, pol_q);
             }
             __syncwarp();
             ++seg;
+            if (!wait(&ctl.ql_read, uint32_t(seg - 1) & 1u)) break;
             const int blocks = uniform(w.bhi - w.blo);
 #pragma unroll 1
             for (int i = 0; i < blocks && ok; ++i) {
@@ -474,6 +485,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                     wait_landed_t(&ctl.k_full[i % kRingK], uint32_t(i / kRingK) & 1u);
                 if (seg > 0) wait_landed_t(&ctl.q_full, uint32_t(seg - 1) & 1u);
             }
+            if (seg > 0) wait_landed_t(&ctl.ql_full, uint32_t(seg - 1) & 1u);
         }
         __syncwarp();
     } else if (warp == 10) {
@@ -616,6 +628,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                 uint32_t zero_phase = 0;
                 while (ok && w.next(p, ctl.plan)) {
                     const int blocks = uniform(w.bhi - w.blo);
+                    const uint64_t drafts = drafts_seen(p, w, lane);
                     uint32_t fresh = 1, bad = 0;
 #pragma unroll 1
                     for (int i = 0; i < blocks && ok; ++i, ++n) {
@@ -634,7 +647,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                             const int steps = good ? uniform((w.valid(page) + 15) >> 4) : 0;
                             if (good && w.zeroes(page)) {
                                 wait(&ctl.vz_full[pg], (zero_phase >> pg) & 1u);
-                                zero_unseen(page == w.np ? p.mask + int64_t(w.req()) * p.tokens : nullptr, w.drafted, w.valid(page),
+                                zero_unseen(page == w.np ? drafts : low_bits(w.valid(page)), w.valid(page),
                                             tiles + kOffVq + pg * kGroupQ);
                                 wait(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u);  // (as p_own: nobody here reads those rows)
                                 zero_phase ^= 1u << pg;
@@ -693,6 +706,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
             uint32_t zero_phase = 0, bad = 0;
             while (ok && w.next(p, ctl.plan)) {
                 const int blocks = uniform(w.bhi - w.blo);
+                const uint64_t drafts = drafts_seen(p, w, lane);
 #pragma unroll 1
                 for (int i = 0; i < blocks && ok; ++i, ++n) {
                     if ((i & 15) == 0)
@@ -705,7 +719,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                         if (((bad >> (2 * (i & 15) + pg)) & 1u) || !w.zeroes(page)) continue;
                         if (!wait(&ctl.vz_full[pg], (zero_phase >> pg) & 1u)) break;
                         zero_phase ^= 1u << pg;
-                        zero_unseen(page == w.np ? p.mask + int64_t(w.req()) * p.tokens : nullptr, w.drafted, w.valid(page),
+                        zero_unseen(page == w.np ? drafts : low_bits(w.valid(page)), w.valid(page),
                                             tiles + kOffVq + pg * kGroupQ);
                         if (issuer) mbar_arrive_remote(cluster_addr(&ctl.vz_ready[pg], leader));
                     }
@@ -749,49 +763,57 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                 sum = ctl.part[0][row] + ctl.part[1][row];
                 if (half == 0) st_async_f32(peer_sum, sum, l_bar);
             }
-            // The last slabs of q, 128 dims a thread: fetched here, ...
-            uint32_t q_regs[kSlabsTm][16];
+            // q's slabs for tensor memory, half of each a thread: the last one straight from global memory, the others
+            // by way of the key ring.
             if (more) {
                 const int token = min(kTileTokens * w.tile + 2 * side + (row >> 6), p.tokens - 1);
-                const __nv_bfloat16_raw* q =
-                    p.q + ((int64_t(w.req()) * p.tokens + token) * kMlaHeads + (row & 63)) * kMlaDim + 64 * kSlabsSm +
-                    32 * kSlabsTm * half;
-                if (q_aligned) {  // a sector a lane (16 bytes a lane took twice as long)
+                const __nv_bfloat16_raw* q = p.q +
+                                             ((int64_t(w.req()) * p.tokens + token) * kMlaHeads + (row & 63)) * kMlaDim +
+                                             64 * (kSlabsQ - 1) + 32 * half;
+                uint32_t last[16];
+                if (q_aligned) {  // a sector a lane
 #pragma unroll
-                    for (int c = 0; c < kSlabsTm; ++c)
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t v[8];
+                        ld_global_v8(v, q + 16 * k);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t v[8];
-                            ld_global_v8(v, q + 32 * c + 16 * k);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) q_regs[c][8 * k + e] = v[e];
-                        }
+                        for (int e = 0; e < 8; ++e) last[8 * k + e] = v[e];
+                    }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < kSlabsTm; ++c)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + 4 * c + k);
-                            q_regs[c][4 * k] = v.x, q_regs[c][4 * k + 1] = v.y, q_regs[c][4 * k + 2] = v.z,
-                            q_regs[c][4 * k + 3] = v.w;
-                        }
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + k);
+                        last[4 * k] = v.x, last[4 * k + 1] = v.y, last[4 * k + 2] = v.z, last[4 * k + 3] = v.w;
+                    }
                 }
-            }
-            if (more) {  // ... and put into tensor memory once the products of the request before have read theirs
-                const bool ok = mbar_await(&ctl.q_empty, uint32_t(q_seg & 1) ^ 1u, &ctl.abort);
+                const bool ok = mbar_await(&ctl.ql_full, uint32_t(q_seg & 1), &ctl.abort);
                 ++q_seg;
                 if (!__all_sync(0xffffffffu, ok)) {
                     failed = true;  // (all warps meet at the next barrier)
                     if (lane == 0) ctl.abort = 1;
                 }
-                tc_fence_after_sync();
+                tc_fence_after_sync();  // (behind q_empty: the products have read what was there)
+#pragma unroll 1
+                for (int c = 0; c < kSlabsLand; ++c) {
+                    uint32_t r[16];
 #pragma unroll
-                for (int c = 0; c < kSlabsTm; ++c)
-                    tmem_st_x16(lane_addr + kColQQ + 16u * kSlabsTm * half + 16u * c, q_regs[c]);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(tiles + kOffKq + c * kSlabQ + row * 128 +
+                                                                        (((4 * half + k) ^ (row & 7)) << 4));
+                        r[4 * k] = v.x, r[4 * k + 1] = v.y, r[4 * k + 2] = v.z, r[4 * k + 3] = v.w;
+                    }
+                    tmem_st_x16(lane_addr + kColQQ + 32u * c + 16u * half, r);
+                }
+                tmem_st_x16(lane_addr + kColQQ + 32u * kSlabsLand + 16u * half, last);
+                // the ring's next contents come by TMA: behind these reads
+                fence_proxy_async_smem();
                 tmem_st_wait();
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(qt_bar);
+                if (lane == 0) {
+                    mbar_arrive(&ctl.ql_read);
+                    mbar_arrive_remote(qt_bar);
+                }
             }
             if (had) {
                 // ---- the output (or partial)
