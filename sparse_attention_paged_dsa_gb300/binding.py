@@ -604,29 +604,41 @@ def dsa_pages_update(seq_lens, new_lens, max_context: int, page_table, free_page
     served keep their length.  ``seq_lens_out`` and ``free_count_out`` may be ``seq_lens`` and ``free_count``
     themselves.  ``workspace``: any of this package's; without one the call makes its own."""
     dev = _device_of(seq_lens, "seq_lens", _I32, (1,))
-    B = seq_lens.shape[0]
-    _on(seq_lens, "seq_lens", _I32, (B,), dev)
-    _on(new_lens, "new_lens", _I32, (B,), dev)
+    lens = seq_lens.shape
+    B, where = lens[0], seq_lens.device
+    _on(seq_lens, "seq_lens", _I32, lens, dev)
+    _on(new_lens, "new_lens", _I32, lens, dev)
     _on(page_table, "page_table", _I32, (B, max_context // PAGE_TOKENS), dev)
     pages = free_pages.shape[0] if isinstance(free_pages, torch.Tensor) and free_pages.dim() == 1 else 0
     _on(free_pages, "free_pages", _I32, (pages,), dev)
     _on(free_count, "free_count", _I32, (1,), dev)
-    given = dict(seq_lens_out=(seq_lens_out, _I32, (B,)), free_count_out=(free_count_out, _I32, (1,)),
-                 cu_slots=(cu_slots, _I32, (B + 1,)), slots=(slots, _I64, (max_slots,)),
-                 positions=(positions, _I32, (max_slots,)))
-    outs = []
-    for name, (t, dtypes, shape) in given.items():
-        if t is None:
-            t = torch.empty(shape, dtype=dtypes[0], device=seq_lens.device)
-        else:
-            _on(t, name, dtypes, shape, dev)
-        outs.append(t)
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty(B, dtype=torch.int32, device=where)
+    else:
+        _on(seq_lens_out, "seq_lens_out", _I32, lens, dev)
+    if free_count_out is None:
+        free_count_out = torch.empty(1, dtype=torch.int32, device=where)
+    else:
+        _on(free_count_out, "free_count_out", _I32, (1,), dev)
+    if cu_slots is None:
+        cu_slots = torch.empty(B + 1, dtype=torch.int32, device=where)
+    else:
+        _on(cu_slots, "cu_slots", _I32, (B + 1,), dev)
+    if slots is None:
+        slots = torch.empty(max_slots, dtype=torch.int64, device=where)
+    else:
+        _on(slots, "slots", _I64, (max_slots,), dev)
+    if positions is None:
+        positions = torch.empty(max_slots, dtype=torch.int32, device=where)
+    else:
+        _on(positions, "positions", _I32, (max_slots,), dev)
     if workspace is None:
-        workspace = _header_workspace(seq_lens.device)
+        workspace = _header_workspace(where)
     _run(load().dsa_pages_update, dev, seq_lens.data_ptr(), new_lens.data_ptr(), B, max_context,
          page_table.data_ptr(), free_pages.data_ptr(), pages, free_count.data_ptr(), max_slots,
-         *(t.data_ptr() for t in outs), *_space(workspace, dev))
-    return tuple(outs)
+         seq_lens_out.data_ptr(), free_count_out.data_ptr(), cu_slots.data_ptr(), slots.data_ptr(),
+         positions.data_ptr(), *_space(workspace, dev))
+    return seq_lens_out, free_count_out, cu_slots, slots, positions
 
 
 def dsa_cache_append(slots, latent=None, latent_weight=None, cos_sin=None, positions=None, kv_cache=None,

@@ -1033,6 +1033,7 @@ dsa_status_t dsa_pages_update(const int32_t* seq_lens, const int32_t* new_lens, 
     p.positions = positions;
     p.err = static_cast<uint32_t*>(workspace);
     p.ticket = p.err + kTicketWord;
+    p.in_place = seq_lens_out == seq_lens || seq_lens_out == new_lens || free_count_out == free_count;
     p.num_pages = num_pages;
     p.max_context = max_context;
     p.max_slots = max_slots;

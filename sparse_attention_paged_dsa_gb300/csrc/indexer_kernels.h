@@ -315,6 +315,7 @@ struct PagesParams {
     int64_t max_slots;
     int32_t table_width;
     int32_t batch;
+    int32_t in_place;          // seq_lens_out or free_count_out is an input
 };
 cudaError_t launch_pages_update(const PagesParams& p, int sms, cudaStream_t stream);
 

@@ -14,7 +14,7 @@
 // on are the returned pages, found in the tables by a search in the prefix sums.
 // Reads and writes meet nowhere: the stack is written from the old count on and read
 // below it, table rows are written behind their old pages only.  Lengths and the
-// count, which may be updated in place, are written by the last CTA to finish
+// count, where they are updated in place, are written by the last CTA to finish
 // (a ticket in the workspace header, which it sets back).  Nothing depends on the
 // order of the CTAs.
 //
@@ -165,12 +165,21 @@ __global__ void __launch_bounds__(kThreadsPg) pages_update_kernel(const PagesPar
         bad |= kErrBadPage;
         return -1;
     };
-    for (int64_t at = count + first; at < left; at += step) p.free_pages[at] = stack(int(at));
-    for (int64_t k = first; k < taken; k += step) {
-        const int b = owner(s.take, p.batch, int(k));
-        p.page_table[int64_t(b) * p.table_width + pages_of(s.now[b]) + (int(k) - s.take[b])] = stack(avail - 1 - int(k));
-    }
-    for (int64_t i0 = kRun * first; i0 < p.max_slots; i0 += kRun * step) {
+    // What there is to do, one after another over all threads, so that a small call's chains of loads run side by
+    // side: runs of slots, pages taken, and returned pages that stay.
+    const int64_t runs = (p.max_slots + kRun - 1) / kRun, stays = left > count ? left - count : 0;
+    for (int64_t job = first; job < runs + taken + stays; job += step) {
+        if (job >= runs + taken) {
+            const int64_t to = count + (job - runs - taken);
+            p.free_pages[to] = stack(int(to));
+            continue;
+        }
+        if (job >= runs) {
+            const int k = int(job - runs), b = owner(s.take, p.batch, k);
+            p.page_table[int64_t(b) * p.table_width + pages_of(s.now[b]) + (k - s.take[b])] = stack(avail - 1 - k);
+            continue;
+        }
+        const int64_t i0 = kRun * job;
         int64_t slot[kRun];
         int pos[kRun];
         int b = i0 < total ? owner(s.slot, p.batch, int(i0)) : 0;
@@ -214,8 +223,10 @@ __global__ void __launch_bounds__(kThreadsPg) pages_update_kernel(const PagesPar
     if (blockIdx.x == 0)
         for (int b = tid; b <= p.batch; b += kThreadsPg) p.cu_slots[b] = s.slot[b];
 
-    // The last CTA to get here: nobody reads the lengths or the count any more.
-    if (gridDim.x > 1) {
+    // Updated in place: by the last CTA to get here, when nobody reads the lengths or the count any more.
+    if (!p.in_place) {
+        if (blockIdx.x != 0) return;
+    } else if (gridDim.x > 1) {
         __syncthreads();
         if (tid == 0) {
             __threadfence();
