@@ -988,6 +988,7 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
         e = dsa::launch_mla_tree(m, t, quads, cs);
         if (e != cudaSuccess) return cuda_fail(e, "MLA tree decode launch");
         p.redo = dsa::mla_tree_ctas(t, quads);
+        p.first_ranges = shape.ranges;
     }
     CUtensorMap q_map, kv_map, kr_map, o_map, d_map;
     st = make_slabs_map(&q_map, q, q_rows, 3, "mla q");

@@ -165,6 +165,7 @@ struct MlaDenseParams {
     const uint32_t* flags;     // of another kernel's CTAs, which has done the call: its outputs are not to be used
     uint32_t* again;           // was the call done again?
     int32_t redo;              // flags to look at: leave if none is set; 0: the call is this kernel's own
+    int32_t first_ranges;      // with redo: of the kernel that has done the call, for the merge of either
 };
 // q_map and kv_map: 576-wide bf16 rows (q: batch * tokens * 64 of them; the cache: num_pages * 64) as
 // (dim in slab, row, slab of 64 dims), boxes of 64 rows x 3 slabs and 64 rows x 2 slabs; kr_map: the
@@ -179,7 +180,8 @@ cudaError_t launch_mla_dense_tree(const CUtensorMap& q_map, const CUtensorMap& k
                                   const CUtensorMap& o_map, const CUtensorMap& d_map, const MlaDenseParams& p,
                                   cudaStream_t stream);
 
-// The log-sum-exp merge of requests that cross ranges (of the dense and the tree decode).
+// The log-sum-exp merge of requests that cross ranges (of the dense and the tree decode).  Rows go by requests, or by
+// cuts between ranges where those are fewer.
 struct MlaMergeParams {
     const int2* plan;          // [batch] first and last range of each request (equal: one)
     const int32_t* cuts;       // [ranges] the request that the range is the second one of, or -1
@@ -188,13 +190,14 @@ struct MlaMergeParams {
     __nv_bfloat16_raw* out;    // [batch, tokens, 64, 512]
     float* lse;                // [batch, tokens, 64]
     const int32_t* counts;     // [batch] tokens of each request, or null: all
-    const uint32_t* run;       // 0 there: nothing is to be done (null: there is)
+    const uint32_t* again;     // of the tree decode's kernel (its partials lie as tiled_part says): not 0 there if
+                               // the dense kernel has done the call again; null: the dense kernel's own call
     int32_t tokens;
-    int32_t rows;              // (set by the launch)
-    int32_t many;              // ranges per request from which on one is split many ways
-    int32_t by_cut;            // rows go by cuts (there are fewer ranges than requests)
-    int32_t tiled;             // the partials lie as tiled_part says, not row by row
+    int32_t by_cut, rows;              // requests (or cuts) x tokens
+    int32_t by_cut_again, rows_again;  // of the dense kernel's second try
+    int32_t one_head;          // few rows that are split many ways: more threads a row
 };
+cudaError_t launch_mla_merge(const MlaMergeParams& p, cudaStream_t stream);
 // Where a dim (a multiple of 4) of a head lies in a tiled partial: eight dims of all 64 heads after one another.
 __host__ __device__ inline int64_t tiled_part(int64_t part, int head, int dim) {
     return ((part * (kMlaDv / 8) + dim / 8) * kMlaHeads + head) * 8 + dim % 8;

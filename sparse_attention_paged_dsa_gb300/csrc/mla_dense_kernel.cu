@@ -980,10 +980,18 @@ cudaError_t launch(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CU
     m.out = p.out;
     m.lse = p.lse;
     m.counts = p.counts;
-    m.run = p.redo > 0 ? p.again : nullptr;
     m.tokens = p.tokens;
     m.by_cut = p.merge_by_cut;
-    return launch_mla_merge(m, p.batch, p.groups, stream);
+    m.rows = (p.merge_by_cut ? p.groups : p.batch) * p.tokens;
+    m.one_head = m.rows <= 16;
+    if (p.redo > 0) {  // one merge, for this kernel's partials or those of the one before
+        m.again = p.again;
+        m.by_cut_again = m.by_cut, m.rows_again = m.rows;
+        m.by_cut = p.batch > p.first_ranges;
+        m.rows = (m.by_cut ? p.first_ranges : p.batch) * p.tokens;
+        m.one_head = m.rows <= 16 && p.first_ranges >= 32 * p.batch;
+    }
+    return launch_mla_merge(m, stream);
 }
 
 }  // namespace

@@ -11,22 +11,20 @@
 namespace dsa {
 namespace {
 
-constexpr int kEarly = 4;
-constexpr int kAgainRows = 16;  // rows of CTAs where the call is hardly ever done again
 
 // o[r] = sum_i exp(lse_i - lse) o_i over the partials of a split request, lse = log sum_i exp(lse_i).
 // 512 threads.  128 of them per 512 dims, four heads a CTA; or (kOneHead: few rows, each split many ways)
 // 64 per 256 dims, half a head a CTA, whose partials go to the eight groups in turn.  Grid (heads / 4 or
 // heads x 2, requests or cuts x tokens).
 template <bool kOneHead, bool kTiled>
-__device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at) {
+__device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at, bool by_cut, bool tiled) {
     __shared__ float wgt[kOneHead ? 1 : 4][kMlaMaxGroups];
     __shared__ float4 acc_s[kOneHead ? 7 : 1][64];
     const int quarter = threadIdx.x >> (kOneHead ? 6 : 7);
     const int d4 = kOneHead ? (int(blockIdx.x) & 1) * 64 + (threadIdx.x & 63) : threadIdx.x & 127;
     const int h = kOneHead ? int(blockIdx.x) >> 1 : int(blockIdx.x) * 4 + quarter;
     const int token = at % p.tokens;
-    const int b = p.by_cut ? p.cuts[at / p.tokens] : at / p.tokens;
+    const int b = by_cut ? p.cuts[at / p.tokens] : at / p.tokens;
     if (b < 0) return;
     if (p.counts && token >= __ldg(p.counts + b)) return;
     const int64_t row = int64_t(b) * p.tokens + token;
@@ -37,15 +35,16 @@ __device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at) {
     const auto part = [&](int i) { return (int64_t(g.x + i) * p.tokens + token) * 2 + (i == 0 ? 1 : 0); };
     // The first partials are on their way while the weights are made.
     const auto value = [&](int i) {
-        return *reinterpret_cast<const float4*>(p.o_part + (kTiled ? tiled_part(part(i), h, 4 * d4)
+        return *reinterpret_cast<const float4*>(p.o_part + (kTiled && tiled ? tiled_part(part(i), h, 4 * d4)
                                                                    : (part(i) * kMlaHeads + h) * kMlaDv + 4 * d4));
     };
     constexpr int kStep = kOneHead ? 8 : 1;
     const int first = kOneHead ? quarter : 0;
-    float4 early[kEarly];
+    // (not for the dense kernel's many requests of two parts each: 200 of 4096 tokens took 71 us, 68 without)
+    constexpr int kEarly = kOneHead || kTiled ? 4 : 0;
+    float4 early[kEarly + 1];
 #pragma unroll
-    for (int k = 0; k < kEarly; ++k)
-        if (first + k * kStep < S) early[k] = value(first + k * kStep);
+    for (int k = 0; k < kEarly; ++k) early[k] = value(min(first + k * kStep, S - 1));
     if ((threadIdx.x & 127) < 32 && (!kOneHead || quarter == 0)) {
         float* const w = wgt[kOneHead ? 0 : quarter];
         const int lane = threadIdx.x & 31;
@@ -94,39 +93,37 @@ __device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at) {
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-// Rows of CTAs take the rows in turn (each one its own, but where nothing is likely to be done).
+// kTiled: of the tree decode's kernel, whose call the dense kernel may have done again, with a plan and partials
+// of its own.
 template <bool kOneHead, bool kTiled>
 __global__ void __launch_bounds__(512) mla_merge_kernel(const MlaMergeParams p) {
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
-    if (p.run && *p.run == 0) return;
-    for (int at = blockIdx.y; at < p.rows; at += gridDim.y) {
-        merge_row<kOneHead, kTiled>(p, at);
-        __syncthreads();
-    }
+    const bool again = kTiled && *p.again != 0;
+    const bool by_cut = again ? p.by_cut_again : p.by_cut;
+    const int rows = again ? p.rows_again : p.rows;
+    if (int(blockIdx.y) < rows) merge_row<kOneHead, kTiled>(p, blockIdx.y, by_cut, !again);
 }
 
 }  // namespace
 
-cudaError_t launch_mla_merge(MlaMergeParams p, int batch, int ranges, cudaStream_t stream) {
-    // One row of CTAs per request, or, where they are fewer, per cut between ranges.  Few rows that are split
-    // many ways: more threads per row read more partials at a time.
-    const int rows = p.rows = (p.by_cut ? ranges : batch) * p.tokens;
-    const bool one_head = rows <= 16 && ranges >= p.many * batch;
+cudaError_t launch_mla_merge(const MlaMergeParams& p, cudaStream_t stream) {
+    const bool tiled = p.again != nullptr;
+    const int rows = tiled && p.rows_again > p.rows ? p.rows_again : p.rows;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(one_head ? kMlaHeads * 2 : kMlaHeads / 4, unsigned(p.run && rows > kAgainRows ? kAgainRows : rows));
+    cfg.gridDim = dim3(p.one_head ? kMlaHeads * 2 : kMlaHeads / 4, unsigned(rows));
     cfg.blockDim = dim3(512);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (p.tiled)
-        return one_head ? cudaLaunchKernelEx(&cfg, mla_merge_kernel<true, true>, p)
-                        : cudaLaunchKernelEx(&cfg, mla_merge_kernel<false, true>, p);
-    return one_head ? cudaLaunchKernelEx(&cfg, mla_merge_kernel<true, false>, p)
-                    : cudaLaunchKernelEx(&cfg, mla_merge_kernel<false, false>, p);
+    if (tiled)
+        return p.one_head ? cudaLaunchKernelEx(&cfg, mla_merge_kernel<true, true>, p)
+                          : cudaLaunchKernelEx(&cfg, mla_merge_kernel<false, true>, p);
+    return p.one_head ? cudaLaunchKernelEx(&cfg, mla_merge_kernel<true, false>, p)
+                      : cudaLaunchKernelEx(&cfg, mla_merge_kernel<false, false>, p);
 }
 
 }  // namespace dsa

@@ -1080,23 +1080,7 @@ cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cu
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, mla_tree_kernel, m.q, m.k, m.v, m.d, m.o, p);
-    if (e != cudaSuccess) return e;
-    // No request is split where none can have more blocks than are kept together.
-    if (tree_blocks(p.table_width, 1) <= kTreeWholeBlocks) return cudaSuccess;
-    MlaMergeParams mp{};
-    mp.plan = p.plan;
-    mp.cuts = p.cuts;
-    mp.o_part = p.o_part;
-    mp.lse_part = p.lse_part;
-    mp.out = p.out;
-    mp.lse = p.lse;
-    mp.counts = p.counts;
-    mp.tokens = p.tokens;
-    mp.by_cut = p.batch > p.ranges;
-    mp.many = 32;
-    mp.tiled = 1;
-    return launch_mla_merge(mp, p.batch, p.ranges, stream);
+    return cudaLaunchKernelEx(&cfg, mla_tree_kernel, m.q, m.k, m.v, m.d, m.o, p);
 }
 
 }  // namespace dsa
