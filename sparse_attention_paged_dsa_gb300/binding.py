@@ -659,7 +659,8 @@ def dsa_cache_append(slots, latent=None, latent_weight=None, cos_sin=None, posit
         raise ValueError("latent and kv_cache come together")
     if (key_codes is None) != (key_scales is None):
         raise ValueError("key_codes and key_scales come together")
-    if (index_keys is None) != (key_pool is None and key_codes is None) or (key_pool is not None and key_codes is not None):
+    caches = (key_pool is not None) + (key_codes is not None)
+    if caches != (index_keys is not None):
         raise ValueError("index_keys goes with one of key_pool and (key_codes, key_scales)")
     pages = row = key_row = cos_rows = 0
     if latent is not None:

@@ -369,6 +369,9 @@ size_t dense_workspace_bytes(int groups, int32_t next_n) {
 
 constexpr int kTicketWord = 32;  // of the workspace header: the page update's, 0 between calls
 
+// From this many tokens x context on, a tree of more than two tokens is worth the kernel on clusters of four CTAs
+// (us, dense kernel and that one: 1 request, 4 tokens, 131072 context 44, 46; 4 x 8, 8192 36, 40; 16 x 8, 4096 58, 58;
+// 1 x 16, 32768 52, 46; 64 x 8, 8192 212, 134; 16 x 32, 131072 2996, 1275).
 constexpr int64_t kTreeWork = int64_t(1) << 19;
 
 // Tree decode: header, cuts, plan, flags, then two partial outputs per range and token.  Two kernels share it
@@ -955,7 +958,8 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
     p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
     p.mask = tree_mask;
     p.counts = token_counts_opt;
-    if (tokens > 2 && int64_t(batch) * tokens * max_context > kTreeWork && shape.ranges * shape.tiles <= dsa::kTreeMaxRounds * quads) {
+    if (tokens > 2 && int64_t(batch) * tokens * max_context > kTreeWork &&
+        shape.ranges * shape.tiles <= dsa::kTreeMaxRounds * quads) {
         dsa::MlaTreeParams t{};
         t.q = static_cast<const __nv_bfloat16_raw*>(q);
         t.page_table = page_table;
@@ -1075,7 +1079,8 @@ dsa_status_t dsa_cache_append(const int64_t* slots, int64_t rows, const void* la
     if (!aligned(slots, 8) || !aligned(latent_opt, 16) || !aligned(kv_cache, 16) || !aligned(index_keys_opt, 4) ||
         !aligned(key_pool_opt, 4) || !aligned(key_codes_opt, 2) || !aligned(key_scales_opt, 4) ||
         !aligned(cos_sin_opt, 4) || !aligned(positions, 4) ||
-        !aligned(latent_weight_opt, latent_weight_fp32 ? 4 : 2) || !aligned(index_weight_opt, index_weight_fp32 ? 4 : 2))
+        !aligned(latent_weight_opt, latent_weight_fp32 ? 4 : 2) ||
+        !aligned(index_weight_opt, index_weight_fp32 ? 4 : 2))
         return DSA_ERR_INVALID_ARG;
     dsa_status_t st = check_workspace(workspace, workspace_bytes, dsa::kWorkspaceHeaderBytes);
     if (st != DSA_OK) return st;

@@ -230,8 +230,8 @@ struct MlaTreeParams {
     float sm_scale_log2;       // sm_scale * log2(e)
 };
 // 576-wide bf16 rows as (dim in slab, row, slab), boxes of rows x slabs: q 128 x 1; the cache's, k 32 x 3, v 64 x
-// 2; the drafted entries as (dim in slab, token, slab, request), d 32 tokens x 1; o, out as [batch * tokens * 64, 512] rows, boxes of
-// 64 x 64.  All 128-byte-swizzled.
+// 2; the drafted entries as (dim in slab, token, slab, request), d 32 tokens x 1; o, out as [batch * tokens * 64, 512]
+// rows, boxes of 64 x 64.  All 128-byte-swizzled.
 struct MlaTreeMaps {
     CUtensorMap q, k, v, d, o;
 };

@@ -1,10 +1,13 @@
 // mla_dense_kernel.cu -- latent attention decode over every live entry of the
-// paged cache (absorbed form), one to four query tokens per request, sm_103a.
+// paged cache (absorbed form), one to four query tokens per request, sm_103a; and for
+// trees of drafted tokens (kTree) where they are small, or again with a running maximum
+// where mla_tree_kernel.cu, which keeps none, has given up.
 //
 //     s[h, t] = sm_scale * q[b, j, h] . kv_t                 (576-wide entries)
 //     o[b, j, h] = sum_t softmax_t(s[h, :]) kv_t[:512],  lse = log sum_t exp(s[h, t])
 //
-// over t < ceil((seq_len - (next_n - 1 - j)) / 4).
+// over t < ceil((seq_len - (next_n - 1 - j)) / 4).  A tree's tokens see all ceil(seq_len / 4)
+// entries, and of one more block, their own entries, those of their masks.
 //
 // Work split.  A block is one page: 64 entries, 73,728 contiguous bytes.  The
 // requests' blocks, laid end to end with kMlaSegUnits units of fixed cost before

@@ -1,29 +1,62 @@
-// mla_tree_kernel.cu -- the tree decode (mla_tree_kernel.cu) on clusters of four
-// CTAs and four drafted tokens, for calls whose time is products, sm_103a.
+// mla_tree_kernel.cu -- latent attention decode (absorbed form) for trees of more
+// than two drafted tokens, sm_103a.
 //
-// What an SM takes in bounds the smaller kernel: 33 bytes a cycle, multicast or not
-// (measured), so a 64-row tile's 1,088 bytes an entry cost twice its multiply-adds.  Here:
-//   * rows: tokens 0 and 1 of the tile are CTAs 0 and 2's 128 rows, tokens 2 and 3 CTAs 1
-//     and 3's.  CTAs 0, 1 and CTAs 2, 3 are pairs (cta_group::2, M = 256: all four tokens);
+//     s[h, t] = sm_scale * q[b, j, h] . e_t                  (576-wide entries)
+//     o[b, j, h] = sum_t softmax_t(s[h, :]) e_t[:512],  lse = log sum_t exp(s[h, t])
+//
+// over the ceil(seq_len / 4) live entries of the request's paged cache and the drafted
+// entries i whose bit of the token's mask is set.  (One or two tokens, and small calls:
+// mla_dense_kernel.cu.)
+//
+// What an SM takes in is 33 bytes a cycle, from L2 by plain or multicast loads alike
+// (measured).  A token's 64 heads on an SM of their own need an entry's 1,152 bytes, 35
+// cycles, for 17 of multiply-adds.  So four tokens share a cluster of four CTAs:
+//   * rows: tokens 0 and 1 of the tile are the 128 rows of CTAs 0 and 2, tokens 2 and 3 of
+//     CTAs 1 and 3.  CTAs 0, 1 and CTAs 2, 3 are pairs (cta_group::2, M = 256: all tokens);
 //   * S = Q . K^T    pair p takes page p of a block of two: N = 64, 32 entries in each CTA;
 //   * O += P . V     pair p takes value dims [256 p, 256 p + 256) of both pages: N = 256, 128
-//                    dims in each CTA.  P of its own page comes from tensor memory, P of the
-//                    other page from the CTA with the same rows in the other pair, through
-//                    distributed shared memory.
-// An entry then costs an SM 288 bytes as key, 256 as value and 128 of weights for 128 rows'
-// scores and half a row's values: 672 bytes, 20 cycles, for 17 of multiply-adds.
+//                    dims in each CTA.  P of the other page comes from the CTA with the same
+//                    rows in the other pair, by bulk copies between their shared memories.
+// A block's entry then costs an SM 288 bytes as key, 256 as value and 128 of weights: 20 cycles.
+// The multiply-adds of a block take 2,464 (36 products of N = 64 at 40, bound by their reads
+// of shared memory, and 8 of N = 256 at 128); the loop runs at 2,490.
 //
-// No running maximum.  Both CTAs that hold a row must use one reference, and agreeing
-// on a new one block by block would cost a round trip each.  They agree once, on the
-// first block's maximum.  Weights may then pass 1 as far as fp32 and bf16 reach (their
-// rounding is relative: nothing is lost).  A CTA whose sums pass 2^58, or any of
-// whose outputs is not finite, sets its flag, and the smaller kernel, which keeps a running
-// maximum, then does the whole call again (launch_mla_tree): it leaves at once where no flag is set.
+// Work.  A request's blocks are those of its pages followed by a page of its drafted
+// entries.  Requests laid end to end, kTreeSegUnits units of fixed cost before each, are cut
+// into ranges (how many: tree_cost); a unit is a range and a tile of four tokens.  Units are
+// dealt out range by range, so that the tiles of one request run at the same time and all but
+// the first read its pages from L2.  A request inside one range is written straight to the
+// output, one that crosses ranges leaves fp32 partials that a second kernel joins.
 //
-// Shared memory holds q (147 KB), eight of a block's nine key slabs, its values, and the other page's
-// weights.  Roles as in the smaller kernel (384 threads): warps 0-7 softmax, one row and 32 entries a
-// thread; warp 8 of each pair's leader MMAs; 9 and 10 TMA; 11 zeroes value rows that nobody sees.
-// Every wait is bounded (about 1 s) but the cluster barriers, which every thread reaches.
+// No running maximum.  Both CTAs that hold a row must use one reference, and agreeing on a new
+// one block by block would cost a round trip each.  They agree once, on the first block's
+// maximum.  Weights may then pass 1 as far as fp32 and bf16 reach (their rounding is relative:
+// nothing is lost).  A CTA one of whose sums passes 2^58, or one of whose outputs is not finite,
+// sets its flag, and the dense kernel, which keeps a running maximum, then does the whole call
+// again; it leaves at once (3 us) where no flag is set.
+//
+// Memory.  q: five slabs of 64 dims in shared memory (80 KB), four in tensor memory beside S
+// (two blocks) and O; keys: a ring of four groups of three slabs; values: one block; weights of both
+// pages: two blocks.  One block's weights less in flight: 2,144 us for 16 x 32 tokens at
+// 128K context, now 1,275 (1,833 TFLOP/s, 0.96 of the measured bf16 rate; in a long run, which
+// power limits, 1,428: 0.97 of the sustained rate).
+//
+// Roles of a CTA (384 threads):
+//   * warps 0-7: softmax, one row and 32 entries a thread; q's slabs into tensor memory; outputs.
+//   * warp 8 of each pair's leader: S.  Warp 11: O.  (One warp for both was late with every
+//     product: 4,650 cycles a block, of them 2,000 in waits for barriers that were complete.)
+//   * warp 11 of the other CTAs: tells the leader of weights that have come there.  Both zero
+//     value rows that nobody sees (behind the last live entry, drafts outside every mask).
+//   * warps 9 and 10: TMA of q and keys, and of values.
+// The roles' loops run side by side and share an instruction cache: with a few hundred
+// instructions more, the loop ran a quarter slower on most of the device.
+//
+// What bounds it: the tensor cores in long requests; in short ones a request's start and end
+// (about 8,000 cycles: q, the first block's maxima, sums, outputs).  64 x 8 tokens at 8192: 134 us
+// (0.57); 64 x 64 at 512: 251 us, of them 86 the bytes of q and the output.
+// Every wait is bounded (about 1 s) but the cluster barriers, which every thread reaches, and the
+// softmax warps' own, which they meet in step whatever fails; a timeout sets an error bit, the
+// roles drain, and TMEM is freed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,7 +73,7 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreadsQ = 384;  // (twelve warps: a thirteenth would leave the softmax 128 registers)
+constexpr int kThreadsQ = 384;         // (a thirteenth warp would leave the softmax 128 registers)
 constexpr int kPg = kPageEntries;      // entries of a page, heads of a token
 constexpr int kSoftWarps = 8;
 constexpr float kLn2T = 0.69314718055994531f;
@@ -140,7 +173,6 @@ __device__ __forceinline__ int tree_page_of_lane(const MlaTreeParams& p, const T
     return (id >= 0 && int64_t(id) < p.num_pages) ? id : -1;
 }
 
-
 __device__ __forceinline__ void clear_plan(const MlaTreeParams& p, TreePlan& plan) {
     for (int k = 0; k < kTreeMaxRounds; ++k) {
         plan.unit[k] = {0, 0, p.batch, 0};
@@ -150,10 +182,9 @@ __device__ __forceinline__ void clear_plan(const MlaTreeParams& p, TreePlan& pla
 
 // Finds the cluster's units, from the prefix sums of the requests' plan units; returns how many the call
 // has.  For all threads, the plan cleared; it is there after the caller's next barrier.
-template <int kThreads>
 __device__ __forceinline__ int find_units(const MlaTreeParams& p, TreePlan& plan, int cluster, int clusters) {
     const int warp = int(threadIdx.x) >> 5, lane = threadIdx.x & 31;
-    const int per = (p.batch + kThreads - 1) / kThreads;
+    const int per = (p.batch + kThreadsQ - 1) / kThreadsQ;
     const int r0 = min(int(threadIdx.x) * per, p.batch), r1 = min(r0 + per, p.batch);
     int mine = 0;
     for (int b = r0; b < r1; ++b) {
@@ -173,13 +204,13 @@ __device__ __forceinline__ int find_units(const MlaTreeParams& p, TreePlan& plan
     if (lane == 31) plan.warp_units[warp] = incl;
     __syncthreads();
     int before = 0, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kThreadsQ / 32; ++w) {
         if (w < warp) before += plan.warp_units[w];
         total += plan.warp_units[w];
     }
     // How many ranges: a thread for each number.
     uint64_t best = ~uint64_t(0);
-    for (int r = int(threadIdx.x) + 1; r <= min(p.ranges, total); r += kThreads) {
+    for (int r = int(threadIdx.x) + 1; r <= min(p.ranges, total); r += kThreadsQ) {
         const uint64_t cost = uint64_t(tree_cost(r, total, p.tiles, p.quads, p.tokens)) << 16 | uint64_t(r);
         best = cost < best ? cost : best;
     }
@@ -190,7 +221,7 @@ __device__ __forceinline__ int find_units(const MlaTreeParams& p, TreePlan& plan
     }
     if (lane == 0) plan.warp_best[warp] = best;
     __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) best = plan.warp_best[w] < best ? plan.warp_best[w] : best;
+    for (int w = 0; w < kThreadsQ / 32; ++w) best = plan.warp_best[w] < best ? plan.warp_best[w] : best;
     const int nranges = total > 0 ? int(best & 0xFFFF) : 1;
     const int units = nranges * p.tiles;
     const Ranges ranges(nranges, total);
@@ -261,7 +292,7 @@ constexpr uint32_t kColOQ = 256;   // O: 256 columns
 constexpr float kSumMost = 288230376151711744.0f;  // 2^58: times 2^18 entries and values below 2^50
 constexpr float kSumLeast = 8.4703294725430034e-22f;  // 2^-70, where the reference is not the row's own
 
-struct __align__(16) QuadCtl {
+struct __align__(16) TreeCtl {
     uint64_t k_full[kRingK], k_empty[kRingK];  // full: the pair's leader's, of both CTAs' copies
     uint64_t v_full[2], v_empty[2];            // per page of a block
     uint64_t vz_full[2], vz_ready[2];
@@ -275,7 +306,7 @@ struct __align__(16) QuadCtl {
     float part[2][kRowsQ];                     // per half of the entries: maxima of the first block, then sums
     float peer[2][kRowsQ];                     // the other pair's maxima, and sums
 };
-constexpr int kSmemQ = kOffCtlQ + int(sizeof(QuadCtl));
+constexpr int kSmemQ = kOffCtlQ + int(sizeof(TreeCtl));
 static_assert(kSmemQ <= 232448, "fits one CTA per SM");
 
 // Arrive once on the barrier at this offset in the CTAs of `mask` when every MMA this thread issued has completed.
@@ -289,7 +320,8 @@ __device__ __forceinline__ void commit_to(uint64_t* bar, uint16_t mask) {
 
 // Copy to another CTA's shared memory, counted on a barrier there.
 __device__ __forceinline__ void bulk_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     dst),
                  "r"(src), "r"(bytes), "r"(bar)
                  : "memory");
 }
@@ -301,8 +333,8 @@ __device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t ba
 }
 
 // 32 rows of one slab of a request's drafted entries (rows behind the last arrive as zeros).
-__device__ __forceinline__ void load_drafts(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t row, int32_t slab,
-                                            int32_t request, uint64_t policy) {
+__device__ __forceinline__ void load_drafts(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t row,
+                                            int32_t slab, int32_t request, uint64_t policy) {
     asm volatile(
         "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
@@ -337,11 +369,11 @@ __device__ __noinline__ void zero_unseen(uint64_t used, int valid, uint8_t* v) {
 
 __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
     mla_tree_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                         const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap d_map,
-                         const __grid_constant__ CUtensorMap o_map, const MlaTreeParams p) {
+                    const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap d_map,
+                    const __grid_constant__ CUtensorMap o_map, const MlaTreeParams p) {
     extern __shared__ uint8_t smem_raw[];  // at the same offset in all CTAs; on a 1,024-byte boundary, checked below
     uint8_t* tiles = smem_raw;
-    QuadCtl& ctl = *reinterpret_cast<QuadCtl*>(tiles + kOffCtlQ);
+    TreeCtl& ctl = *reinterpret_cast<TreeCtl*>(tiles + kOffCtlQ);
     const uint32_t s_base = smem_u32(tiles);
     const int warp = uniform(int(threadIdx.x) >> 5);
     const int lane = threadIdx.x & 31;
@@ -351,7 +383,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
     const uint16_t both = uint16_t(3u << (rank & 2));
     const int cluster = int(blockIdx.x) >> 2, clusters = int(gridDim.x) >> 2;
 
-    if (s_base & 1023u) {  // (the same in every CTA; shared memory has started on such a boundary on every part)
+    if (s_base & 1023u) {  // (the same in every CTA; shared memory has always started on such a boundary)
+        pdl_wait_prior_grid();
         if (threadIdx.x == 0) p.flags[blockIdx.x] = 1;
         return;
     }
@@ -394,7 +427,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
 
-    const int units = find_units<kThreadsQ>(p, ctl.plan, cluster, clusters);
+    const int units = find_units(p, ctl.plan, cluster, clusters);
     tc_fence_before_sync();
     cluster_sync_all();  // the barriers and the plan are there, in all CTAs
     tc_fence_after_sync();
@@ -433,14 +466,15 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
             if (issuer) {
                 const uint32_t bar = cluster_addr(&ctl.q_full, leader);
                 if (side == 0) mbar_arrive_expect_tx(&ctl.q_full, uint32_t(2 * kSlabsSm * kSlabQ));
-                // (rows behind the request's tokens are others' or zeros, and are not written)
-                // those for tensor memory first, by way of the ring: its keys are used
+                // Rows behind the request's tokens are others' or zeros, and their outputs are not written.  The slabs
+                // for tensor memory first, by way of the ring, whose keys are used.
                 mbar_arrive_expect_tx(&ctl.ql_full, uint32_t(kSlabsLand * kSlabQ));
 #pragma unroll 1
                 for (int s = 0; s < kSlabsLand; ++s)
                     tma_load_3d(tiles + kOffKq + s * kSlabQ, &q_map, &ctl.ql_full, 0, row, kSlabsSm + s, pol_q);
 #pragma unroll 1
-                for (int s = 0; s < kSlabsSm; ++s) tma2_load_3d(sb + kOffQq + s * kSlabQ, &q_map, bar, 0, row, s, pol_q);
+                for (int s = 0; s < kSlabsSm; ++s)
+                    tma2_load_3d(sb + kOffQq + s * kSlabQ, &q_map, bar, 0, row, s, pol_q);
             }
             __syncwarp();
             ++seg;
@@ -459,12 +493,14 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                 for (int j = 0; j < kGroupsK; ++j, ++n) {
                     if (!wait(&ctl.k_empty[slot], phase ^ 1u)) break;
                     if (issuer) {
-                        const uint32_t bar = cluster_addr(&ctl.k_full[slot], leader), dst = sb + kOffKq + slot * kGroupK;
+                        const uint32_t bar = cluster_addr(&ctl.k_full[slot], leader);
+                        const uint32_t dst = sb + kOffKq + slot * kGroupK;
                         if (side == 0) mbar_arrive_expect_tx(&ctl.k_full[slot], uint32_t(2 * kGroupK));
                         if (id == -2) {
 #pragma unroll
                             for (int k = 0; k < kSlabsK; ++k)
-                                load_drafts(dst + k * kSlabK, &d_map, bar, kHalfPg * side, kSlabsK * j + k, w.req(), pol_kv);
+                                load_drafts(dst + k * kSlabK, &d_map, bar, kHalfPg * side, kSlabsK * j + k, w.req(),
+                                            pol_kv);
                         } else {
                             tma2_load_3d(dst, &k_map, bar, 0, row, kSlabsK * j, pol_kv);
                         }
@@ -562,9 +598,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
         }
         __syncwarp();
     } else if (warp == 8 || warp == 11) {
-        // ================= MMA (the pairs' leaders'), scores =================
-        // In a warp of their own: one that issued both products was late with every one of them (4,650
-        // cycles a block, of them 2,000 in barriers that were complete).
+        // ================= MMA (the pairs' leaders') =================
         if (side == 0) {
             constexpr uint32_t kIdescQk = idesc_bf16_f32(256, 64);
             constexpr uint32_t kIdescPv = idesc_bf16_f32(256, 256) | (1u << 16);  // B (V) MN-major
@@ -578,6 +612,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
             };
             int n = 0, seg = 0;  // blocks, requests so far
             if (warp == 8) {
+                // ---- scores
                 const uint64_t q_desc = smem_desc_kmajor_sw128(sb + kOffQq);
                 const uint64_t k_desc = smem_desc_kmajor_sw128(sb + kOffKq);
                 int slot = 0;
@@ -607,7 +642,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                                             umma2_bf16_ss(dd, a + uint32_t(k * (kSlabQ >> 4) + 2 * kk), b, kIdescQk,
                                                           (j | k | kk) != 0 ? 1u : 0u);
                                         else
-                                            umma2_bf16_ts(dd, at + uint32_t(32 * (kSlabsK * j + k - kSlabsSm) + 8 * kk), b, kIdescQk, 1u);
+                                            umma2_bf16_ts(dd, at + uint32_t(32 * (kSlabsK * j + k - kSlabsSm) + 8 * kk), b,
+                                                          kIdescQk, 1u);
                                     }
                                 commit_to(&ctl.k_empty[slot], both);
                                 if (j == kGroupsK - 1) {
@@ -623,7 +659,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                 }
             } else {
                 // ---- outputs
-                const uint64_t r_desc = smem_desc_kmajor_sw128(sb + kOffRq), p_desc = smem_desc_kmajor_sw128(sb + kOffPq);
+                const uint64_t r_desc = smem_desc_kmajor_sw128(sb + kOffRq);
+                const uint64_t p_desc = smem_desc_kmajor_sw128(sb + kOffPq);
                 const uint64_t v_desc = desc_mn_sw128(sb + kOffVq, kSlabV);
                 uint32_t zero_phase = 0;
                 while (ok && w.next(p, ctl.plan)) {
@@ -649,7 +686,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                                 wait(&ctl.vz_full[pg], (zero_phase >> pg) & 1u);
                                 zero_unseen(page == w.np ? drafts : low_bits(w.valid(page)), w.valid(page),
                                             tiles + kOffVq + pg * kGroupQ);
-                                wait(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u);  // (as p_own: nobody here reads those rows)
+                                wait(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u);
                                 zero_phase ^= 1u << pg;
                             }
                             wait(&ctl.v_full[pg], uint32_t(n & 1));
@@ -663,7 +700,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                             if (ok && issuer) {
                                 const uint64_t bd = refreshed(v_desc + uint32_t(pg * (kGroupQ >> 4)));
                                 const uint32_t d = refreshed(tmem + kColOQ);
-                                const uint64_t a = refreshed((s == 0 ? p_desc : r_desc) + uint32_t(buf * (kSlabQ >> 4)));
+                                const uint64_t a =
+                                    refreshed((s == 0 ? p_desc : r_desc) + uint32_t(buf * (kSlabQ >> 4)));
                                 const auto step = [&](int kk) {
                                     umma2_bf16_ss(d, a + 2u * kk, bd + uint32_t(kk * (2048 >> 4)), kIdescPv,
                                                   (kk == 0 && fresh) ? 0u : 1u);
@@ -737,16 +775,17 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
         const uint32_t peer = uint32_t(rank ^ 2);        // the same rows, the other page and value dims
         const uint32_t s_bar = cluster_addr(ctl.s_empty, leader), p_bar = cluster_addr(ctl.p_own, leader),
                        o_bar = cluster_addr(&ctl.o_empty, leader), qt_bar = cluster_addr(&ctl.qt_full, leader);
-        const uint32_t r_rows = cluster_addr(tiles + kOffRq, peer) + quad * 4096, r_bar = cluster_addr(ctl.r_full, peer);
+        const uint32_t r_rows = cluster_addr(tiles + kOffRq, peer) + quad * 4096;
+        const uint32_t r_bar = cluster_addr(ctl.r_full, peer);
         uint8_t* const pbuf = tiles + kOffPq + row * 128;
-        const uint32_t peer_max = cluster_addr(ctl.peer[0], peer) + 4 * row, peer_sum = cluster_addr(ctl.peer[1], peer) + 4 * row;
+        const uint32_t peer_max = cluster_addr(ctl.peer[0], peer) + 4 * row;
+        const uint32_t peer_sum = cluster_addr(ctl.peer[1], peer) + 4 * row;
         const uint32_t m_bar = cluster_addr(&ctl.m_full, peer), l_bar = cluster_addr(&ctl.l_full, peer);
         const float c2 = p.sm_scale_log2;
         const bool q_aligned = (reinterpret_cast<uintptr_t>(p.q) & 31) == 0;
         bool failed = false;
         int n = 0, seg = 0;
-        // One request after another; its start is under the last products of the one before, and the code is there
-        // once: the roles' loops share an instruction cache, and 0.25 of the time went to it when they passed it.
+        // One request after another, the start of each under the last products of the one before.
         bool more = w.next(p, ctl.plan), had = false;
         int q_seg = 0;
         // of the request before: its sums, where its outputs go, and what is known of them
@@ -860,7 +899,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                     }
                     if (most != 0.f) flagged = true;
                     if (whole) {  // 64 heads x 64 dims a tile, 128-byte-swizzled, where the weights were
-                        uint8_t* const tile = tiles + kOffRq + ((row >> 6) * 4 + 2 * half + (c >> 1)) * kSlabV + head * 128;
+                        uint8_t* const tile =
+                            tiles + kOffRq + ((row >> 6) * 4 + 2 * half + (c >> 1)) * kSlabV + head * 128;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             uint32_t v[4];
@@ -980,7 +1020,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                 }
                 l += sums.x + sums.y;
                 // The products of the block before the last, of both pairs, have read their weights.
-                if (!__all_sync(0xffffffffu, ok && mbar_await(&ctl.pv_done[buf], (uint32_t(n >> 1) & 1u) ^ 1u, &ctl.abort))) {
+                ok = ok && mbar_await(&ctl.pv_done[buf], (uint32_t(n >> 1) & 1u) ^ 1u, &ctl.abort);
+                if (!__all_sync(0xffffffffu, ok)) {
                     failed = true;  // (the others' waits end the same way; the barriers are met by all)
                     if (lane == 0) ctl.abort = 1;
                 }
@@ -996,7 +1037,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                 asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
                 if (lane == 0) {
                     if (half == 0)
-                        bulk_to_cta(r_rows + buf * kSlabQ, s_base + kOffPq + buf * kSlabQ + quad * 4096, 4096u, r_bar + 8u * buf);
+                        bulk_to_cta(r_rows + buf * kSlabQ, s_base + kOffPq + buf * kSlabQ + quad * 4096, 4096u,
+                                    r_bar + 8u * buf);
                     mbar_arrive_remote(p_bar + 8u * buf);
                 }
                 if (w.valid(2 * blk) > 0 && !(bad_here & 1u)) fresh = false;
