@@ -13,15 +13,14 @@
 // and weight is largest.  fp32 throughout, one rounding per output.  A row's place is
 // fetched two rows ahead, its data (and its row of the rotation's table) one.
 //
-// What bounds it: HBM and, by half, instructions.  262144 rows, norms, rotation, fp8 keys: 132
-// us, 5490 GB/s, 0.81 of the measured copy rate; the latents alone 101 us (a copy of them 95);
-// the keys' 4-byte scales and 64-byte rows are written where the slots say.  One after another
-// the sums took 136 us; weights in registers 142 (24 warps an SM, now 32); five CTAs an SM
-// spill (181).  Few rows: launch latency, 2.5 us.
+// What bounds it: HBM and the rows' places.  262144 rows, norms, rotation, fp8 keys: 123 us, 5900
+// GB/s, 0.87 of the measured copy rate (119 with the slots in order; the latents alone 101, a
+// copy of them 95).  At 400 instructions a row it was bound by them (132 us, 71 % of issue
+// slots); the sums one after another took 136; 24 warps an SM, with the weights in
+// registers, 142; five CTAs an SM spill (181).  Few rows: launch latency, 2.5 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdint>
 
 #include "indexer_kernels.h"
@@ -31,7 +30,7 @@ namespace dsa {
 namespace {
 
 constexpr int kWarpsA = 8;
-constexpr int kCtasA = 4;  // per SM
+constexpr int kCtasA = 4;  // per SM, by their registers
 constexpr float kE4m3Max = 448.0f;
 
 __device__ __forceinline__ float2 widen(uint32_t v) {
@@ -51,38 +50,49 @@ struct Row {
     float cs, sn;
 };
 
+// kKeys: 0 none, 1 bf16, 2 fp8.
+template <bool kLatent, int kKeys>
 __global__ void __launch_bounds__(kWarpsA * 32, kCtasA) append_kernel(const AppendParams p) {
     const int lane = threadIdx.x & 31;
-    const int64_t warp = int64_t(blockIdx.x) * kWarpsA + (threadIdx.x >> 5), warps = int64_t(gridDim.x) * kWarpsA;
+    const uint32_t warp = blockIdx.x * kWarpsA + (threadIdx.x >> 5), warps = gridDim.x * kWarpsA;
+    const uint32_t rows = uint32_t(p.rows);  // (below 2^31, and two rounds of warps more below 2^32)
     __shared__ __align__(16) float wc[kMlaDv];
     __shared__ __align__(16) float wk[kHeadDim];
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
 
-    const auto place = [&](int64_t i) {
+    const bool norm = kLatent && p.latent_weight, rotate = kLatent && p.cos_sin, key_norm = kKeys > 0 && p.key_weight;
+    const auto place = [&](uint32_t i) {
         Place at = {-1, 0};
-        if (i < p.rows) {
+        if (i < rows) {
             at.slot = __ldg(p.slots + i);
-            if (p.cos_sin) at.pos = __ldg(p.positions + i);
+            if (rotate) at.pos = __ldg(p.positions + i);
         }
         return at;
     };
     const auto in_table = [&](int pos) { return pos >= 0 && int64_t(pos) < p.cos_rows; };
-    const auto load = [&](int64_t i, const Place& at) {
+    // Where the next row to load starts, for this lane.
+    const uint8_t* x = p.latent + int64_t(warp) * p.latent_stride * 2 + 16 * lane;
+    const uint8_t* key = p.keys + int64_t(warp) * p.key_stride * 2 + 4 * lane;
+    const int64_t x_step = int64_t(warps) * p.latent_stride * 2, key_step = int64_t(warps) * p.key_stride * 2;
+    const auto load = [&](const Place& at) {
         Row row;
         row.cs = 1.f, row.sn = 0.f;
-        if (i >= p.rows || at.slot == -1) return row;
-        if (p.latent) {
-            const uint8_t* x = p.latent + i * p.latent_stride * 2;
-            row.c[0] = __ldcs(reinterpret_cast<const uint4*>(x) + lane);
-            row.c[1] = __ldcs(reinterpret_cast<const uint4*>(x) + 32 + lane);
-            row.r = __ldcs(reinterpret_cast<const uint32_t*>(x + kMlaDv * 2) + lane);
-            if (p.cos_sin && in_table(at.pos)) {
-                row.cs = __ldg(p.cos_sin + int64_t(at.pos) * 64 + lane);
-                row.sn = __ldg(p.cos_sin + int64_t(at.pos) * 64 + 32 + lane);
+        if (at.slot != -1) {
+            if (kLatent) {
+                row.c[0] = __ldcs(reinterpret_cast<const uint4*>(x));
+                row.c[1] = __ldcs(reinterpret_cast<const uint4*>(x + 512));
+                row.r = __ldcs(reinterpret_cast<const uint32_t*>(x + kMlaDv * 2 - 12 * lane));
+                if (rotate && in_table(at.pos)) {
+                    const float* t = p.cos_sin + int64_t(at.pos) * 64 + lane;
+                    row.cs = __ldg(t);
+                    row.sn = __ldg(t + 32);
+                }
             }
+            if (kKeys) row.k = __ldcs(reinterpret_cast<const uint32_t*>(key));
         }
-        if (p.keys) row.k = __ldcs(reinterpret_cast<const uint32_t*>(p.keys + i * p.key_stride * 2) + lane);
+        if (kLatent) x += x_step;
+        if (kKeys) key += key_step;
         return row;
     };
     const auto weight_at = [&](const void* w, int fp32, int i) {
@@ -90,25 +100,25 @@ __global__ void __launch_bounds__(kWarpsA * 32, kCtasA) append_kernel(const Appe
                     : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + i));
     };
     Place at = place(warp), next = place(warp + warps);
-    if (p.latent_weight)
+    if (norm)
         for (int i = threadIdx.x; i < kMlaDv; i += kWarpsA * 32)
             wc[i] = weight_at(p.latent_weight, p.latent_weight_fp32, i);
-    if (p.key_weight)
+    if (key_norm)
         for (int i = threadIdx.x; i < kHeadDim; i += kWarpsA * 32)
             wk[i] = weight_at(p.key_weight, p.key_weight_fp32, i);
     __syncthreads();
 
     // A row's place is fetched two rows ahead, its data (and its row of the table) one.
-    Row row = load(warp, at);
-    for (int64_t i = warp; i < p.rows; i += warps) {
+    const int64_t slots = p.num_pages * kPageEntries;
+    Row row = load(at);
+    for (uint32_t i = warp; i < rows; i += warps) {
         const Row now = row;
         const Place to = at;
         at = next;
         next = place(i + 2 * warps);
-        row = load(i + warps, at);
+        row = load(at);
         if (to.slot == -1) continue;
-        const bool bad_slot = to.slot < -1 || to.slot >= p.num_pages * kPageEntries;
-        const bool bad_pos = p.cos_sin && !in_table(to.pos);
+        const bool bad_slot = uint64_t(to.slot) >= uint64_t(slots), bad_pos = rotate && !in_table(to.pos);
         if (bad_slot || bad_pos) {
             if (lane == 0) atomicOr(p.err, (bad_slot ? kErrBadPage : 0u) | (bad_pos ? kErrBadRange : 0u));
             continue;
@@ -117,66 +127,78 @@ __global__ void __launch_bounds__(kWarpsA * 32, kCtasA) append_kernel(const Appe
         uint32_t* const u = reinterpret_cast<uint32_t*>(c);
         // What the row needs of the whole warp, three butterflies side by side: both sums of squares, and the
         // largest key times its weight (the norm is the same for all of them).
-        float ss = 0.f, ks = 0.f, top = 0.f;
-        float2 y = make_float2(0.f, 0.f);
-        if (p.latent_weight) {
+        float2 sums = make_float2(0.f, 0.f), y = make_float2(0.f, 0.f);  // of the entry, of the key
+        float top = 0.f;
+        if (norm) {
+            float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float2 v = widen(u[j]);
-                ss = fmaf(v.x, v.x, fmaf(v.y, v.y, ss));
+                ss = fma_f32x2(v, v, ss);
             }
+            sums.x = ss.x + ss.y;
         }
-        if (p.keys) {
+        if (kKeys) {
             y = widen(now.k);
-            if (p.key_weight) {
-                ks = fmaf(y.x, y.x, y.y * y.y);
-                const float2 w = *reinterpret_cast<const float2*>(wk + 2 * lane);
-                y = make_float2(y.x * w.x, y.y * w.y);
+            if (key_norm) {
+                sums.y = fmaf(y.x, y.x, y.y * y.y);
+                y = mul_f32x2(y, *reinterpret_cast<const float2*>(wk + 2 * lane));
             }
-            top = fmaxf(fabsf(y.x), fabsf(y.y));
+            if (kKeys == 2) top = fmaxf(fabsf(y.x), fabsf(y.y));
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const float a = __shfl_xor_sync(0xffffffffu, ss, o), b = __shfl_xor_sync(0xffffffffu, ks, o),
-                        d = __shfl_xor_sync(0xffffffffu, top, o);
-            ss += a, ks += b, top = fmaxf(top, d);
+            float2 other = make_float2(0.f, 0.f);
+            if (kLatent) other.x = __shfl_xor_sync(0xffffffffu, sums.x, o);
+            if (kKeys) other.y = __shfl_xor_sync(0xffffffffu, sums.y, o);
+            if (kKeys == 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            sums = add_f32x2(sums, other);
         }
-        if (p.latent) {
-            if (p.latent_weight) {
-                const float inv = 1.f / sqrtf(ss * (1.f / kMlaDv) + p.eps);
+        if (kLatent) {
+            if (norm) {
+                const float inv = rsqrtf(sums.x * (1.f / kMlaDv) + p.eps);
+                const float2 by = make_float2(inv, inv);
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     const float4 w = *reinterpret_cast<const float4*>(wc + (j >> 2) * 256 + lane * 8 + 2 * (j & 3));
-                    const float2 a = widen(u[j]), b = widen(u[j + 1]);
-                    u[j] = narrow(a.x * w.x * inv, a.y * w.y * inv);
-                    u[j + 1] = narrow(b.x * w.z * inv, b.y * w.w * inv);
+                    const float2 a = mul_f32x2(mul_f32x2(widen(u[j]), make_float2(w.x, w.y)), by);
+                    const float2 b = mul_f32x2(mul_f32x2(widen(u[j + 1]), make_float2(w.z, w.w)), by);
+                    u[j] = narrow(a.x, a.y);
+                    u[j + 1] = narrow(b.x, b.y);
                 }
             }
             uint32_t r = now.r;
-            if (p.cos_sin) {
+            if (rotate) {
                 const float2 v = widen(r);
                 r = narrow(v.x * now.cs - v.y * now.sn, v.x * now.sn + v.y * now.cs);
             }
-            uint8_t* out = p.kv_cache + to.slot * (kMlaDim * 2);
-            reinterpret_cast<uint4*>(out)[lane] = c[0];
-            reinterpret_cast<uint4*>(out)[32 + lane] = c[1];
-            reinterpret_cast<uint32_t*>(out + kMlaDv * 2)[lane] = r;
+            uint8_t* out = p.kv_cache + to.slot * (kMlaDim * 2) + 16 * lane;
+            *reinterpret_cast<uint4*>(out) = c[0];
+            *reinterpret_cast<uint4*>(out + 512) = c[1];
+            *reinterpret_cast<uint32_t*>(out + kMlaDv * 2 - 12 * lane) = r;
         }
-        if (p.keys) {
-            if (p.key_weight) {
-                const float inv = 1.f / sqrtf(ks * (1.f / kHeadDim) + p.eps);
-                y = make_float2(y.x * inv, y.y * inv);
+        if (kKeys) {
+            if (key_norm) {
+                const float inv = rsqrtf(sums.y * (1.f / kHeadDim) + p.eps);
+                y = mul_f32x2(y, make_float2(inv, inv));
                 top *= inv;
             }
-            if (p.key_pool) {
-                reinterpret_cast<uint32_t*>(p.key_pool + to.slot * (kHeadDim * 2))[lane] =
-                    p.key_weight ? narrow(y.x, y.y) : now.k;
+            if (kKeys == 1) {
+                *reinterpret_cast<uint32_t*>(p.key_pool + to.slot * (kHeadDim * 2) + 4 * lane) =
+                    key_norm ? narrow(y.x, y.y) : now.k;
             } else {
                 float scale = top / kE4m3Max;
-                if (!(scale > 0.f) || scale > 3.0e38f) scale = 1.f;
+                float2 q;
+                if (top > 0x1p-100f && top < 0x1p100f) {  // one reciprocal for all 64
+                    const float by = __fdividef(kE4m3Max, top);
+                    q = mul_f32x2(y, make_float2(by, by));
+                } else {
+                    if (!(scale > 0.f) || scale > 3.0e38f) scale = 1.f;
+                    q = make_float2(y.x / scale, y.y / scale);
+                }
                 uint16_t code;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(code) : "f"(y.y / scale), "f"(y.x / scale));
-                reinterpret_cast<uint16_t*>(p.key_codes + to.slot * kHeadDim)[lane] = code;
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(code) : "f"(q.y), "f"(q.x));
+                *reinterpret_cast<uint16_t*>(p.key_codes + to.slot * kHeadDim + 2 * lane) = code;
                 if (lane == 0) p.key_scales[to.slot] = scale;
             }
         }
@@ -185,19 +207,11 @@ __global__ void __launch_bounds__(kWarpsA * 32, kCtasA) append_kernel(const Appe
 
 }  // namespace
 
-cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream) {
-    static std::atomic<int> resident[kMaxDevices];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    int per_sm = resident[dev].load(std::memory_order_relaxed);
-    if (per_sm == 0) {
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, append_kernel, kWarpsA * 32, 0);
-        if (e != cudaSuccess) return e;
-        resident[dev].store(per_sm, std::memory_order_relaxed);
-    }
-    const int64_t ctas = (p.rows + kWarpsA - 1) / kWarpsA, most = int64_t(sms) * per_sm;
+namespace {
+
+template <bool kLatent, int kKeys>
+cudaError_t launch(const AppendParams& p, int sms, cudaStream_t stream) {
+    const int64_t ctas = (p.rows + kWarpsA - 1) / kWarpsA, most = int64_t(sms) * kCtasA;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -207,7 +221,17 @@ cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, append_kernel, p);
+    return cudaLaunchKernelEx(&cfg, append_kernel<kLatent, kKeys>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream) {
+    const int keys = p.keys ? (p.key_pool ? 1 : 2) : 0;
+    if (p.latent)
+        return keys == 0 ? launch<true, 0>(p, sms, stream)
+                         : (keys == 1 ? launch<true, 1>(p, sms, stream) : launch<true, 2>(p, sms, stream));
+    return keys == 1 ? launch<false, 1>(p, sms, stream) : launch<false, 2>(p, sms, stream);
 }
 
 }  // namespace dsa

@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
         tma_prefetch_map(&k_map);
         tma_prefetch_map(&v_map);
         tma_prefetch_map(&d_map);
+        tma_prefetch_map(&o_map);
     }
     if (warp == 8) tmem2_alloc(&ctl.tmem_base, 512);
     __syncwarp();

@@ -2,7 +2,7 @@
 
 Tolerances from the arithmetic (u = 2^-24, fp32 half step).  Norms: the sum of 512 squares adds at most
 16 terms a lane and 5 butterfly levels, with the square's own rounding below 22 u relatively, halved by
-the root; the division by 512, + eps, root, reciprocal and two products add 6 u: |y32 - y| < 18 u |y| <
+the root; + eps, the reciprocal root (2 ulp, 4 u) and two products add 7 u: |y32 - y| < 18 u |y| <
 2^-19 |y|.  bf16 outputs: half a step on top, (2^-8 + 2^-18) |y|.  Rotation: two products and a sum, 3 u
 (|a c| + |b s|) before the rounding to bf16.  Scales: 2^-18 relatively.  Codes: within half an e4m3 step
 (2^-4 |y| for normal codes, 2^-10 scale below them) plus the errors of y and scale, 2^-17 of the largest."""
