@@ -369,18 +369,24 @@ size_t dense_workspace_bytes(int groups, int32_t next_n) {
 
 constexpr int kTicketWord = 32;  // of the workspace header: the page update's, 0 between calls
 
-// From this many tokens x context on, a tree of more than two tokens is worth the kernel on clusters of four CTAs
-// (us, dense kernel and that one: 1 request, 4 tokens, 131072 context 44, 46; 4 x 8, 8192 36, 40; 16 x 8, 4096 58, 58;
-// 1 x 16, 32768 52, 46; 64 x 8, 8192 212, 134; 16 x 32, 131072 2996, 1275).
+// From this many tokens x context on, a tree of two tokens or more is worth a kernel on clusters.  Of two CTAs (us,
+// dense kernel and that one, two tokens each: 4 x 65536 context 41.5, 41.5; 1 x 262144 38, 37; 16 x 131072 183, 139;
+// 64 x 8192 75, 65; 64 x 65536 354, 268), or of four (1 request, 4 tokens, 131072 context 44, 46; 4 x 8, 8192 36, 40;
+// 16 x 8, 4096 58, 58; 1 x 16, 32768 52, 46; 64 x 8, 8192 212, 134; 16 x 32, 131072 2996, 1275).
 constexpr int64_t kTreeWork = int64_t(1) << 19;
+// But not two tokens of requests of a page or two, where a request's start and end count (512: 600 of them 73, 85,
+// 1024 121, 140; 768: 85, 84 and 141, 136).
+constexpr int64_t kPairContext = 512;
 
-// Tree decode: header, cuts, plan, flags, then two partial outputs per range and token.  Two kernels share it
-// (the second one works where the first has not, or again): their plans lie apart, their partials do not.
+// Tree decode: header, cuts, plan, flags, then two partial outputs per range and token, of the kernel that the
+// call takes (the dense one may have to do a call again: it makes its own plan, in the same place).
 struct TreeShape {
-    int groups, quads, tiles, ranges;  // of the dense kernel; of the kernel on clusters of four CTAs
-    TreeShape(int32_t tokens, int sms, int quads_) : groups(dense_groups(sms, tokens)), quads(quads_) {
-        tiles = dsa::tree_tiles(tokens), ranges = dsa::tree_ranges(tiles, quads);
-    }
+    int groups;                   // of the dense kernel
+    int clusters, tiles, ranges;  // of the one on clusters: of two CTAs for two tokens, of four for more
+    TreeShape(int32_t tokens, int sms, int quads, int pairs)
+        : groups(dense_groups(sms, tokens)), clusters(tokens > dsa::kPairTokens ? quads : pairs),
+          tiles(tokens > dsa::kPairTokens ? dsa::tree_tiles(tokens) : 1),
+          ranges(tokens < dsa::kPairTokens ? 0 : dsa::tree_ranges(tiles, clusters)) {}
     size_t parts(int32_t tokens) const { return dense_parts(groups > ranges ? groups : ranges, tokens); }
     size_t workspace_bytes(int32_t tokens) const {
         return dsa::kWorkspaceHeaderBytes + kTreePlanBytes +
@@ -898,11 +904,12 @@ dsa_status_t dsa_mla_prefill(const void* q, int64_t q_row_stride, int64_t q_head
 }
 
 size_t dsa_mla_tree_decode_workspace_size(int32_t batch, int32_t tokens) {
-    int sms = 0, quads = 0;
+    int sms = 0, quads = 0, pairs = 0;
     if (batch < 1 || batch > DSA_MAX_BATCH || tokens < 1 || tokens > DSA_MAX_TREE_TOKENS) return 0;
-    if (sm_count(&sms) != cudaSuccess || dsa::mla_tree_quads(&quads) != cudaSuccess)
-        sms = 160, quads = 40;  // no device: what a large part needs
-    return TreeShape(tokens, sms, quads).workspace_bytes(tokens);
+    if (sm_count(&sms) != cudaSuccess || dsa::mla_tree_quads(&quads) != cudaSuccess ||
+        dsa::mla_tree_pairs(&pairs) != cudaSuccess)
+        sms = 160, quads = 40, pairs = 80;  // no device: what a large part needs
+    return TreeShape(tokens, sms, quads, pairs).workspace_bytes(tokens);
 }
 
 dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t num_pages, const int32_t* page_table,
@@ -925,11 +932,12 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
     if (num_pages > (int64_t(1) << 31) / dsa::kPageEntries - 1) return DSA_ERR_UNSUPPORTED;
     st = check_workspace(workspace, workspace_bytes, dsa::kWorkspaceHeaderBytes);
     if (st != DSA_OK) return st;
-    int sms = 0, quads = 0;
+    int sms = 0, quads = 0, pairs = 0;
     cudaError_t e = sm_count(&sms);
     if (e == cudaSuccess) e = dsa::mla_tree_quads(&quads);
+    if (e == cudaSuccess) e = dsa::mla_tree_pairs(&pairs);
     if (e != cudaSuccess) return cuda_fail(e, "device query");
-    const TreeShape shape(tokens, sms, quads);
+    const TreeShape shape(tokens, sms, quads, pairs);
     st = check_workspace(workspace, workspace_bytes, shape.workspace_bytes(tokens));
     if (st != DSA_OK) return st;
     uint8_t* ws = static_cast<uint8_t*>(workspace) + dsa::kWorkspaceHeaderBytes;
@@ -958,8 +966,9 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
     p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
     p.mask = tree_mask;
     p.counts = token_counts_opt;
-    if (tokens > 2 && int64_t(batch) * tokens * max_context > kTreeWork &&
-        shape.ranges * shape.tiles <= dsa::kTreeMaxRounds * quads) {
+    if (tokens >= dsa::kPairTokens && int64_t(batch) * tokens * max_context > kTreeWork &&
+        (tokens > dsa::kPairTokens || max_context > kPairContext) &&
+        shape.ranges * shape.tiles <= dsa::kTreeMaxRounds * shape.clusters) {
         dsa::MlaTreeParams t{};
         t.q = static_cast<const __nv_bfloat16_raw*>(q);
         t.page_table = page_table;
@@ -983,6 +992,15 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
         t.ranges = shape.ranges;
         t.sm_scale_log2 = p.sm_scale_log2;
         dsa::MlaTreeMaps m;
+        if (tokens == dsa::kPairTokens) {
+            st = make_slabs_map(&m.q, q, q_rows, 3, "mla q");
+            if (st == DSA_OK) st = make_rows_map(&m.k, kv_cache, kv_rows, DSA_MLA_DIM, 64, "mla kv");
+            if (st == DSA_OK) st = make_slabs_map(&m.v, kv_cache, kv_rows, 2, "mla kv");
+            if (st == DSA_OK) st = make_drafts_map(&m.d, draft_kv, batch, tokens, 64);
+            if (st != DSA_OK) return st;
+            e = dsa::launch_mla_tree_pair(m, t, pairs, cs);
+            return e == cudaSuccess ? DSA_OK : cuda_fail(e, "MLA tree decode launch");
+        }
         st = make_slabs_map(&m.q, q, q_rows, 1, "mla q", 128);
         if (st == DSA_OK) st = make_slabs_map(&m.k, kv_cache, kv_rows, 3, "mla kv", 32);
         if (st == DSA_OK) st = make_slabs_map(&m.v, kv_cache, kv_rows, 2, "mla kv");

@@ -190,11 +190,11 @@ struct MlaMergeParams {
     __nv_bfloat16_raw* out;    // [batch, tokens, 64, 512]
     float* lse;                // [batch, tokens, 64]
     const int32_t* counts;     // [batch] tokens of each request, or null: all
-    const uint32_t* again;     // of the tree decode's kernel (its partials lie as tiled_part says): not 0 there if
-                               // the dense kernel has done the call again; null: the dense kernel's own call
+    const uint32_t* again;     // not 0 there: the dense kernel has done the call again (null: it may not)
     int32_t tokens;
     int32_t by_cut, rows;              // requests (or cuts) x tokens
     int32_t by_cut_again, rows_again;  // of the dense kernel's second try
+    int32_t tiled;             // the partials lie as tiled_part says (those of a second try never do)
     int32_t one_head;          // few rows that are split many ways: more threads a row
 };
 cudaError_t launch_mla_merge(const MlaMergeParams& p, cudaStream_t stream);
@@ -202,9 +202,8 @@ cudaError_t launch_mla_merge(const MlaMergeParams& p, cudaStream_t stream);
 __host__ __device__ inline int64_t tiled_part(int64_t part, int head, int dim) {
     return ((part * (kMlaDv / 8) + dim / 8) * kMlaHeads + head) * 8 + dim % 8;
 }
-cudaError_t launch_mla_merge(MlaMergeParams p, int batch, int ranges, cudaStream_t stream);
 
-// Latent attention decode for a tree of drafted tokens, on clusters of four CTAs.
+// Latent attention decode for trees of drafted tokens, on clusters of four CTAs.
 struct MlaTreeParams {
     const __nv_bfloat16_raw* q; // [batch, tokens, 64, 576]
     const int32_t* page_table; // [batch, table_width]
@@ -226,7 +225,7 @@ struct MlaTreeParams {
     int32_t tokens;
     int32_t tiles;             // tree_tiles: of four tokens
     int32_t ranges;            // tree_ranges: at most
-    int32_t quads;             // clusters of the device (set by the launch)
+    int32_t clusters;          // of the device (set by the launch)
     float sm_scale_log2;       // sm_scale * log2(e)
 };
 // 576-wide bf16 rows as (dim in slab, row, slab), boxes of rows x slabs: q 128 x 1; the cache's, k 32 x 3, v 64 x
@@ -238,6 +237,11 @@ struct MlaTreeMaps {
 cudaError_t mla_tree_quads(int* quads);                    // clusters that the current device holds
 int mla_tree_ctas(const MlaTreeParams& p, int quads);      // CTAs of a call
 cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cudaStream_t stream);
+
+// The same for two tokens, on clusters of two CTAs, with a running maximum (flags are not used), and its merge.
+// q and v: boxes of 64 rows x 3 slabs and x 2; k: the cache's rows as (dim, row), 64 x 64; d: 64 tokens x 1.
+cudaError_t mla_tree_pairs(int* pairs);                    // clusters that the current device holds
+cudaError_t launch_mla_tree_pair(const MlaTreeMaps& m, MlaTreeParams p, int pairs, cudaStream_t stream);
 
 // Latent attention over ragged prompts, expanded form: per-head 128 + 64 shared key dims, 128 value dims.
 constexpr int kPrefillQk = 192;

@@ -989,6 +989,7 @@ cudaError_t launch(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CU
     m.one_head = m.rows <= 16;
     if (p.redo > 0) {  // one merge, for this kernel's partials or those of the one before
         m.again = p.again;
+        m.tiled = 1;
         m.by_cut_again = m.by_cut, m.rows_again = m.rows;
         m.by_cut = p.batch > p.first_ranges;
         m.rows = (m.by_cut ? p.first_ranges : p.batch) * p.tokens;

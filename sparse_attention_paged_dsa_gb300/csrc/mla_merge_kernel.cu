@@ -93,13 +93,13 @@ __device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at, bool 
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-// kTiled: of the tree decode's kernel, whose call the dense kernel may have done again, with a plan and partials
-// of its own.
+// kTiled: of the tree decode's kernels on clusters.  Of one of them the dense kernel may have done the call again,
+// with a plan and partials of its own.
 template <bool kOneHead, bool kTiled>
 __global__ void __launch_bounds__(512) mla_merge_kernel(const MlaMergeParams p) {
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
-    const bool again = kTiled && *p.again != 0;
+    const bool again = kTiled && p.again && *p.again != 0;
     const bool by_cut = again ? p.by_cut_again : p.by_cut;
     const int rows = again ? p.rows_again : p.rows;
     if (int(blockIdx.y) < rows) merge_row<kOneHead, kTiled>(p, blockIdx.y, by_cut, !again);
@@ -108,8 +108,7 @@ __global__ void __launch_bounds__(512) mla_merge_kernel(const MlaMergeParams p) 
 }  // namespace
 
 cudaError_t launch_mla_merge(const MlaMergeParams& p, cudaStream_t stream) {
-    const bool tiled = p.again != nullptr;
-    const int rows = tiled && p.rows_again > p.rows ? p.rows_again : p.rows;
+    const int rows = p.again && p.rows_again > p.rows ? p.rows_again : p.rows;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -119,7 +118,7 @@ cudaError_t launch_mla_merge(const MlaMergeParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (tiled)
+    if (p.tiled)
         return p.one_head ? cudaLaunchKernelEx(&cfg, mla_merge_kernel<true, true>, p)
                           : cudaLaunchKernelEx(&cfg, mla_merge_kernel<false, true>, p);
     return p.one_head ? cudaLaunchKernelEx(&cfg, mla_merge_kernel<true, false>, p)

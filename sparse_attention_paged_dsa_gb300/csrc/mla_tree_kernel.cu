@@ -5,8 +5,8 @@
 //     o[b, j, h] = sum_t softmax_t(s[h, :]) e_t[:512],  lse = log sum_t exp(s[h, t])
 //
 // over the ceil(seq_len / 4) live entries of the request's paged cache and the drafted
-// entries i whose bit of the token's mask is set.  (One or two tokens, and small calls:
-// mla_dense_kernel.cu.)
+// entries i whose bit of the token's mask is set.  (Two tokens: mla_tree_pair_kernel.cu.  One,
+// and small calls: mla_dense_kernel.cu.)
 //
 // What an SM takes in is 33 bytes a cycle, from L2 by plain or multicast loads alike
 // (measured).  A token's 64 heads on an SM of their own need an entry's 1,152 bytes, 35
@@ -67,203 +67,11 @@
 #include "cta_pair.cuh"
 #include "indexer_kernels.h"
 #include "mla_common.cuh"
-#include "mla_tree_plan.h"
+#include "mla_tree_common.cuh"
 #include "sm103_ptx.cuh"
 
 namespace dsa {
 namespace {
-
-constexpr int kThreadsQ = 384;         // (a thirteenth warp would leave the softmax 128 registers)
-constexpr int kPg = kPageEntries;      // entries of a page, heads of a token
-constexpr int kSoftWarps = 8;
-constexpr float kLn2T = 0.69314718055994531f;
-
-struct UnitT {
-    int lo, hi;                  // the range, in units of the plan
-    int first_req, first_start;  // request of its first unit, and where that request's units start
-};
-
-// In shared memory: a cluster's units.
-struct TreePlan {
-    UnitT unit[kTreeMaxRounds];
-    int cut[kTreeMaxRounds];     // the request that the range is the second one of, or -1
-    int warp_units[16];
-    uint64_t warp_best[16];
-};
-
-__device__ __forceinline__ bool soft_or(bool v) {  // over the 256 softmax threads
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred pi, po;\n\t"
-        "setp.ne.u32 pi, %1, 0;\n\t"
-        "bar.red.or.pred po, 1, 256, pi;\n\t"
-        "selp.u32 %0, 1, 0, po;\n\t}"
-        : "=r"(r)
-        : "r"(v ? 1u : 0u)
-        : "memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ void wait_landed_t(uint64_t* bar, uint32_t parity) {
-    const uint32_t a = smem_u32(bar);
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(a, parity) && global_timer_ns() - t0 < kWaitLimitNs) {
-    }
-}
-
-__device__ __forceinline__ int tree_tokens(const MlaTreeParams& p, int b) {  // cached, in [0, max_context]
-    const int seq = __ldg(p.seq_lens + b);
-    return seq < 0 ? 0 : (int64_t(seq) > p.max_context ? int(p.max_context) : seq);
-}
-__device__ __forceinline__ int tree_drafted(const MlaTreeParams& p, int b) {  // in [0, tokens]
-    if (!p.counts) return p.tokens;
-    return min(max(__ldg(p.counts + b), 0), p.tokens);
-}
-__device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1; }
-
-// The cluster's walk over its units: one step per request that has blocks in a unit's range and tokens
-// in its tile.
-struct TreeWalk {
-    int k, rounds, first, step;  // units first, first + step, ...
-    int b, u0, lo, hi;
-    int range, tile;
-    int np, live, drafted, nb, blo, bhi;  // current request: cache pages, entries, drafted tokens, blocks
-    __device__ __forceinline__ TreeWalk(int first_, int step_, int units)
-        : k(-1), rounds(first_ < units ? (units - first_ + step_ - 1) / step_ : 0), first(first_), step(step_), b(0),
-          u0(0), lo(0), hi(0) {}
-    __device__ __forceinline__ bool next(const MlaTreeParams& p, const TreePlan& plan) {
-        while (true) {
-            while (b < p.batch && u0 < hi) {
-                const int seq = tree_tokens(p, b);
-                live = (seq + 3) >> 2;
-                np = tree_cache_pages(seq);
-                drafted = tree_drafted(p, b);
-                nb = tree_blocks(np, drafted);
-                const int base = u0 + kTreeSegUnits, end = u0 + tree_units(nb);
-                blo = max(lo, base) - base;
-                bhi = min(hi, end) - base;
-                ++b;
-                u0 = end;
-                if (nb > 0 && bhi > blo && kTileTokens * tile < drafted) return true;
-            }
-            if (++k >= rounds) return false;
-            const int u = first + k * step;
-            range = u / p.tiles;
-            tile = u - range * p.tiles;
-            lo = plan.unit[k].lo, hi = plan.unit[k].hi, b = plan.unit[k].first_req, u0 = plan.unit[k].first_start;
-        }
-    }
-    __device__ __forceinline__ int req() const { return b - 1; }
-    // Entries of a page that somebody may see, if its id is good.
-    __device__ __forceinline__ int valid(int page) const {
-        return page < np ? min(live - page * kPg, kPg) : (page == np ? drafted : 0);
-    }
-    // Has a page value rows to zero?  (The drafted page always, by the masks.)
-    __device__ __forceinline__ bool zeroes(int page) const {
-        return page == np || (page < np && ((live - page * kPg) < kPg) && ((live & 15) != 0));
-    }
-};
-
-// Ids of pages [page0, page0 + 32) of the current request, a lane each: -1 where the table's is outside the
-// cache, -2 for the drafted page and those behind it.
-__device__ __forceinline__ int tree_page_of_lane(const MlaTreeParams& p, const TreeWalk& w, int page0, int lane) {
-    const int page = page0 + lane;
-    if (page >= w.np) return -2;
-    const int id = __ldg(p.page_table + int64_t(w.req()) * p.table_width + page);
-    return (id >= 0 && int64_t(id) < p.num_pages) ? id : -1;
-}
-
-__device__ __forceinline__ void clear_plan(const MlaTreeParams& p, TreePlan& plan) {
-    for (int k = 0; k < kTreeMaxRounds; ++k) {
-        plan.unit[k] = {0, 0, p.batch, 0};
-        plan.cut[k] = -1;
-    }
-}
-
-// Finds the cluster's units, from the prefix sums of the requests' plan units; returns how many the call
-// has.  For all threads, the plan cleared; it is there after the caller's next barrier.
-__device__ __forceinline__ int find_units(const MlaTreeParams& p, TreePlan& plan, int cluster, int clusters) {
-    const int warp = int(threadIdx.x) >> 5, lane = threadIdx.x & 31;
-    const int per = (p.batch + kThreadsQ - 1) / kThreadsQ;
-    const int r0 = min(int(threadIdx.x) * per, p.batch), r1 = min(r0 + per, p.batch);
-    int mine = 0;
-    for (int b = r0; b < r1; ++b) {
-        if (blockIdx.x == 0) {
-            const int seq = __ldg(p.seq_lens + b);
-            if (seq < 0 || int64_t(seq) > p.max_context) atomicOr(p.err, kErrSeqLenClamped);
-            if (p.counts && tree_drafted(p, b) != __ldg(p.counts + b)) atomicOr(p.err, kErrBadRange);
-        }
-        mine += tree_units(tree_blocks(tree_cache_pages(tree_tokens(p, b)), tree_drafted(p, b)));
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) plan.warp_units[warp] = incl;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < kThreadsQ / 32; ++w) {
-        if (w < warp) before += plan.warp_units[w];
-        total += plan.warp_units[w];
-    }
-    // How many ranges: a thread for each number.
-    uint64_t best = ~uint64_t(0);
-    for (int r = int(threadIdx.x) + 1; r <= min(p.ranges, total); r += kThreadsQ) {
-        const uint64_t cost = uint64_t(tree_cost(r, total, p.tiles, p.quads, p.tokens)) << 16 | uint64_t(r);
-        best = cost < best ? cost : best;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t y = __shfl_xor_sync(0xffffffffu, best, o);
-        best = y < best ? y : best;
-    }
-    if (lane == 0) plan.warp_best[warp] = best;
-    __syncthreads();
-    for (int w = 0; w < kThreadsQ / 32; ++w) best = plan.warp_best[w] < best ? plan.warp_best[w] : best;
-    const int nranges = total > 0 ? int(best & 0xFFFF) : 1;
-    const int units = nranges * p.tiles;
-    const Ranges ranges(nranges, total);
-    if (threadIdx.x == 0)  // cuts at the very end lie in no request
-        for (int k = 0; cluster + k * clusters < units; ++k) {
-            const int range = (cluster + k * clusters) / p.tiles;
-            if (ranges.cut(range) == total) plan.unit[k].lo = total;
-            if (ranges.cut(range + 1) == total) plan.unit[k].hi = total;
-        }
-    int u = before + incl - mine;
-    for (int b = r0; b < r1; ++b) {
-        const int nb = tree_blocks(tree_cache_pages(tree_tokens(p, b)), tree_drafted(p, b)), n = tree_units(nb);
-        for (int k = 0; cluster + k * clusters < units; ++k) {
-            const int range = (cluster + k * clusters) / p.tiles;
-            const int lo = ranges.cut(range), hi = ranges.cut(range + 1);
-            if (lo >= u && lo < u + n) {
-                plan.unit[k].lo = tree_settled_cut(lo, u, nb);
-                plan.unit[k].first_req = b;
-                plan.unit[k].first_start = u;
-            }
-            if (hi >= u && hi < u + n) plan.unit[k].hi = tree_settled_cut(hi, u, nb);
-            // Is this the request's second range?  Its first block lies in the one before.
-            if (nb > kTreeWholeBlocks && lo > u + kTreeSegUnits && lo < u + n &&
-                ranges.cut(range - 1) <= u + kTreeSegUnits)
-                plan.cut[k] = b;
-        }
-        if (blockIdx.x == 0)  // the first and last range that hold its blocks, for the merge
-            p.plan[b] = nb > kTreeWholeBlocks ? make_int2(ranges.of(u + kTreeSegUnits), ranges.of(u + n - 1))
-                                              : make_int2(0, 0);
-        u += n;
-    }
-    return units;
-}
-
-// The cuts of the cluster's ranges, for the merge; by one thread.
-__device__ __forceinline__ void write_cuts(const MlaTreeParams& p, const TreePlan& plan, int cluster, int clusters,
-                                           int units) {
-    for (int k = 0; cluster + k * clusters < p.ranges * p.tiles; ++k) {  // ranges without work too
-        const int u = cluster + k * clusters;
-        if (u % p.tiles == 0) p.cuts[u / p.tiles] = u < units ? plan.cut[k] : -1;
-    }
-}
 
 constexpr int kRowsQ = 128;                     // rows of a CTA: two tokens' heads
 constexpr int kHalfPg = kPg / 2;                // entries of a CTA's half page
@@ -332,42 +140,7 @@ __device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t ba
                  : "memory");
 }
 
-// 32 rows of one slab of a request's drafted entries (rows behind the last arrive as zeros).
-__device__ __forceinline__ void load_drafts(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t row,
-                                            int32_t slab, int32_t request, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(slab), "r"(request), "r"(bar), "l"(policy)
-        : "memory");
-}
-
-// What some token of the current request sees of its drafted entries; by a whole warp.
-__device__ __forceinline__ uint64_t drafts_seen(const MlaTreeParams& p, const TreeWalk& w, int lane) {
-    uint64_t any = 0;
-    for (int j = lane; j < w.drafted; j += 32) any |= __ldg(p.mask + int64_t(w.req()) * p.tokens + j);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) any |= __shfl_xor_sync(0xffffffffu, any, o);
-    return any & low_bits(w.drafted);
-}
-
-// Zeroes the value rows of a page (in buffer pg) that nobody sees, up to the last 16-entry step of the product:
-// their weights are 0, but 0 x NaN is not.  By a whole warp, once the page has landed.  Out of line: the loops of
-// the roles run side by side and share an instruction cache.
-__device__ __noinline__ void zero_unseen(uint64_t used, int valid, uint8_t* v) {
-    const int lane = threadIdx.x & 31;
-    const int rows = (valid + 15) & ~15;
-#pragma unroll 1
-    for (int c = lane; c < rows * 8; c += 32) {
-        if ((used >> (c >> 3)) & 1u) continue;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) *reinterpret_cast<uint4*>(v + s * kSlabV + c * 16) = make_uint4(0, 0, 0, 0);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-}
-
-__global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
+__global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
     mla_tree_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap d_map,
                     const __grid_constant__ CUtensorMap o_map, const MlaTreeParams p) {
@@ -434,7 +207,7 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
     tc_fence_after_sync();
     if (threadIdx.x == 0 && rank == 0) write_cuts(p, ctl.plan, cluster, clusters, units);
     const uint32_t tmem_base = ctl.tmem_base;
-    TreeWalk w(cluster, clusters, units);
+    TreeWalk<kTileTokens> w(cluster, clusters, units);
     bool flagged = false;
 
     if (warp == 9) {
@@ -685,8 +458,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                             const int steps = good ? uniform((w.valid(page) + 15) >> 4) : 0;
                             if (good && w.zeroes(page)) {
                                 wait(&ctl.vz_full[pg], (zero_phase >> pg) & 1u);
-                                zero_unseen(page == w.np ? drafts : low_bits(w.valid(page)), w.valid(page),
-                                            tiles + kOffVq + pg * kGroupQ);
+                                zero_unseen<2>(page == w.np ? drafts : low_bits(w.valid(page)), w.valid(page),
+                                               tiles + kOffVq + pg * kGroupQ);
                                 wait(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u);
                                 zero_phase ^= 1u << pg;
                             }
@@ -758,8 +531,8 @@ __global__ void __launch_bounds__(kThreadsQ, 1) __cluster_dims__(4, 1, 1)
                         if (((bad >> (2 * (i & 15) + pg)) & 1u) || !w.zeroes(page)) continue;
                         if (!wait(&ctl.vz_full[pg], (zero_phase >> pg) & 1u)) break;
                         zero_phase ^= 1u << pg;
-                        zero_unseen(page == w.np ? drafts : low_bits(w.valid(page)), w.valid(page),
-                                            tiles + kOffVq + pg * kGroupQ);
+                        zero_unseen<2>(page == w.np ? drafts : low_bits(w.valid(page)), w.valid(page),
+                                       tiles + kOffVq + pg * kGroupQ);
                         if (issuer) mbar_arrive_remote(cluster_addr(&ctl.vz_ready[pg], leader));
                     }
                     wait(&ctl.r_full[n & 1], uint32_t(n >> 1) & 1u);
@@ -1092,7 +865,7 @@ cudaError_t mla_tree_quads(int* quads) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(4);
-    cfg.blockDim = dim3(kThreadsQ);
+    cfg.blockDim = dim3(kTreeThreads);
     cfg.dynamicSmemBytes = size_t(kSmemQ);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -1110,7 +883,7 @@ int mla_tree_ctas(const MlaTreeParams& p, int quads) {
 }
 
 cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cudaStream_t stream) {
-    p.quads = quads;
+    p.clusters = quads;
     const int units = p.ranges * p.tiles;
     if (p.ranges < 1 || p.ranges > kTreeMaxRanges || units > kTreeMaxRounds * quads) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
@@ -1118,7 +891,7 @@ cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cu
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(mla_tree_ctas(p, quads)));
-    cfg.blockDim = dim3(kThreadsQ);
+    cfg.blockDim = dim3(kTreeThreads);
     cfg.dynamicSmemBytes = size_t(kSmemQ);
     cfg.stream = stream;
     cfg.attrs = attr;

@@ -26,7 +26,7 @@ DSA_PLAN int tree_settled_cut(int cut, int u, int blocks) {
 }
 
 // Tiles of drafted tokens, each a unit in every range.
-constexpr int kTileTokens = 4;
+constexpr int kTileTokens = 4, kPairTokens = 2;  // of a cluster of four CTAs, of two
 DSA_PLAN int tree_tiles(int tokens) { return (tokens + kTileTokens - 1) / kTileTokens; }
 
 // The most ranges of a call on `clusters` clusters: as many as fill them in few rounds.  A round more is worth
