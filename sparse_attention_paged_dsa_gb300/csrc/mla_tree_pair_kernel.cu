@@ -35,7 +35,10 @@
 // What bounds it: what an SM takes in, 33 bytes a cycle: 4,220 cycles a block, and the loop runs
 // at 4,700; of HBM's time it needs 1.5 (64 requests of 65536 tokens 268 us, 4,500 GB/s; a CTA
 // for each token took 354).  16 x 131072 139 us (183), 64 x 8192 65 (75), 1 x 1048576 80 (99).
-// Fetching the next pages into L2 one to three blocks ahead did not help (275 to 281).
+// Not kept: the next pages fetched into L2 one to three blocks ahead (275 to 281; the copy engine
+// issues that traffic too); half of a CTA's keys kept as its values, the other half loaded over
+// with the rest of them (832 bytes an entry and CTA, but a block's buffers go through load,
+// scores, load, product before the next but one can come: 267, 142, 67 and 84 us).
 //
 // Every wait is bounded (about 1 s) but the cluster barriers, which every thread reaches, and
 // the softmax warps' own, which they meet in step whatever fails; a timeout sets an error bit,
@@ -354,14 +357,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                     const int blocks = uniform(w.bhi - w.blo);
                     const uint64_t drafts = drafts_seen(p, w, lane);
                     uint32_t fresh = 1, bad = 0;
-    #pragma unroll 1
+#pragma unroll 1
                     for (int i = 0; i < blocks && ok; ++i, ++nv) {
                         if ((i & 15) == 0)
                             bad = __ballot_sync(0xffffffffu, tree_page_of_lane(p, w, 2 * (w.blo + i), lane) == -1);
                         if (i == 0) wait(&ctl.o_empty, uint32_t(seg & 1) ^ 1u);
-                        // (cluster scope: the weights are the other CTA's ordinary stores too)
+                        // (the weights are read in their writers' SMs, behind the writers' fences: no cluster scope)
                         wait(&ctl.p_full, uint32_t(nv & 1));
-    #pragma unroll
+#pragma unroll
                         for (int pg = 0; pg < 2; ++pg) {
                             const int page = 2 * (w.blo + i) + pg;
                             const bool good = !((bad >> (2 * (i & 15) + pg)) & 1u);
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                                 wait(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u);
                                 zero_phase ^= 1u << pg;
                             }
-    #pragma unroll
+#pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const int g = 2 * pg + h;
                                 if (!wait(&ctl.v_full[g], uint32_t(nv & 1))) break;
@@ -387,10 +390,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                                                       (kk == 0 && fresh) ? 0u : 1u);
                                     };
                                     if (steps == 4) {
-    #pragma unroll
+#pragma unroll
                                         for (int kk = 0; kk < 4; ++kk) step(kk);
                                     } else {
-    #pragma unroll 1
+#pragma unroll 1
                                         for (int kk = 0; kk < steps; ++kk) step(kk);
                                     }
                                     umma2_commit(&ctl.v_empty[g]);
