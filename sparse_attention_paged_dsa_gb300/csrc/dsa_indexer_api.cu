@@ -370,16 +370,16 @@ size_t dense_workspace_bytes(int groups, int32_t next_n) {
 constexpr int kTicketWord = 32;  // of the workspace header: the page update's, 0 between calls
 
 // From this many tokens x context on, a tree of two tokens or more is worth a kernel on clusters.  Of two CTAs (us,
-// dense kernel and that one, two tokens each: 4 x 65536 context 41.5, 41.5; 1 x 262144 38, 37; 16 x 131072 183, 139;
-// 64 x 8192 75, 65; 64 x 65536 354, 268), or of four (1 request, 4 tokens, 131072 context 44, 46; 4 x 8, 8192 36, 40;
+// dense kernel and that one, two tokens each: 4 x 65536 context 41.5, 41.5; 1 x 262144 38, 37; 16 x 131072 183, 131;
+// 64 x 8192 75, 65; 64 x 65536 354, 244), or of four (1 request, 4 tokens, 131072 context 44, 46; 4 x 8, 8192 36, 40;
 // 16 x 8, 4096 58, 58; 1 x 16, 32768 52, 46; 64 x 8, 8192 212, 134; 16 x 32, 131072 2996, 1275).
 constexpr int64_t kTreeWork = int64_t(1) << 19;
 // But not two tokens of requests of a page or two, where a request's start and end count (512: 600 of them 73, 85,
 // 1024 121, 140; 768: 85, 84 and 141, 136).
 constexpr int64_t kPairContext = 512;
 
-// Tree decode: header, cuts, plan, flags, then two partial outputs per range and token, of the kernel that the
-// call takes (the dense one may have to do a call again: it makes its own plan, in the same place).
+// Tree decode: header, cuts, plan (of each tile), flags, then two partial outputs per range and token, of the kernel
+// that the call takes (the dense one may have to do a call again: it makes its own plan, in the same place).
 struct TreeShape {
     int groups;                   // of the dense kernel
     int clusters, tiles, ranges;  // of the one on clusters: of two CTAs for two tokens, of four for more
@@ -387,13 +387,18 @@ struct TreeShape {
         : groups(dense_groups(sms, tokens)), clusters(tokens > dsa::kPairTokens ? quads : pairs),
           tiles(tokens > dsa::kPairTokens ? dsa::tree_tiles(tokens) : 1),
           ranges(tokens < dsa::kPairTokens ? 0 : dsa::tree_ranges(tiles, clusters)) {}
-    size_t parts(int32_t tokens) const { return dense_parts(groups > ranges ? groups : ranges, tokens); }
+    size_t parts(int32_t tokens) const {
+        const size_t dense = dense_parts(groups, tokens), tiled = dense_parts(ranges * tiles, dsa::tree_places(tokens));
+        return dense > tiled ? dense : tiled;
+    }
     size_t workspace_bytes(int32_t tokens) const {
         return dsa::kWorkspaceHeaderBytes + kTreePlanBytes +
                parts(tokens) * dsa::kMlaHeads * (dsa::kMlaDv + 1) * sizeof(float);
     }
-    static constexpr size_t kTreePlanBytes =
-        kDensePlanBytes + size_t(dsa::kTreeMaxFlags + 64) * sizeof(uint32_t);
+    static constexpr size_t kCutBytes = size_t(dsa::kTreeMaxUnits) * sizeof(int32_t);
+    static constexpr size_t kFlagsAt = kCutBytes + size_t(dsa::kTreeMaxTiles) * DSA_MAX_BATCH * sizeof(int2);
+    static constexpr size_t kTreePlanBytes = kFlagsAt + size_t(dsa::kTreeMaxFlags + 64) * sizeof(uint32_t);
+    static_assert(kCutBytes >= kDenseCutBytes, "the dense kernel's cuts fit");
 };
 
 dsa_status_t run_rmsnorm(dsa::RmsNormParams p, void* stream) {
@@ -949,8 +954,8 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
     p.out = static_cast<__nv_bfloat16_raw*>(out);
     p.lse = lse;
     p.cuts = reinterpret_cast<int32_t*>(ws);
-    p.plan = reinterpret_cast<int2*>(ws + kDenseCutBytes);
-    uint32_t* flags = reinterpret_cast<uint32_t*>(ws + kDensePlanBytes);
+    p.plan = reinterpret_cast<int2*>(ws + TreeShape::kCutBytes);
+    uint32_t* flags = reinterpret_cast<uint32_t*>(ws + TreeShape::kFlagsAt);
     p.flags = flags;
     p.again = flags + dsa::kTreeMaxFlags;
     p.o_part = reinterpret_cast<float*>(ws + TreeShape::kTreePlanBytes);
@@ -968,7 +973,8 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
     p.counts = token_counts_opt;
     if (tokens >= dsa::kPairTokens && int64_t(batch) * tokens * max_context > kTreeWork &&
         (tokens > dsa::kPairTokens || max_context > kPairContext) &&
-        shape.ranges * shape.tiles <= dsa::kTreeMaxRounds * shape.clusters) {
+        shape.ranges * shape.tiles <= dsa::kTreeMaxRounds * shape.clusters &&
+        shape.ranges * shape.tiles <= dsa::kTreeMaxUnits) {
         dsa::MlaTreeParams t{};
         t.q = static_cast<const __nv_bfloat16_raw*>(q);
         t.page_table = page_table;

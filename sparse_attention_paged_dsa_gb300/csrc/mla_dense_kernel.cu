@@ -64,7 +64,7 @@
 
 #include "indexer_kernels.h"
 #include "mla_common.cuh"
-#include "mla_dense_plan.h"
+#include "mla_tree_plan.h"
 #include "sm103_ptx.cuh"
 
 namespace dsa {
@@ -985,15 +985,18 @@ cudaError_t launch(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CU
     m.counts = p.counts;
     m.tokens = p.tokens;
     m.by_cut = p.merge_by_cut;
-    m.rows = (p.merge_by_cut ? p.groups : p.batch) * p.tokens;
-    m.one_head = m.rows <= 16;
+    m.count = p.merge_by_cut ? p.groups : p.batch;
+    m.one_head = m.count * p.tokens <= 16;
     if (p.redo > 0) {  // one merge, for this kernel's partials or those of the one before
         m.again = p.again;
         m.tiled = 1;
-        m.by_cut_again = m.by_cut, m.rows_again = m.rows;
-        m.by_cut = p.batch > p.first_ranges;
-        m.rows = (m.by_cut ? p.first_ranges : p.batch) * p.tokens;
-        m.one_head = m.rows <= 16 && p.first_ranges >= 32 * p.batch;
+        m.batch = p.batch;
+        m.places = tree_places(p.tokens);
+        m.by_cut_again = m.by_cut, m.count_again = m.count;
+        const int units = p.first_ranges * tree_tiles(p.tokens);
+        m.by_cut = m.flat = p.batch * p.tokens > units * kTileTokens;
+        m.count = m.by_cut ? units : p.batch;
+        m.one_head = p.batch * p.tokens <= 16 && p.first_ranges >= 32 * p.batch;
     }
     return launch_mla_merge(m, stream);
 }

@@ -21,12 +21,15 @@ constexpr float kLn2T = 0.69314718055994531f;
 struct UnitT {
     int lo, hi;                  // the range, in units of the plan
     int first_req, first_start;  // request of its first unit, and where that request's units start
+    int range, tile;             // among the ranges of all tiles
 };
 
 // In shared memory: a cluster's units.
 struct TreePlan {
     UnitT unit[kTreeMaxRounds];
     int cut[kTreeMaxRounds];     // the request that the range is the second one of, or -1
+    int first[kTreeMaxTiles + 1];  // a tile's first range
+    int line[kTreeMaxTiles];       // a tile's plan units
     int warp_units[16];
     uint64_t warp_best[16];
 };
@@ -65,13 +68,12 @@ __device__ __forceinline__ uint64_t low_bits(int n) { return n >= 64 ? ~uint64_t
 // in its tile of kTile.
 template <int kTile>
 struct TreeWalk {
-    int k, rounds, first, step;  // units first, first + step, ...
+    int k, rounds;
     int b, u0, lo, hi;
     int range, tile;
     int np, live, drafted, nb, blo, bhi;  // current request: cache pages, entries, drafted tokens, blocks
     __device__ __forceinline__ TreeWalk(int first_, int step_, int units)
-        : k(-1), rounds(first_ < units ? (units - first_ + step_ - 1) / step_ : 0), first(first_), step(step_), b(0),
-          u0(0), lo(0), hi(0) {}
+        : k(-1), rounds(first_ < units ? (units - first_ + step_ - 1) / step_ : 0), b(0), u0(0), lo(0), hi(0) {}
     __device__ __forceinline__ bool next(const MlaTreeParams& p, const TreePlan& plan) {
         while (true) {
             while (b < p.batch && u0 < hi) {
@@ -80,18 +82,16 @@ struct TreeWalk {
                 np = tree_cache_pages(seq);
                 drafted = tree_drafted(p, b);
                 nb = tree_blocks(np, drafted);
-                const int base = u0 + kTreeSegUnits, end = u0 + tree_units(nb);
+                const int base = u0 + kTreeSegUnits, end = u0 + (kTile * tile < drafted ? tree_units(nb) : 0);
                 blo = max(lo, base) - base;
                 bhi = min(hi, end) - base;
                 ++b;
                 u0 = end;
-                if (nb > 0 && bhi > blo && kTile * tile < drafted) return true;
+                if (bhi > blo) return true;
             }
             if (++k >= rounds) return false;
-            const int u = first + k * step;
-            range = u / p.tiles;
-            tile = u - range * p.tiles;
-            lo = plan.unit[k].lo, hi = plan.unit[k].hi, b = plan.unit[k].first_req, u0 = plan.unit[k].first_start;
+            const volatile UnitT& unit = plan.unit[k];  // (the compiler has moved these loads above the barrier)
+            range = unit.range, tile = unit.tile, lo = unit.lo, hi = unit.hi, b = unit.first_req, u0 = unit.first_start;
         }
     }
     __device__ __forceinline__ int req() const { return b - 1; }
@@ -118,43 +118,81 @@ __device__ __forceinline__ int tree_page_of_lane(const MlaTreeParams& p, const T
 
 __device__ __forceinline__ void clear_plan(const MlaTreeParams& p, TreePlan& plan) {
     for (int k = 0; k < kTreeMaxRounds; ++k) {
-        plan.unit[k] = {0, 0, p.batch, 0};
+        plan.unit[k] = {0, 0, p.batch, 0, 0, 0};
         plan.cut[k] = -1;
     }
+    for (int t = 0; t <= kTreeMaxTiles; ++t) plan.first[t] = 0;
 }
 
-// Finds the cluster's units, from the prefix sums of the requests' plan units; returns how many the call
-// has.  For all threads, the plan cleared; it is there after the caller's next barrier.
+// Finds the cluster's units, from the prefix sums of the requests' plan units (a tile's: of those that have tokens in
+// it); returns how many the call has.  For all threads, the plan cleared; it is there after the caller's next barrier.
+template <int kTile>
 __device__ __forceinline__ int find_units(const MlaTreeParams& p, TreePlan& plan, int cluster, int clusters) {
     const int warp = int(threadIdx.x) >> 5, lane = threadIdx.x & 31;
     const int per = (p.batch + kTreeThreads - 1) / kTreeThreads;
     const int r0 = min(int(threadIdx.x) * per, p.batch), r1 = min(r0 + per, p.batch);
-    int mine = 0;
-    for (int b = r0; b < r1; ++b) {
-        if (blockIdx.x == 0) {
+    const bool ragged = kTile == kTileTokens && p.counts;  // (a pair has one tile)
+    const auto blocks_in = [&](int b, int tile) {
+        const int drafted = tree_drafted(p, b);
+        return kTile * tile < drafted ? tree_blocks(tree_cache_pages(tree_tokens(p, b)), drafted) : 0;
+    };
+    // The tile whose prefix sums are known: where this thread's requests start, and its plan units.
+    int start = 0, total = 0, known = -1;
+    const auto scan = [&](int tile) {
+        if (known == tile || (known >= 0 && !ragged)) return;
+        const bool again = known >= 0;
+        known = tile;
+        int mine = 0;
+#pragma unroll 1
+        for (int b = r0; b < r1; ++b) mine += tree_units(blocks_in(b, tile));
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (again) __syncthreads();
+        if (lane == 31) plan.warp_units[warp] = incl;
+        __syncthreads();
+        start = incl - mine, total = 0;
+        for (int w = 0; w < kTreeThreads / 32; ++w) {
+            if (w < warp) start += plan.warp_units[w];
+            total += plan.warp_units[w];
+        }
+    };
+    if (blockIdx.x == 0)
+        for (int b = r0; b < r1; ++b) {
             const int seq = __ldg(p.seq_lens + b);
             if (seq < 0 || int64_t(seq) > p.max_context) atomicOr(p.err, kErrSeqLenClamped);
             if (p.counts && tree_drafted(p, b) != __ldg(p.counts + b)) atomicOr(p.err, kErrBadRange);
         }
-        mine += tree_units(tree_blocks(tree_cache_pages(tree_tokens(p, b)), tree_drafted(p, b)));
+    scan(0);
+    if (ragged) {  // what each tile has
+        for (int b = r0; b < r1; ++b)
+            if (const int n = tree_units(blocks_in(b, 0)))
+                atomicAdd(&plan.first[(tree_drafted(p, b) - 1) / kTile], n);
+        __syncthreads();
+        if (int(threadIdx.x) < p.tiles) {
+            int sum = 0;
+            for (int t = threadIdx.x; t < p.tiles; ++t) sum += plan.first[t];
+            plan.line[threadIdx.x] = sum;
+        }
+        __syncthreads();
     }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) plan.warp_units[warp] = incl;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < kTreeThreads / 32; ++w) {
-        if (w < warp) before += plan.warp_units[w];
-        total += plan.warp_units[w];
-    }
-    // How many ranges: a thread for each number.
+    // How many ranges (ragged: of tile 0): a thread for each number.
     uint64_t best = ~uint64_t(0);
-    for (int r = int(threadIdx.x) + 1; r <= min(p.ranges, total); r += kTreeThreads) {
-        const uint64_t cost = uint64_t(tree_cost(r, total, p.tiles, p.clusters, p.tokens)) << 16 | uint64_t(r);
+    for (int r = int(threadIdx.x) + 1; r <= min(ragged ? kTreeMaxRanges : p.ranges, total); r += kTreeThreads) {
+        uint64_t cost;
+        if (ragged) {
+            const int each = (total + r - 1) / r;
+            int units = 0;
+            for (int t = 0; t < p.tiles; ++t) units += tree_line_ranges(plan.line[t], each);
+            if (units > p.ranges * p.tiles) continue;  // (one of each tile never are)
+            cost = uint64_t(tree_cost_ragged(units, each, p.tiles, p.clusters));
+        } else {
+            cost = uint64_t(tree_cost(r, total, p.tiles, p.clusters, p.tokens));
+        }
+        cost = cost << 16 | uint64_t(r);
         best = cost < best ? cost : best;
     }
 #pragma unroll
@@ -166,20 +204,51 @@ __device__ __forceinline__ int find_units(const MlaTreeParams& p, TreePlan& plan
     __syncthreads();
     for (int w = 0; w < kTreeThreads / 32; ++w) best = plan.warp_best[w] < best ? plan.warp_best[w] : best;
     const int nranges = total > 0 ? int(best & 0xFFFF) : 1;
-    const int units = nranges * p.tiles;
-    const Ranges ranges(nranges, total);
-    if (threadIdx.x == 0)  // cuts at the very end lie in no request
-        for (int k = 0; cluster + k * clusters < units; ++k) {
-            const int range = (cluster + k * clusters) / p.tiles;
-            if (ranges.cut(range) == total) plan.unit[k].lo = total;
-            if (ranges.cut(range + 1) == total) plan.unit[k].hi = total;
+    int units = nranges * p.tiles;
+    if (ragged) {
+        const int each = total > 0 ? (total + nranges - 1) / nranges : 1;
+        if (threadIdx.x == 0) {
+            int n = 0;
+            for (int t = 0; t < p.tiles; ++t) {
+                plan.first[t] = n;
+                n += tree_line_ranges(plan.line[t], each);
+            }
+            plan.first[p.tiles] = n;
         }
-    int u = before + incl - mine;
-    for (int b = r0; b < r1; ++b) {
-        const int nb = tree_blocks(tree_cache_pages(tree_tokens(p, b)), tree_drafted(p, b)), n = tree_units(nb);
-        for (int k = 0; cluster + k * clusters < units; ++k) {
-            const int range = (cluster + k * clusters) / p.tiles;
-            const int lo = ranges.cut(range), hi = ranges.cut(range + 1);
+        __syncthreads();
+        units = plan.first[p.tiles];
+        for (int i = threadIdx.x; i < units; i += kTreeThreads) {
+            int t = 0;
+            while (plan.first[t + 1] <= i) ++t;
+            const int rank = tree_rank(plan.first, p.tiles, t, i - plan.first[t]);
+            if (rank % clusters == cluster) {
+                plan.unit[rank / clusters].range = i;
+                plan.unit[rank / clusters].tile = t;
+            }
+        }
+        __syncthreads();
+    }
+    const auto first_of = [&](int tile) { return ragged ? plan.first[tile] : tile * nranges; };
+#pragma unroll 1
+    for (int k = 0; cluster + k * clusters < units; ++k) {
+        int tile, g;
+        if (ragged) {
+            tile = plan.unit[k].tile, g = plan.unit[k].range - plan.first[tile];
+        } else {
+            const int u = cluster + k * clusters;
+            g = u / p.tiles, tile = u - g * p.tiles;
+            if (threadIdx.x == 0) plan.unit[k].range = tile * nranges + g, plan.unit[k].tile = tile;
+        }
+        scan(tile);
+        const Ranges ranges(first_of(tile + 1) - first_of(tile), total);
+        const int lo = ranges.cut(g), hi = ranges.cut(g + 1);
+        if (threadIdx.x == 0) {  // cuts at the very end lie in no request
+            if (lo == total) plan.unit[k].lo = total;
+            if (hi == total) plan.unit[k].hi = total;
+        }
+        int u = start;
+        for (int b = r0; b < r1; ++b) {
+            const int nb = blocks_in(b, tile), n = tree_units(nb);
             if (lo >= u && lo < u + n) {
                 plan.unit[k].lo = tree_settled_cut(lo, u, nb);
                 plan.unit[k].first_req = b;
@@ -187,24 +256,42 @@ __device__ __forceinline__ int find_units(const MlaTreeParams& p, TreePlan& plan
             }
             if (hi >= u && hi < u + n) plan.unit[k].hi = tree_settled_cut(hi, u, nb);
             // Is this the request's second range?  Its first block lies in the one before.
-            if (nb > kTreeWholeBlocks && lo > u + kTreeSegUnits && lo < u + n &&
-                ranges.cut(range - 1) <= u + kTreeSegUnits)
+            if (nb > kTreeWholeBlocks && lo > u + kTreeSegUnits && lo < u + n && ranges.cut(g - 1) <= u + kTreeSegUnits)
                 plan.cut[k] = b;
+            u += n;
         }
-        if (blockIdx.x == 0)  // the first and last range that hold its blocks, for the merge
-            p.plan[b] = nb > kTreeWholeBlocks ? make_int2(ranges.of(u + kTreeSegUnits), ranges.of(u + n - 1))
-                                              : make_int2(0, 0);
-        u += n;
     }
+    // The first and last range that hold a request's blocks, for the merge: a tile a CTA.
+#pragma unroll 1
+    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+        scan(tile);
+        const int first = first_of(tile);
+        const Ranges ranges(max(first_of(tile + 1) - first, 1), total);
+        int u = start;
+        for (int b = r0; b < r1; ++b) {
+            const int nb = blocks_in(b, tile), n = tree_units(nb);
+            p.plan[tile * p.batch + b] = nb > kTreeWholeBlocks ? make_int2(first + ranges.of(u + kTreeSegUnits),
+                                                                           first + ranges.of(u + n - 1))
+                                                               : make_int2(0, 0);
+            u += n;
+        }
+    }
+    __syncwarp();
     return units;
 }
 
-// The cuts of the cluster's ranges, for the merge; by one thread.
+// The cuts of the cluster's ranges, and its part of those that no range has, for the merge (16 request + tile, or
+// -1); by one thread.
 __device__ __forceinline__ void write_cuts(const MlaTreeParams& p, const TreePlan& plan, int cluster, int clusters,
                                            int units) {
-    for (int k = 0; cluster + k * clusters < p.ranges * p.tiles; ++k) {  // ranges without work too
+    for (int k = 0; cluster + k * clusters < p.ranges * p.tiles; ++k) {
         const int u = cluster + k * clusters;
-        if (u % p.tiles == 0) p.cuts[u / p.tiles] = u < units ? plan.cut[k] : -1;
+        const volatile UnitT& unit = plan.unit[k];
+        const int b = *const_cast<const volatile int*>(&plan.cut[k]);
+        if (u < units)
+            p.cuts[unit.range] = b < 0 ? -1 : 16 * b + unit.tile;
+        else
+            p.cuts[u] = -1;
     }
 }
 

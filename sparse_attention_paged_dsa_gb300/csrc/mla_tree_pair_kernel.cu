@@ -33,12 +33,15 @@
 // second product's operand.
 //
 // What bounds it: what an SM takes in, 33 bytes a cycle: 4,220 cycles a block, and the loop runs
-// at 4,700; of HBM's time it needs 1.5 (64 requests of 65536 tokens 268 us, 4,500 GB/s; a CTA
-// for each token took 354).  16 x 131072 139 us (183), 64 x 8192 65 (75), 1 x 1048576 80 (99).
-// Not kept: the next pages fetched into L2 one to three blocks ahead (275 to 281; the copy engine
-// issues that traffic too); half of a CTA's keys kept as its values, the other half loaded over
-// with the rest of them (832 bytes an entry and CTA, but a block's buffers go through load,
-// scores, load, product before the next but one can come: 267, 142, 67 and 84 us).
+// at about that; of HBM's time it needs 1.4 (64 requests of 65536 tokens 244 us, 4,950 GB/s; a
+// CTA for each token took 354).  16 x 131072 131 us (183), 64 x 8192 65 (75), 1 x 1048576 80
+// (99).  The loops of the roles run side by side and share an instruction cache: loaders and
+// issuers are rolled (311 us with them unrolled, and up to 15 % more or less with each change
+// anywhere else in the kernel).
+// Not kept: the next pages fetched into L2 one to three blocks ahead (a twentieth more; the copy
+// engine issues that traffic too); half of a CTA's keys kept as its values, the other half
+// loaded over with the rest of them (832 bytes an entry and CTA, but a block's buffers go
+// through load, scores, load, product before the next but one can come: 256 us).
 //
 // Every wait is bounded (about 1 s) but the cluster barriers, which every thread reaches, and
 // the softmax warps' own, which they meet in step whatever fails; a timeout sets an error bit,
@@ -91,7 +94,7 @@ static_assert(kSmemT <= 232448, "fits one CTA per SM");
 __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
     mla_tree_pair_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kv_map,
                          const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap d_map,
-                         const MlaTreeParams p) {
+                         const __grid_constant__ MlaTreeParams p) {
     extern __shared__ uint8_t smem_raw[];
     // Dynamic shared memory starts at the same offset in both CTAs, so the operands and barriers do too.
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -136,11 +139,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
 
-    const int units = find_units(p, ctl.plan, cluster, clusters);
+    const int units = find_units<kPairTokens>(p, ctl.plan, cluster, clusters);
     tc_fence_before_sync();
     cluster_sync_all();  // the barriers and the plan are there, in both CTAs
     tc_fence_after_sync();
     if (threadIdx.x == 0 && rank == 0) write_cuts(p, ctl.plan, cluster, clusters, units);
+    __syncwarp();
     const uint32_t tmem_base = ctl.tmem_base;
     TreeWalk<kPairTokens> w(cluster, clusters, units);
 
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                 // this CTA's page; -1: page 0 stands in, its entries are not used
                 const int id = __shfl_sync(0xffffffffu, id_l, 2 * (i & 15) + rank);
                 const int row = max(id, 0) * kPg;
-#pragma unroll
+#pragma unroll 1
                 for (int j = 0; j < kKeyGroups; ++j) {
                     if (!wait(&ctl.k_empty[j], uint32_t(n & 1) ^ 1u)) break;
                     if (issuer) {
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t sb = uint32_t(uniform(int(s_base)));
         bool ok = true;
         int n = 0;
-        uint32_t zero_fills[2] = {0, 0};
+        uint32_t zero_fills = 0;  // 16 bits for each page of a block (a request has one at most)
         const auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = ok && __all_sync(0xffffffffu, mbar_await(bar, parity, &ctl.abort));
             return ok;
@@ -238,12 +242,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll 1
             for (int i = 0; i < blocks; ++i, ++n) {
                 if ((i & 15) == 0) id_l = tree_page_of_lane(p, w, 2 * (w.blo + i), lane);
-#pragma unroll
+#pragma unroll 1
                 for (int pg = 0; pg < 2; ++pg) {
                     const int id = __shfl_sync(0xffffffffu, id_l, 2 * (i & 15) + pg);
                     const int row = max(id, 0) * kPg;
                     const bool zeroes = id != -1 && w.zeroes(2 * (w.blo + i) + pg);
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         const int g = 2 * pg + h;
                         if (!wait(&ctl.v_empty[g], uint32_t(n & 1) ^ 1u)) break;
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                         __syncwarp();
                         issued |= 1u << g;
                     }
-                    if (ok && zeroes) ++zero_fills[pg];
+                    if (ok && zeroes) zero_fills += 1u << (16 * pg);
                 }
                 if (!ok) break;
                 issued = 0;
@@ -285,7 +289,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                     if (fills > 0) wait_landed_t(&ctl.v_full[g], uint32_t(fills - 1) & 1u);
                 }
             for (int pg = 0; pg < 2; ++pg)
-                if (zero_fills[pg] > 0) wait_landed_t(&ctl.vz_full[pg], (zero_fills[pg] - 1) & 1u);
+                if (const uint32_t fills = (zero_fills >> (16 * pg)) & 0xFFFFu)
+                    wait_landed_t(&ctl.vz_full[pg], (fills - 1) & 1u);
             // After a timeout the two CTAs may have issued different copies, and what only the other counts
             // cannot be waited for here: a millisecond, a thousand times a copy's latency.
             if (*const_cast<volatile int*>(&ctl.abort)) {
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                 const uint32_t phase = uint32_t(nq & 1);
                 wait(&ctl.s_empty[buf], (uint32_t(nq >> 1) & 1u) ^ 1u);
                 const uint32_t d = tmem + kColST + 64u * buf;
-#pragma unroll
+#pragma unroll 1
                 for (int j = 0; j < kKeyGroups; ++j) {
                     if (!wait(&ctl.k_full[j], phase)) return;
                     tc_fence_after_sync();
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                         if (i == 0) wait(&ctl.o_empty, uint32_t(seg & 1) ^ 1u);
                         // (the weights are read in their writers' SMs, behind the writers' fences: no cluster scope)
                         wait(&ctl.p_full, uint32_t(nv & 1));
-#pragma unroll
+#pragma unroll 1
                         for (int pg = 0; pg < 2; ++pg) {
                             const int page = 2 * (w.blo + i) + pg;
                             const bool good = !((bad >> (2 * (i & 15) + pg)) & 1u);
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                                 wait(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u);
                                 zero_phase ^= 1u << pg;
                             }
-#pragma unroll
+#pragma unroll 1
                             for (int h = 0; h < 2; ++h) {
                                 const int g = 2 * pg + h;
                                 if (!wait(&ctl.v_full[g], uint32_t(nv & 1))) break;
@@ -560,7 +565,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
             const float sum = (ctl.part[0][row] + ctl.part[1][row]) + (ctl.part[2][row] + ctl.part[3][row]);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (0: nothing was seen; a NaN goes on to both outputs)
             const bool whole = w.blo == 0 && w.bhi == w.nb;
-            const int64_t at = whole ? q_row : (int64_t(w.range) * p.tokens + token) * 2 + (w.blo == 0 ? 1 : 0);
+            const int64_t at = whole ? q_row : (int64_t(w.range) * kPairTokens + token) * 2 + (w.blo == 0 ? 1 : 0);
             if (live_token && part == 0)
                 (whole ? p.lse : p.lse_part)[at * kMlaHeads + row] =
                     sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2T;
@@ -683,10 +688,12 @@ cudaError_t launch_mla_tree_pair(const MlaTreeMaps& m, MlaTreeParams p, int pair
     g.lse = p.lse;
     g.counts = p.counts;
     g.tokens = p.tokens;
+    g.batch = p.batch;
     g.tiled = 1;
+    g.places = kPairTokens;
     g.by_cut = p.batch > p.ranges;
-    g.rows = (g.by_cut ? p.ranges : p.batch) * p.tokens;
-    g.one_head = g.rows <= 16 && p.ranges >= 32 * p.batch;
+    g.count = g.by_cut ? p.ranges : p.batch;
+    g.one_head = g.count * p.tokens <= 16 && p.ranges >= 32 * p.batch;
     return launch_mla_merge(g, stream);
 }
 
