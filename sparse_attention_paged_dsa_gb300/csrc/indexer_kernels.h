@@ -192,10 +192,8 @@ struct MlaMergeParams {
     const int32_t* counts;     // [batch] tokens of each request, or null: all
     const uint32_t* again;     // not 0 there: the dense kernel has done the call again (null: it may not)
     int32_t tokens, batch;
-    int32_t by_cut, count;             // cuts or requests
-    int32_t by_cut_again, count_again; // of the dense kernel's second try
-    int32_t flat;              // the grid has cuts x 4 in one dimension (tiled ones, that may have a second try)
-    int32_t places;            // tree_places
+    int32_t by_cut, rows;              // requests (or cuts) x tokens (cuts of tiled partials: x places)
+    int32_t by_cut_again, rows_again;  // of the dense kernel's second try
     int32_t tiled;             // the partials are of tiles of four tokens (tree_places of them a range, plans
                                // [tiles, batch], cuts 16 request + tile) and lie as tiled_part says (those of a
                                // second try never do)

@@ -985,18 +985,17 @@ cudaError_t launch(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CU
     m.counts = p.counts;
     m.tokens = p.tokens;
     m.by_cut = p.merge_by_cut;
-    m.count = p.merge_by_cut ? p.groups : p.batch;
-    m.one_head = m.count * p.tokens <= 16;
+    m.rows = (p.merge_by_cut ? p.groups : p.batch) * p.tokens;
+    m.one_head = m.rows <= 16;
     if (p.redo > 0) {  // one merge, for this kernel's partials or those of the one before
         m.again = p.again;
         m.tiled = 1;
         m.batch = p.batch;
-        m.places = tree_places(p.tokens);
-        m.by_cut_again = m.by_cut, m.count_again = m.count;
-        const int units = p.first_ranges * tree_tiles(p.tokens);
-        m.by_cut = m.flat = p.batch * p.tokens > units * kTileTokens;
-        m.count = m.by_cut ? units : p.batch;
-        m.one_head = p.batch * p.tokens <= 16 && p.first_ranges >= 32 * p.batch;
+        m.by_cut_again = m.by_cut, m.rows_again = m.rows;
+        const int places = p.first_ranges * tree_tiles(p.tokens) * tree_places(p.tokens);
+        m.by_cut = p.batch * p.tokens > places;
+        m.rows = m.by_cut ? places : p.batch * p.tokens;
+        m.one_head = m.rows <= 16 && p.first_ranges >= 32 * p.batch;
     }
     return launch_mla_merge(m, stream);
 }

@@ -15,21 +15,29 @@ namespace {
 // o[r] = sum_i exp(lse_i - lse) o_i over the partials of a split request, lse = log sum_i exp(lse_i).
 // 512 threads.  128 of them per 512 dims, four heads a CTA; or (kOneHead: few rows, each split many ways)
 // 64 per 256 dims, half a head a CTA, whose partials go to the eight groups in turn.  Grid (heads / 4 or
-// heads x 2, tokens, requests or cuts; or, flat, heads / 4, cuts x 4).
+// heads x 2, requests or cuts x tokens).
 template <bool kOneHead, bool kTiled>
-__device__ __forceinline__ void merge_row(const MlaMergeParams& p, int token, int b, bool by_cut, bool tiled) {
+__device__ __forceinline__ void merge_row(const MlaMergeParams& p, int at, bool by_cut, bool tiled) {
     __shared__ float wgt[kOneHead ? 1 : 4][kMlaMaxGroups];
     __shared__ float4 acc_s[kOneHead ? 7 : 1][64];
     const int quarter = threadIdx.x >> (kOneHead ? 6 : 7);
     const int d4 = kOneHead ? (int(blockIdx.x) & 1) * 64 + (threadIdx.x & 63) : threadIdx.x & 127;
     const int h = kOneHead ? int(blockIdx.x) >> 1 : int(blockIdx.x) * 4 + quarter;
-    if (by_cut) {
-        b = p.cuts[b];
-        if (b < 0) return;
-        if (kTiled && tiled) {
-            token += kTileTokens * (b & 15), b >>= 4;
-            if (token >= p.tokens) return;
+    const int places = kTiled && tiled ? tree_places(p.tokens) : p.tokens;  // of a range's partials
+    int token = at % p.tokens, b;
+    if constexpr (kTiled) {
+        b = at / p.tokens;
+        if (by_cut) {
+            b = p.cuts[at / places];
+            if (b < 0) return;
+            if (tiled) {
+                token = kTileTokens * (b & 15) + at % places, b >>= 4;
+                if (token >= p.tokens) return;
+            }
         }
+    } else {
+        b = by_cut ? p.cuts[at / p.tokens] : at / p.tokens;
+        if (b < 0) return;
     }
     if (p.counts && token >= __ldg(p.counts + b)) return;
     const int64_t row = int64_t(b) * p.tokens + token;
@@ -37,7 +45,6 @@ __device__ __forceinline__ void merge_row(const MlaMergeParams& p, int token, in
     if (g.x == g.y) return;  // one range: written by the attention kernel
     const int S = g.y - g.x + 1;
     // partial i: range g.x + i; the first one ends in the next range, the others began earlier
-    const int places = kTiled && tiled ? p.places : p.tokens;  // of a range's partials
     const int place = kTiled && tiled ? token % kTileTokens : token;
     const auto part = [&](int i) { return (int64_t(g.x + i) * places + place) * 2 + (i == 0 ? 1 : 0); };
     // The first partials are on their way while the weights are made.
@@ -103,30 +110,24 @@ __device__ __forceinline__ void merge_row(const MlaMergeParams& p, int token, in
 // kTiled: of the tree decode's kernels on clusters.  Of one of them the dense kernel may have done the call again,
 // with a plan and partials of its own.
 template <bool kOneHead, bool kTiled>
-__global__ void __launch_bounds__(512, kOneHead || kTiled ? 3 : 4) mla_merge_kernel(const MlaMergeParams p) {
+__global__ void __launch_bounds__(512) mla_merge_kernel(const MlaMergeParams p) {
     pdl_wait_prior_grid();
     pdl_allow_next_grid();
     const bool again = kTiled && p.again && *p.again != 0;
     const bool by_cut = again ? p.by_cut_again : p.by_cut;
-    int token = blockIdx.y, b = blockIdx.z;
-    if (kTiled && p.flat) {
-        b = again ? token / p.tokens : token / kTileTokens;
-        token = again ? token % p.tokens : token % kTileTokens;
-    }
-    if (b < (again ? p.count_again : p.count)) merge_row<kOneHead, kTiled>(p, token, b, by_cut, !again);
+    const int rows = again ? p.rows_again : p.rows;
+    if (int(blockIdx.y) < rows) merge_row<kOneHead, kTiled>(p, blockIdx.y, by_cut, !again);
 }
 
 }  // namespace
 
 cudaError_t launch_mla_merge(const MlaMergeParams& p, cudaStream_t stream) {
-    const int again = p.again ? p.count_again : 0;
-    const unsigned y = p.flat ? (p.count * kTileTokens > again * p.tokens ? p.count * kTileTokens : again * p.tokens)
-                              : (p.by_cut && p.tiled && !p.again ? p.places : p.tokens);
+    const int rows = p.again && p.rows_again > p.rows ? p.rows_again : p.rows;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.one_head ? kMlaHeads * 2 : kMlaHeads / 4, y, p.flat ? 1 : (p.count > again ? p.count : again));
+    cfg.gridDim = dim3(p.one_head ? kMlaHeads * 2 : kMlaHeads / 4, unsigned(rows));
     cfg.blockDim = dim3(512);
     cfg.stream = stream;
     cfg.attrs = attr;

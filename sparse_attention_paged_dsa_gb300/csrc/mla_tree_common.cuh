@@ -73,7 +73,8 @@ struct TreeWalk {
     int range, tile;
     int np, live, drafted, nb, blo, bhi;  // current request: cache pages, entries, drafted tokens, blocks
     __device__ __forceinline__ TreeWalk(int first_, int step_, int units)
-        : k(-1), rounds(first_ < units ? (units - first_ + step_ - 1) / step_ : 0), b(0), u0(0), lo(0), hi(0) {}
+        : k(-1), rounds(first_ < units ? (units - first_ + step_ - 1) / step_ : 0), b(0), u0(0), lo(0), hi(0),
+          range(0), tile(0) {}
     __device__ __forceinline__ bool next(const MlaTreeParams& p, const TreePlan& plan) {
         while (true) {
             while (b < p.batch && u0 < hi) {
@@ -90,7 +91,7 @@ struct TreeWalk {
                 if (bhi > blo) return true;
             }
             if (++k >= rounds) return false;
-            const volatile UnitT& unit = plan.unit[k];  // (the compiler has moved these loads above the barrier)
+            const volatile UnitT& unit = plan.unit[k];  // (one build read these above the caller's barrier, where they were still cleared)
             range = unit.range, tile = unit.tile, lo = unit.lo, hi = unit.hi, b = unit.first_req, u0 = unit.first_start;
         }
     }
@@ -276,7 +277,7 @@ __device__ __forceinline__ int find_units(const MlaTreeParams& p, TreePlan& plan
             u += n;
         }
     }
-    __syncwarp();
+    __syncthreads();
     return units;
 }
 

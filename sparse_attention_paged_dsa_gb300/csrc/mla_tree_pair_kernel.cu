@@ -690,10 +690,9 @@ cudaError_t launch_mla_tree_pair(const MlaTreeMaps& m, MlaTreeParams p, int pair
     g.tokens = p.tokens;
     g.batch = p.batch;
     g.tiled = 1;
-    g.places = kPairTokens;
     g.by_cut = p.batch > p.ranges;
-    g.count = g.by_cut ? p.ranges : p.batch;
-    g.one_head = g.count * p.tokens <= 16 && p.ranges >= 32 * p.batch;
+    g.rows = (g.by_cut ? p.ranges : p.batch) * p.tokens;
+    g.one_head = g.rows <= 16 && p.ranges >= 32 * p.batch;
     return launch_mla_merge(g, stream);
 }
 
