@@ -495,7 +495,7 @@ DSA_API dsa_status_t dsa_rmsnorm_fp8(const void *x, int64_t x_stride, const void
  * rounded to bf16 for the second product, sums are fp32.  A live page id outside
  * [0, num_pages) is left out and sets DSA_DEVERR_BAD_PAGE; a count outside [0, tokens] is
  * held to it (DSA_DEVERR_BAD_RANGE).  The order of a request's sums depends on the batch's
- * lengths; for the same arguments results are the same bits.  The launch depends on
+ * lengths and counts; for the same arguments results are the same bits.  The launch depends on
  * (batch, tokens, max_context) and the device.  Asynchronous on `stream`, allocates
  * nothing, capture-safe.
  */

@@ -168,8 +168,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
             if (issuer) {
                 const uint32_t bar = cluster_addr(&ctl.q_full, 0);
                 if (rank == 0) mbar_arrive_expect_tx(&ctl.q_full, uint32_t(2 * kSlabsT * kSlabT));
-                const int token = min(2 * w.tile + rank, p.tokens - 1);  // (an odd last one twice)
-                const int row = (w.req() * p.tokens + token) * kMlaHeads;
+                const int row = (w.req() * kPairTokens + rank) * kMlaHeads;
 #pragma unroll
                 for (int s = 0; s < kSlabsT; s += 3)
                     tma2_load_3d(sb + kOffQT + s * kSlabT, &q_map, bar, 0, row, s, pol_q);
@@ -455,9 +454,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
         bool failed = false;
         int n = 0;
         while (!failed && w.next(p, ctl.plan)) {
-            const int token = 2 * w.tile + rank;
-            const bool live_token = token < w.drafted;
-            const int64_t q_row = int64_t(w.req()) * p.tokens + min(token, p.tokens - 1);
+            const bool live_token = rank < w.drafted;
+            const int64_t q_row = int64_t(w.req()) * kPairTokens + rank;
             const uint64_t drafts = __ldg(p.mask + q_row) & low_bits(w.drafted);
             float m = -INFINITY, l = 0.f;
             bool fresh = true;  // no product of this request yet: O holds nothing of it
@@ -565,7 +563,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
             const float sum = (ctl.part[0][row] + ctl.part[1][row]) + (ctl.part[2][row] + ctl.part[3][row]);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (0: nothing was seen; a NaN goes on to both outputs)
             const bool whole = w.blo == 0 && w.bhi == w.nb;
-            const int64_t at = whole ? q_row : (int64_t(w.range) * kPairTokens + token) * 2 + (w.blo == 0 ? 1 : 0);
+            const int64_t at = whole ? q_row : (int64_t(w.range) * kPairTokens + rank) * 2 + (w.blo == 0 ? 1 : 0);
             if (live_token && part == 0)
                 (whole ? p.lse : p.lse_part)[at * kMlaHeads + row] =
                     sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2T;
