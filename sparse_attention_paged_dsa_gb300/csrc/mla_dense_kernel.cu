@@ -116,6 +116,7 @@ static_assert(kSmemD <= 232448, "fits one CTA per SM");
 
 // Named barrier over the 256 softmax threads returning the OR of `v`.
 __device__ __forceinline__ bool soft_bar_or(bool v) {
+    __syncwarp();
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred pi, po;\n\t"
@@ -127,7 +128,10 @@ __device__ __forceinline__ bool soft_bar_or(bool v) {
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void soft_bar_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void soft_bar_sync() {
+    __syncwarp();
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+}
 
 // 16 TMEM lanes x 32 consecutive 32-bit columns over the warp's 32 threads: thread t gets rows
 // t / 4 and t / 4 + 8; r[4 k], r[4 k + 1] are row t / 4, columns 8 k + 2 (t % 4) and the next,

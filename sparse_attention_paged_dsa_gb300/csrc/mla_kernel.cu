@@ -113,6 +113,7 @@ __device__ __forceinline__ void wait_landed_m(uint64_t* bar, uint32_t parity) {
 
 // Named barrier over the 128 softmax threads returning the OR of `v`.
 __device__ __forceinline__ bool softmax_bar_or(bool v) {
+    __syncwarp();
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred pi, po;\n\t"
@@ -124,7 +125,10 @@ __device__ __forceinline__ bool softmax_bar_or(bool v) {
         : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void softmax_bar_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_bar_sync() {
+    __syncwarp();
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+}
 
 // Entry e of request b is used when it lies in the row and points inside the live length.
 __device__ __forceinline__ int entry_pos(const MlaParams& p, int b, int e, int n_live) {

@@ -35,6 +35,7 @@ struct TreePlan {
 };
 
 __device__ __forceinline__ bool soft_or(bool v) {  // over the 256 softmax threads
+    __syncwarp();  // (it stands behind waits that spin lane by lane)
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred pi, po;\n\t"

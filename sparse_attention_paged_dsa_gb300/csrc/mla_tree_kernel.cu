@@ -145,6 +145,12 @@ __device__ __forceinline__ void st_async_f32(uint32_t addr, float v, uint32_t ba
                  : "memory");
 }
 
+// The two warps of a quadrant: both halves of its 32 rows.
+__device__ __forceinline__ void quad_sync(int quad) {
+    __syncwarp();
+    asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
+}
+
 __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
     mla_tree_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                     const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap d_map,
@@ -814,7 +820,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
                 // this SM, behind each writer's fence.  (No thread of another CTA does: the arrivals need no
                 // cluster-scope release, which took 1,900 cycles here and bound the loop: 1662 us for 16 x 32
                 // tokens at 128K context.)
-                asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
+                quad_sync(quad);
                 if (lane == 0) {
                     if (half == 0)
                         bulk_to_cta(r_rows + buf * kSlabQ, s_base + kOffPq + buf * kSlabQ + quad * 4096, 4096u,

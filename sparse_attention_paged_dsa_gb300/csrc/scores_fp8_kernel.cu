@@ -148,7 +148,10 @@ __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
 }
 
 // Named barrier 1 over the splitter warps.
-__device__ __forceinline__ void split_bar_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConvThreads) : "memory"); }
+__device__ __forceinline__ void split_bar_sync() {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(kConvThreads) : "memory");
+}
 
 // Two floats to two e4m3 codes (round to nearest even, saturating); `lo_val` in the low byte.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo_val, float hi_val) {

@@ -131,14 +131,26 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
+// An .aligned instruction is one for the whole warp: with lanes apart, as they may be behind a wait that spins
+// lane by lane or a branch of one lane, its behaviour is undefined.  The wrappers of barriers (here and in the
+// kernels) and of tensor memory's allocation meet the warp first; reads of tensor memory, in the kernels' loops, stand
+// behind a vote or a __syncwarp.
+
 // All threads of all CTAs of the cluster; orders shared-memory writes before remote reads.
 __device__ __forceinline__ void cluster_sync_all() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // The two halves of cluster_sync_all, for work in between.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // Shared-memory address of the same variable in CTA `cta` of the cluster.  Volatile (like the
 // loads below) so that neither moves above the cluster barrier that orders the writes before it.
@@ -246,16 +258,19 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
 
 // ----------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
                  "r"(ncols)
                  : "memory");
 }
 
 __device__ __forceinline__ void tmem_relinquish() {
+    __syncwarp();
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+    __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
