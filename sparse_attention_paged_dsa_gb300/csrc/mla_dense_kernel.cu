@@ -858,6 +858,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                 for (int c = 0; c < 4; ++c) {
                     uint32_t r[32];
                     const int j = 2 * half + (c >> 1), s16 = c & 1;
+                    __syncwarp();
                     if (fresh) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) r[i] = 0u;
@@ -909,6 +910,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                         uint32_t r[32];
                         const int j = 2 * half + (c & 1);
                         const int hb = 32 * (rounds == 1 ? c >> 1 : rd);
+                        __syncwarp();
                         if (fresh) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) r[i] = 0u;

@@ -896,6 +896,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
                             l2.x *= alpha;
                             l2.y *= alpha;
                         }
+                        __syncwarp();
                         // S(j) full means that PV(j - 1), issued before it, has completed: O is at rest.
                         if (j > 0) {
 #pragma unroll 1
@@ -1028,6 +1029,7 @@ __global__ void __launch_bounds__(kThreadsP, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
+                __syncwarp();
                 tmem_ld_32x32b_x32(o_addr + 32u * c, o);
                 tmem_ld_wait(o);
                 if (c == 3) {

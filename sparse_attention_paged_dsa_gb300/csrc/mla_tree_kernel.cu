@@ -616,6 +616,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
                 if (!__all_sync(0xffffffffu, ok)) {
                     failed = true;  // (all warps meet at the next barrier)
                     if (lane == 0) ctl.abort = 1;
+                    __syncwarp();
                 }
                 tc_fence_after_sync();  // (behind q_empty: the products have read what was there)
 #pragma unroll 1
@@ -663,6 +664,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
+                    __syncwarp();
                     if (fresh) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0u;

@@ -509,6 +509,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                         m = top;
                         l *= alpha;
                     }
+                    __syncwarp();
                     if (!fresh) {
                         tc_fence_after_sync();
 #pragma unroll 1
@@ -570,6 +571,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
+                __syncwarp();
                 if (fresh) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
