@@ -56,9 +56,12 @@ __device__ __forceinline__ void tma2_load_2d(uint32_t dst, const CUtensorMap* ma
         : "memory");
 }
 
-// Arrive on a barrier of either CTA (shared::cluster address).  What the arrivals on p_full order is
-// tensor memory, through the tcgen05 fences; the cluster-scope release and acquire below cost 250 to 470
-// cycles a time on the MMA's path and are kept for ordinary stores (the zeroed value rows).
+// Arrive on a barrier of another CTA (shared::cluster address).  Without a scope the arrival orders within its
+// own CTA: enough for tensor memory (through the tcgen05 fences: the prompt kernel's weights) and, in the loops of
+// the tree kernels, for weights that each SM's products read from that SM's own shared memory behind their writers'
+// proxy fence.  The cluster-scope release and acquire below cost 250 to 470 cycles a time on the MMA's path, and
+// 1,900 in the four-CTA loop; what happens once a request (zeroed value rows) and what threads of another CTA read
+// goes by them.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

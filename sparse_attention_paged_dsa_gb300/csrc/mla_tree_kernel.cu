@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
                                 wait(&ctl.vz_full[pg], (zero_phase >> pg) & 1u);
                                 zero_unseen<2>(page == w.np ? drafts : low_bits(w.valid(page)), w.valid(page),
                                                tiles + kOffVq + pg * kGroupQ);
-                                wait(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u);
+                                ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.vz_ready[pg],
+                                                                                     (zero_phase >> pg) & 1u, &ctl.abort));
                                 zero_phase ^= 1u << pg;
                             }
                             wait(&ctl.v_full[pg], uint32_t(n & 1));
@@ -545,7 +546,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
                         zero_phase ^= 1u << pg;
                         zero_unseen<2>(page == w.np ? drafts : low_bits(w.valid(page)), w.valid(page),
                                        tiles + kOffVq + pg * kGroupQ);
-                        if (issuer) mbar_arrive_remote(cluster_addr(&ctl.vz_ready[pg], leader));
+                        if (issuer) mbar_arrive_cluster(cluster_addr(&ctl.vz_ready[pg], leader));
+                        __syncwarp();
                     }
                     wait(&ctl.r_full[n & 1], uint32_t(n >> 1) & 1u);
                     if (ok && issuer) mbar_arrive_remote(cluster_addr(&ctl.p_other[n & 1], leader));

@@ -377,7 +377,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                                 wait(&ctl.vz_full[pg], (zero_phase >> pg) & 1u);
                                 zero_unseen<4>(page == w.np ? drafts : low_bits(w.valid(page)), w.valid(page),
                                                tiles + kOffVT + 2 * (page & 1) * kGroupV);
-                                wait(&ctl.vz_ready[pg], (zero_phase >> pg) & 1u);
+                                ok = ok && __all_sync(0xffffffffu, mbar_wait_cluster(&ctl.vz_ready[pg],
+                                                                                     (zero_phase >> pg) & 1u, &ctl.abort));
                                 zero_phase ^= 1u << pg;
                             }
 #pragma unroll 1
@@ -435,7 +436,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(2, 1, 1)
                     if (!ok) break;
                     zero_unseen<4>(page == w.np ? drafts : low_bits(w.valid(page)), w.valid(page),
                                    tiles + kOffVT + 2 * (page & 1) * kGroupV);
-                    if (lane == 0) mbar_arrive_remote(cluster_addr(&ctl.vz_ready[pg], 0));
+                    if (lane == 0) mbar_arrive_cluster(cluster_addr(&ctl.vz_ready[pg], 0));
+                    __syncwarp();
                 }
             }
             __syncwarp();
