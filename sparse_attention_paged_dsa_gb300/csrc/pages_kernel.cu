@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreadsPg) pages_update_kernel(const PagesPar
     for (int i = 0; i < kReqs; ++i) {
         const int b = tid * kReqs + i;
         if (b >= p.batch) break;
-        const int n = length(__ldg(p.seq_lens + b)), w = length(__ldg(p.new_lens + b));
+        const int n = length(p.seq_lens[b]), w = length(p.new_lens[b]);  // (may be written below: no ld.global.nc)
         s.now[b] = n;
         s.want[b] = w;
         const int d = pages_of(w) - pages_of(n);
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreadsPg) pages_update_kernel(const PagesPar
         if (w < warp) pages_to += s.warp_pages[w], slots_to += s.warp_slots[w];
         pages_all += s.warp_pages[w];
     }
-    int count = __ldg(p.free_count);
+    int count = *p.free_count;
     if (count < 0 || int64_t(count) > p.num_pages) {
         bad |= kErrBadRange;
         count = count < 0 ? 0 : int(p.num_pages);
