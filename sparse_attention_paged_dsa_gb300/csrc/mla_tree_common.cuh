@@ -75,7 +75,7 @@ struct TreeWalk {
     int np, live, drafted, nb, blo, bhi;  // current request: cache pages, entries, drafted tokens, blocks
     __device__ __forceinline__ TreeWalk(int first_, int step_, int units)
         : k(-1), rounds(first_ < units ? (units - first_ + step_ - 1) / step_ : 0), b(0), u0(0), lo(0), hi(0),
-          range(0), tile(0) {}
+          range(0), tile(0), np(0), live(0), drafted(0), nb(0), blo(0), bhi(0) {}
     __device__ __forceinline__ bool next(const MlaTreeParams& p, const TreePlan& plan) {
         while (true) {
             while (b < p.batch && u0 < hi) {
@@ -92,7 +92,9 @@ struct TreeWalk {
                 if (bhi > blo) return true;
             }
             if (++k >= rounds) return false;
-            const volatile UnitT& unit = plan.unit[k];  // (one build read these above the caller's barrier, where they were still cleared)
+            // (In one build the softmax warps read these while they were still cleared, behind a cluster barrier to which
+            // their lanes could come apart; the barriers meet the warp first since, and these are read from memory each time.)
+            const volatile UnitT& unit = plan.unit[k];
             range = unit.range, tile = unit.tile, lo = unit.lo, hi = unit.hi, b = unit.first_req, u0 = unit.first_start;
         }
     }
