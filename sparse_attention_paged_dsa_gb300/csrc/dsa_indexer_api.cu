@@ -367,8 +367,6 @@ size_t dense_workspace_bytes(int groups, int32_t next_n) {
            dense_parts(groups, next_n) * dsa::kMlaHeads * (dsa::kMlaDv + 1) * sizeof(float);
 }
 
-constexpr int kTicketWord = 32;  // of the workspace header: the page update's, 0 between calls
-
 // From this many tokens x context on, a tree of two tokens or more is worth a kernel on clusters.  Of two CTAs (us,
 // dense kernel and that one, two tokens each: 4 x 65536 context 41.5, 41.5; 1 x 262144 38, 37; 16 x 131072 183, 131;
 // 64 x 8192 75, 65; 64 x 65536 354, 244), or of four (1 request, 4 tokens, 131072 context 44, 46; 4 x 8, 8192 36, 40;
@@ -378,8 +376,9 @@ constexpr int64_t kTreeWork = int64_t(1) << 19;
 // 1024 121, 140; 768: 85, 84 and 141, 136).
 constexpr int64_t kPairContext = 512;
 
-// Tree decode: header, cuts, plan (of each tile), flags, then two partial outputs per range and token, of the kernel
-// that the call takes (the dense one may have to do a call again: it makes its own plan, in the same place).
+// Tree decode: header, cuts, plan (of each tile), the same of the dense kernel, then two partial outputs per range
+// and token, of the kernel that the call takes.  (Of more than two tokens the dense one may have to do some requests
+// again while the others' partials wait for the merge: room for both.)
 struct TreeShape {
     int groups;                   // of the dense kernel
     int clusters, tiles, ranges;  // of the one on clusters: of two CTAs for two tokens, of four for more
@@ -387,18 +386,19 @@ struct TreeShape {
         : groups(dense_groups(sms, tokens)), clusters(tokens > dsa::kPairTokens ? quads : pairs),
           tiles(tokens > dsa::kPairTokens ? dsa::tree_tiles(tokens) : 1),
           ranges(tokens < dsa::kPairTokens ? 0 : dsa::tree_ranges(tiles, clusters)) {}
+    size_t tiled_parts(int32_t tokens) const { return dense_parts(ranges * tiles, dsa::tree_places(tokens)); }
     size_t parts(int32_t tokens) const {
-        const size_t dense = dense_parts(groups, tokens), tiled = dense_parts(ranges * tiles, dsa::tree_places(tokens));
-        return dense > tiled ? dense : tiled;
+        const size_t dense = dense_parts(groups, tokens), tiled = tiled_parts(tokens);
+        return tokens > dsa::kPairTokens ? dense + tiled : (dense > tiled ? dense : tiled);
     }
     size_t workspace_bytes(int32_t tokens) const {
         return dsa::kWorkspaceHeaderBytes + kTreePlanBytes +
                parts(tokens) * dsa::kMlaHeads * (dsa::kMlaDv + 1) * sizeof(float);
     }
     static constexpr size_t kCutBytes = size_t(dsa::kTreeMaxUnits) * sizeof(int32_t);
-    static constexpr size_t kFlagsAt = kCutBytes + size_t(dsa::kTreeMaxTiles) * DSA_MAX_BATCH * sizeof(int2);
-    static constexpr size_t kTreePlanBytes = kFlagsAt + size_t(dsa::kTreeMaxFlags + 64) * sizeof(uint32_t);
-    static_assert(kCutBytes >= kDenseCutBytes, "the dense kernel's cuts fit");
+    static constexpr size_t kDenseAt = kCutBytes + size_t(dsa::kTreeMaxTiles) * DSA_MAX_BATCH * sizeof(int2);
+    static constexpr size_t kAgainAt = kDenseAt + kDensePlanBytes;
+    static constexpr size_t kTreePlanBytes = (kAgainAt + (dsa::kAgainWords + 1) * sizeof(uint32_t) + 255) / 256 * 256;
 };
 
 dsa_status_t run_rmsnorm(dsa::RmsNormParams p, void* stream) {
@@ -953,14 +953,14 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
     p.seq_lens = seq_lens;
     p.out = static_cast<__nv_bfloat16_raw*>(out);
     p.lse = lse;
-    p.cuts = reinterpret_cast<int32_t*>(ws);
-    p.plan = reinterpret_cast<int2*>(ws + TreeShape::kCutBytes);
-    uint32_t* flags = reinterpret_cast<uint32_t*>(ws + TreeShape::kFlagsAt);
-    p.flags = flags;
-    p.again = flags + dsa::kTreeMaxFlags;
+    p.cuts = reinterpret_cast<int32_t*>(ws + TreeShape::kDenseAt);
+    p.plan = reinterpret_cast<int2*>(ws + TreeShape::kDenseAt + kDenseCutBytes);
+    p.again = reinterpret_cast<uint32_t*>(ws + TreeShape::kAgainAt);
     p.o_part = reinterpret_cast<float*>(ws + TreeShape::kTreePlanBytes);
     p.lse_part = p.o_part + shape.parts(tokens) * dsa::kMlaHeads * dsa::kMlaDv;
     p.err = static_cast<uint32_t*>(workspace);
+    p.flags = p.err + dsa::kAgainWord;
+    p.ticket = p.err + dsa::kTicketWord;
     p.num_pages = num_pages;
     p.max_context = max_context;
     p.table_width = int32_t(max_context / DSA_PAGE_TOKENS);
@@ -983,12 +983,12 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
         t.counts = token_counts_opt;
         t.out = p.out;
         t.lse = lse;
-        t.plan = p.plan;
-        t.cuts = p.cuts;
+        t.plan = reinterpret_cast<int2*>(ws + TreeShape::kCutBytes);
+        t.cuts = reinterpret_cast<int32_t*>(ws);
         t.o_part = p.o_part;
         t.lse_part = p.lse_part;
         t.err = p.err;
-        t.flags = flags;
+        t.flags = p.flags;
         t.num_pages = num_pages;
         t.max_context = max_context;
         t.table_width = p.table_width;
@@ -1015,8 +1015,10 @@ dsa_status_t dsa_mla_tree_decode(const void* q, const void* kv_cache, int64_t nu
         if (st != DSA_OK) return st;
         e = dsa::launch_mla_tree(m, t, quads, cs);
         if (e != cudaSuccess) return cuda_fail(e, "MLA tree decode launch");
-        p.redo = dsa::mla_tree_ctas(t, quads);
-        p.first_ranges = shape.ranges;
+        p.redo = 1;
+        p.first = {t.plan, t.cuts, t.o_part, t.lse_part, shape.ranges};
+        p.o_part += shape.tiled_parts(tokens) * dsa::kMlaHeads * dsa::kMlaDv;
+        p.lse_part += shape.tiled_parts(tokens) * dsa::kMlaHeads;
     }
     CUtensorMap q_map, kv_map, kr_map, o_map, d_map;
     st = make_slabs_map(&q_map, q, q_rows, 3, "mla q");
@@ -1061,7 +1063,7 @@ dsa_status_t dsa_pages_update(const int32_t* seq_lens, const int32_t* new_lens, 
     p.slots = slots;
     p.positions = positions;
     p.err = static_cast<uint32_t*>(workspace);
-    p.ticket = p.err + kTicketWord;
+    p.ticket = p.err + dsa::kTicketWord;
     p.in_place = seq_lens_out == seq_lens || seq_lens_out == new_lens || free_count_out == free_count;
     p.num_pages = num_pages;
     p.max_context = max_context;

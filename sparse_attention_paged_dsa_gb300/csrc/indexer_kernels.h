@@ -41,6 +41,11 @@ constexpr int kQRowBytes = kHeads * kHeadDim * 2;         // 4 KiB of bf16
 constexpr int kUnitPositions = 2 * kPageEntries;          // one work unit = 2 pages = 128 keys
 constexpr int kMaxBatch = 1024;
 constexpr size_t kWorkspaceHeaderBytes = 256;
+// Words of the header beside the error word (word 0); all of them are 0 between calls.
+constexpr int kAgainWord = 1;    // 32 of them: the requests (a bit each) that a tree decode has to do again
+constexpr int kTicketWord = 33;  // of CTAs that count themselves
+constexpr int kAgainWords = kMaxBatch / 32;
+static_assert(size_t(kTicketWord + 1) * 4 <= kWorkspaceHeaderBytes && kAgainWord + kAgainWords <= kTicketWord, "they fit");
 
 // Device error bits (same values as DSA_DEVERR_* in the public header).
 constexpr uint32_t kErrSeqLenClamped = 0x1u;
@@ -141,6 +146,14 @@ cudaError_t launch_mla(const CUtensorMap& q_map, const CUtensorMap& kv_map, cons
 
 // Latent attention decode over every live entry, 1-4 tokens per request.
 constexpr int kMlaMaxGroups = 256;
+// Where a tree decode's kernel on clusters has left its partial outputs (see MlaMergeParams).
+struct MlaTreeOutputs {
+    const int2* plan;
+    const int32_t* cuts;
+    const float* o_part;
+    const float* lse_part;
+    int32_t ranges;
+};
 struct MlaDenseParams {
     const int32_t* page_table; // [batch, table_width]
     const int32_t* seq_lens;   // [batch] tokens
@@ -162,10 +175,11 @@ struct MlaDenseParams {
     // of a tree of drafted tokens:
     const uint64_t* mask;      // [batch, tokens] bit i: the token sees drafted entry i
     const int32_t* counts;     // [batch] drafted tokens, or null: all `tokens`
-    const uint32_t* flags;     // of another kernel's CTAs, which has done the call: its outputs are not to be used
-    uint32_t* again;           // was the call done again?
-    int32_t redo;              // flags to look at: leave if none is set; 0: the call is this kernel's own
-    int32_t first_ranges;      // with redo: of the kernel that has done the call, for the merge of either
+    uint32_t* flags;           // [kAgainWords] with redo: requests whose outputs of that kernel are not to be used; cleared
+    uint32_t* ticket;          // with redo, 0 between calls
+    uint32_t* again;           // [kAgainWords + 1] with redo: a copy of the flags for the merge, and whether any is set
+    int32_t redo;              // another kernel has done the call: only flagged requests are done here
+    MlaTreeOutputs first;      // with redo: of that kernel, for the merge
 };
 // q_map and kv_map: 576-wide bf16 rows (q: batch * tokens * 64 of them; the cache: num_pages * 64) as
 // (dim in slab, row, slab of 64 dims), boxes of 64 rows x 3 slabs and 64 rows x 2 slabs; kr_map: the
@@ -190,7 +204,12 @@ struct MlaMergeParams {
     __nv_bfloat16_raw* out;    // [batch, tokens, 64, 512]
     float* lse;                // [batch, tokens, 64]
     const int32_t* counts;     // [batch] tokens of each request, or null: all
-    const uint32_t* again;     // not 0 there: the dense kernel has done the call again (null: it may not)
+    const uint32_t* again;     // [kAgainWords + 1] the requests that the dense kernel has done again (null: none), whose
+                               // partials are these four:
+    const int2* plan_again;
+    const int32_t* cuts_again;
+    const float* o_again;
+    const float* lse_again;
     int32_t tokens, batch;
     int32_t by_cut, rows;              // requests (or cuts) x tokens (cuts of tiled partials: x places)
     int32_t by_cut_again, rows_again;  // of the dense kernel's second try
@@ -219,7 +238,7 @@ struct MlaTreeParams {
     float* o_part;
     float* lse_part;
     uint32_t* err;             // device error word
-    uint32_t* flags;           // [kTreeMaxFlags] a CTA each: its outputs are not to be used
+    uint32_t* flags;           // [kAgainWords] a bit each, 0 at first: requests whose outputs are not to be used
     int64_t num_pages;
     int64_t max_context;
     int32_t table_width;
@@ -237,7 +256,6 @@ struct MlaTreeMaps {
     CUtensorMap q, k, v, d, o;
 };
 cudaError_t mla_tree_quads(int* quads);                    // clusters that the current device holds
-int mla_tree_ctas(const MlaTreeParams& p, int quads);      // CTAs of a call
 cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cudaStream_t stream);
 
 // The same for two tokens, on clusters of two CTAs, with a running maximum (flags are not used), and its merge.

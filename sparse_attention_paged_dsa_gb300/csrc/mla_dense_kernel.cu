@@ -1,7 +1,7 @@
 // mla_dense_kernel.cu -- latent attention decode over every live entry of the
 // paged cache (absorbed form), one to four query tokens per request, sm_103a; and for
 // trees of drafted tokens (kTree) where they are small, or again with a running maximum
-// where mla_tree_kernel.cu, which keeps none, has given up.
+// for the requests that mla_tree_kernel.cu, which keeps none, has given up.
 //
 //     s[h, t] = sm_scale * q[b, j, h] . kv_t                 (576-wide entries)
 //     o[b, j, h] = sum_t softmax_t(s[h, :]) kv_t[:512],  lse = log sum_t exp(s[h, t])
@@ -107,6 +107,7 @@ struct __align__(16) DenseCtl {
     int first_req, first_start;  // request of the range's first unit, and where its units start
     int lo, hi;                  // the range, in units
     int cut;                     // the request that this range is the second one of, or -1
+    uint32_t todo[kAgainWords];  // of a tree: a bit for each request that is this call's
     int warp_units[kWarpsD];
     float row_max[2][kMlaHeads];  // per half of the entries; the row sums at a request's end
     alignas(16) float alpha[kMlaHeads];
@@ -221,8 +222,10 @@ struct Walk {
     int b, u0, lo, hi, batch;  // request b starts at unit u0; range [lo, hi)
     int seq, nb, blo, bhi;     // current request: tokens, blocks, and this range's blocks [blo, bhi)
     int token, drafted;        // of a tree: this CTA's, and the request's tokens
+    const uint32_t* todo;
     __device__ __forceinline__ Walk(const DenseCtl& ctl, const MlaDenseParams& p)
-        : b(ctl.first_req), u0(ctl.first_start), lo(ctl.lo), hi(ctl.hi), batch(p.batch), token(blockIdx.x) {}
+        : b(ctl.first_req), u0(ctl.first_start), lo(ctl.lo), hi(ctl.hi), batch(p.batch), token(blockIdx.x),
+          todo(ctl.todo) {}
     __device__ __forceinline__ bool next(const MlaDenseParams& p) {
         while (b < batch && u0 < hi) {
             seq = seq_tokens(p, b);
@@ -233,7 +236,8 @@ struct Walk {
             bhi = min(hi, end) - base;
             ++b;
             u0 = end;
-            if (nb > 0 && bhi > blo && (!kTree || token < drafted)) return true;
+            if (nb > 0 && bhi > blo && (!kTree || (token < drafted && (todo[(b - 1) >> 5] >> ((b - 1) & 31) & 1u))))
+                return true;
         }
         return false;
     }
@@ -267,14 +271,31 @@ __global__ void __launch_bounds__(kThreadsD, 1)
                      const __grid_constant__ CUtensorMap kr_map, const __grid_constant__ CUtensorMap o_map,
                      const __grid_constant__ CUtensorMap d_map, const MlaDenseParams p) {
     extern __shared__ uint8_t smem_raw[];
-    if (kTree && p.redo > 0) {  // the call of another kernel: only if a CTA of it has given up
-        pdl_wait_prior_grid();
-        const int any = __syncthreads_or(int(threadIdx.x) < p.redo && p.flags[threadIdx.x] != 0);
-        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.again = any ? 1 : 0;
-        if (!any) return;
-    }
     uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     DenseCtl& ctl = *reinterpret_cast<DenseCtl*>(tiles + kOffCtl);
+    if (kTree) {
+        // The call of another kernel: the requests that it has given up, if there are any.  The plan is that of the whole
+        // batch, so that a request's sums do not depend on which others are done again.
+        const bool has_word = int(threadIdx.x) < kAgainWords;
+        uint32_t word = 0xffffffffu;
+        if (p.redo) {
+            pdl_wait_prior_grid();
+            word = has_word ? p.flags[threadIdx.x] : 0u;
+        }
+        const int any = __syncthreads_or(has_word && word != 0);
+        if (p.redo && blockIdx.x == 0 && blockIdx.y == 0) {
+            if (has_word) p.again[threadIdx.x] = word;
+            if (threadIdx.x == 0) p.again[kAgainWords] = any ? 1 : 0;
+        }
+        if (!any) return;
+        if (has_word) ctl.todo[threadIdx.x] = word;
+        if (p.redo && threadIdx.x == 0) {  // every thread's word is here: the last CTA clears them
+            if (atomicAdd(p.ticket, 1u) == gridDim.x * gridDim.y - 1) {
+                for (int i = 0; i < kAgainWords; ++i) p.flags[i] = 0;
+                *p.ticket = 0;
+            }
+        }
+    }
     const uint32_t s_base = smem_u32(tiles);
 
     const int warp = uniform(int(threadIdx.x) >> 5);
@@ -993,15 +1014,17 @@ cudaError_t launch(const CUtensorMap& q_map, const CUtensorMap& kv_map, const CU
     m.by_cut = p.merge_by_cut;
     m.rows = (p.merge_by_cut ? p.groups : p.batch) * p.tokens;
     m.one_head = m.rows <= 16;
-    if (p.redo > 0) {  // one merge, for this kernel's partials or those of the one before
+    if (p.redo) {  // one merge, for this kernel's partials and those of the one before
         m.again = p.again;
+        m.plan_again = m.plan, m.cuts_again = m.cuts, m.o_again = m.o_part, m.lse_again = m.lse_part;
+        m.plan = p.first.plan, m.cuts = p.first.cuts, m.o_part = p.first.o_part, m.lse_part = p.first.lse_part;
         m.tiled = 1;
         m.batch = p.batch;
         m.by_cut_again = m.by_cut, m.rows_again = m.rows;
-        const int places = p.first_ranges * tree_tiles(p.tokens) * tree_places(p.tokens);
+        const int places = p.first.ranges * tree_tiles(p.tokens) * tree_places(p.tokens);
         m.by_cut = p.batch * p.tokens > places;
         m.rows = m.by_cut ? places : p.batch * p.tokens;
-        m.one_head = m.rows <= 16 && p.first_ranges >= 32 * p.batch;
+        m.one_head = m.rows <= 16 && p.first.ranges >= 32 * p.batch;
     }
     return launch_mla_merge(m, stream);
 }

@@ -36,9 +36,9 @@
 // No running maximum.  Both CTAs that hold a row must use one reference, and agreeing on a new
 // one block by block would cost a round trip each.  They agree once, on the first block's
 // maximum.  Weights may then pass 1 as far as fp32 and bf16 reach (their rounding is relative:
-// nothing is lost).  A CTA one of whose sums passes 2^58, or one of whose outputs is not finite,
-// sets its flag, and the dense kernel, which keeps a running maximum, then does the whole call
-// again; it leaves at once (3 us) where no flag is set.
+// nothing is lost).  A request one of whose sums passes 2^58, or one of whose outputs is not finite,
+// is flagged, and the dense kernel, which keeps a running maximum, then does the flagged requests
+// again (the others keep their results); it leaves at once (3 us) where there is none.
 //
 // Memory.  q: five slabs of 64 dims in shared memory (80 KB), four in tensor memory beside S
 // (two blocks) and O; keys: a ring of four groups of three slabs; values: one block; weights of both
@@ -102,7 +102,8 @@ constexpr int kOffCtlQ = kOffPq + 2 * kSlabQ;
 constexpr uint32_t kColSQ = 0;     // S: 2 x 64 columns
 constexpr uint32_t kColQQ = 128;   // q: 32 columns a slab
 constexpr uint32_t kColOQ = 256;   // O: 256 columns
-constexpr float kSumMost = 288230376151711744.0f;  // 2^58: times 2^18 entries and values below 2^50
+constexpr float kSumMost = 288230376151711744.0f;  // 2^58: |O| is at most that times the largest |value|, finite for
+                                                   // values below 2^69; what larger ones make infinite is flagged too
 constexpr float kSumLeast = 8.4703294725430034e-22f;  // 2^-70, where the reference is not the row's own
 
 struct __align__(16) TreeCtl {
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
 
     if (s_base & 1023u) {  // (the same in every CTA; shared memory has always started on such a boundary)
         pdl_wait_prior_grid();
-        if (threadIdx.x == 0) p.flags[blockIdx.x] = 1;
+        if (int(threadIdx.x) < (p.batch + 31) / 32) atomicOr(p.flags + threadIdx.x, 0xffffffffu);
         return;
     }
     if (threadIdx.x == 0) {
@@ -220,7 +221,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
     __syncwarp();
     const uint32_t tmem_base = ctl.tmem_base;
     TreeWalk<kTileTokens> w(cluster, clusters, units);
-    bool flagged = false;
 
     if (warp == 9) {
         // ================= TMA: q and keys =================
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
                     const float other = *const_cast<volatile float*>(&ctl.peer[1][row]);
                     sum = pair == 0 ? sum + other : other + sum;
                 }
-                if (live_token && (!(sum <= kSumMost) || (!own && any != 0 && !(sum >= kSumLeast)))) flagged = true;
+                bool flagged = live_token && (!(sum <= kSumMost) || (!own && any != 0 && !(sum >= kSumLeast)));
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 const int head = row & 63;
                 if (live_token && pair == 0 && half == 0)
@@ -712,6 +712,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
                             st_global_v8(p.o_part + tiled_part(at, head, 256 * pair + 128 * half + 32 * c + 8 * k), v);
                         }
                     }
+                }
+                if (__any_sync(0xffffffffu, flagged) && lane == 0) {  // (rows of the request's: live ones)
+                    const int b = int(first_row / p.tokens);
+                    atomicOr(p.flags + (b >> 5), 1u << (b & 31));
                 }
                 if (whole) {
                     fence_proxy_async_smem();
@@ -851,8 +855,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) __cluster_dims__(4, 1, 1)
 
     __syncwarp();
     tc_fence_before_sync();
-    flagged = __syncthreads_or(flagged) != 0;
-    if (threadIdx.x == 0) p.flags[blockIdx.x] = flagged ? 1 : 0;
     cluster_sync_all();  // no CTA leaves while another may read its memory or arrive on its barriers
     tc_fence_after_sync();
     if (warp == 8) {
@@ -888,14 +890,8 @@ cudaError_t mla_tree_quads(int* quads) {
     e = cudaOccupancyMaxActiveClusters(quads, mla_tree_kernel, &cfg);
     if (e != cudaSuccess) return e;
     if (*quads < 1) return cudaErrorInvalidConfiguration;
-    if (*quads > kTreeMaxFlags / 4) *quads = kTreeMaxFlags / 4;
     resident[dev].store(*quads, std::memory_order_relaxed);
     return cudaSuccess;
-}
-
-int mla_tree_ctas(const MlaTreeParams& p, int quads) {
-    const int units = p.ranges * p.tiles;
-    return 4 * (units < quads ? units : quads);
 }
 
 cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cudaStream_t stream) {
@@ -907,7 +903,7 @@ cudaError_t launch_mla_tree(const MlaTreeMaps& m, MlaTreeParams p, int quads, cu
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(mla_tree_ctas(p, quads)));
+    cfg.gridDim = dim3(4u * unsigned(units < quads ? units : quads));
     cfg.blockDim = dim3(kTreeThreads);
     cfg.dynamicSmemBytes = size_t(kSmemQ);
     cfg.stream = stream;

@@ -11,7 +11,6 @@ constexpr int kTreeWholeBlocks = 3;  // requests of at most this many blocks are
 constexpr int kTreeMaxRanges = 256;  // of a tile
 constexpr int kTreeMaxUnits = 512;   // of a call
 constexpr int kTreeMaxTiles = 16;
-constexpr int kTreeMaxFlags = 256;   // CTAs of a call
 constexpr int kTreeMaxRounds = 8;    // units of a cluster, at most
 constexpr int kTreePlanRounds = 4;   // rounds that are tried for a full device
 
