@@ -4,7 +4,11 @@
 //
 //     c = x[0:512] * weight / sqrt(mean(x[0:512]^2) + eps)           (without a weight: x)
 //     r[2j], r[2j + 1] = a cos - b sin, a sin + b cos                 (a, b = x[512 + 2j], x[513 + 2j])
-//     y = k * key_weight / sqrt(mean(k^2) + eps),  scale = max|y| / 448,  code = y / scale
+//     y = k * key_weight / sqrt(mean(k^2) + eps),  scale = max|y| / 448,  code = e4m3(u * 448 / max|u|)
+//
+// with u = k * key_weight: the codes do not depend on the norm, and from u, with the quotient in two parts, they are
+// those of the 8-bit RMS norm (rmsnorm_kernel.cu) bit for bit.  (y * (448 / max|y|) by one approximate quotient moved
+// half as many more codes to a neighbour.)
 //
 // A warp has a row at a time: 8-element chunks lane and lane + 32 of the latent part
 // (16-byte accesses, whole 512-byte lines of the warp), one pair of the rotary dims and
@@ -39,6 +43,11 @@ __device__ __forceinline__ float2 widen(uint32_t v) {
 __device__ __forceinline__ uint32_t narrow(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+// The quotient 448 / most in two parts, q + lo.
+__device__ __forceinline__ float2 code_quotient(float most) {
+    const float q = __fdividef(kE4m3Max, most);
+    return make_float2(q, fmaf(-q, most, kE4m3Max) * (q * (1.f / kE4m3Max)));
 }
 struct Place {
     int64_t slot;
@@ -178,6 +187,8 @@ __global__ void __launch_bounds__(kWarpsA * 32, kCtasA) append_kernel(const Appe
             *reinterpret_cast<uint32_t*>(out + kMlaDv * 2 - 12 * lane) = r;
         }
         if (kKeys) {
+            const float2 u = y;  // before the norm
+            const float most = top;
             if (key_norm) {
                 const float inv = rsqrtf(sums.y * (1.f / kHeadDim) + p.eps);
                 y = mul_f32x2(y, make_float2(inv, inv));
@@ -189,9 +200,9 @@ __global__ void __launch_bounds__(kWarpsA * 32, kCtasA) append_kernel(const Appe
             } else {
                 float scale = top / kE4m3Max;
                 float2 q;
-                if (top > 0x1p-100f && top < 0x1p100f) {  // one reciprocal for all 64
-                    const float by = __fdividef(kE4m3Max, top);
-                    q = mul_f32x2(y, make_float2(by, by));
+                if (top > 0x1p-100f && top < 0x1p100f && most > 1e-30f && most < 1e30f) {
+                    const float2 by = code_quotient(most);
+                    q = fma_f32x2(u, make_float2(by.x, by.x), mul_f32x2(u, make_float2(by.y, by.y)));
                 } else {
                     if (!(scale > 0.f) || scale > 3.0e38f) scale = 1.f;
                     q = make_float2(y.x / scale, y.y / scale);

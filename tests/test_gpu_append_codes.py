@@ -1,0 +1,66 @@
+"""GPU tests of dsa_cache_append's 8-bit codes.
+
+Codes: they are of u = key * weight against max|u|, as dsa_rmsnorm_fp8's, by the same two-part quotient, so the two entry
+points' codes of a key are equal.  Scales: max|u| times the norm's reciprocal over 448; the norms' sums go in
+another order (64 squares: up to 2 terms and 5 levels here, 16 terms and 2 levels there, half of their relative error in
+the root) and each scale has two or three more roundings: 2^-20 relatively.
+
+Off the exact nearest code: with w = u * 448 / max|u| in fp64 rounded to e4m3 as the reference, a code may differ only
+where w lies within the quotient's error of the middle between two codes.  The quotient in two parts is off by under
+2^-23 (its last rounding 2^-24, what its parts leave out below that), so |w - middle| <= 2^-22 w there."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+
+
+def append(lib, keys, weight, eps=EPS):
+    import torch
+    rows = keys.shape[0]
+    pages = -(-rows // 64)
+    codes = torch.zeros(pages, 64, 64, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(pages, 64, device="cuda")
+    ws = lib.new_workspace(1, 256)
+    lib.dsa_cache_append(torch.arange(rows, device="cuda"), index_keys=keys, index_weight=weight, key_codes=codes,
+                         key_scales=scales, eps=eps, workspace=ws)
+    assert lib.get_error(ws) == 0
+    return codes.view(-1, 64)[:rows], scales.view(-1)[:rows]
+
+
+@pytest.mark.parametrize("w32", [False, True])
+@pytest.mark.parametrize("mag", [1.0, 2.0 ** -20, 2.0 ** 20])
+def test_codes_are_those_of_the_norm(gpu_lib, w32, mag):
+    """A million keys: the same codes from both entry points, and scales within their roundings."""
+    import torch
+    g = torch.Generator("cuda").manual_seed(5)
+    rows = 1 << 20
+    keys = (torch.randn(rows, 64, device="cuda", generator=g) * mag).to(torch.bfloat16)
+    weight = 1 + 0.3 * torch.randn(64, device="cuda", generator=g)
+    weight = weight if w32 else weight.to(torch.bfloat16)
+    codes, scales = append(gpu_lib, keys, weight)
+    want, want_scales, _, _ = gpu_lib.dsa_rmsnorm_fp8(keys, weight, EPS, 64)
+    assert torch.equal(codes, want.view(torch.uint8).view(rows, 64))
+    assert not ((scales - want_scales.view(-1)).abs() > 2.0 ** -20 * scales).any()
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_codes_against_the_nearest(gpu_lib, norm):
+    import torch
+    g = torch.Generator("cuda").manual_seed(6)
+    rows = 1 << 18
+    keys = torch.randn(rows, 64, device="cuda", generator=g).to(torch.bfloat16)
+    weight = (1 + 0.3 * torch.randn(64, device="cuda", generator=g)).to(torch.bfloat16) if norm else None
+    codes, _ = append(gpu_lib, keys, weight)
+    # u in fp32: a product of two bf16 numbers is exact
+    u = keys.double() * weight.double() if norm else keys.double()
+    w = u * 448 / u.abs().amax(1, keepdim=True)
+    values = torch.arange(127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).double()  # 0 to 448
+    middles = (values[1:] + values[:-1]) / 2
+    got = codes.view(torch.float8_e4m3fn).double().abs()
+    at = torch.searchsorted(values, got)
+    lo = torch.where(at > 0, middles[(at - 1).clamp(min=0)], torch.full_like(got, -1.0))
+    hi = torch.where(at < 126, middles[at.clamp(max=125)], torch.full_like(got, 1e9))
+    mag = w.abs()
+    assert not ((mag < lo * (1 - 2.0 ** -22)) | (mag > hi * (1 + 2.0 ** -22))).any()
+    assert torch.equal(torch.signbit(codes.view(torch.float8_e4m3fn).float()), torch.signbit(u))
