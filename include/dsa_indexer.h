@@ -523,6 +523,12 @@ DSA_API dsa_status_t dsa_mla_tree_decode(const void *q, const void *kv_cache, in
  *     row behind the old ones, and gets a slot for each entry that is to be written:
  *     entries [seq_len / 4, ceil(new_len / 4)), the old last one again where it is not
  *     full.  Entry e has the slot page_table[b, e / 64] x 64 + e % 64 and the position e.
+ * Lengths are compared as they are: a request that shrinks gets no slot, and entries that both
+ * lengths hold get none.  So with a new length that is not a multiple of 4 the last entry stays as
+ * it was made, of up to 4 tokens of which some are gone.  To have it made again, and for a step
+ * that drops tokens and adds others (rejected drafts and new tokens), call twice: with the kept
+ * length rounded down to a multiple of 4, then with the new length.  The second call gives a slot
+ * to every entry behind the first one's length.
  * All pages returned by the call are on top before any is taken.  Requests are served in
  * order; one that grows for which there are too few pages, or slots, stays as it was,
  * and so does every later one that grows (DSA_DEVERR_NO_PAGES).

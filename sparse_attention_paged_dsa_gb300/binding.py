@@ -601,7 +601,9 @@ def dsa_pages_update(seq_lens, new_lens, max_context: int, page_table, free_page
     of them (all int32), in place: requests that shrink return pages, those that grow take some, in order,
     and get a slot (int64, page x 64 + entry) and a position for each entry to be written; [max_slots] of
     both, -1 behind the last.  Request b's are cu_slots[b] to cu_slots[b + 1].  Requests that cannot be
-    served keep their length.  ``seq_lens_out`` and ``free_count_out`` may be ``seq_lens`` and ``free_count``
+    served keep their length.  A request that shrinks gets no slot; to have its last entry written again, or
+    to drop tokens and add others, call twice: with the kept length rounded down to a multiple of 4, then with
+    the new one.  ``seq_lens_out`` and ``free_count_out`` may be ``seq_lens`` and ``free_count``
     themselves.  ``workspace``: any of this package's; without one the call makes its own."""
     dev = _device_of(seq_lens, "seq_lens", _I32, (1,))
     lens = seq_lens.shape
