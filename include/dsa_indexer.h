@@ -558,7 +558,8 @@ DSA_API dsa_status_t dsa_pages_update(const int32_t *seq_lens, const int32_t *ne
 /* ---- New entries into the paged caches ------------------------------------------
  *
  * Row i goes to slot slots[i] of the caches: entry slot % 64 of page slot / 64.
- * A slot of -1 skips the row.  In fp32, one rounding per output:
+ * A slot of -1 skips the row.  In fp32 (a row whose squares leave fp32's range has its norm all
+ * the same), one rounding per output:
  *   latent entries  x = latent[i, 0:576]:
  *     kv_cache[slot, 0:512] = x[0:512] * weight / sqrt(mean(x[0:512]^2) + eps)
  *                             (x itself without a weight)

@@ -15,7 +15,8 @@
 // of the key a lane.  Both sums of squares and the key's maximum are one set of
 // butterflies over the warp, side by side: the norm does not change which product of key
 // and weight is largest.  fp32 throughout, one rounding per output.  A row's place is
-// fetched two rows ahead, its data (and its row of the rotation's table) one.
+// fetched two rows ahead, its data (and its row of the rotation's table) one.  Rows whose squares leave fp32's range are
+// left for the end of the kernel: with their code called from the loop 262144 rows took 150 us.
 //
 // What bounds it: HBM and the rows' places.  262144 rows, norms, rotation, fp8 keys: 123 us, 5900
 // GB/s, 0.87 of the measured copy rate (119 with the slots in order; the latents alone 101, a
@@ -49,6 +50,26 @@ __device__ __forceinline__ float2 code_quotient(float most) {
     const float q = __fdividef(kE4m3Max, most);
     return make_float2(q, fmaf(-q, most, kE4m3Max) * (q * (1.f / kE4m3Max)));
 }
+// A row whose sum of squares lies past fp32's range, or below what fp32 holds of it where eps does not cover that.
+constexpr float kSumMost = 1e37f, kSumLeast = 1e-30f;
+__device__ __forceinline__ bool far_sum(float sum, float eps) {
+    return !(sum <= kSumMost) || (sum < kSumLeast && eps < kSumLeast);
+}
+// Factors `first` and `second` of the norm's reciprocal for such a row, from its squares moved by a power of two: x *
+// first * second leaves the range nowhere.
+struct FarNorm {
+    float by, first, second;
+    __device__ __forceinline__ explicit FarNorm(float sum) : by(sum < 1.f ? 0x1p100f : 0x1p-70f), first(1.f), second(1.f) {}
+    __device__ __forceinline__ float square(float x) const { return x * by * (x * by); }
+    __device__ __forceinline__ void settle(float sum, float over_n, float eps) {
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = rsqrtf(sum * over_n + eps * by * by);
+        first = by < 1.f ? inv * by : by;
+        second = by < 1.f ? 1.f : inv;
+    }
+    __device__ __forceinline__ float of(float x) const { return x * first * second; }
+};
 struct Place {
     int64_t slot;
     int pos;
@@ -58,6 +79,24 @@ struct Row {
     uint32_t r, k;  // rotary pair, key pair
     float cs, sn;
 };
+
+// The codes and the scale of a key: y, two elements a lane, with top = max|y|, of which u with most = max|u| is a multiple.
+__device__ __forceinline__ void store_codes(const AppendParams& p, int64_t slot, int lane, float2 y, float2 u, float top,
+                                            float most) {
+    float scale = top / kE4m3Max;
+    float2 q;
+    if (top > 0x1p-100f && top < 0x1p100f && most > 1e-30f && most < 1e30f) {
+        const float2 by = code_quotient(most);
+        q = fma_f32x2(u, make_float2(by.x, by.x), mul_f32x2(u, make_float2(by.y, by.y)));
+    } else {
+        if (!(scale > 0.f) || scale > 3.0e38f) scale = 1.f;
+        q = make_float2(y.x / scale, y.y / scale);
+    }
+    uint16_t code;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(code) : "f"(q.y), "f"(q.x));
+    *reinterpret_cast<uint16_t*>(p.key_codes + slot * kHeadDim + 2 * lane) = code;
+    if (lane == 0) p.key_scales[slot] = scale;
+}
 
 // kKeys: 0 none, 1 bf16, 2 fp8.
 template <bool kLatent, int kKeys>
@@ -120,6 +159,7 @@ __global__ void __launch_bounds__(kWarpsA * 32, kCtasA) append_kernel(const Appe
     // A row's place is fetched two rows ahead, its data (and its row of the table) one.
     const int64_t slots = p.num_pages * kPageEntries;
     Row row = load(at);
+    bool late = false;  // rows left for the end: far_sum
     for (uint32_t i = warp; i < rows; i += warps) {
         const Row now = row;
         const Place to = at;
@@ -163,6 +203,10 @@ __global__ void __launch_bounds__(kWarpsA * 32, kCtasA) append_kernel(const Appe
             if (kKeys == 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             sums = add_f32x2(sums, other);
         }
+        if ((norm && far_sum(sums.x, p.eps)) || (key_norm && far_sum(sums.y, p.eps))) {
+            late = true;
+            continue;
+        }
         if (kLatent) {
             if (norm) {
                 const float inv = rsqrtf(sums.x * (1.f / kMlaDv) + p.eps);
@@ -198,19 +242,81 @@ __global__ void __launch_bounds__(kWarpsA * 32, kCtasA) append_kernel(const Appe
                 *reinterpret_cast<uint32_t*>(p.key_pool + to.slot * (kHeadDim * 2) + 4 * lane) =
                     key_norm ? narrow(y.x, y.y) : now.k;
             } else {
-                float scale = top / kE4m3Max;
-                float2 q;
-                if (top > 0x1p-100f && top < 0x1p100f && most > 1e-30f && most < 1e30f) {
-                    const float2 by = code_quotient(most);
-                    q = fma_f32x2(u, make_float2(by.x, by.x), mul_f32x2(u, make_float2(by.y, by.y)));
-                } else {
-                    if (!(scale > 0.f) || scale > 3.0e38f) scale = 1.f;
-                    q = make_float2(y.x / scale, y.y / scale);
-                }
-                uint16_t code;
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(code) : "f"(q.y), "f"(q.x));
-                *reinterpret_cast<uint16_t*>(p.key_codes + to.slot * kHeadDim + 2 * lane) = code;
-                if (lane == 0) p.key_scales[to.slot] = scale;
+                store_codes(p, to.slot, lane, y, u, top, most);
+            }
+        }
+    }
+    // Rows left for the end (rare), one after another: the whole row, whichever of its norms is far.
+    if (!late) return;
+#pragma unroll 1
+    for (uint32_t i = warp; i < rows; i += warps) {
+        const Place to = place(i);
+        if (to.slot == -1 || uint64_t(to.slot) >= uint64_t(slots) || (rotate && !in_table(to.pos))) continue;
+        x = p.latent + int64_t(i) * p.latent_stride * 2 + 16 * lane;
+        key = p.keys + int64_t(i) * p.key_stride * 2 + 4 * lane;
+        const Row now = load(to);
+        const uint4 c[2] = {now.c[0], now.c[1]};
+        const float2 k = widen(now.k);
+        // The sums as above, in the same order: the same rows are far.
+        float2 sums = make_float2(0.f, 0.f);
+        const auto word = [&](int j) {
+            const uint4& w = c[j >> 2];
+            return (j & 3) == 0 ? w.x : (j & 3) == 1 ? w.y : (j & 3) == 2 ? w.z : w.w;
+        };
+        const auto part = [&](int j) { return widen(word(j)); };
+        if (norm) {
+            float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fma_f32x2(part(j), part(j), ss);
+            sums.x = ss.x + ss.y;
+        }
+        if (key_norm) sums.y = fmaf(k.x, k.x, k.y * k.y);
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1)
+            sums = add_f32x2(sums, make_float2(__shfl_xor_sync(0xffffffffu, sums.x, o), __shfl_xor_sync(0xffffffffu, sums.y, o)));
+        const bool far_c = norm && far_sum(sums.x, p.eps), far_k = key_norm && far_sum(sums.y, p.eps);
+        if (!far_c && !far_k) continue;
+        if (kLatent) {
+            FarNorm f(sums.x);
+            if (far_c) {
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum += f.square(part(j).x) + f.square(part(j).y);
+                f.settle(sum, 1.f / kMlaDv, p.eps);
+            } else if (norm) {
+                f.first = rsqrtf(sums.x * (1.f / kMlaDv) + p.eps);
+            }
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float* by = wc + (j >> 2) * 256 + lane * 8 + 2 * (j & 3);
+                w[j] = norm ? narrow(f.of(part(j).x) * by[0], f.of(part(j).y) * by[1]) : word(j);
+            }
+            uint32_t r = now.r;
+            if (rotate) {
+                const float2 v = widen(r);
+                r = narrow(v.x * now.cs - v.y * now.sn, v.x * now.sn + v.y * now.cs);
+            }
+            uint8_t* out = p.kv_cache + to.slot * (kMlaDim * 2) + 16 * lane;
+            *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(out + 512) = make_uint4(w[4], w[5], w[6], w[7]);
+            *reinterpret_cast<uint32_t*>(out + kMlaDv * 2 - 12 * lane) = r;
+        }
+        if (kKeys) {
+            FarNorm f(sums.y);
+            if (far_k)
+                f.settle(f.square(k.x) + f.square(k.y), 1.f / kHeadDim, p.eps);
+            else if (key_norm)
+                f.first = rsqrtf(sums.y * (1.f / kHeadDim) + p.eps);
+            const float2 y = key_norm ? make_float2(f.of(k.x) * wk[2 * lane], f.of(k.y) * wk[2 * lane + 1]) : k;
+            if (kKeys == 1) {
+                *reinterpret_cast<uint32_t*>(p.key_pool + to.slot * (kHeadDim * 2) + 4 * lane) =
+                    key_norm ? narrow(y.x, y.y) : now.k;
+            } else {
+                float top = fmaxf(fabsf(y.x), fabsf(y.y));
+#pragma unroll 1
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                store_codes(p, to.slot, lane, y, y, top, top);
             }
         }
     }

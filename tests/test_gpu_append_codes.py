@@ -1,4 +1,4 @@
-"""GPU tests of dsa_cache_append's 8-bit codes.
+"""GPU tests of dsa_cache_append's 8-bit codes and of rows at the ends of bf16's range.
 
 Codes: they are of u = key * weight against max|u|, as dsa_rmsnorm_fp8's, by the same two-part quotient, so the two entry
 points' codes of a key are equal.  Scales: max|u| times the norm's reciprocal over 448; the norms' sums go in
@@ -7,7 +7,9 @@ the root) and each scale has two or three more roundings: 2^-20 relatively.
 
 Off the exact nearest code: with w = u * 448 / max|u| in fp64 rounded to e4m3 as the reference, a code may differ only
 where w lies within the quotient's error of the middle between two codes.  The quotient in two parts is off by under
-2^-23 (its last rounding 2^-24, what its parts leave out below that), so |w - middle| <= 2^-22 w there."""
+2^-23 (its last rounding 2^-24, what its parts leave out below that), so |w - middle| <= 2^-22 w there.
+
+Range: y = x * weight / sqrt(mean(x^2) + eps) in fp64; squares of what lies past 2^63 leave fp32, y does not."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +66,47 @@ def test_codes_against_the_nearest(gpu_lib, norm):
     mag = w.abs()
     assert not ((mag < lo * (1 - 2.0 ** -22)) | (mag > hi * (1 + 2.0 ** -22))).any()
     assert torch.equal(torch.signbit(codes.view(torch.float8_e4m3fn).float()), torch.signbit(u))
+
+
+@pytest.mark.parametrize("mag, eps", [(2.0 ** 100, EPS), (2.0 ** 124, EPS), (2.0 ** 62, EPS), (2.0 ** -100, 0.0),
+                                      (2.0 ** -125, 0.0), (2.0 ** -55, 0.0), (2.0 ** -100, EPS)])
+@pytest.mark.parametrize("keys_to", ["fp8", "bf16"])
+def test_rows_at_the_ends_of_the_range(gpu_lib, mag, eps, keys_to):
+    """Rows whose squares leave fp32 while their norms do not, beside ordinary ones."""
+    import torch
+    g = torch.Generator("cuda").manual_seed(7)
+    rows = 200
+    x = torch.randn(rows, 640, device="cuda", generator=g).clamp(-7.9, 7.9)
+    x[::2] *= mag
+    x[8] = 3.3895e38                                      # bf16's largest number
+    x = x.to(torch.bfloat16)
+    weight = (1 + 0.3 * torch.randn(640, device="cuda", generator=g)).abs().clamp(min=0.1)
+    weight[::3] *= 40
+    weight = weight.to(torch.bfloat16)
+    pages = 4
+    kv = torch.zeros(pages, 64, 576, dtype=torch.bfloat16, device="cuda")
+    to = {"key_pool": torch.zeros(pages, 64, 64, dtype=torch.bfloat16, device="cuda")} if keys_to == "bf16" else {
+        "key_codes": torch.zeros(pages, 64, 64, dtype=torch.uint8, device="cuda"),
+        "key_scales": torch.zeros(pages, 64, device="cuda")}
+    gpu_lib.dsa_cache_append(torch.arange(rows, device="cuda"), latent=x[:, :576], latent_weight=weight[:512].contiguous(),
+                             kv_cache=kv, index_keys=x[:, 576:], index_weight=weight[576:].contiguous(), eps=eps, **to)
+
+    def normed(v, w):
+        v = v.double()
+        return v * w.double() / torch.sqrt((v * v).mean(1, keepdim=True) + eps)
+
+    y = normed(x[:, :512], weight[:512])
+    tiny = 2.0 ** -133                                    # half of bf16's last step below its normal numbers
+    err = (kv.view(-1, 576)[:rows, :512].double() - y).abs()
+    assert not (err > (2.0 ** -8 + 2.0 ** -18) * y.abs() + tiny).any()
+    assert torch.isfinite(kv[:3].float()).all()
+    y = normed(x[:, 576:], weight[576:])
+    if keys_to == "bf16":
+        err = (to["key_pool"].view(-1, 64)[:rows].double() - y).abs()
+        assert not (err > (2.0 ** -8 + 2.0 ** -18) * y.abs() + tiny).any()
+        return
+    scales = to["key_scales"].view(-1)[:rows].double()
+    top = y.abs().amax(1)
+    assert not ((scales - top / 448).abs() > 2.0 ** -18 * top / 448).any()
+    got = to["key_codes"].view(-1, 64)[:rows].view(torch.float8_e4m3fn).double() * scales[:, None]
+    assert not ((got - y).abs() > 2.0 ** -4 * y.abs() + 2.0 ** -10 * scales[:, None] + 2.0 ** -17 * top[:, None]).any()
