@@ -18,10 +18,10 @@
 // fetched two rows ahead, its data (and its row of the rotation's table) one.  Rows whose squares leave fp32's range are
 // left for the end of the kernel: with their code called from the loop 262144 rows took 150 us.
 //
-// What bounds it: HBM and the rows' places.  262144 rows, norms, rotation, fp8 keys: 123 us, 5900
-// GB/s, 0.87 of the measured copy rate (119 with the slots in order; the latents alone 101, a
-// copy of them 95).  At 400 instructions a row it was bound by them (132 us, 71 % of issue
-// slots); the sums one after another took 136; 24 warps an SM, with the weights in
+// What bounds it: HBM and the rows' places.  262144 rows, norms, rotation, fp8 keys: 117 us in a
+// loop of calls, 123 after other writes to all of L2 (6200 and 5900 GB/s, 0.91 and 0.87 of the measured copy rate; 119
+// for 123 with the slots in order; the latents alone 101, a copy of them 95), at 324 instructions a row (61 % of
+// issue slots).  At 400 it was bound by them (132 us, 71 %); the sums one after another took 136; 24 warps an SM, with the weights in
 // registers, 142; five CTAs an SM spill (181).  Few rows: launch latency, 2.5 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
