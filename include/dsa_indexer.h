@@ -571,7 +571,8 @@ DSA_API dsa_status_t dsa_pages_update(const int32_t *seq_lens, const int32_t *ne
  *     key_pool[slot] = y (bf16), or key_scales[slot] = max|y| / 448 and key_codes[slot] =
  *     e4m3(y / scale), the fp8 index-key cache's format; scale 1 where max|y| / 448 is 0
  *     or not finite.  (The codes are made from k * weight before the norm, which they do not
- *     depend on, and are those of dsa_rmsnorm_fp8.)
+ *     depend on, and are those of dsa_rmsnorm_fp8 wherever max|k * weight| and max|y| lie between
+ *     2^-99 and 2^99.)
  * Either part may be left out (latent_opt and kv_cache NULL; index_keys_opt and the key
  * caches NULL); keys go to exactly one of key_pool and (key_codes, key_scales).
  *   latent_opt     bf16 [rows, 576], rows latent_stride >= 0 elements apart, a multiple of 8;

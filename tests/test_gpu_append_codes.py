@@ -110,3 +110,65 @@ def test_rows_at_the_ends_of_the_range(gpu_lib, mag, eps, keys_to):
     assert not ((scales - top / 448).abs() > 2.0 ** -18 * top / 448).any()
     got = to["key_codes"].view(-1, 64)[:rows].view(torch.float8_e4m3fn).double() * scales[:, None]
     assert not ((got - y).abs() > 2.0 ** -4 * y.abs() + 2.0 ** -10 * scales[:, None] + 2.0 ** -17 * top[:, None]).any()
+
+
+@pytest.mark.parametrize("far", ["latent", "key", "both"])
+@pytest.mark.parametrize("norm_latent", [True, False])
+@pytest.mark.parametrize("keys_to", ["fp8", "bf16"])
+def test_one_part_at_the_end_of_the_range(gpu_lib, far, norm_latent, keys_to):
+    """Rows of which one part alone is far, with rotation and skipped rows among them, more rows than warps:
+    the other part as in ordinary rows, a copied part bit for bit, nothing beside the rows' own entries."""
+    import torch
+    g = torch.Generator("cuda").manual_seed(8)
+    rows, pages = 12000, 200
+    x = torch.randn(rows, 640, device="cuda", generator=g)
+    which = torch.arange(rows, device="cuda") % 5 == 2
+    if far in ("latent", "both"):
+        x[which, :512] *= 2.0 ** 90
+    if far in ("key", "both"):
+        x[which, 576:] *= 2.0 ** 90
+    x = x.to(torch.bfloat16)
+    slots = torch.randperm(pages * 64, device="cuda", generator=g)[:rows]
+    slots[::11] = -1
+    weight = (1 + 0.3 * torch.randn(576, device="cuda", generator=g)).to(torch.bfloat16)
+    angle = torch.rand(500, 32, device="cuda", generator=g, dtype=torch.float64) * 6
+    table = torch.cat([angle.cos(), angle.sin()], 1).float()
+    positions = torch.randint(500, (rows,), device="cuda", generator=g, dtype=torch.int32)
+    kv = torch.full((pages, 64, 576), 3.0, dtype=torch.bfloat16, device="cuda")
+    to = {"key_pool": torch.full((pages, 64, 64), 3.0, dtype=torch.bfloat16, device="cuda")} if keys_to == "bf16" else {
+        "key_codes": torch.full((pages, 64, 64), 3, dtype=torch.uint8, device="cuda"),
+        "key_scales": torch.full((pages, 64), 3.0, device="cuda")}
+    gpu_lib.dsa_cache_append(slots, latent=x[:, :576], latent_weight=weight[:512].contiguous() if norm_latent else None,
+                             cos_sin=table, positions=positions, kv_cache=kv, index_keys=x[:, 576:],
+                             index_weight=weight[512:].contiguous(), eps=EPS, **to)
+    live = slots >= 0
+    at = slots[live]
+    other = torch.ones(pages * 64, dtype=torch.bool, device="cuda")
+    other[at] = False
+    for t in (kv, *to.values()):
+        assert torch.all(t.flatten(0, 1)[other] == 3)
+
+    def normed(v, w):
+        v = v.double()
+        return v * w.double() / torch.sqrt((v * v).mean(1, keepdim=True) + EPS)
+
+    got = kv.view(-1, 576)[at].double()
+    if norm_latent:
+        y = normed(x[live, :512], weight[:512])
+        assert not ((got[:, :512] - y).abs() > (2.0 ** -8 + 2.0 ** -18) * y.abs()).any()
+    else:
+        assert torch.equal(kv.view(-1, 576)[at, :512], x[live, :512])
+    c, s = table.double()[positions[live].long()].chunk(2, 1)
+    a, b = x[live, 512:576:2].double(), x[live, 513:576:2].double()
+    for r, want, size in ((got[:, 512::2], a * c - b * s, (a * c).abs() + (b * s).abs()),
+                          (got[:, 513::2], a * s + b * c, (a * s).abs() + (b * c).abs())):
+        assert not ((r - want).abs() > 2.0 ** -8 * want.abs() + 2.0 ** -22 * size).any()
+    y = normed(x[live, 576:], weight[512:])
+    if keys_to == "bf16":
+        assert not ((to["key_pool"].view(-1, 64)[at].double() - y).abs() > (2.0 ** -8 + 2.0 ** -18) * y.abs()).any()
+        return
+    scales = to["key_scales"].view(-1)[at].double()
+    top = y.abs().amax(1)
+    assert not ((scales - top / 448).abs() > 2.0 ** -18 * top / 448).any()
+    back = to["key_codes"].view(-1, 64)[at].view(torch.float8_e4m3fn).double() * scales[:, None]
+    assert not ((back - y).abs() > 2.0 ** -4 * y.abs() + 2.0 ** -10 * scales[:, None] + 2.0 ** -17 * top[:, None]).any()
