@@ -18,10 +18,11 @@
 // fetched two rows ahead, its data (and its row of the rotation's table) one.  Rows whose squares leave fp32's range are
 // left for the end of the kernel: with their code called from the loop 262144 rows took 150 us.
 //
-// What bounds it: HBM and the rows' places.  262144 rows, norms, rotation, fp8 keys: 117 us in a
-// loop of calls, 123 after other writes to all of L2 (6200 and 5900 GB/s, 0.91 and 0.87 of the measured copy rate; 119
-// for 123 with the slots in order; the latents alone 101, a copy of them 95), at 324 instructions a row (61 % of
-// issue slots).  At 400 it was bound by them (132 us, 71 %); the sums one after another took 136; 24 warps an SM, with the weights in
+// What bounds it: HBM and the rows' places.  262144 rows, norms, rotation, fp8 keys: 117 us in
+// a loop of calls, 123 after other writes to all of L2 (6200 and 5900 GB/s, 0.91 and 0.87 of
+// the measured copy rate; 119 for 123 with the slots in order; the latents alone 101, a copy
+// of them 95), at 324 instructions a row (61 % of issue slots).  At 400 it was bound by them
+// (132 us, 71 %); the sums one after another took 136; 24 warps an SM, with the weights in
 // registers, 142; five CTAs an SM spill (181).  Few rows: launch latency, 2.5 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -59,7 +60,8 @@ __device__ __forceinline__ bool far_sum(float sum, float eps) {
 // first * second leaves the range nowhere.
 struct FarNorm {
     float by, first, second;
-    __device__ __forceinline__ explicit FarNorm(float sum) : by(sum < 1.f ? 0x1p100f : 0x1p-70f), first(1.f), second(1.f) {}
+    __device__ __forceinline__ explicit FarNorm(float sum)
+        : by(sum < 1.f ? 0x1p100f : 0x1p-70f), first(1.f), second(1.f) {}
     __device__ __forceinline__ float square(float x) const { return x * by * (x * by); }
     __device__ __forceinline__ void settle(float sum, float over_n, float eps) {
 #pragma unroll 1
